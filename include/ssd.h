@@ -369,6 +369,153 @@ ssd_status ssd_backward(const ssd_shape* shape, const void* x, const float* dt, 
 /* Workspace bytes ssd_backward needs (0 for an invalid or NULL shape). */
 size_t ssd_backward_workspace_bytes(const ssd_shape* shape);
 
+/* ------------------------------------------------------------------------
+ * The layer around the scan: the short causal convolution in front of it, the
+ * selective scan (a decay per channel and state), and the norm.  The pages
+ * name neither; each follows from its formula below.
+ *
+ * Conventions as above, with these additions.  Activations are [B,L,D] rows
+ * of channels in `in` (F32 or BF16), parameters fp32; all arithmetic, sums
+ * and states are fp32 and an output is rounded once, to nearest even.
+ * Arguments marked "rows" may be column slices of wider rows: a row stride in
+ * elements (0 = dense) leads from one token to the next, batches follow each
+ * other at L rows.  Such arguments need only be aligned to their element, Bm
+ * and Cm to 4 bytes (with row strides in whole 4-byte units); everything else
+ * to 16 bytes.  Optional arguments may be NULL.  A gradient asked for by a
+ * pointer is written whole.  Results do not depend on timing (no atomics).
+ *
+ * Packed sequences as in ssd_forward_varlen: seq_idx [B,L] (optional) names
+ * each token's sequence, and wherever it changes along a row the recurrence
+ * (or the window) restarts from zero; nothing of one sequence, NaN included,
+ * reaches another's outputs or input gradients.  Initial states apply to a row's first
+ * sequence, final states are those of its last.  seq_states[s] receives the
+ * state after token seq_last[s] (flattened b*L + t; an index outside
+ * [0, B*L) leaves its entry untouched); nseq = 0 allows both NULL.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Causal depthwise convolution, W taps (width in {2, 3, 4}):
+ *   pre[b,t,d] = bias[d] + sum_{k<W} w[d,k] x[b,t-W+1+k,d]
+ *   y = pre / (1 + exp(-pre))  (silu != 0)   or   y = pre
+ * x rows (x_row), w [D,W], bias [D] (optional)  ->  y [B,L,D].  The state is
+ * the last W-1 inputs, oldest first: initial_state, final_state [B,W-1,D],
+ * seq_states [nseq,W-1,D], all in `in` and optional (zeros / not written).
+ */
+typedef struct {
+  int64_t batch, seqlen, channels, width;
+} ssd_conv_shape;
+
+ssd_status ssd_causal_conv(const ssd_conv_shape* shape, const void* x, int64_t x_row, const float* w,
+                           const float* bias, ssd_dtype in, int silu, const void* initial_state,
+                           const int32_t* seq_idx, void* y, void* final_state, int64_t nseq,
+                           const int64_t* seq_last, void* seq_states, void* stream);
+
+/* One token (seqlen 1): x rows [B,D]; state [B,W-1,D] is read, the state
+ * after the token is written to state_out (which may be state itself). */
+ssd_status ssd_causal_conv_step(const ssd_conv_shape* shape, const void* x, int64_t x_row, const void* state,
+                                const float* w, const float* bias, ssd_dtype in, int silu, void* state_out, void* y,
+                                void* stream);
+
+/*
+ * Gradients for dL/dy = dy [B,L,D] and dL/d final_state = dfinal (optional:
+ * zero), with pre recomputed:
+ *   dpre = dy silu'(pre),  dx[t] = sum_k w[k] dpre[t+W-1-k],
+ *   dw[d,k] = sum_{b,t} dpre[t] x[t-W+1+k],  dbias[d] = sum_{b,t} dpre[t]
+ * dx rows (dx_row) in `in`, dw [D,W] and dbias [D] (optional) fp32, dinitial
+ * [B,W-1,D] in `in` (optional).  Workspace: device memory of
+ * ssd_causal_conv_backward_workspace_bytes(shape) bytes.
+ */
+ssd_status ssd_causal_conv_backward(const ssd_conv_shape* shape, const void* x, int64_t x_row, const float* w,
+                                    const float* bias, ssd_dtype in, int silu, const void* initial_state,
+                                    const int32_t* seq_idx, const void* dy, const void* dfinal, void* dx,
+                                    int64_t dx_row, float* dw, float* dbias, void* dinitial, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+size_t ssd_causal_conv_backward_workspace_bytes(const ssd_conv_shape* shape);
+
+/*
+ * Selective scan.  Per batch b, channel d (group g = d / (D/G)), state n:
+ *   dt[t]  = softplus(raw[b,t,d] + dt_bias[d])     (softplus != 0; else without)
+ *   h[t,n] = exp(dt[t] A[d,n]) h[t-1,n] + dt[t] u[b,t,d] Bm[b,t,g,n]
+ *   y[t]   = sum_n Cm[b,t,g,n] h[t,n] + Dskip[d] u[b,t,d],  times z / (1 + exp(-z)) with a gate z
+ * u, raw (argument dt), z rows of D channels, Bm, Cm rows [G,N], all `in`;
+ * A [D,N], Dskip, dt_bias [D] fp32; Dskip, z, dt_bias optional.  y [B,L,D] in
+ * `in`; initial_states, final_states [B,N,D], seq_states [nseq,N,D] fp32,
+ * optional.  N (dstate) a multiple of 4 up to 256 (else SSD_ERR_UNSUPPORTED).
+ * Row strides: `rows` NULL = all dense.  Workspace: device memory of
+ * ssd_selective_scan_workspace_bytes(shape) bytes (0 and NULL where the tokens
+ * are not split).
+ */
+typedef struct {
+  int64_t batch, seqlen, channels, dstate, ngroups;
+} ssd_scan_shape;
+typedef struct {
+  int64_t u, dt, Bm, Cm, z; /* elements from a token to the next; 0 = dense */
+} ssd_scan_rows;
+
+ssd_status ssd_selective_scan(const ssd_scan_shape* shape, const ssd_scan_rows* rows, const void* u, const void* dt,
+                              const float* A, const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                              const float* dt_bias, int softplus, ssd_dtype in, const float* initial_states,
+                              const int32_t* seq_idx, void* y, float* final_states, int64_t nseq,
+                              const int64_t* seq_last, float* seq_states, void* workspace, size_t workspace_bytes,
+                              void* stream);
+size_t ssd_selective_scan_workspace_bytes(const ssd_scan_shape* shape);
+
+/* One token (seqlen 1): u, dt, z [B,D], Bm, Cm [B,G,N] rows; state [B,N,D]
+ * fp32 is read, the state after the token is written to state_out (which may
+ * be state itself). */
+ssd_status ssd_selective_step(const ssd_scan_shape* shape, const ssd_scan_rows* rows, const void* u, const void* dt,
+                              const float* A, const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                              const float* dt_bias, int softplus, ssd_dtype in, const float* state, float* state_out,
+                              void* y, void* stream);
+
+/*
+ * Gradients of ssd_selective_scan for dL/dy = dy [B,L,D] (`in`) and
+ * dL/d final_states = dfinal (optional: zero); the states are recomputed.
+ * du, ddt (with respect to raw), dB, dC, dz in `in`, laid out like their
+ * inputs with the row strides of `grad_rows` (NULL = dense); dz is required
+ * exactly when z is given.  dA [D,N], dD, ddt_bias [D] (optional), dinitial
+ * [B,N,D] (optional) fp32.  Workspace: device memory of
+ * ssd_selective_scan_backward_workspace_bytes(shape) bytes.
+ */
+ssd_status ssd_selective_scan_backward(const ssd_scan_shape* shape, const ssd_scan_rows* rows, const void* u,
+                                       const void* dt, const float* A, const void* Bm, const void* Cm,
+                                       const float* Dskip, const void* z, const float* dt_bias, int softplus,
+                                       ssd_dtype in, const float* initial_states, const int32_t* seq_idx,
+                                       const void* dy, const float* dfinal, const ssd_scan_rows* grad_rows, void* du,
+                                       void* ddt, float* dA, void* dB, void* dC, float* dD, void* dz, float* ddt_bias,
+                                       float* dinitial, void* workspace, size_t workspace_bytes, void* stream);
+size_t ssd_selective_scan_backward_workspace_bytes(const ssd_scan_shape* shape);
+
+/*
+ * Layer norm of `rows` dense rows of `dim` columns (dim <= 65536), with an
+ * optional residual stream in front:
+ *   r = x + residual, stored in residual_out (res_dtype; the stored value is
+ *       normalised), or r = x without one
+ *   y = (r - mean) rstd w + bias,  rstd = 1 / sqrt(mean((r - mean)^2) + eps)
+ * rms != 0: mean = 0 throughout (RMS norm).  x, y in `in`; w [dim], bias
+ * [dim] (optional) fp32; mean (NULL exactly for rms) and rstd [rows] fp32.
+ */
+ssd_status ssd_layer_norm(int64_t rows, int64_t dim, const void* x, ssd_dtype in, const void* residual,
+                          ssd_dtype res_dtype, const float* w, const float* bias, float eps, int rms, void* y,
+                          void* residual_out, float* mean, float* rstd, void* stream);
+
+/*
+ * Gradients for dL/dy = dy (`in`): x is what the forward normalised (its
+ * residual_out, or its x) in x_dtype, mean and rstd its statistics.  With
+ * v = w dy, xh = (x - mean) rstd:
+ *   dx = rstd (v - mean(v) - xh mean(v xh)) + dresidual     (rms: no mean(v))
+ *   dw = sum over rows of dy xh,  dbias = sum over rows of dy
+ * dresidual (x_dtype, optional) is the gradient arriving at the residual
+ * stream; dx is written in `in` and, where residual_grad is given, also there
+ * in x_dtype (the gradient of the residual argument).  dw, dbias (optional)
+ * fp32.  Workspace: ssd_layer_norm_backward_workspace_bytes(rows, dim) bytes.
+ */
+ssd_status ssd_layer_norm_backward(int64_t rows, int64_t dim, const void* dy, ssd_dtype in, const void* x,
+                                   ssd_dtype x_dtype, const float* w, const float* mean, const float* rstd, int rms,
+                                   const void* dresidual, void* dx, void* residual_grad, float* dw, float* dbias,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+size_t ssd_layer_norm_backward_workspace_bytes(int64_t rows, int64_t dim);
+
 /* Static, NUL-terminated description of a status code. */
 const char* ssd_status_string(ssd_status status);
 

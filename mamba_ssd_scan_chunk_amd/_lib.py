@@ -36,9 +36,27 @@ class SSDShape(ctypes.Structure):
         return {k: getattr(self, k) for k, _ in self._fields_}
 
 
+class SSDConvShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("width", ctypes.c_int64)]
+
+
+class SSDScanShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64)]
+
+
+class SSDScanRows(ctypes.Structure):
+    _fields_ = [("u", ctypes.c_int64), ("dt", ctypes.c_int64), ("Bm", ctypes.c_int64), ("Cm", ctypes.c_int64),
+                ("z", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _S = ctypes.POINTER(SSDShape)
 _E = ctypes.c_int  # enums
+_I, _F, _Z = ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+_CS, _SS, _SR = ctypes.POINTER(SSDConvShape), ctypes.POINTER(SSDScanShape), ctypes.POINTER(SSDScanRows)
+_SCAN_IN = [_SS, _SR, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int, _E]  # shape .. in
 
 _SIGNATURES = {
     "ssd_chunk_cumsum": (ctypes.c_int, [_S, _P, _P, _P, _P, _P]),
@@ -57,6 +75,20 @@ _SIGNATURES = {
     "ssd_backward": (ctypes.c_int, [_S, _P, _P, _P, _P, _P, _P, _E, _P, _P, _E, _P, _P, _P, _P, _P, _P, _P, _P,
                                     _P, ctypes.c_size_t, _E, _P]),
     "ssd_backward_workspace_bytes": (ctypes.c_size_t, [_S]),
+    "ssd_causal_conv": (ctypes.c_int, [_CS, _P, _I, _P, _P, _E, ctypes.c_int, _P, _P, _P, _P, _I, _P, _P, _P]),
+    "ssd_causal_conv_step": (ctypes.c_int, [_CS, _P, _I, _P, _P, _P, _E, ctypes.c_int, _P, _P, _P]),
+    "ssd_causal_conv_backward": (ctypes.c_int, [_CS, _P, _I, _P, _P, _E, ctypes.c_int, _P, _P, _P, _P, _P, _I, _P, _P,
+                                                _P, _P, _Z, _P]),
+    "ssd_causal_conv_backward_workspace_bytes": (_Z, [_CS]),
+    "ssd_selective_scan": (ctypes.c_int, _SCAN_IN + [_P, _P, _P, _P, _I, _P, _P, _P, _Z, _P]),
+    "ssd_selective_scan_workspace_bytes": (_Z, [_SS]),
+    "ssd_selective_step": (ctypes.c_int, _SCAN_IN + [_P, _P, _P, _P]),
+    "ssd_selective_scan_backward": (ctypes.c_int, _SCAN_IN + [_P, _P, _P, _P, _SR] + [_P] * 9 + [_P, _Z, _P]),
+    "ssd_selective_scan_backward_workspace_bytes": (_Z, [_SS]),
+    "ssd_layer_norm": (ctypes.c_int, [_I, _I, _P, _E, _P, _E, _P, _P, _F, ctypes.c_int, _P, _P, _P, _P, _P]),
+    "ssd_layer_norm_backward": (ctypes.c_int, [_I, _I, _P, _E, _P, _E, _P, _P, _P, ctypes.c_int, _P, _P, _P, _P, _P, _P,
+                                               _Z, _P]),
+    "ssd_layer_norm_backward_workspace_bytes": (_Z, [_I, _I]),
     "ssd_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "ssd_abi_version": (ctypes.c_int, []),
 }

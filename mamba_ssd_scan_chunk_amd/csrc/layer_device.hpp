@@ -1,0 +1,73 @@
+// layer_device.hpp -- device helpers of the layer operators: element types,
+// the sigmoid and softplus they share.
+#pragma once
+
+#include "ssd_device.hpp"
+
+namespace ssd {
+
+// Element type of activations in memory; arithmetic is always fp32.
+struct IoBF16 {
+  typedef uint16_t type;
+  static constexpr int kVec = 8;  // elements in 16 bytes
+  __device__ __forceinline__ static float get(uint16_t v) { return bf16_bits_to_f32(v); }
+  __device__ __forceinline__ static uint16_t put(float v) { return (uint16_t)f32_to_bf16_bits(v); }
+};
+struct IoF32 {
+  typedef float type;
+  static constexpr int kVec = 4;
+  __device__ __forceinline__ static float get(float v) { return v; }
+  __device__ __forceinline__ static float put(float v) { return v; }
+};
+
+// V consecutive elements as fp32: one 16-byte access per IO::kVec elements
+// (V a multiple of it), or a single element (V = 1).
+template <class IO, int V>
+__device__ __forceinline__ void load_vec(const typename IO::type* p, float* o) {
+  if constexpr (V == 1) {
+    o[0] = IO::get(p[0]);
+  } else if constexpr (IO::kVec == 8) {
+#pragma unroll
+    for (int k = 0; k < V; k += 8) {
+      const uint4 q = *reinterpret_cast<const uint4*>(p + k);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        o[k + 2 * e] = __uint_as_float(w[e] << 16);
+        o[k + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; k += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(p + k);
+      o[k] = q.x; o[k + 1] = q.y; o[k + 2] = q.z; o[k + 3] = q.w;
+    }
+  }
+}
+template <class IO, int V>
+__device__ __forceinline__ void store_vec(typename IO::type* p, const float* v) {
+  if constexpr (V == 1) {
+    p[0] = IO::put(v[0]);
+  } else if constexpr (IO::kVec == 8) {
+#pragma unroll
+    for (int k = 0; k < V; k += 8)
+      *reinterpret_cast<uint4*>(p + k) = make_uint4(pack_bf16x2(v[k], v[k + 1]), pack_bf16x2(v[k + 2], v[k + 3]),
+                                                    pack_bf16x2(v[k + 4], v[k + 5]), pack_bf16x2(v[k + 6], v[k + 7]));
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; k += 4) *reinterpret_cast<float4*>(p + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+  }
+}
+
+// 1 / (1 + e^-v): hardware exponential and reciprocal, about 2 ulp.
+__device__ __forceinline__ float sigmoid(float v) {
+  return __builtin_amdgcn_rcpf(1.f + fast_exp2(-v * kLog2e));
+}
+// d/dv [v sigmoid(v)] from v and its sigmoid
+__device__ __forceinline__ float dsilu(float v, float s) { return s * fmaf(v, 1.f - s, 1.f); }
+
+// log(1 + e^v); v itself above 20, where they agree to fp32
+__device__ __forceinline__ float softplus(float v) { return v > 20.f ? v : log1pf(fast_exp2(v * kLog2e)); }
+
+}  // namespace ssd

@@ -12,7 +12,8 @@ from typing import Dict, Optional, Tuple
 
 import torch
 
-from ._lib import MMA, SSD_BF16, SSD_F32, SSDShape, check, load_library
+from ._lib import (MMA, SSD_BF16, SSD_F32, SSDConvShape, SSDScanRows, SSDScanShape, SSDShape, check,
+                   load_library)
 
 _DT = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
 _DTNAME = {"f32": torch.float32, "bf16": torch.bfloat16}
@@ -425,3 +426,350 @@ def shape_of(inp: Dict[str, torch.Tensor], chunk: int) -> SSDShape:
     B, L, H, P = inp["x"].shape
     G, N = inp["Bm"].shape[2], inp["Bm"].shape[3]
     return SSDShape.make(B, L, H, P, N, G, chunk)
+
+
+# ---- the layer around the scan: causal convolution, selective scan, norm ----
+
+_IO = (torch.float32, torch.bfloat16)
+_F32 = (torch.float32,)
+
+
+def _req_rows(t: Optional[torch.Tensor], name: str, shape, dtypes, lead: int = 2) -> int:
+    """Checks a tensor whose tokens may lie in wider rows (a column slice) and
+    returns its row stride in elements (0: dense).  The first ``lead``
+    dimensions count tokens (batch, and seqlen unless a single token); within
+    a token's row the tensor is contiguous, batches are seqlen rows apart."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.is_contiguous():
+        return 0
+    st, inner = t.stride(), 1
+    for k in range(len(shape) - 1, lead - 1, -1):
+        if shape[k] > 1 and st[k] != inner:
+            raise ValueError(f"{name} must be contiguous within a token's row")
+        inner *= shape[k]
+    if lead == 1:
+        row = st[0] if shape[0] > 1 else inner
+    else:
+        row = st[1] if shape[1] > 1 else (st[0] if shape[0] > 1 else inner)
+        if shape[0] > 1 and st[0] != shape[1] * row:
+            raise ValueError(f"{name}'s batches must follow each other at seqlen rows")
+    if row < inner:
+        raise ValueError(f"{name} has overlapping rows")
+    return row
+
+
+def _opt(t: Optional[torch.Tensor], name: str, shape, dtypes) -> None:
+    if t is not None:
+        _req(t, name, shape, dtypes)
+
+
+def _workspace(workspace, query, query_args, device):
+    """The given workspace, or a new one of the queried size; and its bytes."""
+    if workspace is None:
+        workspace = torch.empty(max(int(query(*query_args)), 1), device=device, dtype=torch.uint8)
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous GPU tensor")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _seq_states(seq_last, seq_states, shape, dtype, device):
+    """nseq and the checked (or new) per-sequence states."""
+    if seq_last is None:
+        return 0, None
+    _req(seq_last, "seq_last", (seq_last.numel(),), (torch.int64,))
+    nseq = seq_last.numel()
+    if seq_states is None:
+        seq_states = torch.empty((nseq,) + shape, device=device, dtype=dtype)
+    _req(seq_states, "seq_states", (nseq,) + shape, (dtype,))
+    return nseq, seq_states
+
+
+def ssd_causal_conv(x, weight, bias=None, silu=True, initial_state=None, seq_idx=None, y=None, final_state=None,
+                    want_final=False, seq_last=None, seq_states=None, stream=None):
+    """Causal depthwise convolution with SiLU over x [B,L,D] (may be a column
+    slice of wider rows): weight [D,W] (W 2 to 4) and bias [D] fp32, states
+    [B,W-1,D] in x's dtype, oldest input first.  Returns (y, final_state or
+    None), and with seq_last (see ssd_forward_varlen) also seq_states
+    [nseq,W-1,D]."""
+    B, L, D = x.shape
+    _req(weight, "weight", (D, weight.shape[-1]), _F32)
+    W = weight.shape[1]
+    io = (x.dtype,)
+    row = _req_rows(x, "x", (B, L, D), _IO)
+    _opt(bias, "bias", (D,), _F32)
+    _opt(initial_state, "initial_state", (B, W - 1, D), io)
+    _opt(seq_idx, "seq_idx", (B, L), (torch.int32,))
+    if y is None:
+        y = torch.empty((B, L, D), device=x.device, dtype=x.dtype)
+    _req(y, "y", (B, L, D), io)
+    if final_state is None and want_final:
+        final_state = torch.empty((B, W - 1, D), device=x.device, dtype=x.dtype)
+    _opt(final_state, "final_state", (B, W - 1, D), io)
+    nseq, seq_states = _seq_states(seq_last, seq_states, (W - 1, D), x.dtype, x.device)
+    check(load_library().ssd_causal_conv(SSDConvShape(B, L, D, W), _ptr(x), row, _ptr(weight), _ptr(bias),
+                                         _DT[x.dtype], int(silu), _ptr(initial_state), _ptr(seq_idx), _ptr(y),
+                                         _ptr(final_state), nseq, _ptr(seq_last if nseq else None),
+                                         _ptr(seq_states if nseq else None), _stream(stream)))
+    return (y, final_state) if seq_last is None else (y, final_state, seq_states)
+
+
+def ssd_causal_conv_step(x, state, weight, bias=None, silu=True, y=None, state_out=None, stream=None):
+    """One token of ssd_causal_conv: x [B,D], state [B,W-1,D].  The state after
+    the token goes to ``state_out`` (default: over ``state``).  Returns y."""
+    B, D = x.shape
+    _req(weight, "weight", (D, weight.shape[-1]), _F32)
+    W = weight.shape[1]
+    io = (x.dtype,)
+    row = _req_rows(x, "x", (B, D), _IO, 1)
+    _req(state, "state", (B, W - 1, D), io)
+    _opt(bias, "bias", (D,), _F32)
+    if state_out is None:
+        state_out = state
+    _req(state_out, "state_out", (B, W - 1, D), io)
+    if y is None:
+        y = torch.empty((B, D), device=x.device, dtype=x.dtype)
+    _req(y, "y", (B, D), io)
+    check(load_library().ssd_causal_conv_step(SSDConvShape(B, 1, D, W), _ptr(x), row, _ptr(state), _ptr(weight),
+                                              _ptr(bias), _DT[x.dtype], int(silu), _ptr(state_out), _ptr(y),
+                                              _stream(stream)))
+    return y
+
+
+def ssd_causal_conv_backward_workspace_bytes(batch, seqlen, channels, width) -> int:
+    return int(load_library().ssd_causal_conv_backward_workspace_bytes(SSDConvShape(batch, seqlen, channels, width)))
+
+
+def ssd_causal_conv_backward(x, weight, dy, bias=None, silu=True, initial_state=None, seq_idx=None, dfinal=None,
+                             want_dinitial=False, workspace=None, out=None, stream=None):
+    """Gradients of ssd_causal_conv for dL/dy = dy and dL/dfinal = dfinal:
+    a dict of dx (x's dtype; a given ``out["dx"]`` may be a column slice),
+    dweight [D,W], dbias [D] (fp32; None without a bias) and dinitial (None
+    unless ``want_dinitial``), in the tensors of ``out`` where given."""
+    B, L, D = x.shape
+    _req(weight, "weight", (D, weight.shape[-1]), _F32)
+    W = weight.shape[1]
+    io = (x.dtype,)
+    row = _req_rows(x, "x", (B, L, D), _IO)
+    _req(dy, "dy", (B, L, D), io)
+    _opt(bias, "bias", (D,), _F32)
+    _opt(initial_state, "initial_state", (B, W - 1, D), io)
+    _opt(seq_idx, "seq_idx", (B, L), (torch.int32,))
+    _opt(dfinal, "dfinal", (B, W - 1, D), io)
+    r = dict(dx=None, dweight=None, dbias=None, dinitial=None)
+    r.update(out or {})
+    new = lambda k, shp, dt: torch.empty(shp, device=x.device, dtype=dt) if r[k] is None else r[k]
+    r["dx"] = new("dx", (B, L, D), x.dtype)
+    dx_row = _req_rows(r["dx"], "dx", (B, L, D), io)
+    r["dweight"] = new("dweight", (D, W), torch.float32)
+    _req(r["dweight"], "dweight", (D, W), _F32)
+    r["dbias"] = new("dbias", (D,), torch.float32) if bias is not None else None
+    _opt(r["dbias"], "dbias", (D,), _F32)
+    r["dinitial"] = new("dinitial", (B, W - 1, D), x.dtype) if want_dinitial else None
+    _opt(r["dinitial"], "dinitial", (B, W - 1, D), io)
+    lib = load_library()
+    sh = SSDConvShape(B, L, D, W)
+    workspace, wsb = _workspace(workspace, lib.ssd_causal_conv_backward_workspace_bytes, (sh,), x.device)
+    check(lib.ssd_causal_conv_backward(sh, _ptr(x), row, _ptr(weight), _ptr(bias), _DT[x.dtype], int(silu),
+                                       _ptr(initial_state), _ptr(seq_idx), _ptr(dy), _ptr(dfinal), _ptr(r["dx"]),
+                                       dx_row, _ptr(r["dweight"]), _ptr(r["dbias"]), _ptr(r["dinitial"]),
+                                       _ptr(workspace), wsb, _stream(stream)))
+    return r
+
+
+def _scan_inputs(u, dt, A, Bm, Cm, D, z, dt_bias, lead):
+    """Checks the inputs shared by the selective scan's calls; returns the
+    shape struct and the row strides."""
+    tok = tuple(u.shape[:lead])
+    Dn = u.shape[lead]
+    G, N = Bm.shape[lead:]
+    io = (u.dtype,)
+    rows = SSDScanRows(_req_rows(u, "u", tok + (Dn,), _IO, lead), _req_rows(dt, "dt", tok + (Dn,), io, lead),
+                       _req_rows(Bm, "Bm", tok + (G, N), io, lead), _req_rows(Cm, "Cm", tok + (G, N), io, lead),
+                       0 if z is None else _req_rows(z, "z", tok + (Dn,), io, lead))
+    _req(A, "A", (Dn, N), _F32)
+    _opt(D, "D", (Dn,), _F32)
+    _opt(dt_bias, "dt_bias", (Dn,), _F32)
+    return SSDScanShape(tok[0], tok[1] if lead == 2 else 1, Dn, N, G), rows
+
+
+def ssd_selective_scan_workspace_bytes(batch, seqlen, channels, dstate, ngroups=1) -> int:
+    return int(load_library().ssd_selective_scan_workspace_bytes(SSDScanShape(batch, seqlen, channels, dstate,
+                                                                              ngroups)))
+
+
+def ssd_selective_scan(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=True, initial_states=None,
+                       seq_idx=None, y=None, final_states=None, want_final=True, seq_last=None, seq_states=None,
+                       workspace=None, stream=None):
+    """Selective scan over u, dt, z [B,L,D] and Bm, Cm [B,L,G,N] (each may be
+    a column slice of wider rows), A [D,N], D, dt_bias [D] fp32, states
+    [B,N,D] fp32.  dt is the raw projection; ``softplus`` makes the time step
+    softplus(dt + dt_bias).  Returns (y, final_states or None), and with
+    seq_last also seq_states [nseq,N,D]."""
+    sh, rows = _scan_inputs(u, dt, A, Bm, Cm, D, z, dt_bias, 2)
+    B, L, Dn, N = sh.batch, sh.seqlen, sh.channels, sh.dstate
+    _opt(initial_states, "initial_states", (B, N, Dn), _F32)
+    _opt(seq_idx, "seq_idx", (B, L), (torch.int32,))
+    if y is None:
+        y = torch.empty((B, L, Dn), device=u.device, dtype=u.dtype)
+    _req(y, "y", (B, L, Dn), (u.dtype,))
+    if final_states is None and want_final:
+        final_states = torch.empty((B, N, Dn), device=u.device, dtype=torch.float32)
+    _opt(final_states, "final_states", (B, N, Dn), _F32)
+    nseq, seq_states = _seq_states(seq_last, seq_states, (N, Dn), torch.float32, u.device)
+    lib = load_library()
+    workspace, wsb = _workspace(workspace, lib.ssd_selective_scan_workspace_bytes, (sh,), u.device)
+    check(lib.ssd_selective_scan(sh, rows, _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z),
+                                 _ptr(dt_bias), int(softplus), _DT[u.dtype], _ptr(initial_states), _ptr(seq_idx),
+                                 _ptr(y), _ptr(final_states), nseq, _ptr(seq_last if nseq else None),
+                                 _ptr(seq_states if nseq else None), _ptr(workspace), wsb, _stream(stream)))
+    return (y, final_states) if seq_last is None else (y, final_states, seq_states)
+
+
+def ssd_selective_step(u, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, softplus=True, y=None, state_out=None,
+                       stream=None):
+    """One token of ssd_selective_scan: u, dt, z [B,D], Bm, Cm [B,G,N], state
+    [B,N,D] fp32.  The state after the token goes to ``state_out`` (default:
+    over ``state``).  Returns y."""
+    sh, rows = _scan_inputs(u, dt, A, Bm, Cm, D, z, dt_bias, 1)
+    B, Dn, N = sh.batch, sh.channels, sh.dstate
+    _req(state, "state", (B, N, Dn), _F32)
+    if state_out is None:
+        state_out = state
+    _req(state_out, "state_out", (B, N, Dn), _F32)
+    if y is None:
+        y = torch.empty((B, Dn), device=u.device, dtype=u.dtype)
+    _req(y, "y", (B, Dn), (u.dtype,))
+    check(load_library().ssd_selective_step(sh, rows, _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D),
+                                            _ptr(z), _ptr(dt_bias), int(softplus), _DT[u.dtype], _ptr(state),
+                                            _ptr(state_out), _ptr(y), _stream(stream)))
+    return y
+
+
+def ssd_selective_scan_backward_workspace_bytes(batch, seqlen, channels, dstate, ngroups=1) -> int:
+    return int(load_library().ssd_selective_scan_backward_workspace_bytes(SSDScanShape(batch, seqlen, channels,
+                                                                                       dstate, ngroups)))
+
+
+def ssd_selective_scan_backward(u, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, softplus=True,
+                                initial_states=None, dfinal=None, seq_idx=None, want_dinitial=False, workspace=None,
+                                out=None, stream=None) -> Dict[str, Optional[torch.Tensor]]:
+    """Gradients of ssd_selective_scan for dL/dy = dy and dL/dfinal = dfinal
+    (None: zero): du, ddt (with respect to the raw dt), dB, dC, dz in u's dtype
+    (given ``out`` tensors may be column slices), dA, dD, ddt_bias, dinitial
+    fp32; None where the input is absent, dinitial unless ``want_dinitial``."""
+    sh, rows = _scan_inputs(u, dt, A, Bm, Cm, D, z, dt_bias, 2)
+    B, L, Dn, N, G = sh.batch, sh.seqlen, sh.channels, sh.dstate, sh.ngroups
+    io = (u.dtype,)
+    _req(dy, "dy", (B, L, Dn), io)
+    _opt(initial_states, "initial_states", (B, N, Dn), _F32)
+    _opt(dfinal, "dfinal", (B, N, Dn), _F32)
+    _opt(seq_idx, "seq_idx", (B, L), (torch.int32,))
+    wide = dict(du=(B, L, Dn), ddt=(B, L, Dn), dB=(B, L, G, N), dC=(B, L, G, N), dz=(B, L, Dn))
+    flat = dict(dA=(Dn, N), dD=(Dn,), ddt_bias=(Dn,), dinitial=(B, N, Dn))
+    absent = {"dz": z is None, "dD": D is None, "ddt_bias": dt_bias is None, "dinitial": not want_dinitial}
+    given = dict(out or {})
+    r, grow = {}, {}
+    for k, shp in wide.items():
+        if absent.get(k):
+            r[k], grow[k] = None, 0
+            continue
+        r[k] = given[k] if given.get(k) is not None else torch.empty(shp, device=u.device, dtype=u.dtype)
+        grow[k] = _req_rows(r[k], k, shp, io)
+    for k, shp in flat.items():
+        if absent.get(k):
+            r[k] = None
+            continue
+        r[k] = given[k] if given.get(k) is not None else torch.empty(shp, device=u.device)
+        _req(r[k], k, shp, _F32)
+    lib = load_library()
+    workspace, wsb = _workspace(workspace, lib.ssd_selective_scan_backward_workspace_bytes, (sh,), u.device)
+    check(lib.ssd_selective_scan_backward(
+        sh, rows, _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias), int(softplus),
+        _DT[u.dtype], _ptr(initial_states), _ptr(seq_idx), _ptr(dy), _ptr(dfinal),
+        SSDScanRows(grow["du"], grow["ddt"], grow["dB"], grow["dC"], grow["dz"]), _ptr(r["du"]), _ptr(r["ddt"]),
+        _ptr(r["dA"]), _ptr(r["dB"]), _ptr(r["dC"]), _ptr(r["dD"]), _ptr(r["dz"]), _ptr(r["ddt_bias"]),
+        _ptr(r["dinitial"]), _ptr(workspace), wsb, _stream(stream)))
+    return r
+
+
+def ssd_layer_norm(x, weight, bias=None, residual=None, eps=1e-5, rms=False, y=None, residual_out=None, mean=None,
+                   rstd=None, stream=None):
+    """Layer norm (``rms``: RMS norm) of the rows of x [..., D], weight, bias
+    [D] fp32, with ``residual`` (fp32 or bf16) added first.  Returns (y in x's
+    dtype, the sum in the residual's dtype or None, mean or None for rms,
+    rstd): the sum (or x), mean and rstd are what the backward takes."""
+    D = x.shape[-1]
+    rows = x.numel() // max(D, 1)
+    shp, st = tuple(x.shape), tuple(x.shape[:-1])
+    _req(x, "x", shp, _IO)
+    _req(weight, "weight", (D,), _F32)
+    _opt(bias, "bias", (D,), _F32)
+    if residual is not None:
+        _req(residual, "residual", shp, _IO)
+        if residual_out is None:
+            residual_out = torch.empty(shp, device=x.device, dtype=residual.dtype)
+        _req(residual_out, "residual_out", shp, (residual.dtype,))
+    elif residual_out is not None:
+        raise ValueError("residual_out is given without a residual")
+    if y is None:
+        y = torch.empty(shp, device=x.device, dtype=x.dtype)
+    _req(y, "y", shp, (x.dtype,))
+    if rms:
+        mean = None
+    elif mean is None:
+        mean = torch.empty(st, device=x.device, dtype=torch.float32)
+    _opt(mean, "mean", st, _F32)
+    if rstd is None:
+        rstd = torch.empty(st, device=x.device, dtype=torch.float32)
+    _req(rstd, "rstd", st, _F32)
+    check(load_library().ssd_layer_norm(rows, D, _ptr(x), _DT[x.dtype], _ptr(residual),
+                                        _DT[(x if residual is None else residual).dtype], _ptr(weight), _ptr(bias),
+                                        float(eps), int(rms), _ptr(y), _ptr(residual_out), _ptr(mean), _ptr(rstd),
+                                        _stream(stream)))
+    return y, residual_out, mean, rstd
+
+
+def ssd_layer_norm_backward_workspace_bytes(rows, dim) -> int:
+    return int(load_library().ssd_layer_norm_backward_workspace_bytes(rows, dim))
+
+
+def ssd_layer_norm_backward(dy, x, weight, mean, rstd, dresidual=None, rms=False, want_dbias=True,
+                            want_dresidual=False, workspace=None, out=None, stream=None):
+    """Gradients of ssd_layer_norm: x is what it normalised (its sum, or its
+    x), mean (None for rms) and rstd its statistics, ``dresidual`` (x's dtype)
+    the gradient arriving at the residual stream.  Returns a dict of dx (dy's
+    dtype), dweight, dbias (fp32; None unless ``want_dbias``) and dresidual
+    (dx in x's dtype, for the stream; None unless ``want_dresidual``)."""
+    D = dy.shape[-1]
+    rows = dy.numel() // max(D, 1)
+    shp, st = tuple(dy.shape), tuple(dy.shape[:-1])
+    _req(dy, "dy", shp, _IO)
+    _req(x, "x", shp, _IO)
+    _req(weight, "weight", (D,), _F32)
+    _req(rstd, "rstd", st, _F32)
+    if not rms:
+        _req(mean, "mean", st, _F32)
+    _opt(dresidual, "dresidual", shp, (x.dtype,))
+    want = dict(dx=(True, shp, dy.dtype), dweight=(True, (D,), torch.float32),
+                dbias=(want_dbias, (D,), torch.float32), dresidual=(want_dresidual, shp, x.dtype))
+    given = dict(out or {})
+    r = {}
+    for k, (wanted, s, t) in want.items():
+        r[k] = None
+        if wanted:
+            r[k] = given[k] if given.get(k) is not None else torch.empty(s, device=dy.device, dtype=t)
+            _req(r[k], k, s, (t,))
+    lib = load_library()
+    workspace, wsb = _workspace(workspace, lib.ssd_layer_norm_backward_workspace_bytes, (rows, D), dy.device)
+    check(lib.ssd_layer_norm_backward(rows, D, _ptr(dy), _DT[dy.dtype], _ptr(x), _DT[x.dtype], _ptr(weight),
+                                      _ptr(None if rms else mean), _ptr(rstd), int(rms), _ptr(dresidual),
+                                      _ptr(r["dx"]), _ptr(r["dresidual"]), _ptr(r["dweight"]), _ptr(r["dbias"]),
+                                      _ptr(workspace), wsb, _stream(stream)))
+    return r
