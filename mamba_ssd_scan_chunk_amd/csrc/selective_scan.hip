@@ -13,8 +13,8 @@
 // channel.
 //
 // One wave takes 64 channels (a lane each) and a chunk of tokens; states stay
-// in LDS, four of them in registers at a time over 16 tokens.  B and C are the
-// same for all lanes, so they come through scalar loads as scalar operands.
+// in LDS, one at a time in a register over 16 tokens whose time steps, inputs
+// and outputs stay in registers.  B and C come as scalar operands.
 // Where channels alone leave compute units idle the tokens are split: a first
 // pass takes every chunk's state from zero, a second carries the states from
 // chunk to chunk (decays multiply as exp of the summed dt), and the last
@@ -25,6 +25,51 @@
 
 namespace ssd {
 
+// Packs B and C to [B,G,tile,N][kEntry] in fp32 (tokens past the row: zero),
+// A log2(e) to [N,D], and the sequence starts to a bit a token.  Small beside
+// the scan (2 G N of each token's elements against 3 D or more), it spares the
+// inner loops the address arithmetic and the widening of scalars.
+template <class IO>
+__global__ __launch_bounds__(256) void scan_pack_kernel(ScanArgs a, ScanGrid g, ScanWs ws) {
+  typedef typename IO::type T;
+  const int64_t N = a.N, nbc = a.B * a.G * g.ntile * N * kEntry, na = N * a.D, ns = ws.starts ? a.B * g.ntile : 0;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < nbc + na + ns; i += (int64_t)gridDim.x * 256) {
+    if (i < nbc) {
+      // consecutive threads take consecutive states of one token: reads in rows
+      const int64_t n = i % N, r = i / N;
+      const int tok = (int)(r % kScanT), isC = (int)(r / kScanT % 2);
+      const int64_t tile = r / kEntry % g.ntile, bg = r / kEntry / g.ntile;
+      const int64_t grp = bg % a.G, b = bg / a.G, t = tile * kScanT + tok;
+      float v = 0.f;
+      if (t < a.L)
+        v = isC ? IO::get(static_cast<const T*>(a.Cm)[(b * a.L + t) * a.rows.c + grp * N + n])
+                : IO::get(static_cast<const T*>(a.Bm)[(b * a.L + t) * a.rows.b + grp * N + n]);
+      ws.bc[((bg * g.ntile + tile) * N + n) * kEntry + tok / kHalf * kScanT + isC * kHalf + tok % kHalf] = v;
+    } else if (i < nbc + na) {
+      const int64_t k = i - nbc;
+      ws.a2[k] = a.A[k % a.D * N + k / a.D] * kLog2e;
+    } else {
+      const int64_t k = i - nbc - na, b = k / g.ntile, t0 = k % g.ntile * kScanT;
+      const int* sq = a.seq_idx + b * a.L;
+      uint32_t m = 0;
+      for (int e = 0; e < kScanT; ++e) {
+        const int64_t t = t0 + e;
+        if (t > 0 && t < a.L && sq[t] != sq[t - 1]) m |= 1u << e;
+      }
+      ws.starts[k] = m;
+    }
+  }
+}
+
+hipError_t launch_scan_pack(const ScanArgs& a, const ScanGrid& g, const ScanWs& ws, bool bf16, hipStream_t s) {
+  const int64_t n = a.B * a.G * g.ntile * a.N * kEntry + a.N * a.D + a.B * g.ntile;
+  const int64_t blocks = (n + 1023) / 1024;
+  const dim3 grid((unsigned)(blocks < 8192 ? blocks : 8192));
+  if (bf16) hipLaunchKernelGGL((scan_pack_kernel<IoBF16>), grid, dim3(256), 0, s, a, g, ws);
+  else hipLaunchKernelGGL((scan_pack_kernel<IoF32>), grid, dim3(256), 0, s, a, g, ws);
+  return hipGetLastError();
+}
+
 // State passes: FINAL writes outputs from the chunk's entering state, else
 // only the state the chunk leaves and its summed dt.
 template <class IO, bool PACKED, bool FINAL>
@@ -34,92 +79,103 @@ __global__ __launch_bounds__(64) void scan_chunk_kernel(ScanArgs a, ScanGrid g, 
   const int lane = threadIdx.x;
   const ScanBlock k = scan_block(g, a);
   const int N = (int)a.N;
-  float* hs = lds;  // h[n][lane]
+  float* hs = lds + lane;   // hs[n*64]: state
+  float* as = hs + N * 64;  // as[n*64]: A log2(e)
   const int64_t d = k.d0 + lane < k.dend ? k.d0 + lane : k.dend - 1;
   const bool ok = k.d0 + lane < k.dend;
 
   const float* h_in = nullptr;
   if (FINAL && g.nc > 1) h_in = ws.carry + (k.b * g.nc + k.c) * N * a.D;
   if (k.c == 0) h_in = a.h0 ? a.h0 + k.b * N * a.D : nullptr;
-  for (int n = 0; n < N; ++n) hs[n * 64 + lane] = h_in ? h_in[(int64_t)n * a.D + d] : 0.f;
+  for (int n = 0; n < N; ++n) {
+    hs[n * 64] = h_in ? h_in[(int64_t)n * a.D + d] : 0.f;
+    as[n * 64] = ws.a2[(int64_t)n * a.D + d];
+  }
   const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
   const float skip = a.D_skip ? a.D_skip[d] : 0.f;
   const int64_t row0 = k.b * a.L;
-  const T* up = static_cast<const T*>(a.u) + row0 * a.rows.u + d;
-  const T* dp = static_cast<const T*>(a.dt) + row0 * a.rows.dt + d;
-  const T* zp = a.z ? static_cast<const T*>(a.z) + row0 * a.rows.z + d : nullptr;
-  const T* Bp = static_cast<const T*>(a.Bm) + row0 * a.rows.b + k.grp * N;
-  const T* Cp = static_cast<const T*>(a.Cm) + row0 * a.rows.c + k.grp * N;
-  const int* sq = PACKED ? a.seq_idx + row0 : nullptr;
-  T* yp = FINAL ? static_cast<T*>(a.y) + row0 * a.D + d : nullptr;
+  const int off = (int)(d * sizeof(T));
+  const T* up = static_cast<const T*>(a.u) + row0 * a.rows.u;
+  const T* dp = static_cast<const T*>(a.dt) + row0 * a.rows.dt;
+  const T* zp = a.z ? static_cast<const T*>(a.z) + row0 * a.rows.z : nullptr;
+  T* yp = FINAL ? static_cast<T*>(a.y) + row0 * a.D : nullptr;
+  const float* ep = ws.bc + (((k.b * a.G + k.grp) * g.ntile + k.t0 / kScanT) * N) * kEntry;
+  BCHalf<FINAL> lo, hi;
+  lo.load(ep);
+  float a2n = as[0], hn = hs[0];
+  RawTile<IO> ru, rd, rz;
+  ru.load(up, a.rows.u, k.t0, tile_tokens(k, k.t0), off);
+  rd.load(dp, a.rows.dt, k.t0, tile_tokens(k, k.t0), off);
 
   float sdt = 0.f;
   bool restarted = false;
   for (int64_t t0 = k.t0; t0 < k.t1; t0 += kScanT) {
-    const int nt = (int)(k.t1 - t0 < kScanT ? k.t1 - t0 : kScanT);
+    const int nt = tile_tokens(k, t0);
+    const uint32_t starts = PACKED ? ws.starts[k.b * g.ntile + t0 / kScanT] : 0;
     float dt[kScanT], x[kScanT], y[kScanT];
-    uint32_t starts = 0;  // bit i: token t0 + i begins another sequence
+    time_steps<IO>(rd, bias, a.softplus, nt, dt);
 #pragma unroll
     for (int i = 0; i < kScanT; ++i) {
-      const int64_t t = t0 + (i < nt ? i : nt - 1);
-      const float u = IO::get(up[t * a.rows.u]);
-      const float raw = IO::get(dp[t * a.rows.dt]) + bias;
-      const float v = a.softplus ? softplus(raw) : raw;
-      dt[i] = i < nt ? v : 0.f;          // tokens past the chunk: decay 1, input 0
-      x[i] = i < nt ? v * u : 0.f;
-      if (FINAL) y[i] = skip * u;
-      if (PACKED && i < nt && t > 0 && sq[t] != sq[t - 1]) starts |= 1u << i;
+      x[i] = dt[i] * ru.at(i);
+      if (FINAL) y[i] = skip * ru.at(i);
+    }
+    if (nt < kScanT) {  // past the row u is the last token's, which may be anything
+#pragma unroll
+      for (int i = 0; i < kScanT; ++i)
+        if (i >= nt) x[i] = 0.f;
+    }
+    // the gate of this tile and the next tile's inputs arrive behind the states
+    if (FINAL && zp) rz.load(zp, a.rows.z, t0, nt, off);
+    if (t0 + kScanT < k.t1) {
+      ru.load(up, a.rows.u, t0 + kScanT, tile_tokens(k, t0 + kScanT), off);
+      rd.load(dp, a.rows.dt, t0 + kScanT, tile_tokens(k, t0 + kScanT), off);
     }
     if (!FINAL) {
 #pragma unroll
-      for (int i = 0; i < kScanT; ++i) {
-        sdt = (PACKED && (starts >> i & 1)) ? dt[i] : sdt + dt[i];
-      }
+      for (int i = 0; i < kScanT; ++i) sdt = (PACKED && (starts >> i & 1)) ? dt[i] : sdt + dt[i];
       if (PACKED) restarted = restarted || starts != 0;
     }
-    for (int n0 = 0; n0 < N; n0 += 4) {
-      const float4 av = *reinterpret_cast<const float4*>(a.A + d * N + n0);
-      const float a2[4] = {av.x * kLog2e, av.y * kLog2e, av.z * kLog2e, av.w * kLog2e};
-      float h[4];
+    for (int n = 0; n < N; ++n) {
+      const float a2 = a2n;
+      float h = hn;
+      lo.settle();
+      hi.load(ep + kScanT);
+      const int nn = n + 1 == N ? 0 : (n + 1) * 64;
+      a2n = as[nn];
+      hn = hs[nn];
+      auto half = [&](const BCHalf<FINAL>& e, int i0) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) h[s] = hs[(n0 + s) * 64 + lane];
-#pragma unroll
-      for (int i = 0; i < kScanT; ++i) {
-        const int64_t t = t0 + (i < nt ? i : nt - 1);
-        float bv[4], cv[4];
-        uniform4<IO>(Bp + t * a.rows.b + n0, bv);
-        if (FINAL) uniform4<IO>(Cp + t * a.rows.c + n0, cv);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const float dec = fast_exp2(dt[i] * a2[s]);
-          const float hp = (PACKED && (starts >> i & 1)) ? 0.f : h[s];
-          h[s] = fmaf(dec, hp, x[i] * bv[s]);
-          if (FINAL) y[i] = fmaf(cv[s], h[s], y[i]);
+        for (int i = i0; i < i0 + kHalf; ++i) {
+          const float dec = fast_exp2(dt[i] * a2);
+          if (PACKED && (starts >> i & 1)) h = 0.f;
+          h = fmaf(dec, h, x[i] * e.b(i - i0));
+          if (FINAL) y[i] = fmaf(e.c(i - i0), h, y[i]);
         }
-      }
-#pragma unroll
-      for (int s = 0; s < 4; ++s) hs[(n0 + s) * 64 + lane] = h[s];
+      };
+      half(lo, 0);
+      hi.settle();
+      ep += kEntry;
+      lo.load(ep);
+      half(hi, kHalf);
+      hs[n * 64] = h;
     }
     if (FINAL) {
+      if (zp) {
 #pragma unroll
-      for (int i = 0; i < kScanT; ++i) {
-        if (i < nt) {
-          float o = y[i];
-          if (zp) {
-            const float z = IO::get(zp[(t0 + i) * a.rows.z]);
-            o *= z * sigmoid(z);
-          }
-          if (ok) yp[(t0 + i) * a.D] = IO::put(o);
+        for (int i = 0; i < kScanT; ++i) {
+          const float z = rz.at(i);
+          y[i] *= z * sigmoid(z);
         }
       }
+      if (ok) store_tile<IO>(yp, a.D, t0, nt, off, y);
     }
   }
   if (FINAL) {
     if (k.c == g.nc - 1 && a.hfin && ok)
-      for (int n = 0; n < N; ++n) a.hfin[(k.b * N + n) * a.D + d] = hs[n * 64 + lane];
+      for (int n = 0; n < N; ++n) a.hfin[(k.b * N + n) * a.D + d] = hs[n * 64];
   } else if (ok) {
     float* o = ws.carry + (k.b * g.nc + k.c) * N * a.D + d;
-    for (int n = 0; n < N; ++n) o[(int64_t)n * a.D] = hs[n * 64 + lane];
+    for (int n = 0; n < N; ++n) o[(int64_t)n * a.D] = hs[n * 64];
     ws.sdt[(k.b * g.nc + k.c) * a.D + d] = sdt;
     if (PACKED && lane == 0 && k.d0 == 0) ws.cut[k.b * g.nc + k.c] = restarted;
   }
@@ -190,6 +246,23 @@ __global__ __launch_bounds__(64) void scan_seq_states_kernel(ScanArgs a, ScanGri
   a.seq_states[(s * N + n) * a.D + d] = h;
 }
 
+// Four consecutive elements at an address that is the same for all lanes
+// (4-byte aligned): scalar loads, widened on the scalar unit.
+template <class IO>
+__device__ __forceinline__ void uniform4(const typename IO::type* p, float (&o)[4]) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
+  if constexpr (IO::kVec == 8) {
+    const uint32_t w0 = w[0], w1 = w[1];
+    o[0] = __uint_as_float(w0 << 16);
+    o[1] = __uint_as_float(w0 & 0xffff0000u);
+    o[2] = __uint_as_float(w1 << 16);
+    o[3] = __uint_as_float(w1 & 0xffff0000u);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = __uint_as_float(w[k]);
+  }
+}
+
 // Single-token step.  A lane takes one channel and all its states; the states
 // (8 bytes each, read and written) bound it.
 template <class IO>
@@ -241,34 +314,58 @@ static ScanGrid forward_grid(int64_t B, int64_t L, int64_t D, int64_t G) {
   ScanGrid g;
   g.ncb = (D / G + 63) / 64;
   const int64_t waves = B * G * g.ncb, want = (int64_t)device_cu_count() * 16;
-  int64_t nc = (want + waves - 1) / waves;
+  int64_t nc = want / waves;  // rounded down: one wave too many would run in a round of its own
   const int64_t most = (L + 63) / 64;
   if (nc > most) nc = most;
   if (nc < 1) nc = 1;
   g.Q = ((L + nc - 1) / nc + kScanT - 1) / kScanT * kScanT;
   g.nc = (L + g.Q - 1) / g.Q;
+  g.ntile = (L + kScanT - 1) / kScanT;
   return g;
 }
 
 static size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
+struct FwdLayout {
+  size_t carry, sdt, cut, bc, a2, starts, total;
+};
+static FwdLayout forward_layout(const ScanGrid& g, int64_t B, int64_t D, int64_t N, int64_t G) {
+  FwdLayout w;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { const size_t r = o; o += up256(bytes); return r; };
+  const int64_t nc = g.nc > 1 ? g.nc : 0;  // nothing is carried inside one chunk
+  w.carry = take(sizeof(float) * B * nc * N * D);
+  w.sdt = take(sizeof(float) * B * nc * D);
+  w.cut = take(sizeof(int) * B * nc);
+  w.bc = take(sizeof(float) * scan_bc_floats(B, G, g.ntile, N));
+  w.a2 = take(sizeof(float) * N * D);
+  w.starts = take(sizeof(uint32_t) * B * g.ntile);
+  w.total = o;
+  return w;
+}
 size_t scan_forward_ws_bytes(int64_t B, int64_t L, int64_t D, int64_t N, int64_t G) {
-  const ScanGrid g = forward_grid(B, L, D, G);
-  if (g.nc == 1) return 0;
-  return up256(sizeof(float) * B * g.nc * N * D) + up256(sizeof(float) * B * g.nc * D) +
-         up256(sizeof(int) * B * g.nc);
+  return forward_layout(forward_grid(B, L, D, G), B, D, N, G).total;
 }
 
 template <class IO, bool PACKED>
 static hipError_t scan_forward_t(const ScanArgs& a, hipStream_t s) {
   const ScanGrid g = forward_grid(a.B, a.L, a.D, a.G);
-  ScanWs ws = {};
+  const FwdLayout w = forward_layout(g, a.B, a.D, a.N, a.G);
   char* base = static_cast<char*>(a.ws);
-  ws.carry = reinterpret_cast<float*>(base);
-  ws.sdt = reinterpret_cast<float*>(base + up256(sizeof(float) * a.B * g.nc * a.N * a.D));
-  ws.cut = reinterpret_cast<int*>(reinterpret_cast<char*>(ws.sdt) + up256(sizeof(float) * a.B * g.nc * a.D));
-  const size_t lds = 64 * sizeof(float) * a.N;  // 64 KB at N = 256
-  hipError_t e;
+  auto at = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
+  const ScanWs ws = {at(w.carry), at(w.sdt), reinterpret_cast<int*>(base + w.cut), nullptr, at(w.bc), at(w.a2),
+                     PACKED ? reinterpret_cast<uint32_t*>(base + w.starts) : nullptr};
+  const size_t lds = 2 * 64 * sizeof(float) * a.N;
+  hipError_t e = launch_scan_pack(a, g, ws, IO::kVec == 8, s);
+  if (e != hipSuccess) return e;
+  if (lds > 64 * 1024) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&scan_chunk_kernel<IO, PACKED, false>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&scan_chunk_kernel<IO, PACKED, true>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
   if (g.nc > 1) {
     const dim3 grid((unsigned)(a.G * g.ncb), (unsigned)(g.nc - 1), (unsigned)a.B);
     hipLaunchKernelGGL((scan_chunk_kernel<IO, PACKED, false>), grid, dim3(64), lds, s, a, g, ws);

@@ -1,24 +1,31 @@
 // selective_scan.hpp -- what the selective scan's forward and backward kernels
-// share: the split of the work over waves and the scalar loads of B and C.
+// share: the split of the work over waves, and the packed form of B, C and A
+// that their inner loops read.
 #pragma once
+
+#include <type_traits>
 
 #include "layer_device.hpp"
 #include "layer_launch.hpp"
 
 namespace ssd {
 
-constexpr int kScanT = 16;  // tokens held in registers at a time
+constexpr int kScanT = 16;  // tokens held in registers at a time (a tile)
 
 struct ScanGrid {
-  int64_t Q, nc;  // tokens a chunk (a multiple of kScanT), chunks
-  int64_t ncb;    // blocks of 64 channels per group
+  int64_t Q, nc;     // tokens a chunk (a multiple of kScanT), chunks
+  int64_t ncb;       // blocks of 64 channels per group
+  int64_t ntile;     // tiles of a row
 };
 
 struct ScanWs {
-  float* carry;  // [B,nc,N,D] states
-  float* sdt;    // [B,nc,D] summed dt of a chunk (since its last restart)
-  int* cut;      // [B,nc] whether a sequence starts inside the chunk
-  float* adj;    // backward: [B,nc,N,D] adjoint states
+  float* carry;      // [B,nc,N,D] states
+  float* sdt;        // [B,nc,D] summed dt of a chunk (since its last restart)
+  int* cut;          // [B,nc] whether a sequence starts inside the chunk
+  float* adj;        // backward: [B,nc,N,D] adjoint states
+  float* bc;         // [B,G,ntile,N][kEntry] fp32, and one entry more
+  float* a2;         // [N,D] A log2(e)
+  uint32_t* starts;  // [B,ntile] bit i: token i of the tile begins another sequence
 };
 
 struct ScanBlock {
@@ -40,34 +47,94 @@ __device__ __forceinline__ ScanBlock scan_block(const ScanGrid& g, const ScanArg
   return k;
 }
 
-// Four consecutive elements at an address that is the same for all lanes
-// (4-byte aligned): scalar loads, widened on the scalar unit.
+// B and C of one state over the 16 tokens of a tile, in two halves.  They are
+// the same for all lanes (channels), so they are read by scalar loads of 64
+// bytes and feed the vector ALU as scalar operands.  Scalar loads return out
+// of order and can only be waited for all together: `settle` makes the half in
+// hand arrive before the next one is asked for, whose latency then hides
+// behind the arithmetic of this one (and of the SIMD's other waves).
+typedef float f32x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+constexpr int kHalf = kScanT / 2;
+constexpr int kEntry = 2 * kScanT;  // floats of a state's [B0-7 | C0-7 | B8-15 | C8-15]
+template <bool WANT_C>
+struct BCHalf {
+  typedef std::conditional_t<WANT_C, f32x16_t, f32x8_t> vec;
+  vec v;
+  __device__ __forceinline__ void load(const float* p) {
+    v = *(const __attribute__((address_space(4))) vec*)(uintptr_t)p;
+  }
+  __device__ __forceinline__ void settle() { asm volatile("" : "+s"(v)); }
+  __device__ __forceinline__ float b(int i) const { return v[i]; }
+  __device__ __forceinline__ float c(int i) const { return v[kHalf + i]; }
+};
+
+// Tokens of the tile at t0 (uniform, kept in 32 bits).
+__device__ __forceinline__ int tile_tokens(const ScanBlock& k, int64_t t0) {
+  return __builtin_amdgcn_readfirstlane((int)(k.t1 - t0 < kScanT ? k.t1 - t0 : kScanT));
+}
+
+// Raw elements of a tile, one channel a lane: buffer loads from the tile's
+// first row, the token's row as the scalar offset (the last token's again past
+// the tile's nt tokens), `off` the lane's byte offset in a row.
 template <class IO>
-__device__ __forceinline__ void uniform4(const typename IO::type* p, float (&o)[4]) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
-  if constexpr (IO::kVec == 8) {
-    const uint32_t w0 = w[0], w1 = w[1];
-    o[0] = __uint_as_float(w0 << 16);
-    o[1] = __uint_as_float(w0 & 0xffff0000u);
-    o[2] = __uint_as_float(w1 << 16);
-    o[3] = __uint_as_float(w1 & 0xffff0000u);
-  } else {
+struct RawTile {
+  typename IO::type v[kScanT];
+  __device__ __forceinline__ void load(const typename IO::type* base, int64_t row, int64_t t0, int nt, int off) {
+    constexpr int es = sizeof(typename IO::type);
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<typename IO::type*>(base + t0 * row), 0, 0x7fffffff, 0x00027000);
+    const int step = (int)row * es;
+    int so = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] = __uint_as_float(w[k]);
+    for (int i = 0; i < kScanT; ++i) {
+      if constexpr (es == 2) v[i] = __builtin_amdgcn_raw_buffer_load_b16(r, off, so, 0);
+      else v[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, so, 0));
+      so += i + 1 < nt ? step : 0;
+    }
+  }
+  __device__ __forceinline__ float at(int i) const { return IO::get(v[i]); }
+};
+// The same for storing.
+template <class IO>
+__device__ __forceinline__ void store_tile(typename IO::type* base, int64_t row, int64_t t0, int nt, int off,
+                                           const float (&v)[kScanT]) {
+  constexpr int es = sizeof(typename IO::type);
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(base + t0 * row, 0, 0x7fffffff, 0x00027000);
+  const int step = (int)row * es;
+  int so = 0;
+#pragma unroll
+  for (int i = 0; i < kScanT; ++i) {
+    if (i < nt) {
+      if constexpr (es == 2) __builtin_amdgcn_raw_buffer_store_b16(IO::put(v[i]), r, off, so, 0);
+      else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), r, off, so, 0);
+    }
+    so += step;
   }
 }
 
-// Element n of a row at an address that is the same for all lanes (the row
-// 4-byte aligned).
+// Time steps of a tile from the raw projections; zero past the tile's tokens,
+// where the decay is then 1.
 template <class IO>
-__device__ __forceinline__ float uniform1(const typename IO::type* row, int n) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(row);
-  if constexpr (IO::kVec == 8) {
-    const uint32_t v = w[n >> 1];
-    return __uint_as_float((n & 1) ? (v & 0xffff0000u) : (v << 16));
+__device__ __forceinline__ void time_steps(const RawTile<IO>& raw, float bias, bool plus, int nt, float (&dt)[kScanT]) {
+  if (plus) {
+#pragma unroll
+    for (int i = 0; i < kScanT; ++i) dt[i] = softplus(raw.at(i) + bias);
   } else {
-    return __uint_as_float(w[n]);
+#pragma unroll
+    for (int i = 0; i < kScanT; ++i) dt[i] = raw.at(i) + bias;
+  }
+  if (nt < kScanT) {
+#pragma unroll
+    for (int i = 0; i < kScanT; ++i)
+      if (i >= nt) dt[i] = 0.f;
   }
 }
+
+// Floats of the packed B and C (the entry more is what the last prefetch reads).
+inline int64_t scan_bc_floats(int64_t B, int64_t G, int64_t ntile, int64_t N) { return (B * G * ntile * N + 1) * kEntry; }
+
+// Fills ws.bc, ws.a2 and (packed sequences) ws.starts.
+hipError_t launch_scan_pack(const ScanArgs& a, const ScanGrid& g, const ScanWs& ws, bool bf16, hipStream_t s);
 
 }  // namespace ssd

@@ -30,22 +30,30 @@ struct BwdWs {
   float* dbp;    // [B nc][D]
 };
 
+// One row of the batch (b) of each input; lanes add their channel.
 template <class IO>
-struct ChunkPtrs {
+struct RowPtrs {
   typedef typename IO::type T;
-  const T *u, *dt, *z, *dy, *B, *C;
-  const int* sq;
-  __device__ __forceinline__ ChunkPtrs(const ScanArgs& a, int64_t b, int64_t grp, int64_t d) {
+  const T *u, *dt, *z, *dy;
+  __device__ __forceinline__ RowPtrs(const ScanArgs& a, int64_t b) {
     const int64_t r = b * a.L;
-    u = static_cast<const T*>(a.u) + r * a.rows.u + d;
-    dt = static_cast<const T*>(a.dt) + r * a.rows.dt + d;
-    z = a.z ? static_cast<const T*>(a.z) + r * a.rows.z + d : nullptr;
-    dy = static_cast<const T*>(a.dy) + r * a.D + d;
-    B = static_cast<const T*>(a.Bm) + r * a.rows.b + grp * a.N;
-    C = static_cast<const T*>(a.Cm) + r * a.rows.c + grp * a.N;
-    sq = a.seq_idx ? a.seq_idx + r : nullptr;
+    u = static_cast<const T*>(a.u) + r * a.rows.u;
+    dt = static_cast<const T*>(a.dt) + r * a.rows.dt;
+    z = a.z ? static_cast<const T*>(a.z) + r * a.rows.z : nullptr;
+    dy = static_cast<const T*>(a.dy) + r * a.D;
   }
 };
+
+// dy z sigmoid(z), or dy
+template <class IO>
+__device__ __forceinline__ void gated(const RawTile<IO>& rg, const RawTile<IO>& rz, bool gate, float (&g)[kScanT]) {
+#pragma unroll
+  for (int i = 0; i < kScanT; ++i) g[i] = rg.at(i);
+  if (gate) {
+#pragma unroll
+    for (int i = 0; i < kScanT; ++i) g[i] *= rz.at(i) * sigmoid(rz.at(i));
+  }
+}
 
 // Pass 1: carry = the state the chunk leaves (chunk 0 from the initial state,
 // others from zero), adj = what the chunk's outputs send back to its entering
@@ -56,39 +64,43 @@ __global__ __launch_bounds__(64) void scan_bwd_local_kernel(ScanArgs a, ScanGrid
   const int lane = threadIdx.x;
   const ScanBlock k = scan_block(g, a);
   const int N = (int)a.N;
-  float* hs = lds;
-  float* gs = lds + N * 64;
+  float* hs = lds + lane;        // hs[n*64]: state
+  float* gs = hs + N * 64;       // gs[n*64]: what goes back to the entering state
   const int64_t d = k.d0 + lane < k.dend ? k.d0 + lane : k.dend - 1;
   const bool ok = k.d0 + lane < k.dend;
   const float* h_in = k.c == 0 && a.h0 ? a.h0 + k.b * N * a.D : nullptr;
   for (int n = 0; n < N; ++n) {
-    hs[n * 64 + lane] = h_in ? h_in[(int64_t)n * a.D + d] : 0.f;
-    gs[n * 64 + lane] = 0.f;
+    hs[n * 64] = h_in ? h_in[(int64_t)n * a.D + d] : 0.f;
+    gs[n * 64] = 0.f;
   }
   const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
-  const ChunkPtrs<IO> p(a, k.b, k.grp, d);
+  const RowPtrs<IO> p(a, k.b);
+  const int off = (int)(d * sizeof(typename IO::type));
+  const float* a2p = ws.a2 + d;
+  const float* ep = ws.bc + (((k.b * a.G + k.grp) * g.ntile + k.t0 / kScanT) * N) * kEntry;
+  BCHalf<true> lo, hi;
+  lo.load(ep);
+  float a2n = a2p[0];
   float sdt = 0.f;        // since the chunk's start
   float last = 0.f;       // since its last restart
   bool cut = false;
   for (int64_t t0 = k.t0; t0 < k.t1; t0 += kScanT) {
-    const int nt = (int)(k.t1 - t0 < kScanT ? k.t1 - t0 : kScanT);
+    const int nt = tile_tokens(k, t0);
     float dt[kScanT], x[kScanT], dy[kScanT];
-    uint32_t starts = 0;
+    const uint32_t starts = PACKED ? ws.starts[k.b * g.ntile + t0 / kScanT] : 0;
+    RawTile<IO> ru, rd, rg, rz;
+    rd.load(p.dt, a.rows.dt, t0, nt, off);
+    ru.load(p.u, a.rows.u, t0, nt, off);
+    rg.load(p.dy, a.D, t0, nt, off);
+    if (p.z) rz.load(p.z, a.rows.z, t0, nt, off);
+    time_steps<IO>(rd, bias, a.softplus, nt, dt);
+    gated<IO>(rg, rz, p.z, dy);
 #pragma unroll
-    for (int i = 0; i < kScanT; ++i) {
-      const int64_t t = t0 + (i < nt ? i : nt - 1);
-      const float u = IO::get(p.u[t * a.rows.u]);
-      const float raw = IO::get(p.dt[t * a.rows.dt]) + bias;
-      const float v = a.softplus ? softplus(raw) : raw;
-      float gy = IO::get(p.dy[t * a.D]);
-      if (p.z) {
-        const float z = IO::get(p.z[t * a.rows.z]);
-        gy *= z * sigmoid(z);
-      }
-      dt[i] = i < nt ? v : 0.f;
-      x[i] = i < nt ? v * u : 0.f;
-      dy[i] = i < nt ? gy : 0.f;
-      if (PACKED && i < nt && t > 0 && p.sq[t] != p.sq[t - 1]) starts |= 1u << i;
+    for (int i = 0; i < kScanT; ++i) x[i] = dt[i] * ru.at(i);
+    if (nt < kScanT) {  // past the row: decay 1, nothing added
+#pragma unroll
+      for (int i = 0; i < kScanT; ++i)
+        if (i >= nt) x[i] = dy[i] = 0.f;
     }
     // tokens of this step that still reach the chunk's entering state
     const int live = cut ? 0 : (starts ? __builtin_ctz(starts) : kScanT);
@@ -98,45 +110,38 @@ __global__ __launch_bounds__(64) void scan_bwd_local_kernel(ScanArgs a, ScanGrid
       last = (PACKED && (starts >> i & 1)) ? dt[i] : last + dt[i];
       sdt += dt[i];
     }
-    for (int n0 = 0; n0 < N; n0 += 4) {
-      const float4 av = *reinterpret_cast<const float4*>(a.A + d * N + n0);
-      const float a2[4] = {av.x * kLog2e, av.y * kLog2e, av.z * kLog2e, av.w * kLog2e};
-      float h[4], acc[4], pr[4];
+    for (int n = 0; n < N; ++n) {
+      const float a2 = a2n;
+      lo.settle();
+      hi.load(ep + kScanT);
+      a2n = a2p[(int64_t)(n + 1 < N ? n + 1 : 0) * a.D];
+      float h = hs[n * 64], acc = gs[n * 64], pr = fast_exp2(sdt0 * a2);
+      auto half = [&](const BCHalf<true>& e, int i0) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        h[s] = hs[(n0 + s) * 64 + lane];
-        acc[s] = gs[(n0 + s) * 64 + lane];
-        pr[s] = fast_exp2(sdt0 * a2[s]);
-      }
-#pragma unroll
-      for (int i = 0; i < kScanT; ++i) {
-        const int64_t t = t0 + (i < nt ? i : nt - 1);
-        float bv[4], cv[4];
-        uniform4<IO>(p.B + t * a.rows.b + n0, bv);
-        uniform4<IO>(p.C + t * a.rows.c + n0, cv);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const float dec = fast_exp2(dt[i] * a2[s]);
-          const float hp = (PACKED && (starts >> i & 1)) ? 0.f : h[s];
-          h[s] = fmaf(dec, hp, x[i] * bv[s]);
-          pr[s] *= dec;
-          const float v = fmaf(pr[s], cv[s] * dy[i], acc[s]);
-          acc[s] = (!PACKED || i < live) ? v : acc[s];
+        for (int i = i0; i < i0 + kHalf; ++i) {
+          const float dec = fast_exp2(dt[i] * a2);
+          if (PACKED && (starts >> i & 1)) h = 0.f;
+          h = fmaf(dec, h, x[i] * e.b(i - i0));
+          pr *= dec;
+          const float v = fmaf(pr, e.c(i - i0) * dy[i], acc);
+          acc = (!PACKED || i < live) ? v : acc;
         }
-      }
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        hs[(n0 + s) * 64 + lane] = h[s];
-        gs[(n0 + s) * 64 + lane] = acc[s];
-      }
+      };
+      half(lo, 0);
+      hi.settle();
+      ep += kEntry;
+      lo.load(ep);
+      half(hi, kHalf);
+      hs[n * 64] = h;
+      gs[n * 64] = acc;
     }
     cut = cut || starts != 0;
   }
   if (ok) {
     const int64_t o = (k.b * g.nc + k.c) * N * a.D + d;
     for (int n = 0; n < N; ++n) {
-      ws.carry[o + (int64_t)n * a.D] = hs[n * 64 + lane];
-      ws.adj[o + (int64_t)n * a.D] = gs[n * 64 + lane];
+      ws.carry[o + (int64_t)n * a.D] = hs[n * 64];
+      ws.adj[o + (int64_t)n * a.D] = gs[n * 64];
     }
     ws.sdt[(k.b * g.nc + k.c) * a.D + d] = last;
     if (PACKED && lane == 0 && k.d0 == 0) ws.cut[k.b * g.nc + k.c] = cut;
@@ -263,41 +268,49 @@ __global__ __launch_bounds__(64) void scan_bwd_chunk_kernel(ScanArgs a, ScanGrid
   }
   const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
   const float skip = a.D_skip ? a.D_skip[d] : 0.f;
-  const ChunkPtrs<IO> p(a, k.b, k.grp, d);
+  const RowPtrs<IO> p(a, k.b);
+  const int off = (int)(d * sizeof(typename IO::type));
   const int nstep = (int)((k.t1 - k.t0 + kScanT - 1) / kScanT);
 
+  const float* a2p = ws.a2 + d;
+  const float* e0 = ws.bc + (((k.b * a.G + k.grp) * g.ntile + k.t0 / kScanT) * N) * kEntry;
+
   // states entering steps 1 .. nstep-1
-  for (int j = 0; j + 1 < nstep; ++j) {
-    const int64_t t0 = k.t0 + j * kScanT;
-    float dt[kScanT], x[kScanT];
-    uint32_t starts = 0;
+  if (nstep > 1) {
+    const float* ep = e0;
+    BCHalf<false> lo, hi;
+    lo.load(ep);
+    float a2n = a2p[0];
+    for (int j = 0; j + 1 < nstep; ++j) {
+      const int64_t t0 = k.t0 + j * kScanT;
+      float dt[kScanT], x[kScanT];
+      const uint32_t starts = PACKED ? ws.starts[k.b * g.ntile + t0 / kScanT] : 0;
+      RawTile<IO> ru, rd;  // whole tiles: only the last one can be ragged
+      rd.load(p.dt, a.rows.dt, t0, kScanT, off);
+      ru.load(p.u, a.rows.u, t0, kScanT, off);
+      time_steps<IO>(rd, bias, a.softplus, kScanT, dt);
 #pragma unroll
-    for (int i = 0; i < kScanT; ++i) {  // whole steps: only the last one can be ragged
-      const int64_t t = t0 + i;
-      const float raw = IO::get(p.dt[t * a.rows.dt]) + bias;
-      dt[i] = a.softplus ? softplus(raw) : raw;
-      x[i] = dt[i] * IO::get(p.u[t * a.rows.u]);
-      if (PACKED && t > 0 && p.sq[t] != p.sq[t - 1]) starts |= 1u << i;
-    }
-    for (int n0 = 0; n0 < N; n0 += 4) {
-      const float4 av = *reinterpret_cast<const float4*>(a.A + d * N + n0);
-      const float a2[4] = {av.x * kLog2e, av.y * kLog2e, av.z * kLog2e, av.w * kLog2e};
-      float h[4];
+      for (int i = 0; i < kScanT; ++i) x[i] = dt[i] * ru.at(i);
+      for (int n = 0; n < N; ++n) {
+        const float a2 = a2n;
+        lo.settle();
+        hi.load(ep + kScanT);
+        a2n = a2p[(int64_t)(n + 1 < N ? n + 1 : 0) * a.D];
+        float h = j ? hs[(j - 1) * st + n * 64] : (h_in ? h_in[(int64_t)n * a.D] : 0.f);
+        auto half = [&](const BCHalf<false>& e, int i0) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        h[s] = j ? hs[(j - 1) * st + (n0 + s) * 64] : (h_in ? h_in[(int64_t)(n0 + s) * a.D] : 0.f);
-#pragma unroll
-      for (int i = 0; i < kScanT; ++i) {
-        float bv[4];
-        uniform4<IO>(p.B + (t0 + i) * a.rows.b + n0, bv);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const float hp = (PACKED && (starts >> i & 1)) ? 0.f : h[s];
-          h[s] = fmaf(fast_exp2(dt[i] * a2[s]), hp, x[i] * bv[s]);
-        }
+          for (int i = i0; i < i0 + kHalf; ++i) {
+            if (PACKED && (starts >> i & 1)) h = 0.f;
+            h = fmaf(fast_exp2(dt[i] * a2), h, x[i] * e.b(i - i0));
+          }
+        };
+        half(lo, 0);
+        hi.settle();
+        ep += kEntry;
+        lo.load(ep);
+        half(hi, kHalf);
+        hs[j * st + n * 64] = h;
       }
-#pragma unroll
-      for (int s = 0; s < 4; ++s) hs[j * st + (n0 + s) * 64] = h[s];
     }
   }
 
@@ -308,96 +321,122 @@ __global__ __launch_bounds__(64) void scan_bwd_chunk_kernel(ScanArgs a, ScanGrid
   float* dCp = dBp + g.ncb * BL * GN;
   for (int j = nstep - 1; j >= 0; --j) {
     const int64_t t0 = k.t0 + j * kScanT;
-    const int nt = (int)(k.t1 - t0 < kScanT ? k.t1 - t0 : kScanT);
+    const int nt = tile_tokens(k, t0);
     float dt[kScanT], x[kScanT], gy[kScanT], y[kScanT], sB[kScanT], sA[kScanT];
-    uint32_t starts = 0;
+    const uint32_t starts = PACKED ? ws.starts[k.b * g.ntile + t0 / kScanT] : 0;
+    {
+      RawTile<IO> ru, rd, rg, rz;
+      rd.load(p.dt, a.rows.dt, t0, nt, off);
+      ru.load(p.u, a.rows.u, t0, nt, off);
+      rg.load(p.dy, a.D, t0, nt, off);
+      if (p.z) rz.load(p.z, a.rows.z, t0, nt, off);
+      time_steps<IO>(rd, bias, a.softplus, nt, dt);
+      gated<IO>(rg, rz, p.z, gy);
+#pragma unroll
+      for (int i = 0; i < kScanT; ++i) {
+        x[i] = dt[i] * ru.at(i);
+        y[i] = skip * ru.at(i);
+        sB[i] = 0.f;
+        sA[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kScanT; ++i)
+        if (i >= nt || !ok) x[i] = gy[i] = 0.f;  // lanes past the group add nothing to its sums
+    }
+    const float* ep = e0 + (int64_t)j * N * kEntry;
+    BCHalf<true> lo, hi;
+    lo.load(ep);
+    hi.load(ep + kScanT);
+    auto bv = [&](int i) { return i < kHalf ? lo.b(i) : hi.b(i - kHalf); };
+    auto cv = [&](int i) { return i < kHalf ? lo.c(i) : hi.c(i - kHalf); };
+    float a2n = a2p[0];
+    float rB[4] = {}, rC[4] = {};  // the last four states' sums
+    for (int n = 0; n < N; ++n) {
+      const float a2 = a2n;
+      a2n = a2p[(int64_t)(n + 1 < N ? n + 1 : 0) * a.D];
+      float dec[kScanT], h[kScanT], v[kScanT];
+      const float h0 = j ? hs[(j - 1) * st + n * 64] : (h_in ? h_in[(int64_t)n * a.D] : 0.f);
+      float hp = h0;
+#pragma unroll
+      for (int i = 0; i < kScanT; ++i) {
+        dec[i] = fast_exp2(dt[i] * a2);
+        if (PACKED && (starts >> i & 1)) hp = 0.f;
+        hp = fmaf(dec[i], hp, x[i] * bv(i));
+        h[i] = hp;
+        y[i] = fmaf(cv(i), hp, y[i]);
+        v[i] = hp * gy[i];
+      }
+      const float sC = lane_sum16(v, lane);
+      float ga = gs[n * 64], dA = as[n * 64];
+#pragma unroll
+      for (int i = kScanT - 1; i >= 0; --i) {
+        const float gt = fmaf(cv(i), gy[i], ga);
+        v[i] = gt * x[i];
+        sB[i] = fmaf(gt, bv(i), sB[i]);
+        ga = gt * dec[i];
+        float q = ga * (i ? h[i > 0 ? i - 1 : 0] : h0);
+        if (PACKED && (starts >> i & 1)) {
+          ga = 0.f;
+          q = 0.f;
+        }
+        sA[i] = fmaf(a2, q, sA[i]);  // in units of log2(e)
+        dA = fmaf(dt[i], q, dA);
+      }
+      // B and C are in use up to here; the next entry arrives behind the sums
+      ep += kEntry;
+      lo.load(ep);
+      hi.load(ep + kScanT);
+      gs[n * 64] = ga;
+      as[n * 64] = dA;
+#pragma unroll
+      for (int e = 0; e < 3; ++e) {
+        rB[e] = rB[e + 1];
+        rC[e] = rC[e + 1];
+      }
+      rC[3] = sC;
+      rB[3] = lane_sum16(v, lane);
+      if ((n & 3) == 3) {
+        const float vB = lane_sum4(rB, lane), vC = lane_sum4(rC, lane);
+        const int i = lane >> 2;
+        if (i < nt) {
+          dBp[(t0 + i) * GN + n - 3 + (lane & 3)] = vB;
+          dCp[(t0 + i) * GN + n - 3 + (lane & 3)] = vC;
+        }
+      }
+    }
+    // gradients of this tile's tokens (its inputs once more, from cache)
+    const int64_t r0 = k.b * a.L;
+    RawTile<IO> ru, rd, rg, rz;
+    ru.load(p.u, a.rows.u, t0, nt, off);
+    if (a.softplus) rd.load(p.dt, a.rows.dt, t0, nt, off);
+    if (p.z) {
+      rg.load(p.dy, a.D, t0, nt, off);
+      rz.load(p.z, a.rows.z, t0, nt, off);
+    }
 #pragma unroll
     for (int i = 0; i < kScanT; ++i) {
-      const int64_t t = t0 + (i < nt ? i : nt - 1);
-      const float u = IO::get(p.u[t * a.rows.u]);
-      const float raw = IO::get(p.dt[t * a.rows.dt]) + bias;
-      const float v = a.softplus ? softplus(raw) : raw;
-      float q = IO::get(p.dy[t * a.D]);
-      if (p.z) {
-        const float z = IO::get(p.z[t * a.rows.z]);
-        q *= z * sigmoid(z);
-      }
-      const bool in = i < nt && ok;  // lanes past the group add nothing to its sums
-      dt[i] = i < nt ? v : 0.f;
-      x[i] = in ? v * u : 0.f;
-      gy[i] = in ? q : 0.f;
-      y[i] = skip * u;
-      sB[i] = 0.f;
-      sA[i] = 0.f;
-      if (PACKED && i < nt && t > 0 && p.sq[t] != p.sq[t - 1]) starts |= 1u << i;
+      sA[i] = fmaf(sB[i], ru.at(i), sA[i] * kLn2);
+      sB[i] = fmaf(dt[i], sB[i], skip * gy[i]);
     }
-    for (int n0 = 0; n0 < N; n0 += 4) {
-      const float4 av = *reinterpret_cast<const float4*>(a.A + d * N + n0);
-      const float an[4] = {av.x, av.y, av.z, av.w};
-      float rB[4], rC[4];
+    if (a.softplus) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int n = n0 + s;
-        const float a2 = an[s] * kLog2e;
-        float dec[kScanT], h[kScanT], v[kScanT];
-        const float h0 = j ? hs[(j - 1) * st + n * 64] : (h_in ? h_in[(int64_t)n * a.D] : 0.f);
-        float hp = h0;
-#pragma unroll
-        for (int i = 0; i < kScanT; ++i) {
-          const int64_t t = t0 + (i < nt ? i : nt - 1);
-          dec[i] = fast_exp2(dt[i] * a2);
-          if (PACKED && (starts >> i & 1)) hp = 0.f;
-          hp = fmaf(dec[i], hp, x[i] * uniform1<IO>(p.B + t * a.rows.b, n));
-          h[i] = hp;
-          if (p.z) y[i] = fmaf(uniform1<IO>(p.C + t * a.rows.c, n), hp, y[i]);
-          v[i] = hp * gy[i];
-        }
-        rC[s] = lane_sum16(v, lane);
-        float ga = gs[n * 64], dA = as[n * 64];
-#pragma unroll
-        for (int i = kScanT - 1; i >= 0; --i) {
-          const int64_t t = t0 + (i < nt ? i : nt - 1);
-          const float gt = fmaf(uniform1<IO>(p.C + t * a.rows.c, n), gy[i], ga);
-          v[i] = gt * x[i];
-          sB[i] = fmaf(gt, uniform1<IO>(p.B + t * a.rows.b, n), sB[i]);
-          ga = gt * dec[i];
-          float q = ga * (i ? h[i > 0 ? i - 1 : 0] : h0);
-          if (PACKED && (starts >> i & 1)) {
-            ga = 0.f;
-            q = 0.f;
-          }
-          sA[i] = fmaf(an[s], q, sA[i]);
-          dA = fmaf(dt[i], q, dA);
-        }
-        rB[s] = lane_sum16(v, lane);
-        gs[n * 64] = ga;
-        as[n * 64] = dA;
-      }
-      const float vB = lane_sum4(rB, lane), vC = lane_sum4(rC, lane);
-      const int i = lane >> 2;
-      if (i < nt) {
-        dBp[(t0 + i) * GN + n0 + (lane & 3)] = vB;
-        dCp[(t0 + i) * GN + n0 + (lane & 3)] = vC;
-      }
+      for (int i = 0; i < kScanT; ++i) sA[i] *= sigmoid(rd.at(i) + bias);
     }
 #pragma unroll
     for (int i = 0; i < kScanT; ++i) {
       if (i < nt) {
-        const int64_t t = t0 + i, row = k.b * a.L + t;
-        const float u = IO::get(p.u[t * a.rows.u]);
-        float ddt = fmaf(sB[i], u, sA[i]);
-        if (a.softplus) ddt *= sigmoid(IO::get(p.dt[t * a.rows.dt]) + bias);
-        dbsum += ddt;
-        dDsum = fmaf(gy[i], u, dDsum);
-        if (ok) {
-          static_cast<T*>(a.du)[row * a.grows.u + d] = IO::put(fmaf(dt[i], sB[i], skip * gy[i]));
-          static_cast<T*>(a.ddt)[row * a.grows.dt + d] = IO::put(ddt);
-          if (p.z) {
-            const float z = IO::get(p.z[t * a.rows.z]);
-            static_cast<T*>(a.dz)[row * a.grows.z + d] = IO::put(IO::get(p.dy[t * a.D]) * y[i] * dsilu(z, sigmoid(z)));
-          }
-        }
+        dbsum += sA[i];
+        dDsum = fmaf(gy[i], ru.at(i), dDsum);
       }
+    }
+    if (p.z) {
+#pragma unroll
+      for (int i = 0; i < kScanT; ++i) y[i] *= rg.at(i) * dsilu(rz.at(i), sigmoid(rz.at(i)));
+    }
+    if (ok) {
+      store_tile<IO>(static_cast<T*>(a.du) + r0 * a.grows.u, a.grows.u, t0, nt, off, sB);
+      store_tile<IO>(static_cast<T*>(a.ddt) + r0 * a.grows.dt, a.grows.dt, t0, nt, off, sA);
+      if (p.z) store_tile<IO>(static_cast<T*>(a.dz) + r0 * a.grows.z, a.grows.z, t0, nt, off, y);
     }
   }
   if (ok) {
@@ -450,13 +489,14 @@ static ScanGrid backward_grid(int64_t L, int64_t D, int64_t N, int64_t G) {
   g.ncb = (D / G + 63) / 64;
   g.Q = kScanT * (N <= 32 ? 4 : N <= 64 ? 2 : 1);
   g.nc = (L + g.Q - 1) / g.Q;
+  g.ntile = (L + kScanT - 1) / kScanT;
   return g;
 }
 
 static size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct BwdLayout {
-  size_t carry, adj, sdt, cut, bc, dDp, dbp, sums, total;
+  size_t carry, adj, sdt, cut, pack, a2, starts, bc, dDp, dbp, sums, total;
 };
 static BwdLayout backward_layout(int64_t B, int64_t L, int64_t D, int64_t N, int64_t G) {
   const ScanGrid g = backward_grid(L, D, N, G);
@@ -467,6 +507,9 @@ static BwdLayout backward_layout(int64_t B, int64_t L, int64_t D, int64_t N, int
   w.adj = take(sizeof(float) * B * g.nc * N * D);
   w.sdt = take(sizeof(float) * B * g.nc * D);
   w.cut = take(sizeof(int) * B * g.nc);
+  w.pack = take(sizeof(float) * scan_bc_floats(B, G, g.ntile, N));
+  w.a2 = take(sizeof(float) * N * D);
+  w.starts = take(sizeof(uint32_t) * B * g.ntile);
   w.bc = take(sizeof(float) * 2 * g.ncb * B * L * G * N);
   w.dDp = take(sizeof(float) * B * g.nc * D);
   w.dbp = take(sizeof(float) * B * g.nc * D);
@@ -484,7 +527,8 @@ static hipError_t scan_backward_t(const ScanArgs& a, hipStream_t s) {
   const BwdLayout w = backward_layout(a.B, a.L, a.D, a.N, a.G);
   char* base = static_cast<char*>(a.ws);
   auto at = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
-  const ScanWs ws = {at(w.carry), at(w.sdt), reinterpret_cast<int*>(base + w.cut), at(w.adj)};
+  const ScanWs ws = {at(w.carry), at(w.sdt), reinterpret_cast<int*>(base + w.cut), at(w.adj), at(w.pack), at(w.a2),
+                     PACKED ? reinterpret_cast<uint32_t*>(base + w.starts) : nullptr};
   const BwdWs bw = {at(w.bc), at(w.dDp), at(w.dbp)};
   const dim3 grid((unsigned)(a.G * g.ncb), (unsigned)g.nc, (unsigned)a.B);
   const size_t per = 64 * sizeof(float) * a.N;
@@ -498,6 +542,7 @@ static hipError_t scan_backward_t(const ScanArgs& a, hipStream_t s) {
                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds3);
     if (e != hipSuccess) return e;
   }
+  if ((e = launch_scan_pack(a, g, ws, IO::kVec == 8, s)) != hipSuccess) return e;
   hipLaunchKernelGGL((scan_bwd_local_kernel<IO, PACKED>), grid, dim3(64), lds1, s, a, g, ws);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   hipLaunchKernelGGL((scan_bwd_carry_kernel<PACKED>), dim3((unsigned)((a.B * a.N * a.D + 255) / 256), 2), dim3(256), 0,

@@ -203,6 +203,7 @@ __device__ __forceinline__ void chunk_cumsum_lane(const float (&d)[4], int E, fl
 // base-2 units (pre-multiplied by log2(e)), saving the scaling multiply.
 __device__ __forceinline__ float fast_exp2(float v) { return __builtin_amdgcn_exp2f(v); }
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 // 16-byte rows from MFMA accumulator tiles.  In the 16x16 accumulator layout
 // lane (l16, lg) holds 4 consecutive columns 4lg .. 4lg+3 of row l16 for each
