@@ -64,21 +64,23 @@ __device__ __forceinline__ void store_vec(typename IO::type* p, const float* v) 
 __device__ __forceinline__ float sigmoid(float v) {
   return __builtin_amdgcn_rcpf(1.f + fast_exp2(-v * kLog2e));
 }
+// the same of w ln 2
+__device__ __forceinline__ float sigmoid2(float w) { return __builtin_amdgcn_rcpf(1.f + fast_exp2(-w)); }
 // d/dv [v sigmoid(v)] from v and its sigmoid
 __device__ __forceinline__ float dsilu(float v, float s) { return s * fmaf(v, 1.f - s, 1.f); }
 
-// log(1 + e^v), v itself above 20 where they agree to fp32.  With e = e^v and
-// u = 1 + e rounded, log(1+e) = log(u) + (e - (u-1)) / u to first order: the
-// second term is what rounding u lost, which matters where log(u) is small;
-// there 1/u is near 1 - e/2 (above e = 2 the term is below half a unit and
-// left out).  Branch-free: about 16 issue slots against some 110 for the
-// library's log1p, whose branches also kept a tile's loads from overlapping.
-__device__ __forceinline__ float softplus(float v) {
-  const float e = fast_exp2(v * kLog2e);
+// log2(1 + 2^w).  With e = 2^w and u = 1 + e rounded it is log2(u) plus what
+// rounding u lost, log2(e) (e - (u-1)) / u to first order, which matters where
+// log2(u) is small; there 1/u is near 1 - e/2 (above e = 2 the term is below
+// half a unit and left out).  It is never below w: the maximum also covers the
+// e that overflows.  Branch-free, about a third of the library's log1p, whose
+// branches also kept a tile's loads from overlapping.
+__device__ __forceinline__ float softplus2(float w) {
+  const float e = fast_exp2(w);
   const float u = 1.f + e;
   const float lost = e - (u - 1.f);
-  const float l = fmaf(lost, fmaxf(fmaf(-0.5f, e, 1.f), 0.f), __builtin_amdgcn_logf(u) * kLn2);
-  return v > 20.f ? v : l;
+  const float l = fmaf(lost, fmaxf(fmaf(-0.5f * kLog2e, e, kLog2e), 0.f), __builtin_amdgcn_logf(u));
+  return fmaxf(l, w);
 }
 
 }  // namespace ssd

@@ -22,11 +22,12 @@
 #include "layer_device.hpp"
 #include "layer_launch.hpp"
 #include "selective_scan.hpp"
+#include <cstdlib>
 
 namespace ssd {
 
-// Packs B and C to [B,G,tile,N][kEntry] in fp32 (tokens past the row: zero),
-// A log2(e) to [N,D], and the sequence starts to a bit a token.  Small beside
+// Packs B ln 2 and C to [B,G,tile,N][kEntry] in fp32 (tokens past the row:
+// zero), A to [N,D], and the sequence starts to a bit a token.  Small beside
 // the scan (2 G N of each token's elements against 3 D or more), it spares the
 // inner loops the address arithmetic and the widening of scalars.
 template <class IO>
@@ -43,11 +44,11 @@ __global__ __launch_bounds__(256) void scan_pack_kernel(ScanArgs a, ScanGrid g, 
       float v = 0.f;
       if (t < a.L)
         v = isC ? IO::get(static_cast<const T*>(a.Cm)[(b * a.L + t) * a.rows.c + grp * N + n])
-                : IO::get(static_cast<const T*>(a.Bm)[(b * a.L + t) * a.rows.b + grp * N + n]);
+                : IO::get(static_cast<const T*>(a.Bm)[(b * a.L + t) * a.rows.b + grp * N + n]) * kLn2;
       ws.bc[((bg * g.ntile + tile) * N + n) * kEntry + tok / kHalf * kScanT + isC * kHalf + tok % kHalf] = v;
     } else if (i < nbc + na) {
       const int64_t k = i - nbc;
-      ws.a2[k] = a.A[k % a.D * N + k / a.D] * kLog2e;
+      ws.at[k] = a.A[k % a.D * N + k / a.D];
     } else {
       const int64_t k = i - nbc - na, b = k / g.ntile, t0 = k % g.ntile * kScanT;
       const int* sq = a.seq_idx + b * a.L;
@@ -73,14 +74,15 @@ hipError_t launch_scan_pack(const ScanArgs& a, const ScanGrid& g, const ScanWs& 
 // State passes: FINAL writes outputs from the chunk's entering state, else
 // only the state the chunk leaves and its summed dt.
 template <class IO, bool PACKED, bool FINAL>
-__global__ __launch_bounds__(64) void scan_chunk_kernel(ScanArgs a, ScanGrid g, ScanWs ws) {
+__global__ __launch_bounds__(64 * kScanWaves) void scan_chunk_kernel(ScanArgs a, ScanGrid g, ScanWs ws) {
   typedef typename IO::type T;
   extern __shared__ float lds[];
-  const int lane = threadIdx.x;
-  const ScanBlock k = scan_block(g, a);
+  const int lane = threadIdx.x & 63;
+  ScanBlock k;
+  if (!scan_block(g, a, k)) return;
   const int N = (int)a.N;
-  float* hs = lds + lane;   // hs[n*64]: state
-  float* as = hs + N * 64;  // as[n*64]: A log2(e)
+  float* hs = lds + k.wave * 2 * N * 64 + lane;   // hs[n*64]: state
+  float* as = hs + N * 64;  // as[n*64]: A
   const int64_t d = k.d0 + lane < k.dend ? k.d0 + lane : k.dend - 1;
   const bool ok = k.d0 + lane < k.dend;
 
@@ -89,9 +91,9 @@ __global__ __launch_bounds__(64) void scan_chunk_kernel(ScanArgs a, ScanGrid g, 
   if (k.c == 0) h_in = a.h0 ? a.h0 + k.b * N * a.D : nullptr;
   for (int n = 0; n < N; ++n) {
     hs[n * 64] = h_in ? h_in[(int64_t)n * a.D + d] : 0.f;
-    as[n * 64] = ws.a2[(int64_t)n * a.D + d];
+    as[n * 64] = ws.at[(int64_t)n * a.D + d];
   }
-  const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
+  const float bias = a.dt_bias ? a.dt_bias[d] * kLog2e : 0.f;
   const float skip = a.D_skip ? a.D_skip[d] : 0.f;
   const int64_t row0 = k.b * a.L;
   const int off = (int)(d * sizeof(T));
@@ -100,9 +102,9 @@ __global__ __launch_bounds__(64) void scan_chunk_kernel(ScanArgs a, ScanGrid g, 
   const T* zp = a.z ? static_cast<const T*>(a.z) + row0 * a.rows.z : nullptr;
   T* yp = FINAL ? static_cast<T*>(a.y) + row0 * a.D : nullptr;
   const float* ep = ws.bc + (((k.b * a.G + k.grp) * g.ntile + k.t0 / kScanT) * N) * kEntry;
-  BCHalf<FINAL> lo, hi;
-  lo.load(ep);
-  float a2n = as[0], hn = hs[0];
+  BCPair<FINAL> cur;
+  cur.load(ep);
+  float a_n = as[0], h_n = hs[0];
   RawTile<IO> ru, rd, rz;
   ru.load(up, a.rows.u, k.t0, tile_tokens(k, k.t0), off);
   rd.load(dp, a.rows.dt, k.t0, tile_tokens(k, k.t0), off);
@@ -110,6 +112,7 @@ __global__ __launch_bounds__(64) void scan_chunk_kernel(ScanArgs a, ScanGrid g, 
   float sdt = 0.f;
   bool restarted = false;
   for (int64_t t0 = k.t0; t0 < k.t1; t0 += kScanT) {
+    pace(t0 - k.t0, k.t1 - k.t0);
     const int nt = tile_tokens(k, t0);
     const uint32_t starts = PACKED ? ws.starts[k.b * g.ntile + t0 / kScanT] : 0;
     float dt[kScanT], x[kScanT], y[kScanT];
@@ -135,29 +138,32 @@ __global__ __launch_bounds__(64) void scan_chunk_kernel(ScanArgs a, ScanGrid g, 
       for (int i = 0; i < kScanT; ++i) sdt = (PACKED && (starts >> i & 1)) ? dt[i] : sdt + dt[i];
       if (PACKED) restarted = restarted || starts != 0;
     }
-    for (int n = 0; n < N; ++n) {
-      const float a2 = a2n;
-      float h = hn;
-      lo.settle();
-      hi.load(ep + kScanT);
-      const int nn = n + 1 == N ? 0 : (n + 1) * 64;
-      a2n = as[nn];
-      hn = hs[nn];
-      auto half = [&](const BCHalf<FINAL>& e, int i0) {
+    for (int n0 = 0; n0 < N; n0 += 4) {
+      // the last one's successor is the next tile's first
+      float* hq = hs + n0 * 64;
+      const float* aq = as + n0 * 64;
+      const int next = n0 + 4 < N ? 4 * 64 : -n0 * 64;
 #pragma unroll
-        for (int i = i0; i < i0 + kHalf; ++i) {
-          const float dec = fast_exp2(dt[i] * a2);
+      for (int s = 0; s < 4; ++s) {
+        const float an = a_n;
+        float h = h_n;
+        cur.settle();
+        ep += kEntry;
+        BCPair<FINAL> nxt;
+        nxt.load(ep);
+        a_n = s < 3 ? aq[(s + 1) * 64] : aq[next];
+        if (s < 3) h_n = hq[(s + 1) * 64];
+#pragma unroll
+        for (int i = 0; i < kScanT; ++i) {
+          const float dec = fast_exp2(dt[i] * an);
           if (PACKED && (starts >> i & 1)) h = 0.f;
-          h = fmaf(dec, h, x[i] * e.b(i - i0));
-          if (FINAL) y[i] = fmaf(e.c(i - i0), h, y[i]);
+          h = fmaf(dec, h, x[i] * cur.b(i));
+          if (FINAL) y[i] = fmaf(cur.c(i), h, y[i]);
         }
-      };
-      half(lo, 0);
-      hi.settle();
-      ep += kEntry;
-      lo.load(ep);
-      half(hi, kHalf);
-      hs[n * 64] = h;
+        cur = nxt;
+        hq[s * 64] = h;
+        if (s == 3) h_n = hq[next];
+      }
     }
     if (FINAL) {
       if (zp) {
@@ -188,7 +194,7 @@ __global__ __launch_bounds__(256) void scan_carry_kernel(ScanArgs a, ScanGrid g,
   const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (idx >= a.B * a.N * a.D) return;
   const int64_t d = idx % a.D, n = idx / a.D % a.N, b = idx / a.D / a.N;
-  const float a2 = a.A[d * a.N + n] * kLog2e;
+  const float an = a.A[d * a.N + n];
   float* s = ws.carry + (b * g.nc * a.N + n) * a.D + d;
   const float* sd = ws.sdt + b * g.nc * a.D + d;
   const int64_t cs = a.N * a.D;
@@ -200,7 +206,7 @@ __global__ __launch_bounds__(256) void scan_carry_kernel(ScanArgs a, ScanGrid g,
     for (int i = 0; i < U; ++i) {
       const int64_t c = c0 + i < g.nc - 1 ? c0 + i : g.nc - 2;  // the last chunk left no state
       v[i] = c > 0 ? s[c * cs] : 0.f;
-      p[i] = fast_exp2(sd[c * a.D] * a2);
+      p[i] = fast_exp2(sd[c * a.D] * an);
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
@@ -229,8 +235,8 @@ __global__ __launch_bounds__(64) void scan_seq_states_kernel(ScanArgs a, ScanGri
   if (d >= (grp + 1) * gd) return;
   const int n = blockIdx.y;
   const int N = (int)a.N;
-  const float a2 = a.A[d * N + n] * kLog2e;
-  const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
+  const float an = a.A[d * N + n];
+  const float bias = a.dt_bias ? a.dt_bias[d] * kLog2e : 0.f;
   const float* h_in = c > 0 ? ws.carry + (b * g.nc + c) * N * a.D : (a.h0 ? a.h0 + b * N * a.D : nullptr);
   float h = h_in ? h_in[(int64_t)n * a.D + d] : 0.f;
   const int64_t row0 = b * a.L;
@@ -238,10 +244,10 @@ __global__ __launch_bounds__(64) void scan_seq_states_kernel(ScanArgs a, ScanGri
   const T* dp = static_cast<const T*>(a.dt) + row0 * a.rows.dt + d;
   const T* Bp = static_cast<const T*>(a.Bm) + row0 * a.rows.b + grp * N + n;
   for (int64_t j = c * g.Q; j <= t; ++j) {
-    const float raw = IO::get(dp[j * a.rows.dt]) + bias;
-    const float dt = a.softplus ? softplus(raw) : raw;
+    const float raw = fmaf(IO::get(dp[j * a.rows.dt]), kLog2e, bias);
+    const float dt = a.softplus ? softplus2(raw) : raw;
     if (a.seq_idx && j > 0 && a.seq_idx[row0 + j] != a.seq_idx[row0 + j - 1]) h = 0.f;
-    h = fmaf(fast_exp2(dt * a2), h, dt * IO::get(up[j * a.rows.u]) * IO::get(Bp[j * a.rows.b]));
+    h = fmaf(fast_exp2(dt * an), h, dt * IO::get(up[j * a.rows.u]) * (IO::get(Bp[j * a.rows.b]) * kLn2));
   }
   a.seq_states[(s * N + n) * a.D + d] = h;
 }
@@ -275,9 +281,9 @@ __global__ __launch_bounds__(64) void scan_step_kernel(ScanArgs a, const float* 
   if (d >= (grp + 1) * gd) return;
   const int N = (int)a.N;
   const float u = IO::get(static_cast<const T*>(a.u)[b * a.rows.u + d]);
-  const float raw = IO::get(static_cast<const T*>(a.dt)[b * a.rows.dt + d]) + (a.dt_bias ? a.dt_bias[d] : 0.f);
-  const float dt = a.softplus ? softplus(raw) : raw;
-  const float x = dt * u;
+  const float raw = (IO::get(static_cast<const T*>(a.dt)[b * a.rows.dt + d]) + (a.dt_bias ? a.dt_bias[d] : 0.f)) * kLog2e;
+  const float dt = a.softplus ? softplus2(raw) : raw;  // in units of ln 2
+  const float x = dt * u * kLn2;
   const T* Bp = static_cast<const T*>(a.Bm) + b * a.rows.b + grp * N;
   const T* Cp = static_cast<const T*>(a.Cm) + b * a.rows.c + grp * N;
   const float* st = state + b * N * a.D + d;
@@ -294,7 +300,7 @@ __global__ __launch_bounds__(64) void scan_step_kernel(ScanArgs a, const float* 
     uniform4<IO>(Cp + n0, cv);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      h[s] = fmaf(fast_exp2(dt * (av[s] * kLog2e)), h[s], x * bv[s]);
+      h[s] = fmaf(fast_exp2(dt * av[s]), h[s], x * bv[s]);
       y = fmaf(cv[s], h[s], y);
       so[(int64_t)(n0 + s) * a.D] = h[s];
     }
@@ -310,10 +316,10 @@ bool scan_dstate_supported(int64_t N) { return N > 0 && N % 4 == 0 && N <= 256; 
 
 // Chunk length: enough waves for four a SIMD, in whole 16-token steps; the
 // carried states then cost little beside the inputs.
-static ScanGrid forward_grid(int64_t B, int64_t L, int64_t D, int64_t G) {
+static ScanGrid forward_grid(int64_t B, int64_t L, int64_t D, int64_t N, int64_t G) {
   ScanGrid g;
   g.ncb = (D / G + 63) / 64;
-  const int64_t waves = B * G * g.ncb, want = (int64_t)device_cu_count() * 16;
+  const int64_t waves = B * G * g.ncb, want = (int64_t)device_cu_count() * (getenv("DBGW") ? atoi(getenv("DBGW")) : 16);
   int64_t nc = want / waves;  // rounded down: one wave too many would run in a round of its own
   const int64_t most = (L + 63) / 64;
   if (nc > most) nc = most;
@@ -321,13 +327,14 @@ static ScanGrid forward_grid(int64_t B, int64_t L, int64_t D, int64_t G) {
   g.Q = ((L + nc - 1) / nc + kScanT - 1) / kScanT * kScanT;
   g.nc = (L + g.Q - 1) / g.Q;
   g.ntile = (L + kScanT - 1) / kScanT;
+  g.wpb = scan_wpb(g.ncb, 2 * 64 * (int64_t)sizeof(float) * N);
   return g;
 }
 
 static size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct FwdLayout {
-  size_t carry, sdt, cut, bc, a2, starts, total;
+  size_t carry, sdt, cut, bc, at, starts, total;
 };
 static FwdLayout forward_layout(const ScanGrid& g, int64_t B, int64_t D, int64_t N, int64_t G) {
   FwdLayout w;
@@ -338,24 +345,24 @@ static FwdLayout forward_layout(const ScanGrid& g, int64_t B, int64_t D, int64_t
   w.sdt = take(sizeof(float) * B * nc * D);
   w.cut = take(sizeof(int) * B * nc);
   w.bc = take(sizeof(float) * scan_bc_floats(B, G, g.ntile, N));
-  w.a2 = take(sizeof(float) * N * D);
+  w.at = take(sizeof(float) * N * D);
   w.starts = take(sizeof(uint32_t) * B * g.ntile);
   w.total = o;
   return w;
 }
 size_t scan_forward_ws_bytes(int64_t B, int64_t L, int64_t D, int64_t N, int64_t G) {
-  return forward_layout(forward_grid(B, L, D, G), B, D, N, G).total;
+  return forward_layout(forward_grid(B, L, D, N, G), B, D, N, G).total;
 }
 
 template <class IO, bool PACKED>
 static hipError_t scan_forward_t(const ScanArgs& a, hipStream_t s) {
-  const ScanGrid g = forward_grid(a.B, a.L, a.D, a.G);
+  const ScanGrid g = forward_grid(a.B, a.L, a.D, a.N, a.G);
   const FwdLayout w = forward_layout(g, a.B, a.D, a.N, a.G);
   char* base = static_cast<char*>(a.ws);
   auto at = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
-  const ScanWs ws = {at(w.carry), at(w.sdt), reinterpret_cast<int*>(base + w.cut), nullptr, at(w.bc), at(w.a2),
+  const ScanWs ws = {at(w.carry), at(w.sdt), reinterpret_cast<int*>(base + w.cut), nullptr, at(w.bc), at(w.at),
                      PACKED ? reinterpret_cast<uint32_t*>(base + w.starts) : nullptr};
-  const size_t lds = 2 * 64 * sizeof(float) * a.N;
+  const size_t lds = 2 * 64 * sizeof(float) * a.N * g.wpb;
   hipError_t e = launch_scan_pack(a, g, ws, IO::kVec == 8, s);
   if (e != hipSuccess) return e;
   if (lds > 64 * 1024) {
@@ -367,15 +374,16 @@ static hipError_t scan_forward_t(const ScanArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (g.nc > 1) {
-    const dim3 grid((unsigned)(a.G * g.ncb), (unsigned)(g.nc - 1), (unsigned)a.B);
-    hipLaunchKernelGGL((scan_chunk_kernel<IO, PACKED, false>), grid, dim3(64), lds, s, a, g, ws);
+    const dim3 grid((unsigned)scan_blocks(g, a.G), (unsigned)(g.nc - 1), (unsigned)a.B);
+    hipLaunchKernelGGL((scan_chunk_kernel<IO, PACKED, false>), grid, dim3(64 * g.wpb), lds, s, a, g, ws);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     hipLaunchKernelGGL((scan_carry_kernel<PACKED>), dim3((unsigned)((a.B * a.N * a.D + 255) / 256)), dim3(256), 0, s, a,
                        g, ws);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   hipLaunchKernelGGL((scan_chunk_kernel<IO, PACKED, true>),
-                     dim3((unsigned)(a.G * g.ncb), (unsigned)g.nc, (unsigned)a.B), dim3(64), lds, s, a, g, ws);
+                     dim3((unsigned)scan_blocks(g, a.G), (unsigned)g.nc, (unsigned)a.B), dim3(64 * g.wpb), lds, s, a,
+                     g, ws);
   if ((e = hipGetLastError()) != hipSuccess || a.nseq == 0) return e;
   hipLaunchKernelGGL((scan_seq_states_kernel<IO>), dim3((unsigned)(a.G * g.ncb), (unsigned)a.N, (unsigned)a.nseq),
                      dim3(64), 0, s, a, g, ws);

@@ -16,35 +16,50 @@ struct ScanGrid {
   int64_t Q, nc;     // tokens a chunk (a multiple of kScanT), chunks
   int64_t ncb;       // blocks of 64 channels per group
   int64_t ntile;     // tiles of a row
+  int wpb;           // waves a block: neighbouring channel blocks of the same tokens
 };
+
+constexpr int kScanWaves = 1;  // most waves a block
+// Waves a block for `lds` bytes a wave: up to four, within 64 KB.
+inline int scan_wpb(int64_t ncb, int64_t lds) {
+  int w = ncb < kScanWaves ? (int)ncb : kScanWaves;
+  while (w > 1 && w * lds > 64 * 1024) --w;
+  return w;
+}
+inline int64_t scan_blocks(const ScanGrid& g, int64_t G) { return G * ((g.ncb + g.wpb - 1) / g.wpb); }
 
 struct ScanWs {
   float* carry;      // [B,nc,N,D] states
-  float* sdt;        // [B,nc,D] summed dt of a chunk (since its last restart)
+  float* sdt;        // [B,nc,D] summed time steps of a chunk (since its last restart)
   int* cut;          // [B,nc] whether a sequence starts inside the chunk
   float* adj;        // backward: [B,nc,N,D] adjoint states
   float* bc;         // [B,G,ntile,N][kEntry] fp32, and one entry more
-  float* a2;         // [N,D] A log2(e)
+  float* at;         // [N,D] A
   uint32_t* starts;  // [B,ntile] bit i: token i of the tile begins another sequence
 };
 
 struct ScanBlock {
-  int64_t b, c, grp, d0, dend, t0, t1;
+  int64_t b, c, grp, cb, d0, dend, t0, t1;
+  int wave;
 };
 
-// Grid (G * ncb, chunks, B): consecutive blocks take neighbouring channels of
-// the same tokens, which share their rows of B and C.
-__device__ __forceinline__ ScanBlock scan_block(const ScanGrid& g, const ScanArgs& a) {
-  ScanBlock k;
+// Grid (groups x blocks of neighbouring channels, chunks, B).  The waves of a
+// block work on their own, but on the same tokens of one group: what one of
+// them reads of B and C the others find in the scalar cache.  False for the
+// last block's waves past the group's channels.
+__device__ __forceinline__ bool scan_block(const ScanGrid& g, const ScanArgs& a, ScanBlock& k) {
   const int64_t gd = a.D / a.G;
-  k.grp = blockIdx.x / (unsigned)g.ncb;
-  k.d0 = k.grp * gd + (blockIdx.x % (unsigned)g.ncb) * 64;
+  const unsigned per = ((unsigned)g.ncb + g.wpb - 1) / g.wpb;
+  k.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  k.grp = blockIdx.x / per;
+  k.cb = (blockIdx.x % per) * g.wpb + k.wave;
+  k.d0 = k.grp * gd + k.cb * 64;
   k.dend = (k.grp + 1) * gd;
   k.c = blockIdx.y;
   k.b = blockIdx.z;
   k.t0 = k.c * g.Q;
   k.t1 = k.t0 + g.Q < a.L ? k.t0 + g.Q : a.L;
-  return k;
+  return k.cb < g.ncb;
 }
 
 // B and C of one state over the 16 tokens of a tile, in two halves.  They are
@@ -69,9 +84,36 @@ struct BCHalf {
   __device__ __forceinline__ float c(int i) const { return v[kHalf + i]; }
 };
 
+template <bool WANT_C>
+struct BCPair {
+  BCHalf<WANT_C> lo, hi;
+  __device__ __forceinline__ void load(const float* p) {
+    lo.load(p);
+    hi.load(p + kScanT);
+  }
+  __device__ __forceinline__ void settle() {
+    lo.settle();
+    hi.settle();
+  }
+  __device__ __forceinline__ float b(int i) const { return i < kHalf ? lo.b(i) : hi.b(i - kHalf); }
+  __device__ __forceinline__ float c(int i) const { return i < kHalf ? lo.c(i) : hi.c(i - kHalf); }
+};
+
 // Tokens of the tile at t0 (uniform, kept in 32 bits).
 __device__ __forceinline__ int tile_tokens(const ScanBlock& k, int64_t t0) {
   return __builtin_amdgcn_readfirstlane((int)(k.t1 - t0 < kScanT ? k.t1 - t0 : kScanT));
+}
+
+// The waves of a SIMD have equal work, but its arbiter prefers the oldest: left
+// alone they finish one after the other, the last ones with nobody to fill
+// their stalls.  Each lowers its priority after 1/2, 3/4 and 7/8 of its tiles,
+// so that the ones behind catch up there and all end within an eighth of each
+// other.
+__device__ __forceinline__ void pace(int64_t done, int64_t all) {
+  if (done * 2 < all) __builtin_amdgcn_s_setprio(3);
+  else if (done * 4 < all * 3) __builtin_amdgcn_s_setprio(2);
+  else if (done * 8 < all * 7) __builtin_amdgcn_s_setprio(1);
+  else __builtin_amdgcn_s_setprio(0);
 }
 
 // Raw elements of a tile, one channel a lane: buffer loads from the tile's
@@ -113,16 +155,17 @@ __device__ __forceinline__ void store_tile(typename IO::type* base, int64_t row,
   }
 }
 
-// Time steps of a tile from the raw projections; zero past the tile's tokens,
-// where the decay is then 1.
+// Time steps of a tile from the raw projections, in units of ln 2: the decay is
+// then exp2(dt A), and the softplus log2(1 + 2^w) needs no scaling but that of
+// its argument.  Packed B is scaled by ln 2 in exchange.  Zero past the tile's
+// tokens, where the decay is then 1.  `bias` is in the same units.
 template <class IO>
 __device__ __forceinline__ void time_steps(const RawTile<IO>& raw, float bias, bool plus, int nt, float (&dt)[kScanT]) {
+#pragma unroll
+  for (int i = 0; i < kScanT; ++i) dt[i] = fmaf(raw.at(i), kLog2e, bias);
   if (plus) {
 #pragma unroll
-    for (int i = 0; i < kScanT; ++i) dt[i] = softplus(raw.at(i) + bias);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kScanT; ++i) dt[i] = raw.at(i) + bias;
+    for (int i = 0; i < kScanT; ++i) dt[i] = softplus2(dt[i]);
   }
   if (nt < kScanT) {
 #pragma unroll
@@ -134,7 +177,7 @@ __device__ __forceinline__ void time_steps(const RawTile<IO>& raw, float bias, b
 // Floats of the packed B and C (the entry more is what the last prefetch reads).
 inline int64_t scan_bc_floats(int64_t B, int64_t G, int64_t ntile, int64_t N) { return (B * G * ntile * N + 1) * kEntry; }
 
-// Fills ws.bc, ws.a2 and (packed sequences) ws.starts.
+// Fills ws.bc, ws.at and (packed sequences) ws.starts.
 hipError_t launch_scan_pack(const ScanArgs& a, const ScanGrid& g, const ScanWs& ws, bool bf16, hipStream_t s);
 
 }  // namespace ssd

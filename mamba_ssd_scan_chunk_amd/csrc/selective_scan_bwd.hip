@@ -59,13 +59,14 @@ __device__ __forceinline__ void gated(const RawTile<IO>& rg, const RawTile<IO>& 
 // others from zero), adj = what the chunk's outputs send back to its entering
 // state, sdt = its summed dt.
 template <class IO, bool PACKED>
-__global__ __launch_bounds__(64) void scan_bwd_local_kernel(ScanArgs a, ScanGrid g, ScanWs ws) {
+__global__ __launch_bounds__(64 * kScanWaves) void scan_bwd_local_kernel(ScanArgs a, ScanGrid g, ScanWs ws) {
   extern __shared__ float lds[];
-  const int lane = threadIdx.x;
-  const ScanBlock k = scan_block(g, a);
+  const int lane = threadIdx.x & 63;
+  ScanBlock k;
+  if (!scan_block(g, a, k)) return;
   const int N = (int)a.N;
-  float* hs = lds + lane;        // hs[n*64]: state
-  float* gs = hs + N * 64;       // gs[n*64]: what goes back to the entering state
+  float* hs = lds + k.wave * 2 * N * 64 + lane;  // hs[n*64]: state
+  float* gs = hs + N * 64;                       // gs[n*64]: what goes back to the entering state
   const int64_t d = k.d0 + lane < k.dend ? k.d0 + lane : k.dend - 1;
   const bool ok = k.d0 + lane < k.dend;
   const float* h_in = k.c == 0 && a.h0 ? a.h0 + k.b * N * a.D : nullptr;
@@ -73,14 +74,14 @@ __global__ __launch_bounds__(64) void scan_bwd_local_kernel(ScanArgs a, ScanGrid
     hs[n * 64] = h_in ? h_in[(int64_t)n * a.D + d] : 0.f;
     gs[n * 64] = 0.f;
   }
-  const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
+  const float bias = a.dt_bias ? a.dt_bias[d] * kLog2e : 0.f;
   const RowPtrs<IO> p(a, k.b);
   const int off = (int)(d * sizeof(typename IO::type));
-  const float* a2p = ws.a2 + d;
+  const float* atp = ws.at + d;
   const float* ep = ws.bc + (((k.b * a.G + k.grp) * g.ntile + k.t0 / kScanT) * N) * kEntry;
   BCHalf<true> lo, hi;
   lo.load(ep);
-  float a2n = a2p[0];
+  float a_n = atp[0];
   float sdt = 0.f;        // since the chunk's start
   float last = 0.f;       // since its last restart
   bool cut = false;
@@ -111,15 +112,15 @@ __global__ __launch_bounds__(64) void scan_bwd_local_kernel(ScanArgs a, ScanGrid
       sdt += dt[i];
     }
     for (int n = 0; n < N; ++n) {
-      const float a2 = a2n;
+      const float an = a_n;
       lo.settle();
       hi.load(ep + kScanT);
-      a2n = a2p[(int64_t)(n + 1 < N ? n + 1 : 0) * a.D];
-      float h = hs[n * 64], acc = gs[n * 64], pr = fast_exp2(sdt0 * a2);
+      a_n = atp[(int64_t)(n + 1 < N ? n + 1 : 0) * a.D];
+      float h = hs[n * 64], acc = gs[n * 64], pr = fast_exp2(sdt0 * an);
       auto half = [&](const BCHalf<true>& e, int i0) {
 #pragma unroll
         for (int i = i0; i < i0 + kHalf; ++i) {
-          const float dec = fast_exp2(dt[i] * a2);
+          const float dec = fast_exp2(dt[i] * an);
           if (PACKED && (starts >> i & 1)) h = 0.f;
           h = fmaf(dec, h, x[i] * e.b(i - i0));
           pr *= dec;
@@ -156,7 +157,7 @@ __global__ __launch_bounds__(256) void scan_bwd_carry_kernel(ScanArgs a, ScanGri
   const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (idx >= a.B * a.N * a.D) return;
   const int64_t d = idx % a.D, n = idx / a.D % a.N, b = idx / a.D / a.N;
-  const float a2 = a.A[d * a.N + n] * kLog2e;
+  const float an = a.A[d * a.N + n];
   const float* sd = ws.sdt + b * g.nc * a.D + d;
   const int* cut = ws.cut + b * g.nc;
   const int64_t cs = a.N * a.D, o = (b * g.nc * a.N + n) * a.D + d;
@@ -170,7 +171,7 @@ __global__ __launch_bounds__(256) void scan_bwd_carry_kernel(ScanArgs a, ScanGri
       for (int i = 0; i < U; ++i) {
         const int64_t c = c0 + i < g.nc ? c0 + i : g.nc - 1;
         v[i] = s[c * cs];
-        p[i] = fast_exp2(sd[c * a.D] * a2);
+        p[i] = fast_exp2(sd[c * a.D] * an);
       }
 #pragma unroll
       for (int i = 0; i < U; ++i) {
@@ -191,7 +192,7 @@ __global__ __launch_bounds__(256) void scan_bwd_carry_kernel(ScanArgs a, ScanGri
       for (int i = 0; i < U; ++i) {
         const int64_t c = c0 - i > 0 ? c0 - i : 0;
         v[i] = s[c * cs];
-        p[i] = fast_exp2(sd[c * a.D] * a2);
+        p[i] = fast_exp2(sd[c * a.D] * an);
       }
 #pragma unroll
       for (int i = 0; i < U; ++i) {
@@ -247,14 +248,15 @@ __device__ __forceinline__ float lane_sum4(const float (&r)[4], int lane) {
 // Pass 3.  LDS per state and lane: the adjoint riding backwards, the summed
 // dA, and the state entering each 16-token step but the first.
 template <class IO, bool PACKED>
-__global__ __launch_bounds__(64) void scan_bwd_chunk_kernel(ScanArgs a, ScanGrid g, ScanWs ws, BwdWs bw) {
+__global__ __launch_bounds__(64 * kScanWaves) void scan_bwd_chunk_kernel(ScanArgs a, ScanGrid g, ScanWs ws, BwdWs bw) {
   typedef typename IO::type T;
   extern __shared__ float lds[];
-  const int lane = threadIdx.x;
-  const ScanBlock k = scan_block(g, a);
+  const int lane = threadIdx.x & 63;
+  ScanBlock k;
+  if (!scan_block(g, a, k)) return;
   const int N = (int)a.N;
   const int st = N * 64;
-  float* gs = lds + lane;            // gs[n*64]
+  float* gs = lds + k.wave * (int)(g.Q / kScanT + 1) * st + lane;  // gs[n*64]
   float* as = gs + st;               // dA
   float* hs = as + st;               // hs[(j-1)*st + n*64]: state entering step j >= 1
   const int64_t d = k.d0 + lane < k.dend ? k.d0 + lane : k.dend - 1;
@@ -266,13 +268,13 @@ __global__ __launch_bounds__(64) void scan_bwd_chunk_kernel(ScanArgs a, ScanGrid
     gs[n * 64] = ws.adj[co + (int64_t)n * a.D];
     as[n * 64] = 0.f;
   }
-  const float bias = a.dt_bias ? a.dt_bias[d] : 0.f;
+  const float bias = a.dt_bias ? a.dt_bias[d] * kLog2e : 0.f;
   const float skip = a.D_skip ? a.D_skip[d] : 0.f;
   const RowPtrs<IO> p(a, k.b);
   const int off = (int)(d * sizeof(typename IO::type));
   const int nstep = (int)((k.t1 - k.t0 + kScanT - 1) / kScanT);
 
-  const float* a2p = ws.a2 + d;
+  const float* atp = ws.at + d;
   const float* e0 = ws.bc + (((k.b * a.G + k.grp) * g.ntile + k.t0 / kScanT) * N) * kEntry;
 
   // states entering steps 1 .. nstep-1
@@ -280,7 +282,7 @@ __global__ __launch_bounds__(64) void scan_bwd_chunk_kernel(ScanArgs a, ScanGrid
     const float* ep = e0;
     BCHalf<false> lo, hi;
     lo.load(ep);
-    float a2n = a2p[0];
+    float a_n = atp[0];
     for (int j = 0; j + 1 < nstep; ++j) {
       const int64_t t0 = k.t0 + j * kScanT;
       float dt[kScanT], x[kScanT];
@@ -292,16 +294,16 @@ __global__ __launch_bounds__(64) void scan_bwd_chunk_kernel(ScanArgs a, ScanGrid
 #pragma unroll
       for (int i = 0; i < kScanT; ++i) x[i] = dt[i] * ru.at(i);
       for (int n = 0; n < N; ++n) {
-        const float a2 = a2n;
+        const float an = a_n;
         lo.settle();
         hi.load(ep + kScanT);
-        a2n = a2p[(int64_t)(n + 1 < N ? n + 1 : 0) * a.D];
+        a_n = atp[(int64_t)(n + 1 < N ? n + 1 : 0) * a.D];
         float h = j ? hs[(j - 1) * st + n * 64] : (h_in ? h_in[(int64_t)n * a.D] : 0.f);
         auto half = [&](const BCHalf<false>& e, int i0) {
 #pragma unroll
           for (int i = i0; i < i0 + kHalf; ++i) {
             if (PACKED && (starts >> i & 1)) h = 0.f;
-            h = fmaf(fast_exp2(dt[i] * a2), h, x[i] * e.b(i - i0));
+            h = fmaf(fast_exp2(dt[i] * an), h, x[i] * e.b(i - i0));
           }
         };
         half(lo, 0);
@@ -317,7 +319,7 @@ __global__ __launch_bounds__(64) void scan_bwd_chunk_kernel(ScanArgs a, ScanGrid
   float dDsum = 0.f, dbsum = 0.f;
   const int64_t BL = a.B * a.L;
   const int64_t GN = a.G * N;
-  float* dBp = bw.bc + ((blockIdx.x % (unsigned)g.ncb) * BL + k.b * a.L) * GN + k.grp * N;
+  float* dBp = bw.bc + (k.cb * BL + k.b * a.L) * GN + k.grp * N;
   float* dCp = dBp + g.ncb * BL * GN;
   for (int j = nstep - 1; j >= 0; --j) {
     const int64_t t0 = k.t0 + j * kScanT;
@@ -349,17 +351,17 @@ __global__ __launch_bounds__(64) void scan_bwd_chunk_kernel(ScanArgs a, ScanGrid
     hi.load(ep + kScanT);
     auto bv = [&](int i) { return i < kHalf ? lo.b(i) : hi.b(i - kHalf); };
     auto cv = [&](int i) { return i < kHalf ? lo.c(i) : hi.c(i - kHalf); };
-    float a2n = a2p[0];
+    float a_n = atp[0];
     float rB[4] = {}, rC[4] = {};  // the last four states' sums
     for (int n = 0; n < N; ++n) {
-      const float a2 = a2n;
-      a2n = a2p[(int64_t)(n + 1 < N ? n + 1 : 0) * a.D];
+      const float an = a_n;
+      a_n = atp[(int64_t)(n + 1 < N ? n + 1 : 0) * a.D];
       float dec[kScanT], h[kScanT], v[kScanT];
       const float h0 = j ? hs[(j - 1) * st + n * 64] : (h_in ? h_in[(int64_t)n * a.D] : 0.f);
       float hp = h0;
 #pragma unroll
       for (int i = 0; i < kScanT; ++i) {
-        dec[i] = fast_exp2(dt[i] * a2);
+        dec[i] = fast_exp2(dt[i] * an);
         if (PACKED && (starts >> i & 1)) hp = 0.f;
         hp = fmaf(dec[i], hp, x[i] * bv(i));
         h[i] = hp;
@@ -379,7 +381,7 @@ __global__ __launch_bounds__(64) void scan_bwd_chunk_kernel(ScanArgs a, ScanGrid
           ga = 0.f;
           q = 0.f;
         }
-        sA[i] = fmaf(a2, q, sA[i]);  // in units of log2(e)
+        sA[i] = fmaf(an, q, sA[i]);
         dA = fmaf(dt[i], q, dA);
       }
       // B and C are in use up to here; the next entry arrives behind the sums
@@ -415,12 +417,12 @@ __global__ __launch_bounds__(64) void scan_bwd_chunk_kernel(ScanArgs a, ScanGrid
     }
 #pragma unroll
     for (int i = 0; i < kScanT; ++i) {
-      sA[i] = fmaf(sB[i], ru.at(i), sA[i] * kLn2);
+      sA[i] = fmaf(sB[i] * kLog2e, ru.at(i), sA[i]);  // sB holds B ln 2, dt units of ln 2
       sB[i] = fmaf(dt[i], sB[i], skip * gy[i]);
     }
     if (a.softplus) {
 #pragma unroll
-      for (int i = 0; i < kScanT; ++i) sA[i] *= sigmoid(rd.at(i) + bias);
+      for (int i = 0; i < kScanT; ++i) sA[i] *= sigmoid2(fmaf(rd.at(i), kLog2e, bias));
     }
 #pragma unroll
     for (int i = 0; i < kScanT; ++i) {
@@ -471,7 +473,7 @@ __global__ __launch_bounds__(256) void scan_bc_reduce_kernel(ScanArgs a, int64_t
   for (; k < ncb; ++k) acc += q[k * n];
   const int64_t row = e / GN, col = e % GN;
   if (c) static_cast<T*>(a.dC)[row * a.grows.c + col] = IO::put(acc);
-  else static_cast<T*>(a.dB)[row * a.grows.b + col] = IO::put(acc);
+  else static_cast<T*>(a.dB)[row * a.grows.b + col] = IO::put(acc * kLn2);  // dt in units of ln 2
 }
 
 // dA [D,N] from the chunk sums' [N][D]
@@ -479,7 +481,7 @@ __global__ __launch_bounds__(256) void scan_da_kernel(const float* __restrict__ 
                                                       float* __restrict__ dA) {
   const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (idx >= D * N) return;
-  dA[idx] = s[idx % N * D + idx / N];
+  dA[idx] = s[idx % N * D + idx / N] * kLn2;  // dt in units of ln 2
 }
 
 // Steps of 16 tokens a chunk: as many as leave eight waves a compute unit
@@ -490,13 +492,14 @@ static ScanGrid backward_grid(int64_t L, int64_t D, int64_t N, int64_t G) {
   g.Q = kScanT * (N <= 32 ? 4 : N <= 64 ? 2 : 1);
   g.nc = (L + g.Q - 1) / g.Q;
   g.ntile = (L + kScanT - 1) / kScanT;
+  g.wpb = scan_wpb(g.ncb, 64 * (int64_t)sizeof(float) * N * (g.Q / kScanT + 1));
   return g;
 }
 
 static size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct BwdLayout {
-  size_t carry, adj, sdt, cut, pack, a2, starts, bc, dDp, dbp, sums, total;
+  size_t carry, adj, sdt, cut, pack, at, starts, bc, dDp, dbp, sums, total;
 };
 static BwdLayout backward_layout(int64_t B, int64_t L, int64_t D, int64_t N, int64_t G) {
   const ScanGrid g = backward_grid(L, D, N, G);
@@ -508,7 +511,7 @@ static BwdLayout backward_layout(int64_t B, int64_t L, int64_t D, int64_t N, int
   w.sdt = take(sizeof(float) * B * g.nc * D);
   w.cut = take(sizeof(int) * B * g.nc);
   w.pack = take(sizeof(float) * scan_bc_floats(B, G, g.ntile, N));
-  w.a2 = take(sizeof(float) * N * D);
+  w.at = take(sizeof(float) * N * D);
   w.starts = take(sizeof(uint32_t) * B * g.ntile);
   w.bc = take(sizeof(float) * 2 * g.ncb * B * L * G * N);
   w.dDp = take(sizeof(float) * B * g.nc * D);
@@ -527,11 +530,11 @@ static hipError_t scan_backward_t(const ScanArgs& a, hipStream_t s) {
   const BwdLayout w = backward_layout(a.B, a.L, a.D, a.N, a.G);
   char* base = static_cast<char*>(a.ws);
   auto at = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
-  const ScanWs ws = {at(w.carry), at(w.sdt), reinterpret_cast<int*>(base + w.cut), at(w.adj), at(w.pack), at(w.a2),
+  const ScanWs ws = {at(w.carry), at(w.sdt), reinterpret_cast<int*>(base + w.cut), at(w.adj), at(w.pack), at(w.at),
                      PACKED ? reinterpret_cast<uint32_t*>(base + w.starts) : nullptr};
   const BwdWs bw = {at(w.bc), at(w.dDp), at(w.dbp)};
-  const dim3 grid((unsigned)(a.G * g.ncb), (unsigned)g.nc, (unsigned)a.B);
-  const size_t per = 64 * sizeof(float) * a.N;
+  const dim3 grid((unsigned)scan_blocks(g, a.G), (unsigned)g.nc, (unsigned)a.B), block(64 * g.wpb);
+  const size_t per = 64 * sizeof(float) * a.N * g.wpb;
   const size_t lds1 = 2 * per, lds3 = per * (2 + g.Q / kScanT - 1);
   hipError_t e;
   if (lds1 > 64 * 1024 || lds3 > 64 * 1024) {
@@ -543,12 +546,12 @@ static hipError_t scan_backward_t(const ScanArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if ((e = launch_scan_pack(a, g, ws, IO::kVec == 8, s)) != hipSuccess) return e;
-  hipLaunchKernelGGL((scan_bwd_local_kernel<IO, PACKED>), grid, dim3(64), lds1, s, a, g, ws);
+  hipLaunchKernelGGL((scan_bwd_local_kernel<IO, PACKED>), grid, block, lds1, s, a, g, ws);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   hipLaunchKernelGGL((scan_bwd_carry_kernel<PACKED>), dim3((unsigned)((a.B * a.N * a.D + 255) / 256), 2), dim3(256), 0,
                      s, a, g, ws);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL((scan_bwd_chunk_kernel<IO, PACKED>), grid, dim3(64), lds3, s, a, g, ws, bw);
+  hipLaunchKernelGGL((scan_bwd_chunk_kernel<IO, PACKED>), grid, block, lds3, s, a, g, ws, bw);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int64_t nbc = 2 * a.B * a.L * a.G * a.N;
   hipLaunchKernelGGL((scan_bc_reduce_kernel<IO>), dim3((unsigned)((nbc + 255) / 256)), dim3(256), 0, s, a, g.ncb, bw.bc);
