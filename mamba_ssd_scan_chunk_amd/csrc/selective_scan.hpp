@@ -127,13 +127,22 @@ struct RawTile {
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<typename IO::type*>(base + t0 * row), 0, 0x7fffffff, 0x00027000);
     const int step = (int)row * es;
-    int so = 0;
+    if (nt == kScanT) {
+      int so = 0;
 #pragma unroll
-    for (int i = 0; i < kScanT; ++i) {
-      if constexpr (es == 2) v[i] = __builtin_amdgcn_raw_buffer_load_b16(r, off, so, 0);
-      else v[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, so, 0));
-      so += i + 1 < nt ? step : 0;
+      for (int i = 0; i < kScanT; ++i) {
+        v[i] = load1(r, off, so);
+        so += step;
+        asm volatile("" : "+s"(so));  // one running offset, not sixteen multiples kept in registers
+      }
+    } else {
+#pragma unroll
+      for (int i = 0, so = 0; i < kScanT; ++i, so += i < nt ? step : 0) v[i] = load1(r, off, so);
     }
+  }
+  __device__ __forceinline__ static typename IO::type load1(__amdgpu_buffer_rsrc_t r, int off, int so) {
+    if constexpr (IO::kVec == 8) return __builtin_amdgcn_raw_buffer_load_b16(r, off, so, 0);
+    else return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, so, 0));
   }
   __device__ __forceinline__ float at(int i) const { return IO::get(v[i]); }
 };
@@ -144,14 +153,25 @@ __device__ __forceinline__ void store_tile(typename IO::type* base, int64_t row,
   constexpr int es = sizeof(typename IO::type);
   const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(base + t0 * row, 0, 0x7fffffff, 0x00027000);
   const int step = (int)row * es;
+  auto put = [&](int i, int so) {
+    if constexpr (es == 2) __builtin_amdgcn_raw_buffer_store_b16(IO::put(v[i]), r, off, so, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), r, off, so, 0);
+  };
   int so = 0;
+  if (nt == kScanT) {
 #pragma unroll
-  for (int i = 0; i < kScanT; ++i) {
-    if (i < nt) {
-      if constexpr (es == 2) __builtin_amdgcn_raw_buffer_store_b16(IO::put(v[i]), r, off, so, 0);
-      else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), r, off, so, 0);
+    for (int i = 0; i < kScanT; ++i) {
+      put(i, so);
+      so += step;
+      asm volatile("" : "+s"(so));
     }
-    so += step;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kScanT; ++i) {
+      if (i < nt) put(i, so);
+      so += step;
+      asm volatile("" : "+s"(so));
+    }
   }
 }
 

@@ -316,6 +316,7 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_bwd_chunk_kernel(ScanArg
     }
   }
 
+  const bool whole = k.d0 + 64 <= k.dend;
   float dDsum = 0.f, dbsum = 0.f;
   const int64_t BL = a.B * a.L;
   const int64_t GN = a.G * N;
@@ -341,9 +342,18 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_bwd_chunk_kernel(ScanArg
         sB[i] = 0.f;
         sA[i] = 0.f;
       }
+      if (nt < kScanT) {
 #pragma unroll
-      for (int i = 0; i < kScanT; ++i)
-        if (i >= nt || !ok) x[i] = gy[i] = 0.f;  // lanes past the group add nothing to its sums
+        for (int i = 0; i < kScanT; ++i)
+          if (i >= nt) x[i] = gy[i] = 0.f;
+      }
+      if (!whole) {  // lanes past the group add nothing to its sums
+#pragma unroll
+        for (int i = 0; i < kScanT; ++i) {
+          x[i] = ok ? x[i] : 0.f;
+          gy[i] = ok ? gy[i] : 0.f;
+        }
+      }
     }
     const float* ep = e0 + (int64_t)j * N * kEntry;
     BCHalf<true> lo, hi;
@@ -384,6 +394,11 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_bwd_chunk_kernel(ScanArg
         sA[i] = fmaf(an, q, sA[i]);
         dA = fmaf(dt[i], q, dA);
       }
+      // summed here and now: put off past the branch below, the terms would
+      // stay in registers beside the sums
+#pragma unroll
+      for (int i = 0; i < kScanT; ++i) asm volatile("" : "+v"(sA[i]), "+v"(sB[i]), "+v"(y[i]));
+      asm volatile("" : "+v"(dA));
       // B and C are in use up to here; the next entry arrives behind the sums
       ep += kEntry;
       lo.load(ep);
@@ -424,12 +439,15 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_bwd_chunk_kernel(ScanArg
 #pragma unroll
       for (int i = 0; i < kScanT; ++i) sA[i] *= sigmoid2(fmaf(rd.at(i), kLog2e, bias));
     }
+    if (nt < kScanT) {  // past the row: gy is zero already
+#pragma unroll
+      for (int i = 0; i < kScanT; ++i)
+        if (i >= nt) sA[i] = 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < kScanT; ++i) {
-      if (i < nt) {
-        dbsum += sA[i];
-        dDsum = fmaf(gy[i], ru.at(i), dDsum);
-      }
+      dbsum += sA[i];
+      dDsum = fmaf(gy[i], ru.at(i), dDsum);
     }
     if (p.z) {
 #pragma unroll
