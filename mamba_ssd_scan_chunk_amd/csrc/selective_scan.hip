@@ -22,7 +22,6 @@
 #include "layer_device.hpp"
 #include "layer_launch.hpp"
 #include "selective_scan.hpp"
-#include <cstdlib>
 
 namespace ssd {
 
@@ -74,14 +73,13 @@ hipError_t launch_scan_pack(const ScanArgs& a, const ScanGrid& g, const ScanWs& 
 // State passes: FINAL writes outputs from the chunk's entering state, else
 // only the state the chunk leaves and its summed dt.
 template <class IO, bool PACKED, bool FINAL>
-__global__ __launch_bounds__(64 * kScanWaves) void scan_chunk_kernel(ScanArgs a, ScanGrid g, ScanWs ws) {
+__global__ __launch_bounds__(64) void scan_chunk_kernel(ScanArgs a, ScanGrid g, ScanWs ws) {
   typedef typename IO::type T;
   extern __shared__ float lds[];
-  const int lane = threadIdx.x & 63;
-  ScanBlock k;
-  if (!scan_block(g, a, k)) return;
+  const int lane = threadIdx.x;
+  const ScanBlock k = scan_block(g, a);
   const int N = (int)a.N;
-  float* hs = lds + k.wave * 2 * N * 64 + lane;   // hs[n*64]: state
+  float* hs = lds + lane;   // hs[n*64]: state
   float* as = hs + N * 64;  // as[n*64]: A
   const int64_t d = k.d0 + lane < k.dend ? k.d0 + lane : k.dend - 1;
   const bool ok = k.d0 + lane < k.dend;
@@ -116,7 +114,7 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_chunk_kernel(ScanArgs a,
     const int nt = tile_tokens(k, t0);
     const uint32_t starts = PACKED ? ws.starts[k.b * g.ntile + t0 / kScanT] : 0;
     float dt[kScanT], x[kScanT], y[kScanT];
-    time_steps<IO>(rd, bias, a.softplus, nt, dt);
+    time_steps(rd, bias, a.softplus, nt, dt);
 #pragma unroll
     for (int i = 0; i < kScanT; ++i) {
       x[i] = dt[i] * ru.at(i);
@@ -316,10 +314,10 @@ bool scan_dstate_supported(int64_t N) { return N > 0 && N % 4 == 0 && N <= 256; 
 
 // Chunk length: enough waves for four a SIMD, in whole 16-token steps; the
 // carried states then cost little beside the inputs.
-static ScanGrid forward_grid(int64_t B, int64_t L, int64_t D, int64_t N, int64_t G) {
+static ScanGrid forward_grid(int64_t B, int64_t L, int64_t D, int64_t G) {
   ScanGrid g;
   g.ncb = (D / G + 63) / 64;
-  const int64_t waves = B * G * g.ncb, want = (int64_t)device_cu_count() * (getenv("DBGW") ? atoi(getenv("DBGW")) : 16);
+  const int64_t waves = B * G * g.ncb, want = (int64_t)device_cu_count() * 16;
   int64_t nc = want / waves;  // rounded down: one wave too many would run in a round of its own
   const int64_t most = (L + 63) / 64;
   if (nc > most) nc = most;
@@ -327,7 +325,6 @@ static ScanGrid forward_grid(int64_t B, int64_t L, int64_t D, int64_t N, int64_t
   g.Q = ((L + nc - 1) / nc + kScanT - 1) / kScanT * kScanT;
   g.nc = (L + g.Q - 1) / g.Q;
   g.ntile = (L + kScanT - 1) / kScanT;
-  g.wpb = scan_wpb(g.ncb, 2 * 64 * (int64_t)sizeof(float) * N);
   return g;
 }
 
@@ -351,18 +348,18 @@ static FwdLayout forward_layout(const ScanGrid& g, int64_t B, int64_t D, int64_t
   return w;
 }
 size_t scan_forward_ws_bytes(int64_t B, int64_t L, int64_t D, int64_t N, int64_t G) {
-  return forward_layout(forward_grid(B, L, D, N, G), B, D, N, G).total;
+  return forward_layout(forward_grid(B, L, D, G), B, D, N, G).total;
 }
 
 template <class IO, bool PACKED>
 static hipError_t scan_forward_t(const ScanArgs& a, hipStream_t s) {
-  const ScanGrid g = forward_grid(a.B, a.L, a.D, a.N, a.G);
+  const ScanGrid g = forward_grid(a.B, a.L, a.D, a.G);
   const FwdLayout w = forward_layout(g, a.B, a.D, a.N, a.G);
   char* base = static_cast<char*>(a.ws);
   auto at = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
   const ScanWs ws = {at(w.carry), at(w.sdt), reinterpret_cast<int*>(base + w.cut), nullptr, at(w.bc), at(w.at),
-                     PACKED ? reinterpret_cast<uint32_t*>(base + w.starts) : nullptr};
-  const size_t lds = 2 * 64 * sizeof(float) * a.N * g.wpb;
+                     PACKED ? reinterpret_cast<uint32_t*>(base + w.starts) : nullptr, nullptr, nullptr};
+  const size_t lds = 2 * 64 * sizeof(float) * a.N;
   hipError_t e = launch_scan_pack(a, g, ws, IO::kVec == 8, s);
   if (e != hipSuccess) return e;
   if (lds > 64 * 1024) {
@@ -374,15 +371,15 @@ static hipError_t scan_forward_t(const ScanArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (g.nc > 1) {
-    const dim3 grid((unsigned)scan_blocks(g, a.G), (unsigned)(g.nc - 1), (unsigned)a.B);
-    hipLaunchKernelGGL((scan_chunk_kernel<IO, PACKED, false>), grid, dim3(64 * g.wpb), lds, s, a, g, ws);
+    const dim3 grid((unsigned)(a.G * g.ncb), (unsigned)(g.nc - 1), (unsigned)a.B);
+    hipLaunchKernelGGL((scan_chunk_kernel<IO, PACKED, false>), grid, dim3(64), lds, s, a, g, ws);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     hipLaunchKernelGGL((scan_carry_kernel<PACKED>), dim3((unsigned)((a.B * a.N * a.D + 255) / 256)), dim3(256), 0, s, a,
                        g, ws);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   hipLaunchKernelGGL((scan_chunk_kernel<IO, PACKED, true>),
-                     dim3((unsigned)scan_blocks(g, a.G), (unsigned)g.nc, (unsigned)a.B), dim3(64 * g.wpb), lds, s, a,
+                     dim3((unsigned)(a.G * g.ncb), (unsigned)g.nc, (unsigned)a.B), dim3(64), lds, s, a,
                      g, ws);
   if ((e = hipGetLastError()) != hipSuccess || a.nseq == 0) return e;
   hipLaunchKernelGGL((scan_seq_states_kernel<IO>), dim3((unsigned)(a.G * g.ncb), (unsigned)a.N, (unsigned)a.nseq),

@@ -16,17 +16,7 @@ struct ScanGrid {
   int64_t Q, nc;     // tokens a chunk (a multiple of kScanT), chunks
   int64_t ncb;       // blocks of 64 channels per group
   int64_t ntile;     // tiles of a row
-  int wpb;           // waves a block: neighbouring channel blocks of the same tokens
 };
-
-constexpr int kScanWaves = 1;  // most waves a block
-// Waves a block for `lds` bytes a wave: up to four, within 64 KB.
-inline int scan_wpb(int64_t ncb, int64_t lds) {
-  int w = ncb < kScanWaves ? (int)ncb : kScanWaves;
-  while (w > 1 && w * lds > 64 * 1024) --w;
-  return w;
-}
-inline int64_t scan_blocks(const ScanGrid& g, int64_t G) { return G * ((g.ncb + g.wpb - 1) / g.wpb); }
 
 struct ScanWs {
   float* carry;      // [B,nc,N,D] states
@@ -36,30 +26,28 @@ struct ScanWs {
   float* bc;         // [B,G,ntile,N][kEntry] fp32, and one entry more
   float* at;         // [N,D] A
   uint32_t* starts;  // [B,ntile] bit i: token i of the tile begins another sequence
+  float* tstate;     // backward: [B,ntile,N,D] states entering each tile, from a zero chunk start
+  float* tsdt;       // backward: [B,ntile,D] time steps summed up to the tile (since the last restart)
 };
 
 struct ScanBlock {
   int64_t b, c, grp, cb, d0, dend, t0, t1;
-  int wave;
 };
 
-// Grid (groups x blocks of neighbouring channels, chunks, B).  The waves of a
-// block work on their own, but on the same tokens of one group: what one of
-// them reads of B and C the others find in the scalar cache.  False for the
-// last block's waves past the group's channels.
-__device__ __forceinline__ bool scan_block(const ScanGrid& g, const ScanArgs& a, ScanBlock& k) {
+// Grid (G * ncb, chunks, B), a wave a block: consecutive blocks take
+// neighbouring channels of the same tokens, which share their rows of B and C.
+__device__ __forceinline__ ScanBlock scan_block(const ScanGrid& g, const ScanArgs& a) {
+  ScanBlock k;
   const int64_t gd = a.D / a.G;
-  const unsigned per = ((unsigned)g.ncb + g.wpb - 1) / g.wpb;
-  k.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  k.grp = blockIdx.x / per;
-  k.cb = (blockIdx.x % per) * g.wpb + k.wave;
+  k.grp = blockIdx.x / (unsigned)g.ncb;
+  k.cb = blockIdx.x % (unsigned)g.ncb;
   k.d0 = k.grp * gd + k.cb * 64;
   k.dend = (k.grp + 1) * gd;
   k.c = blockIdx.y;
   k.b = blockIdx.z;
   k.t0 = k.c * g.Q;
   k.t1 = k.t0 + g.Q < a.L ? k.t0 + g.Q : a.L;
-  return k.cb < g.ncb;
+  return k;
 }
 
 // B and C of one state over the 16 tokens of a tile, in two halves.  They are

@@ -13,11 +13,10 @@
 // Three passes over chunks of tokens, a wave per (64 channels, chunk): the
 // state each chunk leaves and the adjoint it sends back, each from zero; the
 // carry of both over the chunks; then the chunk itself, whose states are
-// recomputed forwards 16 tokens at a time (the steps' entering states in LDS)
-// and swept backwards.  The sums over channels take a wave reduction that
-// halves the number of values with each lane bit it sums over, so 16 tokens x
-// 4 states end as one value a lane; the channel blocks' partial sums are then
-// added in order.  No atomics: results do not depend on timing.
+// recomputed forwards 16 tokens at a time (from the states the first pass left
+// at every 16th token) and swept backwards.  The sums over channels go through
+// LDS, 16 tokens of one state at a time; the channel blocks' partial sums are
+// then added in order.  No atomics: results do not depend on timing.
 #include "layer_device.hpp"
 #include "layer_launch.hpp"
 #include "selective_scan.hpp"
@@ -26,8 +25,7 @@ namespace ssd {
 
 struct BwdWs {
   float* bc;     // [ncb][B L][G N] dB partial sums, then the same for dC
-  float* dDp;    // [B nc][D]
-  float* dbp;    // [B nc][D]
+  float* dDb;    // [B nc][2][D] dD, then ddt_bias
 };
 
 // One row of the batch (b) of each input; lanes add their channel.
@@ -59,13 +57,12 @@ __device__ __forceinline__ void gated(const RawTile<IO>& rg, const RawTile<IO>& 
 // others from zero), adj = what the chunk's outputs send back to its entering
 // state, sdt = its summed dt.
 template <class IO, bool PACKED>
-__global__ __launch_bounds__(64 * kScanWaves) void scan_bwd_local_kernel(ScanArgs a, ScanGrid g, ScanWs ws) {
+__global__ __launch_bounds__(64) void scan_bwd_local_kernel(ScanArgs a, ScanGrid g, ScanWs ws) {
   extern __shared__ float lds[];
-  const int lane = threadIdx.x & 63;
-  ScanBlock k;
-  if (!scan_block(g, a, k)) return;
+  const int lane = threadIdx.x;
+  const ScanBlock k = scan_block(g, a);
   const int N = (int)a.N;
-  float* hs = lds + k.wave * 2 * N * 64 + lane;  // hs[n*64]: state
+  float* hs = lds + lane;  // hs[n*64]: state
   float* gs = hs + N * 64;                       // gs[n*64]: what goes back to the entering state
   const int64_t d = k.d0 + lane < k.dend ? k.d0 + lane : k.dend - 1;
   const bool ok = k.d0 + lane < k.dend;
@@ -79,13 +76,14 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_bwd_local_kernel(ScanArg
   const int off = (int)(d * sizeof(typename IO::type));
   const float* atp = ws.at + d;
   const float* ep = ws.bc + (((k.b * a.G + k.grp) * g.ntile + k.t0 / kScanT) * N) * kEntry;
-  BCHalf<true> lo, hi;
-  lo.load(ep);
+  BCPair<true> e;
+  e.load(ep);
   float a_n = atp[0];
   float sdt = 0.f;        // since the chunk's start
   float last = 0.f;       // since its last restart
   bool cut = false;
   for (int64_t t0 = k.t0; t0 < k.t1; t0 += kScanT) {
+    pace(t0 - k.t0, k.t1 - k.t0);
     const int nt = tile_tokens(k, t0);
     float dt[kScanT], x[kScanT], dy[kScanT];
     const uint32_t starts = PACKED ? ws.starts[k.b * g.ntile + t0 / kScanT] : 0;
@@ -94,8 +92,8 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_bwd_local_kernel(ScanArg
     ru.load(p.u, a.rows.u, t0, nt, off);
     rg.load(p.dy, a.D, t0, nt, off);
     if (p.z) rz.load(p.z, a.rows.z, t0, nt, off);
-    time_steps<IO>(rd, bias, a.softplus, nt, dt);
-    gated<IO>(rg, rz, p.z, dy);
+    time_steps(rd, bias, a.softplus, nt, dt);
+    gated(rg, rz, p.z, dy);
 #pragma unroll
     for (int i = 0; i < kScanT; ++i) x[i] = dt[i] * ru.at(i);
     if (nt < kScanT) {  // past the row: decay 1, nothing added
@@ -106,6 +104,7 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_bwd_local_kernel(ScanArg
     // tokens of this step that still reach the chunk's entering state
     const int live = cut ? 0 : (starts ? __builtin_ctz(starts) : kScanT);
     const float sdt0 = sdt;
+    float* ts = ws.tstate + ((k.b * g.ntile + t0 / kScanT + 1) * N) * a.D + d;  // entering the next tile
 #pragma unroll
     for (int i = 0; i < kScanT; ++i) {
       last = (PACKED && (starts >> i & 1)) ? dt[i] : last + dt[i];
@@ -113,30 +112,28 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_bwd_local_kernel(ScanArg
     }
     for (int n = 0; n < N; ++n) {
       const float an = a_n;
-      lo.settle();
-      hi.load(ep + kScanT);
+      e.settle();
+      ep += kEntry;
+      BCPair<true> nxt;
+      nxt.load(ep);
       a_n = atp[(int64_t)(n + 1 < N ? n + 1 : 0) * a.D];
       float h = hs[n * 64], acc = gs[n * 64], pr = fast_exp2(sdt0 * an);
-      auto half = [&](const BCHalf<true>& e, int i0) {
 #pragma unroll
-        for (int i = i0; i < i0 + kHalf; ++i) {
-          const float dec = fast_exp2(dt[i] * an);
-          if (PACKED && (starts >> i & 1)) h = 0.f;
-          h = fmaf(dec, h, x[i] * e.b(i - i0));
-          pr *= dec;
-          const float v = fmaf(pr, e.c(i - i0) * dy[i], acc);
-          acc = (!PACKED || i < live) ? v : acc;
-        }
-      };
-      half(lo, 0);
-      hi.settle();
-      ep += kEntry;
-      lo.load(ep);
-      half(hi, kHalf);
+      for (int i = 0; i < kScanT; ++i) {
+        const float dec = fast_exp2(dt[i] * an);
+        if (PACKED && (starts >> i & 1)) h = 0.f;
+        h = fmaf(dec, h, x[i] * e.b(i));
+        pr *= dec;
+        const float v = fmaf(pr, e.c(i) * dy[i], acc);
+        acc = (!PACKED || i < live) ? v : acc;
+      }
+      e = nxt;
       hs[n * 64] = h;
       gs[n * 64] = acc;
+      if (ok && t0 + kScanT < k.t1) ts[(int64_t)n * a.D] = h;
     }
     cut = cut || starts != 0;
+    if (ok && t0 + kScanT < k.t1) ws.tsdt[(k.b * g.ntile + t0 / kScanT + 1) * a.D + d] = last;
   }
   if (ok) {
     const int64_t o = (k.b * g.nc + k.c) * N * a.D + d;
@@ -211,59 +208,47 @@ __device__ __forceinline__ float dpp_mov(float v) {
   return __uint_as_float(
       __builtin_amdgcn_update_dpp(0u, __float_as_uint(v), CTRL, 0xf, 0xf, true));
 }
-// v0 summed over the two halves where the lane bit is clear, v1 where it is
-// set (lane bits 5 and 4 by the row swaps, lower ones by data-parallel moves).
-__device__ __forceinline__ float pair_sum32(float v0, float v1) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v0), __float_as_uint(v1), false, false);
-  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-__device__ __forceinline__ float pair_sum16(float v0, float v1) {
-  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v0), __float_as_uint(v1), false, false);
-  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-template <int CTRL>
-__device__ __forceinline__ float pair_sum_dpp(float v0, float v1, bool set) {
-  const float s0 = v0 + dpp_mov<CTRL>(v0), s1 = v1 + dpp_mov<CTRL>(v1);
-  return set ? s1 : s0;
-}
-// 16 values a lane -> one: lane l holds value l >> 2, summed over the 16 lanes
-// that share its low two bits up to the mirroring of the last step; two more
-// pair sums over lane bits 1 and 0 complete it.
-__device__ __forceinline__ float lane_sum16(const float (&v)[16], int lane) {
-  float w[8];
+// Sum over the 64 lanes of 16 values a lane, through LDS: red[t*kRedRow + lane]
+// holds them; lane l sums token l >> 2 over the 16 lanes of its quarter l & 3,
+// and the four quarters meet by data-parallel moves: the whole sum of token
+// l >> 2 in each of its four lanes.  (Halving the values with each lane bit in
+// registers instead took 45 issue slots a state against 18.)
+constexpr int kRedRow = 68;  // rows of 64 lanes shifted by four banks each
+__device__ __forceinline__ float lane_sums(const float* red, int lane) {
+  const float4* p = reinterpret_cast<const float4*>(red + (lane >> 2) * kRedRow + (lane & 3) * 16);
+  float4 v[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = pair_sum32(v[i], v[i + 8]);
+  for (int e = 0; e < 4; ++e) v[e] = p[e];
+  float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = pair_sum16(w[i], w[i + 4]);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) w[i] = pair_sum_dpp<0x128>(w[i], w[i + 2], lane & 8);
-  return pair_sum_dpp<0x141>(w[0], w[1], lane & 4);
-}
-__device__ __forceinline__ float lane_sum4(const float (&r)[4], int lane) {
-  const float a = pair_sum_dpp<0x4E>(r[0], r[2], lane & 2);
-  const float b = pair_sum_dpp<0x4E>(r[1], r[3], lane & 2);
-  return pair_sum_dpp<0xB1>(a, b, lane & 1);
+  for (int e = 0; e < 4; ++e) s += (v[e].x + v[e].y) + (v[e].z + v[e].w);
+  s += dpp_mov<0x4E>(s);
+  s += dpp_mov<0xB1>(s);
+  return s;
 }
 
-// Pass 3.  LDS per state and lane: the adjoint riding backwards, the summed
-// dA, and the state entering each 16-token step but the first.
+// Pass 3, two waves a SIMD: six values a token in registers beside the state's
+// own leave no room for a third (forced to three the compiler spills and the
+// step below took 792 us; tiles of 8 tokens at three waves took as long as
+// this, their loads of states and sums being twice as many).  LDS of a wave: the adjoint riding backwards and the summed dA, per
+// state and lane, and the values being summed over lanes.
 template <class IO, bool PACKED>
-__global__ __launch_bounds__(64 * kScanWaves) void scan_bwd_chunk_kernel(ScanArgs a, ScanGrid g, ScanWs ws, BwdWs bw) {
+__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(2, 2))) void scan_bwd_chunk_kernel(ScanArgs a, ScanGrid g, ScanWs ws, BwdWs bw) {
   typedef typename IO::type T;
   extern __shared__ float lds[];
-  const int lane = threadIdx.x & 63;
-  ScanBlock k;
-  if (!scan_block(g, a, k)) return;
+  const int lane = threadIdx.x;
+  const ScanBlock k = scan_block(g, a);
   const int N = (int)a.N;
-  const int st = N * 64;
-  float* gs = lds + k.wave * (int)(g.Q / kScanT + 1) * st + lane;  // gs[n*64]
-  float* as = gs + st;               // dA
-  float* hs = as + st;               // hs[(j-1)*st + n*64]: state entering step j >= 1
+  float* red = lds;
+  float* gs = lds + kScanT * kRedRow + lane;  // gs[n*64]
+  float* as = gs + N * 64;                    // dA
   const int64_t d = k.d0 + lane < k.dend ? k.d0 + lane : k.dend - 1;
   const bool ok = k.d0 + lane < k.dend;
   const int64_t co = (k.b * g.nc + k.c) * N * a.D + d;  // this chunk's slot
-  const float* h_in = ws.carry + co;
-  if (k.c == 0) h_in = a.h0 ? a.h0 + k.b * N * a.D + d : nullptr;
+  // the state entering the chunk; with none, any readable row times zero
+  const float* h_in = k.c == 0 ? (a.h0 ? a.h0 + k.b * N * a.D + d : nullptr) : ws.carry + co;
+  const bool entered = h_in != nullptr;
+  if (!entered) h_in = ws.carry + co;
   for (int n = 0; n < N; ++n) {
     gs[n * 64] = ws.adj[co + (int64_t)n * a.D];
     as[n * 64] = 0.f;
@@ -273,49 +258,8 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_bwd_chunk_kernel(ScanArg
   const RowPtrs<IO> p(a, k.b);
   const int off = (int)(d * sizeof(typename IO::type));
   const int nstep = (int)((k.t1 - k.t0 + kScanT - 1) / kScanT);
-
   const float* atp = ws.at + d;
   const float* e0 = ws.bc + (((k.b * a.G + k.grp) * g.ntile + k.t0 / kScanT) * N) * kEntry;
-
-  // states entering steps 1 .. nstep-1
-  if (nstep > 1) {
-    const float* ep = e0;
-    BCHalf<false> lo, hi;
-    lo.load(ep);
-    float a_n = atp[0];
-    for (int j = 0; j + 1 < nstep; ++j) {
-      const int64_t t0 = k.t0 + j * kScanT;
-      float dt[kScanT], x[kScanT];
-      const uint32_t starts = PACKED ? ws.starts[k.b * g.ntile + t0 / kScanT] : 0;
-      RawTile<IO> ru, rd;  // whole tiles: only the last one can be ragged
-      rd.load(p.dt, a.rows.dt, t0, kScanT, off);
-      ru.load(p.u, a.rows.u, t0, kScanT, off);
-      time_steps<IO>(rd, bias, a.softplus, kScanT, dt);
-#pragma unroll
-      for (int i = 0; i < kScanT; ++i) x[i] = dt[i] * ru.at(i);
-      for (int n = 0; n < N; ++n) {
-        const float an = a_n;
-        lo.settle();
-        hi.load(ep + kScanT);
-        a_n = atp[(int64_t)(n + 1 < N ? n + 1 : 0) * a.D];
-        float h = j ? hs[(j - 1) * st + n * 64] : (h_in ? h_in[(int64_t)n * a.D] : 0.f);
-        auto half = [&](const BCHalf<false>& e, int i0) {
-#pragma unroll
-          for (int i = i0; i < i0 + kHalf; ++i) {
-            if (PACKED && (starts >> i & 1)) h = 0.f;
-            h = fmaf(fast_exp2(dt[i] * an), h, x[i] * e.b(i - i0));
-          }
-        };
-        half(lo, 0);
-        hi.settle();
-        ep += kEntry;
-        lo.load(ep);
-        half(hi, kHalf);
-        hs[j * st + n * 64] = h;
-      }
-    }
-  }
-
   const bool whole = k.d0 + 64 <= k.dend;
   float dDsum = 0.f, dbsum = 0.f;
   const int64_t BL = a.B * a.L;
@@ -323,18 +267,26 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_bwd_chunk_kernel(ScanArg
   float* dBp = bw.bc + (k.cb * BL + k.b * a.L) * GN + k.grp * N;
   float* dCp = dBp + g.ncb * BL * GN;
   for (int j = nstep - 1; j >= 0; --j) {
-    const int64_t t0 = k.t0 + j * kScanT;
+    pace(nstep - 1 - j, nstep);
+    const int64_t t0 = k.t0 + j * kScanT, tile = k.b * g.ntile + t0 / kScanT;
     const int nt = tile_tokens(k, t0);
     float dt[kScanT], x[kScanT], gy[kScanT], y[kScanT], sB[kScanT], sA[kScanT];
-    const uint32_t starts = PACKED ? ws.starts[k.b * g.ntile + t0 / kScanT] : 0;
+    const uint32_t starts = PACKED ? ws.starts[tile] : 0;
+    // what reaches this tile of the chunk's entering state
+    bool reached = entered && (j == 0 || k.c > 0);  // chunk 0 started from the initial state
+    if (PACKED) {
+      for (int q = 0; q < j; ++q) reached = reached && ws.starts[tile - j + q] == 0;
+    }
+    const float tsd = j ? ws.tsdt[tile * a.D + d] : 0.f;
+    const float* ts = ws.tstate + tile * N * a.D + d;
     {
       RawTile<IO> ru, rd, rg, rz;
       rd.load(p.dt, a.rows.dt, t0, nt, off);
       ru.load(p.u, a.rows.u, t0, nt, off);
       rg.load(p.dy, a.D, t0, nt, off);
       if (p.z) rz.load(p.z, a.rows.z, t0, nt, off);
-      time_steps<IO>(rd, bias, a.softplus, nt, dt);
-      gated<IO>(rg, rz, p.z, gy);
+      time_steps(rd, bias, a.softplus, nt, dt);
+      gated(rg, rz, p.z, gy);
 #pragma unroll
       for (int i = 0; i < kScanT; ++i) {
         x[i] = dt[i] * ru.at(i);
@@ -355,36 +307,42 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_bwd_chunk_kernel(ScanArg
         }
       }
     }
+    BCPair<true> e;
     const float* ep = e0 + (int64_t)j * N * kEntry;
-    BCHalf<true> lo, hi;
-    lo.load(ep);
-    hi.load(ep + kScanT);
-    auto bv = [&](int i) { return i < kHalf ? lo.b(i) : hi.b(i - kHalf); };
-    auto cv = [&](int i) { return i < kHalf ? lo.c(i) : hi.c(i - kHalf); };
-    float a_n = atp[0];
-    float rB[4] = {}, rC[4] = {};  // the last four states' sums
+    e.load(ep);
+    float a_n = atp[0], in_n = h_in[0], ts_n = j ? ts[0] : 0.f;
+    float rB = 0.f, rC = 0.f;  // of token lane >> 2, state lane & 3 of four
     for (int n = 0; n < N; ++n) {
       const float an = a_n;
-      a_n = atp[(int64_t)(n + 1 < N ? n + 1 : 0) * a.D];
-      float dec[kScanT], h[kScanT], v[kScanT];
-      const float h0 = j ? hs[(j - 1) * st + n * 64] : (h_in ? h_in[(int64_t)n * a.D] : 0.f);
+      float h0 = ts_n;
+      if (reached) h0 = fmaf(fast_exp2(tsd * an), in_n, h0);
+      e.settle();
+      {
+        const int64_t nn = (int64_t)(n + 1 < N ? n + 1 : n) * a.D;
+        a_n = atp[nn];
+        in_n = h_in[nn];
+        if (j) ts_n = ts[nn];
+      }
+      float dec[kScanT], h[kScanT];
       float hp = h0;
 #pragma unroll
       for (int i = 0; i < kScanT; ++i) {
         dec[i] = fast_exp2(dt[i] * an);
         if (PACKED && (starts >> i & 1)) hp = 0.f;
-        hp = fmaf(dec[i], hp, x[i] * bv(i));
+        hp = fmaf(dec[i], hp, x[i] * e.b(i));
         h[i] = hp;
-        y[i] = fmaf(cv(i), hp, y[i]);
-        v[i] = hp * gy[i];
+        y[i] = fmaf(e.c(i), hp, y[i]);
+        red[i * kRedRow + lane] = hp * gy[i];
       }
-      const float sC = lane_sum16(v, lane);
+      __builtin_amdgcn_wave_barrier();
+      const float sumC = lane_sums(red, lane);
+      __builtin_amdgcn_wave_barrier();
       float ga = gs[n * 64], dA = as[n * 64];
 #pragma unroll
       for (int i = kScanT - 1; i >= 0; --i) {
-        const float gt = fmaf(cv(i), gy[i], ga);
-        v[i] = gt * x[i];
-        sB[i] = fmaf(gt, bv(i), sB[i]);
+        const float gt = fmaf(e.c(i), gy[i], ga);
+        red[i * kRedRow + lane] = gt * x[i];
+        sB[i] = fmaf(gt, e.b(i), sB[i]);
         ga = gt * dec[i];
         float q = ga * (i ? h[i > 0 ? i - 1 : 0] : h0);
         if (PACKED && (starts >> i & 1)) {
@@ -400,35 +358,37 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_bwd_chunk_kernel(ScanArg
       for (int i = 0; i < kScanT; ++i) asm volatile("" : "+v"(sA[i]), "+v"(sB[i]), "+v"(y[i]));
       asm volatile("" : "+v"(dA));
       // B and C are in use up to here; the next entry arrives behind the sums
+      // (asked for earlier, the 64 scalar registers of two entries spill)
       ep += kEntry;
-      lo.load(ep);
-      hi.load(ep + kScanT);
+      e.load(ep);
       gs[n * 64] = ga;
       as[n * 64] = dA;
-#pragma unroll
-      for (int e = 0; e < 3; ++e) {
-        rB[e] = rB[e + 1];
-        rC[e] = rC[e + 1];
-      }
-      rC[3] = sC;
-      rB[3] = lane_sum16(v, lane);
+      __builtin_amdgcn_wave_barrier();
+      const float sumB = lane_sums(red, lane);
+      __builtin_amdgcn_wave_barrier();
+      const bool mine = (n & 3) == (lane & 3);
+      rB = mine ? sumB : rB;
+      rC = mine ? sumC : rC;
       if ((n & 3) == 3) {
-        const float vB = lane_sum4(rB, lane), vC = lane_sum4(rC, lane);
         const int i = lane >> 2;
         if (i < nt) {
-          dBp[(t0 + i) * GN + n - 3 + (lane & 3)] = vB;
-          dCp[(t0 + i) * GN + n - 3 + (lane & 3)] = vC;
+          dBp[(t0 + i) * GN + n - 3 + (lane & 3)] = rB;
+          dCp[(t0 + i) * GN + n - 3 + (lane & 3)] = rC;
         }
       }
     }
-    // gradients of this tile's tokens (its inputs once more, from cache)
+    // gradients of this tile's tokens; its inputs once more, from cache (by an
+    // offset the compiler cannot tell from the first one's: it would keep
+    // their 64 registers through the loop instead)
     const int64_t r0 = k.b * a.L;
+    int off2 = off;
+    asm volatile("" : "+v"(off2));
     RawTile<IO> ru, rd, rg, rz;
-    ru.load(p.u, a.rows.u, t0, nt, off);
-    if (a.softplus) rd.load(p.dt, a.rows.dt, t0, nt, off);
+    ru.load(p.u, a.rows.u, t0, nt, off2);
+    if (a.softplus) rd.load(p.dt, a.rows.dt, t0, nt, off2);
     if (p.z) {
-      rg.load(p.dy, a.D, t0, nt, off);
-      rz.load(p.z, a.rows.z, t0, nt, off);
+      rg.load(p.dy, a.D, t0, nt, off2);
+      rz.load(p.z, a.rows.z, t0, nt, off2);
     }
 #pragma unroll
     for (int i = 0; i < kScanT; ++i) {
@@ -464,8 +424,8 @@ __global__ __launch_bounds__(64 * kScanWaves) void scan_bwd_chunk_kernel(ScanArg
       for (int n = 0; n < N; ++n) a.dinit[(k.b * N + n) * a.D + d] = gs[n * 64];
     // the chunk's adjoint has been used: its slot takes the chunk's dA
     for (int n = 0; n < N; ++n) ws.adj[co + (int64_t)n * a.D] = as[n * 64];
-    bw.dDp[(k.b * g.nc + k.c) * a.D + d] = dDsum;
-    bw.dbp[(k.b * g.nc + k.c) * a.D + d] = dbsum;
+    bw.dDb[(k.b * g.nc + k.c) * 2 * a.D + d] = dDsum;
+    bw.dDb[((k.b * g.nc + k.c) * 2 + 1) * a.D + d] = dbsum;
   }
 }
 
@@ -494,33 +454,66 @@ __global__ __launch_bounds__(256) void scan_bc_reduce_kernel(ScanArgs a, int64_t
   else static_cast<T*>(a.dB)[row * a.grows.b + col] = IO::put(acc * kLn2);  // dt in units of ln 2
 }
 
-// dA [D,N] from the chunk sums' [N][D]
-__global__ __launch_bounds__(256) void scan_da_kernel(const float* __restrict__ s, int64_t D, int64_t N,
-                                                      float* __restrict__ dA) {
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (idx >= D * N) return;
-  dA[idx] = s[idx % N * D + idx / N] * kLn2;  // dt in units of ln 2
+// dA [D,N], dD and ddt_bias [D]: the chunks' partial sums ([R][N D] and
+// [R][2 D]) added over the rows in slices of 16 and the slices in order.
+constexpr int kSlices = 16;
+__global__ __launch_bounds__(64 * kSlices) void scan_param_kernel(const float* __restrict__ dAp,
+                                                                  const float* __restrict__ dDb, int64_t R, int64_t D,
+                                                                  int64_t N, float* __restrict__ dA,
+                                                                  float* __restrict__ dD, float* __restrict__ db) {
+  __shared__ float part[kSlices][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  const bool ok = c < (N + 2) * D;
+  if (!ok) c = (N + 2) * D - 1;
+  const bool isA = c < N * D;
+  const float* p = isA ? dAp + c : dDb + c - N * D;
+  const int64_t step = isA ? N * D : 2 * D;
+  float acc = 0.f;
+  int64_t r = w;
+  for (; r + 7 * kSlices < R; r += 8 * kSlices) {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = p[(r + e * kSlices) * step];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc += v[e];
+  }
+  for (; r < R; r += kSlices) acc += p[r * step];
+  part[w][lane] = acc;
+  __syncthreads();
+  if (w == 0 && ok) {
+    float s = part[0][lane];
+#pragma unroll
+    for (int e = 1; e < kSlices; ++e) s += part[e][lane];
+    if (isA) dA[c % D * N + c / D] = s * kLn2;  // dt in units of ln 2
+    else if (c < (N + 1) * D) { if (dD) dD[c - N * D] = s; }
+    else if (db) db[c - (N + 1) * D] = s;
+  }
 }
 
-// Steps of 16 tokens a chunk: as many as leave eight waves a compute unit
-// their LDS (N <= 32: four), fewer for large N.
-static ScanGrid backward_grid(int64_t L, int64_t D, int64_t N, int64_t G) {
+// Chunks of four tiles: the carried states then cost a quarter of the per-tile
+// states.  Shorter ones, down to one tile, where four would leave the third
+// pass's two waves a SIMD unfilled (3 x 777 tokens of 1002 channels, fp32:
+// 122 us with four tiles, 97 with two).
+static ScanGrid backward_grid(int64_t B, int64_t L, int64_t D, int64_t N, int64_t G) {
   ScanGrid g;
   g.ncb = (D / G + 63) / 64;
-  g.Q = kScanT * (N <= 32 ? 4 : N <= 64 ? 2 : 1);
+  const int64_t slots = (int64_t)device_cu_count() * 8;
+  int tiles = 4;
+  while (tiles > 1 && B * G * g.ncb * ((L + kScanT * tiles - 1) / (kScanT * tiles)) < slots) tiles /= 2;
+  g.Q = kScanT * tiles;
   g.nc = (L + g.Q - 1) / g.Q;
   g.ntile = (L + kScanT - 1) / kScanT;
-  g.wpb = scan_wpb(g.ncb, 64 * (int64_t)sizeof(float) * N * (g.Q / kScanT + 1));
   return g;
 }
 
 static size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct BwdLayout {
-  size_t carry, adj, sdt, cut, pack, at, starts, bc, dDp, dbp, sums, total;
+  size_t carry, adj, sdt, cut, pack, at, starts, tstate, tsdt, bc, dDb, total;
 };
 static BwdLayout backward_layout(int64_t B, int64_t L, int64_t D, int64_t N, int64_t G) {
-  const ScanGrid g = backward_grid(L, D, N, G);
+  const ScanGrid g = backward_grid(B, L, D, N, G);
   BwdLayout w;
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t r = o; o += up256(bytes); return r; };
@@ -531,10 +524,10 @@ static BwdLayout backward_layout(int64_t B, int64_t L, int64_t D, int64_t N, int
   w.pack = take(sizeof(float) * scan_bc_floats(B, G, g.ntile, N));
   w.at = take(sizeof(float) * N * D);
   w.starts = take(sizeof(uint32_t) * B * g.ntile);
+  w.tstate = take(sizeof(float) * B * g.ntile * N * D);
+  w.tsdt = take(sizeof(float) * B * g.ntile * D);
   w.bc = take(sizeof(float) * 2 * g.ncb * B * L * G * N);
-  w.dDp = take(sizeof(float) * B * g.nc * D);
-  w.dbp = take(sizeof(float) * B * g.nc * D);
-  w.sums = take(sizeof(float) * N * D);
+  w.dDb = take(sizeof(float) * B * g.nc * 2 * D);
   w.total = o;
   return w;
 }
@@ -544,16 +537,16 @@ size_t scan_backward_ws_bytes(int64_t B, int64_t L, int64_t D, int64_t N, int64_
 
 template <class IO, bool PACKED>
 static hipError_t scan_backward_t(const ScanArgs& a, hipStream_t s) {
-  const ScanGrid g = backward_grid(a.L, a.D, a.N, a.G);
+  const ScanGrid g = backward_grid(a.B, a.L, a.D, a.N, a.G);
   const BwdLayout w = backward_layout(a.B, a.L, a.D, a.N, a.G);
   char* base = static_cast<char*>(a.ws);
   auto at = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
   const ScanWs ws = {at(w.carry), at(w.sdt), reinterpret_cast<int*>(base + w.cut), at(w.adj), at(w.pack), at(w.at),
-                     PACKED ? reinterpret_cast<uint32_t*>(base + w.starts) : nullptr};
-  const BwdWs bw = {at(w.bc), at(w.dDp), at(w.dbp)};
-  const dim3 grid((unsigned)scan_blocks(g, a.G), (unsigned)g.nc, (unsigned)a.B), block(64 * g.wpb);
-  const size_t per = 64 * sizeof(float) * a.N * g.wpb;
-  const size_t lds1 = 2 * per, lds3 = per * (2 + g.Q / kScanT - 1);
+                     PACKED ? reinterpret_cast<uint32_t*>(base + w.starts) : nullptr, at(w.tstate), at(w.tsdt)};
+  const BwdWs bw = {at(w.bc), at(w.dDb)};
+  const dim3 grid((unsigned)(a.G * g.ncb), (unsigned)g.nc, (unsigned)a.B), block(64);
+  const size_t per = 64 * sizeof(float) * a.N;
+  const size_t lds1 = 2 * per, lds3 = 2 * per + sizeof(float) * kScanT * kRedRow;
   hipError_t e;
   if (lds1 > 64 * 1024 || lds3 > 64 * 1024) {
     e = hipFuncSetAttribute(reinterpret_cast<const void*>(&scan_bwd_local_kernel<IO, PACKED>),
@@ -574,13 +567,10 @@ static hipError_t scan_backward_t(const ScanArgs& a, hipStream_t s) {
   const int64_t nbc = 2 * a.B * a.L * a.G * a.N;
   hipLaunchKernelGGL((scan_bc_reduce_kernel<IO>), dim3((unsigned)((nbc + 255) / 256)), dim3(256), 0, s, a, g.ncb, bw.bc);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  float* sums = at(w.sums);
-  if ((e = launch_colsum(ws.adj, a.B * g.nc, a.N * a.D, sums, s)) != hipSuccess) return e;
-  hipLaunchKernelGGL(scan_da_kernel, dim3((unsigned)((a.N * a.D + 255) / 256)), dim3(256), 0, s, sums, a.D, a.N, a.dA);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  if (a.dD && (e = launch_colsum(bw.dDp, a.B * g.nc, a.D, a.dD, s)) != hipSuccess) return e;
-  if (a.ddt_bias && (e = launch_colsum(bw.dbp, a.B * g.nc, a.D, a.ddt_bias, s)) != hipSuccess) return e;
-  return hipSuccess;
+  const int64_t np = (a.N + 2) * a.D;
+  hipLaunchKernelGGL(scan_param_kernel, dim3((unsigned)((np + 63) / 64)), dim3(64 * kSlices), 0, s, ws.adj, bw.dDb,
+                     a.B * g.nc, a.D, a.N, a.dA, a.dD, a.ddt_bias);
+  return hipGetLastError();
 }
 
 hipError_t launch_scan_backward(const ScanArgs& a, bool bf16, hipStream_t s) {
