@@ -487,7 +487,7 @@ ssd_status ssd_selective_scan_backward(const ssd_scan_shape* shape, const ssd_sc
 size_t ssd_selective_scan_backward_workspace_bytes(const ssd_scan_shape* shape);
 
 /*
- * Layer norm of `rows` dense rows of `dim` columns (dim <= 65536), with an
+ * Layer norm of `rows` dense rows of `dim` columns (dim <= 16384), with an
  * optional residual stream in front:
  *   r = x + residual, stored in residual_out (res_dtype; the stored value is
  *       normalised), or r = x without one

@@ -10,17 +10,50 @@
 //     dw[k] = sum_t dpre[t] x[t-W+1+k],  dbias = sum_t dpre[t]
 //
 // Bound by memory: 2 elements moved per output (3 backward) against 2W + 4
-// operations.  A thread owns 16 bytes of channels (one channel where rows or
-// widths are not whole 16-byte units) and walks a run of tokens with the last
-// W-1 inputs in registers, so each input is read once plus a halo of W-1 rows
-// per run; consecutive lanes take consecutive channels of one row.
+// operations.  A wave takes 64 neighbouring groups of V channels (8 bytes a
+// lane; one channel where rows are not whole 8-byte units) and walks a run of
+// tokens with the last W-1 inputs in registers, so each input is read once
+// plus a halo of W-1 rows per run.  The run, its row addresses and its
+// sequence starts are the same for the whole wave and live in scalars.
 #include "layer_device.hpp"
 #include "layer_launch.hpp"
 
 namespace ssd {
 
-constexpr int kConvThreads = 256;
+constexpr int kConvWaves = 4;  // runs of a block
+constexpr int kConvThreads = 64 * kConvWaves;
 constexpr int kConvBatch = 8;  // token rows whose loads are in flight together
+
+// The wave's run of tokens and its lane's channels.
+struct ConvRun {
+  int64_t rb, b, t0, t1, d;
+  bool live;  // the run exists
+  bool ok;    // the lane has channels (one without takes the last ones' and stores nothing)
+};
+template <int V>
+__device__ __forceinline__ ConvRun conv_run_of(const ConvArgs& a, int64_t nrun, int run, int64_t ncb) {
+  ConvRun r;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  r.rb = (int64_t)(blockIdx.x / (unsigned)ncb) * kConvWaves + wave;
+  r.live = r.rb < a.B * nrun;
+  const int64_t rb = r.live ? r.rb : 0;
+  r.b = rb / nrun;
+  r.t0 = (rb - r.b * nrun) * run;
+  r.t1 = r.t0 + run < a.L ? r.t0 + run : a.L;
+  r.d = ((int64_t)(blockIdx.x % (unsigned)ncb) * 64 + (threadIdx.x & 63)) * V;
+  r.ok = r.d < a.D;
+  if (!r.ok) r.d = a.D - V;
+  return r;
+}
+
+// Bit i of the result (uniform): token t + i, i < n <= 64, lies in the row and
+// begins another sequence than its predecessor's.
+__device__ __forceinline__ uint64_t start_bits(const int* sr, int64_t t, int n, int64_t L) {
+  const int64_t j = t + (threadIdx.x & 63);
+  bool s = false;
+  if ((int)(threadIdx.x & 63) < n && j > 0 && j < L) s = sr[j] != sr[j - 1];
+  return __ballot(s);
+}
 
 // Window of the W-1 inputs before the current token, oldest first.
 template <int W, int V>
@@ -42,7 +75,7 @@ struct Window {
   }
 };
 
-template <class IO, int V, int W>
+template <int V, int W>
 __device__ __forceinline__ void load_weights(const float* w, const float* bias, int64_t d, float (&wv)[W][V],
                                              float (&bv)[V]) {
 #pragma unroll
@@ -59,49 +92,45 @@ template <class IO, int V, int W, bool PACKED>
 __device__ __forceinline__ void window_at(const ConvArgs& a, const typename IO::type* xr, const int* sr, int64_t b,
                                           int64_t d, int64_t t0, Window<W, V>& win) {
   win.clear();
+  const uint64_t st = PACKED ? start_bits(sr, t0 - (W - 1), W, a.L) : 0;
 #pragma unroll
   for (int k = 0; k < W - 1; ++k) {
     const int64_t j = t0 - (W - 1) + k;
     float x[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) x[e] = 0.f;
-    if (j >= 0) {
-      if (PACKED && j > 0 && sr[j] != sr[j - 1]) win.clear();
-      load_vec<IO, V>(xr + j * a.x_row, x);
-    } else if (a.init) {
-      load_vec<IO, V>(static_cast<const typename IO::type*>(a.init) + (b * (W - 1) + j + W - 1) * a.D + d, x);
-    }
+    if (j >= 0) load_vec<IO, V>(xr + j * a.x_row, x);
+    else if (a.init) load_vec<IO, V>(static_cast<const typename IO::type*>(a.init) + (b * (W - 1) + j + W - 1) * a.D + d, x);
+    if (PACKED && (st >> k & 1)) win.clear();
     win.push(x);
   }
-  if (PACKED && t0 > 0 && t0 < a.L && sr[t0] != sr[t0 - 1]) win.clear();
+  if (PACKED && (st >> (W - 1) & 1)) win.clear();
 }
 
 template <class IO, int V, int W, bool PACKED, bool SILU>
-__global__ __launch_bounds__(kConvThreads) void conv_forward_kernel(ConvArgs a, int64_t nrun, int run, int64_t total) {
+__global__ __launch_bounds__(kConvThreads) void conv_forward_kernel(ConvArgs a, int64_t nrun, int run, int64_t ncb) {
   typedef typename IO::type T;
-  const int64_t idx = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
-  if (idx >= total) return;
-  const int64_t Dv = a.D / V;
-  const int64_t d = (idx % Dv) * V;
-  const int64_t rb = idx / Dv;
-  const int64_t b = rb / nrun, t0 = (rb % nrun) * run;
-  const int64_t t1 = t0 + run < a.L ? t0 + run : a.L;
-  const T* xr = static_cast<const T*>(a.x) + b * a.L * a.x_row + d;
-  const int* sr = PACKED ? a.seq_idx + b * a.L : nullptr;
-  T* yr = static_cast<T*>(a.y) + b * a.L * a.D + d;
+  const ConvRun r = conv_run_of<V>(a, nrun, run, ncb);
+  if (!r.live) return;  // whole waves only: sequence starts are found by ballot
+  const T* xr = static_cast<const T*>(a.x) + r.b * a.L * a.x_row + r.d;
+  const int* sr = PACKED ? a.seq_idx + r.b * a.L : nullptr;
+  T* yr = static_cast<T*>(a.y) + r.b * a.L * a.D + r.d;
   float wv[W][V], bv[V];
-  load_weights<IO, V, W>(a.w, a.bias, d, wv, bv);
+  load_weights<V, W>(a.w, a.bias, r.d, wv, bv);
   Window<W, V> win;
-  window_at<IO, V, W, PACKED>(a, xr, sr, b, d, t0, win);
-  for (int64_t t = t0; t < t1; t += kConvBatch) {
+  window_at<IO, V, W, PACKED>(a, xr, sr, r.b, r.d, r.t0, win);
+  for (int64_t t = r.t0; t < r.t1; t += kConvBatch) {
+    const int n = (int)(r.t1 - t < kConvBatch ? r.t1 - t : kConvBatch);
     float x[kConvBatch][V];
 #pragma unroll
-    for (int i = 0; i < kConvBatch; ++i)
-      load_vec<IO, V>(xr + (t + i < t1 ? t + i : t1 - 1) * a.x_row, x[i]);
+    for (int i = 0; i < kConvBatch; ++i) load_vec<IO, V>(xr + (t + (i < n ? i : n - 1)) * a.x_row, x[i]);
+    // the run's first token was seen to when the window was made
+    uint64_t st = PACKED ? start_bits(sr, t, n, a.L) : 0;
+    if (PACKED && t == r.t0) st &= ~uint64_t(1);
 #pragma unroll
     for (int i = 0; i < kConvBatch; ++i) {
-      if (t + i >= t1) break;
-      if (PACKED && t + i > t0 && sr[t + i] != sr[t + i - 1]) win.clear();
+      if (i >= n) break;
+      if (PACKED && (st >> i & 1)) win.clear();
       float o[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) {
@@ -111,14 +140,14 @@ __global__ __launch_bounds__(kConvThreads) void conv_forward_kernel(ConvArgs a, 
         p = fmaf(wv[W - 1][e], x[i][e], p);
         o[e] = SILU ? p * sigmoid(p) : p;
       }
-      store_vec<IO, V>(yr + (t + i) * a.D, o);
+      if (r.ok) store_vec<IO, V>(yr + (t + i) * a.D, o);
       win.push(x[i]);
     }
   }
-  if (t1 == a.L && a.final_state) {
+  if (r.t1 == a.L && a.final_state && r.ok) {
 #pragma unroll
     for (int k = 0; k < W - 1; ++k)
-      store_vec<IO, V>(static_cast<T*>(a.final_state) + (b * (W - 1) + k) * a.D + d, win.v[k]);
+      store_vec<IO, V>(static_cast<T*>(a.final_state) + (r.b * (W - 1) + k) * a.D + r.d, win.v[k]);
   }
 }
 
@@ -151,27 +180,14 @@ __global__ __launch_bounds__(kConvThreads) void conv_seq_states_kernel(ConvArgs 
 // the window) reaches dx of t-W+1 .. t; the pending sums of the last W-1
 // inputs ride in registers beside the window.  A run also computes the W-1
 // dpre after its end, for its own last inputs.  Inputs before the run belong
-// to the run before it (or to the initial state).
+// to the run before it (or to the initial state).  The block's runs meet in
+// LDS before dw and dbias go to memory.
 template <class IO, int V, int W, bool PACKED, bool SILU>
-__global__ __launch_bounds__(kConvThreads) void conv_backward_kernel(ConvArgs a, int64_t nrun, int run, int64_t total) {
+__global__ __launch_bounds__(kConvThreads) void conv_backward_kernel(ConvArgs a, int64_t nrun, int run, int64_t ncb) {
   typedef typename IO::type T;
-  const int64_t idx = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
-  if (idx >= total) return;
-  const int64_t Dv = a.D / V;
-  const int64_t d = (idx % Dv) * V;
-  const int64_t rb = idx / Dv;
-  const int64_t b = rb / nrun, t0 = (rb % nrun) * run;
-  const int64_t t1 = t0 + run < a.L ? t0 + run : a.L;
-  const int64_t t2 = t1 + W - 1 < a.L ? t1 + W - 1 : a.L;  // dpre needed up to here
-  const T* xr = static_cast<const T*>(a.x) + b * a.L * a.x_row + d;
-  const T* gr = static_cast<const T*>(a.dy) + b * a.L * a.D + d;
-  const int* sr = PACKED ? a.seq_idx + b * a.L : nullptr;
-  T* dxr = static_cast<T*>(a.dx) + b * a.L * a.dx_row + d;
-  float wv[W][V], bv[V];
-  load_weights<IO, V, W>(a.w, a.bias, d, wv, bv);
-  Window<W, V> win, pend;  // pend.v[k]: dx collected so far of the input win.v[k]
-  window_at<IO, V, W, PACKED>(a, xr, sr, b, d, t0, win);
-  pend.clear();
+  __shared__ float part[kConvWaves][(W + 1) * V][64];
+  const ConvRun r = conv_run_of<V>(a, nrun, run, ncb);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float dw[W][V], db[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) {
@@ -179,119 +195,140 @@ __global__ __launch_bounds__(kConvThreads) void conv_backward_kernel(ConvArgs a,
 #pragma unroll
     for (int k = 0; k < W; ++k) dw[k][e] = 0.f;
   }
-  // A sequence start at t ends every pending sum: the inputs before it are
-  // complete.  The W-1 pending inputs of token t are t-W+1 .. t-1.
-  auto finish = [&](int64_t j, const float* g) {  // dx of input j is complete
-    float o[V];
+  if (r.live) {
+    const int64_t t0 = r.t0, t1 = r.t1, b = r.b, d = r.d;
+    const int64_t t2 = t1 + W - 1 < a.L ? t1 + W - 1 : a.L;  // dpre needed up to here
+    const T* xr = static_cast<const T*>(a.x) + b * a.L * a.x_row + d;
+    const T* gr = static_cast<const T*>(a.dy) + b * a.L * a.D + d;
+    const int* sr = PACKED ? a.seq_idx + b * a.L : nullptr;
+    T* dxr = static_cast<T*>(a.dx) + b * a.L * a.dx_row + d;
+    float wv[W][V], bv[V];
+    load_weights<V, W>(a.w, a.bias, d, wv, bv);
+    Window<W, V> win, pend;  // pend.v[k]: dx collected so far of the input win.v[k]
+    window_at<IO, V, W, PACKED>(a, xr, sr, b, d, t0, win);
+    pend.clear();
+    // tokens since the last sequence start, the token of the start itself
+    // counting 0; no more than W-1 matter
+    int since = W;
+    if (PACKED) {
+      const uint64_t st = start_bits(sr, t0 - W + 1, W, a.L);
+      since = st ? __builtin_clzll(st) - (64 - W) : W;
+    }
+    auto finish = [&](int64_t j, const float* g) {  // dx of input j is complete
+      float o[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = g[e];
-    if (j >= 0) {
-      if (j >= t0 && j < t1) {
-        if (a.dfinal && j >= a.L - (W - 1) ) {
-          bool own = true;
-          if (PACKED)
-            for (int64_t q = j + 1; q < a.L; ++q) own = own && sr[q] == sr[q - 1];
-          if (own) {
-            float f[V];
-            load_vec<IO, V>(static_cast<const T*>(a.dfinal) + (b * (W - 1) + j - (a.L - (W - 1))) * a.D + d, f);
-#pragma unroll
-            for (int e = 0; e < V; ++e) o[e] += f[e];
-          }
-        }
-        store_vec<IO, V>(dxr + j * a.dx_row, o);
-      }
-    } else if (t0 == 0 && a.dinit) {
-      // row j of the initial state; with fewer tokens than taps part of it is
-      // still in the final state
-      const int64_t k = j + W - 1;
-      const int64_t kf = k - a.L;  // its place in the final state
-      if (a.dfinal && kf >= 0) {
+      for (int e = 0; e < V; ++e) o[e] = g[e];
+      // with dfinal: the place of input j in the final state, if it is there
+      // and no sequence starts after it
+      const int64_t f = j - (a.L - (W - 1));
+      if (a.dfinal && f >= 0) {
         bool own = true;
         if (PACKED)
-          for (int64_t q = 1; q < a.L; ++q) own = own && sr[q] == sr[q - 1];
+          for (int64_t q = j < 0 ? 1 : j + 1; q < a.L; ++q) own = own && sr[q] == sr[q - 1];
         if (own) {
-          float f[V];
-          load_vec<IO, V>(static_cast<const T*>(a.dfinal) + (b * (W - 1) + kf) * a.D + d, f);
+          float v[V];
+          load_vec<IO, V>(static_cast<const T*>(a.dfinal) + (b * (W - 1) + f) * a.D + d, v);
 #pragma unroll
-          for (int e = 0; e < V; ++e) o[e] += f[e];
+          for (int e = 0; e < V; ++e) o[e] += v[e];
         }
       }
-      store_vec<IO, V>(static_cast<T*>(a.dinit) + (b * (W - 1) + k) * a.D + d, o);
-    }
-  };
-  for (int64_t t = t0; t < t2; t += kConvBatch) {
-    float x[kConvBatch][V], g[kConvBatch][V];
-#pragma unroll
-    for (int i = 0; i < kConvBatch; ++i) {
-      const int64_t tc = t + i < t2 ? t + i : t2 - 1;
-      load_vec<IO, V>(xr + tc * a.x_row, x[i]);
-      load_vec<IO, V>(gr + tc * a.D, g[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kConvBatch; ++i) {
-      if (t + i >= t2) break;
-      const int64_t tt = t + i;
-      bool live[W - 1];  // whether pending input k shares the token's sequence
-#pragma unroll
-      for (int k = 0; k < W - 1; ++k) live[k] = true;
-      if (PACKED) {
-        bool same = true;
-#pragma unroll
-        for (int k = W - 2; k >= 0; --k) {
-          const int64_t j = tt - (W - 1) + k;
-          if (j + 1 > 0 && sr[j + 1] != sr[j < 0 ? 0 : j]) same = false;
-          live[k] = same;
-        }
-        if (tt > 0 && sr[tt] != sr[tt - 1]) win.clear();
+      if (!r.ok) return;
+      if (j >= 0) {
+        if (j >= t0 && j < t1) store_vec<IO, V>(dxr + j * a.dx_row, o);
+      } else if (t0 == 0 && a.dinit) {
+        store_vec<IO, V>(static_cast<T*>(a.dinit) + (b * (W - 1) + j + W - 1) * a.D + d, o);
       }
-      const bool in = tt < t1;
-      float fresh[V];
+    };
+    for (int64_t t = t0; t < t2; t += kConvBatch) {
+      const int n = (int)(t2 - t < kConvBatch ? t2 - t : kConvBatch);
+      float x[kConvBatch][V], g[kConvBatch][V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float p = bv[e];
+      for (int i = 0; i < kConvBatch; ++i) {
+        const int64_t tc = t + (i < n ? i : n - 1);
+        load_vec<IO, V>(xr + tc * a.x_row, x[i]);
+        load_vec<IO, V>(gr + tc * a.D, g[i]);
+      }
+      const uint64_t st = PACKED ? start_bits(sr, t, n, a.L) : 0;
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) p = fmaf(wv[k][e], win.v[k][e], p);
-        p = fmaf(wv[W - 1][e], x[i][e], p);
-        float dp = g[i][e];
-        if (SILU) dp *= dsilu(p, sigmoid(p));
+      for (int i = 0; i < kConvBatch; ++i) {
+        if (i >= n) break;
+        const int64_t tt = t + i;
+        if (PACKED) {
+          since = (st >> i & 1) ? 0 : (since < W ? since + 1 : W);
+          if (since == 0) win.clear();
+        }
+        const bool in = tt < t1;
+        float dp[V], fresh[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          float p = bv[e];
+#pragma unroll
+          for (int k = 0; k < W - 1; ++k) p = fmaf(wv[k][e], win.v[k][e], p);
+          p = fmaf(wv[W - 1][e], x[i][e], p);
+          dp[e] = g[i][e];
+          if (SILU) dp[e] *= dsilu(p, sigmoid(p));
+          fresh[e] = dp[e] * wv[W - 1][e];
+        }
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
-          const float c = dp * wv[k][e];
-          pend.v[k][e] += (!PACKED || live[k]) ? c : 0.f;
+          if (!PACKED || W - 1 - k <= since) {  // the input is of the token's sequence
+#pragma unroll
+            for (int e = 0; e < V; ++e) pend.v[k][e] = fmaf(dp[e], wv[k][e], pend.v[k][e]);
+          }
         }
-        fresh[e] = dp * wv[W - 1][e];
         if (in) {
 #pragma unroll
-          for (int k = 0; k < W - 1; ++k) dw[k][e] = fmaf(dp, win.v[k][e], dw[k][e]);
-          dw[W - 1][e] = fmaf(dp, x[i][e], dw[W - 1][e]);
-          db[e] += dp;
+          for (int e = 0; e < V; ++e) {
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) dw[k][e] = fmaf(dp[e], win.v[k][e], dw[k][e]);
+            dw[W - 1][e] = fmaf(dp[e], x[i][e], dw[W - 1][e]);
+            db[e] += dp[e];
+          }
         }
+        finish(tt - (W - 1), pend.v[0]);
+        win.push(x[i]);
+        pend.push(fresh);
       }
-      finish(tt - (W - 1), pend.v[0]);
-      win.push(x[i]);
-      pend.push(fresh);
+    }
+    if (t2 == a.L) {  // no dpre after the row: what is pending is complete
+#pragma unroll
+      for (int k = 0; k < W - 1; ++k) finish(a.L - (W - 1) + k, pend.v[k]);
     }
   }
-  if (t2 == a.L) {  // no dpre after the row: what is pending is complete
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) finish(a.L - (W - 1) + k, pend.v[k]);
+  for (int e = 0; e < V; ++e) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) part[wave][k * V + e][lane] = dw[k][e];
+    part[wave][W * V + e][lane] = db[e];
   }
-  // partial sums of this run: ws[rb][W+1][D]
-  float* ws = a.ws + rb * (W + 1) * a.D + d;
+  __syncthreads();
+  // partial sums of the block's runs: ws[row group][W+1][D]
+  if (r.ok) {
+    float* ws = a.ws + (int64_t)(blockIdx.x / (unsigned)ncb) * (W + 1) * a.D + r.d;
+    for (int k = wave; k <= W; k += kConvWaves) {
+      float s[V];
 #pragma unroll
-  for (int k = 0; k < W; ++k) store_vec<IoF32, V>(ws + k * a.D, dw[k]);
-  store_vec<IoF32, V>(ws + W * a.D, db);
+      for (int e = 0; e < V; ++e) {
+        s[e] = 0.f;
+#pragma unroll
+        for (int q = 0; q < kConvWaves; ++q) s[e] += part[q][k * V + e][lane];
+      }
+      store_vec<IoF32, V>(ws + k * a.D, s);
+    }
+  }
 }
 
-// dw [D,W] and dbias [D] from the column sums [W+1][D]
+// dw [D,W] and dbias [D] from the row groups' partial sums [R][W+1][D]
 template <int W>
-__global__ __launch_bounds__(kConvThreads) void conv_weight_kernel(const float* __restrict__ sums, int64_t D,
-                                                                   float* __restrict__ dw, float* __restrict__ db) {
-  const int64_t d = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
-  if (d >= D) return;
-#pragma unroll
-  for (int k = 0; k < W; ++k) dw[d * W + k] = sums[k * D + d];
-  if (db) db[d] = sums[W * D + d];
+__global__ __launch_bounds__(kColsumThreads) void conv_param_kernel(const float* __restrict__ part, int64_t R, int64_t D,
+                                                                    float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ float lds[kColsumThreads];
+  const int64_t c = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63), C = (W + 1) * D;
+  const float s = column_sum(part + (c < C ? c : C - 1), R, C, lds);
+  if (threadIdx.x >= 64 || c >= C) return;
+  const int64_t k = c / D, d = c - k * D;
+  if (k < W) dw[d * W + k] = s;
+  else if (db) db[d] = s;
 }
 
 template <class IO, int V, int W, bool SILU>
@@ -306,7 +343,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_step_kernel(ConvArgs a, con
   load_vec<IO, V>(static_cast<const T*>(a.x) + b * a.x_row + d, x);
 #pragma unroll
   for (int k = 0; k < W - 1; ++k) load_vec<IO, V>(state + (b * (W - 1) + k) * a.D + d, st[k]);
-  load_weights<IO, V, W>(a.w, a.bias, d, wv, bv);
+  load_weights<V, W>(a.w, a.bias, d, wv, bv);
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     float p = bv[e];
@@ -321,31 +358,42 @@ __global__ __launch_bounds__(kConvThreads) void conv_step_kernel(ConvArgs a, con
   store_vec<IO, V>(state_out + (b * (W - 1) + W - 2) * a.D + d, x);
 }
 
-static bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// 16-byte accesses need whole 16-byte units in every row
-static bool conv_vec(const ConvArgs& a, int kvec) {
-  return a.D % kvec == 0 && a.x_row % kvec == 0 && a.dx_row % kvec == 0 && al16(a.x) && al16(a.dx);
+// Vector accesses (four channels a lane) need rows in whole multiples of them
+static bool conv_vec(const ConvArgs& a, int es) {
+  const uintptr_t m = 4 * es - 1;
+  return a.D % 4 == 0 && a.x_row % 4 == 0 && a.dx_row % 4 == 0 && (reinterpret_cast<uintptr_t>(a.x) & m) == 0 &&
+         (reinterpret_cast<uintptr_t>(a.dx) & m) == 0;
 }
 
-// Tokens a thread walks: runs of 32 keep the halo under a tenth of the reads;
-// short runs where 32 would leave compute units without a wave.
-static int conv_run(int64_t B, int64_t L, int64_t Dv) {
-  int run = 32;
-  while (run > kConvBatch && B * ((L + run - 1) / run) * Dv < (int64_t)device_cu_count() * 8 * 64) run /= 2;
+// Tokens of a run: `most` (the halo is then a small part of the reads), less
+// where that leaves a compute unit fewer than eight waves.
+static int conv_run(int64_t B, int64_t L, int64_t ncb, int most) {
+  int run = most;
+  while (run > kConvBatch && B * ((L + run - 1) / run) * ncb < (int64_t)device_cu_count() * 8) run /= 2;
   return run;
 }
+static int64_t conv_blocks_of(int64_t D, int V) { return (D / V + 63) / 64; }
+
+struct ConvGrid {
+  int run;
+  int64_t nrun, ncb, groups;  // groups of kConvWaves runs
+};
+static ConvGrid conv_grid(int64_t B, int64_t L, int64_t D, int V, int most) {
+  ConvGrid g;
+  g.ncb = conv_blocks_of(D, V);
+  g.run = conv_run(B, L, g.ncb, most);
+  g.nrun = (L + g.run - 1) / g.run;
+  g.groups = (B * g.nrun + kConvWaves - 1) / kConvWaves;
+  return g;
+}
+constexpr int kConvFwdRun = 32, kConvBwdRun = 32;
 
 template <class IO, int V, int W, bool PACKED>
 static hipError_t conv_forward_v(const ConvArgs& a, hipStream_t s) {
-  const int64_t Dv = a.D / V;
-  const int run = conv_run(a.B, a.L, Dv);
-  const int64_t nrun = (a.L + run - 1) / run, total = a.B * nrun * Dv;
-  const dim3 grid((unsigned)((total + kConvThreads - 1) / kConvThreads));
-  if (a.silu)
-    hipLaunchKernelGGL((conv_forward_kernel<IO, V, W, PACKED, true>), grid, dim3(kConvThreads), 0, s, a, nrun, run, total);
-  else
-    hipLaunchKernelGGL((conv_forward_kernel<IO, V, W, PACKED, false>), grid, dim3(kConvThreads), 0, s, a, nrun, run, total);
+  const ConvGrid g = conv_grid(a.B, a.L, a.D, V, kConvFwdRun);
+  const dim3 grid((unsigned)(g.groups * g.ncb));
+  auto kern = a.silu ? conv_forward_kernel<IO, V, W, PACKED, true> : conv_forward_kernel<IO, V, W, PACKED, false>;
+  hipLaunchKernelGGL(kern, grid, dim3(kConvThreads), 0, s, a, g.nrun, g.run, g.ncb);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.nseq == 0) return e;
   hipLaunchKernelGGL((conv_seq_states_kernel<IO, W>),
@@ -354,39 +402,24 @@ static hipError_t conv_forward_v(const ConvArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Partial rows of dw / dbias: one per run of tokens.
-static int conv_bwd_run(int64_t B, int64_t L, int64_t Dv) {
-  int run = 64;
-  while (run > kConvBatch && B * ((L + run - 1) / run) * Dv < (int64_t)device_cu_count() * 8 * 64) run /= 2;
-  return run;
-}
-
 template <class IO, int V, int W, bool PACKED>
 static hipError_t conv_backward_v(const ConvArgs& a, hipStream_t s) {
-  const int64_t Dv = a.D / V;
-  const int run = conv_bwd_run(a.B, a.L, Dv);
-  const int64_t nrun = (a.L + run - 1) / run, total = a.B * nrun * Dv;
-  const dim3 grid((unsigned)((total + kConvThreads - 1) / kConvThreads));
-  if (a.silu)
-    hipLaunchKernelGGL((conv_backward_kernel<IO, V, W, PACKED, true>), grid, dim3(kConvThreads), 0, s, a, nrun, run, total);
-  else
-    hipLaunchKernelGGL((conv_backward_kernel<IO, V, W, PACKED, false>), grid, dim3(kConvThreads), 0, s, a, nrun, run, total);
+  const ConvGrid g = conv_grid(a.B, a.L, a.D, V, kConvBwdRun);
+  const dim3 grid((unsigned)(g.groups * g.ncb));
+  auto kern = a.silu ? conv_backward_kernel<IO, V, W, PACKED, true> : conv_backward_kernel<IO, V, W, PACKED, false>;
+  hipLaunchKernelGGL(kern, grid, dim3(kConvThreads), 0, s, a, g.nrun, g.run, g.ncb);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t C = (W + 1) * a.D;
-  float* sums = a.ws + a.B * nrun * C;
-  if ((e = launch_colsum(a.ws, a.B * nrun, C, sums, s)) != hipSuccess) return e;
-  hipLaunchKernelGGL((conv_weight_kernel<W>), dim3((unsigned)((a.D + kConvThreads - 1) / kConvThreads)),
-                     dim3(kConvThreads), 0, s, sums, a.D, a.dw, a.dbias);
+  hipLaunchKernelGGL((conv_param_kernel<W>), dim3((unsigned)(((W + 1) * a.D + 63) / 64)), dim3(kColsumThreads), 0, s,
+                     a.ws, g.groups, a.D, a.dw, a.dbias);
   return hipGetLastError();
 }
 
 size_t conv_backward_ws_bytes(int64_t B, int64_t L, int64_t D, int W) {
-  // the widest thread leaves the shortest runs: size for the smaller of both
-  const int r8 = conv_bwd_run(B, L, D / 8 > 0 ? D / 8 : 1), r1 = conv_bwd_run(B, L, D);
-  const int run = r8 < r1 ? r8 : r1;
-  const int64_t nrun = (L + run - 1) / run;
-  return sizeof(float) * (size_t)((B * nrun + 1) * (W + 1) * D);
+  // vector or single-element accesses depend on the pointers: the larger of both
+  const int64_t g4 = D >= 4 ? conv_grid(B, L, D, 4, kConvBwdRun).groups : 0;
+  const int64_t g1 = conv_grid(B, L, D, 1, kConvBwdRun).groups;
+  return sizeof(float) * (size_t)(g4 > g1 ? g4 : g1) * (size_t)((W + 1) * D);
 }
 
 template <class IO, int V, int W>
@@ -422,8 +455,8 @@ hipError_t launch_conv_forward(const ConvArgs& a, bool bf16, hipStream_t s) {
     typedef decltype(io) IO;
     return with_width(a.W, [&](auto w) {
       constexpr int W = decltype(w)::value;
-      if (conv_vec(a, IO::kVec))
-        return a.seq_idx ? conv_forward_v<IO, IO::kVec, W, true>(a, s) : conv_forward_v<IO, IO::kVec, W, false>(a, s);
+      if (conv_vec(a, sizeof(typename IO::type)))
+        return a.seq_idx ? conv_forward_v<IO, 4, W, true>(a, s) : conv_forward_v<IO, 4, W, false>(a, s);
       return a.seq_idx ? conv_forward_v<IO, 1, W, true>(a, s) : conv_forward_v<IO, 1, W, false>(a, s);
     });
   });
@@ -434,8 +467,8 @@ hipError_t launch_conv_backward(const ConvArgs& a, bool bf16, hipStream_t s) {
     typedef decltype(io) IO;
     return with_width(a.W, [&](auto w) {
       constexpr int W = decltype(w)::value;
-      if (conv_vec(a, IO::kVec))
-        return a.seq_idx ? conv_backward_v<IO, IO::kVec, W, true>(a, s) : conv_backward_v<IO, IO::kVec, W, false>(a, s);
+      if (conv_vec(a, sizeof(typename IO::type)))
+        return a.seq_idx ? conv_backward_v<IO, 4, W, true>(a, s) : conv_backward_v<IO, 4, W, false>(a, s);
       return a.seq_idx ? conv_backward_v<IO, 1, W, true>(a, s) : conv_backward_v<IO, 1, W, false>(a, s);
     });
   });
@@ -446,7 +479,7 @@ hipError_t launch_conv_step(const ConvArgs& a, const void* state, void* state_ou
     typedef decltype(io) IO;
     return with_width(a.W, [&](auto w) {
       constexpr int W = decltype(w)::value;
-      if (conv_vec(a, IO::kVec)) return conv_step_v<IO, IO::kVec, W>(a, state, state_out, s);
+      if (conv_vec(a, sizeof(typename IO::type))) return conv_step_v<IO, 4, W>(a, state, state_out, s);
       return conv_step_v<IO, 1, W>(a, state, state_out, s);
     });
   });

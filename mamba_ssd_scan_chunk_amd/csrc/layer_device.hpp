@@ -21,11 +21,17 @@ struct IoF32 {
 };
 
 // V consecutive elements as fp32: one 16-byte access per IO::kVec elements
-// (V a multiple of it), or a single element (V = 1).
+// (V a multiple of it), one 8-byte access (four bf16), or a single element.
 template <class IO, int V>
 __device__ __forceinline__ void load_vec(const typename IO::type* p, float* o) {
   if constexpr (V == 1) {
     o[0] = IO::get(p[0]);
+  } else if constexpr (IO::kVec == 8 && V == 4) {
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    o[0] = __uint_as_float(q.x << 16);
+    o[1] = __uint_as_float(q.x & 0xffff0000u);
+    o[2] = __uint_as_float(q.y << 16);
+    o[3] = __uint_as_float(q.y & 0xffff0000u);
   } else if constexpr (IO::kVec == 8) {
 #pragma unroll
     for (int k = 0; k < V; k += 8) {
@@ -49,6 +55,8 @@ template <class IO, int V>
 __device__ __forceinline__ void store_vec(typename IO::type* p, const float* v) {
   if constexpr (V == 1) {
     p[0] = IO::put(v[0]);
+  } else if constexpr (IO::kVec == 8 && V == 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
   } else if constexpr (IO::kVec == 8) {
 #pragma unroll
     for (int k = 0; k < V; k += 8)
@@ -81,6 +89,32 @@ __device__ __forceinline__ float softplus2(float w) {
   const float lost = e - (u - 1.f);
   const float l = fmaf(lost, fmaxf(fmaf(-0.5f * kLog2e, e, kLog2e), 0.f), __builtin_amdgcn_logf(u));
   return fmaxf(l, w);
+}
+
+// Sum of a column of fp32 partials, p[0], p[stride], .. (R of them), for a
+// block of 16 waves that take 64 columns a lane each: wave w adds rows w,
+// w + 16, .., the waves' sums meet in LDS (a float a thread) and are added in
+// order.  Valid in the first wave; every thread must call it.
+constexpr int kColsumThreads = 1024;
+__device__ __forceinline__ float column_sum(const float* p, int64_t R, int64_t stride, float* lds) {
+  constexpr int S = kColsumThreads / 64;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  float acc = 0.f;
+  int64_t r = w;
+  for (; r + 7 * S < R; r += 8 * S) {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = p[(r + e * S) * stride];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc += v[e];
+  }
+  for (; r < R; r += S) acc += p[r * stride];
+  lds[threadIdx.x] = acc;
+  __syncthreads();
+  float s = lds[lane];
+#pragma unroll
+  for (int e = 1; e < S; ++e) s += lds[e * 64 + lane];
+  return s;
 }
 
 }  // namespace ssd

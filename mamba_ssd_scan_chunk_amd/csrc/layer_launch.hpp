@@ -95,13 +95,9 @@ struct NormArgs {
   float* db;                // or null
   float* ws;
 };
-constexpr int64_t kNormMaxDim = 65536;
+constexpr int64_t kNormMaxDim = 16384;
 size_t norm_backward_ws_bytes(int64_t rows, int64_t D);
 hipError_t launch_norm_forward(const NormArgs& a, bool bf16, hipStream_t s);
 hipError_t launch_norm_backward(const NormArgs& a, bool bf16, hipStream_t s);
-
-// out[c] = sum over r of in[r][c] (fp32, fixed order), written as fp32 or
-// rounded to bf16.  `seg` > 1 also sums `seg` runs: see layer_reduce.hip.
-hipError_t launch_colsum(const float* in, int64_t R, int64_t C, float* out, hipStream_t s);
 
 }  // namespace ssd

@@ -10,9 +10,12 @@
 //     dw = sum over rows of dy xh,  dbias = sum over rows of dy
 //
 // Bound by memory.  A row stays in registers between its one read and its one
-// write: 64, 256 or 1024 threads a row by its length, 16 bytes a load (single
-// elements where rows are not whole 16-byte units).  The backward keeps dw and
-// dbias of its columns in registers over the rows a block walks; the blocks'
+// write.  Forward: a wave a row up to 4096 columns, 256 threads beyond, 16
+// bytes a load (single elements where rows are not whole units of 8).
+// Backward: 64, 256 or 1024 threads a row, 16 values a thread at most, so that
+// the five values a column (x, dy, w, dw, dbias) leave room for waves beside;
+// blocks walk rows, the next row's loads in flight behind the sums of this
+// one, and keep dw and dbias of their columns in registers.  The blocks'
 // partial sums are added in a fixed order.
 #include "layer_device.hpp"
 #include "layer_launch.hpp"
@@ -48,7 +51,7 @@ __device__ __forceinline__ void load_cols(const void* base, int64_t row0, int64_
 }
 
 template <class IO, class RO, int V, int NV, int TPR>
-__global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void norm_forward_kernel(NormArgs a) {
+__global__ __launch_bounds__(256) void norm_forward_kernel(NormArgs a) {
   __shared__ float red[TPR == 64 ? 1 : TPR / 64];
   const int64_t row = TPR == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
   if (TPR == 64 && row >= a.rows) return;
@@ -110,137 +113,218 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void norm_forward_kernel(Nor
   }
 }
 
+// Both sums of a row at once over its TPR threads; `red` holds two rounds of
+// them, so that one barrier a row is enough.
+template <int TPR>
+__device__ __forceinline__ float2 row_sum2(float a, float b, float2* red) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    a += __shfl_xor(a, o, 64);
+    b += __shfl_xor(b, o, 64);
+  }
+  if constexpr (TPR > 64) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = make_float2(a, b);
+    __syncthreads();
+    a = b = 0.f;
+#pragma unroll
+    for (int k = 0; k < TPR / 64; ++k) {
+      a += red[k].x;
+      b += red[k].y;
+    }
+  }
+  return make_float2(a, b);
+}
+
+// Threads of a backward block: whole rows of TPR threads, four rows for TPR = 64.
+constexpr int norm_bwd_threads(int tpr) { return tpr == 64 ? 256 : tpr; }
+
 // IO: type of dy and dx; RO: type of x, dres and dres_out.
 template <class IO, class RO, int V, int NV, int TPR>
-__global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void norm_backward_kernel(NormArgs a) {
-  __shared__ float red[TPR == 64 ? 1 : TPR / 64];
+__global__ __launch_bounds__(norm_bwd_threads(TPR)) void norm_backward_kernel(NormArgs a) {
+  __shared__ float2 red[2][TPR == 64 ? 1 : TPR / 64];
+  __shared__ float part[TPR == 64 ? 3 * 2 * 64 * NV * V : 1];
   const int tid = TPR == 64 ? threadIdx.x & 63 : threadIdx.x;
-  const int64_t first = TPR == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  const int wave = threadIdx.x >> 6;
+  const int64_t first = TPR == 64 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
   const int64_t step = TPR == 64 ? (int64_t)gridDim.x * 4 : gridDim.x;
   const float inv = 1.f / (float)a.D;
-  float w[NV][V], dw[NV][V], db[NV][V];
+  auto col = [&](int j) { return ((int64_t)j * TPR + tid) * V; };
+  float w[NV][V], dw[NV][V], db[NV][V], x[NV][V], g[NV][V];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    load_cols<IoF32, V>(a.w, 0, ((int64_t)j * TPR + tid) * V, a.D, w[j]);
+    load_cols<IoF32, V>(a.w, 0, col(j), a.D, w[j]);
 #pragma unroll
     for (int e = 0; e < V; ++e) dw[j][e] = db[j][e] = 0.f;
   }
-  for (int64_t row = first; row < a.rows; row += step) {
-    const int64_t r0 = row * a.D;
-    const float rstd = a.rstd[row], mean = a.mean ? a.mean[row] : 0.f;
-    float x[NV][V], g[NV][V];
+  auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      load_cols<RO, V>(a.x, r0, ((int64_t)j * TPR + tid) * V, a.D, x[j]);
-      load_cols<IO, V>(a.dy, r0, ((int64_t)j * TPR + tid) * V, a.D, g[j]);
+      load_cols<RO, V>(a.x, row * a.D, col(j), a.D, x[j]);
+      load_cols<IO, V>(a.dy, row * a.D, col(j), a.D, g[j]);
     }
+  };
+  // the next row's loads in flight behind this one's sums, but for the blocks
+  // of 1024 threads whose 128 registers do not hold both
+  constexpr bool kAhead = TPR < 1024 || NV * V <= 8;
+  if (kAhead && first < a.rows) fetch(first);
+  int round = 0;
+  for (int64_t row = first; row < a.rows; row += step, round ^= 1) {
+    const int64_t r0 = row * a.D;
+    if (!kAhead) fetch(row);
+    const float rstd = a.rstd[row], mean = a.mean ? a.mean[row] : 0.f;
+    float xh[NV][V], v[NV][V], q[NV][V];
     float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (a.dres) {
+        load_cols<RO, V>(a.dres, r0, col(j), a.D, q[j]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) q[j][e] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        xh[j][e] = (x[j][e] - mean) * rstd;
+        dw[j][e] = fmaf(g[j][e], xh[j][e], dw[j][e]);
+        db[j][e] += g[j][e];
+        v[j][e] = g[j][e] * w[j][e];  // zero past the row
+        s1 += v[j][e];
+        s2 = fmaf(v[j][e], xh[j][e], s2);
+      }
+    }
+    if (kAhead && row + step < a.rows) fetch(row + step);
+    const float2 s = row_sum2<TPR>(s1, s2, red[round]);
+    const float m1 = a.rms ? 0.f : s.x * inv, m2 = s.y * inv;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (col(j) < a.D) {
+        float o[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = fmaf(rstd, v[j][e] - fmaf(xh[j][e], m2, m1), q[j][e]);
+        store_vec<IO, V>(static_cast<typename IO::type*>(a.dx) + r0 + col(j), o);
+        if (a.dres_out) store_vec<RO, V>(static_cast<typename RO::type*>(a.dres_out) + r0 + col(j), o);
+      }
+    }
+  }
+  // a row of partial sums a block: ws[block][2][D]; with four waves a block
+  // they meet first
+  if constexpr (TPR == 64) {
+    constexpr int P = 64 * NV * V;
+    if (wave > 0) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          part[((wave - 1) * 2) * P + (j * V + e) * 64 + tid] = dw[j][e];
+          part[((wave - 1) * 2 + 1) * P + (j * V + e) * 64 + tid] = db[j][e];
+        }
+    }
+    __syncthreads();
+    if (wave > 0) return;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float xh = (x[j][e] - mean) * rstd;
-        dw[j][e] = fmaf(g[j][e], xh, dw[j][e]);
-        db[j][e] += g[j][e];
-        const float v = g[j][e] * w[j][e];  // zero past the row
-        s1 += v;
-        s2 = fmaf(v, xh, s2);
-        x[j][e] = xh;
-        g[j][e] = v;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          dw[j][e] += part[(k * 2) * P + (j * V + e) * 64 + tid];
+          db[j][e] += part[(k * 2 + 1) * P + (j * V + e) * 64 + tid];
+        }
       }
-    s2 = row_sum<TPR>(s2, red) * inv;
-    s1 = a.rms ? 0.f : row_sum<TPR>(s1, red) * inv;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int64_t c = ((int64_t)j * TPR + tid) * V;
-      if (c < a.D) {
-        float q[V], o[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) q[e] = 0.f;
-        if (a.dres) load_vec<RO, V>(static_cast<const typename RO::type*>(a.dres) + r0 + c, q);
-#pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = fmaf(rstd, g[j][e] - fmaf(x[j][e], s2, s1), q[e]);
-        store_vec<IO, V>(static_cast<typename IO::type*>(a.dx) + r0 + c, o);
-        if (a.dres_out) store_vec<RO, V>(static_cast<typename RO::type*>(a.dres_out) + r0 + c, o);
-      }
-    }
   }
-  // partial sums: ws[first][2][D]
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int64_t c = ((int64_t)j * TPR + tid) * V;
-    if (c < a.D) {
-      store_vec<IoF32, V>(a.ws + first * 2 * a.D + c, dw[j]);
-      store_vec<IoF32, V>(a.ws + first * 2 * a.D + a.D + c, db[j]);
+    if (col(j) < a.D) {
+      store_vec<IoF32, V>(a.ws + (int64_t)blockIdx.x * 2 * a.D + col(j), dw[j]);
+      store_vec<IoF32, V>(a.ws + (int64_t)blockIdx.x * 2 * a.D + a.D + col(j), db[j]);
     }
   }
 }
 
-__global__ __launch_bounds__(256) void norm_weight_kernel(const float* __restrict__ sums, int64_t D,
-                                                          float* __restrict__ dw, float* __restrict__ db) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c >= D) return;
-  dw[c] = sums[c];
-  if (db) db[c] = sums[D + c];
+// dw and dbias [D] from the walkers' partial sums [R][2][D]
+__global__ __launch_bounds__(kColsumThreads) void norm_param_kernel(const float* __restrict__ part, int64_t R, int64_t D,
+                                                                    float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ float lds[kColsumThreads];
+  const int64_t c = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+  const float s = column_sum(part + (c < 2 * D ? c : 2 * D - 1), R, 2 * D, lds);
+  if (threadIdx.x >= 64 || c >= 2 * D) return;
+  if (c < D) dw[c] = s;
+  else if (db) db[c - D] = s;
 }
 
-// Threads a row: a wave up to 64 values a thread, then 256, then 1024.
-static int norm_tpr(int64_t D) { return D <= 64 * 64 ? 64 : D <= 256 * 64 ? 256 : 1024; }
+// Backward: threads a row, for 16 values a thread at most.
+static int norm_bwd_tpr(int64_t D) { return D <= 64 * 16 ? 64 : D <= 256 * 16 ? 256 : 1024; }
 
-// Rows of partial sums the backward leaves: one per wave or block that walks rows.
-static int64_t norm_bwd_walkers(int64_t rows, int64_t D) {
+// Blocks the backward walks the rows with, each leaving a row of partial sums:
+// two a compute unit (one of 1024 threads), but four rows a walker at least
+// where that still leaves half a block a unit: the partial sums cost as much
+// as reading one fp32 row each, and their addition as much again.
+static int64_t norm_bwd_blocks(int64_t rows, int64_t D) {
   const int64_t cus = device_cu_count();
-  const int64_t w = norm_tpr(D) == 64 ? cus * 8 : norm_tpr(D) == 256 ? cus * 2 : cus;
-  return rows < w ? rows : w;
+  const int tpr = norm_bwd_tpr(D);
+  const int64_t walkers = tpr == 64 ? (rows + 3) / 4 : rows;  // if each walked one row
+  int64_t b = tpr == 1024 ? cus : 2 * cus;
+  const int64_t quarter = (walkers + 3) / 4;
+  if (quarter < b) b = quarter > cus / 2 ? quarter : cus / 2;
+  return walkers < b ? walkers : b;
 }
 
 size_t norm_backward_ws_bytes(int64_t rows, int64_t D) {
-  return sizeof(float) * (size_t)(2 * D) * (size_t)(norm_bwd_walkers(rows, D) + 3 + 1);
+  return sizeof(float) * (size_t)(2 * D) * (size_t)norm_bwd_blocks(rows, D);
 }
 
-template <class IO, class RO, int V, int NV, int TPR, bool BWD>
-static hipError_t norm_go(const NormArgs& a, hipStream_t s) {
-  if (!BWD) {
-    const int64_t blocks = TPR == 64 ? (a.rows + 3) / 4 : a.rows;
-    hipLaunchKernelGGL((norm_forward_kernel<IO, RO, V, NV, TPR>), dim3((unsigned)blocks), dim3(TPR == 64 ? 256 : TPR), 0,
-                       s, a);
-    return hipGetLastError();
-  }
-  int64_t walkers = norm_bwd_walkers(a.rows, a.D);
-  if (TPR == 64) walkers = (walkers + 3) / 4 * 4;  // whole blocks of four waves
-  hipLaunchKernelGGL((norm_backward_kernel<IO, RO, V, NV, TPR>), dim3((unsigned)(TPR == 64 ? walkers / 4 : walkers)),
-                     dim3(TPR == 64 ? 256 : TPR), 0, s, a);
+template <class IO, class RO, int V, int NV, int TPR>
+static hipError_t norm_fwd_go(const NormArgs& a, hipStream_t s) {
+  const int64_t blocks = TPR == 64 ? (a.rows + 3) / 4 : a.rows;
+  hipLaunchKernelGGL((norm_forward_kernel<IO, RO, V, NV, TPR>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+template <class IO, class RO, int V, int NV, int TPR>
+static hipError_t norm_bwd_go(const NormArgs& a, hipStream_t s) {
+  const int64_t blocks = norm_bwd_blocks(a.rows, a.D);
+  hipLaunchKernelGGL((norm_backward_kernel<IO, RO, V, NV, TPR>), dim3((unsigned)blocks), dim3(norm_bwd_threads(TPR)), 0,
+                     s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  float* sums = a.ws + walkers * 2 * a.D;
-  if ((e = launch_colsum(a.ws, walkers, 2 * a.D, sums, s)) != hipSuccess) return e;
-  hipLaunchKernelGGL(norm_weight_kernel, dim3((unsigned)((a.D + 255) / 256)), dim3(256), 0, s, sums, a.D, a.dw, a.db);
+  hipLaunchKernelGGL(norm_param_kernel, dim3((unsigned)((2 * a.D + 63) / 64)), dim3(kColsumThreads), 0, s, a.ws, blocks,
+                     a.D, a.dw, a.db);
   return hipGetLastError();
 }
 
 // Values a thread holds: NV runs of V (the loads past a short row are skipped).
-template <class IO, class RO, int V, int TPR, bool BWD>
-static hipError_t norm_nv(const NormArgs& a, hipStream_t s) {
-  const int64_t per = (a.D + TPR - 1) / TPR;  // elements a thread
-  if (per <= 8) return norm_go<IO, RO, V, 8 / V, TPR, BWD>(a, s);
-  if (per <= 16) return norm_go<IO, RO, V, 16 / V, TPR, BWD>(a, s);
-  if (per <= 24) return norm_go<IO, RO, V, 24 / V, TPR, BWD>(a, s);
-  if (per <= 40) return norm_go<IO, RO, V, 40 / V, TPR, BWD>(a, s);
-  return norm_go<IO, RO, V, 64 / V, TPR, BWD>(a, s);
+template <class IO, class RO, int V, int TPR>
+static hipError_t norm_fwd_nv(const NormArgs& a, hipStream_t s) {
+  const int64_t per = (a.D + TPR - 1) / TPR;
+  if (per <= 8) return norm_fwd_go<IO, RO, V, 8 / V, TPR>(a, s);
+  if (per <= 16) return norm_fwd_go<IO, RO, V, 16 / V, TPR>(a, s);
+  if (per <= 40) return norm_fwd_go<IO, RO, V, 40 / V, TPR>(a, s);
+  return norm_fwd_go<IO, RO, V, 64 / V, TPR>(a, s);
+}
+template <class IO, class RO, int V, int TPR>
+static hipError_t norm_bwd_nv(const NormArgs& a, hipStream_t s) {
+  const int64_t per = (a.D + TPR - 1) / TPR;
+  if (per <= 8) return norm_bwd_go<IO, RO, V, 8 / V, TPR>(a, s);
+  if (per <= 12) return norm_bwd_go<IO, RO, V, 12 / V, TPR>(a, s);
+  return norm_bwd_go<IO, RO, V, 16 / V, TPR>(a, s);
 }
 
 template <class IO, class RO, bool BWD>
 static hipError_t norm_types(const NormArgs& a, hipStream_t s) {
-  const int tpr = norm_tpr(a.D);
-  // 16-byte loads of the narrower type: whole units of 8 elements a row
-  if (a.D % 8 == 0) {
-    if (tpr == 64) return norm_nv<IO, RO, 8, 64, BWD>(a, s);
-    if (tpr == 256) return norm_nv<IO, RO, 8, 256, BWD>(a, s);
-    return norm_nv<IO, RO, 8, 1024, BWD>(a, s);
+  if constexpr (BWD) {
+    const int tpr = norm_bwd_tpr(a.D);
+    if (a.D % 4 == 0) {
+      if (tpr == 64) return norm_bwd_nv<IO, RO, 4, 64>(a, s);
+      if (tpr == 256) return norm_bwd_nv<IO, RO, 4, 256>(a, s);
+      return norm_bwd_nv<IO, RO, 4, 1024>(a, s);
+    }
+    if (tpr == 64) return norm_bwd_nv<IO, RO, 1, 64>(a, s);
+    if (tpr == 256) return norm_bwd_nv<IO, RO, 1, 256>(a, s);
+    return norm_bwd_nv<IO, RO, 1, 1024>(a, s);
+  } else {
+    const bool wave = a.D <= 64 * 64;
+    if (a.D % 8 == 0) return wave ? norm_fwd_nv<IO, RO, 8, 64>(a, s) : norm_fwd_nv<IO, RO, 8, 256>(a, s);
+    return wave ? norm_fwd_nv<IO, RO, 1, 64>(a, s) : norm_fwd_nv<IO, RO, 1, 256>(a, s);
   }
-  if (tpr == 64) return norm_nv<IO, RO, 1, 64, BWD>(a, s);
-  if (tpr == 256) return norm_nv<IO, RO, 1, 256, BWD>(a, s);
-  return norm_nv<IO, RO, 1, 1024, BWD>(a, s);
 }
 
 template <bool BWD>

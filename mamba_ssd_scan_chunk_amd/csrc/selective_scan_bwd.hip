@@ -454,41 +454,22 @@ __global__ __launch_bounds__(256) void scan_bc_reduce_kernel(ScanArgs a, int64_t
   else static_cast<T*>(a.dB)[row * a.grows.b + col] = IO::put(acc * kLn2);  // dt in units of ln 2
 }
 
-// dA [D,N], dD and ddt_bias [D]: the chunks' partial sums ([R][N D] and
-// [R][2 D]) added over the rows in slices of 16 and the slices in order.
-constexpr int kSlices = 16;
-__global__ __launch_bounds__(64 * kSlices) void scan_param_kernel(const float* __restrict__ dAp,
-                                                                  const float* __restrict__ dDb, int64_t R, int64_t D,
-                                                                  int64_t N, float* __restrict__ dA,
-                                                                  float* __restrict__ dD, float* __restrict__ db) {
-  __shared__ float part[kSlices][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  int64_t c = (int64_t)blockIdx.x * 64 + lane;
+// dA [D,N], dD and ddt_bias [D] from the chunks' partial sums ([R][N D] and
+// [R][2 D])
+__global__ __launch_bounds__(kColsumThreads) void scan_param_kernel(const float* __restrict__ dAp,
+                                                                    const float* __restrict__ dDb, int64_t R, int64_t D,
+                                                                    int64_t N, float* __restrict__ dA,
+                                                                    float* __restrict__ dD, float* __restrict__ db) {
+  __shared__ float lds[kColsumThreads];
+  int64_t c = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
   const bool ok = c < (N + 2) * D;
   if (!ok) c = (N + 2) * D - 1;
   const bool isA = c < N * D;
-  const float* p = isA ? dAp + c : dDb + c - N * D;
-  const int64_t step = isA ? N * D : 2 * D;
-  float acc = 0.f;
-  int64_t r = w;
-  for (; r + 7 * kSlices < R; r += 8 * kSlices) {
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = p[(r + e * kSlices) * step];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc += v[e];
-  }
-  for (; r < R; r += kSlices) acc += p[r * step];
-  part[w][lane] = acc;
-  __syncthreads();
-  if (w == 0 && ok) {
-    float s = part[0][lane];
-#pragma unroll
-    for (int e = 1; e < kSlices; ++e) s += part[e][lane];
-    if (isA) dA[c % D * N + c / D] = s * kLn2;  // dt in units of ln 2
-    else if (c < (N + 1) * D) { if (dD) dD[c - N * D] = s; }
-    else if (db) db[c - (N + 1) * D] = s;
-  }
+  const float s = column_sum(isA ? dAp + c : dDb + c - N * D, R, isA ? N * D : 2 * D, lds);
+  if (threadIdx.x >= 64 || !ok) return;
+  if (isA) dA[c % D * N + c / D] = s * kLn2;  // dt in units of ln 2
+  else if (c < (N + 1) * D) { if (dD) dD[c - N * D] = s; }
+  else if (db) db[c - (N + 1) * D] = s;
 }
 
 // Chunks of four tiles: the carried states then cost a quarter of the per-tile
@@ -568,7 +549,7 @@ static hipError_t scan_backward_t(const ScanArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((scan_bc_reduce_kernel<IO>), dim3((unsigned)((nbc + 255) / 256)), dim3(256), 0, s, a, g.ncb, bw.bc);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int64_t np = (a.N + 2) * a.D;
-  hipLaunchKernelGGL(scan_param_kernel, dim3((unsigned)((np + 63) / 64)), dim3(64 * kSlices), 0, s, ws.adj, bw.dDb,
+  hipLaunchKernelGGL(scan_param_kernel, dim3((unsigned)((np + 63) / 64)), dim3(kColsumThreads), 0, s, ws.adj, bw.dDb,
                      a.B * g.nc, a.D, a.N, a.dA, a.dD, a.ddt_bias);
   return hipGetLastError();
 }

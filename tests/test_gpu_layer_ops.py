@@ -89,6 +89,8 @@ CONV = [
     (1, 1000, 33, 3, 7, None, False),
     (2, 517, 264, 4, 5, [100, 1, 1, 3], True),
     (1, 64, 2048, 4, 0, [8], False),
+    (2, 70, 260, 4, 0, [1, 2, 5, 13], True),  # one group of channels in the last wave
+    (1, 40, 5, 3, 0, [3, 1, 6], True),
 ]
 
 
@@ -319,7 +321,7 @@ def test_other_sequences_nan_stays_there(dtype):
 
 # (rows, D)
 NORM = [(1, 1), (3, 7), (1, 8), (5, 64), (4, 768), (130, 1537), (33, 2560), (9, 4096), (7, 4100), (3, 6001),
-        (2, 20000), (2, 65536), (2100, 72)]
+        (2, 16384), (3, 16381), (2100, 72), (600, 1024)]
 
 
 @pytest.mark.parametrize("rms", [False, True])
