@@ -5,6 +5,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <initializer_list>
+
 #include "layer_launch.hpp"
 
 namespace {
@@ -51,9 +53,8 @@ ssd_status check_conv(const ssd_conv_shape* s, bool step) {
   if (step && s->seqlen != 1) return SSD_ERR_SHAPE;
   if (s->width < 2 || s->width > 4) return SSD_ERR_UNSUPPORTED;
   SSD_TRY(product({s->batch, s->seqlen, s->channels}, kMaxElems));
-  // threads of the forward (a channel and at least 8 tokens each) in 32-bit blocks of 256
-  const int64_t runs = (s->seqlen - 1) / 8 + 1;
-  return product({s->batch, runs, s->channels}, (k31 - 1) * 256);
+  // waves (64 channels and at least 8 tokens each) in 31 bits
+  return product({s->batch, (s->seqlen - 1) / 8 + 1, (s->channels - 1) / 64 + 1}, k31 - 1);
 }
 
 ssd::ConvArgs conv_args(const ssd_conv_shape* s) {
@@ -96,6 +97,9 @@ ssd_status scan_rows(const ssd_scan_shape* s, const ssd_scan_rows* r, ssd_dtype 
   SSD_TRY(row_stride(r->Bm, gn, tok, &o->b));
   SSD_TRY(row_stride(r->Cm, gn, tok, &o->c));
   SSD_TRY(row_stride(r->z, D, tok, &o->z));
+  // a tile's 16 rows are addressed by 32-bit byte offsets from its first
+  for (int64_t v : {o->u, o->dt, o->b, o->c, o->z})
+    if (v >= int64_t(1) << 25) return SSD_ERR_UNSUPPORTED;
   // B and C are read in 4-byte units
   if (in == SSD_BF16 && (o->b % 2 != 0 || o->c % 2 != 0)) return SSD_ERR_ALIGN;
   return SSD_OK;
