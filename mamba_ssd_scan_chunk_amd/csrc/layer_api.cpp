@@ -81,10 +81,12 @@ ssd_status check_scan(const ssd_scan_shape* s, bool step) {
   if (step && s->seqlen != 1) return SSD_ERR_SHAPE;
   if (s->channels % s->ngroups != 0) return SSD_ERR_SHAPE;
   if (!ssd::scan_dstate_supported(s->dstate)) return SSD_ERR_UNSUPPORTED;
-  // grid limits: batches and 16-token chunks in 16-bit dimensions, channel blocks in 31 bits
-  if (s->batch > 65535 || (s->seqlen - 1) / 16 + 1 > 65535 || s->channels >= k31) return SSD_ERR_UNSUPPORTED;
+  // grid limits: twice the batches and the 16-token chunks in 16-bit dimensions, channel blocks in 31 bits
+  if (s->batch > 32767 || (s->seqlen - 1) / 16 + 1 > 65535 || s->channels >= k31) return SSD_ERR_UNSUPPORTED;
   SSD_TRY(product({s->batch, s->seqlen, s->channels}, kMaxElems));
   SSD_TRY(product({s->batch, s->seqlen, s->ngroups, s->dstate}, (int64_t(1) << 36)));
+  // a block a tile of a group in 31 bits, beside the few for A and the starts
+  SSD_TRY(product({s->batch, (s->seqlen - 1) / 16 + 1, s->ngroups}, int64_t(1) << 30));
   return product({s->batch, s->dstate, s->channels}, (int64_t(1) << 38));
 }
 

@@ -29,44 +29,53 @@ namespace ssd {
 // zero), A to [N,D], and the sequence starts to a bit a token.  Small beside
 // the scan (2 G N of each token's elements against 3 D or more), it spares the
 // inner loops the address arithmetic and the widening of scalars.
+// A block turns one tile of one group through LDS, so that reads go along the
+// states and writes along the entries; the blocks after those take A and the
+// starts.
 template <class IO>
 __global__ __launch_bounds__(256) void scan_pack_kernel(ScanArgs a, ScanGrid g, ScanWs ws) {
   typedef typename IO::type T;
-  const int64_t N = a.N, nbc = a.B * a.G * g.ntile * N * kEntry, na = N * a.D, ns = ws.starts ? a.B * g.ntile : 0;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < nbc + na + ns; i += (int64_t)gridDim.x * 256) {
-    if (i < nbc) {
-      // consecutive threads take consecutive states of one token: reads in rows
-      const int64_t n = i % N, r = i / N;
-      const int tok = (int)(r % kScanT), isC = (int)(r / kScanT % 2);
-      const int64_t tile = r / kEntry % g.ntile, bg = r / kEntry / g.ntile;
-      const int64_t grp = bg % a.G, b = bg / a.G, t = tile * kScanT + tok;
+  extern __shared__ float turn[];  // [N][kEntry + 1]
+  const int N = (int)a.N;
+  const int64_t tiles = a.B * a.G * g.ntile;
+  if (blockIdx.x < tiles) {
+    const int64_t bg = blockIdx.x / g.ntile, tile = blockIdx.x - bg * g.ntile;
+    const int64_t b = bg / a.G, grp = bg - b * a.G;
+    for (int e = threadIdx.x; e < kEntry * N; e += 256) {
+      const int isC = e / (kScanT * N), r = e - isC * kScanT * N, tok = r / N, n = r - tok * N;
+      const int64_t t = tile * kScanT + tok, row = b * a.L + t;
       float v = 0.f;
       if (t < a.L)
-        v = isC ? IO::get(static_cast<const T*>(a.Cm)[(b * a.L + t) * a.rows.c + grp * N + n])
-                : IO::get(static_cast<const T*>(a.Bm)[(b * a.L + t) * a.rows.b + grp * N + n]) * kLn2;
-      ws.bc[((bg * g.ntile + tile) * N + n) * kEntry + tok / kHalf * kScanT + isC * kHalf + tok % kHalf] = v;
-    } else if (i < nbc + na) {
-      const int64_t k = i - nbc;
-      ws.at[k] = a.A[k % a.D * N + k / a.D];
-    } else {
-      const int64_t k = i - nbc - na, b = k / g.ntile, t0 = k % g.ntile * kScanT;
-      const int* sq = a.seq_idx + b * a.L;
-      uint32_t m = 0;
-      for (int e = 0; e < kScanT; ++e) {
-        const int64_t t = t0 + e;
-        if (t > 0 && t < a.L && sq[t] != sq[t - 1]) m |= 1u << e;
-      }
-      ws.starts[k] = m;
+        v = isC ? IO::get(static_cast<const T*>(a.Cm)[row * a.rows.c + grp * N + n])
+                : IO::get(static_cast<const T*>(a.Bm)[row * a.rows.b + grp * N + n]) * kLn2;
+      turn[n * (kEntry + 1) + tok / kHalf * kScanT + isC * kHalf + tok % kHalf] = v;
     }
+    __syncthreads();
+    float* o = ws.bc + (int64_t)blockIdx.x * N * kEntry;
+    for (int e = threadIdx.x; e < kEntry * N; e += 256) o[e] = turn[e / kEntry * (kEntry + 1) + e % kEntry];
+    return;
+  }
+  const int64_t k = (blockIdx.x - tiles) * 256 + threadIdx.x, na = N * a.D;
+  if (k < na) {
+    ws.at[k] = a.A[k % a.D * N + k / a.D];
+  } else if (ws.starts && k - na < a.B * g.ntile) {
+    const int64_t q = k - na, b = q / g.ntile, t0 = q % g.ntile * kScanT;
+    const int* sq = a.seq_idx + b * a.L;
+    uint32_t m = 0;
+    for (int e = 0; e < kScanT; ++e) {
+      const int64_t t = t0 + e;
+      if (t > 0 && t < a.L && sq[t] != sq[t - 1]) m |= 1u << e;
+    }
+    ws.starts[q] = m;
   }
 }
 
 hipError_t launch_scan_pack(const ScanArgs& a, const ScanGrid& g, const ScanWs& ws, bool bf16, hipStream_t s) {
-  const int64_t n = a.B * a.G * g.ntile * a.N * kEntry + a.N * a.D + a.B * g.ntile;
-  const int64_t blocks = (n + 1023) / 1024;
-  const dim3 grid((unsigned)(blocks < 8192 ? blocks : 8192));
-  if (bf16) hipLaunchKernelGGL((scan_pack_kernel<IoBF16>), grid, dim3(256), 0, s, a, g, ws);
-  else hipLaunchKernelGGL((scan_pack_kernel<IoF32>), grid, dim3(256), 0, s, a, g, ws);
+  const int64_t rest = a.N * a.D + (ws.starts ? a.B * g.ntile : 0);
+  const dim3 grid((unsigned)(a.B * a.G * g.ntile + (rest + 255) / 256));
+  const size_t lds = sizeof(float) * a.N * (kEntry + 1);
+  if (bf16) hipLaunchKernelGGL((scan_pack_kernel<IoBF16>), grid, dim3(256), lds, s, a, g, ws);
+  else hipLaunchKernelGGL((scan_pack_kernel<IoF32>), grid, dim3(256), lds, s, a, g, ws);
   return hipGetLastError();
 }
 
@@ -185,37 +194,89 @@ __global__ __launch_bounds__(64) void scan_chunk_kernel(ScanArgs a, ScanGrid g, 
   }
 }
 
-// Carry: from the states the chunks leave (slot c) to the states entering them
-// (in place; slot 0, whose state is the initial one, is not rewritten).
+// Carry, in place.  Forward (z < B): from the states the chunks leave to the
+// states entering them; chunk 0 leaves its full state (it started from the
+// initial one) and what enters it is not used.  Backward (z >= B): from what
+// each chunk sends back to the gradient reaching its last state, the last
+// chunk's being dfinal.  One fused multiply-add a chunk, bound by the latency
+// of the loads: a wave a block, so that few states still spread over all
+// compute units, and the next kCarryAhead chunks' loads in flight behind these.
+// Batches are whole and branch-free: behind a conditional store the compiler
+// waits for every access in flight (256 chunks: 42 us then).
+constexpr int kCarryAhead = 16;
 template <bool PACKED>
-__global__ __launch_bounds__(256) void scan_carry_kernel(ScanArgs a, ScanGrid g, ScanWs ws) {
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (idx >= a.B * a.N * a.D) return;
-  const int64_t d = idx % a.D, n = idx / a.D % a.N, b = idx / a.D / a.N;
-  const float an = a.A[d * a.N + n];
-  float* s = ws.carry + (b * g.nc * a.N + n) * a.D + d;
-  const float* sd = ws.sdt + b * g.nc * a.D + d;
-  const int64_t cs = a.N * a.D;
-  float run = s[0];
-  constexpr int U = 8;
-  for (int64_t c0 = 1; c0 < g.nc; c0 += U) {
-    float v[U], p[U];
+__global__ __launch_bounds__(64) void scan_carry_kernel(ScanArgs a, ScanGrid g, ScanWs ws) {
+  const bool rev = blockIdx.z >= a.B;
+  const int64_t b = rev ? blockIdx.z - a.B : blockIdx.z, n = blockIdx.y;
+  const int64_t d = (int64_t)blockIdx.x * 64 + threadIdx.x;
+  if (d >= a.D) return;
+  const int64_t nc = g.nc;
+  const float an = ws.at[n * a.D + d];
+  // in walking order, from the first chunk or back from the last
+  const int64_t c0 = rev ? nc - 1 : 0, cs = rev ? -a.N * a.D : a.N * a.D, ds = rev ? -a.D : a.D;
+  float* s = (rev ? ws.adj : ws.carry) + ((b * nc + c0) * a.N + n) * a.D + d;
+  const float* sd = ws.sdt + (b * nc + c0) * a.D + d;
+  const int* cut = ws.cut + b * nc + c0;
+  // what enters a chunk in which a sequence starts does not leave it
+  auto advance = [&](float run, float v, float p, int64_t q) {
+    const float r = fmaf(fast_exp2(p * an), run, v);
+    return PACKED && cut[rev ? -q : q] ? v : r;
+  };
+  float run = rev && a.dfinal ? a.dfinal[(b * a.N + n) * a.D + d] : 0.f;
+  // the last chunk's slot takes what reaches it and is not read
+  const int64_t steps = nc - 1;
+  int64_t q = 0;
+  if (!rev && steps > 0) {  // chunk 0 leaves its full state
+    run = s[0];
+    q = 1;
+  }
+  float v1[kCarryAhead], p1[kCarryAhead];
+  auto fetch = [&](int64_t q0) {
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int64_t c = c0 + i < g.nc - 1 ? c0 + i : g.nc - 2;  // the last chunk left no state
-      v[i] = c > 0 ? s[c * cs] : 0.f;
-      p[i] = fast_exp2(sd[c * a.D] * an);
+    for (int i = 0; i < kCarryAhead; ++i) {
+      v1[i] = s[(q0 + i) * cs];
+      p1[i] = sd[(q0 + i) * ds];
     }
+  };
+  if (q + kCarryAhead <= steps) fetch(q);
+  while (q + kCarryAhead <= steps) {
+    float v[kCarryAhead], p[kCarryAhead];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int64_t c = c0 + i;
-      if (c < g.nc) {
-        s[c * cs] = run;
-        if (PACKED && c < g.nc - 1 && ws.cut[b * g.nc + c]) run = v[i];
-        else run = fmaf(p[i], run, v[i]);
-      }
+    for (int i = 0; i < kCarryAhead; ++i) {
+      v[i] = v1[i];
+      p[i] = p1[i];
+    }
+    // before this batch's stores: waiting for loads waits for earlier stores
+    if (q + 2 * kCarryAhead <= steps) fetch(q + kCarryAhead);
+#pragma unroll
+    for (int i = 0; i < kCarryAhead; ++i) {
+      s[(q + i) * cs] = run;
+      run = advance(run, v[i], p[i], q + i);
+    }
+    q += kCarryAhead;
+  }
+  float v[kCarryAhead], p[kCarryAhead];
+#pragma unroll
+  for (int i = 0; i < kCarryAhead; ++i) {  // the rest, loaded together too
+    const int64_t k = q + i < steps ? q + i : q;
+    v[i] = k < steps ? s[k * cs] : 0.f;
+    p[i] = k < steps ? sd[k * ds] : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < kCarryAhead; ++i) {
+    if (q + i < steps) {
+      s[(q + i) * cs] = run;
+      run = advance(run, v[i], p[i], q + i);
     }
   }
+  s[steps * cs] = run;
+}
+
+hipError_t launch_scan_carry(const ScanArgs& a, const ScanGrid& g, const ScanWs& ws, hipStream_t s) {
+  const dim3 grid((unsigned)((a.D + 63) / 64), (unsigned)a.N, (unsigned)(ws.adj ? 2 * a.B : a.B));
+  auto kern = ws.starts ? scan_carry_kernel<true> : scan_carry_kernel<false>;
+  hipLaunchKernelGGL(kern, grid, dim3(64), 0, s, a, g, ws);
+  return hipGetLastError();
 }
 
 // States after given tokens: from the state entering the token's chunk.
@@ -374,9 +435,7 @@ static hipError_t scan_forward_t(const ScanArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)(a.G * g.ncb), (unsigned)(g.nc - 1), (unsigned)a.B);
     hipLaunchKernelGGL((scan_chunk_kernel<IO, PACKED, false>), grid, dim3(64), lds, s, a, g, ws);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL((scan_carry_kernel<PACKED>), dim3((unsigned)((a.B * a.N * a.D + 255) / 256)), dim3(256), 0, s, a,
-                       g, ws);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if ((e = launch_scan_carry(a, g, ws, s)) != hipSuccess) return e;
   }
   hipLaunchKernelGGL((scan_chunk_kernel<IO, PACKED, true>),
                      dim3((unsigned)(a.G * g.ncb), (unsigned)g.nc, (unsigned)a.B), dim3(64), lds, s, a,

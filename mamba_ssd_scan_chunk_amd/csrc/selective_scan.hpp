@@ -188,4 +188,7 @@ inline int64_t scan_bc_floats(int64_t B, int64_t G, int64_t ntile, int64_t N) { 
 // Fills ws.bc, ws.at and (packed sequences) ws.starts.
 hipError_t launch_scan_pack(const ScanArgs& a, const ScanGrid& g, const ScanWs& ws, bool bf16, hipStream_t s);
 
+// Carries ws.carry and, where there is one, ws.adj from chunk to chunk.
+hipError_t launch_scan_carry(const ScanArgs& a, const ScanGrid& g, const ScanWs& ws, hipStream_t s);
+
 }  // namespace ssd

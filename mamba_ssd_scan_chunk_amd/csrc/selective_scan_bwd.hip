@@ -146,62 +146,7 @@ __global__ __launch_bounds__(64) void scan_bwd_local_kernel(ScanArgs a, ScanGrid
   }
 }
 
-// Pass 2, in place: carry[c] = state entering chunk c (c >= 1; chunk 0 enters
-// with the initial state), adj[c] = gradient reaching chunk c's last state
-// from the tokens after it.
-template <bool PACKED>
-__global__ __launch_bounds__(256) void scan_bwd_carry_kernel(ScanArgs a, ScanGrid g, ScanWs ws) {
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (idx >= a.B * a.N * a.D) return;
-  const int64_t d = idx % a.D, n = idx / a.D % a.N, b = idx / a.D / a.N;
-  const float an = a.A[d * a.N + n];
-  const float* sd = ws.sdt + b * g.nc * a.D + d;
-  const int* cut = ws.cut + b * g.nc;
-  const int64_t cs = a.N * a.D, o = (b * g.nc * a.N + n) * a.D + d;
-  constexpr int U = 8;
-  if (blockIdx.y == 0) {
-    float* s = ws.carry + o;
-    float run = 0.f;
-    for (int64_t c0 = 0; c0 < g.nc; c0 += U) {
-      float v[U], p[U];
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int64_t c = c0 + i < g.nc ? c0 + i : g.nc - 1;
-        v[i] = s[c * cs];
-        p[i] = fast_exp2(sd[c * a.D] * an);
-      }
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int64_t c = c0 + i;
-        if (c < g.nc) {
-          s[c * cs] = run;
-          // chunk 0's left state already holds the initial state
-          run = (c == 0 || (PACKED && cut[c])) ? v[i] : fmaf(p[i], run, v[i]);
-        }
-      }
-    }
-  } else {
-    float* s = ws.adj + o;
-    float run = a.dfinal ? a.dfinal[(b * a.N + n) * a.D + d] : 0.f;
-    for (int64_t c0 = g.nc - 1; c0 >= 0; c0 -= U) {
-      float v[U], p[U];
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int64_t c = c0 - i > 0 ? c0 - i : 0;
-        v[i] = s[c * cs];
-        p[i] = fast_exp2(sd[c * a.D] * an);
-      }
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int64_t c = c0 - i;
-        if (c >= 0) {
-          s[c * cs] = run;
-          run = (PACKED && cut[c]) ? v[i] : fmaf(p[i], run, v[i]);
-        }
-      }
-    }
-  }
-}
+// Pass 2 is the carry of both, shared with the forward.
 
 template <int CTRL>
 __device__ __forceinline__ float dpp_mov(float v) {
@@ -540,9 +485,7 @@ static hipError_t scan_backward_t(const ScanArgs& a, hipStream_t s) {
   if ((e = launch_scan_pack(a, g, ws, IO::kVec == 8, s)) != hipSuccess) return e;
   hipLaunchKernelGGL((scan_bwd_local_kernel<IO, PACKED>), grid, block, lds1, s, a, g, ws);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL((scan_bwd_carry_kernel<PACKED>), dim3((unsigned)((a.B * a.N * a.D + 255) / 256), 2), dim3(256), 0,
-                     s, a, g, ws);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if ((e = launch_scan_carry(a, g, ws, s)) != hipSuccess) return e;
   hipLaunchKernelGGL((scan_bwd_chunk_kernel<IO, PACKED>), grid, block, lds3, s, a, g, ws, bw);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int64_t nbc = 2 * a.B * a.L * a.G * a.N;
