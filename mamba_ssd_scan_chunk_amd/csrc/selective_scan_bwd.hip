@@ -104,7 +104,13 @@ __global__ __launch_bounds__(64) void scan_bwd_local_kernel(ScanArgs a, ScanGrid
     // tokens of this step that still reach the chunk's entering state
     const int live = cut ? 0 : (starts ? __builtin_ctz(starts) : kScanT);
     const float sdt0 = sdt;
-    float* ts = ws.tstate + ((k.b * g.ntile + t0 / kScanT + 1) * N) * a.D + d;  // entering the next tile
+    // The state entering the next tile.  Stored always, from every lane (a lane
+    // past the group repeats its last channel, value and all): behind a
+    // condition the next state's load would wait for the store too.  What
+    // enters the next chunk is not read back; the row after the last tile need
+    // only be there.
+    const int64_t next = k.b * g.ntile + t0 / kScanT + 1;
+    float* ts = ws.tstate + next * N * a.D + d;
 #pragma unroll
     for (int i = 0; i < kScanT; ++i) {
       last = (PACKED && (starts >> i & 1)) ? dt[i] : last + dt[i];
@@ -117,23 +123,28 @@ __global__ __launch_bounds__(64) void scan_bwd_local_kernel(ScanArgs a, ScanGrid
       BCPair<true> nxt;
       nxt.load(ep);
       a_n = atp[(int64_t)(n + 1 < N ? n + 1 : 0) * a.D];
-      float h = hs[n * 64], acc = gs[n * 64], pr = fast_exp2(sdt0 * an);
+      float h = hs[n * 64];
+      float dec[kScanT];
 #pragma unroll
       for (int i = 0; i < kScanT; ++i) {
-        const float dec = fast_exp2(dt[i] * an);
+        dec[i] = fast_exp2(dt[i] * an);
         if (PACKED && (starts >> i & 1)) h = 0.f;
-        h = fmaf(dec, h, x[i] * e.b(i));
-        pr *= dec;
-        const float v = fmaf(pr, e.c(i) * dy[i], acc);
-        acc = (!PACKED || i < live) ? v : acc;
+        h = fmaf(dec[i], h, x[i] * e.b(i));
+      }
+      // what the tile's live tokens send back to the state entering it
+      float r = 0.f;
+#pragma unroll
+      for (int i = kScanT - 1; i >= 0; --i) {
+        const float v = fmaf(e.c(i), dy[i], r) * dec[i];
+        r = (!PACKED || i < live) ? v : 0.f;
       }
       e = nxt;
       hs[n * 64] = h;
-      gs[n * 64] = acc;
-      if (ok && t0 + kScanT < k.t1) ts[(int64_t)n * a.D] = h;
+      gs[n * 64] = fmaf(fast_exp2(sdt0 * an), r, gs[n * 64]);
+      ts[(int64_t)n * a.D] = h;
     }
     cut = cut || starts != 0;
-    if (ok && t0 + kScanT < k.t1) ws.tsdt[(k.b * g.ntile + t0 / kScanT + 1) * a.D + d] = last;
+    ws.tsdt[next * a.D + d] = last;
   }
   if (ok) {
     const int64_t o = (k.b * g.nc + k.c) * N * a.D + d;
@@ -450,8 +461,8 @@ static BwdLayout backward_layout(int64_t B, int64_t L, int64_t D, int64_t N, int
   w.pack = take(sizeof(float) * scan_bc_floats(B, G, g.ntile, N));
   w.at = take(sizeof(float) * N * D);
   w.starts = take(sizeof(uint32_t) * B * g.ntile);
-  w.tstate = take(sizeof(float) * B * g.ntile * N * D);
-  w.tsdt = take(sizeof(float) * B * g.ntile * D);
+  w.tstate = take(sizeof(float) * (B * g.ntile + 1) * N * D);
+  w.tsdt = take(sizeof(float) * (B * g.ntile + 1) * D);
   w.bc = take(sizeof(float) * 2 * g.ncb * B * L * G * N);
   w.dDb = take(sizeof(float) * B * g.nc * 2 * D);
   w.total = o;
