@@ -80,9 +80,10 @@ hipError_t launch_scan_pack(const ScanArgs& a, const ScanGrid& g, const ScanWs& 
 }
 
 // State passes: FINAL writes outputs from the chunk's entering state, else
-// only the state the chunk leaves and its summed dt.
+// only the state the chunk leaves and its summed dt.  Four waves a SIMD, which
+// the compiler would give up for a register (164 of them: 563 -> 593 us).
 template <class IO, bool PACKED, bool FINAL>
-__global__ __launch_bounds__(64) void scan_chunk_kernel(ScanArgs a, ScanGrid g, ScanWs ws) {
+__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(4, 4))) void scan_chunk_kernel(ScanArgs a, ScanGrid g, ScanWs ws) {
   typedef typename IO::type T;
   extern __shared__ float lds[];
   const int lane = threadIdx.x;
@@ -96,10 +97,15 @@ __global__ __launch_bounds__(64) void scan_chunk_kernel(ScanArgs a, ScanGrid g, 
   const float* h_in = nullptr;
   if (FINAL && g.nc > 1) h_in = ws.carry + (k.b * g.nc + k.c) * N * a.D;
   if (k.c == 0) h_in = a.h0 ? a.h0 + k.b * N * a.D : nullptr;
-  for (int n = 0; n < N; ++n) {
-    hs[n * 64] = h_in ? h_in[(int64_t)n * a.D + d] : 0.f;
-    as[n * 64] = ws.at[(int64_t)n * a.D + d];
+  const float* ep = ws.bc + (((k.b * a.G + k.grp) * g.ntile + k.t0 / kScanT) * N) * kEntry;
+  Touch ahead;
+  ahead.entries(ep, N, lane);
+  if (h_in) {
+    rows_to_lds(hs, h_in + d, a.D, N);
+  } else {
+    for (int n = 0; n < N; ++n) hs[n * 64] = 0.f;
   }
+  rows_to_lds(as, ws.at + d, a.D, N);
   const float bias = a.dt_bias ? a.dt_bias[d] * kLog2e : 0.f;
   const float skip = a.D_skip ? a.D_skip[d] : 0.f;
   const int64_t row0 = k.b * a.L;
@@ -108,7 +114,6 @@ __global__ __launch_bounds__(64) void scan_chunk_kernel(ScanArgs a, ScanGrid g, 
   const T* dp = static_cast<const T*>(a.dt) + row0 * a.rows.dt;
   const T* zp = a.z ? static_cast<const T*>(a.z) + row0 * a.rows.z : nullptr;
   T* yp = FINAL ? static_cast<T*>(a.y) + row0 * a.D : nullptr;
-  const float* ep = ws.bc + (((k.b * a.G + k.grp) * g.ntile + k.t0 / kScanT) * N) * kEntry;
   BCPair<FINAL> cur;
   cur.load(ep);
   float a_n = as[0], h_n = hs[0];
@@ -135,6 +140,8 @@ __global__ __launch_bounds__(64) void scan_chunk_kernel(ScanArgs a, ScanGrid g, 
         if (i >= nt) x[i] = 0.f;
     }
     // the gate of this tile and the next tile's inputs arrive behind the states
+    ahead.settle();
+    ahead.entries(t0 + kScanT < k.t1 ? ep + N * kEntry : ep, N, lane);
     if (FINAL && zp) rz.load(zp, a.rows.z, t0, nt, off);
     if (t0 + kScanT < k.t1) {
       ru.load(up, a.rows.u, t0 + kScanT, tile_tokens(k, t0 + kScanT), off);
@@ -199,83 +206,111 @@ __global__ __launch_bounds__(64) void scan_chunk_kernel(ScanArgs a, ScanGrid g, 
 // initial one) and what enters it is not used.  Backward (z >= B): from what
 // each chunk sends back to the gradient reaching its last state, the last
 // chunk's being dfinal.  One fused multiply-add a chunk, bound by the latency
-// of the loads: a wave a block, so that few states still spread over all
-// compute units, and the next kCarryAhead chunks' loads in flight behind these.
-// Batches are whole and branch-free: behind a conditional store the compiler
-// waits for every access in flight (256 chunks: 42 us then).
-constexpr int kCarryAhead = 16;
+// of the loads: the waves of a block take up to kCarryAhead chunks each, whose
+// loads are in flight together, compose them, and then, with what the waves
+// before let through, write their carries.  Longer stretches are walked twice,
+// or once by one wave where the columns alone fill the chip.
+// Lanes past D repeat its last column.  Pointers step from chunk to chunk: with
+// a product of 64 bits an address the code outgrew the time it took to fetch.
+constexpr int kCarryAhead = 16, kCarryWaves = 16;
 template <bool PACKED>
-__global__ __launch_bounds__(64) void scan_carry_kernel(ScanArgs a, ScanGrid g, ScanWs ws) {
+__global__ __launch_bounds__(64 * kCarryWaves) void scan_carry_kernel(ScanArgs a, ScanGrid g, ScanWs ws, int part) {
+  __shared__ float left[kCarryWaves][64], kept[kCarryWaves][64];
   const bool rev = blockIdx.z >= a.B;
   const int64_t b = rev ? blockIdx.z - a.B : blockIdx.z, n = blockIdx.y;
-  const int64_t d = (int64_t)blockIdx.x * 64 + threadIdx.x;
-  if (d >= a.D) return;
-  const int64_t nc = g.nc;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = (int)(blockDim.x >> 6);
+  int64_t d = (int64_t)blockIdx.x * 64 + lane;
+  if (d >= a.D) d = a.D - 1;
   const float an = ws.at[n * a.D + d];
-  // in walking order, from the first chunk or back from the last
-  const int64_t c0 = rev ? nc - 1 : 0, cs = rev ? -a.N * a.D : a.N * a.D, ds = rev ? -a.D : a.D;
-  float* s = (rev ? ws.adj : ws.carry) + ((b * nc + c0) * a.N + n) * a.D + d;
-  const float* sd = ws.sdt + (b * nc + c0) * a.D + d;
-  const int* cut = ws.cut + b * nc + c0;
-  // what enters a chunk in which a sequence starts does not leave it
-  auto advance = [&](float run, float v, float p, int64_t q) {
-    const float r = fmaf(fast_exp2(p * an), run, v);
-    return PACKED && cut[rev ? -q : q] ? v : r;
-  };
-  float run = rev && a.dfinal ? a.dfinal[(b * a.N + n) * a.D + d] : 0.f;
-  // the last chunk's slot takes what reaches it and is not read
-  const int64_t steps = nc - 1;
-  int64_t q = 0;
-  if (!rev && steps > 0) {  // chunk 0 leaves its full state
-    run = s[0];
-    q = 1;
-  }
-  float v1[kCarryAhead], p1[kCarryAhead];
-  auto fetch = [&](int64_t q0) {
-#pragma unroll
-    for (int i = 0; i < kCarryAhead; ++i) {
-      v1[i] = s[(q0 + i) * cs];
-      p1[i] = sd[(q0 + i) * ds];
-    }
-  };
-  if (q + kCarryAhead <= steps) fetch(q);
-  while (q + kCarryAhead <= steps) {
-    float v[kCarryAhead], p[kCarryAhead];
-#pragma unroll
-    for (int i = 0; i < kCarryAhead; ++i) {
-      v[i] = v1[i];
-      p[i] = p1[i];
-    }
-    // before this batch's stores: waiting for loads waits for earlier stores
-    if (q + 2 * kCarryAhead <= steps) fetch(q + kCarryAhead);
-#pragma unroll
-    for (int i = 0; i < kCarryAhead; ++i) {
-      s[(q + i) * cs] = run;
-      run = advance(run, v[i], p[i], q + i);
-    }
-    q += kCarryAhead;
-  }
+  // The chunks in walking order, from the first or back from the last; the last
+  // one's slot takes what reaches it and is not read.
+  const int steps = (int)g.nc - 1;
+  const int q0 = wave * part < steps ? wave * part : steps, q1 = q0 + part < steps ? q0 + part : steps;
+  const int64_t sign = rev ? -1 : 1, c0 = b * g.nc + (rev ? steps - q0 : q0);
+  const int64_t cs = sign * a.N * a.D, ds = sign * a.D;
+  float* const s0 = (rev ? ws.adj : ws.carry) + (c0 * a.N + n) * a.D + d;
+  const float* const sd0 = ws.sdt + c0 * a.D + d;
+  const int* const cut0 = ws.cut + c0;
   float v[kCarryAhead], p[kCarryAhead];
+  uint32_t cuts = 0;  // bit i: a sequence starts in chunk i, nothing that enters leaves it
+  auto load = [&](int q) {  // past q1: nothing added, nothing decays
+    const float *s = s0 + (q - q0) * cs, *sd = sd0 + (q - q0) * ds;
+    const int* cut = cut0 + (q - q0) * sign;
+    cuts = 0;
 #pragma unroll
-  for (int i = 0; i < kCarryAhead; ++i) {  // the rest, loaded together too
-    const int64_t k = q + i < steps ? q + i : q;
-    v[i] = k < steps ? s[k * cs] : 0.f;
-    p[i] = k < steps ? sd[k * ds] : 0.f;
-  }
+    for (int i = 0; i < kCarryAhead; ++i) {
+      v[i] = *s;
+      p[i] = *sd;
+      const bool more = q + i + 1 < q1;
+      if (PACKED) {
+        cuts |= (*cut != 0 ? 1u : 0u) << i;
+        cut += more ? sign : 0;
+      }
+      s += more ? cs : 0;
+      sd += more ? ds : 0;
+    }
 #pragma unroll
-  for (int i = 0; i < kCarryAhead; ++i) {
-    if (q + i < steps) {
-      s[(q + i) * cs] = run;
-      run = advance(run, v[i], p[i], q + i);
+    for (int i = 0; i < kCarryAhead; ++i) {
+      if (q + i >= q1) v[i] = p[i] = 0.f;
+    }
+    if (!rev && q == 0) p[0] = 0.f;  // chunk 0 leaves its full state
+    if (PACKED && q1 - q < kCarryAhead) cuts &= (1u << (q1 - q)) - 1;
+  };
+  auto after = [&](float run, int i) {
+    const float r = fmaf(fast_exp2(p[i] * an), run, v[i]);
+    return PACKED && (cuts >> i & 1) ? v[i] : r;
+  };
+  const float first = rev && wave == 0 && a.dfinal ? a.dfinal[(b * a.N + n) * a.D + d] : 0.f;
+  const bool held = part <= kCarryAhead;  // this wave's chunks stay in registers
+  float run = first;
+  if (held) load(q0);
+  if (waves > 1) {
+    float sum = 0.f;  // time steps of the stretch
+    uint32_t any = 0;
+    for (int q = q0; q < q1; q += kCarryAhead) {
+      if (!held) load(q);
+#pragma unroll
+      for (int i = 0; i < kCarryAhead; ++i) {
+        // (a stretch starts from nothing: not even an overflowing decay of it)
+        run = i == 0 && q == q0 && wave > 0 ? v[0] : after(run, i);
+        sum += p[i];
+      }
+      any |= cuts;
+    }
+    left[wave][lane] = run;
+    kept[wave][lane] = any ? -1.f : fast_exp2(sum * an);  // -1: nothing gets through
+    __syncthreads();
+    run = wave == 0 ? first : left[0][lane];
+    for (int w = 1; w < wave; ++w) {
+      const float k = kept[w][lane], l = left[w][lane];
+      run = k < 0.f || run == 0.f ? l : fmaf(k, run, l);
     }
   }
-  s[steps * cs] = run;
+  float* s = s0;
+  for (int q = q0; q < q1; q += kCarryAhead) {
+    if (!held) load(q);
+#pragma unroll
+    for (int i = 0; i < kCarryAhead; ++i) {
+      if (q + i < q1) {
+        *s = run;
+        s += cs;
+        run = after(run, i);
+      }
+    }
+  }
+  if (wave == waves - 1) *s = run;
 }
 
 hipError_t launch_scan_carry(const ScanArgs& a, const ScanGrid& g, const ScanWs& ws, hipStream_t s) {
   const dim3 grid((unsigned)((a.D + 63) / 64), (unsigned)a.N, (unsigned)(ws.adj ? 2 * a.B : a.B));
+  const int64_t blocks = (int64_t)grid.x * grid.y * grid.z;
+  const int steps = (int)g.nc - 1;
+  int waves = (steps + kCarryAhead - 1) / kCarryAhead;
+  if (waves > kCarryWaves) waves = blocks < (int64_t)device_cu_count() * 8 ? kCarryWaves : 1;
+  if (waves < 1) waves = 1;
   auto kern = ws.starts ? scan_carry_kernel<true> : scan_carry_kernel<false>;
-  hipLaunchKernelGGL(kern, grid, dim3(64), 0, s, a, g, ws);
+  hipLaunchKernelGGL(kern, grid, dim3((unsigned)(64 * waves)), 0, s, a, g, ws, (steps + waves - 1) / waves);
   return hipGetLastError();
 }
 
@@ -373,14 +408,17 @@ __global__ __launch_bounds__(64) void scan_step_kernel(ScanArgs a, const float* 
 
 bool scan_dstate_supported(int64_t N) { return N > 0 && N % 4 == 0 && N <= 256; }
 
-// Chunk length: enough waves for four a SIMD, in whole 16-token steps; the
-// carried states then cost little beside the inputs.
+// Chunk length: enough waves for four a SIMD, in whole 16-token tiles; the
+// carried states then cost little beside the inputs.  Short problems go down to
+// a tile a chunk (1 x 512 tokens of 1536 channels: chunks of 64 tokens 57 us,
+// 32 39, 16 30), but rows of up to three tiles stay whole: two passes and a
+// carry take as long as three tiles in one.
 static ScanGrid forward_grid(int64_t B, int64_t L, int64_t D, int64_t G) {
   ScanGrid g;
   g.ncb = (D / G + 63) / 64;
   const int64_t waves = B * G * g.ncb, want = (int64_t)device_cu_count() * 16;
   int64_t nc = want / waves;  // rounded down: one wave too many would run in a round of its own
-  const int64_t most = (L + 63) / 64;
+  const int64_t most = L <= 3 * kScanT ? 1 : (L + kScanT - 1) / kScanT;
   if (nc > most) nc = most;
   if (nc < 1) nc = 1;
   g.Q = ((L + nc - 1) / nc + kScanT - 1) / kScanT * kScanT;

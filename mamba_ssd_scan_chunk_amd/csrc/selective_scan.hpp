@@ -87,6 +87,36 @@ struct BCPair {
   __device__ __forceinline__ float c(int i) const { return i < kHalf ? lo.c(i) : hi.c(i - kHalf); }
 };
 
+// Lines that coming loads will need, asked for early, one a lane, and held until
+// `settle`.  A tile's entries miss its die's L2 when first read, and the states
+// would wait for theirs one after another: 2 x 8192 tokens of 5120 channels
+// 565 us without, 491 with; 1 x 4 tokens of 1058 channels, 32 states, 31 and 20.
+struct Touch {
+  float v;
+  // the entries (128 bytes) of N states, the first 64 of them
+  __device__ __forceinline__ void entries(const float* p, int N, int lane) {
+    v = p[(lane < N ? lane : N - 1) * kEntry];
+  }
+  // both ends of the 64 channels (the first, and `last` after it) in N rows of
+  // D, the first 32 rows
+  __device__ __forceinline__ void rows(const float* p, int64_t D, int last, int N, int lane) {
+    v = p[(lane < 2 * N ? lane >> 1 : N - 1) * D + (lane & 1) * last];
+  }
+  __device__ __forceinline__ void settle() { asm volatile("" : : "v"(v)); }
+};
+
+// Rows 0..N-1 of [N, D], a channel a lane, to or from LDS, 16 rows' loads at a
+// time (N is a multiple of 4; past it the last row again).
+__device__ __forceinline__ void rows_to_lds(float* dst, const float* src, int64_t D, int N) {
+  for (int n0 = 0; n0 < N; n0 += 16) {
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = src[(n0 + i < N ? n0 + i : N - 1) * D];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) dst[(n0 + i < N ? n0 + i : N - 1) * 64] = v[i];
+  }
+}
+
 // Tokens of the tile at t0 (uniform, kept in 32 bits).
 __device__ __forceinline__ int tile_tokens(const ScanBlock& k, int64_t t0) {
   return __builtin_amdgcn_readfirstlane((int)(k.t1 - t0 < kScanT ? k.t1 - t0 : kScanT));

@@ -67,15 +67,15 @@ __global__ __launch_bounds__(64) void scan_bwd_local_kernel(ScanArgs a, ScanGrid
   const int64_t d = k.d0 + lane < k.dend ? k.d0 + lane : k.dend - 1;
   const bool ok = k.d0 + lane < k.dend;
   const float* h_in = k.c == 0 && a.h0 ? a.h0 + k.b * N * a.D : nullptr;
-  for (int n = 0; n < N; ++n) {
-    hs[n * 64] = h_in ? h_in[(int64_t)n * a.D + d] : 0.f;
-    gs[n * 64] = 0.f;
-  }
+  const float* ep = ws.bc + (((k.b * a.G + k.grp) * g.ntile + k.t0 / kScanT) * N) * kEntry;
+  Touch ahead;
+  ahead.entries(ep, N, lane);
+  for (int n = 0; n < N; ++n) hs[n * 64] = gs[n * 64] = 0.f;
+  if (h_in) rows_to_lds(hs, h_in + d, a.D, N);
   const float bias = a.dt_bias ? a.dt_bias[d] * kLog2e : 0.f;
   const RowPtrs<IO> p(a, k.b);
   const int off = (int)(d * sizeof(typename IO::type));
   const float* atp = ws.at + d;
-  const float* ep = ws.bc + (((k.b * a.G + k.grp) * g.ntile + k.t0 / kScanT) * N) * kEntry;
   BCPair<true> e;
   e.load(ep);
   float a_n = atp[0];
@@ -116,6 +116,8 @@ __global__ __launch_bounds__(64) void scan_bwd_local_kernel(ScanArgs a, ScanGrid
       last = (PACKED && (starts >> i & 1)) ? dt[i] : last + dt[i];
       sdt += dt[i];
     }
+    ahead.settle();
+    ahead.entries(t0 + kScanT < k.t1 ? ep + N * kEntry : ep, N, lane);
     for (int n = 0; n < N; ++n) {
       const float an = a_n;
       e.settle();
@@ -205,17 +207,17 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(2, 2))) void
   const float* h_in = k.c == 0 ? (a.h0 ? a.h0 + k.b * N * a.D + d : nullptr) : ws.carry + co;
   const bool entered = h_in != nullptr;
   if (!entered) h_in = ws.carry + co;
-  for (int n = 0; n < N; ++n) {
-    gs[n * 64] = ws.adj[co + (int64_t)n * a.D];
-    as[n * 64] = 0.f;
-  }
+  const int nstep = (int)((k.t1 - k.t0 + kScanT - 1) / kScanT);
+  const float* e0 = ws.bc + (((k.b * a.G + k.grp) * g.ntile + k.t0 / kScanT) * N) * kEntry;
+  Touch ahead;
+  ahead.entries(e0 + (int64_t)(nstep - 1) * N * kEntry, N, lane);
+  rows_to_lds(gs, ws.adj + co, a.D, N);
+  for (int n = 0; n < N; ++n) as[n * 64] = 0.f;
   const float bias = a.dt_bias ? a.dt_bias[d] * kLog2e : 0.f;
   const float skip = a.D_skip ? a.D_skip[d] : 0.f;
   const RowPtrs<IO> p(a, k.b);
   const int off = (int)(d * sizeof(typename IO::type));
-  const int nstep = (int)((k.t1 - k.t0 + kScanT - 1) / kScanT);
   const float* atp = ws.at + d;
-  const float* e0 = ws.bc + (((k.b * a.G + k.grp) * g.ntile + k.t0 / kScanT) * N) * kEntry;
   const bool whole = k.d0 + 64 <= k.dend;
   float dDsum = 0.f, dbsum = 0.f;
   const int64_t BL = a.B * a.L;
@@ -266,6 +268,8 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(2, 2))) void
     BCPair<true> e;
     const float* ep = e0 + (int64_t)j * N * kEntry;
     e.load(ep);
+    ahead.settle();
+    ahead.entries(j ? ep - N * kEntry : ep, N, lane);
     float a_n = atp[0], in_n = h_in[0], ts_n = j ? ts[0] : 0.f;
     float rB = 0.f, rC = 0.f;  // of token lane >> 2, state lane & 3 of four
     for (int n = 0; n < N; ++n) {
@@ -494,8 +498,10 @@ static hipError_t scan_backward_t(const ScanArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if ((e = launch_scan_pack(a, g, ws, IO::kVec == 8, s)) != hipSuccess) return e;
-  hipLaunchKernelGGL((scan_bwd_local_kernel<IO, PACKED>), grid, block, lds1, s, a, g, ws);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (g.ntile > 1) {  // a single tile has nothing to pass on
+    hipLaunchKernelGGL((scan_bwd_local_kernel<IO, PACKED>), grid, block, lds1, s, a, g, ws);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   if ((e = launch_scan_carry(a, g, ws, s)) != hipSuccess) return e;
   hipLaunchKernelGGL((scan_bwd_chunk_kernel<IO, PACKED>), grid, block, lds3, s, a, g, ws, bw);
   if ((e = hipGetLastError()) != hipSuccess) return e;

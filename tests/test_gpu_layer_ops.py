@@ -260,6 +260,34 @@ def test_scan_backward(case, dtype):
         assert torch.equal(t, again[n]), n
 
 
+# Long rows: carries over 18 to 300 chunks by one wave or several, sequences
+# that start in, before and after a wave's chunks, and many states of few channels.
+CARRY = [
+    (1, 288, 20, 4, 1, 0, [30, 226], True, True, True),
+    (2, 500, 64, 4, 1, 0, None, True, True, True),
+    (1, 4000, 20, 4, 1, 0, [255, 1, 1000, 16, 1500], True, True, True),
+    (1, 4800, 20, 4, 1, 0, None, False, True, True),
+    (1, 4700, 70, 4, 1, 0, [4300, 100, 3], True, True, True),
+    (8, 4250, 2, 256, 1, 0, [4000, 9], False, True, True),
+]
+
+
+@pytest.mark.parametrize("case", CARRY, ids=str)
+def test_scan_of_many_chunks(case):
+    say(f"scan of many chunks {case}")
+    B, L = case[:2]
+    c = scan_case(case, "f32", 2)
+    y, ym, h, hm = ref.scan(*c["ref"], *c["opt"])
+    gy, gh = ops.ssd_selective_scan(**c["t"])[:2]
+    close("y", gy, (y, ym), k_scan(L), "f32")
+    close("final", gh, (h, hm), k_scan(L), "f32")
+    want = ref.scan_backward(*c["ref"], c["dy"], *c["opt"], c["df"])
+    got = ops.ssd_selective_scan_backward(**c["t"], dy=dev(c["dy"], "f32"), dfinal=dev(c["df"]), want_dinitial=True)
+    for n, t in got.items():
+        if t is not None:
+            close(n, t, want[n], 2 * k_scan(L) + 64, "f32")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("B,D,N,G,gate", [(1, 64, 16, 1, True), (3, 33, 4, 1, False), (2, 130, 16, 2, True),
                                           (5, 20, 64, 1, True), (2, 8, 256, 1, True), (7, 1028, 8, 2, True)])
