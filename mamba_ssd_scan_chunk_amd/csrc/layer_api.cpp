@@ -38,10 +38,14 @@ ssd_status product(std::initializer_list<int64_t> f, int64_t most) {
 }
 
 // A row stride: 0 stands for `dense`; shorter rows than the channels overlap.
-ssd_status row_stride(int64_t given, int64_t dense, int64_t tokens, int64_t* out) {
+// Up to 16 rows of a sequence are addressed by 32-bit byte offsets from the first.
+bool row_too_long(int64_t seqlen, int64_t row) { return seqlen > 1 && row >= int64_t(1) << 25; }
+
+ssd_status row_stride(int64_t given, int64_t dense, int64_t batch, int64_t seqlen, int64_t* out) {
   if (given == 0) given = dense;
   if (given < dense) return SSD_ERR_SHAPE;
-  SSD_TRY(product({tokens, given}, kMaxElems));
+  SSD_TRY(product({batch, seqlen, given}, kMaxElems));
+  if (row_too_long(seqlen, given)) return SSD_ERR_UNSUPPORTED;
   *out = given;
   return SSD_OK;
 }
@@ -53,6 +57,7 @@ ssd_status check_conv(const ssd_conv_shape* s, bool step) {
   if (step && s->seqlen != 1) return SSD_ERR_SHAPE;
   if (s->width < 2 || s->width > 4) return SSD_ERR_UNSUPPORTED;
   SSD_TRY(product({s->batch, s->seqlen, s->channels}, kMaxElems));
+  if (row_too_long(s->seqlen, s->channels)) return SSD_ERR_UNSUPPORTED;
   // waves (64 channels and at least 8 tokens each) in 31 bits
   return product({s->batch, (s->seqlen - 1) / 8 + 1, (s->channels - 1) / 64 + 1}, k31 - 1);
 }
@@ -85,6 +90,7 @@ ssd_status check_scan(const ssd_scan_shape* s, bool step) {
   if (s->batch > 32767 || (s->seqlen - 1) / 16 + 1 > 65535 || s->channels >= k31) return SSD_ERR_UNSUPPORTED;
   SSD_TRY(product({s->batch, s->seqlen, s->channels}, kMaxElems));
   SSD_TRY(product({s->batch, s->seqlen, s->ngroups, s->dstate}, (int64_t(1) << 36)));
+  if (row_too_long(s->seqlen, s->channels) || row_too_long(s->seqlen, s->ngroups * s->dstate)) return SSD_ERR_UNSUPPORTED;
   // a block a tile of a group in 31 bits, beside the few for A and the starts
   SSD_TRY(product({s->batch, (s->seqlen - 1) / 16 + 1, s->ngroups}, int64_t(1) << 30));
   return product({s->batch, s->dstate, s->channels}, (int64_t(1) << 38));
@@ -93,15 +99,12 @@ ssd_status check_scan(const ssd_scan_shape* s, bool step) {
 ssd_status scan_rows(const ssd_scan_shape* s, const ssd_scan_rows* r, ssd_dtype in, ssd::ScanRows* o) {
   const ssd_scan_rows none = {0, 0, 0, 0, 0};
   if (!r) r = &none;
-  const int64_t tok = s->batch * s->seqlen, D = s->channels, gn = s->ngroups * s->dstate;
-  SSD_TRY(row_stride(r->u, D, tok, &o->u));
-  SSD_TRY(row_stride(r->dt, D, tok, &o->dt));
-  SSD_TRY(row_stride(r->Bm, gn, tok, &o->b));
-  SSD_TRY(row_stride(r->Cm, gn, tok, &o->c));
-  SSD_TRY(row_stride(r->z, D, tok, &o->z));
-  // a tile's 16 rows are addressed by 32-bit byte offsets from its first
-  for (int64_t v : {o->u, o->dt, o->b, o->c, o->z})
-    if (v >= int64_t(1) << 25) return SSD_ERR_UNSUPPORTED;
+  const int64_t D = s->channels, gn = s->ngroups * s->dstate;
+  SSD_TRY(row_stride(r->u, D, s->batch, s->seqlen, &o->u));
+  SSD_TRY(row_stride(r->dt, D, s->batch, s->seqlen, &o->dt));
+  SSD_TRY(row_stride(r->Bm, gn, s->batch, s->seqlen, &o->b));
+  SSD_TRY(row_stride(r->Cm, gn, s->batch, s->seqlen, &o->c));
+  SSD_TRY(row_stride(r->z, D, s->batch, s->seqlen, &o->z));
   // B and C are read in 4-byte units
   if (in == SSD_BF16 && (o->b % 2 != 0 || o->c % 2 != 0)) return SSD_ERR_ALIGN;
   return SSD_OK;
@@ -153,7 +156,7 @@ ssd_status ssd_causal_conv(const ssd_conv_shape* shape, const void* x, int64_t x
   SSD_TRY(check_dtype(in));
   if (!x || !w || !y) return SSD_ERR_NULL;
   ssd::ConvArgs a = conv_args(shape);
-  SSD_TRY(row_stride(x_row, a.D, a.B * a.L, &a.x_row));
+  SSD_TRY(row_stride(x_row, a.D, a.B, a.L, &a.x_row));
   SSD_TRY(check_seq_list(nseq, seq_last, seq_states));
   if (!aligned(x, elem(in)) || !a16(w) || !a16(bias) || !a16(initial_state) || !a16(seq_idx) || !a16(y) ||
       !a16(final_state))
@@ -179,7 +182,7 @@ ssd_status ssd_causal_conv_step(const ssd_conv_shape* shape, const void* x, int6
   SSD_TRY(check_dtype(in));
   if (!x || !state || !w || !state_out || !y) return SSD_ERR_NULL;
   ssd::ConvArgs a = conv_args(shape);
-  SSD_TRY(row_stride(x_row, a.D, a.B, &a.x_row));
+  SSD_TRY(row_stride(x_row, a.D, a.B, 1, &a.x_row));
   if (!aligned(x, elem(in)) || !a16(state) || !a16(w) || !a16(bias) || !a16(state_out) || !a16(y)) return SSD_ERR_ALIGN;
   a.silu = silu != 0;
   a.x = x;
@@ -203,8 +206,8 @@ ssd_status ssd_causal_conv_backward(const ssd_conv_shape* shape, const void* x, 
   SSD_TRY(check_dtype(in));
   if (!x || !w || !dy || !dx || !dw) return SSD_ERR_NULL;
   ssd::ConvArgs a = conv_args(shape);
-  SSD_TRY(row_stride(x_row, a.D, a.B * a.L, &a.x_row));
-  SSD_TRY(row_stride(dx_row, a.D, a.B * a.L, &a.dx_row));
+  SSD_TRY(row_stride(x_row, a.D, a.B, a.L, &a.x_row));
+  SSD_TRY(row_stride(dx_row, a.D, a.B, a.L, &a.dx_row));
   if (!workspace || workspace_bytes < ssd_causal_conv_backward_workspace_bytes(shape)) return SSD_ERR_WORKSPACE;
   if (!aligned(x, elem(in)) || !aligned(dx, elem(in)) || !a16(w) || !a16(bias) || !a16(initial_state) ||
       !a16(seq_idx) || !a16(dy) || !a16(dfinal) || !a16(dw) || !a16(dbias) || !a16(dinitial) || !a16(workspace))
