@@ -10,13 +10,17 @@
 //     dw = sum over rows of dy xh,  dbias = sum over rows of dy
 //
 // Bound by memory.  A row stays in registers between its one read and its one
-// write.  Forward: a wave a row up to 4096 columns, 256 threads beyond, 16
-// bytes a load (single elements where rows are not whole units of 8).
+// write.  Forward: a wave a row up to 4096 columns, 256 threads beyond, 8 or 4
+// elements a load.  Rows that are not whole groups of 4 begin anywhere in one:
+// in bf16 their threads take the groups as memory has them, the first beginning
+// up to 3 columns before the row and the last ending after it (4866 rows of
+// 1669 columns: 51 us an element a load, 26 so; gradients 57 and 41).
 // Backward: 64, 256 or 1024 threads a row, 16 values a thread at most, so that
 // the five values a column (x, dy, w, dw, dbias) leave room for waves beside;
 // blocks walk rows, the next row's loads in flight behind the sums of this
-// one, and keep dw and dbias of their columns in registers.  The blocks'
-// partial sums are added in a fixed order.
+// one, and keep dw and dbias of their columns in registers (walking in steps
+// of 4 rows, they find the same columns in each).  The blocks' partial sums are
+// added in a fixed order.
 #include "layer_device.hpp"
 #include "layer_launch.hpp"
 
@@ -39,37 +43,86 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   return v;
 }
 
-// Loads V elements at column c (below D) as fp32, zeros past the row.
-template <class IO, int V>
-__device__ __forceinline__ void load_cols(const void* base, int64_t row0, int64_t c, int64_t D, float* o) {
-  if (c < D) {
-    load_vec<IO, V>(static_cast<const typename IO::type*>(base) + row0 + c, o);
+// Columns of the row before its first group of V in memory: rows of whole
+// groups (SHIFT false) begin with one.
+template <int V, bool SHIFT>
+__device__ __forceinline__ int row_shift(int64_t r0) {
+  return SHIFT ? (int)(r0 & (V - 1)) : 0;
+}
+// Whether column c + e of a group at c is in the row.
+template <bool SHIFT>
+__device__ __forceinline__ bool in_row(int c, int e, int D) {
+  return SHIFT ? (unsigned)(c + e) < (unsigned)D : c < D;
+}
+// Loads V elements at column c as fp32, zeros outside the row.  Groups over a
+// row's ends hold elements of its neighbours, all within the `total` elements
+// but for the last row's.  (Loads of groups past the row made unconditional, to
+// leave the compiler no branches, cost more in traffic than they saved.)
+template <class IO, int V, bool SHIFT>
+__device__ __forceinline__ void load_cols(const void* base, int64_t row0, int c, int D, int64_t total, float* o) {
+  const typename IO::type* p = static_cast<const typename IO::type*>(base) + row0 + c;
+  if (c < D && (!SHIFT || row0 + c + V <= total)) {
+    load_vec<IO, V>(p, o);
+    if constexpr (SHIFT) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = in_row<SHIFT>(c, e, D) ? o[e] : 0.f;
+    }
   } else {
 #pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = 0.f;
+    for (int e = 0; e < V; ++e) o[e] = SHIFT && in_row<SHIFT>(c, e, D) ? IO::get(p[e]) : 0.f;
+  }
+}
+template <class IO, int V, bool SHIFT>
+__device__ __forceinline__ void store_cols(void* base, int64_t row0, int c, int D, const float* v) {
+  typename IO::type* p = static_cast<typename IO::type*>(base) + row0 + c;
+  if (SHIFT ? c >= 0 && c + V <= D : c < D) {
+    store_vec<IO, V>(p, v);
+  } else if (SHIFT) {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (in_row<SHIFT>(c, e, D)) p[e] = IO::put(v[e]);
+  }
+}
+// The same of an fp32 vector of D, whose groups are aligned only without a shift.
+typedef float f32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));
+template <int V, bool SHIFT>
+__device__ __forceinline__ void load_param(const float* p, int c, int D, float* o) {
+  if constexpr (SHIFT) {
+    if (c >= 0 && c + V <= D) {
+      const f32x4_any_t q = *reinterpret_cast<const f32x4_any_t*>(p + c);
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = q[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = in_row<SHIFT>(c, e, D) ? p[c + e] : 0.f;
+    }
+  } else {
+    load_cols<IoF32, V, false>(p, 0, c, D, D, o);
   }
 }
 
-template <class IO, class RO, int V, int NV, int TPR>
+template <class IO, class RO, int V, bool SHIFT, int NV, int TPR>
 __global__ __launch_bounds__(256) void norm_forward_kernel(NormArgs a) {
   __shared__ float red[TPR == 64 ? 1 : TPR / 64];
   const int64_t row = TPR == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
   if (TPR == 64 && row >= a.rows) return;
   const int tid = TPR == 64 ? threadIdx.x & 63 : threadIdx.x;
   const int64_t r0 = row * a.D;
+  const int D = (int)a.D, m = row_shift<V, SHIFT>(r0);
+  const int64_t total = a.rows * a.D;
+  auto col = [&](int j) { return (j * TPR + tid) * V - m; };
   float x[NV][V];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) load_cols<IO, V>(a.x, r0, ((int64_t)j * TPR + tid) * V, a.D, x[j]);
+  for (int j = 0; j < NV; ++j) load_cols<IO, V, SHIFT>(a.x, r0, col(j), D, total, x[j]);
   if (a.residual) {
     float q[NV][V];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) load_cols<RO, V>(a.residual, r0, ((int64_t)j * TPR + tid) * V, a.D, q[j]);
+    for (int j = 0; j < NV; ++j) load_cols<RO, V, SHIFT>(a.residual, r0, col(j), D, total, q[j]);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t c = ((int64_t)j * TPR + tid) * V;
 #pragma unroll
       for (int e = 0; e < V; ++e) x[j][e] = RO::get(RO::put(x[j][e] + q[j][e]));
-      if (c < a.D) store_vec<RO, V>(static_cast<typename RO::type*>(a.residual_out) + r0 + c, x[j]);
+      store_cols<RO, V, SHIFT>(a.residual_out, r0, col(j), D, x[j]);
     }
   }
   const float inv = 1.f / (float)a.D;
@@ -85,11 +138,10 @@ __global__ __launch_bounds__(256) void norm_forward_kernel(NormArgs a) {
   float s2 = 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const bool in = ((int64_t)j * TPR + tid) * V < a.D;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       x[j][e] -= mean;
-      s2 = in ? fmaf(x[j][e], x[j][e], s2) : s2;
+      s2 = in_row<SHIFT>(col(j), e, D) ? fmaf(x[j][e], x[j][e], s2) : s2;
     }
   }
   const float rstd = 1.f / sqrtf(fmaf(row_sum<TPR>(s2, red), inv, a.eps));
@@ -99,16 +151,15 @@ __global__ __launch_bounds__(256) void norm_forward_kernel(NormArgs a) {
   }
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int64_t c = ((int64_t)j * TPR + tid) * V;
-    if (c < a.D) {
+    if (col(j) < D) {
       float w[V], b[V], o[V];
-      load_vec<IoF32, V>(a.w + c, w);
+      load_param<V, SHIFT>(a.w, col(j), D, w);
 #pragma unroll
       for (int e = 0; e < V; ++e) b[e] = 0.f;
-      if (a.bias) load_vec<IoF32, V>(a.bias + c, b);
+      if (a.bias) load_param<V, SHIFT>(a.bias, col(j), D, b);
 #pragma unroll
       for (int e = 0; e < V; ++e) o[e] = fmaf(x[j][e] * rstd, w[e], b[e]);
-      store_vec<IO, V>(static_cast<typename IO::type*>(a.y) + r0 + c, o);
+      store_cols<IO, V, SHIFT>(a.y, r0, col(j), D, o);
     }
   }
 }
@@ -139,7 +190,7 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float2* red) {
 constexpr int norm_bwd_threads(int tpr) { return tpr == 64 ? 256 : tpr; }
 
 // IO: type of dy and dx; RO: type of x, dres and dres_out.
-template <class IO, class RO, int V, int NV, int TPR>
+template <class IO, class RO, int V, bool SHIFT, int NV, int TPR>
 __global__ __launch_bounds__(norm_bwd_threads(TPR)) void norm_backward_kernel(NormArgs a) {
   __shared__ float2 red[2][TPR == 64 ? 1 : TPR / 64];
   __shared__ float part[TPR == 64 ? 3 * 2 * 64 * NV * V : 1];
@@ -148,19 +199,21 @@ __global__ __launch_bounds__(norm_bwd_threads(TPR)) void norm_backward_kernel(No
   const int64_t first = TPR == 64 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
   const int64_t step = TPR == 64 ? (int64_t)gridDim.x * 4 : gridDim.x;
   const float inv = 1.f / (float)a.D;
-  auto col = [&](int j) { return ((int64_t)j * TPR + tid) * V; };
+  const int D = (int)a.D, m = row_shift<V, SHIFT>(first * a.D);  // of each of the walker's rows
+  const int64_t total = a.rows * a.D;
+  auto col = [&](int j) { return (j * TPR + tid) * V - m; };
   float w[NV][V], dw[NV][V], db[NV][V], x[NV][V], g[NV][V];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    load_cols<IoF32, V>(a.w, 0, col(j), a.D, w[j]);
+    load_param<V, SHIFT>(a.w, col(j), D, w[j]);
 #pragma unroll
     for (int e = 0; e < V; ++e) dw[j][e] = db[j][e] = 0.f;
   }
   auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      load_cols<RO, V>(a.x, row * a.D, col(j), a.D, x[j]);
-      load_cols<IO, V>(a.dy, row * a.D, col(j), a.D, g[j]);
+      load_cols<RO, V, SHIFT>(a.x, row * a.D, col(j), D, total, x[j]);
+      load_cols<IO, V, SHIFT>(a.dy, row * a.D, col(j), D, total, g[j]);
     }
   };
   // the next row's loads in flight behind this one's sums, but for the blocks
@@ -177,7 +230,7 @@ __global__ __launch_bounds__(norm_bwd_threads(TPR)) void norm_backward_kernel(No
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (a.dres) {
-        load_cols<RO, V>(a.dres, r0, col(j), a.D, q[j]);
+        load_cols<RO, V, SHIFT>(a.dres, r0, col(j), D, total, q[j]);
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) q[j][e] = 0.f;
@@ -197,12 +250,12 @@ __global__ __launch_bounds__(norm_bwd_threads(TPR)) void norm_backward_kernel(No
     const float m1 = a.rms ? 0.f : s.x * inv, m2 = s.y * inv;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (col(j) < a.D) {
+      if (col(j) < D) {
         float o[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) o[e] = fmaf(rstd, v[j][e] - fmaf(xh[j][e], m2, m1), q[j][e]);
-        store_vec<IO, V>(static_cast<typename IO::type*>(a.dx) + r0 + col(j), o);
-        if (a.dres_out) store_vec<RO, V>(static_cast<typename RO::type*>(a.dres_out) + r0 + col(j), o);
+        store_cols<IO, V, SHIFT>(a.dx, r0, col(j), D, o);
+        if (a.dres_out) store_cols<RO, V, SHIFT>(a.dres_out, r0, col(j), D, o);
       }
     }
   }
@@ -210,13 +263,19 @@ __global__ __launch_bounds__(norm_bwd_threads(TPR)) void norm_backward_kernel(No
   // they meet first
   if constexpr (TPR == 64) {
     constexpr int P = 64 * NV * V;
+    // a lane's values side by side with the other lanes'; by column where the
+    // waves' columns differ (those outside the row stay unused)
+    auto place = [&](int j, int e) { return SHIFT ? col(j) + e : (j * V + e) * 64 + tid; };
+    auto used = [&](int j, int e) { return !SHIFT || in_row<SHIFT>(col(j), e, D); };
     if (wave > 0) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          part[((wave - 1) * 2) * P + (j * V + e) * 64 + tid] = dw[j][e];
-          part[((wave - 1) * 2 + 1) * P + (j * V + e) * 64 + tid] = db[j][e];
+          if (used(j, e)) {
+            part[((wave - 1) * 2) * P + place(j, e)] = dw[j][e];
+            part[((wave - 1) * 2 + 1) * P + place(j, e)] = db[j][e];
+          }
         }
     }
     __syncthreads();
@@ -227,16 +286,27 @@ __global__ __launch_bounds__(norm_bwd_threads(TPR)) void norm_backward_kernel(No
       for (int e = 0; e < V; ++e) {
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-          dw[j][e] += part[(k * 2) * P + (j * V + e) * 64 + tid];
-          db[j][e] += part[(k * 2 + 1) * P + (j * V + e) * 64 + tid];
+          if (used(j, e)) {
+            dw[j][e] += part[(k * 2) * P + place(j, e)];
+            db[j][e] += part[(k * 2 + 1) * P + place(j, e)];
+          }
         }
       }
   }
+  float* ws = a.ws + (int64_t)blockIdx.x * 2 * a.D;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    if (col(j) < a.D) {
-      store_vec<IoF32, V>(a.ws + (int64_t)blockIdx.x * 2 * a.D + col(j), dw[j]);
-      store_vec<IoF32, V>(a.ws + (int64_t)blockIdx.x * 2 * a.D + a.D + col(j), db[j]);
+    if constexpr (SHIFT) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if (in_row<SHIFT>(col(j), e, D)) {
+          ws[col(j) + e] = dw[j][e];
+          ws[a.D + col(j) + e] = db[j][e];
+        }
+      }
+    } else {
+      store_cols<IoF32, V, false>(ws, 0, col(j), D, dw[j]);
+      store_cols<IoF32, V, false>(ws + a.D, 0, col(j), D, db[j]);
     }
   }
 }
@@ -252,13 +322,21 @@ __global__ __launch_bounds__(kColsumThreads) void norm_param_kernel(const float*
   else if (db) db[c - D] = s;
 }
 
-// Backward: threads a row, for 16 values a thread at most.
-static int norm_bwd_tpr(int64_t D) { return D <= 64 * 16 ? 64 : D <= 256 * 16 ? 256 : 1024; }
+// Columns a row's threads have to cover: with the most that the first group can
+// begin before a row that is not whole groups of 4.
+static int64_t norm_cover(int64_t D) { return D % 4 == 0 ? D : D + (D % 2 ? 3 : 2); }
+
+// Backward: threads a row, for 16 values a thread at most (but one row length).
+static int norm_bwd_tpr(int64_t D) {
+  const int64_t n = norm_cover(D);
+  return n <= 64 * 16 ? 64 : n <= 256 * 16 ? 256 : 1024;
+}
 
 // Blocks the backward walks the rows with, each leaving a row of partial sums:
 // two a compute unit (one of 1024 threads), but four rows a walker at least
 // where that still leaves half a block a unit: the partial sums cost as much
-// as reading one fp32 row each, and their addition as much again.
+// as reading one fp32 row each, and their addition as much again.  Where rows
+// begin inside groups, steps in whole fours.
 static int64_t norm_bwd_blocks(int64_t rows, int64_t D) {
   const int64_t cus = device_cu_count();
   const int tpr = norm_bwd_tpr(D);
@@ -266,6 +344,7 @@ static int64_t norm_bwd_blocks(int64_t rows, int64_t D) {
   int64_t b = tpr == 1024 ? cus : 2 * cus;
   const int64_t quarter = (walkers + 3) / 4;
   if (quarter < b) b = quarter > cus / 2 ? quarter : cus / 2;
+  b = (b + 3) / 4 * 4;
   return walkers < b ? walkers : b;
 }
 
@@ -273,17 +352,17 @@ size_t norm_backward_ws_bytes(int64_t rows, int64_t D) {
   return sizeof(float) * (size_t)(2 * D) * (size_t)norm_bwd_blocks(rows, D);
 }
 
-template <class IO, class RO, int V, int NV, int TPR>
+template <class IO, class RO, int V, bool SHIFT, int NV, int TPR>
 static hipError_t norm_fwd_go(const NormArgs& a, hipStream_t s) {
   const int64_t blocks = TPR == 64 ? (a.rows + 3) / 4 : a.rows;
-  hipLaunchKernelGGL((norm_forward_kernel<IO, RO, V, NV, TPR>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((norm_forward_kernel<IO, RO, V, SHIFT, NV, TPR>), dim3((unsigned)blocks), dim3(256), 0, s, a);
   return hipGetLastError();
 }
-template <class IO, class RO, int V, int NV, int TPR>
+template <class IO, class RO, int V, bool SHIFT, int NV, int TPR>
 static hipError_t norm_bwd_go(const NormArgs& a, hipStream_t s) {
   const int64_t blocks = norm_bwd_blocks(a.rows, a.D);
-  hipLaunchKernelGGL((norm_backward_kernel<IO, RO, V, NV, TPR>), dim3((unsigned)blocks), dim3(norm_bwd_threads(TPR)), 0,
-                     s, a);
+  hipLaunchKernelGGL((norm_backward_kernel<IO, RO, V, SHIFT, NV, TPR>), dim3((unsigned)blocks),
+                     dim3(norm_bwd_threads(TPR)), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(norm_param_kernel, dim3((unsigned)((2 * a.D + 63) / 64)), dim3(kColsumThreads), 0, s, a.ws, blocks,
@@ -291,39 +370,56 @@ static hipError_t norm_bwd_go(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Values a thread holds: NV runs of V (the loads past a short row are skipped).
-template <class IO, class RO, int V, int TPR>
+// Values a thread holds: NV groups of V (the loads past a short row are
+// skipped).  16383 columns, the one length that its shift takes over the most
+// that 16384 need, get a group more.
+template <class IO, class RO, int V, bool SHIFT, int TPR>
 static hipError_t norm_fwd_nv(const NormArgs& a, hipStream_t s) {
-  const int64_t per = (a.D + TPR - 1) / TPR;
-  if (per <= 8) return norm_fwd_go<IO, RO, V, 8 / V, TPR>(a, s);
-  if (per <= 16) return norm_fwd_go<IO, RO, V, 16 / V, TPR>(a, s);
-  if (per <= 40) return norm_fwd_go<IO, RO, V, 40 / V, TPR>(a, s);
-  return norm_fwd_go<IO, RO, V, 64 / V, TPR>(a, s);
+  const int64_t per = ((SHIFT ? norm_cover(a.D) : a.D) + TPR - 1) / TPR;
+  if (per <= 8) return norm_fwd_go<IO, RO, V, SHIFT, 8 / V, TPR>(a, s);
+  if (per <= 16) return norm_fwd_go<IO, RO, V, SHIFT, 16 / V, TPR>(a, s);
+  if (per <= 40) return norm_fwd_go<IO, RO, V, SHIFT, 40 / V, TPR>(a, s);
+  if (per <= 64) return norm_fwd_go<IO, RO, V, SHIFT, 64 / V, TPR>(a, s);
+  if constexpr (SHIFT && TPR == 256) return norm_fwd_go<IO, RO, V, SHIFT, 64 / V + 1, TPR>(a, s);
+  return hipErrorInvalidValue;
 }
-template <class IO, class RO, int V, int TPR>
+template <class IO, class RO, int V, bool SHIFT, int TPR>
 static hipError_t norm_bwd_nv(const NormArgs& a, hipStream_t s) {
-  const int64_t per = (a.D + TPR - 1) / TPR;
-  if (per <= 8) return norm_bwd_go<IO, RO, V, 8 / V, TPR>(a, s);
-  if (per <= 12) return norm_bwd_go<IO, RO, V, 12 / V, TPR>(a, s);
-  return norm_bwd_go<IO, RO, V, 16 / V, TPR>(a, s);
+  const int64_t per = ((SHIFT ? norm_cover(a.D) : a.D) + TPR - 1) / TPR;
+  if (per <= 8) return norm_bwd_go<IO, RO, V, SHIFT, 8 / V, TPR>(a, s);
+  if (per <= 12) return norm_bwd_go<IO, RO, V, SHIFT, 12 / V, TPR>(a, s);
+  if (per <= 16) return norm_bwd_go<IO, RO, V, SHIFT, 16 / V, TPR>(a, s);
+  if constexpr (SHIFT && TPR == 1024) return norm_bwd_go<IO, RO, V, SHIFT, 16 / V + 1, TPR>(a, s);
+  return hipErrorInvalidValue;
 }
 
+template <class IO, class RO, int V, bool SHIFT>
+static hipError_t norm_fwd_rows(const NormArgs& a, hipStream_t s) {
+  return norm_cover(a.D) <= 64 * 64 ? norm_fwd_nv<IO, RO, V, SHIFT, 64>(a, s) : norm_fwd_nv<IO, RO, V, SHIFT, 256>(a, s);
+}
+template <class IO, class RO, int V, bool SHIFT>
+static hipError_t norm_bwd_rows(const NormArgs& a, hipStream_t s) {
+  switch (norm_bwd_tpr(a.D)) {
+    case 64: return norm_bwd_nv<IO, RO, V, SHIFT, 64>(a, s);
+    case 256: return norm_bwd_nv<IO, RO, V, SHIFT, 256>(a, s);
+    default: return norm_bwd_nv<IO, RO, V, SHIFT, 1024>(a, s);
+  }
+}
+
+// Rows that are not whole groups: shifted groups where a type is bf16, whose
+// single elements make loads of half a line a wave; single elements in fp32
+// (4096 rows of 5001 columns forward: 67 us, in groups 79; 3000 of 733
+// backward: 16 and 20).
 template <class IO, class RO, bool BWD>
 static hipError_t norm_types(const NormArgs& a, hipStream_t s) {
+  constexpr bool bf16 = IO::kVec == 8 || RO::kVec == 8;
   if constexpr (BWD) {
-    const int tpr = norm_bwd_tpr(a.D);
-    if (a.D % 4 == 0) {
-      if (tpr == 64) return norm_bwd_nv<IO, RO, 4, 64>(a, s);
-      if (tpr == 256) return norm_bwd_nv<IO, RO, 4, 256>(a, s);
-      return norm_bwd_nv<IO, RO, 4, 1024>(a, s);
-    }
-    if (tpr == 64) return norm_bwd_nv<IO, RO, 1, 64>(a, s);
-    if (tpr == 256) return norm_bwd_nv<IO, RO, 1, 256>(a, s);
-    return norm_bwd_nv<IO, RO, 1, 1024>(a, s);
+    if (a.D % 4 == 0) return norm_bwd_rows<IO, RO, 4, false>(a, s);
+    return norm_bwd_rows<IO, RO, bf16 ? 4 : 1, bf16>(a, s);
   } else {
-    const bool wave = a.D <= 64 * 64;
-    if (a.D % 8 == 0) return wave ? norm_fwd_nv<IO, RO, 8, 64>(a, s) : norm_fwd_nv<IO, RO, 8, 256>(a, s);
-    return wave ? norm_fwd_nv<IO, RO, 1, 64>(a, s) : norm_fwd_nv<IO, RO, 1, 256>(a, s);
+    if (a.D % 8 == 0) return norm_fwd_rows<IO, RO, 8, false>(a, s);
+    if (a.D % 4 == 0) return norm_fwd_rows<IO, RO, 4, false>(a, s);
+    return norm_fwd_rows<IO, RO, bf16 ? 4 : 1, bf16>(a, s);
   }
 }
 

@@ -395,6 +395,17 @@ def test_norm(rows, D, dtype, res, rms):
         assert g[n] is None or torch.equal(g[n], again[n]), n
 
 
+# Rows that begin anywhere in a group of four, walked in steps of four.
+NORM_ODD = [(9, 2), (11, 3), (70, 5), (1029, 130), (2500, 61), (700, 1021), (37, 1022), (41, 1023), (1300, 1669),
+            (6, 4093), (530, 4094), (7, 4095), (5, 16382), (3, 16383), (270, 16383)]
+
+
+@pytest.mark.parametrize("dtype,res,rms", [("bf16", "f32", False), ("bf16", "bf16", True), ("f32", "", False)])
+@pytest.mark.parametrize("rows,D", NORM_ODD)
+def test_norm_of_odd_rows(rows, D, dtype, res, rms):
+    test_norm(rows, D, dtype, res, rms)
+
+
 def test_norm_without_optional_arguments():
     x = torch.randn((5, 3, 24), device="cuda")
     w = torch.ones(24, device="cuda")
