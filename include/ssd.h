@@ -381,7 +381,8 @@ size_t ssd_backward_workspace_bytes(const ssd_shape* shape);
  * elements (0 = dense) leads from one token to the next, batches follow each
  * other at L rows.  Such arguments need only be aligned to their element, Bm
  * and Cm to 4 bytes (with row strides in whole 4-byte units); everything else
- * to 16 bytes.  Optional arguments may be NULL.  A gradient asked for by a
+ * to 16 bytes.  Of rows longer than one token the stride (given or dense) is
+ * below 2^25 elements (else SSD_ERR_UNSUPPORTED).  Optional arguments may be NULL.  A gradient asked for by a
  * pointer is written whole.  Results do not depend on timing (no atomics).
  *
  * Packed sequences as in ssd_forward_varlen: seq_idx [B,L] (optional) names
@@ -441,9 +442,9 @@ size_t ssd_causal_conv_backward_workspace_bytes(const ssd_conv_shape* shape);
  * A [D,N], Dskip, dt_bias [D] fp32; Dskip, z, dt_bias optional.  y [B,L,D] in
  * `in`; initial_states, final_states [B,N,D], seq_states [nseq,N,D] fp32,
  * optional.  N (dstate) a multiple of 4 up to 256 (else SSD_ERR_UNSUPPORTED).
- * Row strides: `rows` NULL = all dense.  Workspace: device memory of
- * ssd_selective_scan_workspace_bytes(shape) bytes (0 and NULL where the tokens
- * are not split).
+ * At most 32767 batches of 65535 * 16 tokens (else SSD_ERR_UNSUPPORTED).  Row
+ * strides: `rows` NULL = all dense.  Workspace: device memory of
+ * ssd_selective_scan_workspace_bytes(shape) bytes, never 0 for a valid shape.
  */
 typedef struct {
   int64_t batch, seqlen, channels, dstate, ngroups;

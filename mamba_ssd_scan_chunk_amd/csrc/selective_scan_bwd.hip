@@ -16,7 +16,9 @@
 // recomputed forwards 16 tokens at a time (from the states the first pass left
 // at every 16th token) and swept backwards.  The sums over channels go through
 // LDS, 16 tokens of one state at a time; the channel blocks' partial sums are
-// then added in order.  No atomics: results do not depend on timing.
+// then added in order.  No atomics: results do not depend on timing.  2 x 2048
+// tokens of 5120 channels and 16 states, bf16, gated: 427 us, 300 of them the
+// third pass and 115 the first, bound by the vector ALUs.
 #include "layer_device.hpp"
 #include "layer_launch.hpp"
 #include "selective_scan.hpp"
@@ -186,10 +188,12 @@ __device__ __forceinline__ float lane_sums(const float* red, int lane) {
 }
 
 // Pass 3, two waves a SIMD: six values a token in registers beside the state's
-// own leave no room for a third (forced to three the compiler spills and the
-// step below took 792 us; tiles of 8 tokens at three waves took as long as
-// this, their loads of states and sums being twice as many).  LDS of a wave: the adjoint riding backwards and the summed dA, per
-// state and lane, and the values being summed over lanes.
+// own leave no room for a third (forced to three the compiler spills: 792 us;
+// tiles of 8 tokens at three waves read and write twice the states and take as
+// long over most shapes).  300 us at 2 x 2048 tokens of 5120 channels and 16
+// states, the vector ALUs busy for 71% of it.  LDS of a wave: the adjoint
+// riding backwards and the summed dA, per state and lane, and the values being
+// summed over lanes.
 template <class IO, bool PACKED>
 __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(2, 2))) void scan_bwd_chunk_kernel(ScanArgs a, ScanGrid g, ScanWs ws, BwdWs bw) {
   typedef typename IO::type T;
@@ -435,7 +439,7 @@ __global__ __launch_bounds__(kColsumThreads) void scan_param_kernel(const float*
 // Chunks of four tiles: the carried states then cost a quarter of the per-tile
 // states.  Shorter ones, down to one tile, where four would leave the third
 // pass's two waves a SIMD unfilled (3 x 777 tokens of 1002 channels, fp32:
-// 122 us with four tiles, 97 with two).
+// 122 us with four tiles where two took 97).
 static ScanGrid backward_grid(int64_t B, int64_t L, int64_t D, int64_t N, int64_t G) {
   ScanGrid g;
   g.ncb = (D / G + 63) / 64;
