@@ -193,7 +193,7 @@ __device__ __forceinline__ float lane_sums(const float* red, int lane) {
 // long over most shapes).  300 us at 2 x 2048 tokens of 5120 channels and 16
 // states, the vector ALUs busy for 71% of it.  LDS of a wave: the adjoint
 // riding backwards and the summed dA, per state and lane, and the values being
-// summed over lanes.
+// summed over lanes, dC's beside dB's: one wait for both sums, behind the sweep.
 template <class IO, bool PACKED>
 __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(2, 2))) void scan_bwd_chunk_kernel(ScanArgs a, ScanGrid g, ScanWs ws, BwdWs bw) {
   typedef typename IO::type T;
@@ -202,7 +202,8 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(2, 2))) void
   const ScanBlock k = scan_block(g, a);
   const int N = (int)a.N;
   float* red = lds;
-  float* gs = lds + kScanT * kRedRow + lane;  // gs[n*64]
+  float* redc = red + kScanT * kRedRow;
+  float* gs = lds + 2 * kScanT * kRedRow + lane;  // gs[n*64]
   float* as = gs + N * 64;                    // dA
   const int64_t d = k.d0 + lane < k.dend ? k.d0 + lane : k.dend - 1;
   const bool ok = k.d0 + lane < k.dend;
@@ -296,11 +297,8 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(2, 2))) void
         hp = fmaf(dec[i], hp, x[i] * e.b(i));
         h[i] = hp;
         y[i] = fmaf(e.c(i), hp, y[i]);
-        red[i * kRedRow + lane] = hp * gy[i];
+        redc[i * kRedRow + lane] = hp * gy[i];
       }
-      __builtin_amdgcn_wave_barrier();
-      const float sumC = lane_sums(red, lane);
-      __builtin_amdgcn_wave_barrier();
       float ga = gs[n * 64], dA = as[n * 64];
 #pragma unroll
       for (int i = kScanT - 1; i >= 0; --i) {
@@ -328,7 +326,7 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(2, 2))) void
       gs[n * 64] = ga;
       as[n * 64] = dA;
       __builtin_amdgcn_wave_barrier();
-      const float sumB = lane_sums(red, lane);
+      const float sumB = lane_sums(red, lane), sumC = lane_sums(redc, lane);
       __builtin_amdgcn_wave_barrier();
       const bool mine = (n & 3) == (lane & 3);
       rB = mine ? sumB : rB;
@@ -491,7 +489,7 @@ static hipError_t scan_backward_t(const ScanArgs& a, hipStream_t s) {
   const BwdWs bw = {at(w.bc), at(w.dDb)};
   const dim3 grid((unsigned)(a.G * g.ncb), (unsigned)g.nc, (unsigned)a.B), block(64);
   const size_t per = 64 * sizeof(float) * a.N;
-  const size_t lds1 = 2 * per, lds3 = 2 * per + sizeof(float) * kScanT * kRedRow;
+  const size_t lds1 = 2 * per, lds3 = 2 * per + 2 * sizeof(float) * kScanT * kRedRow;
   hipError_t e;
   if (lds1 > 64 * 1024 || lds3 > 64 * 1024) {
     e = hipFuncSetAttribute(reinterpret_cast<const void*>(&scan_bwd_local_kernel<IO, PACKED>),
