@@ -144,7 +144,8 @@ __global__ __launch_bounds__(64) void scan_bwd_local_kernel(ScanArgs a, ScanGrid
       }
       e = nxt;
       hs[n * 64] = h;
-      gs[n * 64] = fmaf(fast_exp2(sdt0 * an), r, gs[n * 64]);
+      // (nothing of tokens behind a start, whose time steps may be anything)
+      if (!PACKED || live > 0) gs[n * 64] = fmaf(fast_exp2(sdt0 * an), r, gs[n * 64]);
       ts[(int64_t)n * a.D] = h;
     }
     cut = cut || starts != 0;

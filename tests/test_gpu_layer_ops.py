@@ -345,6 +345,31 @@ def test_other_sequences_nan_stays_there(dtype):
         assert torch.isfinite(a).all() and torch.equal(a, b), i
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_other_sequences_nan_stays_there_in_long_chunks(dtype):
+    """The same where a chunk holds several tiles: the bad sequence begins and
+    ends inside a tile, with tiles of its own chunk before and after."""
+    B, L, D, N, lo, hi = 4, 1024, 2048, 4, 470, 570
+    say(f"packed NaN in long chunks {dtype}")
+    idx = np.repeat(np.arange(3, dtype=np.int32), [lo, hi - lo, L - hi])[None].repeat(B, 0)
+    out = {}
+    for bad in (False, True):
+        c = scan_case((B, L, D, N, 1, 0, [L], True, True, True), dtype, 6)
+        t = dict(c["t"], seq_idx=torch.from_numpy(np.ascontiguousarray(idx)).cuda())
+        dy = dev(c["dy"], dtype)
+        if bad:
+            for v in [t[n] for n in ("u", "dt", "Bm", "Cm", "z")] + [dy]:
+                v[:, lo:hi] = float("nan")
+                v[:, lo + 3:hi - 20] = float("inf")
+        y, fin = ops.ssd_selective_scan(**t)
+        g = ops.ssd_selective_scan_backward(**t, dy=dy, dfinal=dev(c["df"]), want_dinitial=True)
+        torch.cuda.synchronize()
+        keep = [torch.cat([v[:, :lo], v[:, hi:]], 1) for v in (y, *(g[n] for n in ("du", "ddt", "dB", "dC", "dz")))]
+        out[bad] = keep + [fin, g["dinitial"]]
+    for i, (a, b) in enumerate(zip(out[False], out[True])):
+        assert torch.isfinite(a).all() and torch.equal(a, b), i
+
+
 # ---------------------------------------------------------------- norm
 
 # (rows, D)
