@@ -105,7 +105,7 @@ __global__ __launch_bounds__(64) void scan_bwd_local_kernel(ScanArgs a, ScanGrid
     }
     // tokens of this step that still reach the chunk's entering state
     const int live = cut ? 0 : (starts ? __builtin_ctz(starts) : kScanT);
-    const float sdt0 = sdt;
+    const float sdt0 = PACKED && cut ? 0.f : sdt;  // behind a start r is zero, but time steps may be anything
     // The state entering the next tile.  Stored always, from every lane (a lane
     // past the group repeats its last channel, value and all): behind a
     // condition the next state's load would wait for the store too.  What
@@ -144,8 +144,7 @@ __global__ __launch_bounds__(64) void scan_bwd_local_kernel(ScanArgs a, ScanGrid
       }
       e = nxt;
       hs[n * 64] = h;
-      // (nothing of tokens behind a start, whose time steps may be anything)
-      if (!PACKED || live > 0) gs[n * 64] = fmaf(fast_exp2(sdt0 * an), r, gs[n * 64]);
+      gs[n * 64] = fmaf(fast_exp2(sdt0 * an), r, gs[n * 64]);
       ts[(int64_t)n * a.D] = h;
     }
     cut = cut || starts != 0;

@@ -370,6 +370,32 @@ def test_other_sequences_nan_stays_there_in_long_chunks(dtype):
         assert torch.isfinite(a).all() and torch.equal(a, b), i
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lo,hi", [(1000, 1003), (1023, 1025), (704, 1000), (31, 32)])
+def test_other_sequences_nan_stays_there_in_long_conv_runs(lo, hi, dtype):
+    """The convolution's runs of 32 tokens, a bad sequence of a token or more
+    inside a run, over a run's border, over several."""
+    B, L, D, W = 4, 2048, 1024, 4
+    say(f"packed NaN in long convolution runs {lo} {hi} {dtype}")
+    idx = np.repeat(np.arange(3, dtype=np.int32), [lo, hi - lo, L - hi])[None].repeat(B, 0)
+    ci = torch.from_numpy(np.ascontiguousarray(idx)).cuda()
+    out = {}
+    for bad in (False, True):
+        c = conv_case((B, L, D, W, 0, [L], True), dtype, 6)
+        gy = dev(c["dy"], dtype)
+        if bad:
+            for v in (c["tx"], gy):
+                v[:, lo:hi] = float("nan")
+                v[:, lo:hi - 1] = float("inf")
+        y, fin = ops.ssd_causal_conv(c["tx"], dev(c["w"]), dev(c["bias"]), True, c["tinit"], ci, want_final=True)
+        g = ops.ssd_causal_conv_backward(c["tx"], dev(c["w"]), gy, dev(c["bias"]), True, c["tinit"], ci,
+                                         want_dinitial=True)
+        torch.cuda.synchronize()
+        out[bad] = [torch.cat([v[:, :lo], v[:, hi:]], 1) for v in (y, g["dx"])] + [fin, g["dinitial"]]
+    for i, (a, b) in enumerate(zip(out[False], out[True])):
+        assert torch.isfinite(a).all() and torch.equal(a, b), i
+
+
 # ---------------------------------------------------------------- norm
 
 # (rows, D)
