@@ -11,17 +11,19 @@
 //
 // Bound by memory.  A row stays in registers between its one read and its one
 // write: 16384 rows of 2560 columns (bf16, fp32 residual) 100 us forward, 5.0
-// TB/s, and 140 us backward, 4.8 TB/s, where a copy reaches 4.95.  Forward: a wave a row up to 4096 columns, 256 threads beyond, 8 or 4
+// TB/s, and 124 us backward, 5.4 TB/s, where a copy reaches 4.95.  Forward: a wave a row up to 4096 columns, 256 threads beyond, 8 or 4
 // elements a load.  Rows that are not whole groups of 4 begin anywhere in one:
 // in bf16 their threads take the groups as memory has them, the first beginning
 // up to 3 columns before the row and the last ending after it (4866 rows of
-// 1669 columns: 51 us an element a load, 26 so; gradients 57 and 41).
+// 1669 columns: 51 us an element a load, 21 so; gradients 57 and 32).
 // Backward: 64, 256 or 1024 threads a row, 16 values a thread at most, so that
 // the five values a column (x, dy, w, dw, dbias) leave room for waves beside;
 // blocks walk rows, the next row's loads in flight behind the sums of this
 // one, and keep dw and dbias of their columns in registers (walking in steps
 // of 4 rows, they find the same columns in each).  The blocks' partial sums are
 // added in a fixed order.
+#include <type_traits>
+
 #include "layer_device.hpp"
 #include "layer_launch.hpp"
 
@@ -55,24 +57,56 @@ template <bool SHIFT>
 __device__ __forceinline__ bool in_row(int c, int e, int D) {
   return SHIFT ? (unsigned)(c + e) < (unsigned)D : c < D;
 }
-// Loads V elements at column c as fp32, zeros outside the row.  Groups over a
-// row's ends hold elements of its neighbours, all within the `total` elements
-// but for the last row's.  (Loads of groups past the row made unconditional, to
-// leave the compiler no branches, cost more in traffic than they saved.)
+// V elements at column c, zeros outside the row, held as loaded until they are
+// widened: widened in the branch that loads them each group would be waited
+// for before the next is asked for (4866 rows of 1669 columns, bf16: 26 us,
+// 21 so; gradients of 16384 x 2560 142 and 124).  Groups over a row's ends hold elements of its neighbours, all
+// within the `total` elements but for the last row's.  (Loads of groups past the
+// row made unconditional, to leave no branches, cost more in traffic than they
+// saved.)
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 template <class IO, int V, bool SHIFT>
-__device__ __forceinline__ void load_cols(const void* base, int64_t row0, int c, int D, int64_t total, float* o) {
-  const typename IO::type* p = static_cast<const typename IO::type*>(base) + row0 + c;
-  if (c < D && (!SHIFT || row0 + c + V <= total)) {
-    load_vec<IO, V>(p, o);
+struct Cols {
+  typedef typename IO::type T;
+  static constexpr bool kWords = sizeof(T) == 2 && V > 1;  // bf16 in whole words
+  typedef std::conditional_t<kWords, std::conditional_t<V == 8, u32x4_t, u32x2_t>, T> Q;
+  Q q[kWords ? 1 : V];
+  __device__ __forceinline__ void load(const void* base, int64_t row0, int c, int D, int64_t total) {
+    const T* p = static_cast<const T*>(base) + row0 + c;
+#pragma unroll
+    for (int e = 0; e < (kWords ? 1 : V); ++e) q[e] = Q(0);
+    if (c < D && (!SHIFT || row0 + c + V <= total)) {
+      if constexpr (kWords || V == 1) {
+        q[0] = *reinterpret_cast<const Q*>(p);
+      } else {
+        load_vec<IO, V>(p, q);
+      }
+    } else if constexpr (SHIFT) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if (in_row<SHIFT>(c, e, D)) {
+          if constexpr (kWords) q[0][e / 2] |= (uint32_t)p[e] << (e % 2 * 16);
+          else q[e] = p[e];
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void widen(int c, int D, float* o) const {
+    if constexpr (kWords) {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        o[e] = __uint_as_float(e % 2 ? q[0][e / 2] & 0xffff0000u : q[0][e / 2] << 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = IO::get(q[e]);
+    }
     if constexpr (SHIFT) {
 #pragma unroll
       for (int e = 0; e < V; ++e) o[e] = in_row<SHIFT>(c, e, D) ? o[e] : 0.f;
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = SHIFT && in_row<SHIFT>(c, e, D) ? IO::get(p[e]) : 0.f;
   }
-}
+};
 template <class IO, int V, bool SHIFT>
 __device__ __forceinline__ void store_cols(void* base, int64_t row0, int c, int D, const float* v) {
   typename IO::type* p = static_cast<typename IO::type*>(base) + row0 + c;
@@ -98,7 +132,9 @@ __device__ __forceinline__ void load_param(const float* p, int c, int D, float* 
       for (int e = 0; e < V; ++e) o[e] = in_row<SHIFT>(c, e, D) ? p[c + e] : 0.f;
     }
   } else {
-    load_cols<IoF32, V, false>(p, 0, c, D, D, o);
+    Cols<IoF32, V, false> q;
+    q.load(p, 0, c, D, D);
+    q.widen(c, D, o);
   }
 }
 
@@ -113,18 +149,25 @@ __global__ __launch_bounds__(256) void norm_forward_kernel(NormArgs a) {
   const int64_t total = a.rows * a.D;
   auto col = [&](int j) { return (j * TPR + tid) * V - m; };
   float x[NV][V];
+  Cols<IO, V, SHIFT> xq[NV];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) load_cols<IO, V, SHIFT>(a.x, r0, col(j), D, total, x[j]);
+  for (int j = 0; j < NV; ++j) xq[j].load(a.x, r0, col(j), D, total);
   if (a.residual) {
-    float q[NV][V];
+    Cols<RO, V, SHIFT> q[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) load_cols<RO, V, SHIFT>(a.residual, r0, col(j), D, total, q[j]);
+    for (int j = 0; j < NV; ++j) q[j].load(a.residual, r0, col(j), D, total);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      float t[V];
+      xq[j].widen(col(j), D, x[j]);
+      q[j].widen(col(j), D, t);
 #pragma unroll
-      for (int e = 0; e < V; ++e) x[j][e] = RO::get(RO::put(x[j][e] + q[j][e]));
+      for (int e = 0; e < V; ++e) x[j][e] = RO::get(RO::put(x[j][e] + t[e]));
       store_cols<RO, V, SHIFT>(a.residual_out, r0, col(j), D, x[j]);
     }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) xq[j].widen(col(j), D, x[j]);
   }
   const float inv = 1.f / (float)a.D;
   float mean = 0.f;
@@ -203,7 +246,9 @@ __global__ __launch_bounds__(norm_bwd_threads(TPR)) void norm_backward_kernel(No
   const int D = (int)a.D, m = row_shift<V, SHIFT>(first * a.D);  // of each of the walker's rows
   const int64_t total = a.rows * a.D;
   auto col = [&](int j) { return (j * TPR + tid) * V - m; };
-  float w[NV][V], dw[NV][V], db[NV][V], x[NV][V], g[NV][V];
+  float w[NV][V], dw[NV][V], db[NV][V];
+  Cols<RO, V, SHIFT> x[NV];
+  Cols<IO, V, SHIFT> g[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     load_param<V, SHIFT>(a.w, col(j), D, w[j]);
@@ -213,8 +258,8 @@ __global__ __launch_bounds__(norm_bwd_threads(TPR)) void norm_backward_kernel(No
   auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      load_cols<RO, V, SHIFT>(a.x, row * a.D, col(j), D, total, x[j]);
-      load_cols<IO, V, SHIFT>(a.dy, row * a.D, col(j), D, total, g[j]);
+      x[j].load(a.x, row * a.D, col(j), D, total);
+      g[j].load(a.dy, row * a.D, col(j), D, total);
     }
   };
   // the next row's loads in flight behind this one's sums, but for the blocks
@@ -226,22 +271,24 @@ __global__ __launch_bounds__(norm_bwd_threads(TPR)) void norm_backward_kernel(No
     const int64_t r0 = row * a.D;
     if (!kAhead) fetch(row);
     const float rstd = a.rstd[row], mean = a.mean ? a.mean[row] : 0.f;
-    float xh[NV][V], v[NV][V], q[NV][V];
+    float xh[NV][V], v[NV][V];
+    Cols<RO, V, SHIFT> q[NV];
+    if (a.dres) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) q[j].load(a.dres, r0, col(j), D, total);
+    }
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (a.dres) {
-        load_cols<RO, V, SHIFT>(a.dres, r0, col(j), D, total, q[j]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) q[j][e] = 0.f;
-      }
+      float xv[V], gv[V];
+      x[j].widen(col(j), D, xv);
+      g[j].widen(col(j), D, gv);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        xh[j][e] = (x[j][e] - mean) * rstd;
-        dw[j][e] = fmaf(g[j][e], xh[j][e], dw[j][e]);
-        db[j][e] += g[j][e];
-        v[j][e] = g[j][e] * w[j][e];  // zero past the row
+        xh[j][e] = (xv[e] - mean) * rstd;
+        dw[j][e] = fmaf(gv[e], xh[j][e], dw[j][e]);
+        db[j][e] += gv[e];
+        v[j][e] = gv[e] * w[j][e];  // zero past the row
         s1 += v[j][e];
         s2 = fmaf(v[j][e], xh[j][e], s2);
       }
@@ -252,9 +299,12 @@ __global__ __launch_bounds__(norm_bwd_threads(TPR)) void norm_backward_kernel(No
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (col(j) < D) {
-        float o[V];
+        float o[V], t[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = fmaf(rstd, v[j][e] - fmaf(xh[j][e], m2, m1), q[j][e]);
+        for (int e = 0; e < V; ++e) t[e] = 0.f;
+        if (a.dres) q[j].widen(col(j), D, t);
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = fmaf(rstd, v[j][e] - fmaf(xh[j][e], m2, m1), t[e]);
         store_cols<IO, V, SHIFT>(a.dx, r0, col(j), D, o);
         if (a.dres_out) store_cols<RO, V, SHIFT>(a.dres_out, r0, col(j), D, o);
       }
