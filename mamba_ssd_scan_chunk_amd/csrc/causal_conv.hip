@@ -15,8 +15,8 @@
 // tokens with the last W-1 inputs in registers, so each input is read once
 // plus a halo of W-1 rows per run.  The run, its row addresses and its
 // sequence starts are the same for the whole wave and live in scalars.
-// 2 x 8192 tokens of 5376 channels (bf16): 71 us forward, 5.0 TB/s, and 115 us
-// backward, 4.6 TB/s, where a copy reaches 4.95.
+// 2 x 8192 tokens of 5376 channels (bf16): 71 us forward, 5.0 TB/s, and 112 us
+// backward, 4.7 TB/s, where a copy reaches 4.95.
 #include <type_traits>
 
 #include "layer_device.hpp"
@@ -178,25 +178,36 @@ __device__ __forceinline__ void load_weights(const float* w, const float* bias, 
 }
 
 // The window entering token t0 of row b: the W-1 inputs before it, zero from
-// where another sequence starts.
+// where another sequence starts.  `ask` loads them, all at once, `fill` takes
+// them; the run's first rows are asked for in between.
 template <class IO, int V, int W, bool PACKED>
-__device__ __forceinline__ void window_at(const ConvArgs& a, const typename IO::type* xr, const int* sr, int64_t b,
-                                          int64_t d, int64_t t0, Window<W, V>& win) {
-  win.clear();
-  const uint64_t st = PACKED ? start_bits(sr, t0 - (W - 1), W, a.L) : 0;
+struct WindowAt {
+  typename Raw<IO, V>::type q[W - 1];
+  __device__ __forceinline__ void ask(const ConvArgs& a, const typename IO::type* xr, int64_t b, int64_t d, int64_t t0) {
+    const typename IO::type* init = static_cast<const typename IO::type*>(a.init) + b * (W - 1) * a.D + d;
 #pragma unroll
-  for (int k = 0; k < W - 1; ++k) {
-    const int64_t j = t0 - (W - 1) + k;
-    float x[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) x[e] = 0.f;
-    if (j >= 0) load_vec<IO, V>(xr + j * a.x_row, x);
-    else if (a.init) load_vec<IO, V>(static_cast<const typename IO::type*>(a.init) + (b * (W - 1) + j + W - 1) * a.D + d, x);
-    if (PACKED && (st >> k & 1)) win.clear();
-    win.push(x);
+    for (int k = 0; k < W - 1; ++k) {
+      const int64_t j = t0 - (W - 1) + k;
+      const typename IO::type* p = j >= 0 ? xr + j * a.x_row : a.init ? init + (j + W - 1) * a.D : xr;
+      q[k] = *reinterpret_cast<const typename Raw<IO, V>::type*>(p);
+    }
   }
-  if (PACKED && (st >> (W - 1) & 1)) win.clear();
-}
+  // st: the starts from token t0 - W + 1 on
+  __device__ __forceinline__ void fill(const ConvArgs& a, int64_t t0, uint64_t st, Window<W, V>& win) const {
+    win.clear();
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+      float x[V];
+      Raw<IO, V>::widen(q[k], x);
+      const bool there = t0 - (W - 1) + k >= 0 || a.init;
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[e] = there ? x[e] : 0.f;
+      if (PACKED && (st >> k & 1)) win.clear();
+      win.push(x);
+    }
+    if (PACKED && (st >> (W - 1) & 1)) win.clear();
+  }
+};
 
 template <class IO, int V, int W, bool PACKED, bool SILU>
 __global__ __launch_bounds__(kConvThreads) void conv_forward_kernel(ConvArgs a, int64_t nrun, int run, int64_t ncb) {
@@ -207,10 +218,8 @@ __global__ __launch_bounds__(kConvThreads) void conv_forward_kernel(ConvArgs a, 
   const int* sr = PACKED ? a.seq_idx + r.b * a.L : nullptr;
   float wv[W][V], bv[V];
   load_weights<V, W>(a.w, a.bias, r.d, wv, bv);
-  Window<W, V> win;
-  window_at<IO, V, W, PACKED>(a, xr, sr, r.b, r.d, r.t0, win);
-  // the run's starts; its first token was seen to when the window was made
-  const uint64_t starts = PACKED ? start_bits(sr, r.t0, (int)(r.t1 - r.t0), a.L) & ~uint64_t(1) : 0;
+  WindowAt<IO, V, W, PACKED> before;
+  before.ask(a, xr, r.b, r.d, r.t0);
   auto out = [&](const float (&tap)[W][V], float* o) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
@@ -225,6 +234,11 @@ __global__ __launch_bounds__(kConvThreads) void conv_forward_kernel(ConvArgs a, 
   T* yb = static_cast<T*>(a.y) + (r.b * a.L + r.t0) * a.D + r.d0;
   Rows<IO, V, kConvBatch> x;
   x.load(xb, a.x_row, tokens_left<kConvBatch>(r.t0, r.t1), off);
+  // the starts that the run can see, from token t0 - W + 1 on
+  uint64_t starts = PACKED ? start_bits(sr, r.t0 - (W - 1), (int)(r.t1 - r.t0) + W - 1, a.L) : 0;
+  Window<W, V> win;
+  before.fill(a, r.t0, starts, win);
+  starts = starts >> (W - 1) & ~uint64_t(1);  // from t0 on, whose own the window has seen
   x.settle();
   for (int64_t t = r.t0; t < r.t1; t += kConvBatch) {
     const int n = tokens_left<kConvBatch>(t, r.t1);
@@ -346,11 +360,10 @@ __global__ __launch_bounds__(kConvThreads) void conv_backward_kernel(ConvArgs a,
     T* dxr = static_cast<T*>(a.dx) + b * a.L * a.dx_row + d;
     float wv[W][V], bv[V];
     load_weights<V, W>(a.w, a.bias, d, wv, bv);
+    WindowAt<IO, V, W, PACKED> before;
+    before.ask(a, xr, b, d, t0);
     Window<W, V> win, pend;  // pend.v[k]: dx collected so far of the input win.v[k]
-    window_at<IO, V, W, PACKED>(a, xr, sr, b, d, t0, win);
     pend.clear();
-    // starts from token t0 - W + 1 on, all the run can see
-    const uint64_t starts = PACKED ? start_bits(sr, t0 - (W - 1), (int)(t2 - t0) + W - 1, a.L) : 0;
     auto finish = [&](int64_t j, const float* g) {  // dx of input j is complete
       float o[V];
 #pragma unroll
@@ -400,6 +413,9 @@ __global__ __launch_bounds__(kConvThreads) void conv_backward_kernel(ConvArgs a,
     Rows<IO, V, NB> x, g;
     x.load(xb, a.x_row, tokens_left<NB>(t0, t2), off);
     g.load(gb, a.D, tokens_left<NB>(t0, t2), off);
+    // starts from token t0 - W + 1 on, all the run can see
+    const uint64_t starts = PACKED ? start_bits(sr, t0 - (W - 1), (int)(t2 - t0) + W - 1, a.L) : 0;
+    before.fill(a, t0, starts, win);
     x.settle();
     g.settle();
     // bit of token t in `starts`
@@ -607,8 +623,8 @@ static ConvGrid conv_grid(int64_t B, int64_t L, int64_t D, int V, int most) {
   return g;
 }
 // Measured at 2 x 8192 tokens of 5376 channels (bf16): forward runs of 16 tokens
-// 71 us, 8 79, 24 71, 32 72, 64 75; backward runs of 32 115 us, 40 120, 48 117, 56 121
-// (4 x 8192 tokens of 2304 channels in packed rows: 104, 108, 112, 109).
+// 71 us, 8 79, 24 71, 32 72, 64 75; backward runs of 32 112 us, of 40, 48 and 56
+// 2 to 5% more (4 x 8192 tokens of 2304 channels in packed rows: 101, 3 to 7%).
 constexpr int kConvFwdRun = 16, kConvBwdRun = 32;
 
 template <class IO, int V, int W, bool PACKED>

@@ -11,7 +11,8 @@
 //
 // Bound by memory.  A row stays in registers between its one read and its one
 // write: 16384 rows of 2560 columns (bf16, fp32 residual) 100 us forward, 5.0
-// TB/s, and 124 us backward, 5.4 TB/s, where a copy reaches 4.95.  Forward: a wave a row up to 4096 columns, 256 threads beyond, 8 or 4
+// TB/s, and 124 us backward, 5.4 TB/s, where a copy reaches 4.95.
+// Forward: a wave a row up to 4096 columns, 256 threads beyond, 8 or 4
 // elements a load.  Rows that are not whole groups of 4 begin anywhere in one:
 // in bf16 their threads take the groups as memory has them, the first beginning
 // up to 3 columns before the row and the last ending after it (4866 rows of
