@@ -283,3 +283,24 @@ def test_binding_refuses():
         ops.ssd_layer_norm(x, torch.zeros(8))
     with pytest.raises(ValueError, match="GPU"):
         ops.ssd_layer_norm_backward(x, x, torch.zeros(8), torch.zeros(2, 4), torch.zeros(2, 4))
+
+
+def test_rows_beyond_32_bit_offsets(lib):
+    """Strides, given or dense, of 2^25 elements and more: refused for rows of
+    several tokens, by the queries too, and no matter for single ones."""
+    far = 1 << 25
+    assert conv(lib, row=far) == UNSUP and conv(lib, channels=far) == UNSUP
+    assert conv(lib, row=far - 1, nseq=-1) == SHAPE and conv(lib, row=far, seqlen=1, nseq=-1) == SHAPE
+    for seqlen, there in ((2, False), (1, True)):
+        s = SSDConvShape(1, seqlen, far, 4)
+        assert (lib.ssd_causal_conv_backward_workspace_bytes(s) > 0) == there
+        s = scan_shape(batch=1, seqlen=seqlen, channels=far, dstate=4, ngroups=1)
+        assert (lib.ssd_selective_scan_workspace_bytes(s) > 0) == there
+        assert (lib.ssd_selective_scan_backward_workspace_bytes(s) > 0) == there
+    for k in range(5):
+        rows = [0] * 5
+        rows[k] = far
+        assert fwd(lib, rows=SSDScanRows(*rows)) == UNSUP, k
+        assert fwd(lib, s=scan_shape(seqlen=1), rows=SSDScanRows(*rows), nseq=-1) == SHAPE, k
+    s = SSDConvShape(2, 100, 64, 4)
+    assert lib.ssd_causal_conv_backward(s, F, 0, F, F, 1, 1, None, None, F, None, F, far, F, F, None, F, BIG, None) == UNSUP
