@@ -2,9 +2,11 @@
 
 Each function checks that its tensors are CUDA (HIP) tensors of the expected
 dtype, shape and contiguity, then calls the matching ``ssd_*`` function of
-``libmamba_ssd.so`` on torch's current stream.  Nothing is computed here and
-nothing is copied or converted silently: a mismatch raises ``ValueError``, a
-failed call raises ``SSDError``.
+``libmamba_ssd.so`` on torch's current stream.  ``stream=s`` is the same call
+inside ``torch.cuda.stream(s)``: workspaces and outputs made by the call belong
+to ``s``; making ``s`` wait for the inputs, and other streams for the outputs,
+is the caller's.  Nothing is computed here and nothing is copied or converted
+silently: a mismatch raises ``ValueError``, a failed call raises ``SSDError``.
 """
 from __future__ import annotations
 
@@ -54,12 +56,19 @@ def _ptr(t: Optional[torch.Tensor]):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream=None):
-    if stream is not None:
-        return stream.cuda_stream
+def _stream():
     if _raw_stream is not None:
         return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
+
+
+def _on_stream(f, args):
+    """The call ``f(**args)`` made on its ``stream`` argument: with that stream
+    current, its workspace and the outputs it makes come from that stream's
+    memory.  Taken from another stream's, their blocks could still be in use
+    there, or go to its next allocation before the kernels here are through."""
+    with torch.cuda.stream(args.pop("stream")):
+        return f(**args)
 
 
 def _mma(mma: str) -> int:
@@ -70,6 +79,8 @@ def _mma(mma: str) -> int:
 
 def ssd_chunk_cumsum(shape, dt, A, dA_cumsum=None, dt_bhl=None, with_dt=True, stream=None):
     """dA_cumsum, dt_bhl [B,H,nc,Q] from dt [B,L,H], A [H] (fp32)."""
+    if stream is not None:
+        return _on_stream(ssd_chunk_cumsum, locals())
     sh = _shape(shape)
     B, L, H, P, N, G, Q, nc = _dims(sh)
     f32 = (torch.float32,)
@@ -83,7 +94,7 @@ def ssd_chunk_cumsum(shape, dt, A, dA_cumsum=None, dt_bhl=None, with_dt=True, st
     if dt_bhl is not None:
         _req(dt_bhl, "dt_bhl", (B, H, nc, Q), f32)
     lib = load_library()
-    check(lib.ssd_chunk_cumsum(sh, _ptr(dt), _ptr(A), _ptr(dA_cumsum), _ptr(dt_bhl), _stream(stream)))
+    check(lib.ssd_chunk_cumsum(sh, _ptr(dt), _ptr(A), _ptr(dA_cumsum), _ptr(dt_bhl), _stream()))
     return dA_cumsum, dt_bhl
 
 
@@ -91,6 +102,8 @@ def ssd_chunk_state(shape, x, Bm, dt_bhl, dA_cumsum, states=None, mma="bf16", st
     """Per-chunk states [B,nc,H,N,P] (jump formula with decay), stored in
     ``states_dtype`` ("f32", or "bf16" rounded to nearest even; a given
     ``states`` tensor's dtype wins)."""
+    if stream is not None:
+        return _on_stream(ssd_chunk_state, locals())
     sh = _shape(shape)
     B, L, H, P, N, G, Q, nc = _dims(sh)
     io = (torch.float32, torch.bfloat16)
@@ -104,7 +117,7 @@ def ssd_chunk_state(shape, x, Bm, dt_bhl, dA_cumsum, states=None, mma="bf16", st
     _req(states, "states", (B, nc, H, N, P), io)
     lib = load_library()
     check(lib.ssd_chunk_state(sh, _ptr(x), _ptr(Bm), _DT[x.dtype], _ptr(dt_bhl), _ptr(dA_cumsum),
-                              _ptr(states), _DT[states.dtype], _mma(mma), _stream(stream)))
+                              _ptr(states), _DT[states.dtype], _mma(mma), _stream()))
     return states
 
 
@@ -113,6 +126,8 @@ def ssd_chunk_cumsum_state(shape, x, Bm, dt, A, dA_cumsum=None, dt_bhl=None, sta
     """ssd_chunk_cumsum then ssd_chunk_state in one call (one kernel where the
     chunk states have a head-group kernel).  Returns (dA_cumsum, dt_bhl,
     states)."""
+    if stream is not None:
+        return _on_stream(ssd_chunk_cumsum_state, locals())
     sh = _shape(shape)
     B, L, H, P, N, G, Q, nc = _dims(sh)
     io = (torch.float32, torch.bfloat16)
@@ -133,7 +148,7 @@ def ssd_chunk_cumsum_state(shape, x, Bm, dt, A, dA_cumsum=None, dt_bhl=None, sta
     _req(states, "states", (B, nc, H, N, P), io)
     lib = load_library()
     check(lib.ssd_chunk_cumsum_state(sh, _ptr(x), _ptr(Bm), _DT[x.dtype], _ptr(dt), _ptr(A), _ptr(dA_cumsum),
-                                     _ptr(dt_bhl), _ptr(states), _DT[states.dtype], _mma(mma), _stream(stream)))
+                                     _ptr(dt_bhl), _ptr(states), _DT[states.dtype], _mma(mma), _stream()))
     return dA_cumsum, dt_bhl, states
 
 
@@ -145,6 +160,8 @@ def ssd_state_passing(shape, chunk_states, dA_cumsum, initial_states=None, carri
     chunk states in fp32 or bf16 (the recurrence runs in fp32).
     ``in_place=True`` writes the carried states over ``chunk_states``, in
     their dtype."""
+    if stream is not None:
+        return _on_stream(ssd_state_passing, locals())
     sh = _shape(shape)
     B, L, H, P, N, G, Q, nc = _dims(sh)
     f32 = (torch.float32,)
@@ -164,7 +181,7 @@ def ssd_state_passing(shape, chunk_states, dA_cumsum, initial_states=None, carri
     _req(final_states, "final_states", (B, H, N, P), f32)
     lib = load_library()
     check(lib.ssd_state_passing(sh, _ptr(chunk_states), _DT[chunk_states.dtype], _ptr(carried), _DT[carried.dtype],
-                                _ptr(dA_cumsum), _ptr(initial_states), _ptr(final_states), _stream(stream)))
+                                _ptr(dA_cumsum), _ptr(initial_states), _ptr(final_states), _stream()))
     return carried, final_states
 
 
@@ -174,6 +191,8 @@ def ssd_chunk_state_passing(shape, x, Bm, dt_bhl, dA_cumsum, initial_states=None
     fp32 final states [B,H,N,P] (None when ``want_final`` is false), without
     materialising the chunk states; bit-identical to ssd_chunk_state followed
     by ssd_state_passing."""
+    if stream is not None:
+        return _on_stream(ssd_chunk_state_passing, locals())
     sh = _shape(shape)
     B, L, H, P, N, G, Q, nc = _dims(sh)
     io = (torch.float32, torch.bfloat16)
@@ -195,13 +214,15 @@ def ssd_chunk_state_passing(shape, x, Bm, dt_bhl, dA_cumsum, initial_states=None
     lib = load_library()
     check(lib.ssd_chunk_state_passing(sh, _ptr(x), _ptr(Bm), _DT[x.dtype], _ptr(dt_bhl), _ptr(dA_cumsum),
                                       _ptr(initial_states), _ptr(carried), _DT[carried.dtype],
-                                      _ptr(final_states), _mma(mma), _stream(stream)))
+                                      _ptr(final_states), _mma(mma), _stream()))
     return carried, final_states
 
 
 def ssd_chunk_scan(shape, x, Bm, Cm, dt_bhl, dA_cumsum, carried, D, y=None, y_dtype=None, mma="bf16",
                    stream=None):
     """y [B,L,H,P] in ``y_dtype`` (default: x's dtype)."""
+    if stream is not None:
+        return _on_stream(ssd_chunk_scan, locals())
     sh = _shape(shape)
     B, L, H, P, N, G, Q, nc = _dims(sh)
     io = (torch.float32, torch.bfloat16)
@@ -220,7 +241,7 @@ def ssd_chunk_scan(shape, x, Bm, Cm, dt_bhl, dA_cumsum, carried, D, y=None, y_dt
     lib = load_library()
     check(lib.ssd_chunk_scan(sh, _ptr(x), _ptr(Bm), _ptr(Cm), _DT[x.dtype], _ptr(dt_bhl), _ptr(dA_cumsum),
                              _ptr(carried), _DT[carried.dtype], _ptr(D), _ptr(y), _DT[y.dtype], _mma(mma),
-                             _stream(stream)))
+                             _stream()))
     return y
 
 
@@ -228,6 +249,8 @@ def ssd_decode_step(x, dt, A, Bm, Cm, D, state, y=None, y_dtype=None, stream=Non
     """One token per sequence: ``state`` [B,H,N,P] fp32 is advanced in place,
     returns y [B,H,P] in ``y_dtype`` (default: x's dtype).  x [B,H,P], dt
     [B,H], A [H], Bm/Cm [B,G,N] (x's dtype), D [H]."""
+    if stream is not None:
+        return _on_stream(ssd_decode_step, locals())
     if x.dim() != 3 or Bm.dim() != 3 or state.dim() != 4:
         raise ValueError("x must be [B,H,P], Bm/Cm [B,G,N], state [B,H,N,P]")
     B, H, P = x.shape
@@ -248,7 +271,7 @@ def ssd_decode_step(x, dt, A, Bm, Cm, D, state, y=None, y_dtype=None, stream=Non
     sh = SSDShape.make(B, 1, H, P, N, G, 1)
     lib = load_library()
     check(lib.ssd_decode_step(sh, _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _DT[x.dtype],
-                              _ptr(state), _ptr(y), _DT[y.dtype], _stream(stream)))
+                              _ptr(state), _ptr(y), _DT[y.dtype], _stream()))
     return y
 
 
@@ -263,6 +286,8 @@ def ssd_workspace_bytes_varlen(shape) -> int:
 def ssd_forward(shape, x, dt, A, Bm, Cm, D, initial_states=None, y=None, y_dtype=None, final_states=None,
                 want_final=True, workspace=None, mma="bf16", stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """One-call forward.  Returns (y, final_states or None)."""
+    if stream is not None:
+        return _on_stream(ssd_forward, locals())
     sh = _shape(shape)
     B, L, H, P, N, G, Q, nc = _dims(sh)
     io = (torch.float32, torch.bfloat16)
@@ -291,7 +316,7 @@ def ssd_forward(shape, x, dt, A, Bm, Cm, D, initial_states=None, y=None, y_dtype
         raise ValueError("workspace must be a contiguous GPU tensor")
     check(lib.ssd_forward(sh, _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _DT[x.dtype],
                           _ptr(initial_states), _ptr(y), _DT[y.dtype], _ptr(final_states), _ptr(workspace),
-                          workspace.numel() * workspace.element_size(), _mma(mma), _stream(stream)))
+                          workspace.numel() * workspace.element_size(), _mma(mma), _stream()))
     return y, final_states
 
 
@@ -301,6 +326,8 @@ def ssd_forward_noalloc(shape, x, dt, A, Bm, Cm, D, initial_states=None, y=None,
     workspace; for callers that cannot allocate).  Returns (y,
     final_states or None); y and final_states are allocated here only when
     not given."""
+    if stream is not None:
+        return _on_stream(ssd_forward_noalloc, locals())
     sh = _shape(shape)
     B, L, H, P, N, G, Q, nc = _dims(sh)
     io = (torch.float32, torch.bfloat16)
@@ -324,7 +351,7 @@ def ssd_forward_noalloc(shape, x, dt, A, Bm, Cm, D, initial_states=None, y=None,
     lib = load_library()
     check(lib.ssd_forward_noalloc(sh, _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _DT[x.dtype],
                                   _ptr(initial_states), _ptr(y), _DT[y.dtype], _ptr(final_states), _mma(mma),
-                                  _stream(stream)))
+                                  _stream()))
     return y, final_states
 
 
@@ -336,6 +363,8 @@ def ssd_forward_varlen(shape, x, dt, A, Bm, Cm, D, seq_idx, initial_states=None,
     a row.  Returns (y, final_states of each row's last sequence or None) and,
     when seq_last (int64 [nseq] flattened token indices b*L+t) is given, also
     seq_states [nseq,H,N,P]: the state after each of those tokens."""
+    if stream is not None:
+        return _on_stream(ssd_forward_varlen, locals())
     sh = _shape(shape)
     B, L, H, P, N, G, Q, nc = _dims(sh)
     io = (torch.float32, torch.bfloat16)
@@ -374,7 +403,7 @@ def ssd_forward_varlen(shape, x, dt, A, Bm, Cm, D, seq_idx, initial_states=None,
                                  _ptr(seq_idx), _ptr(initial_states), _ptr(y), _DT[y.dtype], _ptr(final_states),
                                  nseq, _ptr(seq_last if nseq else None), _ptr(seq_states if nseq else None),
                                  _ptr(workspace), workspace.numel() * workspace.element_size(), _mma(mma),
-                                 _stream(stream)))
+                                 _stream()))
     if seq_last is not None:
         return y, final_states, seq_states
     return y, final_states
@@ -387,6 +416,8 @@ def ssd_backward(shape, x, dt, A, Bm, Cm, D, dy, initial_states=None, dfinal=Non
     (None unless ``want_dinitial``), written into the tensors of ``out`` (a
     dict with those keys) where given.  ``mma``: "f32" (fp32 matrix operands)
     or "bf16" (bf16 operands, fp32 accumulation; faster, ~1e-2 relative)."""
+    if stream is not None:
+        return _on_stream(ssd_backward, locals())
     sh = _shape(shape)
     B, L, H, P, N, G, Q, nc = _dims(sh)
     io = (torch.float32, torch.bfloat16)
@@ -423,7 +454,7 @@ def ssd_backward(shape, x, dt, A, Bm, Cm, D, dy, initial_states=None, dfinal=Non
                            _ptr(initial_states), _ptr(dy), _DT[dy.dtype], _ptr(dfinal), _ptr(out["dx"]),
                            _ptr(out["ddt"]), _ptr(out["dA"]), _ptr(out["dB"]), _ptr(out["dC"]), _ptr(out["dD"]),
                            _ptr(out["dinitial"]), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                           _mma(mma), _stream(stream)))
+                           _mma(mma), _stream()))
     return out
 
 
@@ -508,6 +539,8 @@ def ssd_causal_conv(x, weight, bias=None, silu=True, initial_state=None, seq_idx
     [B,W-1,D] in x's dtype, oldest input first.  Returns (y, final_state or
     None), and with seq_last (see ssd_forward_varlen) also seq_states
     [nseq,W-1,D]."""
+    if stream is not None:
+        return _on_stream(ssd_causal_conv, locals())
     B, L, D = x.shape
     _req(weight, "weight", (D, weight.shape[-1]), _F32)
     W = weight.shape[1]
@@ -526,13 +559,15 @@ def ssd_causal_conv(x, weight, bias=None, silu=True, initial_state=None, seq_idx
     check(load_library().ssd_causal_conv(SSDConvShape(B, L, D, W), _ptr(x), row, _ptr(weight), _ptr(bias),
                                          _DT[x.dtype], int(silu), _ptr(initial_state), _ptr(seq_idx), _ptr(y),
                                          _ptr(final_state), nseq, _ptr(seq_last if nseq else None),
-                                         _ptr(seq_states if nseq else None), _stream(stream)))
+                                         _ptr(seq_states if nseq else None), _stream()))
     return (y, final_state) if seq_last is None else (y, final_state, seq_states)
 
 
 def ssd_causal_conv_step(x, state, weight, bias=None, silu=True, y=None, state_out=None, stream=None):
     """One token of ssd_causal_conv: x [B,D], state [B,W-1,D].  The state after
     the token goes to ``state_out`` (default: over ``state``).  Returns y."""
+    if stream is not None:
+        return _on_stream(ssd_causal_conv_step, locals())
     B, D = x.shape
     _req(weight, "weight", (D, weight.shape[-1]), _F32)
     W = weight.shape[1]
@@ -548,7 +583,7 @@ def ssd_causal_conv_step(x, state, weight, bias=None, silu=True, y=None, state_o
     _req(y, "y", (B, D), io)
     check(load_library().ssd_causal_conv_step(SSDConvShape(B, 1, D, W), _ptr(x), row, _ptr(state), _ptr(weight),
                                               _ptr(bias), _DT[x.dtype], int(silu), _ptr(state_out), _ptr(y),
-                                              _stream(stream)))
+                                              _stream()))
     return y
 
 
@@ -562,6 +597,8 @@ def ssd_causal_conv_backward(x, weight, dy, bias=None, silu=True, initial_state=
     a dict of dx (x's dtype; a given ``out["dx"]`` may be a column slice),
     dweight [D,W], dbias [D] (fp32; None without a bias) and dinitial (None
     unless ``want_dinitial``), in the tensors of ``out`` where given."""
+    if stream is not None:
+        return _on_stream(ssd_causal_conv_backward, locals())
     B, L, D = x.shape
     _req(weight, "weight", (D, weight.shape[-1]), _F32)
     W = weight.shape[1]
@@ -589,7 +626,7 @@ def ssd_causal_conv_backward(x, weight, dy, bias=None, silu=True, initial_state=
     check(lib.ssd_causal_conv_backward(sh, _ptr(x), row, _ptr(weight), _ptr(bias), _DT[x.dtype], int(silu),
                                        _ptr(initial_state), _ptr(seq_idx), _ptr(dy), _ptr(dfinal), _ptr(r["dx"]),
                                        dx_row, _ptr(r["dweight"]), _ptr(r["dbias"]), _ptr(r["dinitial"]),
-                                       _ptr(workspace), wsb, _stream(stream)))
+                                       _ptr(workspace), wsb, _stream()))
     return r
 
 
@@ -622,6 +659,8 @@ def ssd_selective_scan(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=
     [B,N,D] fp32.  dt is the raw projection; ``softplus`` makes the time step
     softplus(dt + dt_bias).  Returns (y, final_states or None), and with
     seq_last also seq_states [nseq,N,D]."""
+    if stream is not None:
+        return _on_stream(ssd_selective_scan, locals())
     sh, rows = _scan_inputs(u, dt, A, Bm, Cm, D, z, dt_bias, 2)
     B, L, Dn, N = sh.batch, sh.seqlen, sh.channels, sh.dstate
     _opt(initial_states, "initial_states", (B, N, Dn), _F32)
@@ -638,7 +677,7 @@ def ssd_selective_scan(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=
     check(lib.ssd_selective_scan(sh, rows, _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z),
                                  _ptr(dt_bias), int(softplus), _DT[u.dtype], _ptr(initial_states), _ptr(seq_idx),
                                  _ptr(y), _ptr(final_states), nseq, _ptr(seq_last if nseq else None),
-                                 _ptr(seq_states if nseq else None), _ptr(workspace), wsb, _stream(stream)))
+                                 _ptr(seq_states if nseq else None), _ptr(workspace), wsb, _stream()))
     return (y, final_states) if seq_last is None else (y, final_states, seq_states)
 
 
@@ -647,6 +686,8 @@ def ssd_selective_step(u, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, so
     """One token of ssd_selective_scan: u, dt, z [B,D], Bm, Cm [B,G,N], state
     [B,N,D] fp32.  The state after the token goes to ``state_out`` (default:
     over ``state``).  Returns y."""
+    if stream is not None:
+        return _on_stream(ssd_selective_step, locals())
     sh, rows = _scan_inputs(u, dt, A, Bm, Cm, D, z, dt_bias, 1)
     B, Dn, N = sh.batch, sh.channels, sh.dstate
     _req(state, "state", (B, N, Dn), _F32)
@@ -658,7 +699,7 @@ def ssd_selective_step(u, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, so
     _req(y, "y", (B, Dn), (u.dtype,))
     check(load_library().ssd_selective_step(sh, rows, _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D),
                                             _ptr(z), _ptr(dt_bias), int(softplus), _DT[u.dtype], _ptr(state),
-                                            _ptr(state_out), _ptr(y), _stream(stream)))
+                                            _ptr(state_out), _ptr(y), _stream()))
     return y
 
 
@@ -674,6 +715,8 @@ def ssd_selective_scan_backward(u, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=No
     (None: zero): du, ddt (with respect to the raw dt), dB, dC, dz in u's dtype
     (given ``out`` tensors may be column slices), dA, dD, ddt_bias, dinitial
     fp32; None where the input is absent, dinitial unless ``want_dinitial``."""
+    if stream is not None:
+        return _on_stream(ssd_selective_scan_backward, locals())
     sh, rows = _scan_inputs(u, dt, A, Bm, Cm, D, z, dt_bias, 2)
     B, L, Dn, N, G = sh.batch, sh.seqlen, sh.channels, sh.dstate, sh.ngroups
     io = (u.dtype,)
@@ -705,7 +748,7 @@ def ssd_selective_scan_backward(u, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=No
         _DT[u.dtype], _ptr(initial_states), _ptr(seq_idx), _ptr(dy), _ptr(dfinal),
         SSDScanRows(grow["du"], grow["ddt"], grow["dB"], grow["dC"], grow["dz"]), _ptr(r["du"]), _ptr(r["ddt"]),
         _ptr(r["dA"]), _ptr(r["dB"]), _ptr(r["dC"]), _ptr(r["dD"]), _ptr(r["dz"]), _ptr(r["ddt_bias"]),
-        _ptr(r["dinitial"]), _ptr(workspace), wsb, _stream(stream)))
+        _ptr(r["dinitial"]), _ptr(workspace), wsb, _stream()))
     return r
 
 
@@ -715,6 +758,8 @@ def ssd_layer_norm(x, weight, bias=None, residual=None, eps=1e-5, rms=False, y=N
     [D] fp32, with ``residual`` (fp32 or bf16) added first.  Returns (y in x's
     dtype, the sum in the residual's dtype or None, mean or None for rms,
     rstd): the sum (or x), mean and rstd are what the backward takes."""
+    if stream is not None:
+        return _on_stream(ssd_layer_norm, locals())
     shp = x.shape
     D, st = shp[-1], shp[:-1]
     rows = st.numel()
@@ -746,7 +791,7 @@ def ssd_layer_norm(x, weight, bias=None, residual=None, eps=1e-5, rms=False, y=N
     check(load_library().ssd_layer_norm(rows, D, _ptr(x), _DT[x.dtype], _ptr(residual),
                                         _DT[(x if residual is None else residual).dtype], _ptr(weight), _ptr(bias),
                                         float(eps), int(rms), _ptr(y), _ptr(residual_out), _ptr(mean), _ptr(rstd),
-                                        _stream(stream)))
+                                        _stream()))
     return y, residual_out, mean, rstd
 
 
@@ -761,6 +806,8 @@ def ssd_layer_norm_backward(dy, x, weight, mean, rstd, dresidual=None, rms=False
     the gradient arriving at the residual stream.  Returns a dict of dx (dy's
     dtype), dweight, dbias (fp32; None unless ``want_dbias``) and dresidual
     (dx in x's dtype, for the stream; None unless ``want_dresidual``)."""
+    if stream is not None:
+        return _on_stream(ssd_layer_norm_backward, locals())
     shp = dy.shape
     D, st = shp[-1], shp[:-1]
     rows = st.numel()
@@ -787,5 +834,5 @@ def ssd_layer_norm_backward(dy, x, weight, mean, rstd, dresidual=None, rms=False
     check(lib.ssd_layer_norm_backward(rows, D, _ptr(dy), _DT[dy.dtype], _ptr(x), _DT[x.dtype], _ptr(weight),
                                       _ptr(None if rms else mean), _ptr(rstd), int(rms), _ptr(dresidual),
                                       _ptr(r["dx"]), _ptr(r["dresidual"]), _ptr(r["dweight"]), _ptr(r["dbias"]),
-                                      _ptr(workspace), wsb, _stream(stream)))
+                                      _ptr(workspace), wsb, _stream()))
     return r
