@@ -488,8 +488,8 @@ ssd_status ssd_selective_scan_backward(const ssd_scan_shape* shape, const ssd_sc
 size_t ssd_selective_scan_backward_workspace_bytes(const ssd_scan_shape* shape);
 
 /*
- * Layer norm of `rows` dense rows of `dim` columns (dim <= 16384), with an
- * optional residual stream in front:
+ * Layer norm of `rows` dense rows of `dim` columns (rows < 2^31, dim <= 16384,
+ * else SSD_ERR_UNSUPPORTED), with an optional residual stream in front:
  *   r = x + residual, stored in residual_out (res_dtype; the stored value is
  *       normalised), or r = x without one
  *   y = (r - mean) rstd w + bias,  rstd = 1 / sqrt(mean((r - mean)^2) + eps)

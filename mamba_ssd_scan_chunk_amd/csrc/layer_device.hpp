@@ -2,9 +2,13 @@
 // the sigmoid and softplus they share.
 #pragma once
 
+#include "layer_launch.hpp"
 #include "ssd_device.hpp"
 
 namespace ssd {
+
+// The block's place in a flat_grid.
+__device__ __forceinline__ uint32_t flat_block() { return blockIdx.y * kGridX + blockIdx.x; }
 
 // Element type of activations in memory; arithmetic is always fp32.
 struct IoBF16 {

@@ -11,6 +11,14 @@ namespace ssd {
 
 int device_cu_count();
 
+// A flat grid of n < 2^32 blocks of up to 1024 threads.  A launch takes fewer
+// than 2^32 threads a dimension, so past kGridX blocks the others lie along y;
+// flat_block() in the kernel is the block's place, n and more for the last few.
+constexpr uint32_t kGridX = 1u << 21;
+inline dim3 flat_grid(int64_t n) {
+  return n <= kGridX ? dim3((unsigned)n) : dim3(kGridX, (unsigned)((n + kGridX - 1) / kGridX));
+}
+
 // ---- causal convolution ----
 struct ConvArgs {
   int64_t B, L, D;

@@ -142,8 +142,8 @@ __device__ __forceinline__ void load_param(const float* p, int c, int D, float* 
 template <class IO, class RO, int V, bool SHIFT, int NV, int TPR>
 __global__ __launch_bounds__(256) void norm_forward_kernel(NormArgs a) {
   __shared__ float red[TPR == 64 ? 1 : TPR / 64];
-  const int64_t row = TPR == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
-  if (TPR == 64 && row >= a.rows) return;
+  const int64_t row = TPR == 64 ? (int64_t)flat_block() * 4 + (threadIdx.x >> 6) : flat_block();
+  if (row >= a.rows) return;  // whole waves, or the whole block
   const int tid = TPR == 64 ? threadIdx.x & 63 : threadIdx.x;
   const int64_t r0 = row * a.D;
   const int D = (int)a.D, m = row_shift<V, SHIFT>(r0);
@@ -407,7 +407,7 @@ size_t norm_backward_ws_bytes(int64_t rows, int64_t D) {
 template <class IO, class RO, int V, bool SHIFT, int NV, int TPR>
 static hipError_t norm_fwd_go(const NormArgs& a, hipStream_t s) {
   const int64_t blocks = TPR == 64 ? (a.rows + 3) / 4 : a.rows;
-  hipLaunchKernelGGL((norm_forward_kernel<IO, RO, V, SHIFT, NV, TPR>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((norm_forward_kernel<IO, RO, V, SHIFT, NV, TPR>), flat_grid(blocks), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 template <class IO, class RO, int V, bool SHIFT, int NV, int TPR>
