@@ -442,8 +442,9 @@ size_t ssd_causal_conv_backward_workspace_bytes(const ssd_conv_shape* shape);
  * A [D,N], Dskip, dt_bias [D] fp32; Dskip, z, dt_bias optional.  y [B,L,D] in
  * `in`; initial_states, final_states [B,N,D], seq_states [nseq,N,D] fp32,
  * optional.  N (dstate) a multiple of 4 up to 256 (else SSD_ERR_UNSUPPORTED).
- * At most 32767 batches of 65535 * 16 tokens (else SSD_ERR_UNSUPPORTED).  Row
- * strides: `rows` NULL = all dense.  Workspace: device memory of
+ * At most 32767 batches of 65535 * 16 tokens, and fewer than 2^26 runs of up to
+ * 64 channels of one group (else SSD_ERR_UNSUPPORTED).  Row strides: `rows`
+ * NULL = all dense.  Workspace: device memory of
  * ssd_selective_scan_workspace_bytes(shape) bytes, never 0 for a valid shape.
  */
 typedef struct {

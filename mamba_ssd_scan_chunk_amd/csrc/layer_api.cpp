@@ -91,9 +91,12 @@ ssd_status check_scan(const ssd_scan_shape* s, bool step) {
   SSD_TRY(product({s->batch, s->seqlen, s->channels}, kMaxElems));
   SSD_TRY(product({s->batch, s->seqlen, s->ngroups, s->dstate}, (int64_t(1) << 36)));
   if (row_too_long(s->seqlen, s->channels) || row_too_long(s->seqlen, s->ngroups * s->dstate)) return SSD_ERR_UNSUPPORTED;
+  // blocks of 64 threads, one a group's 64 channels, along one dimension of a launch: below 2^32 threads
+  if (s->ngroups * ((s->channels / s->ngroups - 1) / 64 + 1) >= int64_t(1) << 26) return SSD_ERR_UNSUPPORTED;
   // a block a tile of a group in 31 bits, beside the few for A and the starts
   SSD_TRY(product({s->batch, (s->seqlen - 1) / 16 + 1, s->ngroups}, int64_t(1) << 30));
-  return product({s->batch, s->dstate, s->channels}, (int64_t(1) << 38));
+  // 512 GiB of states; (dstate + 2) channels / 64 blocks in 32 bits
+  return product({s->batch, s->dstate, s->channels}, (int64_t(1) << 37));
 }
 
 ssd_status scan_rows(const ssd_scan_shape* s, const ssd_scan_rows* r, ssd_dtype in, ssd::ScanRows* o) {

@@ -40,8 +40,9 @@ __global__ __launch_bounds__(256) void scan_pack_kernel(ScanArgs a, ScanGrid g, 
   extern __shared__ float turn[];  // [N][kEntry + 1]
   const int N = (int)a.N;
   const int64_t tiles = a.B * a.G * g.ntile;
-  if (blockIdx.x < tiles) {
-    const int64_t bg = blockIdx.x / g.ntile, tile = blockIdx.x - bg * g.ntile;
+  const int64_t block = flat_block();
+  if (block < tiles) {
+    const int64_t bg = block / g.ntile, tile = block - bg * g.ntile;
     const int64_t b = bg / a.G, grp = bg - b * a.G;
     for (int e = threadIdx.x; e < kEntry * N; e += 256) {
       const int isC = e / (kScanT * N), r = e - isC * kScanT * N, tok = r / N, n = r - tok * N;
@@ -53,11 +54,11 @@ __global__ __launch_bounds__(256) void scan_pack_kernel(ScanArgs a, ScanGrid g, 
       turn[n * (kEntry + 1) + tok / kHalf * kScanT + isC * kHalf + tok % kHalf] = v;
     }
     __syncthreads();
-    float* o = ws.bc + (int64_t)blockIdx.x * N * kEntry;
+    float* o = ws.bc + block * N * kEntry;
     for (int e = threadIdx.x; e < kEntry * N; e += 256) o[e] = turn[e / kEntry * (kEntry + 1) + e % kEntry];
     return;
   }
-  const int64_t k = (blockIdx.x - tiles) * 256 + threadIdx.x, na = N * a.D;
+  const int64_t k = (block - tiles) * 256 + threadIdx.x, na = N * a.D;
   if (k < na) {
     ws.at[k] = a.A[k % a.D * N + k / a.D];
   } else if (ws.starts && k - na < a.B * g.ntile) {
@@ -74,7 +75,7 @@ __global__ __launch_bounds__(256) void scan_pack_kernel(ScanArgs a, ScanGrid g, 
 
 hipError_t launch_scan_pack(const ScanArgs& a, const ScanGrid& g, const ScanWs& ws, bool bf16, hipStream_t s) {
   const int64_t rest = a.N * a.D + (ws.starts ? a.B * g.ntile : 0);
-  const dim3 grid((unsigned)(a.B * a.G * g.ntile + (rest + 255) / 256));
+  const dim3 grid = flat_grid(a.B * a.G * g.ntile + (rest + 255) / 256);
   const size_t lds = sizeof(float) * a.N * (kEntry + 1);
   if (bf16) hipLaunchKernelGGL((scan_pack_kernel<IoBF16>), grid, dim3(256), lds, s, a, g, ws);
   else hipLaunchKernelGGL((scan_pack_kernel<IoF32>), grid, dim3(256), lds, s, a, g, ws);

@@ -396,7 +396,7 @@ template <class IO>
 __global__ __launch_bounds__(256) void scan_bc_reduce_kernel(ScanArgs a, int64_t ncb, const float* __restrict__ part) {
   typedef typename IO::type T;
   const int64_t GN = a.G * a.N, n = a.B * a.L * GN;
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t idx = (int64_t)flat_block() * 256 + threadIdx.x;
   if (idx >= 2 * n) return;
   const bool c = idx >= n;
   const int64_t e = c ? idx - n : idx;
@@ -423,7 +423,7 @@ __global__ __launch_bounds__(kColsumThreads) void scan_param_kernel(const float*
                                                                     int64_t N, float* __restrict__ dA,
                                                                     float* __restrict__ dD, float* __restrict__ db) {
   __shared__ float lds[kColsumThreads];
-  int64_t c = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+  int64_t c = (int64_t)flat_block() * 64 + (threadIdx.x & 63);
   const bool ok = c < (N + 2) * D;
   if (!ok) c = (N + 2) * D - 1;
   const bool isA = c < N * D;
@@ -508,10 +508,10 @@ static hipError_t scan_backward_t(const ScanArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((scan_bwd_chunk_kernel<IO, PACKED>), grid, block, lds3, s, a, g, ws, bw);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int64_t nbc = 2 * a.B * a.L * a.G * a.N;
-  hipLaunchKernelGGL((scan_bc_reduce_kernel<IO>), dim3((unsigned)((nbc + 255) / 256)), dim3(256), 0, s, a, g.ncb, bw.bc);
+  hipLaunchKernelGGL((scan_bc_reduce_kernel<IO>), flat_grid((nbc + 255) / 256), dim3(256), 0, s, a, g.ncb, bw.bc);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int64_t np = (a.N + 2) * a.D;
-  hipLaunchKernelGGL(scan_param_kernel, dim3((unsigned)((np + 63) / 64)), dim3(kColsumThreads), 0, s, ws.adj, bw.dDb,
+  hipLaunchKernelGGL(scan_param_kernel, flat_grid((np + 63) / 64), dim3(kColsumThreads), 0, s, ws.adj, bw.dDb,
                      a.B * g.nc, a.D, a.N, a.dA, a.dD, a.ddt_bias);
   return hipGetLastError();
 }

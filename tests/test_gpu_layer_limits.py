@@ -36,3 +36,60 @@ def test_norm_of_more_rows_than_a_launch_has_threads(D):
             assert rms or torch.equal(mean[s], part[2])
         assert torch.isfinite(y).all()
         del y, mean, rstd
+
+
+def test_scan_parameter_sums_past_a_launch_of_threads():
+    """(N + 2) D columns of 16 threads each, 2^28 of them and more are 2^32
+    threads; channels do not depend on each other, so the far ones' gradients
+    equal a call on them alone bit for bit."""
+    D, N, B = 2 ** 26 + 64, 4, 2
+    say(f"scan gradients of {D} channels")
+    f = lambda *s: torch.randn(s, device="cuda")
+    u, dt, dy, z = (f(B, 1, D) for _ in range(4))
+    A, Ds, bias, Bm, Cm, h0 = -torch.rand((D, N), device="cuda"), f(D), f(D), f(B, 1, 1, N), f(B, 1, 1, N), f(B, N, D)
+    g = ops.ssd_selective_scan_backward(u, dt, A, Bm, Cm, dy, D=Ds, z=z, dt_bias=bias, initial_states=h0,
+                                        want_dinitial=True)
+    for s in (slice(0, 128), slice(D // 2, D // 2 + 128), slice(D - 192, D)):
+        c = lambda v: v[..., s].contiguous()
+        p = ops.ssd_selective_scan_backward(c(u), c(dt), A[s].contiguous(), Bm, Cm, c(dy), D=c(Ds), z=c(z),
+                                            dt_bias=c(bias), initial_states=c(h0), want_dinitial=True)
+        torch.cuda.synchronize()
+        for n in ("du", "ddt", "dz", "dD", "ddt_bias", "dinitial"):
+            assert torch.equal(g[n][..., s], p[n]), n
+        assert torch.equal(g["dA"][s], p["dA"])
+
+
+def test_scan_of_more_tiles_than_a_launch_has_threads():
+    """A block of 256 threads a tile of a group, and a thread an entry of dB and
+    dC: 2^24 tiles and 2^32 entries.  Every batch holds the same row, so every
+    batch's results are the first one's bit for bit; that one's are those of a
+    call of its own but for the order of what is carried over chunks (fp32
+    roundings of sums below 100: 1e-4) and one rounding to bf16 (a step at
+    most: 2^-7)."""
+    B, L, D, N, G = 17, 65535 * 16, 16, 8, 16
+    say(f"scan of {B * G * L // 16} tiles")
+    row = lambda *s: _bf(1, L, *s)
+    one = dict(u=row(D), dt=row(D), Bm=row(G, N), Cm=row(G, N))
+    dy1 = row(D)
+    A, b = -0.5 - torch.rand((D, N), device="cuda"), torch.zeros(D, device="cuda")
+    rep = lambda v: v.repeat((B,) + (1,) * (v.dim() - 1))
+    many, dy = {k: rep(v) for k, v in one.items()}, rep(dy1)
+
+    def same(name, whole, alone):
+        for i in range(1, B):
+            assert torch.equal(whole[i], whole[0]), (name, i)
+        a, c = whole[0].float(), alone[0].float()
+        assert ((a - c).abs() <= 2.0 ** -7 * c.abs() + 1e-4).all(), name
+
+    y, fin = ops.ssd_selective_scan(**many, A=A, dt_bias=b)
+    y1, fin1 = ops.ssd_selective_scan(**one, A=A, dt_bias=b)
+    torch.cuda.synchronize()
+    same("y", y, y1)
+    same("final", fin, fin1)
+    del y, fin
+    say("  gradients")
+    g = ops.ssd_selective_scan_backward(**many, A=A, dt_bias=b, dy=dy)
+    g1 = ops.ssd_selective_scan_backward(**one, A=A, dt_bias=b, dy=dy1)
+    torch.cuda.synchronize()
+    for n in ("du", "ddt", "dB", "dC"):
+        same(n, g[n], g1[n])

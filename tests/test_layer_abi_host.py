@@ -304,3 +304,14 @@ def test_rows_beyond_32_bit_offsets(lib):
         assert fwd(lib, s=scan_shape(seqlen=1), rows=SSDScanRows(*rows), nseq=-1) == SHAPE, k
     s = SSDConvShape(2, 100, 64, 4)
     assert lib.ssd_causal_conv_backward(s, F, 0, F, F, 1, 1, None, None, F, None, F, far, F, F, None, F, BIG, None) == UNSUP
+
+
+def test_scan_channel_runs(lib):
+    """A block of 64 threads a run of up to 64 channels of one group, along one
+    dimension of a launch: fewer than 2^26 of them, in the queries too."""
+    for groups, there in ((1 << 26, False), ((1 << 26) - 1, True)):
+        s = scan_shape(batch=1, seqlen=1, channels=groups, dstate=4, ngroups=groups)
+        assert (lib.ssd_selective_scan_workspace_bytes(s) > 0) == there
+        assert (lib.ssd_selective_scan_backward_workspace_bytes(s) > 0) == there
+        assert fwd(lib, s, y=None) == (NULL if there else UNSUP)
+        assert lib.ssd_selective_step(s, None, *scan_args(GOOD), F, F, None, None) == (NULL if there else UNSUP)
