@@ -31,7 +31,7 @@ constexpr int kConvBwdBatch = 4;  // and backward, of two inputs
 
 // The wave's run of tokens and its lane's channels.
 struct ConvRun {
-  int64_t rb, b, t0, t1;
+  int64_t group, rb, b, t0, t1;  // the block's runs are those of a group
   int64_t d0, d;  // first channel of the wave, and of the lane
   bool live;      // the run exists
   bool ok;        // the lane has channels (one without repeats the last ones')
@@ -40,13 +40,15 @@ template <int V>
 __device__ __forceinline__ ConvRun conv_run_of(const ConvArgs& a, int64_t nrun, int run, int64_t ncb) {
   ConvRun r;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  r.rb = (int64_t)(blockIdx.x / (unsigned)ncb) * kConvWaves + wave;
+  const uint32_t block = flat_block();
+  r.group = block / (unsigned)ncb;
+  r.rb = r.group * kConvWaves + wave;
   r.live = r.rb < a.B * nrun;
   const int64_t rb = r.live ? r.rb : 0;
   r.b = rb / nrun;
   r.t0 = (rb - r.b * nrun) * run;
   r.t1 = r.t0 + run < a.L ? r.t0 + run : a.L;
-  r.d0 = (int64_t)(blockIdx.x % (unsigned)ncb) * 64 * V;
+  r.d0 = (int64_t)(block % (unsigned)ncb) * 64 * V;
   r.d = r.d0 + (threadIdx.x & 63) * V;
   r.ok = r.d < a.D;
   if (!r.ok) r.d = a.D - V;
@@ -305,24 +307,24 @@ __global__ __launch_bounds__(kConvThreads) void conv_forward_kernel(ConvArgs a, 
 template <class IO, int W>
 __global__ __launch_bounds__(kConvThreads) void conv_seq_states_kernel(ConvArgs a) {
   typedef typename IO::type T;
-  const int64_t d = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
   const int64_t s = blockIdx.y;
-  if (d >= a.D) return;
   const int64_t tok = a.seq_last[s];
   if (tok < 0 || tok >= a.B * a.L) return;
   const int64_t b = tok / a.L, t = tok % a.L;
-  const T* xr = static_cast<const T*>(a.x) + b * a.L * a.x_row + d;
   const int* sr = a.seq_idx ? a.seq_idx + b * a.L : nullptr;
-  T* o = static_cast<T*>(a.seq_states) + s * (W - 1) * a.D + d;
-  bool same = true;
+  for (int64_t d = (int64_t)blockIdx.x * kConvThreads + threadIdx.x; d < a.D; d += (int64_t)gridDim.x * kConvThreads) {
+    const T* xr = static_cast<const T*>(a.x) + b * a.L * a.x_row + d;
+    T* o = static_cast<T*>(a.seq_states) + s * (W - 1) * a.D + d;
+    bool same = true;
 #pragma unroll
-  for (int k = W - 2; k >= 0; --k) {
-    const int64_t j = t - (W - 2) + k;
-    if (sr && j + 1 > 0 && j + 1 <= t && sr[j + 1] != sr[j < 0 ? 0 : j]) same = false;
-    T v = IO::put(0.f);
-    if (same && j >= 0) v = xr[j * a.x_row];
-    else if (same && a.init) v = static_cast<const T*>(a.init)[(b * (W - 1) + j + W - 1) * a.D + d];
-    o[k * a.D] = v;
+    for (int k = W - 2; k >= 0; --k) {
+      const int64_t j = t - (W - 2) + k;
+      if (sr && j + 1 > 0 && j + 1 <= t && sr[j + 1] != sr[j < 0 ? 0 : j]) same = false;
+      T v = IO::put(0.f);
+      if (same && j >= 0) v = xr[j * a.x_row];
+      else if (same && a.init) v = static_cast<const T*>(a.init)[(b * (W - 1) + j + W - 1) * a.D + d];
+      o[k * a.D] = v;
+    }
   }
 }
 
@@ -344,6 +346,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_backward_kernel(ConvArgs a,
   static_assert(NB >= W - 1, "only a run's first batch reaches inputs before the run");
   __shared__ float part[kConvWaves][(W + 1) * V][64];
   const ConvRun r = conv_run_of<V>(a, nrun, run, ncb);
+  if (r.group * kConvWaves >= a.B * nrun) return;  // a block past the last one
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float dw[W][V], db[V];
 #pragma unroll
@@ -537,7 +540,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_backward_kernel(ConvArgs a,
   __syncthreads();
   // partial sums of the block's runs: ws[row group][W+1][D]
   if (r.ok) {
-    float* ws = a.ws + (int64_t)(blockIdx.x / (unsigned)ncb) * (W + 1) * a.D + r.d;
+    float* ws = a.ws + r.group * (W + 1) * a.D + r.d;
     for (int k = wave; k <= W; k += kConvWaves) {
       float s[V];
 #pragma unroll
@@ -556,7 +559,7 @@ template <int W>
 __global__ __launch_bounds__(kColsumThreads) void conv_param_kernel(const float* __restrict__ part, int64_t R, int64_t D,
                                                                     float* __restrict__ dw, float* __restrict__ db) {
   __shared__ float lds[kColsumThreads];
-  const int64_t c = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63), C = (W + 1) * D;
+  const int64_t c = (int64_t)flat_block() * 64 + (threadIdx.x & 63), C = (W + 1) * D;
   const float s = column_sum(part + (c < C ? c : C - 1), R, C, lds);
   if (threadIdx.x >= 64 || c >= C) return;
   const int64_t k = c / D, d = c - k * D;
@@ -570,7 +573,7 @@ template <class IO, int V, int W, bool SILU>
 __global__ __launch_bounds__(kConvThreads) void conv_step_kernel(ConvArgs a, const typename IO::type* state,
                                                                  typename IO::type* state_out, int64_t total) {
   typedef typename IO::type T;
-  const int64_t idx = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
+  const int64_t idx = (int64_t)flat_block() * kConvThreads + threadIdx.x;
   if (idx >= total) return;
   const int64_t Dv = a.D / V;
   const int64_t d = (idx % Dv) * V, b = idx / Dv;
@@ -630,13 +633,13 @@ constexpr int kConvFwdRun = 16, kConvBwdRun = 32;
 template <class IO, int V, int W, bool PACKED>
 static hipError_t conv_forward_v(const ConvArgs& a, hipStream_t s) {
   const ConvGrid g = conv_grid(a.B, a.L, a.D, V, kConvFwdRun);
-  const dim3 grid((unsigned)(g.groups * g.ncb));
+  const dim3 grid = flat_grid(g.groups * g.ncb);
   auto kern = a.silu ? conv_forward_kernel<IO, V, W, PACKED, true> : conv_forward_kernel<IO, V, W, PACKED, false>;
   hipLaunchKernelGGL(kern, grid, dim3(kConvThreads), 0, s, a, g.nrun, g.run, g.ncb);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.nseq == 0) return e;
   hipLaunchKernelGGL((conv_seq_states_kernel<IO, W>),
-                     dim3((unsigned)((a.D + kConvThreads - 1) / kConvThreads), (unsigned)a.nseq), dim3(kConvThreads), 0,
+                     dim3(flat_grid((a.D + kConvThreads - 1) / kConvThreads).x, (unsigned)a.nseq), dim3(kConvThreads), 0,
                      s, a);
   return hipGetLastError();
 }
@@ -644,12 +647,12 @@ static hipError_t conv_forward_v(const ConvArgs& a, hipStream_t s) {
 template <class IO, int V, int W, bool PACKED>
 static hipError_t conv_backward_v(const ConvArgs& a, hipStream_t s) {
   const ConvGrid g = conv_grid(a.B, a.L, a.D, V, kConvBwdRun);
-  const dim3 grid((unsigned)(g.groups * g.ncb));
+  const dim3 grid = flat_grid(g.groups * g.ncb);
   auto kern = a.silu ? conv_backward_kernel<IO, V, W, PACKED, true> : conv_backward_kernel<IO, V, W, PACKED, false>;
   hipLaunchKernelGGL(kern, grid, dim3(kConvThreads), 0, s, a, g.nrun, g.run, g.ncb);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((conv_param_kernel<W>), dim3((unsigned)(((W + 1) * a.D + 63) / 64)), dim3(kColsumThreads), 0, s,
+  hipLaunchKernelGGL((conv_param_kernel<W>), flat_grid(((W + 1) * a.D + 63) / 64), dim3(kColsumThreads), 0, s,
                      a.ws, g.groups, a.D, a.dw, a.dbias);
   return hipGetLastError();
 }
@@ -665,7 +668,7 @@ template <class IO, int V, int W>
 static hipError_t conv_step_v(const ConvArgs& a, const void* st, void* so, hipStream_t s) {
   typedef typename IO::type T;
   const int64_t total = a.B * (a.D / V);
-  const dim3 grid((unsigned)((total + kConvThreads - 1) / kConvThreads));
+  const dim3 grid = flat_grid((total + kConvThreads - 1) / kConvThreads);
   if (a.silu)
     hipLaunchKernelGGL((conv_step_kernel<IO, V, W, true>), grid, dim3(kConvThreads), 0, s, a,
                        static_cast<const T*>(st), static_cast<T*>(so), total);

@@ -58,6 +58,7 @@ ssd_status check_conv(const ssd_conv_shape* s, bool step) {
   if (s->width < 2 || s->width > 4) return SSD_ERR_UNSUPPORTED;
   SSD_TRY(product({s->batch, s->seqlen, s->channels}, kMaxElems));
   if (row_too_long(s->seqlen, s->channels)) return SSD_ERR_UNSUPPORTED;
+  SSD_TRY(product({s->channels, s->width + 1}, int64_t(1) << 37));  // 512 GiB of partial sums
   // waves (64 channels and at least 8 tokens each) in 31 bits
   return product({s->batch, (s->seqlen - 1) / 8 + 1, (s->channels - 1) / 64 + 1}, k31 - 1);
 }

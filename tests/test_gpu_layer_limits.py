@@ -93,3 +93,71 @@ def test_scan_of_more_tiles_than_a_launch_has_threads():
     torch.cuda.synchronize()
     for n in ("du", "ddt", "dB", "dC"):
         same(n, g[n], g1[n])
+
+
+def test_conv_of_more_runs_than_a_launch_has_threads():
+    """2^24 groups of runs of 256 threads each: runs of 16 tokens forward, of 32
+    backward.  The tokens at the row's end equal a call on them alone, with the
+    inputs before them as its initial state, bit for bit; dy is zero but there,
+    so the sums over tokens are its too, but for their order (256 terms of at
+    most 1.1 |dy x| each, and a tree: 300 roundings)."""
+    L, D, W, tail = 2 ** 31 + 1000, 4, 4, 256
+    say(f"convolution of {L} tokens")
+    x = _bf(1, L, D)
+    w, b = torch.randn((D, W), device="cuda"), torch.randn(D, device="cuda")
+    xt, init = x[:, -tail:].clone(), x[:, -tail - W + 1:-tail].clone()
+    half = x[:, :2 ** 30 + 500]
+    y, fin = ops.ssd_causal_conv(half.contiguous(), w, b, want_final=True)
+    ht, hi = half[:, -tail:].clone(), half[:, -tail - W + 1:-tail].clone()
+    part = ops.ssd_causal_conv(ht, w, b, initial_state=hi, want_final=True)
+    torch.cuda.synchronize()
+    assert torch.equal(y[:, -tail:], part[0]) and torch.equal(fin, part[1])
+    del y, half
+    say("  gradients")
+    dy = torch.zeros_like(x)
+    dy[:, -tail:] = _bf(1, tail, D)
+    g = ops.ssd_causal_conv_backward(x, w, dy, b)
+    p = ops.ssd_causal_conv_backward(xt, w, dy[:, -tail:].contiguous(), b, initial_state=init, want_dinitial=True)
+    torch.cuda.synchronize()
+    assert torch.equal(g["dx"][:, -tail:], p["dx"])
+    assert torch.equal(g["dx"][:, -tail - W + 1:-tail], p["dinitial"])
+    assert not g["dx"][:, :-tail - W + 1].any()
+    size = 1.1 * dy[:, -tail:].float().abs().sum((0, 1)) * max(1.0, x[:, -tail - W:].float().abs().max().item())
+    assert ((g["dbias"] - p["dbias"]).abs() <= 300 * 2.0 ** -24 * size).all()
+    assert ((g["dweight"] - p["dweight"]).abs() <= 300 * 2.0 ** -24 * size[:, None]).all()
+
+
+def test_conv_of_more_channels_than_a_launch_has_threads():
+    """Single tokens of very many channels: the states' and the parameters'
+    kernels, and the step's threads past 2^32; the far channels equal a call on
+    them alone bit for bit."""
+    D, W = 2 ** 29 + 64, 2
+    say(f"convolution of {D} channels")
+    x, dy, init = _bf(1, 1, D), _bf(1, 1, D), _bf(1, W - 1, D)
+    w, b = torch.randn((D, W), device="cuda"), torch.randn(D, device="cuda")
+    last = torch.tensor([0], device="cuda")
+    y, fin, sst = ops.ssd_causal_conv(x, w, b, initial_state=init, want_final=True, seq_last=last)
+    g = ops.ssd_causal_conv_backward(x, w, dy, b, initial_state=init, want_dinitial=True)
+    for s in (slice(0, 128), slice(D // 2, D // 2 + 128), slice(D - 192, D)):
+        c = lambda v: v[..., s].contiguous()
+        p = ops.ssd_causal_conv(c(x), w[s].contiguous(), c(b), initial_state=c(init), want_final=True, seq_last=last)
+        q = ops.ssd_causal_conv_backward(c(x), w[s].contiguous(), c(dy), c(b), initial_state=c(init),
+                                         want_dinitial=True)
+        torch.cuda.synchronize()
+        assert all(torch.equal(v[..., s], t) for v, t in zip((y, fin, sst), p))
+        assert all(torch.equal(g[n][..., s], q[n]) for n in ("dx", "dbias", "dinitial"))
+        assert torch.equal(g["dweight"][s], q["dweight"])
+    del y, fin, sst, g, x, dy, init, w, b
+    B, D = 17, 2 ** 28 + 1
+    say(f"  step of {B} x {D}")
+    x, st = _bf(B, D), _bf(B, W - 1, D)
+    w, b = torch.randn((D, W), device="cuda"), torch.randn(D, device="cuda")
+    so = torch.empty_like(st)
+    y = ops.ssd_causal_conv_step(x, st, w, b, state_out=so)
+    assert torch.equal(so[:, 0], x)
+    for s in (slice(0, 128), slice(D - 129, D)):
+        o = torch.empty((B, W - 1, s.stop - s.start), device="cuda", dtype=torch.bfloat16)
+        p = ops.ssd_causal_conv_step(x[:, s].contiguous(), st[..., s].contiguous(), w[s].contiguous(),
+                                     b[s].contiguous(), state_out=o)
+        torch.cuda.synchronize()
+        assert torch.equal(y[:, s], p)
