@@ -112,11 +112,11 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(4, 4))) void
   const float bias = a.dt_bias ? a.dt_bias[d] * kLog2e : 0.f;
   const float skip = a.D_skip ? a.D_skip[d] : 0.f;
   const int64_t row0 = k.b * a.L;
-  const int off = (int)(d * sizeof(T));
-  const T* up = static_cast<const T*>(a.u) + row0 * a.rows.u;
-  const T* dp = static_cast<const T*>(a.dt) + row0 * a.rows.dt;
-  const T* zp = a.z ? static_cast<const T*>(a.z) + row0 * a.rows.z : nullptr;
-  T* yp = FINAL ? static_cast<T*>(a.y) + row0 * a.D : nullptr;
+  const int off = (int)((d - k.d0) * sizeof(T));
+  const T* up = static_cast<const T*>(a.u) + row0 * a.rows.u + k.d0;
+  const T* dp = static_cast<const T*>(a.dt) + row0 * a.rows.dt + k.d0;
+  const T* zp = a.z ? static_cast<const T*>(a.z) + row0 * a.rows.z + k.d0 : nullptr;
+  T* yp = FINAL ? static_cast<T*>(a.y) + row0 * a.D + k.d0 : nullptr;
   BCPair<FINAL> cur;
   cur.load(ep);
   float a_n = as[0], h_n = hs[0];

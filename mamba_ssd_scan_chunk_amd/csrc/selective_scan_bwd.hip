@@ -30,17 +30,18 @@ struct BwdWs {
   float* dDb;    // [B nc][2][D] dD, then ddt_bias
 };
 
-// One row of the batch (b) of each input; lanes add their channel.
+// One row of the batch (b) of each input, from the wave's first channel on;
+// lanes add their own.
 template <class IO>
 struct RowPtrs {
   typedef typename IO::type T;
   const T *u, *dt, *z, *dy;
-  __device__ __forceinline__ RowPtrs(const ScanArgs& a, int64_t b) {
+  __device__ __forceinline__ RowPtrs(const ScanArgs& a, int64_t b, int64_t d0) {
     const int64_t r = b * a.L;
-    u = static_cast<const T*>(a.u) + r * a.rows.u;
-    dt = static_cast<const T*>(a.dt) + r * a.rows.dt;
-    z = a.z ? static_cast<const T*>(a.z) + r * a.rows.z : nullptr;
-    dy = static_cast<const T*>(a.dy) + r * a.D;
+    u = static_cast<const T*>(a.u) + r * a.rows.u + d0;
+    dt = static_cast<const T*>(a.dt) + r * a.rows.dt + d0;
+    z = a.z ? static_cast<const T*>(a.z) + r * a.rows.z + d0 : nullptr;
+    dy = static_cast<const T*>(a.dy) + r * a.D + d0;
   }
 };
 
@@ -75,8 +76,8 @@ __global__ __launch_bounds__(64) void scan_bwd_local_kernel(ScanArgs a, ScanGrid
   for (int n = 0; n < N; ++n) hs[n * 64] = gs[n * 64] = 0.f;
   if (h_in) rows_to_lds(hs, h_in + d, a.D, N);
   const float bias = a.dt_bias ? a.dt_bias[d] * kLog2e : 0.f;
-  const RowPtrs<IO> p(a, k.b);
-  const int off = (int)(d * sizeof(typename IO::type));
+  const RowPtrs<IO> p(a, k.b, k.d0);
+  const int off = (int)((d - k.d0) * sizeof(typename IO::type));
   const float* atp = ws.at + d;
   BCPair<true> e;
   e.load(ep);
@@ -220,8 +221,8 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(2, 2))) void
   for (int n = 0; n < N; ++n) as[n * 64] = 0.f;
   const float bias = a.dt_bias ? a.dt_bias[d] * kLog2e : 0.f;
   const float skip = a.D_skip ? a.D_skip[d] : 0.f;
-  const RowPtrs<IO> p(a, k.b);
-  const int off = (int)(d * sizeof(typename IO::type));
+  const RowPtrs<IO> p(a, k.b, k.d0);
+  const int off = (int)((d - k.d0) * sizeof(typename IO::type));
   const float* atp = ws.at + d;
   const bool whole = k.d0 + 64 <= k.dend;
   float dDsum = 0.f, dbsum = 0.f;
@@ -376,9 +377,9 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(2, 2))) void
       for (int i = 0; i < kScanT; ++i) y[i] *= rg.at(i) * dsilu(rz.at(i), sigmoid(rz.at(i)));
     }
     if (ok) {
-      store_tile<IO>(static_cast<T*>(a.du) + r0 * a.grows.u, a.grows.u, t0, nt, off, sB);
-      store_tile<IO>(static_cast<T*>(a.ddt) + r0 * a.grows.dt, a.grows.dt, t0, nt, off, sA);
-      if (p.z) store_tile<IO>(static_cast<T*>(a.dz) + r0 * a.grows.z, a.grows.z, t0, nt, off, y);
+      store_tile<IO>(static_cast<T*>(a.du) + r0 * a.grows.u + k.d0, a.grows.u, t0, nt, off, sB);
+      store_tile<IO>(static_cast<T*>(a.ddt) + r0 * a.grows.dt + k.d0, a.grows.dt, t0, nt, off, sA);
+      if (p.z) store_tile<IO>(static_cast<T*>(a.dz) + r0 * a.grows.z + k.d0, a.grows.z, t0, nt, off, y);
     }
   }
   if (ok) {

@@ -161,3 +161,43 @@ def test_conv_of_more_channels_than_a_launch_has_threads():
                                      b[s].contiguous(), state_out=o)
         torch.cuda.synchronize()
         assert torch.equal(y[:, s], p)
+
+
+def test_scan_of_more_channels_than_a_lane_offset_holds():
+    """One token of 2^29 fp32 channels and more, whose byte offsets pass 2^31:
+    the far channels equal a call on them alone bit for bit; all but the first
+    and last 256 add nothing to dB and dC, which are then a call's on those but
+    for the sums' order (512 terms: 600 roundings of their sizes' sum)."""
+    D, N = 2 ** 29 + 4096, 4
+    say(f"scan of {D} channels")
+    ends = [slice(0, 256), slice(D - 256, D)]
+
+    def thin():
+        v = torch.zeros((1, 1, D), device="cuda")
+        for s in ends:
+            v[..., s] = torch.randn((1, 1, 256), device="cuda")
+        return v
+
+    u, dy = thin(), thin()
+    dt = torch.randn((1, 1, D), device="cuda")
+    A, Bm, Cm = -torch.rand((D, N), device="cuda"), *(torch.randn((1, 1, 1, N), device="cuda") for _ in range(2))
+    cut = lambda v: torch.cat([v[..., s] for s in ends], -1)
+    Ac = torch.cat([A[s] for s in ends]).contiguous()
+    small = (cut(u), cut(dt), Ac, Bm, Cm)
+    y, fin = ops.ssd_selective_scan(u, dt, A, Bm, Cm)
+    yp, finp = ops.ssd_selective_scan(*small)
+    torch.cuda.synchronize()
+    assert torch.equal(cut(y), yp) and torch.equal(cut(fin), finp)
+    del y, fin
+    say("  gradients")
+    g = ops.ssd_selective_scan_backward(u, dt, A, Bm, Cm, dy)
+    p = ops.ssd_selective_scan_backward(*small, cut(dy))
+    torch.cuda.synchronize()
+    assert torch.equal(cut(g["du"]), p["du"]) and torch.equal(cut(g["ddt"]), p["ddt"])
+    assert torch.equal(torch.cat([g["dA"][s] for s in ends]), p["dA"])
+    step = torch.nn.functional.softplus(cut(dt))
+    x, gy = (step * cut(u)).abs().flatten(), cut(dy).abs().flatten()
+    # one token from a zero state: h = B x, dB = sum C dy x, dC = sum h dy
+    for n, other in (("dB", Cm), ("dC", Bm)):
+        size = (other.abs().flatten()[:, None] * gy * x).sum(1)
+        assert ((g[n] - p[n]).flatten().abs() <= 600 * 2.0 ** -24 * size).all(), n
