@@ -382,8 +382,11 @@ size_t ssd_backward_workspace_bytes(const ssd_shape* shape);
  * other at L rows.  Such arguments need only be aligned to their element, Bm
  * and Cm to 4 bytes (with row strides in whole 4-byte units); everything else
  * to 16 bytes.  Of rows longer than one token the stride (given or dense) is
- * below 2^25 elements (else SSD_ERR_UNSUPPORTED).  Optional arguments may be NULL.  A gradient asked for by a
- * pointer is written whole.  Results do not depend on timing (no atomics).
+ * below 2^25 elements (else SSD_ERR_UNSUPPORTED).  Optional arguments may be
+ * NULL.  A gradient asked for by a pointer is written whole.  Outputs overlap
+ * no input and no other output, except where a call says so (a prompt's final
+ * state in its initial state's place is refused: SSD_ERR_UNSUPPORTED).
+ * Results do not depend on timing (no atomics).
  *
  * Packed sequences as in ssd_forward_varlen: seq_idx [B,L] (optional) names
  * each token's sequence, and wherever it changes along a row the recurrence

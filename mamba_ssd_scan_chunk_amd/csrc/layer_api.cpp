@@ -72,6 +72,12 @@ ssd::ConvArgs conv_args(const ssd_conv_shape* s) {
   return a;
 }
 
+// The state after a row goes to memory of its own: other blocks still read the
+// one before it.
+ssd_status check_states(const void* initial, const void* final) {
+  return final && final == initial ? SSD_ERR_UNSUPPORTED : SSD_OK;
+}
+
 ssd_status check_seq_list(int64_t nseq, const int64_t* last, const void* states) {
   if (nseq < 0) return SSD_ERR_SHAPE;
   if (nseq > 65535) return SSD_ERR_UNSUPPORTED;
@@ -165,6 +171,7 @@ ssd_status ssd_causal_conv(const ssd_conv_shape* shape, const void* x, int64_t x
   if (!aligned(x, elem(in)) || !a16(w) || !a16(bias) || !a16(initial_state) || !a16(seq_idx) || !a16(y) ||
       !a16(final_state))
     return SSD_ERR_ALIGN;
+  SSD_TRY(check_states(initial_state, final_state));
   a.silu = silu != 0;
   a.x = x;
   a.w = w;
@@ -251,6 +258,7 @@ ssd_status ssd_selective_scan(const ssd_scan_shape* shape, const ssd_scan_rows* 
   const size_t need = ssd_selective_scan_workspace_bytes(shape);
   if (need > 0 && (!workspace || workspace_bytes < need)) return SSD_ERR_WORKSPACE;
   if (!a16(initial_states) || !a16(seq_idx) || !a16(y) || !a16(final_states) || !a16(workspace)) return SSD_ERR_ALIGN;
+  SSD_TRY(check_states(initial_states, final_states));
   a.seq_idx = seq_idx;
   a.h0 = initial_states;
   a.y = y;

@@ -511,6 +511,11 @@ def _opt(t: Optional[torch.Tensor], name: str, shape, dtypes) -> None:
         _req(t, name, shape, dtypes)
 
 
+def _own_memory(final, initial, name: str) -> None:
+    if final is not None and initial is not None and final.data_ptr() == initial.data_ptr():
+        raise ValueError(f"{name} must not be the initial state's memory: the call reads it to its end")
+
+
 def _workspace(workspace, query, query_args, device):
     """The given workspace, or a new one of the queried size; and its bytes."""
     if workspace is None:
@@ -555,6 +560,7 @@ def ssd_causal_conv(x, weight, bias=None, silu=True, initial_state=None, seq_idx
     if final_state is None and want_final:
         final_state = x.new_empty((B, W - 1, D))
     _opt(final_state, "final_state", (B, W - 1, D), io)
+    _own_memory(final_state, initial_state, "final_state")
     nseq, seq_states = _seq_states(seq_last, seq_states, (W - 1, D), x.dtype, x.device)
     check(load_library().ssd_causal_conv(SSDConvShape(B, L, D, W), _ptr(x), row, _ptr(weight), _ptr(bias),
                                          _DT[x.dtype], int(silu), _ptr(initial_state), _ptr(seq_idx), _ptr(y),
@@ -671,6 +677,7 @@ def ssd_selective_scan(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=
     if final_states is None and want_final:
         final_states = A.new_empty((B, N, Dn))
     _opt(final_states, "final_states", (B, N, Dn), _F32)
+    _own_memory(final_states, initial_states, "final_states")
     nseq, seq_states = _seq_states(seq_last, seq_states, (N, Dn), torch.float32, u.device)
     lib = load_library()
     workspace, wsb = _workspace(workspace, lib.ssd_selective_scan_workspace_bytes, (sh,), u.device)

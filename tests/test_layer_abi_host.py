@@ -315,3 +315,16 @@ def test_scan_channel_runs(lib):
         assert (lib.ssd_selective_scan_backward_workspace_bytes(s) > 0) == there
         assert fwd(lib, s, y=None) == (NULL if there else UNSUP)
         assert lib.ssd_selective_step(s, None, *scan_args(GOOD), F, F, None, None) == (NULL if there else UNSUP)
+
+
+def test_final_state_in_the_initial_states_place(lib):
+    """Other blocks read the initial state while the last one writes the final
+    one: refused, by the binding too; steps take one state for both."""
+    assert conv(lib, init=F, fin=F) == UNSUP
+    assert fwd(lib, h0=F, fin=F) == UNSUP
+    a, b = torch.zeros(4), torch.zeros(4)
+    ops._own_memory(a, b, "final_state")
+    ops._own_memory(None, b, "final_state")
+    ops._own_memory(a, None, "final_state")
+    with pytest.raises(ValueError, match="final_state"):
+        ops._own_memory(a, a.view(2, 2), "final_state")
