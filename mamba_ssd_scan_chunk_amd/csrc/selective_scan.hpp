@@ -97,11 +97,6 @@ struct Touch {
   __device__ __forceinline__ void entries(const float* p, int N, int lane) {
     v = p[(lane < N ? lane : N - 1) * kEntry];
   }
-  // both ends of the 64 channels (the first, and `last` after it) in N rows of
-  // D, the first 32 rows
-  __device__ __forceinline__ void rows(const float* p, int64_t D, int last, int N, int lane) {
-    v = p[(lane < 2 * N ? lane >> 1 : N - 1) * D + (lane & 1) * last];
-  }
   __device__ __forceinline__ void settle() { asm volatile("" : : "v"(v)); }
 };
 
