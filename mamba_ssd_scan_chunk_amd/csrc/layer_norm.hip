@@ -16,12 +16,13 @@
 // elements a load.  Rows that are not whole groups of 4 begin anywhere in one:
 // in bf16 their threads take the groups as memory has them, the first beginning
 // up to 3 columns before the row and the last ending after it (4866 rows of
-// 1669 columns: 51 us an element a load, 21 so; gradients 57 and 32).
+// 1669 columns, bf16 with bf16 residual: 51 us an element a load, 20 so).
 // Backward: 64, 256 or 1024 threads a row, 16 values a thread at most, so that
 // the five values a column (x, dy, w, dw, dbias) leave room for waves beside;
 // blocks walk rows, the next row's loads in flight behind the sums of this
 // one, and keep dw and dbias of their columns in registers (walking in steps
-// of 4 rows, they find the same columns in each).  The blocks' partial sums are
+// of 4 rows, they find the same columns in each also where rows begin inside
+// groups).  The blocks' partial sums are
 // added in a fixed order.
 #include <type_traits>
 
@@ -60,8 +61,9 @@ __device__ __forceinline__ bool in_row(int c, int e, int D) {
 }
 // V elements at column c, zeros outside the row, held as loaded until they are
 // widened: widened in the branch that loads them each group would be waited
-// for before the next is asked for (4866 rows of 1669 columns, bf16: 26 us,
-// 21 so; gradients of 16384 x 2560 142 and 124).  Groups over a row's ends hold elements of its neighbours, all
+// for before the next is asked for (4866 rows of 1669 columns, bf16 with bf16
+// residual: 26 us, 20 so; gradients of 16384 x 2560, bf16 with fp32 residual,
+// 142 and 124).  Groups over a row's ends hold elements of its neighbours, all
 // within the `total` elements but for the last row's.  (Loads of groups past the
 // row made unconditional, to leave no branches, cost more in traffic than they
 // saved.)
@@ -314,20 +316,17 @@ __global__ __launch_bounds__(norm_bwd_threads(TPR)) void norm_backward_kernel(No
   // a row of partial sums a block: ws[block][2][D]; with four waves a block
   // they meet first
   if constexpr (TPR == 64) {
+    static_assert(!SHIFT, "the waves of a block share their columns");
     constexpr int P = 64 * NV * V;
-    // a lane's values side by side with the other lanes'; by column where the
-    // waves' columns differ (those outside the row stay unused)
-    auto place = [&](int j, int e) { return SHIFT ? col(j) + e : (j * V + e) * 64 + tid; };
-    auto used = [&](int j, int e) { return !SHIFT || in_row<SHIFT>(col(j), e, D); };
+    // a lane's values side by side with the other lanes'
+    auto place = [&](int j, int e) { return (j * V + e) * 64 + tid; };
     if (wave > 0) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          if (used(j, e)) {
-            part[((wave - 1) * 2) * P + place(j, e)] = dw[j][e];
-            part[((wave - 1) * 2 + 1) * P + place(j, e)] = db[j][e];
-          }
+          part[((wave - 1) * 2) * P + place(j, e)] = dw[j][e];
+          part[((wave - 1) * 2 + 1) * P + place(j, e)] = db[j][e];
         }
     }
     __syncthreads();
@@ -338,10 +337,8 @@ __global__ __launch_bounds__(norm_bwd_threads(TPR)) void norm_backward_kernel(No
       for (int e = 0; e < V; ++e) {
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-          if (used(j, e)) {
-            dw[j][e] += part[(k * 2) * P + place(j, e)];
-            db[j][e] += part[(k * 2 + 1) * P + place(j, e)];
-          }
+          dw[j][e] += part[(k * 2) * P + place(j, e)];
+          db[j][e] += part[(k * 2 + 1) * P + place(j, e)];
         }
       }
   }
@@ -449,25 +446,33 @@ template <class IO, class RO, int V, bool SHIFT>
 static hipError_t norm_fwd_rows(const NormArgs& a, hipStream_t s) {
   return norm_cover(a.D) <= 64 * 64 ? norm_fwd_nv<IO, RO, V, SHIFT, 64>(a, s) : norm_fwd_nv<IO, RO, V, SHIFT, 256>(a, s);
 }
-template <class IO, class RO, int V, bool SHIFT>
+template <class IO, class RO, int V>
 static hipError_t norm_bwd_rows(const NormArgs& a, hipStream_t s) {
   switch (norm_bwd_tpr(a.D)) {
-    case 64: return norm_bwd_nv<IO, RO, V, SHIFT, 64>(a, s);
-    case 256: return norm_bwd_nv<IO, RO, V, SHIFT, 256>(a, s);
-    default: return norm_bwd_nv<IO, RO, V, SHIFT, 1024>(a, s);
+    case 64: return norm_bwd_nv<IO, RO, V, false, 64>(a, s);
+    case 256: return norm_bwd_nv<IO, RO, V, false, 256>(a, s);
+    default: return norm_bwd_nv<IO, RO, V, false, 1024>(a, s);
   }
 }
 
-// Rows that are not whole groups: shifted groups where a type is bf16, whose
-// single elements make loads of half a line a wave; single elements in fp32
-// (4096 rows of 5001 columns forward: 67 us, in groups 79; 3000 of 733
-// backward: 16 and 20).
+// Rows that are not whole groups.  Forward: shifted groups where a type is
+// bf16, single elements in fp32 (bf16 without residual 11753 x 1021 14 us,
+// single elements 23; fp32 with residual 11753 x 1021 38, groups 45; bf16 rows of
+// 61 and fp32 ones past 2048 columns would be the other way: 72 and 49, 4692 x
+// 2557 51 and 43).  Gradients, whose five values a column weigh more than the
+// loads: single elements (bf16 without residual 7189 x 1669 31 us, groups 36;
+// bf16 with fp32 residual 196721 x 61 142 and 269, 999 x 12001 59 and 96) but
+// for the longest bf16 rows (732 x 16382 bf16 residual 115 and 93; fp32
+// residual 99 and 144).
 template <class IO, class RO, bool BWD>
 static hipError_t norm_types(const NormArgs& a, hipStream_t s) {
   constexpr bool bf16 = IO::kVec == 8 || RO::kVec == 8;
   if constexpr (BWD) {
-    if (a.D % 4 == 0) return norm_bwd_rows<IO, RO, 4, false>(a, s);
-    return norm_bwd_rows<IO, RO, bf16 ? 4 : 1, bf16>(a, s);
+    if (a.D % 4 == 0) return norm_bwd_rows<IO, RO, 4>(a, s);
+    if constexpr (bf16) {
+      if (a.D > 12 * 1024) return norm_bwd_nv<IO, RO, 4, true, 1024>(a, s);
+    }
+    return norm_bwd_rows<IO, RO, 1>(a, s);
   } else {
     if (a.D % 8 == 0) return norm_fwd_rows<IO, RO, 8, false>(a, s);
     if (a.D % 4 == 0) return norm_fwd_rows<IO, RO, 4, false>(a, s);
