@@ -420,7 +420,12 @@ static hipError_t norm_bwd_go(const NormArgs& a, hipStream_t s) {
 }
 
 // Values a thread holds: NV groups of V (the loads past a short row are
-// skipped).  16383 columns, the one length that its shift takes over the most
+// skipped).  Fewer than a row's most leave registers for more waves: forward
+// 40 beside 64 (16384 x 2557, bf16 with fp32 residual 109 us, 64 131; 16000 x
+// 2557 fp32 150 and 199; whole groups do not mind, 16384 x 2560 99 and 96), 16
+// (40960 x 1024 bf16 31 us, 64 46), 8 (262144 x 128 135, 64 280); backward 12
+// (3400 x 12288 137 us, 16 158; no difference with fewer threads a row).
+// 16383 columns, the one length that its shift takes over the most
 // that 16384 need, get a group more.
 template <class IO, class RO, int V, bool SHIFT, int TPR>
 static hipError_t norm_fwd_nv(const NormArgs& a, hipStream_t s) {

@@ -19,8 +19,8 @@
 // pass takes every chunk's state from zero, a second carries the states from
 // chunk to chunk (decays multiply as exp of the summed dt), and the last
 // computes the outputs from the carried states.  2 x 8192 tokens of 5120
-// channels and 16 states, bf16, gated: 492 us, the ALUs issuing throughout;
-// 65536 tokens of 1024 channels: 418.
+// channels and 16 states, bf16, gated: 491 us, of which the two passes' instructions come to
+// 461 at the rates measured for them; 65536 tokens of 1024 channels: 418.
 #include "layer_device.hpp"
 #include "layer_launch.hpp"
 #include "selective_scan.hpp"
@@ -84,7 +84,8 @@ hipError_t launch_scan_pack(const ScanArgs& a, const ScanGrid& g, const ScanWs& 
 
 // State passes: FINAL writes outputs from the chunk's entering state, else
 // only the state the chunk leaves and its summed dt.  Four waves a SIMD, which
-// the compiler would give up for a register (164 of them: 563 -> 593 us).
+// the compiler would give up for a register (164 of them: 563 -> 593 us); the
+// packed last pass spills 9 registers for them (fp32 12).
 template <class IO, bool PACKED, bool FINAL>
 __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(4, 4))) void scan_chunk_kernel(ScanArgs a, ScanGrid g, ScanWs ws) {
   typedef typename IO::type T;

@@ -17,8 +17,8 @@
 // at every 16th token) and swept backwards.  The sums over channels go through
 // LDS, 16 tokens of one state at a time; the channel blocks' partial sums are
 // then added in order.  No atomics: results do not depend on timing.  2 x 2048
-// tokens of 5120 channels and 16 states, bf16, gated: 425 us, 300 of them the
-// third pass and 115 the first, bound by the vector ALUs.
+// tokens of 5120 channels and 16 states, bf16, gated: 425 us, 306 of them the
+// third pass and 116 the first, bound by the vector ALUs.
 #include "layer_device.hpp"
 #include "layer_launch.hpp"
 #include "selective_scan.hpp"
@@ -191,8 +191,8 @@ __device__ __forceinline__ float lane_sums(const float* red, int lane) {
 // Pass 3, two waves a SIMD: six values a token in registers beside the state's
 // own leave no room for a third (forced to three the compiler spills: 792 us;
 // tiles of 8 tokens at three waves read and write twice the states and take as
-// long over most shapes).  300 us at 2 x 2048 tokens of 5120 channels and 16
-// states, the vector ALUs busy for 71% of it.  LDS of a wave: the adjoint
+// long over most shapes).  306 us at 2 x 2048 tokens of 5120 channels and 16
+// states, the vector ALUs busy for 72% of it.  LDS of a wave: the adjoint
 // riding backwards and the summed dA, per state and lane, and the values being
 // summed over lanes, dC's beside dB's: one wait for both sums, behind the sweep.
 template <class IO, bool PACKED>
