@@ -521,6 +521,57 @@ ssd_status ssd_layer_norm_backward(int64_t rows, int64_t dim, const void* dy, ss
                                    void* workspace, size_t workspace_bytes, void* stream);
 size_t ssd_layer_norm_backward_workspace_bytes(int64_t rows, int64_t dim);
 
+/* ------------------------------------------------------------------------
+ * The gated delta rule: a scan whose state is corrected towards each value
+ * instead of only added to.  The pages name none of this; it follows from its
+ * formulas.  Conventions of the layer's operators above, with the differences
+ * stated here.
+ *
+ * Per batch b, head h (key group g = h / (H/G)), with
+ *   step  = softplus(dt[b,t,h] + dt_bias[h])   (SSD_DELTA_SOFTPLUS; else without)
+ *   a_t   = exp(step A[h])                     (A negative: a decay)
+ *   w_t   = 1 / (1 + exp(-beta[b,t,h]))        (SSD_DELTA_SIGMOID; else beta itself)
+ *   k_t, q_t = their rows of group g, over sqrt(sum of squares + 1e-6)
+ *              (SSD_DELTA_QK_NORM; else as they are), q_t times scale
+ * the state h (N x P) and the outputs are
+ *   u_t = w_t (v_t - k_t^T (a_t h_{t-1})),  h_t = a_t h_{t-1} + k_t u_t^T,  y_t = q_t^T h_t
+ * q, k rows [G,N], v rows [H,P], dt, beta rows [H], all `in`; A, dt_bias [H]
+ * fp32, dt_bias optional.  y [B,L,H,P] in `in`; initial_states, final_states
+ * [B,H,N,P], seq_states [nseq,H,N,P] fp32, optional.  N (dstate) and P
+ * (headdim) multiples of 16 up to 256, B H < 2^22, B H ceil(L/64) < 2^24 (else
+ * SSD_ERR_UNSUPPORTED).  q and k of prompts are 16-byte aligned with row
+ * strides in whole 16 bytes.  final_states may be initial_states.
+ *
+ * Precision: fp32 inputs use fp32 matrix instructions.  bf16 inputs enter the
+ * products as they are; computed operands (states, u, the triangular matrices
+ * of a window of 64 tokens) enter as the sum of two bf16 values, 16 bits;
+ * sums and states are fp32.  fp32 outputs of bf16 inputs are so within 1e-5 of
+ * their values (2-norm), bf16 ones one rounding.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int64_t batch, seqlen, nheads, headdim, dstate, ngroups;
+} ssd_delta_shape;
+typedef struct {
+  int64_t q, k, v, dt, beta; /* elements from a token to the next; 0 = dense */
+} ssd_delta_rows;
+#define SSD_DELTA_SOFTPLUS 1
+#define SSD_DELTA_SIGMOID 2
+#define SSD_DELTA_QK_NORM 4
+
+ssd_status ssd_delta_rule(const ssd_delta_shape* shape, const ssd_delta_rows* rows, const void* q, const void* k,
+                          const void* v, const void* dt, const void* beta, const float* A, const float* dt_bias,
+                          int flags, float scale, ssd_dtype in, const float* initial_states, const int32_t* seq_idx,
+                          void* y, float* final_states, int64_t nseq, const int64_t* seq_last, float* seq_states,
+                          void* workspace, size_t workspace_bytes, void* stream);
+size_t ssd_delta_rule_workspace_bytes(const ssd_delta_shape* shape);
+
+/* One token (seqlen 1): state [B,H,N,P] fp32 is read, the state after the
+ * token is written to state_out (which may be state itself). */
+ssd_status ssd_delta_step(const ssd_delta_shape* shape, const ssd_delta_rows* rows, const void* q, const void* k,
+                          const void* v, const void* dt, const void* beta, const float* A, const float* dt_bias,
+                          int flags, float scale, ssd_dtype in, const float* state, float* state_out, void* y,
+                          void* stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char* ssd_status_string(ssd_status status);
 

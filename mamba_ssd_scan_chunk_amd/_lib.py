@@ -51,12 +51,26 @@ class SSDScanRows(ctypes.Structure):
                 ("z", ctypes.c_int64)]
 
 
+class SSDDeltaShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int64),
+                ("headdim", ctypes.c_int64), ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64)]
+
+
+class SSDDeltaRows(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_int64), ("k", ctypes.c_int64), ("v", ctypes.c_int64), ("dt", ctypes.c_int64),
+                ("beta", ctypes.c_int64)]
+
+
+SSD_DELTA_SOFTPLUS, SSD_DELTA_SIGMOID, SSD_DELTA_QK_NORM = 1, 2, 4
+
 _P = ctypes.c_void_p
 _S = ctypes.POINTER(SSDShape)
 _E = ctypes.c_int  # enums
 _I, _F, _Z = ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _CS, _SS, _SR = ctypes.POINTER(SSDConvShape), ctypes.POINTER(SSDScanShape), ctypes.POINTER(SSDScanRows)
 _SCAN_IN = [_SS, _SR, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int, _E]  # shape .. in
+_DS, _DR = ctypes.POINTER(SSDDeltaShape), ctypes.POINTER(SSDDeltaRows)
+_DELTA_IN = [_DS, _DR, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int, _F, _E]  # shape .. in
 
 _SIGNATURES = {
     "ssd_chunk_cumsum": (ctypes.c_int, [_S, _P, _P, _P, _P, _P]),
@@ -89,6 +103,9 @@ _SIGNATURES = {
     "ssd_layer_norm_backward": (ctypes.c_int, [_I, _I, _P, _E, _P, _E, _P, _P, _P, ctypes.c_int, _P, _P, _P, _P, _P, _P,
                                                _Z, _P]),
     "ssd_layer_norm_backward_workspace_bytes": (_Z, [_I, _I]),
+    "ssd_delta_rule": (ctypes.c_int, _DELTA_IN + [_P, _P, _P, _P, _I, _P, _P, _P, _Z, _P]),
+    "ssd_delta_rule_workspace_bytes": (_Z, [_DS]),
+    "ssd_delta_step": (ctypes.c_int, _DELTA_IN + [_P, _P, _P, _P]),
     "ssd_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "ssd_abi_version": (ctypes.c_int, []),
 }

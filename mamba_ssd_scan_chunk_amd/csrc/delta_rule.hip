@@ -1,0 +1,655 @@
+// delta_rule.hip -- the gated delta rule: prompts and single tokens.  The
+// formulas and the operands' types are in delta_rule.hpp.
+//
+// A prompt takes two launches.  delta_prepare_kernel, one block a (window,
+// head), leaves what needs no state: the triangular operands R and P, laid out
+// as the chain's fragments, and the scalars of the rows.  delta_chain_kernel
+// walks the windows in order.  A wave owns 16 value columns of a head, whose
+// state it holds in accumulators, and nothing passes between waves: every
+// product of the chain contracts over what are rows of the one before (state
+// rows, tokens), and an accumulator's rows are the contraction slots of the
+// next operand.  Only k, q (from LDS, shared by a block's waves), R and P
+// (from the workspace) are read as left operands.
+#include "delta_rule.hpp"
+
+namespace ssd {
+
+// ---------------------------------------------------------------- preparation
+constexpr int kTP = kC + 4;  // pitch of the 64 x 64 fp32 tiles in LDS
+constexpr int kMP = 20;      // of a 16 x 16 one
+constexpr int kPrepLds = 4 * kC * kTP * 4 + 4 * 16 * kMP * 4 + kC * 8 + 5 * kC * 4;
+
+__device__ __forceinline__ f32x4_t mma4(const float4& a, const f32x4_t& b, f32x4_t c) {
+  c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.x, b[0], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.y, b[1], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.z, b[2], c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(a.w, b[3], c, 0, 0, 0);
+}
+
+// Four waves.  Wave i takes rows 16 i .. of the Gram products, then column
+// block i of R: with T = I + E diag(b) in blocks of 16,
+//     R_ij = T_ii^-1 (-E_ij - sum_{j <= k < i} (E b)_ik R_kj),  T_ii^-1 = I + R_ii diag(b),
+// the diagonal blocks by substitution, a lane a column, the others by fp32
+// matrix instructions.  Entries between pieces are set, not multiplied, to
+// zero, so that no value of one sequence meets another's.
+template <class M, bool BACK>
+__global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaWs ws) {
+  typedef typename M::IO::type T;
+  extern __shared__ __align__(16) char lds[];
+  float(*E)[kTP] = reinterpret_cast<float(*)[kTP]>(lds);
+  float(*Eb)[kTP] = E + kC;
+  float(*Pm)[kTP] = Eb + kC;
+  float(*R)[kTP] = Pm + kC;
+  float(*Md)[16][kMP] = reinterpret_cast<float(*)[16][kMP]>(R + kC);
+  double* sG = reinterpret_cast<double*>(Md + 4);
+  float* sBeta = reinterpret_cast<float*>(sG + kC);
+  float* sIn = sBeta + kC;
+  float* sOut = sIn + kC;
+  float* sRk = sOut + kC;
+  float* sRq = sRk + kC;
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int64_t bid = near_block(blockIdx.x, gridDim.x);
+  const int64_t h = bid % a.H, win = bid / a.H % ws.nw, b = bid / a.H / ws.nw;
+  const int64_t row = b * a.L, t0 = win * kC, bhw = (b * a.H + h) * ws.nw + win;
+  const int64_t grp = h / (a.H / a.G);
+  const int n = (int)(a.L - t0 < kC ? a.L - t0 : kC);
+  const uint8_t* marks = !BACK && a.nseq > 0 ? reinterpret_cast<const uint8_t*>(a.ws + ws.marks) : nullptr;
+  const uint64_t cuts = a.seq_idx || marks ? window_cuts(a.seq_idx, marks, row, t0, a.L, lane).piece : 0;
+  DeltaGates* gates = reinterpret_cast<DeltaGates*>(a.ws + ws.gates) + bhw;
+
+  if (wave == 0) {
+    const bool in = lane < n;
+    float gv = 0.f, beta = 0.f;
+    if (in) {
+      const int64_t t = row + t0 + lane;
+      float raw = M::IO::get(static_cast<const T*>(a.dt)[t * a.rows.dt + h]);
+      if (a.dt_bias) raw += a.dt_bias[h];
+      const float step = a.softplus ? softplus2(raw * kLog2e) * kLn2 : raw;
+      gv = step * a.A[h];
+      if (gv < -1e5f) gv = -1e5f;  // e^gv is 0 well before; sums stay finite
+      beta = M::IO::get(static_cast<const T*>(a.beta)[t * a.rows.beta + h]);
+      if (a.sigmoid) beta = sigmoid(beta);
+    }
+    const int begin = piece_begin(cuts, lane + 1);
+    const int end = piece_end(cuts, begin, n);
+    // sums in 64 bits: differences of far tokens keep all of an exponent's bits
+    double G = gv;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const double o = __shfl_up(G, off, 64);
+      if (lane - off >= begin) G += o;
+    }
+    const double last = __shfl(G, end - 1, 64);
+    sG[lane] = G;
+    sBeta[lane] = beta;
+    sIn[lane] = in ? expf((float)G) : 0.f;
+    sOut[lane] = in ? expf((float)(last - G)) : 0.f;
+  }
+  // Gram tiles of rows 16 wave ..
+  f32x4_t kk[4], qk[4], qq = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) kk[j] = qk[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const T* kbase = static_cast<const T*>(a.k) + (row + t0) * a.rows.k + grp * a.N;
+  const T* qbase = static_cast<const T*>(a.q) + (row + t0) * a.rows.q + grp * a.N;
+  for (int s = 0; s * 32 < (int)a.N; ++s) {
+    const int col = 32 * s + 8 * g;
+    auto load = [&](const T* base, int64_t stride, int tile) {
+      const int t = 16 * tile + c;
+      return t < n && col < (int)a.N ? M::global8(base + t * stride + col) : M::zero();
+    };
+    const typename M::One ka = load(kbase, a.rows.k, wave), qa = load(qbase, a.rows.q, wave);
+    qq = M::mma(qa, qa, qq);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j > wave) continue;
+      const typename M::One kb = j == wave ? ka : load(kbase, a.rows.k, j);
+      kk[j] = M::mma(ka, kb, kk[j]);
+      qk[j] = M::mma(qa, kb, qk[j]);
+    }
+  }
+  // lengths from the diagonals
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if (c != 4 * g + r) continue;
+    float k2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k2 = j == wave ? kk[j][r] : k2;
+    sRk[16 * wave + c] = a.qk_norm ? 1.f / sqrtf(k2 + kQkEps) : 1.f;
+    sRq[16 * wave + c] = (a.qk_norm ? 1.f / sqrtf(qq[r] + kQkEps) : 1.f) * a.scale;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int s = 16 * j + c;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 16 * wave + 4 * g + r;
+      float e = 0.f, eb = 0.f, p = 0.f;
+      if (j <= wave && s <= t && t < n && piece_of(cuts, t) == piece_of(cuts, s)) {
+        const float rel = expf((float)(sG[t] - sG[s])) * sRk[s];
+        p = rel * sRq[t] * qk[j][r];
+        if (s < t) {
+          e = rel * sRk[t] * kk[j][r];
+          eb = e * sBeta[s];
+        }
+      }
+      E[t][s] = e;
+      Eb[t][s] = eb;
+      Pm[t][s] = p;
+      if (j > wave) R[t][s] = 0.f;
+    }
+  }
+  if (wave == 0) {
+    const float in = sIn[lane];
+    gates->beta[lane] = sBeta[lane];
+    gates->kin[lane] = in * sRk[lane];
+    gates->qin[lane] = in * sRq[lane];
+    gates->kout[lane] = sOut[lane] * sRk[lane];
+    gates->in[lane] = in;
+    gates->rk[lane] = sRk[lane];
+    gates->rq[lane] = sRq[lane];
+    gates->G[lane] = sG[lane];
+  }
+  __syncthreads();
+  {
+    const int o = 16 * wave;
+    float r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float v = -E[o + i][o + c];
+#pragma unroll
+      for (int k = 0; k < i; ++k) v = fmaf(-Eb[o + i][o + k], r[k], v);
+      r[i] = c < i && piece_of(cuts, o + i) == piece_of(cuts, o + c) ? v : 0.f;
+    }
+    if (g == 0) {
+      const float beta = sBeta[o + c];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const bool on = c < i && piece_of(cuts, o + i) == piece_of(cuts, o + c);
+        R[o + i][o + c] = r[i];
+        Md[wave][i][c] = i == c ? 1.f : on ? r[i] * beta : 0.f;
+      }
+    }
+  }
+  __syncthreads();
+  {
+    f32x4_t col[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < wave) continue;
+      if (i == wave) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) col[i][r] = R[16 * i + 4 * g + r][16 * wave + c];
+        continue;
+      }
+      f32x4_t acc;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[r] = -E[16 * i + 4 * g + r][16 * wave + c];
+#pragma unroll
+      for (int k = 0; k < i; ++k) {
+        if (k < wave) continue;
+        float4 m = *reinterpret_cast<const float4*>(&Eb[16 * i + c][16 * k + 4 * g]);
+        m = make_float4(-m.x, -m.y, -m.z, -m.w);
+        acc = mma4(m, col[k], acc);
+      }
+      const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+      col[i] = mma4(*reinterpret_cast<const float4*>(&Md[i][c][4 * g]), acc, zero);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 16 * i + 4 * g + r;
+        R[t][16 * wave + c] = piece_of(cuts, t) == piece_of(cuts, 16 * wave + c) ? col[i][r] : 0.f;
+      }
+    }
+  }
+  __syncthreads();
+  // fragments: lane (c, g), slots 4t + r, column (of the contraction) 32 s + 16 t + 4 g + r
+  char* low_r = a.ws + ws.low_r + bhw * kTriBytes;
+  auto put_low = [&](char* base, float(*m)[kTP], int f) {
+    const int i = f < 2 ? f : 2 + (f - 2) / 2, s = f < 2 ? 0 : (f - 2) % 2;
+    const float* p = &m[16 * i + c][32 * s + 4 * g];
+    const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 16);
+    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    M::store(base + f * 2048, lane, M::two(v));
+  };
+  for (int f = wave; f < kTriFrags; f += 4) put_low(low_r, R, f);
+  if constexpr (!BACK) {
+    char* low_p = a.ws + ws.low_p + bhw * kTriBytes;
+    for (int f = 3 - wave; f < kTriFrags; f += 4) put_low(low_p, Pm, f);
+  } else {
+    char* up_r = a.ws + ws.up_r + bhw * kTriBytes;
+    char* up_p = a.ws + ws.up_p + bhw * kTriBytes;
+    for (int f = wave; f < 2 * kTriFrags; f += 4) {
+      const bool pm = f >= kTriFrags;
+      const int u = pm ? f - kTriFrags : f;
+      const int i = u < 4 ? u / 2 : u - 2, s = u < 4 ? u % 2 : 1;
+      float(*m)[kTP] = pm ? Pm : R;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = m[32 * s + 16 * (e / 4) + 4 * g + e % 4][16 * i + c];
+      M::store((pm ? up_p : up_r) + u * 2048, lane, M::two(v));
+    }
+  }
+}
+
+// ---------------------------------------------------------------- marks of the tokens whose state is asked for
+__global__ __launch_bounds__(256) void delta_marks_clear_kernel(uint8_t* marks, int64_t n) {
+  const int64_t i = (int64_t)flat_block() * 256 + threadIdx.x;
+  if (i < n) marks[i] = 0;
+}
+__global__ __launch_bounds__(256) void delta_marks_kernel(uint8_t* marks, int64_t n, const int64_t* last, int64_t nseq) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < nseq && last[i] >= 0 && last[i] < n) marks[last[i]] = 1;
+}
+
+// ---------------------------------------------------------------- the chain
+template <class M, int NP>
+constexpr int chain_pitch() { return NP + 16 / (int)sizeof(typename M::IO::type); }
+template <class M, int NP, bool SAVE>
+constexpr size_t chain_lds() {
+  return (size_t)(SAVE ? 1 : 2) * kC * chain_pitch<M, NP>() * sizeof(typename M::IO::type) + 5 * kC * 4;
+}
+
+// Eight slots of two accumulator tiles.
+__device__ __forceinline__ void slots(const f32x4_t& lo, const f32x4_t& hi, float* o) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    o[r] = lo[r];
+    o[4 + r] = hi[r];
+  }
+}
+
+// SAVE: for the gradients, the state in front of every window and w instead of y.
+template <class M, int NP, bool VL, bool SAVE>
+__global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs ws) {
+  typedef typename M::IO::type T;
+  typedef typename M::Two Two;
+  constexpr int NT = NP / 16, KS = NP / 32, LP = chain_pitch<M, NP>(), V = M::IO::kVec;
+  extern __shared__ __align__(16) char lds[];
+  T* kt = reinterpret_cast<T*>(lds);
+  T* qt = kt + (SAVE ? 0 : kC * LP);
+  float* gt = reinterpret_cast<float*>(qt + kC * LP);
+  const float *sBeta = gt, *sKin = gt + kC, *sQin = gt + 2 * kC, *sKout = gt + 3 * kC, *sIn = gt + 4 * kC;
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int nthr = blockDim.x, c = lane & 15, g = lane >> 4;
+  const uint32_t bid = near_block(blockIdx.x, gridDim.x);
+  const uint32_t slices = (uint32_t)(a.P / 16) / (nthr / 64);
+  const int64_t bh = bid / slices, h = bh % a.H, b = bh / a.H, grp = h / (a.H / a.G);
+  const int64_t p = ((bid % slices) * (nthr / 64) + wave) * 16 + c;
+  const int N = (int)a.N;
+  const int64_t row = b * a.L;
+  const uint8_t* marks = !SAVE && a.nseq > 0 ? reinterpret_cast<const uint8_t*>(a.ws + ws.marks) : nullptr;
+
+  f32x4_t S[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int nn = 16 * j + 4 * g + r;
+      S[j][r] = a.h0 && nn < N ? a.h0[(bh * N + nn) * a.P + p] : 0.f;
+    }
+
+  for (int64_t win = 0; win < ws.nw; ++win) {
+    const int64_t t0 = win * kC, bhw = bh * ws.nw + win;
+    const int n = (int)(a.L - t0 < kC ? a.L - t0 : kC);
+    Cuts cuts = {0, 0};
+    if constexpr (VL) {
+      cuts = window_cuts(a.seq_idx, marks, row, t0, a.L, lane);
+      if (cuts.fresh & 1) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) S[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
+    }
+    if constexpr (SAVE) {
+      float* out = reinterpret_cast<float*>(a.ws + ws.S) + bhw * N * a.P + p;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int nn = 16 * j + 4 * g + r;
+          if (nn < N) out[nn * a.P] = S[j][r];
+        }
+    }
+    const char* fr = a.ws + ws.low_r + bhw * kTriBytes;
+    const char* fp = a.ws + ws.low_p + bhw * kTriBytes;
+    int begin = 0;
+    while (begin < n) {
+      const int end = VL ? piece_end(cuts.piece, begin, n) : n;
+      if (VL && begin > 0 && (cuts.fresh >> begin & 1)) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) S[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
+      // rows of other pieces are zero
+      __syncthreads();
+      for (int i = tid; i < kC * (NP / V); i += nthr) {
+        const int t = i / (NP / V), col = i % (NP / V) * V;
+        uint4 kv = make_uint4(0, 0, 0, 0), qv = kv;
+        if (t >= begin && t < end && col < N) {
+          kv = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.k) + (row + t0 + t) * a.rows.k + grp * N + col);
+          if (!SAVE)
+            qv = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (row + t0 + t) * a.rows.q + grp * N + col);
+        }
+        *reinterpret_cast<uint4*>(kt + t * LP + col) = kv;
+        if (!SAVE) *reinterpret_cast<uint4*>(qt + t * LP + col) = qv;
+      }
+      const float* gsrc = reinterpret_cast<const float*>(reinterpret_cast<const DeltaGates*>(a.ws + ws.gates) + bhw);
+      for (int i = tid; i < 5 * kC; i += nthr) gt[i] = i % kC >= begin && i % kC < end ? gsrc[i] : 0.f;
+      __syncthreads();
+
+      f32x4_t X[4], Q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) X[i] = Q[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        float v[8];
+        slots(S[2 * s], S[2 * s + 1], v);
+        const Two sb = M::two(v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const T* kp = kt + (16 * i + c) * LP + 32 * s + 4 * g;
+          X[i] = M::mma(lds_4x2<M>(kp, kp + 16), sb, X[i]);
+          if constexpr (!SAVE) {
+            const T* qp = qt + (16 * i + c) * LP + 32 * s + 4 * g;
+            Q[i] = M::mma(lds_4x2<M>(qp, qp + 16), sb, Q[i]);
+          }
+        }
+      }
+      // X = v - e^G k S
+      const T* vp = static_cast<const T*>(a.v) + (row + t0) * a.rows.v + h * a.P + p;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 kin = *reinterpret_cast<const float4*>(sKin + 16 * i + 4 * g);
+        const float4 qin = *reinterpret_cast<const float4*>(sQin + 16 * i + 4 * g);
+        const float ki[4] = {kin.x, kin.y, kin.z, kin.w}, qi[4] = {qin.x, qin.y, qin.z, qin.w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = 16 * i + 4 * g + r;
+          const float v = t >= begin && t < end ? M::IO::get(vp[t * a.rows.v]) : 0.f;
+          X[i][r] = v - ki[r] * X[i][r];
+          Q[i][r] *= qi[r];
+        }
+      }
+      // w = X + R (b X); u = b w
+      float be[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 q = *reinterpret_cast<const float4*>(sBeta + 16 * i + 4 * g);
+        be[i][0] = q.x; be[i][1] = q.y; be[i][2] = q.z; be[i][3] = q.w;
+      }
+      f32x4_t u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) u[i][r] = be[i][r] * X[i][r];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        float v[8];
+        slots(u[2 * s], u[2 * s + 1], v);
+        const Two xb = M::two(v);
+#pragma unroll
+        for (int i = 2 * s; i < 4; ++i) X[i] = M::mma(M::load(fr + low_frag(i, s) * 2048, lane), xb, X[i]);
+      }
+      if constexpr (SAVE) {
+        float* out = reinterpret_cast<float*>(a.ws + ws.w) + bhw * kC * a.P + p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int t = 16 * i + 4 * g + r;
+            if (t >= begin && t < end) out[t * a.P] = X[i][r];
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = 16 * i + 4 * g + r;
+          u[i][r] = !VL || (t >= begin && t < end) ? be[i][r] * X[i][r] : 0.f;
+        }
+      if constexpr (!SAVE) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          float v[8];
+          slots(u[2 * s], u[2 * s + 1], v);
+          const Two ub = M::two(v);
+#pragma unroll
+          for (int i = 2 * s; i < 4; ++i) Q[i] = M::mma(M::load(fp + low_frag(i, s) * 2048, lane), ub, Q[i]);
+        }
+        T* yp = static_cast<T*>(a.y) + ((row + t0) * a.H + h) * a.P + p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int t = 16 * i + 4 * g + r;
+            if (t >= begin && t < end) yp[t * a.H * a.P] = M::IO::put(Q[i][r]);
+          }
+      }
+      // S = e^G_end S + k^T (e^{G_end - G} u)
+      const float whole = sIn[end - 1];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) S[j] *= whole;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          v[e] = u[2 * s + e / 4][e % 4] * sKout[32 * s + 16 * (e / 4) + 4 * g + e % 4];
+        const Two ub = M::two(v);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) S[j] = M::mma(M::transposed(kt + 32 * s * LP + 16 * j, LP, lane), ub, S[j]);
+      }
+      if constexpr (VL) {
+        if (marks && marks[row + t0 + end - 1]) {
+          for (int64_t s = 0; s < a.nseq; ++s) {
+            if (a.seq_last[s] != row + t0 + end - 1) continue;
+            float* out = a.seq_states + (s * a.H + h) * N * a.P + p;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const int nn = 16 * j + 4 * g + r;
+                if (nn < N) out[nn * a.P] = S[j][r];
+              }
+          }
+        }
+      }
+      begin = end;
+    }
+  }
+  if (!SAVE && a.hfin) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int nn = 16 * j + 4 * g + r;
+        if (nn < N) a.hfin[(bh * N + nn) * a.P + p] = S[j][r];
+      }
+  }
+}
+
+// ---------------------------------------------------------------- one token
+// A block takes 64 value columns of a (row, head): 16 threads of four columns
+// by 16 state rows, whose up to 16 rows a thread are all asked for first.
+// Bound by the state, read and written once: k^T h and q^T h are summed
+// together, for y = a q^T h + (q.k) u.
+constexpr int kStepCols = 64, kStepRows = (int)kDeltaMaxDim / 16;
+template <class IO>
+__global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a, const float* state, float* state_out) {
+  typedef typename IO::type T;
+  __shared__ float sk[kDeltaMaxDim], sq[kDeltaMaxDim];
+  __shared__ float red[3][4];
+  __shared__ float4 part[2][4][16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, cg = tid & 15, rg = tid >> 4;
+  const uint32_t slices = (uint32_t)((a.P + kStepCols - 1) / kStepCols);
+  const uint32_t bid = flat_block();
+  const int64_t bh = bid / slices;
+  if (bh >= a.B * a.H) return;
+  const int64_t h = bh % a.H, b = bh / a.H, grp = h / (a.H / a.G);
+  const int N = (int)a.N;
+  const int64_t p = (int64_t)(bid % slices) * kStepCols + 4 * cg;
+  const bool on = p < a.P;
+  const float4* st = reinterpret_cast<const float4*>(state + bh * N * a.P + p);
+  float4 s[kStepRows];
+#pragma unroll
+  for (int u = 0; u < kStepRows; ++u) {
+    const int nn = rg + 16 * u;
+    s[u] = on && nn < N ? st[nn * (a.P / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  const float kv = tid < N ? IO::get(static_cast<const T*>(a.k)[b * a.rows.k + grp * N + tid]) : 0.f;
+  const float qv = tid < N ? IO::get(static_cast<const T*>(a.q)[b * a.rows.q + grp * N + tid]) : 0.f;
+  float raw = IO::get(static_cast<const T*>(a.dt)[b * a.rows.dt + h]);
+  if (a.dt_bias) raw += a.dt_bias[h];
+  const float decay = expf((a.softplus ? softplus2(raw * kLog2e) * kLn2 : raw) * a.A[h]);
+  float beta = IO::get(static_cast<const T*>(a.beta)[b * a.rows.beta + h]);
+  if (a.sigmoid) beta = sigmoid(beta);
+  sk[tid] = kv;
+  sq[tid] = qv;
+  float k2 = kv * kv, q2 = qv * qv, qk = kv * qv;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    k2 += __shfl_xor(k2, o, 64);
+    q2 += __shfl_xor(q2, o, 64);
+    qk += __shfl_xor(qk, o, 64);
+  }
+  if (lane == 0) {
+    red[0][wave] = k2;
+    red[1][wave] = q2;
+    red[2][wave] = qk;
+  }
+  __syncthreads();
+  auto total = [&](const float* r) { return (r[0] + r[1]) + (r[2] + r[3]); };
+  const float rk = a.qk_norm ? 1.f / sqrtf(total(red[0]) + kQkEps) : 1.f;
+  const float rq = (a.qk_norm ? 1.f / sqrtf(total(red[1]) + kQkEps) : 1.f) * a.scale;
+  qk = total(red[2]) * rk * rq;
+  float4 ks = make_float4(0.f, 0.f, 0.f, 0.f), qs = ks;
+#pragma unroll
+  for (int u = 0; u < kStepRows; ++u) {
+    const int nn = rg + 16 * u;
+    if (nn >= N) break;
+    const float kn = sk[nn], qn = sq[nn];
+    ks.x = fmaf(kn, s[u].x, ks.x); ks.y = fmaf(kn, s[u].y, ks.y);
+    ks.z = fmaf(kn, s[u].z, ks.z); ks.w = fmaf(kn, s[u].w, ks.w);
+    qs.x = fmaf(qn, s[u].x, qs.x); qs.y = fmaf(qn, s[u].y, qs.y);
+    qs.z = fmaf(qn, s[u].z, qs.z); qs.w = fmaf(qn, s[u].w, qs.w);
+  }
+#pragma unroll
+  for (int o = 16; o < 64; o <<= 1) {
+    ks.x += __shfl_xor(ks.x, o, 64); ks.y += __shfl_xor(ks.y, o, 64);
+    ks.z += __shfl_xor(ks.z, o, 64); ks.w += __shfl_xor(ks.w, o, 64);
+    qs.x += __shfl_xor(qs.x, o, 64); qs.y += __shfl_xor(qs.y, o, 64);
+    qs.z += __shfl_xor(qs.z, o, 64); qs.w += __shfl_xor(qs.w, o, 64);
+  }
+  if (lane < 16) {
+    part[0][wave][cg] = ks;
+    part[1][wave][cg] = qs;
+  }
+  __syncthreads();
+  auto sum4 = [&](const float4(*q)[16]) {
+    float4 o = q[0][cg];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) {
+      const float4 e = q[w][cg];
+      o.x += e.x; o.y += e.y; o.z += e.z; o.w += e.w;
+    }
+    return o;
+  };
+  if (!on) return;
+  ks = sum4(part[0]);
+  qs = sum4(part[1]);
+  float v[4], u[4];
+  load_vec<IO, 1>(static_cast<const T*>(a.v) + b * a.rows.v + h * a.P + p, v);
+#pragma unroll
+  for (int e = 1; e < 4; ++e) v[e] = IO::get((static_cast<const T*>(a.v) + b * a.rows.v + h * a.P + p)[e]);
+  const float kse[4] = {ks.x, ks.y, ks.z, ks.w}, qse[4] = {qs.x, qs.y, qs.z, qs.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) u[e] = beta * (v[e] - decay * rk * kse[e]);
+  if (rg == 0) {
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = fmaf(decay * rq, qse[e], qk * u[e]);
+    store_vec<IO, 4>(static_cast<T*>(a.y) + bh * a.P + p, y);
+  }
+  float4* so = reinterpret_cast<float4*>(state_out + bh * N * a.P + p);
+#pragma unroll
+  for (int r = 0; r < kStepRows; ++r) {
+    const int nn = rg + 16 * r;
+    if (nn >= N) break;
+    const float kn = rk * sk[nn];
+    so[nn * (a.P / 4)] = make_float4(fmaf(decay, s[r].x, kn * u[0]), fmaf(decay, s[r].y, kn * u[1]),
+                                     fmaf(decay, s[r].z, kn * u[2]), fmaf(decay, s[r].w, kn * u[3]));
+  }
+}
+
+// ---------------------------------------------------------------- launches
+size_t delta_forward_ws_bytes(int64_t B, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P) {
+  return delta_ws(B, L, H, N, P, false).total;
+}
+
+hipError_t launch_delta_prepare(const DeltaArgs& a, const DeltaWs& ws, bool back, bool bf16, hipStream_t s) {
+  auto kern = bf16 ? (back ? delta_prepare_kernel<DeltaB, true> : delta_prepare_kernel<DeltaB, false>)
+                   : (back ? delta_prepare_kernel<DeltaF, true> : delta_prepare_kernel<DeltaF, false>);
+  hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, kPrepLds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * ws.nw * a.H)), dim3(256), kPrepLds, s, a, ws);
+  return hipGetLastError();
+}
+
+// Enough blocks for every compute unit come before waves that share k and q.
+int delta_chain_waves(int64_t B, int64_t H, int64_t P) {
+  const int64_t waves = P / 16;
+  for (int w = 4; w > 1; w /= 2)
+    if (waves % w == 0 && B * H * (waves / w) >= device_cu_count()) return w;
+  return waves % 2 == 0 ? 2 : 1;
+}
+
+template <class M, int NP, bool VL, bool SAVE>
+static hipError_t chain(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) {
+  auto kern = delta_chain_kernel<M, NP, VL, SAVE>;
+  const size_t lds = chain_lds<M, NP, SAVE>();
+  hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (e != hipSuccess) return e;
+  const int w = delta_chain_waves(a.B, a.H, a.P);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * a.H * (a.P / 16 / w))), dim3(64 * w), lds, s, a, ws);
+  return hipGetLastError();
+}
+template <class M, int NP>
+static hipError_t chain_of(const DeltaArgs& a, const DeltaWs& ws, bool save, hipStream_t s) {
+  const bool vl = a.seq_idx || (!save && a.nseq > 0);
+  if (save) return vl ? chain<M, NP, true, true>(a, ws, s) : chain<M, NP, false, true>(a, ws, s);
+  return vl ? chain<M, NP, true, false>(a, ws, s) : chain<M, NP, false, false>(a, ws, s);
+}
+template <class M>
+static hipError_t chain_at(const DeltaArgs& a, const DeltaWs& ws, bool save, hipStream_t s) {
+  if (a.N <= 32) return chain_of<M, 32>(a, ws, save, s);
+  if (a.N <= 64) return chain_of<M, 64>(a, ws, save, s);
+  if (a.N <= 128) return chain_of<M, 128>(a, ws, save, s);
+  return chain_of<M, 256>(a, ws, save, s);
+}
+hipError_t launch_delta_chain(const DeltaArgs& a, const DeltaWs& ws, bool save, bool bf16, hipStream_t s) {
+  return bf16 ? chain_at<DeltaB>(a, ws, save, s) : chain_at<DeltaF>(a, ws, save, s);
+}
+
+hipError_t launch_delta_forward(const DeltaArgs& a, bool bf16, hipStream_t s) {
+  const DeltaWs ws = delta_ws(a.B, a.L, a.H, a.N, a.P, false);
+  if (a.nseq > 0) {
+    uint8_t* marks = reinterpret_cast<uint8_t*>(a.ws + ws.marks);
+    hipLaunchKernelGGL(delta_marks_clear_kernel, flat_grid((a.B * a.L + 255) / 256), dim3(256), 0, s, marks, a.B * a.L);
+    hipLaunchKernelGGL(delta_marks_kernel, dim3((unsigned)((a.nseq + 255) / 256)), dim3(256), 0, s, marks, a.B * a.L,
+                       a.seq_last, a.nseq);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const hipError_t e = launch_delta_prepare(a, ws, false, bf16, s);
+  return e != hipSuccess ? e : launch_delta_chain(a, ws, false, bf16, s);
+}
+
+hipError_t launch_delta_step(const DeltaArgs& a, const float* state, float* state_out, bool bf16, hipStream_t s) {
+  auto kern = bf16 ? delta_step_kernel<IoBF16> : delta_step_kernel<IoF32>;
+  hipLaunchKernelGGL(kern, flat_grid(a.B * a.H * ((a.P + kStepCols - 1) / kStepCols)), dim3(256), 0, s, a, state,
+                     state_out);
+  return hipGetLastError();
+}
+
+}  // namespace ssd

@@ -1,0 +1,224 @@
+// delta_rule.hpp -- what the gated delta rule's kernels share.
+//
+// Per head, with unit (or raw) keys k_t, queries q_t (scaled), decays a_t =
+// e^{g_t} and writing strengths b_t, the state h (N x P) follows
+//     h~ = a_t h_{t-1},  u_t = b_t (v_t - k_t^T h~),  h_t = h~ + k_t u_t^T,
+//     y_t = q_t^T h_t.
+// Tokens are taken in windows of 64, a window in pieces of one sequence (one
+// piece unless sequences are packed).  With G the running sum of g in a piece,
+// S the state in front of it and
+//     E_ts = e^{G_t - G_s} k_t.k_s (s < t),   P_ts = e^{G_t - G_s} q_t.k_s (s <= t),
+//     R = -(I + E diag(b))^{-1} E             (strictly lower triangular)
+// a piece is a few products:
+//     X = v - diag(e^G) k S,   w = X + R (b X),   u = b w,
+//     y = diag(e^G) q S + P u,   S' = e^{G_end} S + k^T diag(e^{G_end - G}) u.
+// R in place of (I + b E)^{-1} b keeps b = 0 exact here and in the gradients.
+//
+// Matrix operands.  bf16 inputs enter as they are; what is computed (states,
+// corrected values, R, P) enters as the sum of two bf16 values, 16 bits, and
+// every sum and the states themselves are fp32, so that states and sums over
+// tokens are 4e-6 from the 64-bit values, not 4e-3 as with one bf16 operand.
+// Unit length goes into the fp32 scalars of a row, never into rounded rows.
+// fp32 inputs use the fp32 matrix instructions throughout.
+#pragma once
+
+#include "delta_launch.hpp"
+#include "layer_device.hpp"
+
+namespace ssd {
+
+constexpr float kQkEps = 1e-6f;
+constexpr int kC = (int)kDeltaC;
+
+// One: an operand of inputs.  Two: of computed values.
+struct DeltaB {
+  typedef IoBF16 IO;
+  typedef OpBF16::Frag One;
+  struct Two { One hi, lo; };
+  __device__ __forceinline__ static Two two(const float* s) {
+    Two t;
+    t.hi = OpBF16::from_f32(s);
+    const uint32_t w[4] = {t.hi.v.x, t.hi.v.y, t.hi.v.z, t.hi.v.w};
+    float d[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      d[2 * e] = s[2 * e] - __uint_as_float(w[e] << 16);
+      d[2 * e + 1] = s[2 * e + 1] - __uint_as_float(w[e] & 0xffff0000u);
+    }
+    t.lo = OpBF16::from_f32(d);
+    return t;
+  }
+  __device__ __forceinline__ static One one(const float* s) { return OpBF16::from_f32(s); }
+  __device__ __forceinline__ static f32x4_t mma(const One& a, const One& b, f32x4_t c) { return OpBF16::mma(a, b, c); }
+  __device__ __forceinline__ static f32x4_t mma(const One& a, const Two& b, f32x4_t c) {
+    return OpBF16::mma(a, b.hi, OpBF16::mma(a, b.lo, c));
+  }
+  __device__ __forceinline__ static f32x4_t mma(const Two& a, const One& b, f32x4_t c) {
+    return OpBF16::mma(a.hi, b, OpBF16::mma(a.lo, b, c));
+  }
+  __device__ __forceinline__ static f32x4_t mma(const Two& a, const Two& b, f32x4_t c) {
+    return OpBF16::mma(a.hi, b.hi, OpBF16::mma(a.lo, b.hi, OpBF16::mma(a.hi, b.lo, c)));
+  }
+  // 2 KB a fragment in memory: 16 bytes a lane, twice
+  __device__ __forceinline__ static Two load(const char* p, int lane) {
+    Two t;
+    t.hi.v = *reinterpret_cast<const uint4*>(p + 16 * lane);
+    t.lo.v = *reinterpret_cast<const uint4*>(p + 1024 + 16 * lane);
+    return t;
+  }
+  __device__ __forceinline__ static void store(char* p, int lane, const Two& t) {
+    *reinterpret_cast<uint4*>(p + 16 * lane) = t.hi.v;
+    *reinterpret_cast<uint4*>(p + 1024 + 16 * lane) = t.lo.v;
+  }
+  // eight consecutive inputs
+  __device__ __forceinline__ static One global8(const uint16_t* p) {
+    One f;
+    f.v = *reinterpret_cast<const uint4*>(p);
+    return f;
+  }
+  __device__ __forceinline__ static One zero() { return OpBF16::zero(); }
+  // rows of a tile in LDS as the transposed operand: lane (i, g) gets, as slots
+  // 4t + r, tile[16t + 4g + r][i]
+  __device__ __forceinline__ static One transposed(const uint16_t* tile, int pitch, int lane) {
+    return lds_frag_tr(tile, pitch, lane);
+  }
+};
+struct DeltaF {
+  typedef IoF32 IO;
+  typedef OpF32::Frag One;
+  typedef OpF32::Frag Two;
+  __device__ __forceinline__ static Two two(const float* s) { return OpF32::from_f32(s); }
+  __device__ __forceinline__ static One one(const float* s) { return OpF32::from_f32(s); }
+  __device__ __forceinline__ static f32x4_t mma(const One& a, const One& b, f32x4_t c) { return OpF32::mma(a, b, c); }
+  __device__ __forceinline__ static Two load(const char* p, int lane) {
+    Two t;
+    t.lo = *reinterpret_cast<const float4*>(p + 16 * lane);
+    t.hi = *reinterpret_cast<const float4*>(p + 1024 + 16 * lane);
+    return t;
+  }
+  __device__ __forceinline__ static void store(char* p, int lane, const Two& t) {
+    *reinterpret_cast<float4*>(p + 16 * lane) = t.lo;
+    *reinterpret_cast<float4*>(p + 1024 + 16 * lane) = t.hi;
+  }
+  __device__ __forceinline__ static One global8(const float* p) { return Lds<OpF32>::load8(p); }
+  __device__ __forceinline__ static One zero() { return OpF32::zero(); }
+  __device__ __forceinline__ static One transposed(const float* tile, int pitch, int lane) {
+    const float* p = tile + 4 * (lane >> 4) * pitch + (lane & 15);
+    One f;
+    f.lo = make_float4(p[0], p[pitch], p[2 * pitch], p[3 * pitch]);
+    p += 16 * pitch;
+    f.hi = make_float4(p[0], p[pitch], p[2 * pitch], p[3 * pitch]);
+    return f;
+  }
+};
+// Slots 0..3 of p0, 4..7 of p1.
+template <class M>
+__device__ __forceinline__ typename M::One lds_4x2(const typename M::IO::type* p0, const typename M::IO::type* p1) {
+  if constexpr (sizeof(typename M::IO::type) == 2) return Lds<OpBF16>::load4x2(p0, p1);
+  else return Lds<OpF32>::load4x2(p0, p1);
+}
+
+// ---- what the preparation leaves for a (row, head, window) ----
+struct DeltaGates {
+  float beta[kC];
+  float kin[kC];   // e^G |k|^-1
+  float qin[kC];   // e^G |q|^-1 scale
+  float kout[kC];  // e^{G_end - G} |k|^-1
+  float in[kC];    // e^G
+  float rk[kC], rq[kC];  // |k|^-1, |q|^-1 scale
+  double G[kC];
+};
+// Triangular 64 x 64 operands: 6 of 8 fragments, those of row tile i and
+// 32-column step s that are not all zero.
+constexpr int kTriFrags = 6;
+constexpr int kTriBytes = kTriFrags * 2048;
+// lower triangular: (0,0) (1,0) (2,0) (2,1) (3,0) (3,1)
+__host__ __device__ constexpr int low_frag(int i, int s) { return i < 2 ? i : 2 + 2 * (i - 2) + s; }
+// its transpose, upper triangular: (0,0) (0,1) (1,0) (1,1) (2,1) (3,1)
+__host__ __device__ constexpr int up_frag(int i, int s) { return i < 2 ? 2 * i + s : 2 + i; }
+
+// ---- pieces of a window ----
+// Bits of the tokens t > 0 of a window at which a piece begins: another
+// sequence, or behind a token whose state is asked for; `fresh`: where a
+// sequence begins, t = 0 included (not at a row's start).
+struct Cuts {
+  uint64_t piece, fresh;
+};
+__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v) |
+         ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) << 32);
+}
+// Every lane of a wave calls this; row: the batch's first token, t0 the window's.
+__device__ __forceinline__ Cuts window_cuts(const int* seq_idx, const uint8_t* marks, int64_t row, int64_t t0,
+                                            int64_t L, int lane) {
+  const int64_t t = t0 + lane;
+  bool fresh = false, mark = false;
+  if (t < L && t > 0) {
+    if (seq_idx) fresh = seq_idx[row + t] != seq_idx[row + t - 1];
+    if (marks) mark = marks[row + t - 1] != 0;
+  }
+  Cuts c;
+  c.fresh = uniform64(__ballot(fresh));
+  c.piece = (c.fresh | uniform64(__ballot(mark))) & ~uint64_t(1);
+  return c;
+}
+// The piece's number of token t.
+__device__ __forceinline__ int piece_of(uint64_t cuts, int t) { return __popcll(cuts & (~uint64_t(0) >> (63 - t))); }
+// The end of the piece that begins at a, in a window of n tokens.
+__device__ __forceinline__ int piece_end(uint64_t cuts, int a, int n) {
+  const uint64_t later = a >= 63 ? 0 : cuts >> (a + 1);
+  return later ? min(n, a + 1 + (int)__builtin_ctzll(later)) : n;
+}
+// The beginning of the piece that ends before e.
+__device__ __forceinline__ int piece_begin(uint64_t cuts, int e) {
+  const uint64_t before = cuts & (~uint64_t(0) >> (64 - e));
+  return before ? 63 - (int)__builtin_clzll(before) : 0;
+}
+
+// Neighbouring blocks (slices of a head, heads of a group) on one XCD's L2.
+__device__ __forceinline__ uint32_t near_block(uint32_t bid, uint32_t n) {
+  return n % 8 == 0 ? (bid & 7u) * (n >> 3) + (bid >> 3) : bid;
+}
+
+// ---- the workspace ----
+struct DeltaWs {
+  int64_t nw;        // windows a row
+  size_t gates, low_r, low_p, up_r, up_p, marks, S, D, w, du, dq, dk, part, total;
+};
+inline DeltaWs delta_ws(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P, bool back) {
+  DeltaWs o = {};
+  o.nw = (L + kDeltaC - 1) / kDeltaC;
+  const size_t bhw = (size_t)(B * H * o.nw);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t p = at;
+    at += (bytes + 255) / 256 * 256;
+    return p;
+  };
+  o.gates = take(bhw * sizeof(DeltaGates));
+  o.low_r = take(bhw * kTriBytes);
+  if (!back) {
+    o.low_p = take(bhw * kTriBytes);
+    o.marks = take((size_t)(B * L));
+  } else {
+    o.up_r = take(bhw * kTriBytes);
+    o.up_p = take(bhw * kTriBytes);
+    o.S = take(bhw * N * P * 4);
+    o.D = take(bhw * N * P * 4);
+    o.w = take(bhw * kDeltaC * P * 4);
+    o.du = take(bhw * kDeltaC * P * 4);
+    o.dq = take(bhw * kDeltaC * N * 4);
+    o.dk = take(bhw * kDeltaC * N * 4);
+    o.part = take(bhw * 2 * 4);
+  }
+  o.total = at;
+  return o;
+}
+
+// Launches shared by the forward and the gradients (delta_rule.hip).
+hipError_t launch_delta_prepare(const DeltaArgs& a, const DeltaWs& ws, bool back, bool bf16, hipStream_t s);
+hipError_t launch_delta_chain(const DeltaArgs& a, const DeltaWs& ws, bool save, bool bf16, hipStream_t s);
+// Waves of 16 value columns a block of the chains.
+int delta_chain_waves(int64_t B, int64_t H, int64_t P);
+
+}  // namespace ssd

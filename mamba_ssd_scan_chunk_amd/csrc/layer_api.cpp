@@ -5,50 +5,12 @@
 
 #include <hip/hip_runtime.h>
 
-#include <initializer_list>
-
+#include "api_checks.hpp"
 #include "layer_launch.hpp"
 
+using namespace ssd::api;
+
 namespace {
-
-constexpr int64_t k31 = int64_t(1) << 31;
-constexpr int64_t kMaxElems = int64_t(1) << 46;  // far below where byte offsets leave 64 bits
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-bool a16(const void* p) { return aligned(p, 16); }  // true for NULL
-
-ssd_status check_dtype(ssd_dtype t) { return (t == SSD_F32 || t == SSD_BF16) ? SSD_OK : SSD_ERR_DTYPE; }
-ssd_status from_hip(hipError_t e) { return e == hipSuccess ? SSD_OK : SSD_ERR_HIP; }
-uintptr_t elem(ssd_dtype t) { return t == SSD_BF16 ? 2 : 4; }
-
-#define SSD_TRY(expr)              \
-  do {                             \
-    const ssd_status st_ = (expr); \
-    if (st_ != SSD_OK) return st_; \
-  } while (0)
-
-// A product of positive sizes, or SSD_ERR_UNSUPPORTED past `most`.
-ssd_status product(std::initializer_list<int64_t> f, int64_t most) {
-  int64_t p = 1;
-  for (int64_t v : f) {
-    if (v > most / p) return SSD_ERR_UNSUPPORTED;
-    p *= v;
-  }
-  return SSD_OK;
-}
-
-// A row stride: 0 stands for `dense`; shorter rows than the channels overlap.
-// Up to 16 rows of a sequence are addressed by 32-bit byte offsets from the first.
-bool row_too_long(int64_t seqlen, int64_t row) { return seqlen > 1 && row >= int64_t(1) << 25; }
-
-ssd_status row_stride(int64_t given, int64_t dense, int64_t batch, int64_t seqlen, int64_t* out) {
-  if (given == 0) given = dense;
-  if (given < dense) return SSD_ERR_SHAPE;
-  SSD_TRY(product({batch, seqlen, given}, kMaxElems));
-  if (row_too_long(seqlen, given)) return SSD_ERR_UNSUPPORTED;
-  *out = given;
-  return SSD_OK;
-}
 
 // ---- convolution ----
 ssd_status check_conv(const ssd_conv_shape* s, bool step) {
@@ -70,20 +32,6 @@ ssd::ConvArgs conv_args(const ssd_conv_shape* s) {
   a.D = s->channels;
   a.W = (int)s->width;
   return a;
-}
-
-// The state after a row goes to memory of its own: other blocks still read the
-// one before it.
-ssd_status check_states(const void* initial, const void* final) {
-  return final && final == initial ? SSD_ERR_UNSUPPORTED : SSD_OK;
-}
-
-ssd_status check_seq_list(int64_t nseq, const int64_t* last, const void* states) {
-  if (nseq < 0) return SSD_ERR_SHAPE;
-  if (nseq > 65535) return SSD_ERR_UNSUPPORTED;
-  if (nseq > 0 && (!last || !states)) return SSD_ERR_NULL;
-  if (nseq > 0 && (!a16(last) || !a16(states))) return SSD_ERR_ALIGN;
-  return SSD_OK;
 }
 
 // ---- selective scan ----

@@ -14,8 +14,8 @@ from typing import Dict, Optional, Tuple
 
 import torch
 
-from ._lib import (MMA, SSD_BF16, SSD_F32, SSDConvShape, SSDScanRows, SSDScanShape, SSDShape, check,
-                   load_library)
+from ._lib import (MMA, SSD_BF16, SSD_DELTA_QK_NORM, SSD_DELTA_SIGMOID, SSD_DELTA_SOFTPLUS, SSD_F32, SSDConvShape,
+                   SSDDeltaRows, SSDDeltaShape, SSDScanRows, SSDScanShape, SSDShape, check, load_library)
 
 _DT = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
 _DTNAME = {"f32": torch.float32, "bf16": torch.bfloat16}
@@ -843,3 +843,86 @@ def ssd_layer_norm_backward(dy, x, weight, mean, rstd, dresidual=None, rms=False
                                       _ptr(r["dx"]), _ptr(r["dresidual"]), _ptr(r["dweight"]), _ptr(r["dbias"]),
                                       _ptr(workspace), wsb, _stream()))
     return r
+
+
+def _delta_inputs(q, k, v, dt, beta, A, dt_bias, softplus, sigmoid, qk_norm, scale, lead):
+    """Checks the inputs shared by the delta rule's calls; returns the shape
+    struct, the row strides, the flags and the scale."""
+    tok = tuple(v.shape[:lead])
+    if v.dim() != lead + 2 or k.dim() != lead + 2:
+        raise ValueError("q and k must be [B,L,G,N] and v [B,L,H,P] (of one token without L)")
+    H, P = v.shape[lead:]
+    G, N = k.shape[lead:]
+    io = (v.dtype,)
+    rows = SSDDeltaRows(_req_rows(q, "q", tok + (G, N), io, lead), _req_rows(k, "k", tok + (G, N), io, lead),
+                        _req_rows(v, "v", tok + (H, P), _IO, lead), _req_rows(dt, "dt", tok + (H,), io, lead),
+                        _req_rows(beta, "beta", tok + (H,), io, lead))
+    _req(A, "A", (H,), _F32)
+    _opt(dt_bias, "dt_bias", (H,), _F32)
+    flags = SSD_DELTA_SOFTPLUS * bool(softplus) | SSD_DELTA_SIGMOID * bool(sigmoid) | SSD_DELTA_QK_NORM * bool(qk_norm)
+    sh = SSDDeltaShape(tok[0], tok[1] if lead == 2 else 1, H, P, N, G)
+    return sh, rows, flags, float(N ** -0.5 if scale is None else scale)
+
+
+def ssd_delta_rule_workspace_bytes(batch, seqlen, nheads, ngroups, dstate, headdim, dtype=None) -> int:
+    """``dtype`` (of the activations) makes no difference."""
+    return int(load_library().ssd_delta_rule_workspace_bytes(SSDDeltaShape(batch, seqlen, nheads, headdim, dstate,
+                                                                           ngroups)))
+
+
+def ssd_delta_rule(q, k, v, dt, beta, A, dt_bias=None, softplus=True, sigmoid=True, qk_norm=True, scale=None,
+                   initial_states=None, seq_idx=None, y=None, final_states=None, want_final=True, seq_last=None,
+                   seq_states=None, workspace=None, stream=None):
+    """Gated delta rule over q, k [B,L,G,N], v [B,L,H,P] and the raw decays and
+    writing strengths dt, beta [B,L,H] (each may be a column slice of wider
+    rows), A, dt_bias [H] fp32, states [B,H,N,P] fp32:
+
+        h <- exp(A softplus(dt + dt_bias)) h;  u = sigmoid(beta) (v - k^T h);
+        h <- h + k u^T;  y = q^T h
+
+    with q and k of unit length (``qk_norm``) and q times ``scale`` (default
+    N^-1/2).  Returns (y, final_states or None), and with seq_last (see
+    ssd_forward_varlen) also seq_states [nseq,H,N,P].  final_states may be the
+    initial_states tensor."""
+    if stream is not None:
+        return _on_stream(ssd_delta_rule, locals())
+    sh, rows, flags, scale = _delta_inputs(q, k, v, dt, beta, A, dt_bias, softplus, sigmoid, qk_norm, scale, 2)
+    B, L, H, P, N = sh.batch, sh.seqlen, sh.nheads, sh.headdim, sh.dstate
+    _opt(initial_states, "initial_states", (B, H, N, P), _F32)
+    _opt(seq_idx, "seq_idx", (B, L), (torch.int32,))
+    if y is None:
+        y = v.new_empty((B, L, H, P))
+    _req(y, "y", (B, L, H, P), (v.dtype,))
+    if final_states is None and want_final:
+        final_states = A.new_empty((B, H, N, P))
+    _opt(final_states, "final_states", (B, H, N, P), _F32)
+    nseq, seq_states = _seq_states(seq_last, seq_states, (H, N, P), torch.float32, v.device)
+    lib = load_library()
+    workspace, wsb = _workspace(workspace, lib.ssd_delta_rule_workspace_bytes, (sh,), v.device)
+    check(lib.ssd_delta_rule(sh, rows, _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(A), _ptr(dt_bias), flags,
+                             scale, _DT[v.dtype], _ptr(initial_states), _ptr(seq_idx), _ptr(y), _ptr(final_states),
+                             nseq, _ptr(seq_last if nseq else None), _ptr(seq_states if nseq else None),
+                             _ptr(workspace), wsb, _stream()))
+    return (y, final_states) if seq_last is None else (y, final_states, seq_states)
+
+
+def ssd_delta_step(q, k, v, dt, beta, A, state, dt_bias=None, softplus=True, sigmoid=True, qk_norm=True, scale=None,
+                   y=None, state_out=None, stream=None):
+    """One token of ssd_delta_rule: q, k [B,G,N], v [B,H,P], dt, beta [B,H],
+    state [B,H,N,P] fp32.  The state after the token goes to ``state_out``
+    (default: over ``state``).  Returns y [B,H,P]."""
+    if stream is not None:
+        return _on_stream(ssd_delta_step, locals())
+    sh, rows, flags, scale = _delta_inputs(q, k, v, dt, beta, A, dt_bias, softplus, sigmoid, qk_norm, scale, 1)
+    B, H, P, N = sh.batch, sh.nheads, sh.headdim, sh.dstate
+    _req(state, "state", (B, H, N, P), _F32)
+    if state_out is None:
+        state_out = state
+    _req(state_out, "state_out", (B, H, N, P), _F32)
+    if y is None:
+        y = v.new_empty((B, H, P))
+    _req(y, "y", (B, H, P), (v.dtype,))
+    check(load_library().ssd_delta_step(sh, rows, _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(A),
+                                        _ptr(dt_bias), flags, scale, _DT[v.dtype], _ptr(state), _ptr(state_out),
+                                        _ptr(y), _stream()))
+    return y

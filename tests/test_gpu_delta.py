@@ -1,0 +1,186 @@
+"""The gated delta rule on the GPU against its 64-bit recurrence.
+
+Tolerances.  fp32 inputs: every product is fp32 throughout; five products deep
+(k S, R X, P u, k^T u, the state), each of at most 256 + 64 terms of relative
+error 2^-24: 5 * 320 * 2^-24 = 9.5e-5 of the largest value.  bf16 inputs:
+computed operands are sums of two bf16 values: a product of two of them loses
+at most 3 * 2^-16 of its terms' sizes, five deep, corrections at most doubling:
+30 * 2^-16 = 4.6e-4 of the largest value; a bf16 output adds half a step, 2^-8
+of its own value."""
+import pytest
+import torch
+
+import delta_reference as ref
+from mamba_ssd_scan_chunk_amd import ops
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def bound(dtype):
+    return 1e-4 if dtype == F32 else 30 * 2.0 ** -16
+
+
+def check(got, want, dtype, what):
+    want = want.double()
+    assert tuple(got.shape) == tuple(want.shape), (what, got.shape, want.shape)
+    half = 2.0 ** -8 if got.dtype == BF else 0.0
+    got = got.double().cpu()
+    assert torch.isfinite(got).all(), what
+    tol = bound(dtype) * want.abs().max().clamp(min=1e-30) + half * want.abs()
+    off = (got - want).abs()
+    assert (off <= tol).all(), f"{what}: off by {float((off / tol).max()):.3g} times the tolerance"
+
+
+def gpu(a):
+    return {k: None if v is None else v.cuda() for k, v in a.items()}
+
+
+def call(a, **how):
+    d = gpu(a)
+    h0 = d.pop("h0")
+    return ops.ssd_delta_rule(d["q"], d["k"], d["v"], d["dt"], d["beta"], d["A"], dt_bias=d["dt_bias"],
+                              initial_states=h0, **how)
+
+
+SHAPES = [
+    # B, L, H, G, N, P
+    (1, 1, 1, 1, 16, 16), (2, 2, 2, 1, 64, 64), (1, 15, 3, 3, 32, 48), (2, 63, 4, 2, 128, 64), (1, 64, 2, 2, 128, 128),
+    (1, 65, 2, 1, 48, 80), (2, 130, 3, 1, 96, 16), (1, 257, 1, 1, 256, 256), (1, 191, 5, 5, 80, 112),
+    (3, 100, 24, 1, 128, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_forward(shape, dtype):
+    a = ref.inputs(*shape, dtype=dtype, seed=sum(shape))
+    y, fin = call(a)
+    wy, wf, _ = ref.forward(**a)
+    check(y, wy, dtype, "y")
+    check(fin, wf, dtype, "final")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_forward_flags_and_absent_arguments(dtype):
+    a = ref.inputs(2, 90, 4, 2, 64, 32, dtype=dtype, seed=3, h0=False, bias=False)
+    a["beta"] = a["beta"].sigmoid().to(dtype)
+    a["beta"][:, ::7] = 0                       # tokens that write nothing
+    a["k"] = (a["k"].float() * 0.1).to(dtype)
+    a["dt"] = a["dt"].abs() * 0.1
+    how = dict(softplus=False, sigmoid=False, qk_norm=False, scale=0.25)
+    y, fin = call(a, **how)
+    wy, wf, _ = ref.forward(**a, **how)
+    check(y, wy, dtype, "y")
+    check(fin, wf, dtype, "final")
+    y2, none = call(a, want_final=False, **how)
+    assert none is None and torch.equal(y, y2)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("L,starts", [(1, 1), (64, 3), (200, 9), (130, 130)])
+def test_packed(L, starts, dtype):
+    a = ref.inputs(2, L, 4, 2, 64, 48, dtype=dtype, seed=L)
+    idx = ref.packed(2, L, starts, seed=L)
+    y, fin = call(a, seq_idx=idx.cuda())
+    wy, wf, _ = ref.forward(**a, seq_idx=idx)
+    check(y, wy, dtype, "y")
+    check(fin, wf, dtype, "final")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("with_idx", [False, True])
+def test_states_after_tokens(with_idx, dtype):
+    B, L = 2, 150
+    a = ref.inputs(B, L, 4, 2, 32, 32, dtype=dtype, seed=8)
+    idx = ref.packed(B, L, 5, seed=8) if with_idx else None
+    last = [0, 63, 64, 149, 150, 299, 63, 200, -1, B * L]      # one of them twice, two outside
+    states = torch.full((len(last), 4, 32, 32), 7.0, device="cuda")
+    y, fin, st = call(a, seq_idx=None if idx is None else idx.cuda(), seq_last=torch.tensor(last).cuda(),
+                      seq_states=states)
+    wy, wf, asked = ref.forward(**a, seq_idx=idx, states_after=last)
+    check(y, wy, dtype, "y")
+    check(fin, wf, dtype, "final")
+    for s, i in enumerate(last):
+        if i in asked:
+            check(st[s], asked[i], dtype, f"state after {i}")
+        else:
+            assert (st[s] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_nan_and_infinity_stay_in_their_sequence(dtype):
+    B, L = 1, 200
+    a = ref.inputs(B, L, 2, 1, 64, 32, dtype=dtype, seed=5)
+    idx = torch.zeros((B, L), dtype=torch.int32)
+    idx[:, 40:] = 1
+    idx[:, 70:] = 2
+    idx[:, 180:] = 3
+    want, wf, _ = ref.forward(**a, seq_idx=idx)
+    for name, bad in [("v", float("nan")), ("q", float("inf")), ("k", float("nan")), ("dt", float("nan")),
+                      ("beta", float("nan")), ("dt", float("-inf"))]:
+        d = dict(a)
+        d[name] = a[name].clone()
+        d[name][:, 50] = bad
+        d[name][:, 100] = bad
+        y, fin = call(d, seq_idx=idx.cuda())
+        y = y.cpu()
+        for s in (slice(0, 40), slice(180, L)):
+            check(y[:, s], want[:, s], dtype, f"y beside {name}")
+        check(fin, wf, dtype, f"final beside {name}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_column_slices_continue_and_in_place_state(dtype):
+    B, L, H, G, N, P = 2, 100, 4, 2, 64, 32
+    a = ref.inputs(B, L, H, G, N, P, dtype=dtype, seed=11)
+    d = gpu(a)
+    wide = torch.cat([d["q"].flatten(2), d["k"].flatten(2), d["v"].flatten(2)], -1)
+    ab = torch.cat([d["dt"], d["beta"], d["dt"][..., :1]], -1)
+    q, k = wide[..., :G * N].unflatten(-1, (G, N)), wide[..., G * N:2 * G * N].unflatten(-1, (G, N))
+    v = wide[..., 2 * G * N:].unflatten(-1, (H, P))
+    dense, fin = call(a)
+    y, fin2 = ops.ssd_delta_rule(q, k, v, ab[..., :H], ab[..., H:2 * H], d["A"], dt_bias=d["dt_bias"],
+                                 initial_states=d["h0"])
+    assert torch.equal(dense, y) and torch.equal(fin, fin2)
+    # in two calls, the state handed on in place
+    st = d["h0"].clone()
+    parts = []
+    for s in (slice(0, 64), slice(64, L)):
+        yy, st2 = ops.ssd_delta_rule(d["q"][:, s].contiguous(), d["k"][:, s].contiguous(), d["v"][:, s].contiguous(),
+                                     d["dt"][:, s].contiguous(), d["beta"][:, s].contiguous(), d["A"],
+                                     dt_bias=d["dt_bias"], initial_states=st, final_states=st)
+        parts.append(yy)
+    assert torch.equal(torch.cat(parts, 1), dense) and torch.equal(st, fin)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("B,H,G,N,P", [(1, 1, 1, 16, 16), (3, 4, 2, 128, 128), (2, 6, 3, 48, 80), (1, 2, 1, 256, 256),
+                                       (5, 24, 1, 128, 64)])
+def test_step(B, H, G, N, P, dtype):
+    a = ref.inputs(B, 1, H, G, N, P, dtype=dtype, seed=B + H)
+    d = gpu(a)
+    one = {k: d[k][:, 0].contiguous() for k in ("q", "k", "v", "dt", "beta")}
+    out = torch.empty_like(d["h0"])
+    y = ops.ssd_delta_step(*one.values(), d["A"], d["h0"], dt_bias=d["dt_bias"], state_out=out)
+    wy, wf, _ = ref.forward(**a)
+    check(y, wy[:, 0], dtype, "y")
+    check(out, wf, F32, "state")          # nothing is rounded on the way to a step's state
+    assert torch.equal(d["h0"].cpu(), a["h0"])
+    y2 = ops.ssd_delta_step(*one.values(), d["A"], d["h0"], dt_bias=d["dt_bias"])
+    assert torch.equal(y, y2) and torch.equal(d["h0"], out)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_steps_go_on_from_a_prompt(dtype):
+    L, extra = 70, 6
+    a = ref.inputs(2, L + extra, 4, 2, 64, 64, dtype=dtype, seed=21)
+    wy, wf, _ = ref.forward(**a)
+    head = {k: v[:, :L].contiguous() if k in ("q", "k", "v", "dt", "beta") else v for k, v in a.items()}
+    y, st = call(head)
+    d = gpu(a)
+    for t in range(L, L + extra):
+        yt = ops.ssd_delta_step(*(d[k][:, t] for k in ("q", "k", "v", "dt", "beta")), d["A"], st, dt_bias=d["dt_bias"])
+        check(yt, wy[:, t], dtype, f"y of token {t}")
+    check(st, wf, dtype, "state")
