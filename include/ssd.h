@@ -572,6 +572,24 @@ ssd_status ssd_delta_step(const ssd_delta_shape* shape, const ssd_delta_rows* ro
                           int flags, float scale, ssd_dtype in, const float* state, float* state_out, void* y,
                           void* stream);
 
+/*
+ * Gradients of ssd_delta_rule for dL/dy = dy [B,L,H,P] (`in`) and
+ * dL/d final_states = dfinal (optional: zero); the states are recomputed.
+ * dq, dk, dv, ddt, dbeta (the last two with respect to the raw dt and beta) in
+ * `in`, laid out like their inputs with the row strides of `grad_rows` (NULL =
+ * dense); dA, ddt_bias (optional) [H] and dinitial [B,H,N,P] (optional) fp32.
+ * B L G <= 2^25 (else SSD_ERR_UNSUPPORTED).  Workspace: device memory of
+ * ssd_delta_rule_backward_workspace_bytes(shape) bytes.
+ */
+ssd_status ssd_delta_rule_backward(const ssd_delta_shape* shape, const ssd_delta_rows* rows, const void* q,
+                                   const void* k, const void* v, const void* dt, const void* beta, const float* A,
+                                   const float* dt_bias, int flags, float scale, ssd_dtype in,
+                                   const float* initial_states, const int32_t* seq_idx, const void* dy,
+                                   const float* dfinal, const ssd_delta_rows* grad_rows, void* dq, void* dk, void* dv,
+                                   void* ddt, void* dbeta, float* dA, float* ddt_bias, float* dinitial,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+size_t ssd_delta_rule_backward_workspace_bytes(const ssd_delta_shape* shape);
+
 /* Static, NUL-terminated description of a status code. */
 const char* ssd_status_string(ssd_status status);
 

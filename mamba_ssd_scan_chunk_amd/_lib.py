@@ -105,6 +105,8 @@ _SIGNATURES = {
     "ssd_layer_norm_backward_workspace_bytes": (_Z, [_I, _I]),
     "ssd_delta_rule": (ctypes.c_int, _DELTA_IN + [_P, _P, _P, _P, _I, _P, _P, _P, _Z, _P]),
     "ssd_delta_rule_workspace_bytes": (_Z, [_DS]),
+    "ssd_delta_rule_backward": (ctypes.c_int, _DELTA_IN + [_P, _P, _P, _P, _DR] + [_P] * 8 + [_P, _Z, _P]),
+    "ssd_delta_rule_backward_workspace_bytes": (_Z, [_DS]),
     "ssd_delta_step": (ctypes.c_int, _DELTA_IN + [_P, _P, _P, _P]),
     "ssd_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "ssd_abi_version": (ctypes.c_int, []),

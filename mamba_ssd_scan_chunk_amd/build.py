@@ -22,7 +22,8 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["chunk_cumsum.hip", "chunk_state.hip", "chunk_state_hg.hip", "state_passing.hip", "state_fused.hip", "forward_fused.hip",
            "chunk_scan.hip", "chunk_scan_hg.hip", "decode.hip", "varlen_states.hip", "backward.hip", "bwd_dbc.hip",
            "ssd_api.cpp", "tuning.cpp", "forward_noalloc.hip", "causal_conv.hip", "selective_scan.hip",
-           "selective_scan_bwd.hip", "layer_norm.hip", "layer_api.cpp", "delta_rule.hip", "delta_api.cpp"]
+           "selective_scan_bwd.hip", "layer_norm.hip", "layer_api.cpp", "delta_rule.hip", "delta_rule_bwd.hip",
+           "delta_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -116,4 +116,45 @@ ssd_status ssd_delta_step(const ssd_delta_shape* shape, const ssd_delta_rows* ro
   return from_hip(ssd::launch_delta_step(a, state, state_out, in == SSD_BF16, (hipStream_t)stream));
 }
 
+size_t ssd_delta_rule_backward_workspace_bytes(const ssd_delta_shape* s) {
+  if (check_delta(s, false) != SSD_OK) return 0;
+  return ssd::delta_backward_ws_bytes(s->batch, s->seqlen, s->nheads, s->ngroups, s->dstate, s->headdim);
+}
+
+ssd_status ssd_delta_rule_backward(const ssd_delta_shape* shape, const ssd_delta_rows* rows, const void* q,
+                                   const void* k, const void* v, const void* dt, const void* beta, const float* A,
+                                   const float* dt_bias, int flags, float scale, ssd_dtype in,
+                                   const float* initial_states, const int32_t* seq_idx, const void* dy,
+                                   const float* dfinal, const ssd_delta_rows* grad_rows, void* dq, void* dk, void* dv,
+                                   void* ddt, void* dbeta, float* dA, float* ddt_bias, float* dinitial,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  ssd::DeltaArgs a = {};
+  SSD_TRY(check_delta(shape, false));
+  SSD_TRY(delta_inputs(shape, rows, q, k, v, dt, beta, A, dt_bias, flags, scale, in, false, &a));
+  if (!dy || !dq || !dk || !dv || !ddt || !dbeta || !dA) return SSD_ERR_NULL;
+  SSD_TRY(delta_rows(shape, grad_rows, &a.grows));
+  // blocks of four waves, one a (token, key group)
+  SSD_TRY(product({shape->batch, shape->seqlen, shape->ngroups}, (int64_t(1) << 25)));
+  if (!workspace || workspace_bytes < ssd_delta_rule_backward_workspace_bytes(shape)) return SSD_ERR_WORKSPACE;
+  const uintptr_t e = elem(in);
+  if (!aligned(dq, e) || !aligned(dk, e) || !aligned(dv, e) || !aligned(ddt, e) || !aligned(dbeta, e) || !a16(dy) ||
+      !a16(initial_states) || !a16(seq_idx) || !a16(dfinal) || !a16(dA) || !a16(ddt_bias) || !a16(dinitial) ||
+      !a16(workspace))
+    return SSD_ERR_ALIGN;
+  a.h0 = initial_states;
+  a.seq_idx = seq_idx;
+  a.dy = dy;
+  a.dfinal = dfinal;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.ddt = ddt;
+  a.dbeta = dbeta;
+  a.dA = dA;
+  a.ddt_bias = ddt_bias;
+  a.dinit = dinitial;
+  a.ws = static_cast<char*>(workspace);
+  return from_hip(ssd::launch_delta_backward(a, in == SSD_BF16, (hipStream_t)stream));
+}
+
 }  // extern "C"

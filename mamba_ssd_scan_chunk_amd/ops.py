@@ -926,3 +926,50 @@ def ssd_delta_step(q, k, v, dt, beta, A, state, dt_bias=None, softplus=True, sig
                                         _ptr(dt_bias), flags, scale, _DT[v.dtype], _ptr(state), _ptr(state_out),
                                         _ptr(y), _stream()))
     return y
+
+
+def ssd_delta_rule_backward_workspace_bytes(batch, seqlen, nheads, ngroups, dstate, headdim, dtype=None) -> int:
+    """``dtype`` (of the activations) makes no difference."""
+    return int(load_library().ssd_delta_rule_backward_workspace_bytes(SSDDeltaShape(batch, seqlen, nheads, headdim,
+                                                                                    dstate, ngroups)))
+
+
+def ssd_delta_rule_backward(q, k, v, dt, beta, A, dy, dt_bias=None, softplus=True, sigmoid=True, qk_norm=True,
+                            scale=None, initial_states=None, dfinal=None, seq_idx=None, want_dinitial=False,
+                            workspace=None, out=None, stream=None) -> Dict[str, Optional[torch.Tensor]]:
+    """Gradients of ssd_delta_rule for dL/dy = dy [B,L,H,P] and dL/dfinal =
+    dfinal (None: zero): dq, dk, dv, ddt, dbeta (of the raw dt and beta) in v's
+    dtype (given ``out`` tensors may be column slices), dA, ddt_bias, dinitial
+    fp32; None where the input is absent, dinitial unless ``want_dinitial``."""
+    if stream is not None:
+        return _on_stream(ssd_delta_rule_backward, locals())
+    sh, rows, flags, scale = _delta_inputs(q, k, v, dt, beta, A, dt_bias, softplus, sigmoid, qk_norm, scale, 2)
+    B, L, H, P, N, G = sh.batch, sh.seqlen, sh.nheads, sh.headdim, sh.dstate, sh.ngroups
+    io = (v.dtype,)
+    _req(dy, "dy", (B, L, H, P), io)
+    _opt(initial_states, "initial_states", (B, H, N, P), _F32)
+    _opt(dfinal, "dfinal", (B, H, N, P), _F32)
+    _opt(seq_idx, "seq_idx", (B, L), (torch.int32,))
+    wide = dict(dq=(B, L, G, N), dk=(B, L, G, N), dv=(B, L, H, P), ddt=(B, L, H), dbeta=(B, L, H))
+    flat = dict(dA=(H,), ddt_bias=(H,), dinitial=(B, H, N, P))
+    absent = {"ddt_bias": dt_bias is None, "dinitial": not want_dinitial}
+    given = dict(out or {})
+    r, grow = {}, {}
+    for n, shp in wide.items():
+        r[n] = given[n] if given.get(n) is not None else torch.empty(shp, device=v.device, dtype=v.dtype)
+        grow[n] = _req_rows(r[n], n, shp, io)
+    for n, shp in flat.items():
+        if absent.get(n):
+            r[n] = None
+            continue
+        r[n] = given[n] if given.get(n) is not None else torch.empty(shp, device=v.device)
+        _req(r[n], n, shp, _F32)
+    lib = load_library()
+    workspace, wsb = _workspace(workspace, lib.ssd_delta_rule_backward_workspace_bytes, (sh,), v.device)
+    check(lib.ssd_delta_rule_backward(
+        sh, rows, _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(A), _ptr(dt_bias), flags, scale, _DT[v.dtype],
+        _ptr(initial_states), _ptr(seq_idx), _ptr(dy), _ptr(dfinal),
+        SSDDeltaRows(grow["dq"], grow["dk"], grow["dv"], grow["ddt"], grow["dbeta"]), _ptr(r["dq"]), _ptr(r["dk"]),
+        _ptr(r["dv"]), _ptr(r["ddt"]), _ptr(r["dbeta"]), _ptr(r["dA"]), _ptr(r["ddt_bias"]), _ptr(r["dinitial"]),
+        _ptr(workspace), wsb, _stream()))
+    return r

@@ -184,3 +184,116 @@ def test_steps_go_on_from_a_prompt(dtype):
         yt = ops.ssd_delta_step(*(d[k][:, t] for k in ("q", "k", "v", "dt", "beta")), d["A"], st, dt_bias=d["dt_bias"])
         check(yt, wy[:, t], dtype, f"y of token {t}")
     check(st, wf, dtype, "state")
+
+
+# ---- gradients.  They pass through twice the products of a forward, and ddt, dA
+# and ddt_bias are sums of terms of both signs: twice the forward's bound, of the
+# largest value; a sum over the tokens of terms that may cancel takes the bound
+# of its terms' size.
+
+def check_grads(got, want, dtype, B, L):
+    for name, w in want.items():
+        g = got[name]
+        tol = 2 * bound(dtype) * w.abs().max().clamp(min=1e-30)
+        if name in ("dA", "ddt_bias"):
+            # each head's sum runs over B L terms of the size of ddt's
+            tol = tol + 2 * bound(dtype) * want["ddt"].abs().max() * (B * L) ** 0.5 * 8
+        half = 2.0 ** -8 if g.dtype == BF else 0.0
+        gd = g.double().cpu()
+        assert tuple(gd.shape) == tuple(w.shape), name
+        assert torch.isfinite(gd).all(), name
+        off = (gd - w).abs()
+        assert (off <= tol + half * w.abs()).all(), f"{name}: off by {float(off.max()):.3g} of {float(w.abs().max()):.3g}"
+
+
+def back(a, dy, dfinal=None, **how):
+    d = gpu(a)
+    h0 = d.pop("h0")
+    return ops.ssd_delta_rule_backward(d["q"], d["k"], d["v"], d["dt"], d["beta"], d["A"], dy.cuda(),
+                                       dt_bias=d["dt_bias"], initial_states=h0,
+                                       dfinal=None if dfinal is None else dfinal.cuda(),
+                                       want_dinitial=h0 is not None, **how)
+
+
+def cotangents(shape, dtype, seed):
+    B, L, H, G, N, P = shape
+    r = torch.Generator().manual_seed(seed)
+    return torch.randn(B, L, H, P, generator=r).to(dtype), torch.randn(B, H, N, P, generator=r)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_gradients(shape, dtype):
+    a = ref.inputs(*shape, dtype=dtype, seed=sum(shape))
+    dy, df = cotangents(shape, dtype, 7)
+    got = back(a, dy, df)
+    check_grads(got, ref.backward(a, dy, df), dtype, *shape[:2])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_gradients_flags_and_absent_arguments(dtype):
+    shape = (2, 90, 4, 2, 64, 32)
+    a = ref.inputs(*shape, dtype=dtype, seed=3, h0=False, bias=False)
+    a["beta"] = a["beta"].sigmoid().to(dtype)
+    a["beta"][:, ::7] = 0                       # tokens that write nothing still have a gradient
+    a["k"] = (a["k"].float() * 0.1).to(dtype)
+    a["dt"] = a["dt"].abs() * 0.1
+    how = dict(softplus=False, sigmoid=False, qk_norm=False, scale=0.25)
+    dy, _ = cotangents(shape, dtype, 8)
+    got = back(a, dy, **how)
+    assert got["ddt_bias"] is None and got["dinitial"] is None
+    check_grads(got, ref.backward(a, dy, **how), dtype, 2, 90)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("L,starts", [(1, 1), (64, 3), (200, 9), (130, 130)])
+def test_gradients_packed(L, starts, dtype):
+    shape = (2, L, 4, 2, 64, 48)
+    a = ref.inputs(*shape, dtype=dtype, seed=L)
+    idx = ref.packed(2, L, starts, seed=L)
+    dy, df = cotangents(shape, dtype, 9)
+    got = back(a, dy, df, seq_idx=idx.cuda())
+    check_grads(got, ref.backward(a, dy, df, seq_idx=idx), dtype, 2, L)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_gradients_nan_stays_in_its_sequence(dtype):
+    B, L = 1, 200
+    shape = (B, L, 2, 1, 64, 32)
+    a = ref.inputs(*shape, dtype=dtype, seed=5)
+    idx = torch.zeros((B, L), dtype=torch.int32)
+    idx[:, 40:] = 1
+    idx[:, 70:] = 2
+    idx[:, 180:] = 3
+    dy, df = cotangents(shape, dtype, 10)
+    want = ref.backward(a, dy, df, seq_idx=idx)
+    for name, bad in [("v", float("nan")), ("q", float("inf")), ("k", float("nan")), ("dt", float("nan")),
+                      ("beta", float("nan")), ("dy", float("nan"))]:
+        d = dict(a, dy=dy)
+        d[name] = d[name].clone()
+        d[name][:, 50] = bad
+        d[name][:, 100] = bad
+        dyb = d.pop("dy")
+        got = back(d, dyb, df, seq_idx=idx.cuda())
+        for s in (slice(0, 40), slice(180, L)):
+            part = {n: got[n][:, s] for n in ("dq", "dk", "dv", "ddt", "dbeta")}
+            w = {n: want[n][:, s] for n in part}
+            check_grads(part, w, dtype, B, L)
+        check_grads({"dinitial": got["dinitial"]}, {"dinitial": want["dinitial"]}, dtype, B, L)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_gradients_into_column_slices(dtype):
+    B, L, H, G, N, P = shape = (2, 70, 4, 2, 64, 32)
+    a = ref.inputs(*shape, dtype=dtype, seed=12)
+    dy, df = cotangents(shape, dtype, 11)
+    dense = back(a, dy, df)
+    wide = torch.full((B, L, 2 * G * N + H * P + 3), 5.0, device="cuda", dtype=dtype)
+    ab = torch.full((B, L, 2 * H + 1), 5.0, device="cuda", dtype=dtype)
+    out = dict(dq=wide[..., :G * N].unflatten(-1, (G, N)), dk=wide[..., G * N:2 * G * N].unflatten(-1, (G, N)),
+               dv=wide[..., 2 * G * N:2 * G * N + H * P].unflatten(-1, (H, P)), ddt=ab[..., :H],
+               dbeta=ab[..., H:2 * H])
+    got = back(a, dy, df, out=out)
+    for n in out:
+        assert torch.equal(got[n], dense[n]), n
+    assert (wide[..., -3:] == 5).all() and (ab[..., -1:] == 5).all()
