@@ -590,6 +590,61 @@ ssd_status ssd_delta_rule_backward(const ssd_delta_shape* shape, const ssd_delta
                                    void* workspace, size_t workspace_bytes, void* stream);
 size_t ssd_delta_rule_backward_workspace_bytes(const ssd_delta_shape* shape);
 
+/* ------------------------------------------------------------------------
+ * Norm of groups of a token's channels with an activation, between a scan and
+ * the output projection, and activations kept in 8 bits for the backward pass.
+ * Conventions of the layer's operators above.
+ *
+ * Per row of `dim` columns in `groups` groups of S = dim / groups, with
+ * act(z) = z / (1 + exp(-z)) and a gate z (optional):
+ *   r  = x,  or x act(z)                        (SSD_GROUP_GATE_FIRST)
+ *   xh = (r - mean) rstd,  rstd = 1 / sqrt(mean((r - mean)^2) + eps), sums over
+ *        the group                               (SSD_GROUP_RMS: mean = 0)
+ *   y  = xh w + bias,  times act(z)              (a gate without GATE_FIRST)
+ *                      or y = act(xh w + bias)   (SSD_GROUP_SILU, without a gate behind)
+ * x [rows,dim] dense, z rows (z_row), y [rows,dim] in `in`; w, bias (optional)
+ * fp32 [dim], or [S] for all groups (SSD_GROUP_SHARED); mean (NULL exactly for
+ * RMS) and rstd fp32 [rows,groups].  S <= 16384, rows groups < 2^31 (else
+ * SSD_ERR_UNSUPPORTED).
+ * ------------------------------------------------------------------------ */
+#define SSD_GROUP_RMS 1
+#define SSD_GROUP_GATE_FIRST 2
+#define SSD_GROUP_SILU 4
+#define SSD_GROUP_SHARED 8
+
+ssd_status ssd_group_norm(int64_t rows, int64_t dim, int64_t groups, const void* x, ssd_dtype in, const void* z,
+                          int64_t z_row, const float* w, const float* bias, float eps, int flags, void* y, float* mean,
+                          float* rstd, void* stream);
+
+/*
+ * Gradients for dL/dy = dy [rows,dim] (`in`), with mean and rstd the
+ * forward's: dx [rows,dim] and dz rows (dz_row; given exactly when z is) in
+ * `in`; dw and dbias (optional) fp32, like w.  Where x_scale is given, x (and z,
+ * with z_scale; both or neither) are in 8 bits as ssd_pack8 leaves them: x, z
+ * int8 [rows,dim] dense, the scales bf16 [rows, ceil(dim/64)].  Workspace:
+ * ssd_group_norm_backward_workspace_bytes(rows, dim, groups) bytes.
+ */
+ssd_status ssd_group_norm_backward(int64_t rows, int64_t dim, int64_t groups, const void* dy, ssd_dtype in,
+                                   const void* x, const void* x_scale, const void* z, int64_t z_row,
+                                   const void* z_scale, const float* w, const float* bias, const float* mean,
+                                   const float* rstd, int flags, void* dx, void* dz, int64_t dz_row, float* dw,
+                                   float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+size_t ssd_group_norm_backward_workspace_bytes(int64_t rows, int64_t dim, int64_t groups);
+
+/*
+ * Rows of `dim` values (x_row elements apart, 0 = dense) into 8 bits: 64
+ * consecutive values share a scale s, the least bf16 with 127 s >= their
+ * largest magnitude, and are held as q = round(x / s), ties to even, -127 ..
+ * 127 (0 where s = 0); they come back as q s.  A block with an infinity or NaN has
+ * s = NaN and comes back as NaN.  q int8 [rows,dim], scale bf16
+ * [rows, ceil(dim/64)], dense, of any alignment to their elements.
+ * rows < 2^31, dim <= 2^24, rows ceil(dim/64) < 2^36 (else SSD_ERR_UNSUPPORTED).
+ */
+ssd_status ssd_pack8(int64_t rows, int64_t dim, const void* x, int64_t x_row, ssd_dtype in, int8_t* q, void* scale,
+                     void* stream);
+ssd_status ssd_unpack8(int64_t rows, int64_t dim, const int8_t* q, const void* scale, void* x, int64_t x_row,
+                       ssd_dtype in, void* stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char* ssd_status_string(ssd_status status);
 

@@ -62,6 +62,7 @@ class SSDDeltaRows(ctypes.Structure):
 
 
 SSD_DELTA_SOFTPLUS, SSD_DELTA_SIGMOID, SSD_DELTA_QK_NORM = 1, 2, 4
+SSD_GROUP_RMS, SSD_GROUP_GATE_FIRST, SSD_GROUP_SILU, SSD_GROUP_SHARED = 1, 2, 4, 8
 
 _P = ctypes.c_void_p
 _S = ctypes.POINTER(SSDShape)
@@ -108,6 +109,12 @@ _SIGNATURES = {
     "ssd_delta_rule_backward": (ctypes.c_int, _DELTA_IN + [_P, _P, _P, _P, _DR] + [_P] * 8 + [_P, _Z, _P]),
     "ssd_delta_rule_backward_workspace_bytes": (_Z, [_DS]),
     "ssd_delta_step": (ctypes.c_int, _DELTA_IN + [_P, _P, _P, _P]),
+    "ssd_group_norm": (ctypes.c_int, [_I, _I, _I, _P, _E, _P, _I, _P, _P, _F, ctypes.c_int, _P, _P, _P, _P]),
+    "ssd_group_norm_backward": (ctypes.c_int, [_I, _I, _I, _P, _E, _P, _P, _P, _I, _P, _P, _P, _P, _P, ctypes.c_int,
+                                               _P, _P, _I, _P, _P, _P, _Z, _P]),
+    "ssd_group_norm_backward_workspace_bytes": (_Z, [_I, _I, _I]),
+    "ssd_pack8": (ctypes.c_int, [_I, _I, _P, _I, _E, _P, _P, _P]),
+    "ssd_unpack8": (ctypes.c_int, [_I, _I, _P, _P, _P, _I, _E, _P]),
     "ssd_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "ssd_abi_version": (ctypes.c_int, []),
 }

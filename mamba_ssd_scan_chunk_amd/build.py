@@ -23,7 +23,7 @@ SOURCES = ["chunk_cumsum.hip", "chunk_state.hip", "chunk_state_hg.hip", "state_p
            "chunk_scan.hip", "chunk_scan_hg.hip", "decode.hip", "varlen_states.hip", "backward.hip", "bwd_dbc.hip",
            "ssd_api.cpp", "tuning.cpp", "forward_noalloc.hip", "causal_conv.hip", "selective_scan.hip",
            "selective_scan_bwd.hip", "layer_norm.hip", "layer_api.cpp", "delta_rule.hip", "delta_rule_bwd.hip",
-           "delta_api.cpp"]
+           "delta_api.cpp", "group_norm.hip", "group_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

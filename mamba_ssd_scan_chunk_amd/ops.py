@@ -14,8 +14,9 @@ from typing import Dict, Optional, Tuple
 
 import torch
 
-from ._lib import (MMA, SSD_BF16, SSD_DELTA_QK_NORM, SSD_DELTA_SIGMOID, SSD_DELTA_SOFTPLUS, SSD_F32, SSDConvShape,
-                   SSDDeltaRows, SSDDeltaShape, SSDScanRows, SSDScanShape, SSDShape, check, load_library)
+from ._lib import (MMA, SSD_BF16, SSD_DELTA_QK_NORM, SSD_DELTA_SIGMOID, SSD_DELTA_SOFTPLUS, SSD_F32,
+                   SSD_GROUP_GATE_FIRST, SSD_GROUP_RMS, SSD_GROUP_SHARED, SSD_GROUP_SILU, SSDConvShape, SSDDeltaRows,
+                   SSDDeltaShape, SSDScanRows, SSDScanShape, SSDShape, check, load_library)
 
 _DT = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
 _DTNAME = {"f32": torch.float32, "bf16": torch.bfloat16}
@@ -973,3 +974,177 @@ def ssd_delta_rule_backward(q, k, v, dt, beta, A, dy, dt_bias=None, softplus=Tru
         _ptr(r["dv"]), _ptr(r["ddt"]), _ptr(r["dbeta"]), _ptr(r["dA"]), _ptr(r["ddt_bias"]), _ptr(r["dinitial"]),
         _ptr(workspace), wsb, _stream()))
     return r
+
+
+def _flat_rows(t, name: str, shape, dtypes) -> int:
+    """Checks ``t`` [..., D] whose rows may be column slices of wider rows that
+    follow each other evenly; returns the row stride in elements (0: dense)."""
+    if t is not None and t.dim() > 2 and tuple(t.shape) == tuple(shape) and not t.is_contiguous():
+        try:
+            t = t.view(-1, shape[-1])
+        except RuntimeError:
+            raise ValueError(f"{name}'s rows must follow each other evenly") from None
+        shape = t.shape
+    return _req_rows(t, name, shape, dtypes, 1)
+
+
+def _group_flags(weight, D: int, groups: int, rms, gate_first, silu, z) -> int:
+    if groups <= 0 or D % groups:
+        raise ValueError(f"{D} columns are not {groups} equal groups")
+    shared = groups > 1 and weight.dim() == 1 and weight.shape[0] == D // groups
+    _req(weight, "weight", (D // groups if shared else D,), _F32)
+    if gate_first and z is None:
+        raise ValueError("gate_first needs a gate z")
+    if silu and z is not None and not gate_first:
+        raise ValueError("silu is of the norm's own output: no gate behind it")
+    return (SSD_GROUP_RMS * bool(rms) | SSD_GROUP_GATE_FIRST * bool(gate_first) | SSD_GROUP_SILU * bool(silu) |
+            SSD_GROUP_SHARED * shared)
+
+
+def ssd_group_norm(x, weight, bias=None, z=None, groups=1, eps=1e-5, rms=True, gate_first=False, silu=False, y=None,
+                   mean=None, rstd=None, stream=None):
+    """RMS norm (layer norm unless ``rms``) of each of the ``groups`` groups of
+    x's columns [..., D], with an activation: times silu(z) behind the norm or
+    in front of it (``gate_first``), z [..., D] maybe a column slice, or SiLU of
+    the norm's own output (``silu``).  weight and bias fp32 [D], or [D/groups]
+    for all groups.  Returns (y, mean or None for rms, rstd), the statistics
+    [..., groups] fp32."""
+    if stream is not None:
+        return _on_stream(ssd_group_norm, locals())
+    shp = x.shape
+    D, st = shp[-1], shp[:-1] + (groups,)
+    rows = shp[:-1].numel()
+    _req(x, "x", shp, _IO)
+    flags = _group_flags(weight, D, groups, rms, gate_first, silu, z)
+    _opt(bias, "bias", tuple(weight.shape), _F32)
+    z_row = 0 if z is None else _flat_rows(z, "z", shp, (x.dtype,))
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _req(y, "y", shp, (x.dtype,))
+    if rms:
+        mean = None
+    elif mean is None:
+        mean = weight.new_empty(st)
+    else:
+        _req(mean, "mean", st, _F32)
+    if rstd is None:
+        rstd = weight.new_empty(st)
+    else:
+        _req(rstd, "rstd", st, _F32)
+    check(load_library().ssd_group_norm(rows, D, groups, _ptr(x), _DT[x.dtype], _ptr(z), z_row, _ptr(weight),
+                                        _ptr(bias), float(eps), flags, _ptr(y), _ptr(mean), _ptr(rstd), _stream()))
+    return y, mean, rstd
+
+
+def ssd_group_norm_backward_workspace_bytes(rows, dim, groups) -> int:
+    return int(load_library().ssd_group_norm_backward_workspace_bytes(rows, dim, groups))
+
+
+def _kept8(t, name: str, shape):
+    """The checked (values, scales) pair of ssd_pack8."""
+    if not isinstance(t, (tuple, list)) or len(t) != 2:
+        raise ValueError(f"{name} must be kept in 8 bits, (values, scales), like x")
+    _req(t[0], name, shape, (torch.int8,))
+    _req(t[1], f"{name}'s scales", tuple(shape[:-1]) + (-(-shape[-1] // 64),), (torch.bfloat16,))
+    return t
+
+
+def ssd_group_norm_backward(dy, x, weight, mean, rstd, bias=None, z=None, groups=1, rms=True, gate_first=False,
+                            silu=False, workspace=None, out=None, stream=None) -> Dict[str, Optional[torch.Tensor]]:
+    """Gradients of ssd_group_norm for dL/dy = dy: mean (None for rms) and rstd
+    are the forward's; x and z are tensors, or both the (values, scales) that
+    ssd_pack8 returned for them.  Returns a dict of dx and dz (dy's dtype; a
+    given ``out["dz"]`` may be a column slice), dweight and dbias (fp32); dz and
+    dbias None without a gate, a bias."""
+    if stream is not None:
+        return _on_stream(ssd_group_norm_backward, locals())
+    shp = dy.shape
+    D, st = shp[-1], shp[:-1] + (groups,)
+    rows = shp[:-1].numel()
+    _req(dy, "dy", shp, _IO)
+    io = (dy.dtype,)
+    flags = _group_flags(weight, D, groups, rms, gate_first, silu, z)
+    _opt(bias, "bias", tuple(weight.shape), _F32)
+    _req(rstd, "rstd", st, _F32)
+    if not rms:
+        _req(mean, "mean", st, _F32)
+    xs = zs = None
+    z_row = 0
+    if isinstance(x, (tuple, list)):
+        x, xs = _kept8(x, "x", shp)
+        if z is not None:
+            z, zs = _kept8(z, "z", shp)
+    else:
+        _req(x, "x", shp, io)
+        if z is not None:
+            if isinstance(z, (tuple, list)):
+                raise ValueError("z is kept in 8 bits and x is not")
+            z_row = _flat_rows(z, "z", shp, io)
+    r = dict(dx=None, dz=None, dweight=None, dbias=None)
+    if out:
+        r.update(out)
+    if r["dx"] is None:
+        r["dx"] = torch.empty_like(dy)
+    else:
+        _req(r["dx"], "dx", shp, io)
+    dz_row = 0
+    if z is None:
+        r["dz"] = None
+    elif r["dz"] is None:
+        r["dz"] = torch.empty_like(dy)
+    else:
+        dz_row = _flat_rows(r["dz"], "dz", shp, io)
+    for k, wanted in (("dweight", True), ("dbias", bias is not None)):
+        if not wanted:
+            r[k] = None
+        elif r[k] is None:
+            r[k] = torch.empty_like(weight)
+        else:
+            _req(r[k], k, tuple(weight.shape), _F32)
+    lib = load_library()
+    workspace, wsb = _workspace(workspace, lib.ssd_group_norm_backward_workspace_bytes, (rows, D, groups), dy.device)
+    check(lib.ssd_group_norm_backward(rows, D, groups, _ptr(dy), _DT[dy.dtype], _ptr(x), _ptr(xs), _ptr(z), z_row,
+                                      _ptr(zs), _ptr(weight), _ptr(bias), _ptr(None if rms else mean), _ptr(rstd),
+                                      flags, _ptr(r["dx"]), _ptr(r["dz"]), dz_row, _ptr(r["dweight"]),
+                                      _ptr(r["dbias"]), _ptr(workspace), wsb, _stream()))
+    return r
+
+
+def ssd_pack8(x, q=None, scale=None, stream=None):
+    """Rows x [..., D] (maybe a column slice) in 8 bits: (values int8 [..., D],
+    scales bf16 [..., ceil(D/64)]).  64 values share a scale, the least bf16 that
+    times 127 reaches their largest magnitude, and are its nearest multiples; a
+    block with an infinity or NaN comes back as NaN."""
+    if stream is not None:
+        return _on_stream(ssd_pack8, locals())
+    shp = x.shape
+    D = shp[-1]
+    row = _flat_rows(x, "x", shp, _IO)
+    sshape = tuple(shp[:-1]) + (-(-D // 64),)
+    if q is None:
+        q = torch.empty(shp, device=x.device, dtype=torch.int8)
+    else:
+        _req(q, "q", shp, (torch.int8,))
+    if scale is None:
+        scale = torch.empty(sshape, device=x.device, dtype=torch.bfloat16)
+    else:
+        _req(scale, "scale", sshape, (torch.bfloat16,))
+    check(load_library().ssd_pack8(shp[:-1].numel(), D, _ptr(x), row, _DT[x.dtype], _ptr(q), _ptr(scale), _stream()))
+    return q, scale
+
+
+def ssd_unpack8(q, scale, x=None, dtype=torch.bfloat16, stream=None):
+    """The values that ssd_pack8's results stand for, in ``x`` [..., D] where
+    given (maybe a column slice), else in a new tensor of ``dtype``."""
+    if stream is not None:
+        return _on_stream(ssd_unpack8, locals())
+    shp = q.shape
+    q, scale = _kept8((q, scale), "q", shp)
+    row = 0
+    if x is None:
+        x = torch.empty(shp, device=q.device, dtype=dtype)
+    row = _flat_rows(x, "x", shp, _IO)
+    check(load_library().ssd_unpack8(shp[:-1].numel(), shp[-1], _ptr(q), _ptr(scale), _ptr(x), row, _DT[x.dtype],
+                                     _stream()))
+    return x
