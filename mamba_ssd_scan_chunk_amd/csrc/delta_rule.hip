@@ -56,7 +56,12 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaWs
   const int64_t grp = h / (a.H / a.G);
   const int n = (int)(a.L - t0 < kC ? a.L - t0 : kC);
   const uint8_t* marks = !BACK && a.nseq > 0 ? reinterpret_cast<const uint8_t*>(a.ws + ws.marks) : nullptr;
-  const uint64_t cuts = a.seq_idx || marks ? window_cuts(a.seq_idx, marks, row, t0, a.L, lane).piece : 0;
+  Cuts both = {0, 0};
+  if (a.seq_idx || marks) {
+    both = window_cuts(a.seq_idx, marks, row, t0, a.L, lane);
+    if (h == 0 && threadIdx.x == 0) reinterpret_cast<Cuts*>(a.ws + ws.cuts)[b * ws.nw + win] = both;
+  }
+  const uint64_t cuts = both.piece;
   DeltaGates* gates = reinterpret_cast<DeltaGates*>(a.ws + ws.gates) + bhw;
 
   if (wave == 0) {
@@ -249,15 +254,6 @@ constexpr int chain_pitch() { return NP + 16 / (int)sizeof(typename M::IO::type)
 template <class M, int NP, bool SAVE>
 constexpr size_t chain_lds() {
   return (size_t)(SAVE ? 1 : 2) * kC * chain_pitch<M, NP>() * sizeof(typename M::IO::type) + 5 * kC * 4;
-}
-
-// Eight slots of two accumulator tiles.
-__device__ __forceinline__ void slots(const f32x4_t& lo, const f32x4_t& hi, float* o) {
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    o[r] = lo[r];
-    o[4 + r] = hi[r];
-  }
 }
 
 // SAVE: for the gradients, the state in front of every window and w instead of y.
@@ -469,6 +465,278 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs w
   }
 }
 
+// ---------------------------------------------------------------- the chain of bf16 inputs
+// C column waves and C helpers, a block a compute unit.  A step takes a piece:
+// the column waves correct its values and update their state, which is the
+// chain's length; the helpers load the next piece's operands into the other
+// half of LDS and work out the outputs of the piece before, from the operands
+// (state, u) that the column waves left in LDS.
+template <int NP, int C>
+struct ChainLds {
+  static constexpr int kPitch = NP + 8;
+  static constexpr int kRows = kC * kPitch * 2;
+  static constexpr int kX = (NP / 32 + 2) * 2048;  // operands of a column wave: state and u
+  static constexpr int k = 0, r = k + kRows, g = r + kTriBytes, half = g + 5 * kC * 4;
+  static constexpr int q = 2 * half, x = q + 2 * kRows, total = x + 2 * C * kX;
+};
+
+template <int NP, int C, bool VL, bool SAVE>
+__global__ __launch_bounds__(128 * C) void delta_chain_bf16_kernel(DeltaArgs a, DeltaWs ws) {
+  typedef DeltaB M;
+  typedef DeltaB::Two Two;
+  typedef ChainLds<NP, C> Lay;
+  constexpr int NT = NP / 16, KS = NP / 32, LP = Lay::kPitch, NH = 64 * C;
+  extern __shared__ __align__(16) char lds[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const uint32_t bid = near_block(blockIdx.x, gridDim.x);
+  const uint32_t slices = (uint32_t)(a.P / 16) / C;
+  const int64_t bh = bid / slices, h = bh % a.H, b = bh / a.H, grp = h / (a.H / a.G);
+  const int64_t p = ((bid % slices) * C + wave % C) * 16 + c;
+  const int N = (int)a.N;
+  const int64_t row = b * a.L;
+  const uint8_t* marks = VL && !SAVE && a.nseq > 0 ? reinterpret_cast<const uint8_t*>(a.ws + ws.marks) : nullptr;
+  Pieces pc;
+  pc.first(VL ? reinterpret_cast<const Cuts*>(a.ws + ws.cuts) + b * ws.nw : nullptr, ws.nw, a.L);
+
+  if (wave >= C) {
+    // ---- helper
+    const int ht = tid - NH;
+    RowTile<NP, NH> kt, qt;
+    Run<kTriBytes / 16 / NH> rt;
+    GateTile<NH> gt;
+    const uint16_t* kb = static_cast<const uint16_t*>(a.k) + row * a.rows.k + grp * N;
+    const uint16_t* qb = static_cast<const uint16_t*>(a.q) + row * a.rows.q + grp * N;
+    auto ask = [&](const Pieces& s) {
+      const int64_t bhw = bh * ws.nw + s.win;
+      kt.load(kb + s.win * kC * a.rows.k, a.rows.k, N, s.begin, s.end, ht);
+      rt.load(a.ws + ws.low_r + bhw * kTriBytes, ht, NH);
+      gt.load(reinterpret_cast<const DeltaGates*>(a.ws + ws.gates) + bhw, s.begin, s.end, ht);
+    };
+    auto put = [&](int half) {
+      char* o = lds + half * Lay::half;
+      kt.store(reinterpret_cast<uint16_t*>(o + Lay::k), LP, ht);
+      rt.store(o + Lay::r, ht, NH);
+      gt.store(reinterpret_cast<float*>(o + Lay::g), ht);
+    };
+    ask(pc);
+    put(0);
+    __syncthreads();
+    Two pf[kTriFrags];
+    float4 qin[4];
+    int64_t t0 = 0;
+    int begin = 0, end = 0;
+    for (int j = 0;; ++j) {
+      // pc: piece j, which the column waves take now
+      const bool more = pc.valid();
+      Pieces nx = pc;
+      if (more) nx.step();
+      const bool ahead = more && nx.valid();
+      if (ahead) ask(nx);
+      if (!SAVE && more)
+        qt.load(qb + pc.win * kC * a.rows.q, a.rows.q, N, pc.begin, pc.end, ht);
+      if (!SAVE && j > 0) {
+        const char* x = lds + Lay::x + (((j - 1) & 1) * C + wave % C) * Lay::kX;
+        const uint16_t* ql = reinterpret_cast<const uint16_t*>(lds + Lay::q + ((j - 1) & 1) * Lay::kRows);
+        f32x4_t y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const Two sb = M::load(x + s * 2048, lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint16_t* qp = ql + (16 * i + c) * LP + 32 * s + 4 * g;
+            y[i] = M::mma(lds_4x2<M>(qp, qp + 16), sb, y[i]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] *= f32x4_t{qin[i].x, qin[i].y, qin[i].z, qin[i].w};
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const Two ub = M::load(x + (KS + s) * 2048, lane);
+#pragma unroll
+          for (int i = 2 * s; i < 4; ++i) y[i] = M::mma(pf[low_frag(i, s)], ub, y[i]);
+        }
+        uint16_t* yp = static_cast<uint16_t*>(a.y) + ((row + t0) * a.H + h) * a.P + p;
+        const int64_t ystep = a.H * a.P;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int t = 16 * i + 4 * g + r;
+            if (t >= begin && t < end) yp[t * ystep] = M::IO::put(y[i][r]);
+          }
+      }
+      if (!more) break;
+      if constexpr (!SAVE) {
+        // kept for the next step, when piece j is worked out
+        const int64_t bhw = bh * ws.nw + pc.win;
+        const char* fp = a.ws + ws.low_p + bhw * kTriBytes;
+#pragma unroll
+        for (int f = 0; f < kTriFrags; ++f) pf[f] = M::load(fp + f * 2048, lane);
+        const float* sq = reinterpret_cast<const float*>(lds + (j & 1) * Lay::half + Lay::g) + 2 * kC;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qin[i] = *reinterpret_cast<const float4*>(sq + 16 * i + 4 * g);
+        qt.store(reinterpret_cast<uint16_t*>(lds + Lay::q + (j & 1) * Lay::kRows), LP, ht);
+        t0 = pc.win * kC;
+        begin = pc.begin;
+        end = pc.end;
+      }
+      if (ahead) put((j + 1) & 1);
+      pc = nx;
+      __syncthreads();
+      if (SAVE && !ahead) break;
+    }
+    return;
+  }
+
+  // ---- column wave
+  f32x4_t S[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int nn = 16 * j + 4 * g + r;
+      S[j][r] = a.h0 && nn < N ? a.h0[(bh * N + nn) * a.P + p] : 0.f;
+    }
+  const uint16_t* vb = static_cast<const uint16_t*>(a.v) + row * a.rows.v + h * a.P + p;
+  uint16_t vn[16];
+  auto ask_v = [&](const Pieces& s) {
+    const uint16_t* vp = vb + s.win * kC * a.rows.v;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int t = 16 * (e / 4) + 4 * g + e % 4;
+      vn[e] = 0;
+      if (t >= s.begin && t < s.end) vn[e] = vp[t * a.rows.v];
+    }
+  };
+  ask_v(pc);
+  __syncthreads();
+  for (int step = 0; pc.valid(); ++step) {
+    const int begin = pc.begin, end = pc.end;
+    const int64_t win = pc.win, bhw = bh * ws.nw + win;
+    const char* in = lds + (step & 1) * Lay::half;
+    const uint16_t* kt = reinterpret_cast<const uint16_t*>(in + Lay::k);
+    const float* gt = reinterpret_cast<const float*>(in + Lay::g);
+    const float *sBeta = gt, *sKin = gt + kC, *sKout = gt + 3 * kC, *sIn = gt + 4 * kC;
+    char* x = lds + Lay::x + ((step & 1) * C + wave) * Lay::kX;
+    if (VL && pc.fresh()) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) S[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    if (SAVE && begin == 0) {
+      float* out = reinterpret_cast<float*>(a.ws + ws.S) + bhw * N * a.P + p;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int nn = 16 * j + 4 * g + r;
+          if (nn < N) out[nn * a.P] = S[j][r];
+        }
+    }
+    f32x4_t X[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) X[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      float v[8];
+      slots(S[2 * s], S[2 * s + 1], v);
+      const Two sb = M::two(v);
+      if constexpr (!SAVE) M::store(x + s * 2048, lane, sb);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint16_t* kp = kt + (16 * i + c) * LP + 32 * s + 4 * g;
+        X[i] = M::mma(lds_4x2<M>(kp, kp + 16), sb, X[i]);
+      }
+    }
+    // X = v - e^G k S
+    float be[4][4], bx[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 kin = *reinterpret_cast<const float4*>(sKin + 16 * i + 4 * g);
+      const float4 q = *reinterpret_cast<const float4*>(sBeta + 16 * i + 4 * g);
+      const float ki[4] = {kin.x, kin.y, kin.z, kin.w};
+      be[i][0] = q.x; be[i][1] = q.y; be[i][2] = q.z; be[i][3] = q.w;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        X[i][r] = bf16_bits_to_f32(vn[4 * i + r]) - ki[r] * X[i][r];
+        bx[i][r] = be[i][r] * X[i][r];
+      }
+    }
+    pc.step();
+    if (pc.valid()) ask_v(pc);
+    // w = X + R (b X); u = b w
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = bx[2 * s + e / 4][e % 4];
+      const Two xb = M::two(v);
+#pragma unroll
+      for (int i = 2 * s; i < 4; ++i) X[i] = M::mma(M::load(in + Lay::r + low_frag(i, s) * 2048, lane), xb, X[i]);
+    }
+    if constexpr (SAVE) {
+      float* out = reinterpret_cast<float*>(a.ws + ws.w) + bhw * kC * a.P + p;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = 16 * i + 4 * g + r;
+          if (t >= begin && t < end) out[t * a.P] = X[i][r];
+        }
+    }
+    const float whole = sIn[end - 1];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) S[j] *= whole;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      float v[8], u[8];
+#pragma unroll
+      for (int t4 = 0; t4 < 2; ++t4) {
+        const float4 ko = *reinterpret_cast<const float4*>(sKout + 32 * s + 16 * t4 + 4 * g);
+        const float k4[4] = {ko.x, ko.y, ko.z, ko.w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = 32 * s + 16 * t4 + 4 * g + r, e = 4 * t4 + r;
+          u[e] = !VL || (t >= begin && t < end) ? be[2 * s + t4][r] * X[2 * s + t4][r] : 0.f;
+          v[e] = u[e] * k4[r];
+        }
+      }
+      if constexpr (!SAVE) M::store(x + (KS + s) * 2048, lane, M::two(u));
+      const Two ub = M::two(v);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) S[j] = M::mma(M::transposed(kt + 32 * s * LP + 16 * j, LP, lane), ub, S[j]);
+    }
+    if constexpr (VL) {
+      const int64_t last = row + win * kC + end - 1;
+      if (marks && marks[last]) {
+        for (int64_t s = 0; s < a.nseq; ++s) {
+          if (a.seq_last[s] != last) continue;
+          float* out = a.seq_states + (s * a.H + h) * N * a.P + p;
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int nn = 16 * j + 4 * g + r;
+              if (nn < N) out[nn * a.P] = S[j][r];
+            }
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if (!SAVE && a.hfin) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int nn = 16 * j + 4 * g + r;
+        if (nn < N) a.hfin[(bh * N + nn) * a.P + p] = S[j][r];
+      }
+  }
+}
+
 // ---------------------------------------------------------------- one token
 // A block takes 64 value columns of a (row, head): 16 threads of four columns
 // by 16 state rows, whose up to 16 rows a thread are all asked for first.
@@ -614,6 +882,25 @@ static hipError_t chain(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) {
   hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * a.H * (a.P / 16 / w))), dim3(64 * w), lds, s, a, ws);
   return hipGetLastError();
 }
+template <int NP, int C, bool VL, bool SAVE>
+static hipError_t chain_bf16(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) {
+  auto kern = delta_chain_bf16_kernel<NP, C, VL, SAVE>;
+  const size_t lds = SAVE ? ChainLds<NP, C>::q : ChainLds<NP, C>::total;
+  hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * a.H * (a.P / 16 / C))), dim3(128 * C), lds, s, a, ws);
+  return hipGetLastError();
+}
+template <int NP, int C>
+static hipError_t chain_bf16_of(const DeltaArgs& a, const DeltaWs& ws, bool save, hipStream_t s) {
+  const bool vl = a.seq_idx || (!save && a.nseq > 0);
+  if (save) return vl ? chain_bf16<NP, C, true, true>(a, ws, s) : chain_bf16<NP, C, false, true>(a, ws, s);
+  return vl ? chain_bf16<NP, C, true, false>(a, ws, s) : chain_bf16<NP, C, false, false>(a, ws, s);
+}
+template <int NP>
+static hipError_t chain_bf16_at(const DeltaArgs& a, const DeltaWs& ws, bool save, hipStream_t s) {
+  return a.P % 32 == 0 ? chain_bf16_of<NP, 2>(a, ws, save, s) : chain_bf16_of<NP, 1>(a, ws, save, s);
+}
 template <class M, int NP>
 static hipError_t chain_of(const DeltaArgs& a, const DeltaWs& ws, bool save, hipStream_t s) {
   const bool vl = a.seq_idx || (!save && a.nseq > 0);
@@ -628,7 +915,11 @@ static hipError_t chain_at(const DeltaArgs& a, const DeltaWs& ws, bool save, hip
   return chain_of<M, 256>(a, ws, save, s);
 }
 hipError_t launch_delta_chain(const DeltaArgs& a, const DeltaWs& ws, bool save, bool bf16, hipStream_t s) {
-  return bf16 ? chain_at<DeltaB>(a, ws, save, s) : chain_at<DeltaF>(a, ws, save, s);
+  if (!bf16) return chain_at<DeltaF>(a, ws, save, s);
+  if (a.N <= 32) return chain_bf16_at<32>(a, ws, save, s);
+  if (a.N <= 64) return chain_bf16_at<64>(a, ws, save, s);
+  if (a.N <= 128) return chain_bf16_at<128>(a, ws, save, s);
+  return chain_of<DeltaB, 256>(a, ws, save, s);  // two halves of LDS do not hold 256 key columns
 }
 
 hipError_t launch_delta_forward(const DeltaArgs& a, bool bf16, hipStream_t s) {

@@ -175,6 +175,140 @@ __device__ __forceinline__ int piece_begin(uint64_t cuts, int e) {
   return before ? 63 - (int)__builtin_clzll(before) : 0;
 }
 
+// The pieces of a row in order.  The windows' cuts come from the preparation,
+// the next one's asked for while one is walked.
+struct Pieces {
+  int64_t win, nw, L;
+  const Cuts* list;  // of the row, or null: a piece a window
+  Cuts cuts, next;
+  int begin, end, n;
+  __device__ __forceinline__ Cuts at(int64_t w) const {
+    const Cuts none = {0, 0};
+    return list && w >= 0 && w < nw ? list[w] : none;
+  }
+  // waited for and put into scalars where it is taken over
+  __device__ __forceinline__ static Cuts uniform(const Cuts& c) { return {uniform64(c.piece), uniform64(c.fresh)}; }
+  __device__ __forceinline__ int tokens() const { return (int)(L - win * kC < kC ? L - win * kC : kC); }
+  __device__ __forceinline__ void first(const Cuts* l, int64_t windows, int64_t len) {
+    list = l;
+    nw = windows;
+    L = len;
+    win = 0;
+    cuts = uniform(at(0));
+    next = at(1);
+    begin = 0;
+    n = tokens();
+    end = piece_end(cuts.piece, 0, n);
+  }
+  __device__ __forceinline__ bool valid() const { return win < nw; }
+  __device__ __forceinline__ void step() {
+    if (end < n) {
+      begin = end;
+    } else {
+      ++win;
+      cuts = uniform(next);
+      next = at(win + 1);
+      begin = 0;
+      n = tokens();
+    }
+    end = piece_end(cuts.piece, begin, n);
+  }
+  // back to front
+  __device__ __forceinline__ void last(const Cuts* l, int64_t windows, int64_t len) {
+    list = l;
+    nw = windows;
+    L = len;
+    win = nw - 1;
+    cuts = uniform(at(win));
+    next = at(win - 1);
+    end = n = tokens();
+    begin = piece_begin(cuts.piece, end);
+  }
+  __device__ __forceinline__ bool valid_back() const { return win >= 0; }
+  __device__ __forceinline__ void step_back() {
+    if (begin > 0) {
+      end = begin;
+    } else {
+      --win;
+      cuts = uniform(next);
+      next = at(win - 1);
+      end = n = kC;
+    }
+    begin = piece_begin(cuts.piece, end);
+  }
+  __device__ __forceinline__ bool fresh() const { return cuts.fresh >> begin & 1; }
+};
+
+// Eight slots of two accumulator tiles.
+__device__ __forceinline__ void slots(const f32x4_t& lo, const f32x4_t& hi, float* o) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    o[r] = lo[r];
+    o[4 + r] = hi[r];
+  }
+}
+
+// ---- staging by a chain's helper waves ----
+// NV 16-byte groups a thread of a contiguous run.
+template <int NV>
+struct Run {
+  uint4 q[NV];
+  __device__ __forceinline__ void load(const char* p, int tid, int nthr) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) q[i] = *reinterpret_cast<const uint4*>(p + 16 * (tid + i * nthr));
+  }
+  __device__ __forceinline__ void store(char* p, int tid, int nthr) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) *reinterpret_cast<uint4*>(p + 16 * (tid + i * nthr)) = q[i];
+  }
+};
+// 64 rows of NP bf16 values (N of them there), rows outside [begin, end) zero.
+template <int NP, int NTHR>
+struct RowTile {
+  static constexpr int kPer = NP / 8, kRows = NTHR / kPer > 0 ? NTHR / kPer : 1, NV = kC * kPer / NTHR;
+  static_assert(NTHR % kPer == 0 && kC % kRows == 0, "whole rows at a time");
+  uint4 q[NV];
+  __device__ __forceinline__ void load(const uint16_t* base, int64_t stride, int N, int begin, int end, int tid) {
+    const int t = tid / kPer, col = tid % kPer * 8;
+    const uint16_t* p = base + t * stride + col;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int ti = t + i * kRows;
+      q[i] = make_uint4(0, 0, 0, 0);
+      if (ti >= begin && ti < end && col < N) q[i] = *reinterpret_cast<const uint4*>(p + (int64_t)(i * kRows) * stride);
+    }
+  }
+  __device__ __forceinline__ void store(uint16_t* tile, int pitch, int tid) const {
+    const int t = tid / kPer, col = tid % kPer * 8;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) *reinterpret_cast<uint4*>(tile + (t + i * kRows) * pitch + col) = q[i];
+  }
+};
+// Five gates of 64 tokens, zero outside [begin, end).
+template <int NTHR>
+struct GateTile {
+  static constexpr int NV = (5 * kC / 4 + NTHR - 1) / NTHR;
+  float4 q[NV];
+  __device__ __forceinline__ void load(const DeltaGates* g, int begin, int end, int tid) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = tid + i * NTHR;
+      q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (e < 5 * kC / 4) {
+        const float4 v = reinterpret_cast<const float4*>(g)[e];
+        const int t = 4 * e % kC;
+        q[i] = make_float4(t >= begin && t < end ? v.x : 0.f, t + 1 >= begin && t + 1 < end ? v.y : 0.f,
+                           t + 2 >= begin && t + 2 < end ? v.z : 0.f, t + 3 >= begin && t + 3 < end ? v.w : 0.f);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(float* p, int tid) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (tid + i * NTHR < 5 * kC / 4) reinterpret_cast<float4*>(p)[tid + i * NTHR] = q[i];
+  }
+};
+
 // Neighbouring blocks (slices of a head, heads of a group) on one XCD's L2.
 __device__ __forceinline__ uint32_t near_block(uint32_t bid, uint32_t n) {
   return n % 8 == 0 ? (bid & 7u) * (n >> 3) + (bid >> 3) : bid;
@@ -183,7 +317,7 @@ __device__ __forceinline__ uint32_t near_block(uint32_t bid, uint32_t n) {
 // ---- the workspace ----
 struct DeltaWs {
   int64_t nw;        // windows a row
-  size_t gates, low_r, low_p, up_r, up_p, marks, S, D, w, du, dq, dk, part, total;
+  size_t gates, cuts, low_r, low_p, up_r, up_p, marks, S, D, w, du, dq, dk, part, total;
 };
 inline DeltaWs delta_ws(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P, bool back) {
   DeltaWs o = {};
@@ -196,6 +330,7 @@ inline DeltaWs delta_ws(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P, b
     return p;
   };
   o.gates = take(bhw * sizeof(DeltaGates));
+  o.cuts = take((size_t)(B * o.nw) * 16);
   o.low_r = take(bhw * kTriBytes);
   if (!back) {
     o.low_p = take(bhw * kTriBytes);

@@ -27,14 +27,6 @@ namespace ssd {
 
 constexpr int kTP = kC + 4;
 
-__device__ __forceinline__ void slots(const f32x4_t& lo, const f32x4_t& hi, float* o) {
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    o[r] = lo[r];
-    o[4 + r] = hi[r];
-  }
-}
-
 // ---------------------------------------------------------------- the chain, back to front
 template <class M, int NP>
 constexpr int rev_pitch() { return NP + 16 / (int)sizeof(typename M::IO::type); }
