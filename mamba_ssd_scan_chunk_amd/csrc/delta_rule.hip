@@ -483,6 +483,7 @@ struct ChainLds {
 template <int NP, int C, bool VL, bool SAVE>
 __global__ __launch_bounds__(128 * C) void delta_chain_bf16_kernel(DeltaArgs a, DeltaWs ws) {
   typedef DeltaB M;
+  typedef DeltaB::One One;
   typedef DeltaB::Two Two;
   typedef ChainLds<NP, C> Lay;
   constexpr int NT = NP / 16, KS = NP / 32, LP = Lay::kPitch, NH = 64 * C;
@@ -503,24 +504,24 @@ __global__ __launch_bounds__(128 * C) void delta_chain_bf16_kernel(DeltaArgs a, 
     // ---- helper
     const int ht = tid - NH;
     RowTile<NP, NH> kt, qt;
-    Run<kTriBytes / 16 / NH> rt;
+    TriTile<NH> rt;
     GateTile<NH> gt;
     const uint16_t* kb = static_cast<const uint16_t*>(a.k) + row * a.rows.k + grp * N;
     const uint16_t* qb = static_cast<const uint16_t*>(a.q) + row * a.rows.q + grp * N;
     auto ask = [&](const Pieces& s) {
       const int64_t bhw = bh * ws.nw + s.win;
       kt.load(kb + s.win * kC * a.rows.k, a.rows.k, N, s.begin, s.end, ht);
-      rt.load(a.ws + ws.low_r + bhw * kTriBytes, ht, NH);
-      gt.load(reinterpret_cast<const DeltaGates*>(a.ws + ws.gates) + bhw, s.begin, s.end, ht);
+      rt.load(a.ws + ws.low_r + bhw * kTriBytes, ht);
+      gt.load(reinterpret_cast<const DeltaGates*>(a.ws + ws.gates) + bhw, ht);
     };
-    auto put = [&](int half) {
+    auto put = [&](const Pieces& s, int half) {
       char* o = lds + half * Lay::half;
-      kt.store(reinterpret_cast<uint16_t*>(o + Lay::k), LP, ht);
-      rt.store(o + Lay::r, ht, NH);
-      gt.store(reinterpret_cast<float*>(o + Lay::g), ht);
+      kt.store(reinterpret_cast<uint16_t*>(o + Lay::k), LP, N, s.begin, s.end, ht);
+      rt.store(o + Lay::r, ht);
+      gt.store(reinterpret_cast<float*>(o + Lay::g), s.begin, s.end, ht);
     };
     ask(pc);
-    put(0);
+    put(pc, 0);
     __syncthreads();
     Two pf[kTriFrags];
     float4 qin[4];
@@ -541,32 +542,39 @@ __global__ __launch_bounds__(128 * C) void delta_chain_bf16_kernel(DeltaArgs a, 
         f32x4_t y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        Two sb[KS], ub[2];
+        One qf[KS][4];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-          const Two sb = M::load(x + s * 2048, lane);
+          sb[s] = M::load(x + s * 2048, lane);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint16_t* qp = ql + (16 * i + c) * LP + 32 * s + 4 * g;
-            y[i] = M::mma(lds_4x2<M>(qp, qp + 16), sb, y[i]);
+            qf[s][i] = lds_4x2<M>(qp, qp + 16);
           }
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) ub[s] = M::load(x + (KS + s) * 2048, lane);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = M::mma(qf[s][i], sb[s].lo, y[i]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = M::mma(qf[s][i], sb[s].hi, y[i]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] *= f32x4_t{qin[i].x, qin[i].y, qin[i].z, qin[i].w};
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const Two ub = M::load(x + (KS + s) * 2048, lane);
 #pragma unroll
-          for (int i = 2 * s; i < 4; ++i) y[i] = M::mma(pf[low_frag(i, s)], ub, y[i]);
+          for (int i = 2 * s; i < 4; ++i) y[i] = M::mma(pf[low_frag(i, s)].hi, ub[s].lo, y[i]);
+#pragma unroll
+          for (int i = 2 * s; i < 4; ++i) y[i] = M::mma(pf[low_frag(i, s)].lo, ub[s].hi, y[i]);
+#pragma unroll
+          for (int i = 2 * s; i < 4; ++i) y[i] = M::mma(pf[low_frag(i, s)].hi, ub[s].hi, y[i]);
         }
-        uint16_t* yp = static_cast<uint16_t*>(a.y) + ((row + t0) * a.H + h) * a.P + p;
-        const int64_t ystep = a.H * a.P;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int t = 16 * i + 4 * g + r;
-            if (t >= begin && t < end) yp[t * ystep] = M::IO::put(y[i][r]);
-          }
+        Column::put(static_cast<uint16_t*>(a.y) + ((row + t0) * a.H + h) * a.P + p, a.H * a.P, y, begin, end, g);
       }
       if (!more) break;
       if constexpr (!SAVE) {
@@ -578,12 +586,12 @@ __global__ __launch_bounds__(128 * C) void delta_chain_bf16_kernel(DeltaArgs a, 
         const float* sq = reinterpret_cast<const float*>(lds + (j & 1) * Lay::half + Lay::g) + 2 * kC;
 #pragma unroll
         for (int i = 0; i < 4; ++i) qin[i] = *reinterpret_cast<const float4*>(sq + 16 * i + 4 * g);
-        qt.store(reinterpret_cast<uint16_t*>(lds + Lay::q + (j & 1) * Lay::kRows), LP, ht);
+        qt.store(reinterpret_cast<uint16_t*>(lds + Lay::q + (j & 1) * Lay::kRows), LP, N, pc.begin, pc.end, ht);
         t0 = pc.win * kC;
         begin = pc.begin;
         end = pc.end;
       }
-      if (ahead) put((j + 1) & 1);
+      if (ahead) put(nx, (j + 1) & 1);
       pc = nx;
       __syncthreads();
       if (SAVE && !ahead) break;
@@ -601,17 +609,8 @@ __global__ __launch_bounds__(128 * C) void delta_chain_bf16_kernel(DeltaArgs a, 
       S[j][r] = a.h0 && nn < N ? a.h0[(bh * N + nn) * a.P + p] : 0.f;
     }
   const uint16_t* vb = static_cast<const uint16_t*>(a.v) + row * a.rows.v + h * a.P + p;
-  uint16_t vn[16];
-  auto ask_v = [&](const Pieces& s) {
-    const uint16_t* vp = vb + s.win * kC * a.rows.v;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int t = 16 * (e / 4) + 4 * g + e % 4;
-      vn[e] = 0;
-      if (t >= s.begin && t < s.end) vn[e] = vp[t * a.rows.v];
-    }
-  };
-  ask_v(pc);
+  Column vn;
+  vn.load(vb + pc.win * kC * a.rows.v, a.rows.v, pc.begin, pc.end, g);
   __syncthreads();
   for (int step = 0; pc.valid(); ++step) {
     const int begin = pc.begin, end = pc.end;
@@ -635,37 +634,68 @@ __global__ __launch_bounds__(128 * C) void delta_chain_bf16_kernel(DeltaArgs a, 
           if (nn < N) out[nn * a.P] = S[j][r];
         }
     }
+    // The wave has its SIMD to itself: what a product needs from LDS is asked for
+    // well before, k and R ahead of the state's rounding, k^T ahead of R's product.
+    One kf[KS][4], kT[2][NT];
+    Two rf[kTriFrags];
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint16_t* kp = kt + (16 * i + c) * LP + 32 * s + 4 * g;
+        kf[s][i] = lds_4x2<M>(kp, kp + 16);
+      }
+    float ki[4][4], be[4][4], ko[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      load_vec<IoF32, 4>(sKin + 16 * i + 4 * g, ki[i]);
+      load_vec<IoF32, 4>(sBeta + 16 * i + 4 * g, be[i]);
+      load_vec<IoF32, 4>(sKout + 16 * i + 4 * g, ko[i]);
+    }
+    const float whole = sIn[end - 1];
+    __builtin_amdgcn_sched_barrier(0);
+    Two sb[KS];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      float v[8];
+      slots(S[2 * s], S[2 * s + 1], v);
+      sb[s] = M::two(v);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int f = 0; f < kTriFrags; ++f) rf[f] = M::load(in + Lay::r + f * 2048, lane);
+    __builtin_amdgcn_sched_barrier(0);
     f32x4_t X[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) X[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      float v[8];
-      slots(S[2 * s], S[2 * s + 1], v);
-      const Two sb = M::two(v);
-      if constexpr (!SAVE) M::store(x + s * 2048, lane, sb);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint16_t* kp = kt + (16 * i + c) * LP + 32 * s + 4 * g;
-        X[i] = M::mma(lds_4x2<M>(kp, kp + 16), sb, X[i]);
-      }
+      for (int i = 0; i < 4; ++i) X[i] = M::mma(kf[s][i], sb[s].lo, X[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) X[i] = M::mma(kf[s][i], sb[s].hi, X[i]);
     }
-    // X = v - e^G k S
-    float be[4][4], bx[4][4];
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 kin = *reinterpret_cast<const float4*>(sKin + 16 * i + 4 * g);
-      const float4 q = *reinterpret_cast<const float4*>(sBeta + 16 * i + 4 * g);
-      const float ki[4] = {kin.x, kin.y, kin.z, kin.w};
-      be[i][0] = q.x; be[i][1] = q.y; be[i][2] = q.z; be[i][3] = q.w;
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) kT[s][j] = M::transposed(kt + 32 * s * LP + 16 * j, LP, lane);
+    if constexpr (!SAVE) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s) M::store(x + s * 2048, lane, sb[s]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    // X = v - e^G k S
+    float bx[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        X[i][r] = bf16_bits_to_f32(vn[4 * i + r]) - ki[r] * X[i][r];
+        X[i][r] = vn.get(i, r, begin, end, g) - ki[i][r] * X[i][r];
         bx[i][r] = be[i][r] * X[i][r];
       }
-    }
     pc.step();
-    if (pc.valid()) ask_v(pc);
+    if (pc.valid()) vn.load(vb + pc.win * kC * a.rows.v, a.rows.v, pc.begin, pc.end, g);
     // w = X + R (b X); u = b w
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -674,39 +704,31 @@ __global__ __launch_bounds__(128 * C) void delta_chain_bf16_kernel(DeltaArgs a, 
       for (int e = 0; e < 8; ++e) v[e] = bx[2 * s + e / 4][e % 4];
       const Two xb = M::two(v);
 #pragma unroll
-      for (int i = 2 * s; i < 4; ++i) X[i] = M::mma(M::load(in + Lay::r + low_frag(i, s) * 2048, lane), xb, X[i]);
-    }
-    if constexpr (SAVE) {
-      float* out = reinterpret_cast<float*>(a.ws + ws.w) + bhw * kC * a.P + p;
+      for (int i = 2 * s; i < 4; ++i) X[i] = M::mma(rf[low_frag(i, s)].hi, xb.lo, X[i]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 2 * s; i < 4; ++i) X[i] = M::mma(rf[low_frag(i, s)].lo, xb.hi, X[i]);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int t = 16 * i + 4 * g + r;
-          if (t >= begin && t < end) out[t * a.P] = X[i][r];
-        }
+      for (int i = 2 * s; i < 4; ++i) X[i] = M::mma(rf[low_frag(i, s)].hi, xb.hi, X[i]);
     }
-    const float whole = sIn[end - 1];
+    if constexpr (SAVE)
+      Column::put(reinterpret_cast<float*>(a.ws + ws.w) + bhw * kC * a.P + p, a.P, X, begin, end, g);
 #pragma unroll
     for (int j = 0; j < NT; ++j) S[j] *= whole;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       float v[8], u[8];
 #pragma unroll
-      for (int t4 = 0; t4 < 2; ++t4) {
-        const float4 ko = *reinterpret_cast<const float4*>(sKout + 32 * s + 16 * t4 + 4 * g);
-        const float k4[4] = {ko.x, ko.y, ko.z, ko.w};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int t = 32 * s + 16 * t4 + 4 * g + r, e = 4 * t4 + r;
-          u[e] = !VL || (t >= begin && t < end) ? be[2 * s + t4][r] * X[2 * s + t4][r] : 0.f;
-          v[e] = u[e] * k4[r];
-        }
+      for (int e = 0; e < 8; ++e) {
+        const int t = 32 * s + 16 * (e / 4) + 4 * g + e % 4, i = 2 * s + e / 4, r = e % 4;
+        u[e] = !VL || (t >= begin && t < end) ? be[i][r] * X[i][r] : 0.f;
+        v[e] = u[e] * ko[i][r];
       }
       if constexpr (!SAVE) M::store(x + (KS + s) * 2048, lane, M::two(u));
       const Two ub = M::two(v);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) S[j] = M::mma(M::transposed(kt + 32 * s * LP + 16 * j, LP, lane), ub, S[j]);
+      for (int j = 0; j < NT; ++j) S[j] = M::mma(kT[s][j], ub.lo, S[j]);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) S[j] = M::mma(kT[s][j], ub.hi, S[j]);
     }
     if constexpr (VL) {
       const int64_t last = row + win * kC + end - 1;

@@ -38,10 +38,11 @@ struct DeltaB {
   __device__ __forceinline__ static Two two(const float* s) {
     Two t;
     t.hi = OpBF16::from_f32(s);
-    const uint32_t w[4] = {t.hi.v.x, t.hi.v.y, t.hi.v.z, t.hi.v.w};
+    uint32_t w[4] = {t.hi.v.x, t.hi.v.y, t.hi.v.z, t.hi.v.w};
     float d[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
+      asm("" : "+v"(w[e]));  // the pair as it is, not each value rounded again
       d[2 * e] = s[2 * e] - __uint_as_float(w[e] << 16);
       d[2 * e + 1] = s[2 * e + 1] - __uint_as_float(w[e] & 0xffff0000u);
     }
@@ -249,20 +250,24 @@ __device__ __forceinline__ void slots(const f32x4_t& lo, const f32x4_t& hi, floa
 }
 
 // ---- staging by a chain's helper waves ----
-// NV 16-byte groups a thread of a contiguous run.
-template <int NV>
-struct Run {
-  uint4 q[NV];
-  __device__ __forceinline__ void load(const char* p, int tid, int nthr) {
+typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));  // copied as a value, where uint4 is a struct
+// The six fragments of a triangular operand.
+template <int NTHR>
+struct TriTile {
+  static constexpr int NV = kTriBytes / 16 / NTHR;
+  u32x4v q[NV];
+  __device__ __forceinline__ void load(const char* p, int tid) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) q[i] = *reinterpret_cast<const uint4*>(p + 16 * (tid + i * nthr));
+    for (int i = 0; i < NV; ++i) q[i] = reinterpret_cast<const u32x4v*>(p)[tid + i * NTHR];
   }
-  __device__ __forceinline__ void store(char* p, int tid, int nthr) const {
+  __device__ __forceinline__ void store(char* p, int tid) const {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) *reinterpret_cast<uint4*>(p + 16 * (tid + i * nthr)) = q[i];
+    for (int i = 0; i < NV; ++i) reinterpret_cast<u32x4v*>(p)[tid + i * NTHR] = q[i];
   }
 };
 // 64 rows of NP bf16 values (N of them there), rows outside [begin, end) zero.
+// Loads are unconditional, of rows that are there, and what does not belong is
+// dropped when it is stored: a branch a load would wait for each.
 template <int NP, int NTHR>
 struct RowTile {
   static constexpr int kPer = NP / 8, kRows = NTHR / kPer > 0 ? NTHR / kPer : 1, NV = kC * kPer / NTHR;
@@ -270,42 +275,78 @@ struct RowTile {
   uint4 q[NV];
   __device__ __forceinline__ void load(const uint16_t* base, int64_t stride, int N, int begin, int end, int tid) {
     const int t = tid / kPer, col = tid % kPer * 8;
-    const uint16_t* p = base + t * stride + col;
+    const uint16_t* p = base + (col < N ? col : 0);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      q[i] = *reinterpret_cast<const uint4*>(p + min(max(t + i * kRows, begin), end - 1) * stride);
+  }
+  __device__ __forceinline__ void store(uint16_t* tile, int pitch, int N, int begin, int end, int tid) const {
+    const int t = tid / kPer, col = tid % kPer * 8;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int ti = t + i * kRows;
-      q[i] = make_uint4(0, 0, 0, 0);
-      if (ti >= begin && ti < end && col < N) q[i] = *reinterpret_cast<const uint4*>(p + (int64_t)(i * kRows) * stride);
+      const bool on = ti >= begin && ti < end && col < N;
+      *reinterpret_cast<uint4*>(tile + ti * pitch + col) = make_uint4(on ? q[i].x : 0, on ? q[i].y : 0, on ? q[i].z : 0,
+                                                                     on ? q[i].w : 0);
     }
-  }
-  __device__ __forceinline__ void store(uint16_t* tile, int pitch, int tid) const {
-    const int t = tid / kPer, col = tid % kPer * 8;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) *reinterpret_cast<uint4*>(tile + (t + i * kRows) * pitch + col) = q[i];
   }
 };
 // Five gates of 64 tokens, zero outside [begin, end).
 template <int NTHR>
 struct GateTile {
-  static constexpr int NV = (5 * kC / 4 + NTHR - 1) / NTHR;
+  static constexpr int kAll = 5 * kC / 4, NV = (kAll + NTHR - 1) / NTHR;
   float4 q[NV];
-  __device__ __forceinline__ void load(const DeltaGates* g, int begin, int end, int tid) {
+  __device__ __forceinline__ void load(const DeltaGates* g, int tid) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) q[i] = reinterpret_cast<const float4*>(g)[min(tid + i * NTHR, kAll - 1)];
+  }
+  __device__ __forceinline__ void store(float* p, int begin, int end, int tid) const {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = tid + i * NTHR;
-      q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (e < 5 * kC / 4) {
-        const float4 v = reinterpret_cast<const float4*>(g)[e];
-        const int t = 4 * e % kC;
-        q[i] = make_float4(t >= begin && t < end ? v.x : 0.f, t + 1 >= begin && t + 1 < end ? v.y : 0.f,
-                           t + 2 >= begin && t + 2 < end ? v.z : 0.f, t + 3 >= begin && t + 3 < end ? v.w : 0.f);
+      const int e = tid + i * NTHR, t = 4 * e % kC;
+      const float4 v = q[i];
+      if (e < kAll)
+        reinterpret_cast<float4*>(p)[e] =
+            make_float4(t >= begin && t < end ? v.x : 0.f, t + 1 >= begin && t + 1 < end ? v.y : 0.f,
+                        t + 2 >= begin && t + 2 < end ? v.z : 0.f, t + 3 >= begin && t + 3 < end ? v.w : 0.f);
+    }
+  }
+};
+// A lane's 16 tokens (rows 16 i + 4 g + r) of one column.
+struct Column {
+  uint16_t q[16];
+  __device__ __forceinline__ void load(const uint16_t* p, int64_t stride, int begin, int end, int g) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) q[e] = p[min(max(16 * (e / 4) + 4 * g + e % 4, begin), end - 1) * stride];
+  }
+  // bf16 values into rows [begin, end) of a column
+  __device__ __forceinline__ static void put(uint16_t* p, int64_t stride, const f32x4_t* v, int begin, int end, int g) {
+    if (begin == 0 && end == kC) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) p[(16 * (e / 4) + 4 * g + e % 4) * stride] = IoBF16::put(v[e / 4][e % 4]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int t = 16 * (e / 4) + 4 * g + e % 4;
+        if (t >= begin && t < end) p[t * stride] = IoBF16::put(v[e / 4][e % 4]);
       }
     }
   }
-  __device__ __forceinline__ void store(float* p, int tid) const {
+  __device__ __forceinline__ static void put(float* p, int64_t stride, const f32x4_t* v, int begin, int end, int g) {
+    if (begin == 0 && end == kC) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (tid + i * NTHR < 5 * kC / 4) reinterpret_cast<float4*>(p)[tid + i * NTHR] = q[i];
+      for (int e = 0; e < 16; ++e) p[(16 * (e / 4) + 4 * g + e % 4) * stride] = v[e / 4][e % 4];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int t = 16 * (e / 4) + 4 * g + e % 4;
+        if (t >= begin && t < end) p[t * stride] = v[e / 4][e % 4];
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int i, int r, int begin, int end, int g) const {
+    const int t = 16 * i + 4 * g + r;
+    return t >= begin && t < end ? bf16_bits_to_f32(q[4 * i + r]) : 0.f;
   }
 };
 
