@@ -22,7 +22,7 @@ ssd_status check_delta(const ssd_delta_shape* s, bool step) {
   // blocks of 256 threads, one a (row, window, head), in one dimension of a launch; of 64 a (row, head, 16 columns)
   SSD_TRY(product({s->batch, s->nheads, (s->seqlen - 1) / ssd::kDeltaC + 1}, (int64_t(1) << 24) - 1));
   SSD_TRY(product({s->batch, s->nheads}, (int64_t(1) << 22) - 1));
-  if (row_too_long(s->seqlen, s->nheads * s->headdim)) return SSD_ERR_UNSUPPORTED;
+  if (s->nheads * s->headdim >= int64_t(1) << 23) return SSD_ERR_UNSUPPORTED;
   return product({s->batch, s->seqlen, s->nheads, s->headdim}, kMaxElems);
 }
 
@@ -30,6 +30,9 @@ ssd_status delta_rows(const ssd_delta_shape* s, const ssd_delta_rows* r, ssd::De
   const ssd_delta_rows none = {0, 0, 0, 0, 0};
   if (!r) r = &none;
   const int64_t qk = s->ngroups * s->dstate;
+  // 64 rows of up to 4 bytes an element are addressed by 32-bit byte offsets
+  for (int64_t given : {r->q, r->k, r->v, r->dt, r->beta})
+    if (given >= int64_t(1) << 23) return SSD_ERR_UNSUPPORTED;
   SSD_TRY(row_stride(r->q, qk, s->batch, s->seqlen, &o->q));
   SSD_TRY(row_stride(r->k, qk, s->batch, s->seqlen, &o->k));
   SSD_TRY(row_stride(r->v, s->nheads * s->headdim, s->batch, s->seqlen, &o->v));

@@ -481,7 +481,7 @@ struct ChainLds {
 };
 
 template <int NP, int C, bool VL, bool SAVE>
-__global__ __launch_bounds__(128 * C) void delta_chain_bf16_kernel(DeltaArgs a, DeltaWs ws) {
+__global__ __launch_bounds__(128 * C, 2) void delta_chain_bf16_kernel(DeltaArgs a, DeltaWs ws) {
   typedef DeltaB M;
   typedef DeltaB::One One;
   typedef DeltaB::Two Two;
@@ -493,8 +493,9 @@ __global__ __launch_bounds__(128 * C) void delta_chain_bf16_kernel(DeltaArgs a, 
   const uint32_t bid = near_block(blockIdx.x, gridDim.x);
   const uint32_t slices = (uint32_t)(a.P / 16) / C;
   const int64_t bh = bid / slices, h = bh % a.H, b = bh / a.H, grp = h / (a.H / a.G);
-  const int64_t p = ((bid % slices) * C + wave % C) * 16 + c;
+  const uint32_t p = ((bid % slices) * C + wave % C) * 16 + c;
   const int N = (int)a.N;
+  const uint32_t P = (uint32_t)a.P;
   const int64_t row = b * a.L;
   const uint8_t* marks = VL && !SAVE && a.nseq > 0 ? reinterpret_cast<const uint8_t*>(a.ws + ws.marks) : nullptr;
   Pieces pc;
@@ -506,27 +507,28 @@ __global__ __launch_bounds__(128 * C) void delta_chain_bf16_kernel(DeltaArgs a, 
     RowTile<NP, NH> kt, qt;
     TriTile<NH> rt;
     GateTile<NH> gt;
+    const uint32_t krow = (uint32_t)a.rows.k, qrow = (uint32_t)a.rows.q, yrow = (uint32_t)(a.H * a.P);
     const uint16_t* kb = static_cast<const uint16_t*>(a.k) + row * a.rows.k + grp * N;
     const uint16_t* qb = static_cast<const uint16_t*>(a.q) + row * a.rows.q + grp * N;
     auto ask = [&](const Pieces& s) {
       const int64_t bhw = bh * ws.nw + s.win;
-      kt.load(kb + s.win * kC * a.rows.k, a.rows.k, N, s.begin, s.end, ht);
+      kt.load(kb + s.win * kC * a.rows.k, krow, N, s.n, ht);
       rt.load(a.ws + ws.low_r + bhw * kTriBytes, ht);
       gt.load(reinterpret_cast<const DeltaGates*>(a.ws + ws.gates) + bhw, ht);
     };
     auto put = [&](const Pieces& s, int half) {
       char* o = lds + half * Lay::half;
-      kt.store(reinterpret_cast<uint16_t*>(o + Lay::k), LP, N, s.begin, s.end, ht);
+      kt.template store<VL>(reinterpret_cast<uint16_t*>(o + Lay::k), LP, s.begin, s.end, ht);
       rt.store(o + Lay::r, ht);
-      gt.store(reinterpret_cast<float*>(o + Lay::g), s.begin, s.end, ht);
+      gt.template store<VL>(reinterpret_cast<float*>(o + Lay::g), s.begin, s.end, ht);
     };
     ask(pc);
     put(pc, 0);
     __syncthreads();
     Two pf[kTriFrags];
-    float4 qin[4];
+    f32x4_t qin[4];
     int64_t t0 = 0;
-    int begin = 0, end = 0;
+    int begin = 0, end = 0, n = 0;
     for (int j = 0;; ++j) {
       // pc: piece j, which the column waves take now
       const bool more = pc.valid();
@@ -534,47 +536,55 @@ __global__ __launch_bounds__(128 * C) void delta_chain_bf16_kernel(DeltaArgs a, 
       if (more) nx.step();
       const bool ahead = more && nx.valid();
       if (ahead) ask(nx);
-      if (!SAVE && more)
-        qt.load(qb + pc.win * kC * a.rows.q, a.rows.q, N, pc.begin, pc.end, ht);
+      if (!SAVE && more) qt.load(qb + pc.win * kC * a.rows.q, qrow, N, pc.n, ht);
       if (!SAVE && j > 0) {
         const char* x = lds + Lay::x + (((j - 1) & 1) * C + wave % C) * Lay::kX;
         const uint16_t* ql = reinterpret_cast<const uint16_t*>(lds + Lay::q + ((j - 1) & 1) * Lay::kRows);
-        f32x4_t y[4];
+        f32x4_t y[4], u[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        Two sb[KS], ub[2];
-        One qf[KS][4];
+        for (int i = 0; i < 4; ++i) {
+          y[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+          u[i] = *reinterpret_cast<const f32x4_t*>(x + KS * 2048 + i * 1024 + 16 * lane);
+        }
+        constexpr int SB = KS > 1 ? 2 : 1;  // steps whose operands are asked for together
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          sb[s] = M::load(x + s * 2048, lane);
+        for (int s0 = 0; s0 < KS; s0 += SB) {
+          Two sb[SB];
+          One qf[SB][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint16_t* qp = ql + (16 * i + c) * LP + 32 * s + 4 * g;
-            qf[s][i] = lds_4x2<M>(qp, qp + 16);
+          for (int s = 0; s < SB; ++s) {
+            sb[s] = M::load(x + (s0 + s) * 2048, lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint16_t* qp = ql + (16 * i + c) * LP + 32 * (s0 + s) + 4 * g;
+              qf[s][i] = lds_4x2<M>(qp, qp + 16);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int s = 0; s < SB; ++s) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = M::mma(qf[s][i], sb[s].lo, y[i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = M::mma(qf[s][i], sb[s].hi, y[i]);
           }
         }
 #pragma unroll
-        for (int s = 0; s < 2; ++s) ub[s] = M::load(x + (KS + s) * 2048, lane);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = M::mma(qf[s][i], sb[s].lo, y[i]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = M::mma(qf[s][i], sb[s].hi, y[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] *= f32x4_t{qin[i].x, qin[i].y, qin[i].z, qin[i].w};
+        for (int i = 0; i < 4; ++i) y[i] *= qin[i];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
+          float v[8];
+          slots(u[2 * s], u[2 * s + 1], v);
+          const Two ub = M::two(v);
 #pragma unroll
-          for (int i = 2 * s; i < 4; ++i) y[i] = M::mma(pf[low_frag(i, s)].hi, ub[s].lo, y[i]);
+          for (int i = 2 * s; i < 4; ++i) y[i] = M::mma(pf[low_frag(i, s)].hi, ub.lo, y[i]);
 #pragma unroll
-          for (int i = 2 * s; i < 4; ++i) y[i] = M::mma(pf[low_frag(i, s)].lo, ub[s].hi, y[i]);
+          for (int i = 2 * s; i < 4; ++i) y[i] = M::mma(pf[low_frag(i, s)].lo, ub.hi, y[i]);
 #pragma unroll
-          for (int i = 2 * s; i < 4; ++i) y[i] = M::mma(pf[low_frag(i, s)].hi, ub[s].hi, y[i]);
+          for (int i = 2 * s; i < 4; ++i) y[i] = M::mma(pf[low_frag(i, s)].hi, ub.hi, y[i]);
         }
-        Column::put(static_cast<uint16_t*>(a.y) + ((row + t0) * a.H + h) * a.P + p, a.H * a.P, y, begin, end, g);
+        Column::put<VL>(static_cast<uint16_t*>(a.y) + ((row + t0) * a.H + h) * a.P, yrow, 4 * g * yrow + p, n, y, begin,
+                        end, g);
       }
       if (!more) break;
       if constexpr (!SAVE) {
@@ -585,9 +595,10 @@ __global__ __launch_bounds__(128 * C) void delta_chain_bf16_kernel(DeltaArgs a, 
         for (int f = 0; f < kTriFrags; ++f) pf[f] = M::load(fp + f * 2048, lane);
         const float* sq = reinterpret_cast<const float*>(lds + (j & 1) * Lay::half + Lay::g) + 2 * kC;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) qin[i] = *reinterpret_cast<const float4*>(sq + 16 * i + 4 * g);
-        qt.store(reinterpret_cast<uint16_t*>(lds + Lay::q + (j & 1) * Lay::kRows), LP, N, pc.begin, pc.end, ht);
+        for (int i = 0; i < 4; ++i) qin[i] = *reinterpret_cast<const f32x4_t*>(sq + 16 * i + 4 * g);
+        qt.template store<VL>(reinterpret_cast<uint16_t*>(lds + Lay::q + (j & 1) * Lay::kRows), LP, pc.begin, pc.end, ht);
         t0 = pc.win * kC;
+        n = pc.n;
         begin = pc.begin;
         end = pc.end;
       }
@@ -608,9 +619,10 @@ __global__ __launch_bounds__(128 * C) void delta_chain_bf16_kernel(DeltaArgs a, 
       const int nn = 16 * j + 4 * g + r;
       S[j][r] = a.h0 && nn < N ? a.h0[(bh * N + nn) * a.P + p] : 0.f;
     }
-  const uint16_t* vb = static_cast<const uint16_t*>(a.v) + row * a.rows.v + h * a.P + p;
+  const uint32_t vrow = (uint32_t)a.rows.v, voff = 4 * g * vrow + p;
+  const uint16_t* vb = static_cast<const uint16_t*>(a.v) + row * a.rows.v + h * a.P;
   Column vn;
-  vn.load(vb + pc.win * kC * a.rows.v, a.rows.v, pc.begin, pc.end, g);
+  vn.load(vb + pc.win * kC * a.rows.v, vrow, voff, pc.n);
   __syncthreads();
   for (int step = 0; pc.valid(); ++step) {
     const int begin = pc.begin, end = pc.end;
@@ -624,16 +636,6 @@ __global__ __launch_bounds__(128 * C) void delta_chain_bf16_kernel(DeltaArgs a, 
 #pragma unroll
       for (int j = 0; j < NT; ++j) S[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
-    if (SAVE && begin == 0) {
-      float* out = reinterpret_cast<float*>(a.ws + ws.S) + bhw * N * a.P + p;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int nn = 16 * j + 4 * g + r;
-          if (nn < N) out[nn * a.P] = S[j][r];
-        }
-    }
     // The wave has its SIMD to itself: what a product needs from LDS is asked for
     // well before, k and R ahead of the state's rounding, k^T ahead of R's product.
     One kf[KS][4], kT[2][NT];
@@ -645,6 +647,33 @@ __global__ __launch_bounds__(128 * C) void delta_chain_bf16_kernel(DeltaArgs a, 
         const uint16_t* kp = kt + (16 * i + c) * LP + 32 * s + 4 * g;
         kf[s][i] = lds_4x2<M>(kp, kp + 16);
       }
+    __builtin_amdgcn_sched_barrier(0);
+    if (SAVE && begin == 0)
+      put_state<NT>(reinterpret_cast<float*>(a.ws + ws.S) + bhw * N * a.P, N, P, 4 * g * P + p, S);
+    f32x4_t X[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) X[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      float v[8];
+      slots(S[2 * s], S[2 * s + 1], v);
+      const Two sb = M::two(v);
+      if constexpr (!SAVE) M::store(x + s * 2048, lane, sb);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) X[i] = M::mma(kf[s][i], sb.lo, X[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) X[i] = M::mma(kf[s][i], sb.hi, X[i]);
+      if (s == 0) {
+#pragma unroll
+        for (int f = 0; f < kTriFrags; ++f) rf[f] = M::load(in + Lay::r + f * 2048, lane);
+      }
+    }
+    // the state's rounding between the products: a product occupies the matrix unit for four issues
+#pragma unroll
+    for (int e = 0; e < 8 * KS; ++e) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x2, 3, 0);
+    }
     float ki[4][4], be[4][4], ko[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -653,49 +682,24 @@ __global__ __launch_bounds__(128 * C) void delta_chain_bf16_kernel(DeltaArgs a, 
       load_vec<IoF32, 4>(sKout + 16 * i + 4 * g, ko[i]);
     }
     const float whole = sIn[end - 1];
-    __builtin_amdgcn_sched_barrier(0);
-    Two sb[KS];
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      float v[8];
-      slots(S[2 * s], S[2 * s + 1], v);
-      sb[s] = M::two(v);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int f = 0; f < kTriFrags; ++f) rf[f] = M::load(in + Lay::r + f * 2048, lane);
-    __builtin_amdgcn_sched_barrier(0);
-    f32x4_t X[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) X[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) X[i] = M::mma(kf[s][i], sb[s].lo, X[i]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) X[i] = M::mma(kf[s][i], sb[s].hi, X[i]);
-    }
-    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int j = 0; j < NT; ++j) kT[s][j] = M::transposed(kt + 32 * s * LP + 16 * j, LP, lane);
-    if constexpr (!SAVE) {
-#pragma unroll
-      for (int s = 0; s < KS; ++s) M::store(x + s * 2048, lane, sb[s]);
-    }
     __builtin_amdgcn_sched_barrier(0);
-    // X = v - e^G k S
+    // X = v - e^G k S; in packed rows the others' values are left out (what is behind the row reads as zero)
     float bx[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        X[i][r] = vn.get(i, r, begin, end, g) - ki[i][r] * X[i][r];
+        const int t = 16 * i + 4 * g + r;
+        const float v = !VL || (t >= begin && t < end) ? vn.get(i, r) : 0.f;
+        X[i][r] = fmaf(-ki[i][r], X[i][r], v);
         bx[i][r] = be[i][r] * X[i][r];
       }
     pc.step();
-    if (pc.valid()) vn.load(vb + pc.win * kC * a.rows.v, a.rows.v, pc.begin, pc.end, g);
+    if (pc.valid()) vn.load(vb + pc.win * kC * a.rows.v, vrow, voff, pc.n);
     // w = X + R (b X); u = b w
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -711,19 +715,24 @@ __global__ __launch_bounds__(128 * C) void delta_chain_bf16_kernel(DeltaArgs a, 
       for (int i = 2 * s; i < 4; ++i) X[i] = M::mma(rf[low_frag(i, s)].hi, xb.hi, X[i]);
     }
     if constexpr (SAVE)
-      Column::put(reinterpret_cast<float*>(a.ws + ws.w) + bhw * kC * a.P + p, a.P, X, begin, end, g);
+      Column::put<VL>(reinterpret_cast<float*>(a.ws + ws.w) + bhw * kC * a.P, P, 4 * g * P + p, kC, X, begin, end, g);
 #pragma unroll
     for (int j = 0; j < NT; ++j) S[j] *= whole;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      float v[8], u[8];
+      float v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int t = 32 * s + 16 * (e / 4) + 4 * g + e % 4, i = 2 * s + e / 4, r = e % 4;
-        u[e] = !VL || (t >= begin && t < end) ? be[i][r] * X[i][r] : 0.f;
-        v[e] = u[e] * ko[i][r];
+      for (int t4 = 0; t4 < 2; ++t4) {
+        const int i = 2 * s + t4;
+        f32x4_t u;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = 16 * i + 4 * g + r;
+          u[r] = !VL || (t >= begin && t < end) ? be[i][r] * X[i][r] : 0.f;
+          v[4 * t4 + r] = u[r] * ko[i][r];
+        }
+        if constexpr (!SAVE) *reinterpret_cast<f32x4_t*>(x + KS * 2048 + i * 1024 + 16 * lane) = u;
       }
-      if constexpr (!SAVE) M::store(x + (KS + s) * 2048, lane, M::two(u));
       const Two ub = M::two(v);
 #pragma unroll
       for (int j = 0; j < NT; ++j) S[j] = M::mma(kT[s][j], ub.lo, S[j]);
@@ -733,30 +742,14 @@ __global__ __launch_bounds__(128 * C) void delta_chain_bf16_kernel(DeltaArgs a, 
     if constexpr (VL) {
       const int64_t last = row + win * kC + end - 1;
       if (marks && marks[last]) {
-        for (int64_t s = 0; s < a.nseq; ++s) {
-          if (a.seq_last[s] != last) continue;
-          float* out = a.seq_states + (s * a.H + h) * N * a.P + p;
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int nn = 16 * j + 4 * g + r;
-              if (nn < N) out[nn * a.P] = S[j][r];
-            }
-        }
+        for (int64_t s = 0; s < a.nseq; ++s)
+          if (a.seq_last[s] == last)
+            put_state<NT>(a.seq_states + (s * a.H + h) * N * a.P, N, P, 4 * g * P + p, S);
       }
     }
     __syncthreads();
   }
-  if (!SAVE && a.hfin) {
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int nn = 16 * j + 4 * g + r;
-        if (nn < N) a.hfin[(bh * N + nn) * a.P + p] = S[j][r];
-      }
-  }
+  if (!SAVE && a.hfin) put_state<NT>(a.hfin + bh * N * a.P, N, P, 4 * g * P + p, S);
 }
 
 // ---------------------------------------------------------------- one token

@@ -265,90 +265,112 @@ struct TriTile {
     for (int i = 0; i < NV; ++i) reinterpret_cast<u32x4v*>(p)[tid + i * NTHR] = q[i];
   }
 };
-// 64 rows of NP bf16 values (N of them there), rows outside [begin, end) zero.
-// Loads are unconditional, of rows that are there, and what does not belong is
-// dropped when it is stored: a branch a load would wait for each.
+// Rows of a window through a buffer descriptor: a lane's offset in one register,
+// the row's in a scalar, and rows behind the window's n read as zero and are not
+// written.  64 rows stay below 2^32 bytes (rows below 2^23 elements).
+constexpr uint32_t kNowhere = 0xfffffff0u;  // a lane's offset that is behind every window
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00027000);
+}
+
+// 64 rows of NP bf16 values (N of them there).
 template <int NP, int NTHR>
 struct RowTile {
   static constexpr int kPer = NP / 8, kRows = NTHR / kPer > 0 ? NTHR / kPer : 1, NV = kC * kPer / NTHR;
   static_assert(NTHR % kPer == 0 && kC % kRows == 0, "whole rows at a time");
-  uint4 q[NV];
-  __device__ __forceinline__ void load(const uint16_t* base, int64_t stride, int N, int begin, int end, int tid) {
-    const int t = tid / kPer, col = tid % kPer * 8;
-    const uint16_t* p = base + (col < N ? col : 0);
+  u32x4v q[NV];
+  // the window's first row, rows `stride` apart
+  __device__ __forceinline__ void load(const uint16_t* base, uint32_t stride, int N, int n, int tid) {
+    const uint32_t col = tid % kPer * 8;
+    const uint32_t off = (int)col < N ? (tid / kPer * stride + col) * 2 : kNowhere;
+    const __amdgpu_buffer_rsrc_t r = rows_of(base, (uint32_t)n * stride * 2);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      q[i] = *reinterpret_cast<const uint4*>(p + min(max(t + i * kRows, begin), end - 1) * stride);
+      q[i] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(r, off, i * kRows * stride * 2, 0));
   }
-  __device__ __forceinline__ void store(uint16_t* tile, int pitch, int N, int begin, int end, int tid) const {
+  // PARTS: rows outside [begin, end) as zero
+  template <bool PARTS>
+  __device__ __forceinline__ void store(uint16_t* tile, int pitch, int begin, int end, int tid) const {
     const int t = tid / kPer, col = tid % kPer * 8;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int ti = t + i * kRows;
-      const bool on = ti >= begin && ti < end && col < N;
-      *reinterpret_cast<uint4*>(tile + ti * pitch + col) = make_uint4(on ? q[i].x : 0, on ? q[i].y : 0, on ? q[i].z : 0,
-                                                                     on ? q[i].w : 0);
+      u32x4v v = q[i];
+      if constexpr (PARTS) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = ti >= begin && ti < end ? v[e] : 0u;
+      }
+      *reinterpret_cast<u32x4v*>(tile + ti * pitch + col) = v;
     }
   }
 };
-// Five gates of 64 tokens, zero outside [begin, end).
+// Five gates of 64 tokens, zero outside [begin, end) (behind the row's end they are zero as prepared).
 template <int NTHR>
 struct GateTile {
   static constexpr int kAll = 5 * kC / 4, NV = (kAll + NTHR - 1) / NTHR;
-  float4 q[NV];
+  f32x4_t q[NV];
   __device__ __forceinline__ void load(const DeltaGates* g, int tid) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) q[i] = reinterpret_cast<const float4*>(g)[min(tid + i * NTHR, kAll - 1)];
+    for (int i = 0; i < NV; ++i) q[i] = reinterpret_cast<const f32x4_t*>(g)[min(tid + i * NTHR, kAll - 1)];
   }
+  template <bool PARTS>
   __device__ __forceinline__ void store(float* p, int begin, int end, int tid) const {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = tid + i * NTHR, t = 4 * e % kC;
-      const float4 v = q[i];
-      if (e < kAll)
-        reinterpret_cast<float4*>(p)[e] =
-            make_float4(t >= begin && t < end ? v.x : 0.f, t + 1 >= begin && t + 1 < end ? v.y : 0.f,
-                        t + 2 >= begin && t + 2 < end ? v.z : 0.f, t + 3 >= begin && t + 3 < end ? v.w : 0.f);
+      f32x4_t v = q[i];
+      if constexpr (PARTS) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = t + r >= begin && t + r < end ? v[r] : 0.f;
+      }
+      if (e < kAll) reinterpret_cast<f32x4_t*>(p)[e] = v;
     }
   }
 };
-// A lane's 16 tokens (rows 16 i + 4 g + r) of one column.
+// A lane's 16 tokens (rows 16 i + 4 g + r) of one column, at lane offset
+// (4 g stride + column) elements.
 struct Column {
   uint16_t q[16];
-  __device__ __forceinline__ void load(const uint16_t* p, int64_t stride, int begin, int end, int g) {
+  __device__ __forceinline__ static uint32_t row(int e) { return 16 * (e / 4) + e % 4; }
+  __device__ __forceinline__ void load(const uint16_t* base, uint32_t stride, uint32_t off, int n) {
+    const __amdgpu_buffer_rsrc_t r = rows_of(base, (uint32_t)n * stride * 2);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) q[e] = p[min(max(16 * (e / 4) + 4 * g + e % 4, begin), end - 1) * stride];
+    for (int e = 0; e < 16; ++e) q[e] = __builtin_amdgcn_raw_buffer_load_b16(r, off * 2, row(e) * stride * 2, 0);
   }
-  // bf16 values into rows [begin, end) of a column
-  __device__ __forceinline__ static void put(uint16_t* p, int64_t stride, const f32x4_t* v, int begin, int end, int g) {
-    if (begin == 0 && end == kC) {
+  __device__ __forceinline__ float get(int i, int r) const { return bf16_bits_to_f32(q[4 * i + r]); }
+  template <bool PARTS>
+  __device__ __forceinline__ static void put(uint16_t* base, uint32_t stride, uint32_t off, int n, const f32x4_t* v,
+                                             int begin, int end, int g) {
+    const __amdgpu_buffer_rsrc_t r = rows_of(base, (uint32_t)n * stride * 2);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) p[(16 * (e / 4) + 4 * g + e % 4) * stride] = IoBF16::put(v[e / 4][e % 4]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int t = 16 * (e / 4) + 4 * g + e % 4;
-        if (t >= begin && t < end) p[t * stride] = IoBF16::put(v[e / 4][e % 4]);
-      }
+    for (int e = 0; e < 16; ++e) {
+      const int t = (int)row(e) + 4 * g;
+      __builtin_amdgcn_raw_buffer_store_b16(IoBF16::put(v[e / 4][e % 4]), r,
+                                            !PARTS || (t >= begin && t < end) ? off * 2 : kNowhere, row(e) * stride * 2, 0);
     }
   }
-  __device__ __forceinline__ static void put(float* p, int64_t stride, const f32x4_t* v, int begin, int end, int g) {
-    if (begin == 0 && end == kC) {
+  template <bool PARTS>
+  __device__ __forceinline__ static void put(float* base, uint32_t stride, uint32_t off, int n, const f32x4_t* v,
+                                             int begin, int end, int g) {
+    const __amdgpu_buffer_rsrc_t r = rows_of(base, (uint32_t)n * stride * 4);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) p[(16 * (e / 4) + 4 * g + e % 4) * stride] = v[e / 4][e % 4];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int t = 16 * (e / 4) + 4 * g + e % 4;
-        if (t >= begin && t < end) p[t * stride] = v[e / 4][e % 4];
-      }
+    for (int e = 0; e < 16; ++e) {
+      const int t = (int)row(e) + 4 * g;
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[e / 4][e % 4]), r,
+                                            !PARTS || (t >= begin && t < end) ? off * 4 : kNowhere, row(e) * stride * 4, 0);
     }
-  }
-  __device__ __forceinline__ float get(int i, int r, int begin, int end, int g) const {
-    const int t = 16 * i + 4 * g + r;
-    return t >= begin && t < end ? bf16_bits_to_f32(q[4 * i + r]) : 0.f;
   }
 };
+// A state's accumulators into [N, P] fp32 (N rows of them), lane offset (4 g P + column).
+template <int NT>
+__device__ __forceinline__ void put_state(float* base, int N, uint32_t P, uint32_t off, const f32x4_t* S) {
+  const __amdgpu_buffer_rsrc_t r = rows_of(base, (uint32_t)N * P * 4);
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[j][e]), r, off * 4, (16 * j + e) * P * 4, 0);
+}
 
 // Neighbouring blocks (slices of a head, heads of a group) on one XCD's L2.
 __device__ __forceinline__ uint32_t near_block(uint32_t bid, uint32_t n) {
