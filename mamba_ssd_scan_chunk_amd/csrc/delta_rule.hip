@@ -17,7 +17,7 @@ namespace ssd {
 // ---------------------------------------------------------------- preparation
 constexpr int kTP = kC + 4;  // pitch of the 64 x 64 fp32 tiles in LDS
 constexpr int kMP = 20;      // of a 16 x 16 one
-constexpr int kPrepLds = 4 * kC * kTP * 4 + 4 * 16 * kMP * 4 + kC * 8 + 5 * kC * 4;
+constexpr int kPrepLds = 2 * kC * kTP * 4 + 4 * 16 * kMP * 4 + kC * 8 + 5 * kC * 4;
 
 __device__ __forceinline__ f32x4_t mma4(const float4& a, const f32x4_t& b, f32x4_t c) {
   c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.x, b[0], c, 0, 0, 0);
@@ -25,22 +25,28 @@ __device__ __forceinline__ f32x4_t mma4(const float4& a, const f32x4_t& b, f32x4
   c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.z, b[2], c, 0, 0, 0);
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a.w, b[3], c, 0, 0, 0);
 }
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
 
-// Four waves.  Wave i takes rows 16 i .. of the Gram products, then column
-// block i of R: with T = I + E diag(b) in blocks of 16,
+// Four waves.  Wave i takes the Gram products of rows 16 i .. (BACK: of columns
+// 16 i ..), so that its accumulators are P's (P^T's) fragments as they are,
+// then column block i of R: with T = I + E diag(b) in blocks of 16,
 //     R_ij = T_ii^-1 (-E_ij - sum_{j <= k < i} (E b)_ik R_kj),  T_ii^-1 = I + R_ii diag(b),
 // the diagonal blocks by substitution, a lane a column, the others by fp32
-// matrix instructions.  Entries between pieces are set, not multiplied, to
-// zero, so that no value of one sequence meets another's.
-template <class M, bool BACK>
+// matrix instructions; R takes E's place in LDS.  Entries between pieces are
+// set, not multiplied, to zero, so that no value of one sequence meets
+// another's.  Bound by the latency of its few dependent parts: all of a
+// wave's loads (of 128 key columns) are asked for together.
+template <class M, int NP, bool BACK, bool VL>
 __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaWs ws) {
   typedef typename M::IO::type T;
+  typedef typename M::One One;
   extern __shared__ __align__(16) char lds[];
   float(*E)[kTP] = reinterpret_cast<float(*)[kTP]>(lds);
+  float(*R)[kTP] = E;
   float(*Eb)[kTP] = E + kC;
-  float(*Pm)[kTP] = Eb + kC;
-  float(*R)[kTP] = Pm + kC;
-  float(*Md)[16][kMP] = reinterpret_cast<float(*)[16][kMP]>(R + kC);
+  float(*Md)[16][kMP] = reinterpret_cast<float(*)[16][kMP]>(Eb + kC);
   double* sG = reinterpret_cast<double*>(Md + 4);
   float* sBeta = reinterpret_cast<float*>(sG + kC);
   float* sIn = sBeta + kC;
@@ -50,35 +56,82 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaWs
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int64_t bid = near_block(blockIdx.x, gridDim.x);
-  const int64_t h = bid % a.H, win = bid / a.H % ws.nw, b = bid / a.H / ws.nw;
+  const uint32_t bid = near_block(blockIdx.x, gridDim.x), H = (uint32_t)a.H, nw = (uint32_t)ws.nw;
+  const int64_t h = bid % H, win = bid / H % nw, b = bid / H / nw;
   const int64_t row = b * a.L, t0 = win * kC, bhw = (b * a.H + h) * ws.nw + win;
-  const int64_t grp = h / (a.H / a.G);
-  const int n = (int)(a.L - t0 < kC ? a.L - t0 : kC);
-  const uint8_t* marks = !BACK && a.nseq > 0 ? reinterpret_cast<const uint8_t*>(a.ws + ws.marks) : nullptr;
+  const int64_t grp = (uint32_t)h / (H / (uint32_t)a.G);
+  const int n = (int)(a.L - t0 < kC ? a.L - t0 : kC), N = (int)a.N;
+
+  // the gates' inputs, a token a lane of wave 0
+  float raw = 0.f, beta = 0.f;
+  if (wave == 0) {
+    const int64_t t = row + t0 + min(lane, n - 1);
+    raw = M::IO::get(static_cast<const T*>(a.dt)[t * a.rows.dt + h]);
+    beta = M::IO::get(static_cast<const T*>(a.beta)[t * a.rows.beta + h]);
+  }
+  // Gram products: kk[j], pq[j] of tiles (wave, j), the columns the wave's own
+  // tokens (BACK: (j, wave), j >= wave)
+  const T* kbase = static_cast<const T*>(a.k) + (row + t0) * a.rows.k + grp * N;
+  const T* qbase = static_cast<const T*>(a.q) + (row + t0) * a.rows.q + grp * N;
+  f32x4_t kk[4], pq[4], qq = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) kk[j] = pq[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  constexpr int SL = NP / 32 < 4 ? NP / 32 : 4;
+#pragma unroll
+  for (int s0 = 0; s0 < NP / 32; s0 += SL) {
+    One kf[4][SL], qf[BACK ? 4 : 1][SL], mine[SL];
+    constexpr uint32_t es = sizeof(T);
+    const uint32_t krow = (uint32_t)a.rows.k * es, qrow = (uint32_t)a.rows.q * es;
+    const __amdgpu_buffer_rsrc_t kr = rows_of(kbase, (uint32_t)n * krow), qr = rows_of(qbase, (uint32_t)n * qrow);
+    auto load = [&](const __amdgpu_buffer_rsrc_t r, uint32_t stride, int tile, int s) {
+      const uint32_t col = 32 * s + 8 * g;
+      return M::rows8(r, (int)col < N ? c * stride + col * es : kNowhere, 16 * tile * stride);
+    };
+#pragma unroll
+    for (int s = 0; s < SL; ++s) {
+      mine[s] = load(qr, qrow, wave, s0 + s);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (BACK ? j < wave : j > wave) continue;
+        kf[j][s] = load(kr, krow, j, s0 + s);
+        if constexpr (BACK) qf[j][s] = load(qr, qrow, j, s0 + s);
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < SL; ++s) {
+      One own = kf[0][s];
+#pragma unroll
+      for (int j = 1; j < 4; ++j)
+        if (j == wave) own = kf[j][s];
+      qq = M::mma(mine[s], mine[s], qq);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (BACK ? j < wave : j > wave) continue;
+        kk[j] = M::mma(kf[j][s], own, kk[j]);
+        if constexpr (BACK) pq[j] = M::mma(qf[j][s], own, pq[j]);
+        else pq[j] = M::mma(kf[j][s], mine[s], pq[j]);
+      }
+    }
+  }
   Cuts both = {0, 0};
-  if (a.seq_idx || marks) {
+  if constexpr (VL) {
+    const uint8_t* marks = !BACK && a.nseq > 0 ? reinterpret_cast<const uint8_t*>(a.ws + ws.marks) : nullptr;
     both = window_cuts(a.seq_idx, marks, row, t0, a.L, lane);
     if (h == 0 && threadIdx.x == 0) reinterpret_cast<Cuts*>(a.ws + ws.cuts)[b * ws.nw + win] = both;
   }
   const uint64_t cuts = both.piece;
-  DeltaGates* gates = reinterpret_cast<DeltaGates*>(a.ws + ws.gates) + bhw;
+  auto same = [&](int t, int s) { return !VL || piece_of(cuts, t) == piece_of(cuts, s); };
 
   if (wave == 0) {
     const bool in = lane < n;
-    float gv = 0.f, beta = 0.f;
-    if (in) {
-      const int64_t t = row + t0 + lane;
-      float raw = M::IO::get(static_cast<const T*>(a.dt)[t * a.rows.dt + h]);
-      if (a.dt_bias) raw += a.dt_bias[h];
-      const float step = a.softplus ? softplus2(raw * kLog2e) * kLn2 : raw;
-      gv = step * a.A[h];
-      if (gv < -1e5f) gv = -1e5f;  // e^gv is 0 well before; sums stay finite
-      beta = M::IO::get(static_cast<const T*>(a.beta)[t * a.rows.beta + h]);
-      if (a.sigmoid) beta = sigmoid(beta);
-    }
-    const int begin = piece_begin(cuts, lane + 1);
-    const int end = piece_end(cuts, begin, n);
+    if (a.dt_bias) raw += a.dt_bias[h];
+    const float step = a.softplus ? softplus2(raw * kLog2e) * kLn2 : raw;
+    float gv = step * a.A[h];
+    if (gv < -1e5f) gv = -1e5f;  // e^gv is 0 well before; sums stay finite
+    if (a.sigmoid) beta = sigmoid(beta);
+    if (!in) gv = beta = 0.f;
+    const int begin = VL ? piece_begin(cuts, lane + 1) : 0;
+    const int end = VL ? piece_end(cuts, begin, n) : n;
     // sums in 64 bits: differences of far tokens keep all of an exponent's bits
     double G = gv;
 #pragma unroll
@@ -91,28 +144,6 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaWs
     sBeta[lane] = beta;
     sIn[lane] = in ? expf((float)G) : 0.f;
     sOut[lane] = in ? expf((float)(last - G)) : 0.f;
-  }
-  // Gram tiles of rows 16 wave ..
-  f32x4_t kk[4], qk[4], qq = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) kk[j] = qk[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const T* kbase = static_cast<const T*>(a.k) + (row + t0) * a.rows.k + grp * a.N;
-  const T* qbase = static_cast<const T*>(a.q) + (row + t0) * a.rows.q + grp * a.N;
-  for (int s = 0; s * 32 < (int)a.N; ++s) {
-    const int col = 32 * s + 8 * g;
-    auto load = [&](const T* base, int64_t stride, int tile) {
-      const int t = 16 * tile + c;
-      return t < n && col < (int)a.N ? M::global8(base + t * stride + col) : M::zero();
-    };
-    const typename M::One ka = load(kbase, a.rows.k, wave), qa = load(qbase, a.rows.q, wave);
-    qq = M::mma(qa, qa, qq);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j > wave) continue;
-      const typename M::One kb = j == wave ? ka : load(kbase, a.rows.k, j);
-      kk[j] = M::mma(ka, kb, kk[j]);
-      qk[j] = M::mma(qa, kb, qk[j]);
-    }
   }
   // lengths from the diagonals
 #pragma unroll
@@ -127,114 +158,140 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaWs
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int s = 16 * j + c;
+    const bool there = BACK ? j >= wave : j <= wave;  // on and below the diagonal
+    f32x4_t e4 = {0.f, 0.f, 0.f, 0.f}, b4 = e4;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int t = 16 * wave + 4 * g + r;
-      float e = 0.f, eb = 0.f, p = 0.f;
-      if (j <= wave && s <= t && t < n && piece_of(cuts, t) == piece_of(cuts, s)) {
+      const int x = 16 * j + 4 * g + r, y = 16 * wave + c, t = BACK ? x : y, s = BACK ? y : x;
+      float p = 0.f;
+      if (there && s <= t && t < n && same(t, s)) {
         const float rel = expf((float)(sG[t] - sG[s])) * sRk[s];
-        p = rel * sRq[t] * qk[j][r];
+        p = rel * sRq[t] * pq[j][r];
         if (s < t) {
-          e = rel * sRk[t] * kk[j][r];
-          eb = e * sBeta[s];
+          e4[r] = rel * sRk[t] * kk[j][r];
+          b4[r] = e4[r] * sBeta[s];
         }
       }
-      E[t][s] = e;
-      Eb[t][s] = eb;
-      Pm[t][s] = p;
-      if (j > wave) R[t][s] = 0.f;
+      pq[j][r] = p;
+      if constexpr (BACK) {
+        E[t][s] = e4[r];
+        Eb[t][s] = b4[r];
+      }
+    }
+    if constexpr (!BACK) {
+      *reinterpret_cast<f32x4_t*>(&E[16 * wave + c][16 * j + 4 * g]) = e4;
+      *reinterpret_cast<f32x4_t*>(&Eb[16 * wave + c][16 * j + 4 * g]) = b4;
     }
   }
   if (wave == 0) {
     const float in = sIn[lane];
+    DeltaGates* gates = reinterpret_cast<DeltaGates*>(a.ws + ws.gates) + bhw;
     gates->beta[lane] = sBeta[lane];
     gates->kin[lane] = in * sRk[lane];
     gates->qin[lane] = in * sRq[lane];
     gates->kout[lane] = sOut[lane] * sRk[lane];
     gates->in[lane] = in;
-    gates->rk[lane] = sRk[lane];
-    gates->rq[lane] = sRq[lane];
-    gates->G[lane] = sG[lane];
+    if constexpr (BACK) {
+      gates->rk[lane] = sRk[lane];
+      gates->rq[lane] = sRq[lane];
+      gates->G[lane] = sG[lane];
+    }
+  }
+  // P's fragments: lane (c, g), slots 4t + r, contraction index 32 s + 16 t + 4 g + r
+  {
+    char* out = a.ws + (BACK ? ws.up_p : ws.low_p) + bhw * kTriBytes;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (BACK ? wave >= 2 * s + 2 : 2 * s > wave) continue;
+      float v[8];
+      slots(pq[2 * s], pq[2 * s + 1], v);
+      M::store(out + (BACK ? up_frag(wave, s) : low_frag(wave, s)) * 2048, lane, M::two(v));
+    }
   }
   __syncthreads();
+  f32x4_t col[4];
   {
     const int o = 16 * wave;
-    float r[16];
+    float r[16], eb[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float v = -E[o + i][o + c];
-#pragma unroll
-      for (int k = 0; k < i; ++k) v = fmaf(-Eb[o + i][o + k], r[k], v);
-      r[i] = c < i && piece_of(cuts, o + i) == piece_of(cuts, o + c) ? v : 0.f;
+      r[i] = -E[o + i][o + c];
+      eb[i] = Eb[o + i][o + c];
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      r[i] = c < i && same(o + i, o + c) ? r[i] : 0.f;
+#pragma unroll
+      for (int k = i + 1; k < 16; ++k) r[k] = fmaf(-lane_value(eb[k], i), r[i], r[k]);
+    }
+    const float beta = sBeta[o + c];
     if (g == 0) {
-      const float beta = sBeta[o + c];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const bool on = c < i && piece_of(cuts, o + i) == piece_of(cuts, o + c);
+        const bool on = c < i && same(o + i, o + c);
         R[o + i][o + c] = r[i];
         Md[wave][i][c] = i == c ? 1.f : on ? r[i] * beta : 0.f;
       }
     }
-  }
-  __syncthreads();
-  {
-    f32x4_t col[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (i < wave) continue;
+      col[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       if (i == wave) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) col[i][r] = R[16 * i + 4 * g + r][16 * wave + c];
-        continue;
-      }
-      f32x4_t acc;
+        for (int e = 0; e < 4; ++e) {
+          float v = r[e];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[r] = -E[16 * i + 4 * g + r][16 * wave + c];
-#pragma unroll
-      for (int k = 0; k < i; ++k) {
-        if (k < wave) continue;
-        float4 m = *reinterpret_cast<const float4*>(&Eb[16 * i + c][16 * k + 4 * g]);
-        m = make_float4(-m.x, -m.y, -m.z, -m.w);
-        acc = mma4(m, col[k], acc);
-      }
-      const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-      col[i] = mma4(*reinterpret_cast<const float4*>(&Md[i][c][4 * g]), acc, zero);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 16 * i + 4 * g + r;
-        R[t][16 * wave + c] = piece_of(cuts, t) == piece_of(cuts, 16 * wave + c) ? col[i][r] : 0.f;
+          for (int k = 1; k < 4; ++k) v = g == k ? r[4 * k + e] : v;
+          col[i][e] = v;
+        }
       }
     }
   }
   __syncthreads();
-  // fragments: lane (c, g), slots 4t + r, column (of the contraction) 32 s + 16 t + 4 g + r
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    if (i <= wave) continue;
+    f32x4_t acc;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[r] = -E[16 * i + 4 * g + r][16 * wave + c];
+#pragma unroll
+    for (int k = 0; k < i; ++k) {
+      if (k < wave) continue;
+      float4 m = *reinterpret_cast<const float4*>(&Eb[16 * i + c][16 * k + 4 * g]);
+      m = make_float4(-m.x, -m.y, -m.z, -m.w);
+      acc = mma4(m, col[k], acc);
+    }
+    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+    col[i] = mma4(*reinterpret_cast<const float4*>(&Md[i][c][4 * g]), acc, zero);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 16 * i + 4 * g + r;
+      const float v = same(t, 16 * wave + c) ? col[i][r] : 0.f;
+      R[t][16 * wave + c] = v;
+      if constexpr (BACK) pq[i][r] = v;
+    }
+  }
+  if constexpr (BACK) {
+    char* out = a.ws + ws.up_r + bhw * kTriBytes;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i <= wave) pq[i] = col[i];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (wave >= 2 * s + 2) continue;
+      float v[8];
+      slots(pq[2 * s], pq[2 * s + 1], v);
+      M::store(out + up_frag(wave, s) * 2048, lane, M::two(v));
+    }
+  }
+  __syncthreads();
   char* low_r = a.ws + ws.low_r + bhw * kTriBytes;
-  auto put_low = [&](char* base, float(*m)[kTP], int f) {
+  for (int f = wave; f < kTriFrags; f += 4) {
     const int i = f < 2 ? f : 2 + (f - 2) / 2, s = f < 2 ? 0 : (f - 2) % 2;
-    const float* p = &m[16 * i + c][32 * s + 4 * g];
+    const float* p = &R[16 * i + c][32 * s + 4 * g];
     const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 16);
     const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-    M::store(base + f * 2048, lane, M::two(v));
-  };
-  for (int f = wave; f < kTriFrags; f += 4) put_low(low_r, R, f);
-  if constexpr (!BACK) {
-    char* low_p = a.ws + ws.low_p + bhw * kTriBytes;
-    for (int f = 3 - wave; f < kTriFrags; f += 4) put_low(low_p, Pm, f);
-  } else {
-    char* up_r = a.ws + ws.up_r + bhw * kTriBytes;
-    char* up_p = a.ws + ws.up_p + bhw * kTriBytes;
-    for (int f = wave; f < 2 * kTriFrags; f += 4) {
-      const bool pm = f >= kTriFrags;
-      const int u = pm ? f - kTriFrags : f;
-      const int i = u < 4 ? u / 2 : u - 2, s = u < 4 ? u % 2 : 1;
-      float(*m)[kTP] = pm ? Pm : R;
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = m[32 * s + 16 * (e / 4) + 4 * g + e % 4][16 * i + c];
-      M::store((pm ? up_p : up_r) + u * 2048, lane, M::two(v));
-    }
+    M::store(low_r + f * 2048, lane, M::two(v));
   }
 }
 
@@ -870,13 +927,22 @@ size_t delta_forward_ws_bytes(int64_t B, int64_t L, int64_t H, int64_t G, int64_
   return delta_ws(B, L, H, N, P, false).total;
 }
 
-hipError_t launch_delta_prepare(const DeltaArgs& a, const DeltaWs& ws, bool back, bool bf16, hipStream_t s) {
-  auto kern = bf16 ? (back ? delta_prepare_kernel<DeltaB, true> : delta_prepare_kernel<DeltaB, false>)
-                   : (back ? delta_prepare_kernel<DeltaF, true> : delta_prepare_kernel<DeltaF, false>);
-  hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, kPrepLds);
-  if (e != hipSuccess) return e;
+template <class M, int NP, bool BACK>
+static hipError_t prepare(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) {
+  const bool vl = a.seq_idx || (!BACK && a.nseq > 0);
+  auto kern = vl ? delta_prepare_kernel<M, NP, BACK, true> : delta_prepare_kernel<M, NP, BACK, false>;
   hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * ws.nw * a.H)), dim3(256), kPrepLds, s, a, ws);
   return hipGetLastError();
+}
+template <class M, bool BACK>
+static hipError_t prepare_at(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) {
+  return a.N <= 64    ? prepare<M, 64, BACK>(a, ws, s)
+         : a.N <= 128 ? prepare<M, 128, BACK>(a, ws, s)
+                      : prepare<M, 256, BACK>(a, ws, s);
+}
+hipError_t launch_delta_prepare(const DeltaArgs& a, const DeltaWs& ws, bool back, bool bf16, hipStream_t s) {
+  if (bf16) return back ? prepare_at<DeltaB, true>(a, ws, s) : prepare_at<DeltaB, false>(a, ws, s);
+  return back ? prepare_at<DeltaF, true>(a, ws, s) : prepare_at<DeltaF, false>(a, ws, s);
 }
 
 // Enough blocks for every compute unit come before waves that share k and q.

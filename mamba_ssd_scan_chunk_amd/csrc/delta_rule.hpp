@@ -30,6 +30,16 @@ namespace ssd {
 constexpr float kQkEps = 1e-6f;
 constexpr int kC = (int)kDeltaC;
 
+// Rows of a window through a buffer descriptor: a lane's offset in one register,
+// the row's in a scalar, and rows behind the window's n read as zero and are not
+// written.  64 rows stay below 2^32 bytes (rows below 2^23 elements).
+constexpr uint32_t kNowhere = 0xfffffff0u;  // a lane's offset that is behind every window
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00027000);
+}
+
+typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));  // copied as a value, where uint4 is a struct
+
 // One: an operand of inputs.  Two: of computed values.
 struct DeltaB {
   typedef IoBF16 IO;
@@ -77,6 +87,12 @@ struct DeltaB {
     f.v = *reinterpret_cast<const uint4*>(p);
     return f;
   }
+  // the same by byte offsets of a lane and of a row
+  __device__ __forceinline__ static One rows8(__amdgpu_buffer_rsrc_t r, uint32_t lane, uint32_t row) {
+    One f;
+    f.v = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, lane, row, 0));
+    return f;
+  }
   __device__ __forceinline__ static One zero() { return OpBF16::zero(); }
   // rows of a tile in LDS as the transposed operand: lane (i, g) gets, as slots
   // 4t + r, tile[16t + 4g + r][i]
@@ -102,6 +118,12 @@ struct DeltaF {
     *reinterpret_cast<float4*>(p + 1024 + 16 * lane) = t.hi;
   }
   __device__ __forceinline__ static One global8(const float* p) { return Lds<OpF32>::load8(p); }
+  __device__ __forceinline__ static One rows8(__amdgpu_buffer_rsrc_t r, uint32_t lane, uint32_t row) {
+    One f;
+    f.lo = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(r, lane, row, 0));
+    f.hi = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(r, lane, row + 16, 0));
+    return f;
+  }
   __device__ __forceinline__ static One zero() { return OpF32::zero(); }
   __device__ __forceinline__ static One transposed(const float* tile, int pitch, int lane) {
     const float* p = tile + 4 * (lane >> 4) * pitch + (lane & 15);
@@ -250,7 +272,6 @@ __device__ __forceinline__ void slots(const f32x4_t& lo, const f32x4_t& hi, floa
 }
 
 // ---- staging by a chain's helper waves ----
-typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));  // copied as a value, where uint4 is a struct
 // The six fragments of a triangular operand.
 template <int NTHR>
 struct TriTile {
@@ -265,14 +286,6 @@ struct TriTile {
     for (int i = 0; i < NV; ++i) reinterpret_cast<u32x4v*>(p)[tid + i * NTHR] = q[i];
   }
 };
-// Rows of a window through a buffer descriptor: a lane's offset in one register,
-// the row's in a scalar, and rows behind the window's n read as zero and are not
-// written.  64 rows stay below 2^32 bytes (rows below 2^23 elements).
-constexpr uint32_t kNowhere = 0xfffffff0u;  // a lane's offset that is behind every window
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* base, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00027000);
-}
-
 // 64 rows of NP bf16 values (N of them there).
 template <int NP, int NTHR>
 struct RowTile {
