@@ -39,7 +39,7 @@ __device__ __forceinline__ float lane_value(float v, int lane) {
 // another's.  Bound by the latency of its few dependent parts: all of a
 // wave's loads (of 128 key columns) are asked for together.
 template <class M, int NP, bool BACK, bool VL>
-__global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaWs ws) {
+__global__ __launch_bounds__(256, 2) void delta_prepare_kernel(DeltaArgs a, DeltaWs ws) {
   typedef typename M::IO::type T;
   typedef typename M::One One;
   extern __shared__ __align__(16) char lds[];
@@ -132,8 +132,8 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaWs
     if (!in) gv = beta = 0.f;
     const int begin = VL ? piece_begin(cuts, lane + 1) : 0;
     const int end = VL ? piece_end(cuts, begin, n) : n;
-    // sums in 64 bits: differences of far tokens keep all of an exponent's bits
-    double G = gv;
+    // in units of ln 2, and in 64 bits: differences of far tokens keep all of an exponent's bits
+    double G = (double)gv * 1.4426950408889634;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const double o = __shfl_up(G, off, 64);
@@ -142,8 +142,8 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaWs
     const double last = __shfl(G, end - 1, 64);
     sG[lane] = G;
     sBeta[lane] = beta;
-    sIn[lane] = in ? expf((float)G) : 0.f;
-    sOut[lane] = in ? expf((float)(last - G)) : 0.f;
+    sIn[lane] = in ? fast_exp2((float)G) : 0.f;
+    sOut[lane] = in ? fast_exp2((float)(last - G)) : 0.f;
   }
   // lengths from the diagonals
 #pragma unroll
@@ -156,31 +156,44 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaWs
     sRq[16 * wave + c] = (a.qk_norm ? 1.f / sqrtf(qq[r] + kQkEps) : 1.f) * a.scale;
   }
   __syncthreads();
+  {
+    const int y = 16 * wave + c;
+    const double Gy = sG[y];
+    const float ry = sRk[y], qy = sRq[y], by = sBeta[y];
+    double Gx[4][4];
+    float rx[4][4], ox[4][4];  // |k|^-1; BACK: |q|^-1 of the rows, else b of the columns
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const bool there = BACK ? j >= wave : j <= wave;  // on and below the diagonal
-    f32x4_t e4 = {0.f, 0.f, 0.f, 0.f}, b4 = e4;
+    for (int j = 0; j < 4; ++j) {
+      const int x = 16 * j + 4 * g;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int x = 16 * j + 4 * g + r, y = 16 * wave + c, t = BACK ? x : y, s = BACK ? y : x;
-      float p = 0.f;
-      if (there && s <= t && t < n && same(t, s)) {
-        const float rel = expf((float)(sG[t] - sG[s])) * sRk[s];
-        p = rel * sRq[t] * pq[j][r];
-        if (s < t) {
-          e4[r] = rel * sRk[t] * kk[j][r];
-          b4[r] = e4[r] * sBeta[s];
+      for (int r = 0; r < 4; ++r) Gx[j][r] = sG[x + r];
+      load_vec<IoF32, 4>(sRk + x, rx[j]);
+      load_vec<IoF32, 4>((BACK ? sRq : sBeta) + x, ox[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool there = BACK ? j >= wave : j <= wave;  // on and below the diagonal
+      f32x4_t e4, b4;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int x = 16 * j + 4 * g + r, t = BACK ? x : y, s = BACK ? y : x;
+        const bool on = there && s <= t && t < n && same(t, s);
+        const float rel = fast_exp2((float)(BACK ? Gx[j][r] - Gy : Gy - Gx[j][r])) * (BACK ? ry : rx[j][r]);
+        const float p = rel * (BACK ? ox[j][r] : qy) * pq[j][r];
+        const float e = rel * (BACK ? rx[j][r] : ry) * kk[j][r];
+        const float eb = e * (BACK ? by : ox[j][r]);
+        pq[j][r] = on ? p : 0.f;
+        e4[r] = on && s < t ? e : 0.f;
+        b4[r] = on && s < t ? eb : 0.f;
+        if constexpr (BACK) {
+          E[t][s] = e4[r];
+          Eb[t][s] = b4[r];
         }
       }
-      pq[j][r] = p;
-      if constexpr (BACK) {
-        E[t][s] = e4[r];
-        Eb[t][s] = b4[r];
+      if constexpr (!BACK) {
+        *reinterpret_cast<f32x4_t*>(&E[y][16 * j + 4 * g]) = e4;
+        *reinterpret_cast<f32x4_t*>(&Eb[y][16 * j + 4 * g]) = b4;
       }
-    }
-    if constexpr (!BACK) {
-      *reinterpret_cast<f32x4_t*>(&E[16 * wave + c][16 * j + 4 * g]) = e4;
-      *reinterpret_cast<f32x4_t*>(&Eb[16 * wave + c][16 * j + 4 * g]) = b4;
     }
   }
   if (wave == 0) {

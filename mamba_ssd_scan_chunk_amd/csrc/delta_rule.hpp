@@ -149,7 +149,7 @@ struct DeltaGates {
   float kout[kC];  // e^{G_end - G} |k|^-1
   float in[kC];    // e^G
   float rk[kC], rq[kC];  // |k|^-1, |q|^-1 scale
-  double G[kC];
+  double G[kC];    // in units of ln 2
 };
 // Triangular 64 x 64 operands: 6 of 8 fragments, those of row tile i and
 // 32-column step s that are not all zero.

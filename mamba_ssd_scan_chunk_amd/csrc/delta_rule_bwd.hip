@@ -425,7 +425,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
         const int t = 16 * wave + 4 * g + r;
         float m1 = 0.f, m2 = 0.f, lo = 0.f, up = 0.f;
         if (j <= wave && s >= begin && s <= t && t < end) {
-          const float rel = expf((float)(sG[t] - sG[s]));
+          const float rel = fast_exp2((float)(sG[t] - sG[s]));
           const float dqk = rel * dP[j][r];
           m1 = dqk * sRk[s];
           m2 = dqk * sRq[t];
