@@ -17,7 +17,7 @@ namespace ssd {
 // ---------------------------------------------------------------- preparation
 constexpr int kTP = kC + 4;  // pitch of the 64 x 64 fp32 tiles in LDS
 constexpr int kMP = 20;      // of a 16 x 16 one
-constexpr int kPrepLds = 2 * kC * kTP * 4 + 4 * 16 * kMP * 4 + kC * 8 + 5 * kC * 4;
+constexpr int kPrepLds = kC * kTP * 4 + 4 * 16 * kMP * 4 + kC * 8 + 5 * kC * 4;
 
 __device__ __forceinline__ f32x4_t mma4(const float4& a, const f32x4_t& b, f32x4_t c) {
   c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.x, b[0], c, 0, 0, 0);
@@ -28,6 +28,9 @@ __device__ __forceinline__ f32x4_t mma4(const float4& a, const f32x4_t& b, f32x4
 __device__ __forceinline__ float lane_value(float v, int lane) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
 }
+
+// e b where e is not zero: an entry between pieces stays zero whatever b is.
+__device__ __forceinline__ float times(float e, float b) { return e != 0.f ? e * b : 0.f; }
 
 // Four waves.  Wave i takes the Gram products of rows 16 i .. (BACK: of columns
 // 16 i ..), so that its accumulators are P's (P^T's) fragments as they are,
@@ -45,8 +48,7 @@ __global__ __launch_bounds__(256, 2) void delta_prepare_kernel(DeltaArgs a, Delt
   extern __shared__ __align__(16) char lds[];
   float(*E)[kTP] = reinterpret_cast<float(*)[kTP]>(lds);
   float(*R)[kTP] = E;
-  float(*Eb)[kTP] = E + kC;
-  float(*Md)[16][kMP] = reinterpret_cast<float(*)[16][kMP]>(Eb + kC);
+  float(*Md)[16][kMP] = reinterpret_cast<float(*)[16][kMP]>(E + kC);
   double* sG = reinterpret_cast<double*>(Md + 4);
   float* sBeta = reinterpret_cast<float*>(sG + kC);
   float* sIn = sBeta + kC;
@@ -159,41 +161,33 @@ __global__ __launch_bounds__(256, 2) void delta_prepare_kernel(DeltaArgs a, Delt
   {
     const int y = 16 * wave + c;
     const double Gy = sG[y];
-    const float ry = sRk[y], qy = sRq[y], by = sBeta[y];
+    const float ry = sRk[y], qy = sRq[y];
     double Gx[4][4];
-    float rx[4][4], ox[4][4];  // |k|^-1; BACK: |q|^-1 of the rows, else b of the columns
+    float rx[4][4], qx[4][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int x = 16 * j + 4 * g;
 #pragma unroll
       for (int r = 0; r < 4; ++r) Gx[j][r] = sG[x + r];
       load_vec<IoF32, 4>(sRk + x, rx[j]);
-      load_vec<IoF32, 4>((BACK ? sRq : sBeta) + x, ox[j]);
+      if constexpr (BACK) load_vec<IoF32, 4>(sRq + x, qx[j]);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const bool there = BACK ? j >= wave : j <= wave;  // on and below the diagonal
-      f32x4_t e4, b4;
+      f32x4_t e4;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int x = 16 * j + 4 * g + r, t = BACK ? x : y, s = BACK ? y : x;
         const bool on = there && s <= t && t < n && same(t, s);
         const float rel = fast_exp2((float)(BACK ? Gx[j][r] - Gy : Gy - Gx[j][r])) * (BACK ? ry : rx[j][r]);
-        const float p = rel * (BACK ? ox[j][r] : qy) * pq[j][r];
+        const float p = rel * (BACK ? qx[j][r] : qy) * pq[j][r];
         const float e = rel * (BACK ? rx[j][r] : ry) * kk[j][r];
-        const float eb = e * (BACK ? by : ox[j][r]);
         pq[j][r] = on ? p : 0.f;
         e4[r] = on && s < t ? e : 0.f;
-        b4[r] = on && s < t ? eb : 0.f;
-        if constexpr (BACK) {
-          E[t][s] = e4[r];
-          Eb[t][s] = b4[r];
-        }
+        if constexpr (BACK) E[t][s] = e4[r];
       }
-      if constexpr (!BACK) {
-        *reinterpret_cast<f32x4_t*>(&E[y][16 * j + 4 * g]) = e4;
-        *reinterpret_cast<f32x4_t*>(&Eb[y][16 * j + 4 * g]) = b4;
-      }
+      if constexpr (!BACK) *reinterpret_cast<f32x4_t*>(&E[y][16 * j + 4 * g]) = e4;
     }
   }
   if (wave == 0) {
@@ -226,18 +220,18 @@ __global__ __launch_bounds__(256, 2) void delta_prepare_kernel(DeltaArgs a, Delt
   {
     const int o = 16 * wave;
     float r[16], eb[16];
+    const float beta = sBeta[o + c];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       r[i] = -E[o + i][o + c];
-      eb[i] = Eb[o + i][o + c];
+      eb[i] = times(r[i], beta);
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       r[i] = c < i && same(o + i, o + c) ? r[i] : 0.f;
 #pragma unroll
-      for (int k = i + 1; k < 16; ++k) r[k] = fmaf(-lane_value(eb[k], i), r[i], r[k]);
+      for (int k = i + 1; k < 16; ++k) r[k] = fmaf(lane_value(eb[k], i), r[i], r[k]);
     }
-    const float beta = sBeta[o + c];
     if (g == 0) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -270,32 +264,37 @@ __global__ __launch_bounds__(256, 2) void delta_prepare_kernel(DeltaArgs a, Delt
 #pragma unroll
     for (int k = 0; k < i; ++k) {
       if (k < wave) continue;
-      float4 m = *reinterpret_cast<const float4*>(&Eb[16 * i + c][16 * k + 4 * g]);
-      m = make_float4(-m.x, -m.y, -m.z, -m.w);
+      const float4 e = *reinterpret_cast<const float4*>(&E[16 * i + c][16 * k + 4 * g]);
+      const float4 be = *reinterpret_cast<const float4*>(sBeta + 16 * k + 4 * g);
+      const float4 m = make_float4(-times(e.x, be.x), -times(e.y, be.y), -times(e.z, be.z), -times(e.w, be.w));
       acc = mma4(m, col[k], acc);
     }
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
     col[i] = mma4(*reinterpret_cast<const float4*>(&Md[i][c][4 * g]), acc, zero);
+  }
+  // what lies between pieces may hold another sequence's NaN by now
+  if constexpr (VL) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = 16 * i + 4 * g + r;
-      const float v = same(t, 16 * wave + c) ? col[i][r] : 0.f;
-      R[t][16 * wave + c] = v;
-      if constexpr (BACK) pq[i][r] = v;
-    }
+    for (int i = 1; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) col[i][r] = same(16 * i + 4 * g + r, 16 * wave + c) ? col[i][r] : 0.f;
   }
   if constexpr (BACK) {
     char* out = a.ws + ws.up_r + bhw * kTriBytes;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i <= wave) pq[i] = col[i];
-#pragma unroll
     for (int s = 0; s < 2; ++s) {
       if (wave >= 2 * s + 2) continue;
       float v[8];
-      slots(pq[2 * s], pq[2 * s + 1], v);
+      slots(col[2 * s], col[2 * s + 1], v);
       M::store(out + up_frag(wave, s) * 2048, lane, M::two(v));
     }
+  }
+  __syncthreads();  // E is done with
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    if (i <= wave) continue;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) R[16 * i + 4 * g + r][16 * wave + c] = col[i][r];
   }
   __syncthreads();
   char* low_r = a.ws + ws.low_r + bhw * kTriBytes;
