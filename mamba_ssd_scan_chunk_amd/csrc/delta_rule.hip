@@ -550,7 +550,7 @@ struct ChainLds {
 };
 
 template <int NP, int C, bool VL, bool SAVE>
-__global__ __launch_bounds__(128 * C, 2) void delta_chain_bf16_kernel(DeltaArgs a, DeltaWs ws) {
+__global__ __launch_bounds__(128 * C, C) void delta_chain_bf16_kernel(DeltaArgs a, DeltaWs ws) {
   typedef DeltaB M;
   typedef DeltaB::One One;
   typedef DeltaB::Two Two;

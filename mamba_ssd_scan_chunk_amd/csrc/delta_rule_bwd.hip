@@ -205,6 +205,291 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, DeltaWs
   }
 }
 
+// ---------------------------------------------------------------- the same of bf16 inputs
+// C column waves and C helpers, as in the forward chain.  What the next piece
+// adds whatever D is, P^T dy to its values and q^T diag(e^G) dy to D, the helpers
+// work out a step ahead and leave in LDS as accumulators.
+template <int NP, int C>
+struct ReverseLds {
+  static constexpr int kPitch = NP + 8;
+  static constexpr int kRows = kC * kPitch * 2;
+  static constexpr int kX = (NP / 16 + 4) * 1024;
+  static constexpr int k = 0, r = k + kRows, g = r + kTriBytes, half = g + 5 * kC * 4;
+  static constexpr int q = 2 * half, x = q + 2 * kRows, total = x + 2 * C * kX;
+};
+
+template <int NP, int C, bool VL>
+__global__ __launch_bounds__(128 * C, C) void delta_reverse_bf16_kernel(DeltaArgs a, DeltaWs ws) {
+  typedef DeltaB M;
+  typedef DeltaB::One One;
+  typedef DeltaB::Two Two;
+  typedef ReverseLds<NP, C> Lay;
+  constexpr int NT = NP / 16, KS = NP / 32, LP = Lay::kPitch, NH = 64 * C;
+  extern __shared__ __align__(16) char lds[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const uint32_t bid = near_block(blockIdx.x, gridDim.x);
+  const uint32_t slices = (uint32_t)(a.P / 16) / C;
+  const int64_t bh = bid / slices, h = bh % a.H, b = bh / a.H, grp = h / (a.H / a.G);
+  const uint32_t p = ((bid % slices) * C + wave % C) * 16 + c;
+  const int N = (int)a.N;
+  const uint32_t P = (uint32_t)a.P;
+  const int64_t row = b * a.L;
+  Pieces pc;
+  pc.last(VL ? reinterpret_cast<const Cuts*>(a.ws + ws.cuts) + b * ws.nw : nullptr, ws.nw, a.L);
+
+  if (wave >= C) {
+    // ---- helper
+    const int ht = tid - NH;
+    RowTile<NP, NH> kt, qt;
+    TriTile<NH> rt;
+    GateTile<NH> gt;
+    Column dy;
+    f32x4_t qin[4];
+    const uint32_t krow = (uint32_t)a.rows.k, qrow = (uint32_t)a.rows.q, yrow = (uint32_t)(a.H * a.P);
+    const uint16_t* kb = static_cast<const uint16_t*>(a.k) + row * a.rows.k + grp * N;
+    const uint16_t* qb = static_cast<const uint16_t*>(a.q) + row * a.rows.q + grp * N;
+    auto gates = [&](const Pieces& s) {
+      return reinterpret_cast<const DeltaGates*>(a.ws + ws.gates) + bh * ws.nw + s.win;
+    };
+    auto ask = [&](const Pieces& s) {
+      kt.load(kb + s.win * kC * a.rows.k, krow, N, s.n, ht);
+      rt.load(a.ws + ws.up_r + (bh * ws.nw + s.win) * kTriBytes, ht);
+      gt.load(gates(s), ht);
+    };
+    auto put = [&](const Pieces& s, int half) {
+      char* o = lds + half * Lay::half;
+      kt.template store<VL>(reinterpret_cast<uint16_t*>(o + Lay::k), LP, s.begin, s.end, ht);
+      rt.store(o + Lay::r, ht);
+      gt.template store<VL>(reinterpret_cast<float*>(o + Lay::g), s.begin, s.end, ht);
+    };
+    auto ask_q = [&](const Pieces& s) { qt.load(qb + s.win * kC * a.rows.q, qrow, N, s.n, ht); };
+    auto put_q = [&](const Pieces& s, int half) {
+      qt.template store<VL>(reinterpret_cast<uint16_t*>(lds + Lay::q + half * Lay::kRows), LP, s.begin, s.end, ht);
+    };
+    auto ask_dy = [&](const Pieces& s) {
+      dy.load(static_cast<const uint16_t*>(a.dy) + ((row + s.win * kC) * a.H + h) * a.P, yrow, 4 * g * yrow + p, s.n);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qin[i] = *reinterpret_cast<const f32x4_t*>(gates(s)->qin + 16 * i + 4 * g);
+    };
+    // P^T dy and q^T diag(e^G) dy of piece s, whose q is in LDS
+    auto work = [&](const Pieces& s, int half) {
+      const char* fp = a.ws + ws.up_p + (bh * ws.nw + s.win) * kTriBytes;
+      Two pf[kTriFrags];
+#pragma unroll
+      for (int f = 0; f < kTriFrags; ++f) pf[f] = M::load(fp + f * 2048, lane);
+      const uint16_t* ql = reinterpret_cast<const uint16_t*>(lds + Lay::q + half * Lay::kRows);
+      char* x = lds + Lay::x + (half * C + wave % C) * Lay::kX;
+      One yb[2];
+      f32x4_t Y[NT], py[4];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) Y[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) py[i] = Y[0];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        One qT[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) qT[j] = M::transposed(ql + 32 * t * LP + 16 * j, LP, lane);
+        float v[8], w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int i = 2 * t + e / 4, r = e % 4, tok = 16 * i + 4 * g + r;
+          const bool on = !VL || (tok >= s.begin && tok < s.end);
+          v[e] = on ? dy.get(i, r) : 0.f;
+          w[e] = on ? qin[i][r] * v[e] : 0.f;
+        }
+        yb[t] = M::one(v);
+        const Two wb = M::two(w);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) Y[j] = M::mma(qT[j], wb.lo, Y[j]);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) Y[j] = M::mma(qT[j], wb.hi, Y[j]);
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int i = 0; i < 2 * t + 2; ++i) py[i] = M::mma(pf[up_frag(i, t)].lo, yb[t], py[i]);
+#pragma unroll
+        for (int i = 0; i < 2 * t + 2; ++i) py[i] = M::mma(pf[up_frag(i, t)].hi, yb[t], py[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4_t*>(x + i * 1024 + 16 * lane) = py[i];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) *reinterpret_cast<f32x4_t*>(x + (4 + j) * 1024 + 16 * lane) = Y[j];
+    };
+    // before the first piece: its operands, q of it and of the next, its products
+    Pieces n1 = pc;
+    n1.step_back();
+    ask(pc);
+    ask_q(pc);
+    ask_dy(pc);
+    put(pc, 0);
+    put_q(pc, 0);
+    if (n1.valid_back()) ask_q(n1);
+    __syncthreads();
+    work(pc, 0);
+    if (n1.valid_back()) {
+      put_q(n1, 1);
+      ask_dy(n1);
+    }
+    __syncthreads();
+    for (int j = 0;; ++j) {
+      // pc: piece j, which the column waves take now; n1: the next
+      if (!n1.valid_back()) {
+        __syncthreads();
+        break;
+      }
+      Pieces n2 = n1;
+      n2.step_back();
+      ask(n1);
+      if (n2.valid_back()) ask_q(n2);
+      work(n1, (j + 1) & 1);
+      put(n1, (j + 1) & 1);
+      if (n2.valid_back()) {
+        put_q(n2, j & 1);
+        ask_dy(n2);
+      }
+      n1 = n2;
+      __syncthreads();
+    }
+    return;
+  }
+
+  // ---- column wave
+  f32x4_t D[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int nn = 16 * j + 4 * g + r;
+      D[j][r] = a.dfinal && nn < N ? a.dfinal[(bh * N + nn) * a.P + p] : 0.f;
+    }
+  const uint32_t vrow = (uint32_t)a.grows.v;
+  uint16_t* dvb = static_cast<uint16_t*>(a.dv) + row * a.grows.v + h * a.P;
+  __syncthreads();
+  __syncthreads();
+  for (int step = 0; pc.valid_back(); ++step) {
+    const int begin = pc.begin, end = pc.end, n = pc.n;
+    const int64_t win = pc.win, bhw = bh * ws.nw + win;
+    const char* in = lds + (step & 1) * Lay::half;
+    const uint16_t* kt = reinterpret_cast<const uint16_t*>(in + Lay::k);
+    const float* gt = reinterpret_cast<const float*>(in + Lay::g);
+    const float *sBeta = gt, *sKin = gt + kC, *sKout = gt + 3 * kC, *sIn = gt + 4 * kC;
+    const char* x = lds + Lay::x + ((step & 1) * C + wave) * Lay::kX;
+    One kf[KS][4], kT[2][NT];
+    Two rf[kTriFrags];
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint16_t* kp = kt + (16 * i + c) * LP + 32 * s + 4 * g;
+        kf[s][i] = lds_4x2<M>(kp, kp + 16);
+      }
+    __builtin_amdgcn_sched_barrier(0);
+    if (!VL || end == n)
+      put_state<NT>(reinterpret_cast<float*>(a.ws + ws.D) + bhw * N * a.P, N, P, 4 * g * P + p, D);
+    f32x4_t du[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) du[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      float v[8];
+      slots(D[2 * s], D[2 * s + 1], v);
+      const Two db = M::two(v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) du[i] = M::mma(kf[s][i], db.lo, du[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) du[i] = M::mma(kf[s][i], db.hi, du[i]);
+      if (s == 0) {
+#pragma unroll
+        for (int f = 0; f < kTriFrags; ++f) rf[f] = M::load(in + Lay::r + f * 2048, lane);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8 * KS; ++e) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x2, 3, 0);
+    }
+    float ki[4][4], be[4][4], ko[4][4];
+    f32x4_t py[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      load_vec<IoF32, 4>(sKin + 16 * i + 4 * g, ki[i]);
+      load_vec<IoF32, 4>(sBeta + 16 * i + 4 * g, be[i]);
+      load_vec<IoF32, 4>(sKout + 16 * i + 4 * g, ko[i]);
+      py[i] = *reinterpret_cast<const f32x4_t*>(x + i * 1024 + 16 * lane);
+    }
+    const float whole = sIn[end - 1];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) kT[s][j] = M::transposed(kt + 32 * s * LP + 16 * j, LP, lane);
+    __builtin_amdgcn_sched_barrier(0);
+    // du = P^T dy + e^{G_end - G} k D, then R^T of what it is here
+    Two xb[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = 2 * s + e / 4, r = e % 4, t = 16 * i + 4 * g + r;
+        du[i][r] = fmaf(ko[i][r], du[i][r], py[i][r]);
+        v[e] = !VL || (t >= begin && t < end) ? be[i][r] * du[i][r] : 0.f;
+      }
+      xb[s] = M::two(v);
+    }
+    pc.step_back();
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int i = 0; i < 2 * s + 2; ++i) du[i] = M::mma(rf[up_frag(i, s)].hi, xb[s].lo, du[i]);
+#pragma unroll
+      for (int i = 0; i < 2 * s + 2; ++i) du[i] = M::mma(rf[up_frag(i, s)].lo, xb[s].hi, du[i]);
+#pragma unroll
+      for (int i = 0; i < 2 * s + 2; ++i) du[i] = M::mma(rf[up_frag(i, s)].hi, xb[s].hi, du[i]);
+    }
+    f32x4_t Y[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) Y[j] = *reinterpret_cast<const f32x4_t*>(x + (4 + j) * 1024 + 16 * lane);
+    Column::put<VL>(reinterpret_cast<float*>(a.ws + ws.du) + bhw * kC * a.P, P, 4 * g * P + p, kC, du, begin, end, g);
+    f32x4_t dw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 16 * i + 4 * g + r;
+        dw[i][r] = !VL || (t >= begin && t < end) ? be[i][r] * du[i][r] : 0.f;
+      }
+    Column::put<VL>(dvb + win * kC * a.grows.v, vrow, 4 * g * vrow + p, n, dw, begin, end, g);
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) D[j][r] = fmaf(whole, D[j][r], Y[j][r]);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = -ki[2 * s + e / 4][e % 4] * dw[2 * s + e / 4][e % 4];
+      const Two wb = M::two(v);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) D[j] = M::mma(kT[s][j], wb.lo, D[j]);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) D[j] = M::mma(kT[s][j], wb.hi, D[j]);
+    }
+    if constexpr (VL) {
+      // nothing goes back past a sequence's start
+      const Cuts* list = reinterpret_cast<const Cuts*>(a.ws + ws.cuts) + b * ws.nw;
+      if (uniform64(list[win].fresh) >> begin & 1) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) D[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
+    }
+    __syncthreads();
+  }
+  if (a.dinit) put_state<NT>(a.dinit + bh * N * a.P, N, P, 4 * g * P + p, D);
+}
+
 // ---------------------------------------------------------------- all windows at once
 // Left operands of 64 tokens by 64 value columns in LDS.
 template <class M> struct GradTile;
@@ -674,6 +959,22 @@ static hipError_t reverse(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) 
   hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * a.H * (a.P / 16 / w))), dim3(64 * w), lds, s, a, ws);
   return hipGetLastError();
 }
+template <int NP, int C, bool VL>
+static hipError_t reverse_bf16(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) {
+  auto kern = delta_reverse_bf16_kernel<NP, C, VL>;
+  const size_t lds = ReverseLds<NP, C>::total;
+  hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * a.H * (a.P / 16 / C))), dim3(128 * C), lds, s, a, ws);
+  return hipGetLastError();
+}
+template <class M, int NP, bool VL>
+static hipError_t reverse_at(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) {
+  if constexpr (sizeof(typename M::IO::type) == 2 && NP <= 128)
+    return a.P % 32 == 0 ? reverse_bf16<NP, 2, VL>(a, ws, s) : reverse_bf16<NP, 1, VL>(a, ws, s);
+  else
+    return reverse<M, NP, VL>(a, ws, s);
+}
 template <class M, int NTW, bool VL>
 static hipError_t grad(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) {
   auto kern = delta_grad_kernel<M, NTW, VL>;
@@ -685,10 +986,10 @@ static hipError_t grad(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) {
 }
 template <class M, bool VL>
 static hipError_t back_of(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) {
-  hipError_t e = a.N <= 32    ? reverse<M, 32, VL>(a, ws, s)
-                 : a.N <= 64  ? reverse<M, 64, VL>(a, ws, s)
-                 : a.N <= 128 ? reverse<M, 128, VL>(a, ws, s)
-                              : reverse<M, 256, VL>(a, ws, s);
+  hipError_t e = a.N <= 32    ? reverse_at<M, 32, VL>(a, ws, s)
+                 : a.N <= 64  ? reverse_at<M, 64, VL>(a, ws, s)
+                 : a.N <= 128 ? reverse_at<M, 128, VL>(a, ws, s)
+                              : reverse_at<M, 256, VL>(a, ws, s);
   if (e != hipSuccess) return e;
   e = a.N <= 64 ? grad<M, 1, VL>(a, ws, s) : a.N <= 128 ? grad<M, 2, VL>(a, ws, s) : grad<M, 4, VL>(a, ws, s);
   if (e != hipSuccess) return e;
