@@ -534,10 +534,10 @@ template <> struct GradTile<DeltaF> {
     return DeltaF::global8(p + 2 * kPlane + t * kPitch + col);
   }
 };
-template <class M>
+template <class M, int WV>
 constexpr size_t grad_lds() {
   const size_t tile = GradTile<M>::bytes(), tri = (size_t)3 * kC * kTP * 4;
-  return (tile > tri ? tile : tri) + (size_t)(7 + 4 + 4 + 4 + 1 + 1) * kC * 4 + kC * 8 + 16 * 4;
+  return (tile > tri ? tile : tri) + kC * 8 + (size_t)(7 + 3 * WV + 2 + 1) * kC * 4 + 16 * 4;
 }
 
 // Sum over the 16 lanes of a group, in every lane.
@@ -547,13 +547,17 @@ __device__ __forceinline__ float sum16(float v) {
   return v;
 }
 
-// Four waves; a wave takes NTW 16-row tiles of the state (dq and dk columns)
-// for all 64 tokens, and rows 16 wave .. of the token-by-token matrices.
-template <class M, int NTW, bool VL>
-__global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws) {
+// WV waves; a wave takes NTW 16-row tiles of the state (dq and dk columns) for
+// all 64 tokens, and 16 rows of the token-by-token matrices: of both where four
+// waves share them, of dQK (the first four) or dKK (the others) where eight do,
+// which leaves each the registers for two waves a SIMD.
+template <class M, int WV, int NTW, bool VL>
+__global__ __launch_bounds__(64 * WV, 2) void delta_grad_kernel(DeltaArgs a, DeltaWs ws) {
   typedef typename M::IO::type T;
   typedef typename M::One One;
   typedef typename M::Two Two;
+  constexpr uint32_t es = sizeof(T);
+  constexpr int kParts = WV == 4 ? 2 : 1, kCols = 64 / WV;  // matrices a wave; columns a thread stages
   extern __shared__ __align__(16) char lds[];
   constexpr size_t kBig = GradTile<M>::bytes() > (size_t)3 * kC * kTP * 4 ? GradTile<M>::bytes() : (size_t)3 * kC * kTP * 4;
   GradTile<M> tile(lds);
@@ -564,31 +568,40 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
   float* gt = reinterpret_cast<float*>(sG + kC);
   const float *sBeta = gt, *sKout = gt + 3 * kC, *sIn = gt + 4 * kC, *sRk = gt + 5 * kC, *sRq = gt + 6 * kC;
   float(*rowS)[kC] = reinterpret_cast<float(*)[kC]>(gt + 7 * kC);  // by wave
-  float(*colD)[kC] = rowS + 4;
-  float(*colZ)[kC] = colD + 4;
-  float* rowZ = reinterpret_cast<float*>(colZ + 4);
-  float* sDb = rowZ + kC;
+  float(*colD)[kC] = rowS + WV;
+  float(*colZ)[kC] = colD + WV;
+  float(*rowZ)[kC] = colZ + WV;  // by matrix
+  float* sDb = reinterpret_cast<float*>(rowZ + 2);
   float* sSD = sDb + kC;  // by wave
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int c = lane & 15, g = lane >> 4;
-  const int64_t bid = near_block(blockIdx.x, gridDim.x);
-  const int64_t h = bid % a.H, win = bid / a.H % ws.nw, b = bid / a.H / ws.nw;
+  const int c = lane & 15, g = lane >> 4, rt = wave & 3;  // rt: the row tile of the matrices
+  auto which = [&](int part) { return WV == 4 ? part : wave >> 2; };  // 0: dQK, 1: dKK
+  const uint32_t bid = near_block(blockIdx.x, gridDim.x), H = (uint32_t)a.H, nw = (uint32_t)ws.nw;
+  const int64_t h = bid % H, win = bid / H % nw, b = bid / H / nw;
   const int64_t row = b * a.L, t0 = win * kC, bhw = (b * a.H + h) * ws.nw + win;
-  const int64_t grp = h / (a.H / a.G);
+  const int64_t grp = (uint32_t)h / (H / (uint32_t)a.G);
   const int n = (int)(a.L - t0 < kC ? a.L - t0 : kC), N = (int)a.N, P = (int)a.P;
   Cuts cuts = {0, 0};
-  if constexpr (VL) cuts = window_cuts(a.seq_idx, nullptr, row, t0, a.L, lane);
+  if constexpr (VL) cuts = Pieces::uniform(reinterpret_cast<const Cuts*>(a.ws + ws.cuts)[b * ws.nw + win]);
   const DeltaGates* gates = reinterpret_cast<const DeltaGates*>(a.ws + ws.gates) + bhw;
-  for (int i = tid; i < 7 * kC; i += 256) gt[i] = reinterpret_cast<const float*>(gates)[i];
+  for (int i = tid; i < 7 * kC / 4; i += 64 * WV)
+    reinterpret_cast<f32x4_t*>(gt)[i] = reinterpret_cast<const f32x4_t*>(gates)[i];
   if (tid < kC) sG[tid] = gates->G[tid];
-  const float* wsw = reinterpret_cast<const float*>(a.ws + ws.w) + bhw * kC * P;
-  const float* wsu = reinterpret_cast<const float*>(a.ws + ws.du) + bhw * kC * P;
+  const __amdgpu_buffer_rsrc_t wr = rows_of(reinterpret_cast<const float*>(a.ws + ws.w) + bhw * kC * P, kC * P * 4);
+  const __amdgpu_buffer_rsrc_t ur = rows_of(reinterpret_cast<const float*>(a.ws + ws.du) + bhw * kC * P, kC * P * 4);
   const float* wsS = reinterpret_cast<const float*>(a.ws + ws.S) + bhw * N * P;
   const float* wsD = reinterpret_cast<const float*>(a.ws + ws.D) + bhw * N * P;
-  const T* kbase = static_cast<const T*>(a.k) + (row + t0) * a.rows.k + grp * N;
-  const T* qbase = static_cast<const T*>(a.q) + (row + t0) * a.rows.q + grp * N;
-  const T* ybase = static_cast<const T*>(a.dy) + ((row + t0) * a.H + h) * P;
+  const uint32_t krow = (uint32_t)a.rows.k * es, qrow = (uint32_t)a.rows.q * es, yrow = (uint32_t)(a.H * a.P) * es;
+  const __amdgpu_buffer_rsrc_t kr =
+      rows_of(static_cast<const T*>(a.k) + (row + t0) * a.rows.k + grp * N, (uint32_t)n * krow);
+  const __amdgpu_buffer_rsrc_t qr =
+      rows_of(static_cast<const T*>(a.q) + (row + t0) * a.rows.q + grp * N, (uint32_t)n * qrow);
+  const __amdgpu_buffer_rsrc_t yr =
+      rows_of(static_cast<const T*>(a.dy) + ((row + t0) * a.H + h) * P, (uint32_t)n * yrow);
+  auto f4 = [](const __amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t s) {
+    return __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, s, 0));
+  };
   float sumA = 0.f, sumB = 0.f;  // of dA and ddt_bias, in wave 0
   const f32x4_t zero4 = {0.f, 0.f, 0.f, 0.f};
 
@@ -597,37 +610,73 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
     const int end = VL ? piece_end(cuts.piece, begin, n) : n;
     // only a row's first piece begins with a state, only its last one hands one on
     const bool first = begin == 0, last = end == n;
-    f32x4_t qS[NTW][4], wS[NTW][4], uD[NTW][4], dP[4], dE[4];
+    const __amdgpu_buffer_rsrc_t Sr = rows_of(wsS, first ? N * P * 4 : 0), Dr = rows_of(wsD, last ? N * P * 4 : 0);
+    f32x4_t qS[NTW][4], wS[NTW][4], uD[NTW][4], dX[kParts][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      dP[i] = dE[i] = zero4;
+#pragma unroll
+      for (int q = 0; q < kParts; ++q) dX[q][i] = zero4;
 #pragma unroll
       for (int m = 0; m < NTW; ++m) qS[m][i] = wS[m][i] = uD[m][i] = zero4;
     }
     float sd = 0.f, db = 0.f;
     for (int p0 = 0; p0 < P; p0 += 64) {
+      // all of a slice's operands are asked for together
+      f32x4_t sv[2][NTW][2], dv[2][NTW][2], w[kCols / 4], du[kCols / 4], dy[kCols / 4];
+      {
+        const int t = tid / WV, col = p0 + tid % WV * kCols;
+        const uint32_t off = col < P ? (t * P + col) * 4 : kNowhere, yoff = col < P ? t * yrow + col * es : kNowhere;
+#pragma unroll
+        for (int e = 0; e < kCols / 4; ++e) {
+          w[e] = f4(wr, off, 16 * e);
+          du[e] = f4(ur, off, 16 * e);
+          if (es == 4 || e < kCols / 8) dy[e] = f4(yr, yoff, 16 * e);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int col = p0 + 32 * s + 8 * g;
+        const uint32_t off = col < P ? ((16 * wave + c) * P + col) * 4 : kNowhere;
+#pragma unroll
+        for (int m = 0; m < NTW; ++m)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            sv[s][m][e] = f4(Sr, off, 16 * WV * m * P * 4 + 16 * e);
+            dv[s][m][e] = f4(Dr, off, 16 * WV * m * P * 4 + 16 * e);
+          }
+      }
       __syncthreads();
       {
-        const int t = tid >> 2, col = (tid & 3) * 16;
-        const bool on = t >= begin && t < end && p0 + col < P;
-        const float beta = on ? sBeta[t] : 0.f;
+        const int t = tid / WV, col = tid % WV * kCols;
+        const bool on = !VL || (t >= begin && t < end);
+        const float beta = sBeta[t];
 #pragma unroll
-        for (int e = 0; e < 16; e += 8) {
-          float w[8], du[8], dy[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) w[k] = du[k] = dy[k] = 0.f;
-          if (on) {
-            load_vec<IoF32, 8>(wsw + t * P + p0 + col + e, w);
-            load_vec<IoF32, 8>(wsu + t * P + p0 + col + e, du);
-            load_vec<typename M::IO, 8>(ybase + t * a.H * P + p0 + col + e, dy);
-          }
+        for (int e = 0; e < kCols / 8; ++e) {
+          float wv[8], uv[8], yv[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            db = fmaf(w[k], du[k], db);
-            w[k] *= beta;
-            du[k] *= beta;
+            wv[k] = w[2 * e + k / 4][k % 4];
+            uv[k] = du[2 * e + k / 4][k % 4];
+            if constexpr (es == 4) {
+              yv[k] = dy[2 * e + k / 4][k % 4];
+            } else {
+              const uint32_t two = __float_as_uint(dy[e][k / 2]);
+              yv[k] = __uint_as_float(k % 2 ? two & 0xffff0000u : two << 16);
+            }
+            if constexpr (VL) {
+              wv[k] = on ? wv[k] : 0.f;
+              uv[k] = on ? uv[k] : 0.f;
+              yv[k] = on ? yv[k] : 0.f;
+            }
+            db = fmaf(wv[k], uv[k], db);
+            wv[k] *= beta;
+            uv[k] *= beta;
+            if constexpr (VL) {  // another piece's b may be NaN
+              wv[k] = on ? wv[k] : 0.f;
+              uv[k] = on ? uv[k] : 0.f;
+            }
           }
-          tile.put8(t, col + e, dy, w, du);
+          tile.put8(t, col + 8 * e, yv, wv, uv);
         }
       }
       __syncthreads();
@@ -635,162 +684,210 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
       for (int s = 0; s < 2; ++s) {
         if (p0 + 32 * s >= P) break;
         const int col = 32 * s + 8 * g;
-        One ya[4];
-        Two ua[4], wa[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ya[i] = tile.dy(16 * i + c, col);
-          ua[i] = tile.u(16 * i + c, col);
-          wa[i] = tile.dw(16 * i + c, col);
-        }
+        Two sf[NTW], df[NTW];
 #pragma unroll
         for (int m = 0; m < NTW; ++m) {
-          const int nn = 16 * (wave + 4 * m) + c;
-          float sv[8], dv[8];
+          float x[8], z[8];
+          slots(sv[s][m][0], sv[s][m][1], x);
+          slots(dv[s][m][0], dv[s][m][1], z);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) sv[k] = dv[k] = 0.f;
-          if (nn < N && p0 + col < P) {
-            if (first) load_vec<IoF32, 8>(wsS + nn * P + p0 + col, sv);
-            if (last) load_vec<IoF32, 8>(wsD + nn * P + p0 + col, dv);
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) sd = fmaf(sv[k], dv[k], sd);
-          const Two sf = M::two(sv), df = M::two(dv);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            qS[m][i] = M::mma(ya[i], sf, qS[m][i]);
-            wS[m][i] = M::mma(wa[i], sf, wS[m][i]);
-            uD[m][i] = M::mma(ua[i], df, uD[m][i]);
-          }
+          for (int k = 0; k < 8; ++k) sd = fmaf(x[k], z[k], sd);
+          sf[m] = M::two(x);
+          df[m] = M::two(z);
         }
-        const One yr = tile.dy(16 * wave + c, col);
-        const Two wr = tile.dw(16 * wave + c, col);
+        const One ym = tile.dy(16 * rt + c, col);
+        const Two wm = tile.dw(16 * rt + c, col);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (j > wave) continue;
-          dP[j] = M::mma(yr, ua[j], dP[j]);
-          dE[j] = M::mma(wr, ua[j], dE[j]);
+        for (int i = 0; i < 4; ++i) {
+          const One ya = tile.dy(16 * i + c, col);
+          const Two ua = tile.u(16 * i + c, col), wa = tile.dw(16 * i + c, col);
+#pragma unroll
+          for (int m = 0; m < NTW; ++m) {
+            qS[m][i] = M::mma(ya, sf[m], qS[m][i]);
+            wS[m][i] = M::mma(wa, sf[m], wS[m][i]);
+            uD[m][i] = M::mma(ua, df[m], uD[m][i]);
+          }
+          if (i > rt) continue;
+#pragma unroll
+          for (int q = 0; q < kParts; ++q) {
+            if (which(q) == 0) dX[q][i] = M::mma(ym, ua, dX[q][i]);
+            else dX[q][i] = M::mma(wm, ua, dX[q][i]);
+          }
         }
       }
     }
-    db += __shfl_xor(db, 1, 64);
-    db += __shfl_xor(db, 2, 64);
-    if ((tid & 3) == 0) sDb[tid >> 2] = db;
+    // q and k of the wave's columns, 16 tokens a lane, for what follows the matrices
+    T kv[NTW][16], qv[NTW][16];
+#pragma unroll
+    for (int m = 0; m < NTW; ++m) {
+      const uint32_t nn = 16 * (wave + WV * m) + c;
+      const uint32_t ko = (int)nn < N ? 4 * g * krow + nn * es : kNowhere, qo = (int)nn < N ? 4 * g * qrow + nn * es : kNowhere;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const uint32_t t = Column::row(e);
+        if constexpr (es == 2) {
+          kv[m][e] = __builtin_amdgcn_raw_buffer_load_b16(kr, ko, t * krow, 0);
+          qv[m][e] = __builtin_amdgcn_raw_buffer_load_b16(qr, qo, t * qrow, 0);
+        } else {
+          kv[m][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(kr, ko, t * krow, 0));
+          qv[m][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(qr, qo, t * qrow, 0));
+        }
+      }
+    }
+    // Gram products of rows 16 rt ..
+    f32x4_t gm[kParts][4];
+#pragma unroll
+    for (int q = 0; q < kParts; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) gm[q][j] = zero4;
+    for (int s0 = 0; 32 * s0 < N; s0 += 2) {
+      One kf[4][2], xa[kParts][2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint32_t col = 32 * (s0 + s) + 8 * g;
+        const uint32_t ko = (int)col < N ? c * krow + col * es : kNowhere, qo = (int)col < N ? c * qrow + col * es : kNowhere;
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+          xa[q][s] = which(q) == 0 ? M::rows8(qr, qo, 16 * rt * qrow) : M::rows8(kr, ko, 16 * rt * krow);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j <= rt) kf[j][s] = M::rows8(kr, ko, 16 * j * krow);
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j > rt) continue;
+#pragma unroll
+          for (int q = 0; q < kParts; ++q) gm[q][j] = M::mma(xa[q][s], kf[j][s], gm[q][j]);
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < WV; o <<= 1) db += __shfl_xor(db, o, 64);
+    if (tid % WV == 0) sDb[tid / WV] = db;
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) sd += __shfl_xor(sd, o, 64);
     if (lane == 0) sSD[wave] = sd;
-
-    // Gram products of rows 16 wave ..
-    f32x4_t kk[4], qk[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) kk[j] = qk[j] = zero4;
-    for (int s = 0; s * 32 < N; ++s) {
-      const int col = 32 * s + 8 * g;
-      auto load = [&](const T* base, int64_t stride, int i) {
-        const int t = 16 * i + c;
-        return t >= begin && t < end && col < N ? M::global8(base + t * stride + col) : M::zero();
-      };
-      const One ka = load(kbase, a.rows.k, wave), qa = load(qbase, a.rows.q, wave);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j > wave) continue;
-        const One kb = load(kbase, a.rows.k, j);
-        kk[j] = M::mma(ka, kb, kk[j]);
-        qk[j] = M::mma(qa, kb, qk[j]);
-      }
-    }
     __syncthreads();  // the tile's place is the matrices' from here
-    float rz[4] = {0.f, 0.f, 0.f, 0.f};
+    {
+      const int tw = 16 * rt + 4 * g;
+      double Gt[4];
+      float rkt[4], rqt[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int s = 16 * j + c;
-      float cz = 0.f;
+      for (int r = 0; r < 4; ++r) Gt[r] = sG[tw + r];
+      load_vec<IoF32, 4>(sRk + tw, rkt);
+      load_vec<IoF32, 4>(sRq + tw, rqt);
+      float cz[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 16 * wave + 4 * g + r;
-        float m1 = 0.f, m2 = 0.f, lo = 0.f, up = 0.f;
-        if (j <= wave && s >= begin && s <= t && t < end) {
-          const float rel = fast_exp2((float)(sG[t] - sG[s]));
-          const float dqk = rel * dP[j][r];
-          m1 = dqk * sRk[s];
-          m2 = dqk * sRq[t];
-          if (s < t) {
-            const float dkk = -rel * dE[j][r];
-            lo = dkk * sRk[s];
-            up = dkk * sRk[t];
-            const float z = m1 * sRq[t] * qk[j][r] + lo * sRk[t] * kk[j][r];
+      for (int q = 0; q < kParts; ++q) {
+        float rz[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int s = 16 * j + c;
+          const double Gs = sG[s];
+          const float rks = sRk[s];
+          f32x4_t v;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int t = tw + r;
+            const bool on = j <= rt && s >= begin && s <= t && t < end, below = on && s < t;
+            v[r] = fast_exp2((float)(Gt[r] - Gs)) * dX[q][j][r];
+            const float x = v[r] * rks;  // of s's unit key
+            const float z = below ? x * (which(q) == 0 ? rqt[r] : -rkt[r]) * gm[q][j][r] : 0.f;
             rz[r] += z;
-            cz += z;
+            cz[j] += z;
+            if (which(q) == 0) {
+              M1[t][s] = on ? x : 0.f;
+              M2[t][s] = on ? v[r] * rqt[r] : 0.f;
+            } else {
+              if (j < rt || (j == rt && s <= t)) M3[t][s] = below ? -x : 0.f;
+              v[r] = below ? -v[r] * rkt[r] : 0.f;
+            }
+          }
+          if (which(q) == 1) {
+            if (j < rt) {
+              *reinterpret_cast<f32x4_t*>(&M3[s][tw]) = v;
+            } else if (j == rt) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (s < tw + r) M3[s][tw + r] = v[r];
+            }
           }
         }
-        M1[t][s] = m1;
-        M2[t][s] = m2;
-        if (j <= wave) {
-          if (s < t || j < wave) M3[t][s] = lo;
-          if (s < t) M3[s][t] = up;
-          if (s == t) M3[t][s] = 0.f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float z = sum16(rz[r]);
+          if (c == 0) rowZ[which(q)][tw + r] = z;
         }
       }
-      cz += __shfl_xor(cz, 16, 64);
-      cz += __shfl_xor(cz, 32, 64);
-      if (g == 0) colZ[wave][s] = cz;
-    }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float z = sum16(rz[r]);
-      if (c == 0) rowZ[16 * wave + 4 * g + r] = z;
+      for (int j = 0; j < 4; ++j) {
+        cz[j] += __shfl_xor(cz[j], 16, 64);
+        cz[j] += __shfl_xor(cz[j], 32, 64);
+        if (g == 0) colZ[wave][16 * j + c] = cz[j];
+      }
     }
     __syncthreads();
     // dq and dk of the wave's columns
-    float rs[4][4], cd[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) rs[i][r] = cd[i][r] = 0.f;
     One kb[NTW][2], qb[NTW][2];
 #pragma unroll
-    for (int m = 0; m < NTW; ++m) {
-      const int nn = 16 * (wave + 4 * m) + c;
+    for (int i = 0; i < 4; ++i) {
+      const int t = 16 * i + 4 * g;
+      float in[4], ko[4], rk[4], rq[4], rs[4], cd[4];
+      load_vec<IoF32, 4>(sIn + t, in);
+      load_vec<IoF32, 4>(sKout + t, ko);
+      load_vec<IoF32, 4>(sRk + t, rk);
+      load_vec<IoF32, 4>(sRq + t, rq);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        float kv[8], qv[8];
+      for (int r = 0; r < 4; ++r) {
+        rs[r] = cd[r] = 0.f;
+        const bool on = !VL || (t + r >= begin && t + r < end);
+        const float rest = ko[r] / rk[r];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int t = 32 * s + 16 * (e / 4) + 4 * g + e % 4;
-          const bool on = nn < N && t >= begin && t < end;
-          kv[e] = on ? M::IO::get(kbase[t * a.rows.k + nn]) : 0.f;
-          qv[e] = on ? M::IO::get(qbase[t * a.rows.q + nn]) : 0.f;
-          const int i = 2 * s + e / 4, r = e % 4;
-          const float in = on ? sIn[t] : 0.f, kout = on ? sKout[t] : 0.f;
-          const float x = in * qS[m][i][r], y = in * wS[m][i][r], z = uD[m][i][r];
-          rs[i][r] += (sRq[t] * qv[e]) * x - (sRk[t] * kv[e]) * y;
-          cd[i][r] = fmaf(kout * kv[e], z, cd[i][r]);
+        for (int m = 0; m < NTW; ++m) {
+          if (VL && !on) kv[m][4 * i + r] = qv[m][4 * i + r] = 0;
+          const float k = M::IO::get(kv[m][4 * i + r]), q = M::IO::get(qv[m][4 * i + r]);
+          const float x = in[r] * qS[m][i][r], y = in[r] * wS[m][i][r], z = uD[m][i][r];
+          rs[r] += (rq[r] * q) * x - (rk[r] * k) * y;
+          cd[r] = fmaf(ko[r] * k, z, cd[r]);
           qS[m][i][r] = x;
-          wS[m][i][r] = (kout / sRk[t]) * z - y;
+          wS[m][i][r] = rest * z - y;
         }
-        kb[m][s] = M::one(kv);
-        qb[m][s] = M::one(qv);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float x = sum16(rs[r]), y = sum16(cd[r]);
+        if (c == 0) {
+          rowS[wave][t + r] = x;
+          colD[wave][t + r] = y;
+        }
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int m = 0; m < NTW; ++m)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float x = sum16(rs[i][r]), y = sum16(cd[i][r]);
-        if (c == 0) {
-          rowS[wave][16 * i + 4 * g + r] = x;
-          colD[wave][16 * i + 4 * g + r] = y;
+      for (int s = 0; s < 2; ++s) {
+        float x[8], y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[e] = M::IO::get(kv[m][8 * s + e]);
+          y[e] = M::IO::get(qv[m][8 * s + e]);
         }
+        kb[m][s] = M::one(x);
+        qb[m][s] = M::one(y);
       }
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float v[8];
+        auto row8 = [&](float(*q)[kTP]) {
+          load_vec<IoF32, 4>(&q[16 * i + c][32 * s + 4 * g], v);
+          load_vec<IoF32, 4>(&q[16 * i + c][32 * s + 16 + 4 * g], v + 4);
+          return M::two(v);
+        };
         if (2 * s <= i) {  // rows 16 i .. of M1, columns 32 s ..
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = M1[16 * i + c][32 * s + 16 * (e / 4) + 4 * g + e % 4];
-          const Two f = M::two(v);
+          const Two f = row8(M1);
 #pragma unroll
           for (int m = 0; m < NTW; ++m) qS[m][i] = M::mma(f, kb[m][s], qS[m][i]);
         }
@@ -801,33 +898,35 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
 #pragma unroll
           for (int m = 0; m < NTW; ++m) wS[m][i] = M::mma(f, qb[m][s], wS[m][i]);
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = M3[16 * i + c][32 * s + 16 * (e / 4) + 4 * g + e % 4];
-        const Two f = M::two(v);
+        const Two f = row8(M3);
 #pragma unroll
         for (int m = 0; m < NTW; ++m) wS[m][i] = M::mma(f, kb[m][s], wS[m][i]);
       }
-    float* dq = reinterpret_cast<float*>(a.ws + ws.dq) + bhw * kC * N;
-    float* dk = reinterpret_cast<float*>(a.ws + ws.dk) + bhw * kC * N;
+    const __amdgpu_buffer_rsrc_t dqr = rows_of(reinterpret_cast<float*>(a.ws + ws.dq) + bhw * kC * N, kC * N * 4);
+    const __amdgpu_buffer_rsrc_t dkr = rows_of(reinterpret_cast<float*>(a.ws + ws.dk) + bhw * kC * N, kC * N * 4);
 #pragma unroll
     for (int m = 0; m < NTW; ++m) {
-      const int nn = 16 * (wave + 4 * m) + c;
+      const uint32_t nn = 16 * (wave + WV * m) + c;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int t = 16 * i + 4 * g + r;
-          if (nn < N && t >= begin && t < end) {
-            dq[t * N + nn] = qS[m][i][r];
-            dk[t * N + nn] = wS[m][i][r];
-          }
-        }
+      for (int e = 0; e < 16; ++e) {
+        const int t = (int)Column::row(e) + 4 * g;
+        const bool on = (int)nn < N && (!VL || (t >= begin && t < end));
+        const uint32_t off = on ? (4 * g * N + nn) * 4 : kNowhere;
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(qS[m][e / 4][e % 4]), dqr, off, Column::row(e) * N * 4, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(wS[m][e / 4][e % 4]), dkr, off, Column::row(e) * N * 4, 0);
+      }
     }
     __syncthreads();
     if (wave == 0) {
       const bool on = lane >= begin && lane < end;
-      auto waves = [&](float(*q)[kC]) { return ((q[0][lane] + q[1][lane]) + q[2][lane]) + q[3][lane]; };
-      double x = on ? (double)rowZ[lane] - waves(colZ) + waves(rowS) : 0.0, y = on ? (double)waves(colD) : 0.0;
+      auto waves = [&](float(*q)[kC]) {
+        float v = q[0][lane];
+#pragma unroll
+        for (int k = 1; k < WV; ++k) v += q[k][lane];
+        return v;
+      };
+      double x = on ? (double)(rowZ[0][lane] + rowZ[1][lane]) - waves(colZ) + waves(rowS) : 0.0;
+      double y = on ? (double)waves(colD) : 0.0;
       const double mine = y;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
@@ -835,7 +934,10 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
         if (lane + off < 64) x += ox;
         if (lane >= off) y += oy;
       }
-      const float whole = first && last ? sIn[end - 1] * (((sSD[0] + sSD[1]) + sSD[2]) + sSD[3]) : 0.f;
+      float whole = sSD[0];
+#pragma unroll
+      for (int k = 1; k < WV; ++k) whole += sSD[k];
+      whole = first && last ? sIn[end - 1] * whole : 0.f;
       float dg = (float)(x + (y - mine) + (double)whole);
       if (VL && lane == begin && (cuts.fresh >> begin & 1)) dg = 0.f;  // nothing comes in
       float pa = 0.f, pb = 0.f;
@@ -874,48 +976,58 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
 }
 
 // ---------------------------------------------------------------- heads of a group together, unit length
-// A wave a (token, key group); blockIdx.y: q or k.
-template <class IO>
+// W lanes of four columns a (token, key group); blockIdx.y: q or k.  Bound by
+// memory: the heads' fp32 shares, read once.
+template <class IO, int W>
 __global__ __launch_bounds__(256) void delta_finish_kernel(DeltaArgs a, DeltaWs ws) {
   typedef typename IO::type T;
-  const int lane = threadIdx.x & 63;
-  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (i >= a.B * a.L * a.G) return;
-  const int64_t grp = i % a.G, t = i / a.G, b = t / a.L, tl = t % a.L;
+  const int l = threadIdx.x % W;
+  const uint32_t i = blockIdx.x * (256 / W) + threadIdx.x / W, G = (uint32_t)a.G;
+  if (i >= (uint64_t)(a.B * a.L * a.G)) return;
+  const uint32_t grp = i % G, t = i / G, b = t / (uint32_t)a.L, tl = t % (uint32_t)a.L;
   const bool isk = blockIdx.y;
   const int N = (int)a.N, rep = (int)(a.H / a.G);
-  const T* x = static_cast<const T*>(isk ? a.k : a.q) + t * (isk ? a.rows.k : a.rows.q) + grp * N;
-  T* out = static_cast<T*>(isk ? a.dk : a.dq) + t * (isk ? a.grows.k : a.grows.q) + grp * N;
-  const float* d = reinterpret_cast<const float*>(a.ws + (isk ? ws.dk : ws.dq));
-  const float scale = isk ? 1.f : a.scale;
-  constexpr int E = (int)kDeltaMaxDim / 64;
-  float v[E], xv[E], ss = 0.f, dot = 0.f;
+  const bool on = 4 * l < N;
+  const T* x = static_cast<const T*>(isk ? a.k : a.q) + (int64_t)t * (isk ? a.rows.k : a.rows.q) + grp * N + 4 * l;
+  T* out = static_cast<T*>(isk ? a.dk : a.dq) + (int64_t)t * (isk ? a.grows.k : a.grows.q) + grp * N + 4 * l;
+  // heads of a group are nw windows of 64 rows apart
+  const float* d = reinterpret_cast<const float*>(a.ws + (isk ? ws.dk : ws.dq)) +
+                   ((((int64_t)b * a.H + (int64_t)grp * rep) * ws.nw + tl / kC) * kC + tl % kC) * N + 4 * l;
+  const int64_t step = ws.nw * kC * N;
+  float xv[4] = {0.f, 0.f, 0.f, 0.f};
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+  if (on) {
+    load_vec<IO, 4>(x, xv);
+#pragma unroll 4
+    for (int r = 0; r < rep; ++r) v += *reinterpret_cast<const f32x4_t*>(d + r * step);
+  }
+  if (!isk) v *= a.scale;
+  float ss = 0.f, dot = 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int nn = lane + 64 * e;
-    v[e] = xv[e] = 0.f;
-    if (nn < N) {
-      for (int r = 0; r < rep; ++r)
-        v[e] += d[(((b * a.H + grp * rep + r) * ws.nw + tl / kC) * kC + tl % kC) * N + nn];
-      v[e] *= scale;
-      xv[e] = IO::get(x[nn]);
-    }
+  for (int e = 0; e < 4; ++e) {
     ss = fmaf(xv[e], xv[e], ss);
     dot = fmaf(xv[e], v[e], dot);
   }
   float rn = 1.f, back = 0.f;
   if (a.qk_norm) {
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
+    for (int o = 1; o < W; o <<= 1) {
       ss += __shfl_xor(ss, o, 64);
       dot += __shfl_xor(dot, o, 64);
     }
     rn = 1.f / sqrtf(ss + kQkEps);
     back = dot * rn * rn;
   }
+  if (!on) return;
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    if (lane + 64 * e < N) out[lane + 64 * e] = IO::put(rn * (v[e] - xv[e] * back));
+  for (int e = 0; e < 4; ++e) v[e] = rn * (v[e] - xv[e] * back);
+  if ((reinterpret_cast<uintptr_t>(out) & (4 * sizeof(T) - 1)) == 0) {
+    float o[4] = {v[0], v[1], v[2], v[3]};
+    store_vec<IO, 4>(out, o);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[e] = IO::put(v[e]);
+  }
 }
 
 // dA and ddt_bias: a block a head, the windows' sums in a fixed order.
@@ -975,13 +1087,13 @@ static hipError_t reverse_at(const DeltaArgs& a, const DeltaWs& ws, hipStream_t 
   else
     return reverse<M, NP, VL>(a, ws, s);
 }
-template <class M, int NTW, bool VL>
+template <class M, int WV, int NTW, bool VL>
 static hipError_t grad(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) {
-  auto kern = delta_grad_kernel<M, NTW, VL>;
-  const size_t lds = grad_lds<M>();
+  auto kern = delta_grad_kernel<M, WV, NTW, VL>;
+  const size_t lds = grad_lds<M, WV>();
   hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * ws.nw * a.H)), dim3(256), lds, s, a, ws);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * ws.nw * a.H)), dim3(64 * WV), lds, s, a, ws);
   return hipGetLastError();
 }
 template <class M, bool VL>
@@ -991,10 +1103,17 @@ static hipError_t back_of(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) 
                  : a.N <= 128 ? reverse_at<M, 128, VL>(a, ws, s)
                               : reverse_at<M, 256, VL>(a, ws, s);
   if (e != hipSuccess) return e;
-  e = a.N <= 64 ? grad<M, 1, VL>(a, ws, s) : a.N <= 128 ? grad<M, 2, VL>(a, ws, s) : grad<M, 4, VL>(a, ws, s);
+  e = a.N <= 64    ? grad<M, 4, 1, VL>(a, ws, s)
+      : a.N <= 128 ? grad<M, 8, 1, VL>(a, ws, s)
+                   : grad<M, 8, 2, VL>(a, ws, s);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(delta_finish_kernel<typename M::IO>, dim3((unsigned)((a.B * a.L * a.G + 3) / 4), 2), dim3(256), 0,
-                     s, a, ws);
+  const int64_t units = a.B * a.L * a.G;
+  if (a.N <= 64)
+    hipLaunchKernelGGL((delta_finish_kernel<typename M::IO, 16>), dim3((unsigned)((units + 15) / 16), 2), dim3(256), 0, s, a, ws);
+  else if (a.N <= 128)
+    hipLaunchKernelGGL((delta_finish_kernel<typename M::IO, 32>), dim3((unsigned)((units + 7) / 8), 2), dim3(256), 0, s, a, ws);
+  else
+    hipLaunchKernelGGL((delta_finish_kernel<typename M::IO, 64>), dim3((unsigned)((units + 3) / 4), 2), dim3(256), 0, s, a, ws);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(delta_param_kernel, dim3((unsigned)a.H), dim3(256), 0, s, a, ws);
