@@ -198,9 +198,9 @@ __global__ __launch_bounds__(group_block(T)) void group_norm_forward_kernel(Grou
   }
 }
 
-// Lanes of a row side by side: lane group_lane<T> of column block blockIdx.x;
-// rows from blockIdx.y on in steps.  A thread keeps its columns, and dw and
-// dbias of them in registers.
+// Lanes of a row side by side, a block's from blockIdx.x on; rows from
+// blockIdx.y on in steps.  A thread keeps its columns, and dw and dbias of them
+// in registers.
 struct GroupWalk {
   int lanes;      // of a row: G T
   int per_block;  // of them in a block
@@ -208,10 +208,78 @@ struct GroupWalk {
   int col_blocks;
   int row_blocks;
 };
-template <class IO, int T, int K, bool KEPT>
+
+// What a row's eight columns are in memory, held so until they are widened: the
+// next row's are asked for before this one is worked out.
+template <class IO, bool KEPT>
+struct GroupRaw {
+  typedef typename IO::type E;
+  static constexpr int kW = sizeof(E) * 2;  // 4-byte words of 8 elements
+  uint32_t dy[kW], x[KEPT ? 2 : kW], z[KEPT ? 2 : kW];
+  uint16_t s[4];  // KEPT: scales of x and z at the first and the last column
+  template <int W>
+  __device__ __forceinline__ static void words(const void* p, uint32_t* o) {
+    if constexpr (W == 2) {
+      const u32x2_any q = *static_cast<const u32x2_any*>(p);
+      o[0] = q[0]; o[1] = q[1];
+    } else {
+#pragma unroll
+      for (int k = 0; k < W; k += 4) {
+        const u32x4_any q = static_cast<const u32x4_any*>(p)[k / 4];
+        o[k] = q[0]; o[k + 1] = q[1]; o[k + 2] = q[2]; o[k + 3] = q[3];
+      }
+    }
+  }
+  __device__ __forceinline__ void load(const GroupNormArgs& a, int64_t row, int col) {
+    words<kW>(static_cast<const E*>(a.dy) + row * a.D + col, dy);
+    if constexpr (KEPT) {
+      const int64_t nb = (a.D + kPackBlock - 1) / kPackBlock, b0 = row * nb + col / (int)kPackBlock,
+                    b1 = row * nb + (col + 7) / (int)kPackBlock;
+      words<2>(static_cast<const int8_t*>(a.x) + row * a.D + col, x);
+      s[0] = a.xs[b0];
+      s[1] = a.xs[b1];
+      if (a.z) {
+        words<2>(static_cast<const int8_t*>(a.z) + row * a.D + col, z);
+        s[2] = a.zs[b0];
+        s[3] = a.zs[b1];
+      }
+    } else {
+      words<kW>(static_cast<const E*>(a.x) + row * a.D + col, x);
+      if (a.z) words<kW>(static_cast<const E*>(a.z) + row * a.z_row + col, z);
+    }
+  }
+  __device__ __forceinline__ static void widen(const uint32_t* w, float* o) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (sizeof(E) == 2) o[e] = __uint_as_float(e % 2 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+      else o[e] = __uint_as_float(w[e]);
+    }
+  }
+  __device__ __forceinline__ static void widen8(const uint32_t* w, uint16_t s0, uint16_t s1, int cut, float* o) {
+    const float f0 = bf16_bits_to_f32(s0), f1 = bf16_bits_to_f32(s1);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = (float)(int8_t)(w[e / 4] >> (8 * (e % 4))) * (e < cut ? f0 : f1);
+  }
+  __device__ __forceinline__ void get(int col, bool gate, float* dyv, float* xv, float* zv) const {
+    widen(dy, dyv);
+    if constexpr (KEPT) {
+      const int cut = (int)kPackBlock - col % (int)kPackBlock;
+      widen8(x, s[0], s[1], cut, xv);
+      if (gate) widen8(z, s[2], s[3], cut, zv);
+    } else {
+      widen(x, xv);
+      if (gate) widen(z, zv);
+    }
+  }
+};
+
+// FULL: groups of whole eights.
+template <class IO, int T, int K, bool KEPT, bool FULL>
 __global__ __launch_bounds__(group_block(T)) void group_norm_backward_kernel(GroupNormArgs a, GroupWalk w) {
   typedef typename IO::type E;
+  constexpr int BT = group_block(T);
   __shared__ float red[16];
+  extern __shared__ float sums[];  // shared weights: a block's dw and dbias by thread
   const int slot = threadIdx.x / w.per_block, in = threadIdx.x % w.per_block;
   const int lane = blockIdx.x * w.per_block + in;
   const int S = (int)(a.D / a.G), D = (int)a.D;
@@ -228,24 +296,47 @@ __global__ __launch_bounds__(group_block(T)) void group_norm_backward_kernel(Gro
     for (int e = 0; e < 8; ++e) bv[k][e] = dw[k][e] = db[k][e] = 0.f;
     if (a.bias) get8<IoF32>(a.bias + w0, left, bv[k]);
   }
-  for (int64_t r0 = (int64_t)blockIdx.y * w.slots; r0 < a.rows; r0 += (int64_t)w.row_blocks * w.slots) {
+  // FULL: threads past the group's end, or the row's lanes, read its last columns instead
+  GroupRaw<IO, KEPT> raw[FULL ? K : 1];
+  float rn = 0.f, mn = 0.f;
+  auto ask = [&](int64_t r0) {
+    const int64_t r = r0 + slot < a.rows ? r0 + slot : a.rows - 1;
+    const int gq = live ? grp : 0;
+    rn = a.rstd[r * a.G + gq];
+    mn = a.rms ? 0.f : a.mean[r * a.G + gq];
+    if constexpr (FULL) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) raw[k].load(a, r, gq * S + min(chunk_col<T>(k, l), S - 8));
+    }
+  };
+  const int64_t step = (int64_t)w.row_blocks * w.slots;
+  ask((int64_t)blockIdx.y * w.slots);
+  for (int64_t r0 = (int64_t)blockIdx.y * w.slots; r0 < a.rows; r0 += step) {
     const int64_t row = r0 + slot;
     const bool on = live && row < a.rows;
-    const float rstd = on ? a.rstd[row * a.G + grp] : 0.f;
-    const float mean = on && !a.rms ? a.mean[row * a.G + grp] : 0.f;
+    const float rstd = rn, mean = mn;
     float x[K][8], z[K][8], dy[K][8];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = chunk_col<T>(k, l), left = on ? S - c : 0, col = grp * S + c;
-      get8<IO>(static_cast<const E*>(a.dy) + row * D + col, left, dy[k]);
-      if constexpr (KEPT) {
-        get8_kept(static_cast<const int8_t*>(a.x), a.xs, row, col, D, left, x[k]);
-        if (a.z) get8_kept(static_cast<const int8_t*>(a.z), a.zs, row, col, D, left, z[k]);
+      if constexpr (FULL) {
+        raw[k].get((live ? grp : 0) * S + min(c, S - 8), a.z != nullptr, dy[k], x[k], z[k]);
+        if (left <= 0) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dy[k][e] = 0.f;
+        }
       } else {
-        get8<IO>(static_cast<const E*>(a.x) + row * D + col, left, x[k]);
-        if (a.z) get8<IO>(static_cast<const E*>(a.z) + row * a.z_row + col, left, z[k]);
+        get8<IO>(static_cast<const E*>(a.dy) + row * D + col, left, dy[k]);
+        if constexpr (KEPT) {
+          get8_kept(static_cast<const int8_t*>(a.x), a.xs, row, col, D, left, x[k]);
+          if (a.z) get8_kept(static_cast<const int8_t*>(a.z), a.zs, row, col, D, left, z[k]);
+        } else {
+          get8<IO>(static_cast<const E*>(a.x) + row * D + col, left, x[k]);
+          if (a.z) get8<IO>(static_cast<const E*>(a.z) + row * a.z_row + col, left, z[k]);
+        }
       }
     }
+    if (r0 + step < a.rows) ask(r0 + step);
     float s1 = 0.f, s2 = 0.f;
     float xh[K][8];
 #pragma unroll
@@ -253,7 +344,7 @@ __global__ __launch_bounds__(group_block(T)) void group_norm_backward_kernel(Gro
       const int c = chunk_col<T>(k, l);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const bool has = c + e < S;
+        const bool has = on && c + e < S;
         float g = dy[k][e], r = x[k][e];
         float sg = 0.f, act = 0.f;
         if (a.z) {
@@ -265,7 +356,7 @@ __global__ __launch_bounds__(group_block(T)) void group_norm_backward_kernel(Gro
         const float pre = fmaf(h, wv[k][e], bv[k][e]);
         if (a.z && !a.gate_first) {
           x[k][e] = g * pre * dsilu(z[k][e], sg);  // dz
-          g *= act;
+          g = has ? g * act : 0.f;
         }
         if (a.silu) g *= dsilu(pre, sigmoid(pre));
         dw[k][e] = fmaf(g, h, dw[k][e]);
@@ -293,8 +384,37 @@ __global__ __launch_bounds__(group_block(T)) void group_norm_backward_kernel(Gro
         }
         o[e] = d;
       }
-      put8<IO>(static_cast<E*>(a.dx) + row * D + col, left, o);
-      if (a.z) put8<IO>(static_cast<E*>(a.dz) + row * a.dz_row + col, left, x[k]);
+      if (FULL ? left > 0 : true) {
+        const int take = FULL ? 8 : left;
+        put8<IO>(static_cast<E*>(a.dx) + row * D + col, take, o);
+        if (a.z) put8<IO>(static_cast<E*>(a.dz) + row * a.dz_row + col, take, x[k]);
+      }
+    }
+  }
+  if constexpr (T < BT) {
+    if (a.shared) {
+      // the block's groups and rows have the same columns: one sum of them a block
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        if (p && !a.db) break;
+        float* out = a.ws + ((int64_t)p * w.row_blocks * w.col_blocks + (int64_t)blockIdx.y * w.col_blocks + blockIdx.x) * S;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          __syncthreads();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sums[e * BT + threadIdx.x] = live ? (p ? db[k][e] : dw[k][e]) : 0.f;
+          __syncthreads();
+          // thread i adds element i / T of lane i % T over the block's BT / T of them
+          for (int i = threadIdx.x; i < 8 * T; i += BT) {
+            const int e = i / T, ll = i % T;
+            float v = 0.f;
+            for (int q = 0; q < BT / T; ++q) v += sums[e * BT + q * T + ll];
+            const int c = chunk_col<T>(k, ll) + e;
+            if (c < S) out[c] = v;
+          }
+        }
+      }
+      return;
     }
   }
   // a partial sum of every column by row block and slot, [.. , G, S] twice
@@ -311,12 +431,12 @@ __global__ __launch_bounds__(group_block(T)) void group_norm_backward_kernel(Gro
 }
 
 // 64 columns a block of `cols`; blockIdx.y: dw or dbias.
-__global__ __launch_bounds__(kColsumThreads) void group_norm_param_kernel(GroupNormArgs a, int64_t parts, int cols,
-                                                                          int64_t rows) {
+// `rows` partial sums of each.
+__global__ __launch_bounds__(kColsumThreads) void group_norm_param_kernel(GroupNormArgs a, int cols, int64_t rows) {
   __shared__ float lds[kColsumThreads];
   const int lane = threadIdx.x & 63;
   const int c = blockIdx.x * 64 + lane;
-  const float* p = a.ws + (blockIdx.y ? parts * a.D : 0) + min(c, cols - 1);
+  const float* p = a.ws + (blockIdx.y ? rows * cols : 0) + min(c, cols - 1);
   const float s = column_sum(p, rows, cols, lds);
   if (threadIdx.x < 64 && c < cols) (blockIdx.y ? a.db : a.dw)[c] = s;
 }
@@ -404,8 +524,8 @@ static GroupWalk group_walk(int64_t rows, int64_t G, int T) {
   w.per_block = w.lanes < block ? w.lanes : block;
   w.slots = block / w.per_block;
   w.col_blocks = (w.lanes + block - 1) / block;
-  // up to eight blocks a compute unit, each with some rows to walk
-  int64_t rb = (int64_t)device_cu_count() * 8 / w.col_blocks;
+  // three blocks a compute unit are there at once
+  int64_t rb = (int64_t)device_cu_count() * (block > 256 ? 1 : 3) / w.col_blocks;
   const int64_t most = (rows + w.slots - 1) / w.slots;
   if (rb > most) rb = most;
   w.row_blocks = (int)(rb < 1 ? 1 : rb > 65535 ? 65535 : rb);
@@ -423,18 +543,27 @@ static hipError_t forward(const GroupNormArgs& a, hipStream_t s) {
                      dim3(group_block(T)), 0, s, a);
   return hipGetLastError();
 }
+template <class IO, int T, int K, bool KEPT, bool FULL>
+static hipError_t backward_as(const GroupNormArgs& a, const GroupWalk& w, hipStream_t s) {
+  constexpr int BT = group_block(T);
+  const size_t lds = T < BT && a.shared ? (size_t)8 * BT * 4 : 0;
+  hipLaunchKernelGGL((group_norm_backward_kernel<IO, T, K, KEPT, FULL>),
+                     dim3((unsigned)w.col_blocks, (unsigned)w.row_blocks), dim3(BT), lds, s, a, w);
+  return hipGetLastError();
+}
 template <class IO, int T, int K>
 static hipError_t backward(const GroupNormArgs& a, hipStream_t s) {
   const GroupWalk w = group_walk(a.rows, a.G, T);
-  const dim3 grid((unsigned)w.col_blocks, (unsigned)w.row_blocks);
-  if (a.xs) hipLaunchKernelGGL((group_norm_backward_kernel<IO, T, K, true>), grid, dim3(group_block(T)), 0, s, a, w);
-  else hipLaunchKernelGGL((group_norm_backward_kernel<IO, T, K, false>), grid, dim3(group_block(T)), 0, s, a, w);
-  const hipError_t e = hipGetLastError();
+  const bool full = a.D / a.G % 8 == 0;
+  hipError_t e;
+  if (a.xs) e = full ? backward_as<IO, T, K, true, true>(a, w, s) : backward_as<IO, T, K, true, false>(a, w, s);
+  else e = full ? backward_as<IO, T, K, false, true>(a, w, s) : backward_as<IO, T, K, false, false>(a, w, s);
   if (e != hipSuccess) return e;
-  const int64_t parts = (int64_t)w.row_blocks * w.slots;
   const int cols = (int)(a.shared ? a.D / a.G : a.D);
+  int64_t rows = (int64_t)w.row_blocks * w.slots;
+  if (a.shared) rows = T < group_block(T) ? (int64_t)w.row_blocks * w.col_blocks : rows * a.G;
   hipLaunchKernelGGL(group_norm_param_kernel, dim3((unsigned)((cols + 63) / 64), a.db ? 2 : 1), dim3(kColsumThreads), 0,
-                     s, a, parts, cols, parts * a.D / cols);
+                     s, a, cols, rows);
   return hipGetLastError();
 }
 #define SSD_GROUP_CASES(f)                          \
