@@ -549,26 +549,39 @@ struct ChainLds {
   static constexpr int q = 2 * half, x = q + 2 * kRows, total = x + 2 * C * kX;
 };
 
-template <int NP, int C, bool VL, bool SAVE>
+// Rows too long and too few to fill the chip are cut into stretches, walked side
+// by side in two passes.  A stretch maps the state in front of it to M S + R:
+// kStretch walks it from the unit matrix (N more columns, without values) and
+// from zero, delta_enter_kernel joins the stretches' maps in order, and kOut
+// then walks each from the state that enters it.
+enum ChainMode { kOut, kSave, kStretch };
+template <int NP, int C, bool VL, ChainMode MODE>
 __global__ __launch_bounds__(128 * C, C) void delta_chain_bf16_kernel(DeltaArgs a, DeltaWs ws) {
   typedef DeltaB M;
   typedef DeltaB::One One;
   typedef DeltaB::Two Two;
   typedef ChainLds<NP, C> Lay;
   constexpr int NT = NP / 16, KS = NP / 32, LP = Lay::kPitch, NH = 64 * C;
+  constexpr bool SAVE = MODE == kSave, OUT = MODE == kOut;
   extern __shared__ __align__(16) char lds[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
   const uint32_t bid = near_block(blockIdx.x, gridDim.x);
-  const uint32_t slices = (uint32_t)(a.P / 16) / C;
-  const int64_t bh = bid / slices, h = bh % a.H, b = bh / a.H, grp = h / (a.H / a.G);
-  const uint32_t p = ((bid % slices) * C + wave % C) * 16 + c;
   const int N = (int)a.N;
+  const uint32_t slices = (uint32_t)((MODE == kStretch ? a.N + a.P : a.P) / 16) / C;
+  const uint32_t segs = MODE == kOut ? (uint32_t)ws.segs : MODE == kStretch ? (uint32_t)ws.segs - 1 : 1;
+  const int64_t seg = bid / slices % segs, bh = bid / slices / segs, h = bh % a.H, b = bh / a.H, grp = h / (a.H / a.G);
+  uint32_t p = ((bid % slices) * C + wave % C) * 16 + c;
+  // kStretch: columns of the unit matrix, then those of the values
+  const bool unit = MODE == kStretch && __builtin_amdgcn_readfirstlane(((bid % slices) * C + wave % C) * 16) < N;
+  if (MODE == kStretch && !unit) p -= N;
   const uint32_t P = (uint32_t)a.P;
   const int64_t row = b * a.L;
-  const uint8_t* marks = VL && !SAVE && a.nseq > 0 ? reinterpret_cast<const uint8_t*>(a.ws + ws.marks) : nullptr;
+  const uint8_t* marks = VL && OUT && a.nseq > 0 ? reinterpret_cast<const uint8_t*>(a.ws + ws.marks) : nullptr;
   Pieces pc;
-  pc.first(VL ? reinterpret_cast<const Cuts*>(a.ws + ws.cuts) + b * ws.nw : nullptr, ws.nw, a.L);
+  const int64_t w0 = MODE == kSave ? 0 : seg * ws.seg_wins;
+  pc.first(VL ? reinterpret_cast<const Cuts*>(a.ws + ws.cuts) + b * ws.nw : nullptr, w0,
+           MODE == kSave || w0 + ws.seg_wins > ws.nw ? ws.nw : w0 + ws.seg_wins, a.L);
 
   if (wave >= C) {
     // ---- helper
@@ -605,8 +618,8 @@ __global__ __launch_bounds__(128 * C, C) void delta_chain_bf16_kernel(DeltaArgs 
       if (more) nx.step();
       const bool ahead = more && nx.valid();
       if (ahead) ask(nx);
-      if (!SAVE && more) qt.load(qb + pc.win * kC * a.rows.q, qrow, N, pc.n, ht);
-      if (!SAVE && j > 0) {
+      if (OUT && more) qt.load(qb + pc.win * kC * a.rows.q, qrow, N, pc.n, ht);
+      if (OUT && j > 0) {
         const char* x = lds + Lay::x + (((j - 1) & 1) * C + wave % C) * Lay::kX;
         const uint16_t* ql = reinterpret_cast<const uint16_t*>(lds + Lay::q + ((j - 1) & 1) * Lay::kRows);
         f32x4_t y[4], u[4];
@@ -656,7 +669,7 @@ __global__ __launch_bounds__(128 * C, C) void delta_chain_bf16_kernel(DeltaArgs 
                         end, g);
       }
       if (!more) break;
-      if constexpr (!SAVE) {
+      if constexpr (OUT) {
         // kept for the next step, when piece j is worked out
         const int64_t bhw = bh * ws.nw + pc.win;
         const char* fp = a.ws + ws.low_p + bhw * kTriBytes;
@@ -674,24 +687,27 @@ __global__ __launch_bounds__(128 * C, C) void delta_chain_bf16_kernel(DeltaArgs 
       if (ahead) put(nx, (j + 1) & 1);
       pc = nx;
       __syncthreads();
-      if (SAVE && !ahead) break;
+      if (!OUT && !ahead) break;
     }
     return;
   }
 
   // ---- column wave
   f32x4_t S[NT];
+  const float* from = a.h0 ? a.h0 + bh * N * a.P : nullptr;
+  if (MODE == kOut && segs > 1) from = reinterpret_cast<const float*>(a.ws + ws.enter) + (bh * segs + seg) * N * a.P;
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int nn = 16 * j + 4 * g + r;
-      S[j][r] = a.h0 && nn < N ? a.h0[(bh * N + nn) * a.P + p] : 0.f;
+      if (MODE == kStretch) S[j][r] = unit && nn == (int)p ? 1.f : 0.f;
+      else S[j][r] = from && nn < N ? from[nn * a.P + p] : 0.f;
     }
   const uint32_t vrow = (uint32_t)a.rows.v, voff = 4 * g * vrow + p;
   const uint16_t* vb = static_cast<const uint16_t*>(a.v) + row * a.rows.v + h * a.P;
   Column vn;
-  vn.load(vb + pc.win * kC * a.rows.v, vrow, voff, pc.n);
+  vn.load(vb + pc.win * kC * a.rows.v, vrow, voff, unit ? 0 : pc.n);
   __syncthreads();
   for (int step = 0; pc.valid(); ++step) {
     const int begin = pc.begin, end = pc.end;
@@ -727,7 +743,7 @@ __global__ __launch_bounds__(128 * C, C) void delta_chain_bf16_kernel(DeltaArgs 
       float v[8];
       slots(S[2 * s], S[2 * s + 1], v);
       const Two sb = M::two(v);
-      if constexpr (!SAVE) M::store(x + s * 2048, lane, sb);
+      if constexpr (OUT) M::store(x + s * 2048, lane, sb);
 #pragma unroll
       for (int i = 0; i < 4; ++i) X[i] = M::mma(kf[s][i], sb.lo, X[i]);
 #pragma unroll
@@ -768,7 +784,7 @@ __global__ __launch_bounds__(128 * C, C) void delta_chain_bf16_kernel(DeltaArgs 
         bx[i][r] = be[i][r] * X[i][r];
       }
     pc.step();
-    if (pc.valid()) vn.load(vb + pc.win * kC * a.rows.v, vrow, voff, pc.n);
+    if (pc.valid()) vn.load(vb + pc.win * kC * a.rows.v, vrow, voff, unit ? 0 : pc.n);
     // w = X + R (b X); u = b w
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -800,7 +816,7 @@ __global__ __launch_bounds__(128 * C, C) void delta_chain_bf16_kernel(DeltaArgs 
           u[r] = !VL || (t >= begin && t < end) ? be[i][r] * X[i][r] : 0.f;
           v[4 * t4 + r] = u[r] * ko[i][r];
         }
-        if constexpr (!SAVE) *reinterpret_cast<f32x4_t*>(x + KS * 2048 + i * 1024 + 16 * lane) = u;
+        if constexpr (OUT) *reinterpret_cast<f32x4_t*>(x + KS * 2048 + i * 1024 + 16 * lane) = u;
       }
       const Two ub = M::two(v);
 #pragma unroll
@@ -818,7 +834,67 @@ __global__ __launch_bounds__(128 * C, C) void delta_chain_bf16_kernel(DeltaArgs 
     }
     __syncthreads();
   }
-  if (!SAVE && a.hfin) put_state<NT>(a.hfin + bh * N * a.P, N, P, 4 * g * P + p, S);
+  if (OUT && a.hfin && seg == segs - 1) put_state<NT>(a.hfin + bh * N * a.P, N, P, 4 * g * P + p, S);
+  if constexpr (MODE == kStretch) {
+    const uint32_t cols = (uint32_t)N + P;
+    put_state<NT>(reinterpret_cast<float*>(a.ws + ws.trans) + (bh * segs + seg) * N * cols, N, cols,
+                  4 * g * cols + (unit ? p : N + p), S);
+  }
+}
+
+// The states that enter the stretches of a row: S' = M S + R, one wave 16 columns.
+template <int NP>
+__global__ __launch_bounds__(64) void delta_enter_kernel(DeltaArgs a, DeltaWs ws) {
+  typedef DeltaB M;
+  constexpr int NT = NP / 16, KS = NP / 32;
+  const int lane = threadIdx.x, c = lane & 15, g = lane >> 4, N = (int)a.N;
+  const uint32_t P = (uint32_t)a.P, cols = N + P, tiles = P / 16;
+  const int64_t bh = blockIdx.x / tiles;
+  const uint32_t p = blockIdx.x % tiles * 16 + c;
+  f32x4_t S[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int nn = 16 * j + 4 * g + r;
+      S[j][r] = a.h0 && nn < N ? a.h0[(bh * N + nn) * a.P + p] : 0.f;
+    }
+  for (int64_t seg = 0;; ++seg) {
+    put_state<NT>(reinterpret_cast<float*>(a.ws + ws.enter) + (bh * ws.segs + seg) * N * P, N, P, 4 * g * P + p, S);
+    if (seg == ws.segs - 1) break;
+    const float* m = reinterpret_cast<const float*>(a.ws + ws.trans) + (bh * (ws.segs - 1) + seg) * N * cols;
+    const __amdgpu_buffer_rsrc_t r = rows_of(m, (uint32_t)N * cols * 4);
+    M::Two sb[KS];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      float v[8];
+      slots(S[2 * s], S[2 * s + 1], v);
+      sb[s] = M::two(v);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        S[j][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (4 * g * cols + N + p) * 4, (16 * j + e) * cols * 4, 0));
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      f32x4_t x[KS][2];
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int col = 32 * s + 16 * t + 4 * g;
+          x[s][t] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                    r, col < N ? (c * cols + col) * 4 : kNowhere, 16 * j * cols * 4, 0));
+        }
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        float v[8];
+        slots(x[s][0], x[s][1], v);
+        S[j] = M::mma(M::two(v), sb[s], S[j]);
+      }
+    }
+  }
 }
 
 // ---------------------------------------------------------------- one token
@@ -935,8 +1011,9 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a, const floa
 }
 
 // ---------------------------------------------------------------- launches
+int64_t delta_segments(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P, bool bf16);
 size_t delta_forward_ws_bytes(int64_t B, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P) {
-  return delta_ws(B, L, H, N, P, false).total;
+  return delta_ws(B, L, H, N, P, false, delta_segments(B, L, H, N, P, true)).total;
 }
 
 template <class M, int NP, bool BACK>
@@ -975,24 +1052,48 @@ static hipError_t chain(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) {
   hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * a.H * (a.P / 16 / w))), dim3(64 * w), lds, s, a, ws);
   return hipGetLastError();
 }
-template <int NP, int C, bool VL, bool SAVE>
+template <int NP, int C, bool VL, ChainMode MODE>
 static hipError_t chain_bf16(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) {
-  auto kern = delta_chain_bf16_kernel<NP, C, VL, SAVE>;
-  const size_t lds = SAVE ? ChainLds<NP, C>::q : ChainLds<NP, C>::total;
+  auto kern = delta_chain_bf16_kernel<NP, C, VL, MODE>;
+  const size_t lds = MODE == kOut ? ChainLds<NP, C>::total : ChainLds<NP, C>::q;
   hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * a.H * (a.P / 16 / C))), dim3(128 * C), lds, s, a, ws);
+  const int64_t cols = MODE == kStretch ? a.N + a.P : a.P, segs = MODE == kOut ? ws.segs : MODE == kStretch ? ws.segs - 1 : 1;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * a.H * segs * (cols / 16 / C))), dim3(128 * C), lds, s, a, ws);
   return hipGetLastError();
 }
-template <int NP, int C>
+template <int NP, bool VL, ChainMode MODE>
+static hipError_t chain_bf16_as(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) {
+  const int64_t cols = MODE == kStretch ? a.N + a.P : a.P;
+  return cols % 32 == 0 ? chain_bf16<NP, 2, VL, MODE>(a, ws, s) : chain_bf16<NP, 1, VL, MODE>(a, ws, s);
+}
+template <int NP, bool VL>
 static hipError_t chain_bf16_of(const DeltaArgs& a, const DeltaWs& ws, bool save, hipStream_t s) {
-  const bool vl = a.seq_idx || (!save && a.nseq > 0);
-  if (save) return vl ? chain_bf16<NP, C, true, true>(a, ws, s) : chain_bf16<NP, C, false, true>(a, ws, s);
-  return vl ? chain_bf16<NP, C, true, false>(a, ws, s) : chain_bf16<NP, C, false, false>(a, ws, s);
+  if (save) return chain_bf16_as<NP, VL, kSave>(a, ws, s);
+  if (ws.segs > 1) {
+    hipError_t e = chain_bf16_as<NP, VL, kStretch>(a, ws, s);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(delta_enter_kernel<NP>, dim3((unsigned)(a.B * a.H * (a.P / 16))), dim3(64), 0, s, a, ws);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return chain_bf16_as<NP, VL, kOut>(a, ws, s);
 }
 template <int NP>
 static hipError_t chain_bf16_at(const DeltaArgs& a, const DeltaWs& ws, bool save, hipStream_t s) {
-  return a.P % 32 == 0 ? chain_bf16_of<NP, 2>(a, ws, save, s) : chain_bf16_of<NP, 1>(a, ws, save, s);
+  const bool vl = a.seq_idx || (!save && a.nseq > 0);
+  return vl ? chain_bf16_of<NP, true>(a, ws, save, s) : chain_bf16_of<NP, false>(a, ws, save, s);
+}
+// Stretches of a row: as many as leave each compute unit a block (of 32 columns)
+// and each stretch four windows; from four on the second pass pays.  Only the
+// bf16 chain of up to 128 key columns has them.
+int64_t delta_segments(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P, bool bf16) {
+  if (!bf16 || N > 128) return 1;
+  const int64_t nw = (L + kDeltaC - 1) / kDeltaC, blocks = B * H * (P % 32 == 0 ? P / 32 : P / 16);
+  int64_t segs = device_cu_count() / blocks;
+  if (segs > nw / 4) segs = nw / 4;
+  if (segs < 4) return 1;
+  return (nw + (nw + segs - 1) / segs - 1) / ((nw + segs - 1) / segs);  // none of them empty
 }
 template <class M, int NP>
 static hipError_t chain_of(const DeltaArgs& a, const DeltaWs& ws, bool save, hipStream_t s) {
@@ -1016,7 +1117,7 @@ hipError_t launch_delta_chain(const DeltaArgs& a, const DeltaWs& ws, bool save, 
 }
 
 hipError_t launch_delta_forward(const DeltaArgs& a, bool bf16, hipStream_t s) {
-  const DeltaWs ws = delta_ws(a.B, a.L, a.H, a.N, a.P, false);
+  const DeltaWs ws = delta_ws(a.B, a.L, a.H, a.N, a.P, false, delta_segments(a.B, a.L, a.H, a.N, a.P, bf16));
   if (a.nseq > 0) {
     uint8_t* marks = reinterpret_cast<uint8_t*>(a.ws + ws.marks);
     hipLaunchKernelGGL(delta_marks_clear_kernel, flat_grid((a.B * a.L + 255) / 256), dim3(256), 0, s, marks, a.B * a.L);

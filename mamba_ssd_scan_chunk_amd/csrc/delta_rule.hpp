@@ -212,13 +212,14 @@ struct Pieces {
   // waited for and put into scalars where it is taken over
   __device__ __forceinline__ static Cuts uniform(const Cuts& c) { return {uniform64(c.piece), uniform64(c.fresh)}; }
   __device__ __forceinline__ int tokens() const { return (int)(L - win * kC < kC ? L - win * kC : kC); }
-  __device__ __forceinline__ void first(const Cuts* l, int64_t windows, int64_t len) {
+  // windows from .. to - 1
+  __device__ __forceinline__ void first(const Cuts* l, int64_t from, int64_t to, int64_t len) {
     list = l;
-    nw = windows;
+    nw = to;
     L = len;
-    win = 0;
-    cuts = uniform(at(0));
-    next = at(1);
+    win = from;
+    cuts = uniform(at(from));
+    next = at(from + 1);
     begin = 0;
     n = tokens();
     end = piece_end(cuts.piece, 0, n);
@@ -393,9 +394,11 @@ __device__ __forceinline__ uint32_t near_block(uint32_t bid, uint32_t n) {
 // ---- the workspace ----
 struct DeltaWs {
   int64_t nw;        // windows a row
-  size_t gates, cuts, low_r, low_p, up_r, up_p, marks, S, D, w, du, dq, dk, part, total;
+  size_t gates, cuts, low_r, low_p, up_r, up_p, marks, trans, enter, S, D, w, du, dq, dk, part, total;
+  int64_t segs, seg_wins;  // stretches of a row that are walked side by side, and their windows
 };
-inline DeltaWs delta_ws(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P, bool back) {
+// segs: see delta_segments().
+inline DeltaWs delta_ws(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P, bool back, int64_t segs = 1) {
   DeltaWs o = {};
   o.nw = (L + kDeltaC - 1) / kDeltaC;
   const size_t bhw = (size_t)(B * H * o.nw);
@@ -411,6 +414,12 @@ inline DeltaWs delta_ws(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P, b
   if (!back) {
     o.low_p = take(bhw * kTriBytes);
     o.marks = take((size_t)(B * L));
+    o.segs = segs;
+    o.seg_wins = (o.nw + segs - 1) / segs;
+    if (segs > 1) {
+      o.trans = take((size_t)(B * H * (segs - 1) * N * (N + P)) * 4);
+      o.enter = take((size_t)(B * H * segs * N * P) * 4);
+    }
   } else {
     o.up_r = take(bhw * kTriBytes);
     o.up_p = take(bhw * kTriBytes);

@@ -297,3 +297,20 @@ def test_gradients_into_column_slices(dtype):
     for n in out:
         assert torch.equal(got[n], dense[n]), n
     assert (wide[..., -3:] == 5).all() and (ab[..., -1:] == 5).all()
+
+
+@pytest.mark.parametrize("shape", [(1, 1500, 2, 1, 64, 32), (1, 2111, 1, 1, 48, 16), (2, 1030, 2, 2, 128, 128)])
+@pytest.mark.parametrize("starts", [0, 6])
+def test_long_rows_of_few_heads(shape, starts):
+    """Rows cut into stretches that are walked side by side."""
+    a = ref.inputs(*shape, dtype=BF, seed=sum(shape))
+    B, L = shape[:2]
+    idx = ref.packed(B, L, starts, seed=L) if starts else None
+    last = [L - 1, 700, 64 * 16, 3] if starts else []
+    how = dict(seq_last=torch.tensor(last).cuda()) if starts else {}
+    got = call(a, seq_idx=None if idx is None else idx.cuda(), **how)
+    wy, wf, asked = ref.forward(**a, seq_idx=idx, states_after=last)
+    check(got[0], wy, BF, "y")
+    check(got[1], wf, BF, "final")
+    for s, i in enumerate(last):
+        check(got[2][s], asked[i], BF, f"state after {i}")
