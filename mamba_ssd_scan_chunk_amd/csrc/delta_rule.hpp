@@ -344,7 +344,7 @@ struct GateTile {
 // A lane's 16 tokens (rows 16 i + 4 g + r) of one column, at lane offset
 // (4 g stride + column) elements.
 struct Column {
-  uint16_t q[16];
+  uint32_t q[16];  // a register each: packed in pairs they would be waited for where they are asked for
   __device__ __forceinline__ static uint32_t row(int e) { return 16 * (e / 4) + e % 4; }
   __device__ __forceinline__ void load(const uint16_t* base, uint32_t stride, uint32_t off, int n) {
     const __amdgpu_buffer_rsrc_t r = rows_of(base, (uint32_t)n * stride * 2);

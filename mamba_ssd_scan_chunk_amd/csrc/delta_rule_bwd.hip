@@ -602,6 +602,7 @@ __global__ __launch_bounds__(64 * WV, 2) void delta_grad_kernel(DeltaArgs a, Del
   auto f4 = [](const __amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t s) {
     return __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, s, 0));
   };
+  auto input = [](uint32_t v) { return es == 2 ? bf16_bits_to_f32(v) : __uint_as_float(v); };
   float sumA = 0.f, sumB = 0.f;  // of dA and ddt_bias, in wave 0
   const f32x4_t zero4 = {0.f, 0.f, 0.f, 0.f};
 
@@ -717,7 +718,7 @@ __global__ __launch_bounds__(64 * WV, 2) void delta_grad_kernel(DeltaArgs a, Del
       }
     }
     // q and k of the wave's columns, 16 tokens a lane, for what follows the matrices
-    T kv[NTW][16], qv[NTW][16];
+    uint32_t kv[NTW][16], qv[NTW][16];
 #pragma unroll
     for (int m = 0; m < NTW; ++m) {
       const uint32_t nn = 16 * (wave + WV * m) + c;
@@ -729,8 +730,8 @@ __global__ __launch_bounds__(64 * WV, 2) void delta_grad_kernel(DeltaArgs a, Del
           kv[m][e] = __builtin_amdgcn_raw_buffer_load_b16(kr, ko, t * krow, 0);
           qv[m][e] = __builtin_amdgcn_raw_buffer_load_b16(qr, qo, t * qrow, 0);
         } else {
-          kv[m][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(kr, ko, t * krow, 0));
-          qv[m][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(qr, qo, t * qrow, 0));
+          kv[m][e] = __builtin_amdgcn_raw_buffer_load_b32(kr, ko, t * krow, 0);
+          qv[m][e] = __builtin_amdgcn_raw_buffer_load_b32(qr, qo, t * qrow, 0);
         }
       }
     }
@@ -846,7 +847,7 @@ __global__ __launch_bounds__(64 * WV, 2) void delta_grad_kernel(DeltaArgs a, Del
 #pragma unroll
         for (int m = 0; m < NTW; ++m) {
           if (VL && !on) kv[m][4 * i + r] = qv[m][4 * i + r] = 0;
-          const float k = M::IO::get(kv[m][4 * i + r]), q = M::IO::get(qv[m][4 * i + r]);
+          const float k = input(kv[m][4 * i + r]), q = input(qv[m][4 * i + r]);
           const float x = in[r] * qS[m][i][r], y = in[r] * wS[m][i][r], z = uD[m][i][r];
           rs[r] += (rq[r] * q) * x - (rk[r] * k) * y;
           cd[r] = fmaf(ko[r] * k, z, cd[r]);
@@ -870,8 +871,8 @@ __global__ __launch_bounds__(64 * WV, 2) void delta_grad_kernel(DeltaArgs a, Del
         float x[8], y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          x[e] = M::IO::get(kv[m][8 * s + e]);
-          y[e] = M::IO::get(qv[m][8 * s + e]);
+          x[e] = input(kv[m][8 * s + e]);
+          y[e] = input(qv[m][8 * s + e]);
         }
         kb[m][s] = M::one(x);
         qb[m][s] = M::one(y);
