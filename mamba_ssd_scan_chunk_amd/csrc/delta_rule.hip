@@ -535,14 +535,14 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs w
 }
 
 // ---------------------------------------------------------------- the chain of bf16 inputs
-// C column waves and C helpers, a block a compute unit.  A step takes a piece:
-// the column waves correct its values and update their state, which is the
-// chain's length; the helpers load the next piece's operands into the other
-// half of LDS and work out the outputs of the piece before, from the operands
-// (state, u) that the column waves left in LDS.
+// C column waves, C stagers and C output waves, a block a compute unit.  A step
+// takes a piece: the column waves correct its values and update their state,
+// which is the chain's length; the stagers put the next piece's operands, asked
+// for a step before, into the other half of LDS; the output waves work out the
+// piece before, from the operands (state, u) that the column waves left in LDS.
 template <int NP, int C>
 struct ChainLds {
-  static constexpr int kPitch = NP + 8;
+  static constexpr int kPitch = NP + 24;  // rows as the products read them begin in different banks
   static constexpr int kRows = kC * kPitch * 2;
   static constexpr int kX = (NP / 32 + 2) * 2048;  // operands of a column wave: state and u
   static constexpr int k = 0, r = k + kRows, g = r + kTriBytes, half = g + 5 * kC * 4;
@@ -556,7 +556,7 @@ struct ChainLds {
 // then walks each from the state that enters it.
 enum ChainMode { kOut, kSave, kStretch };
 template <int NP, int C, bool VL, ChainMode MODE>
-__global__ __launch_bounds__(128 * C, C) void delta_chain_bf16_kernel(DeltaArgs a, DeltaWs ws) {
+__global__ __launch_bounds__(MODE == kOut ? chain_threads(C) : 128 * C, C) void delta_chain_bf16_kernel(DeltaArgs a, DeltaWs ws) {
   typedef DeltaB M;
   typedef DeltaB::One One;
   typedef DeltaB::Two Two;
@@ -583,13 +583,14 @@ __global__ __launch_bounds__(128 * C, C) void delta_chain_bf16_kernel(DeltaArgs 
   pc.first(VL ? reinterpret_cast<const Cuts*>(a.ws + ws.cuts) + b * ws.nw : nullptr, w0,
            MODE == kSave || w0 + ws.seg_wins > ws.nw ? ws.nw : w0 + ws.seg_wins, a.L);
 
-  if (wave >= C) {
-    // ---- helper
-    const int ht = tid - NH;
+  constexpr int SG = OUT ? first_stager(C) : C;
+  if (wave >= SG) {
+    // ---- stager: pc is the piece the column waves take, n1 the next
+    const int ht = tid - 64 * SG;
     RowTile<NP, NH> kt, qt;
     TriTile<NH> rt;
     GateTile<NH> gt;
-    const uint32_t krow = (uint32_t)a.rows.k, qrow = (uint32_t)a.rows.q, yrow = (uint32_t)(a.H * a.P);
+    const uint32_t krow = (uint32_t)a.rows.k, qrow = (uint32_t)a.rows.q;
     const uint16_t* kb = static_cast<const uint16_t*>(a.k) + row * a.rows.k + grp * N;
     const uint16_t* qb = static_cast<const uint16_t*>(a.q) + row * a.rows.q + grp * N;
     auto ask = [&](const Pieces& s) {
@@ -606,50 +607,61 @@ __global__ __launch_bounds__(128 * C, C) void delta_chain_bf16_kernel(DeltaArgs 
     };
     ask(pc);
     put(pc, 0);
+    Pieces n1 = pc;
+    n1.step();
+    if (n1.valid()) ask(n1);
+    if (OUT) qt.load(qb + pc.win * kC * a.rows.q, qrow, N, pc.n, ht);
     __syncthreads();
+    for (int j = 0; pc.valid(); ++j) {
+      if (n1.valid()) put(n1, (j + 1) & 1);
+      if (OUT) qt.template store<VL>(reinterpret_cast<uint16_t*>(lds + Lay::q + (j & 1) * Lay::kRows), LP, pc.begin, pc.end, ht);
+      pc = n1;
+      if (n1.valid()) {
+        if (OUT) qt.load(qb + n1.win * kC * a.rows.q, qrow, N, n1.n, ht);
+        n1.step();
+        if (n1.valid()) ask(n1);
+      }
+      __syncthreads();
+    }
+    return;
+  }
+  if (wave >= 2 * C) return;
+  if (OUT && wave >= C) {
+    // ---- output wave: pc is the piece the column waves take, the one before is worked out
+    const uint32_t yrow = (uint32_t)(a.H * a.P);
     Two pf[kTriFrags];
     f32x4_t qin[4];
     int64_t t0 = 0;
     int begin = 0, end = 0, n = 0;
+    __syncthreads();
     for (int j = 0;; ++j) {
-      // pc: piece j, which the column waves take now
-      const bool more = pc.valid();
-      Pieces nx = pc;
-      if (more) nx.step();
-      const bool ahead = more && nx.valid();
-      if (ahead) ask(nx);
-      if (OUT && more) qt.load(qb + pc.win * kC * a.rows.q, qrow, N, pc.n, ht);
-      if (OUT && j > 0) {
+      if (j > 0) {
         const char* x = lds + Lay::x + (((j - 1) & 1) * C + wave % C) * Lay::kX;
         const uint16_t* ql = reinterpret_cast<const uint16_t*>(lds + Lay::q + ((j - 1) & 1) * Lay::kRows);
         f32x4_t y[4], u[4];
+        Two sb[KS];
+        One qf[KS][4];
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          sb[s] = M::load(x + s * 2048, lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint16_t* qp = ql + (16 * i + c) * LP + 32 * s + 4 * g;
+            qf[s][i] = lds_4x2<M>(qp, qp + 16);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           y[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
           u[i] = *reinterpret_cast<const f32x4_t*>(x + KS * 2048 + i * 1024 + 16 * lane);
         }
-        constexpr int SB = KS > 1 ? 2 : 1;  // steps whose operands are asked for together
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int s0 = 0; s0 < KS; s0 += SB) {
-          Two sb[SB];
-          One qf[SB][4];
+        for (int s = 0; s < KS; ++s) {
 #pragma unroll
-          for (int s = 0; s < SB; ++s) {
-            sb[s] = M::load(x + (s0 + s) * 2048, lane);
+          for (int i = 0; i < 4; ++i) y[i] = M::mma(qf[s][i], sb[s].lo, y[i]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint16_t* qp = ql + (16 * i + c) * LP + 32 * (s0 + s) + 4 * g;
-              qf[s][i] = lds_4x2<M>(qp, qp + 16);
-            }
-          }
-          __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-          for (int s = 0; s < SB; ++s) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = M::mma(qf[s][i], sb[s].lo, y[i]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = M::mma(qf[s][i], sb[s].hi, y[i]);
-          }
+          for (int i = 0; i < 4; ++i) y[i] = M::mma(qf[s][i], sb[s].hi, y[i]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] *= qin[i];
@@ -668,31 +680,26 @@ __global__ __launch_bounds__(128 * C, C) void delta_chain_bf16_kernel(DeltaArgs 
         Column::put<VL>(static_cast<uint16_t*>(a.y) + ((row + t0) * a.H + h) * a.P, yrow, 4 * g * yrow + p, n, y, begin,
                         end, g);
       }
-      if (!more) break;
-      if constexpr (OUT) {
-        // kept for the next step, when piece j is worked out
-        const int64_t bhw = bh * ws.nw + pc.win;
-        const char* fp = a.ws + ws.low_p + bhw * kTriBytes;
+      if (!pc.valid()) break;
+      // kept for the next step, when piece j is worked out
+      const char* fp = a.ws + ws.low_p + (bh * ws.nw + pc.win) * kTriBytes;
 #pragma unroll
-        for (int f = 0; f < kTriFrags; ++f) pf[f] = M::load(fp + f * 2048, lane);
-        const float* sq = reinterpret_cast<const float*>(lds + (j & 1) * Lay::half + Lay::g) + 2 * kC;
+      for (int f = 0; f < kTriFrags; ++f) pf[f] = M::load(fp + f * 2048, lane);
+      const float* sq = reinterpret_cast<const float*>(lds + (j & 1) * Lay::half + Lay::g) + 2 * kC;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) qin[i] = *reinterpret_cast<const f32x4_t*>(sq + 16 * i + 4 * g);
-        qt.template store<VL>(reinterpret_cast<uint16_t*>(lds + Lay::q + (j & 1) * Lay::kRows), LP, pc.begin, pc.end, ht);
-        t0 = pc.win * kC;
-        n = pc.n;
-        begin = pc.begin;
-        end = pc.end;
-      }
-      if (ahead) put(nx, (j + 1) & 1);
-      pc = nx;
+      for (int i = 0; i < 4; ++i) qin[i] = *reinterpret_cast<const f32x4_t*>(sq + 16 * i + 4 * g);
+      t0 = pc.win * kC;
+      n = pc.n;
+      begin = pc.begin;
+      end = pc.end;
+      pc.step();
       __syncthreads();
-      if (!OUT && !ahead) break;
     }
     return;
   }
 
   // ---- column wave
+  __builtin_amdgcn_s_setprio(3);
   f32x4_t S[NT];
   const float* from = a.h0 ? a.h0 + bh * N * a.P : nullptr;
   if (MODE == kOut && segs > 1) from = reinterpret_cast<const float*>(a.ws + ws.enter) + (bh * segs + seg) * N * a.P;
@@ -1059,7 +1066,8 @@ static hipError_t chain_bf16(const DeltaArgs& a, const DeltaWs& ws, hipStream_t 
   hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
   const int64_t cols = MODE == kStretch ? a.N + a.P : a.P, segs = MODE == kOut ? ws.segs : MODE == kStretch ? ws.segs - 1 : 1;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * a.H * segs * (cols / 16 / C))), dim3(128 * C), lds, s, a, ws);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * a.H * segs * (cols / 16 / C))), dim3(MODE == kOut ? chain_threads(C) : 128 * C),
+                     lds, s, a, ws);
   return hipGetLastError();
 }
 template <int NP, bool VL, ChainMode MODE>

@@ -386,6 +386,12 @@ __device__ __forceinline__ void put_state(float* base, int N, uint32_t P, uint32
       __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[j][e]), r, off * 4, (16 * j + e) * P * 4, 0);
 }
 
+// Waves of a block go to the four SIMDs in turn.  Column waves keep theirs to
+// themselves: of two and two others, the stagers are the seventh and eighth wave
+// and share the others' SIMDs, and the two between end at once.
+__host__ __device__ constexpr int first_stager(int C) { return C == 2 ? 6 : 2; }
+__host__ __device__ constexpr int chain_threads(int C) { return 64 * (first_stager(C) + C); }
+
 // Neighbouring blocks (slices of a head, heads of a group) on one XCD's L2.
 __device__ __forceinline__ uint32_t near_block(uint32_t bid, uint32_t n) {
   return n % 8 == 0 ? (bid & 7u) * (n >> 3) + (bid >> 3) : bid;

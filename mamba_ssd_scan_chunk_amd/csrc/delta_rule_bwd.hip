@@ -206,12 +206,12 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, DeltaWs
 }
 
 // ---------------------------------------------------------------- the same of bf16 inputs
-// C column waves and C helpers, as in the forward chain.  What the next piece
-// adds whatever D is, P^T dy to its values and q^T diag(e^G) dy to D, the helpers
-// work out a step ahead and leave in LDS as accumulators.
+// C column waves and C stagers, as in the forward chain, and C waves that work
+// out a step ahead what the next piece adds whatever D is, P^T dy to its values
+// and q^T diag(e^G) dy to D, and leave it in LDS as accumulators.
 template <int NP, int C>
 struct ReverseLds {
-  static constexpr int kPitch = NP + 8;
+  static constexpr int kPitch = NP + 24;  // rows as the products read them begin in different banks
   static constexpr int kRows = kC * kPitch * 2;
   static constexpr int kX = (NP / 16 + 4) * 1024;
   static constexpr int k = 0, r = k + kRows, g = r + kTriBytes, half = g + 5 * kC * 4;
@@ -219,7 +219,7 @@ struct ReverseLds {
 };
 
 template <int NP, int C, bool VL>
-__global__ __launch_bounds__(128 * C, C) void delta_reverse_bf16_kernel(DeltaArgs a, DeltaWs ws) {
+__global__ __launch_bounds__(chain_threads(C), C) void delta_reverse_bf16_kernel(DeltaArgs a, DeltaWs ws) {
   typedef DeltaB M;
   typedef DeltaB::One One;
   typedef DeltaB::Two Two;
@@ -238,20 +238,18 @@ __global__ __launch_bounds__(128 * C, C) void delta_reverse_bf16_kernel(DeltaArg
   Pieces pc;
   pc.last(VL ? reinterpret_cast<const Cuts*>(a.ws + ws.cuts) + b * ws.nw : nullptr, ws.nw, a.L);
 
-  if (wave >= C) {
-    // ---- helper
-    const int ht = tid - NH;
+  auto gates = [&](const Pieces& s) {
+    return reinterpret_cast<const DeltaGates*>(a.ws + ws.gates) + bh * ws.nw + s.win;
+  };
+  if (wave >= first_stager(C)) {
+    // ---- stager.  Step j: piece j + 1 for the column waves, q of piece j + 2
+    const int ht = tid - 64 * first_stager(C);
     RowTile<NP, NH> kt, qt;
     TriTile<NH> rt;
     GateTile<NH> gt;
-    Column dy;
-    f32x4_t qin[4];
-    const uint32_t krow = (uint32_t)a.rows.k, qrow = (uint32_t)a.rows.q, yrow = (uint32_t)(a.H * a.P);
+    const uint32_t krow = (uint32_t)a.rows.k, qrow = (uint32_t)a.rows.q;
     const uint16_t* kb = static_cast<const uint16_t*>(a.k) + row * a.rows.k + grp * N;
     const uint16_t* qb = static_cast<const uint16_t*>(a.q) + row * a.rows.q + grp * N;
-    auto gates = [&](const Pieces& s) {
-      return reinterpret_cast<const DeltaGates*>(a.ws + ws.gates) + bh * ws.nw + s.win;
-    };
     auto ask = [&](const Pieces& s) {
       kt.load(kb + s.win * kC * a.rows.k, krow, N, s.n, ht);
       rt.load(a.ws + ws.up_r + (bh * ws.nw + s.win) * kTriBytes, ht);
@@ -267,20 +265,80 @@ __global__ __launch_bounds__(128 * C, C) void delta_reverse_bf16_kernel(DeltaArg
     auto put_q = [&](const Pieces& s, int half) {
       qt.template store<VL>(reinterpret_cast<uint16_t*>(lds + Lay::q + half * Lay::kRows), LP, s.begin, s.end, ht);
     };
-    auto ask_dy = [&](const Pieces& s) {
+    ask(pc);
+    ask_q(pc);
+    put(pc, 0);
+    put_q(pc, 0);
+    Pieces n1 = pc;  // whose k, R and gates are under way
+    n1.step_back();
+    Pieces n2 = n1;  // whose q is
+    if (n1.valid_back()) {
+      ask_q(n1);
+      ask(n1);
+      n2.step_back();
+    }
+    __syncthreads();
+    if (n1.valid_back()) put_q(n1, 1);
+    if (n1.valid_back() && n2.valid_back()) ask_q(n2);
+    __syncthreads();
+    for (int j = 0; pc.valid_back(); ++j) {
+      if (n1.valid_back()) put(n1, (j + 1) & 1);
+      if (n2.valid_back()) put_q(n2, j & 1);
+      pc = n1;
+      n1 = n2;
+      if (n2.valid_back()) {
+        ask(n1);
+        n2.step_back();
+        if (n2.valid_back()) ask_q(n2);
+      }
+      __syncthreads();
+    }
+    return;
+  }
+  if (wave >= 2 * C) return;
+  if (wave >= C) {
+    // ---- a step ahead of the column waves: pc is the piece worked out
+    const uint32_t yrow = (uint32_t)(a.H * a.P);
+    Column dy;
+    f32x4_t qin[4];
+    Two pf[kTriFrags];
+    auto ask = [&](const Pieces& s) {
       dy.load(static_cast<const uint16_t*>(a.dy) + ((row + s.win * kC) * a.H + h) * a.P, yrow, 4 * g * yrow + p, s.n);
 #pragma unroll
       for (int i = 0; i < 4; ++i) qin[i] = *reinterpret_cast<const f32x4_t*>(gates(s)->qin + 16 * i + 4 * g);
     };
-    // P^T dy and q^T diag(e^G) dy of piece s, whose q is in LDS
-    auto work = [&](const Pieces& s, int half) {
+    auto ask_p = [&](const Pieces& s) {
       const char* fp = a.ws + ws.up_p + (bh * ws.nw + s.win) * kTriBytes;
-      Two pf[kTriFrags];
 #pragma unroll
       for (int f = 0; f < kTriFrags; ++f) pf[f] = M::load(fp + f * 2048, lane);
+    };
+    ask(pc);
+    ask_p(pc);
+    __syncthreads();
+    for (int half = 0;; half ^= 1) {
       const uint16_t* ql = reinterpret_cast<const uint16_t*>(lds + Lay::q + half * Lay::kRows);
       char* x = lds + Lay::x + (half * C + wave % C) * Lay::kX;
-      One yb[2];
+      One yb[2], qT[2][NT];
+      Two wb[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        float v[8], w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int i = 2 * t + e / 4, r = e % 4, tok = 16 * i + 4 * g + r;
+          const bool on = !VL || (tok >= pc.begin && tok < pc.end);
+          v[e] = on ? dy.get(i, r) : 0.f;
+          w[e] = on ? qin[i][r] * v[e] : 0.f;
+        }
+        yb[t] = M::one(v);
+        wb[t] = M::two(w);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) qT[t][j] = M::transposed(ql + 32 * t * LP + 16 * j, LP, lane);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      Pieces nx = pc;
+      nx.step_back();
+      if (nx.valid_back()) ask(nx);
       f32x4_t Y[NT], py[4];
 #pragma unroll
       for (int j = 0; j < NT; ++j) Y[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -288,23 +346,10 @@ __global__ __launch_bounds__(128 * C, C) void delta_reverse_bf16_kernel(DeltaArg
       for (int i = 0; i < 4; ++i) py[i] = Y[0];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        One qT[NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) qT[j] = M::transposed(ql + 32 * t * LP + 16 * j, LP, lane);
-        float v[8], w[8];
+        for (int j = 0; j < NT; ++j) Y[j] = M::mma(qT[t][j], wb[t].lo, Y[j]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int i = 2 * t + e / 4, r = e % 4, tok = 16 * i + 4 * g + r;
-          const bool on = !VL || (tok >= s.begin && tok < s.end);
-          v[e] = on ? dy.get(i, r) : 0.f;
-          w[e] = on ? qin[i][r] * v[e] : 0.f;
-        }
-        yb[t] = M::one(v);
-        const Two wb = M::two(w);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) Y[j] = M::mma(qT[j], wb.lo, Y[j]);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) Y[j] = M::mma(qT[j], wb.hi, Y[j]);
+        for (int j = 0; j < NT; ++j) Y[j] = M::mma(qT[t][j], wb[t].hi, Y[j]);
       }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -317,46 +362,17 @@ __global__ __launch_bounds__(128 * C, C) void delta_reverse_bf16_kernel(DeltaArg
       for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4_t*>(x + i * 1024 + 16 * lane) = py[i];
 #pragma unroll
       for (int j = 0; j < NT; ++j) *reinterpret_cast<f32x4_t*>(x + (4 + j) * 1024 + 16 * lane) = Y[j];
-    };
-    // before the first piece: its operands, q of it and of the next, its products
-    Pieces n1 = pc;
-    n1.step_back();
-    ask(pc);
-    ask_q(pc);
-    ask_dy(pc);
-    put(pc, 0);
-    put_q(pc, 0);
-    if (n1.valid_back()) ask_q(n1);
-    __syncthreads();
-    work(pc, 0);
-    if (n1.valid_back()) {
-      put_q(n1, 1);
-      ask_dy(n1);
-    }
-    __syncthreads();
-    for (int j = 0;; ++j) {
-      // pc: piece j, which the column waves take now; n1: the next
-      if (!n1.valid_back()) {
-        __syncthreads();
-        break;
-      }
-      Pieces n2 = n1;
-      n2.step_back();
-      ask(n1);
-      if (n2.valid_back()) ask_q(n2);
-      work(n1, (j + 1) & 1);
-      put(n1, (j + 1) & 1);
-      if (n2.valid_back()) {
-        put_q(n2, j & 1);
-        ask_dy(n2);
-      }
-      n1 = n2;
+      if (nx.valid_back()) ask_p(nx);
+      pc = nx;
       __syncthreads();
+      if (!pc.valid_back()) break;
     }
+    __syncthreads();  // the column waves' last step
     return;
   }
 
   // ---- column wave
+  __builtin_amdgcn_s_setprio(3);
   f32x4_t D[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j)
@@ -1078,7 +1094,7 @@ static hipError_t reverse_bf16(const DeltaArgs& a, const DeltaWs& ws, hipStream_
   const size_t lds = ReverseLds<NP, C>::total;
   hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * a.H * (a.P / 16 / C))), dim3(128 * C), lds, s, a, ws);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * a.H * (a.P / 16 / C))), dim3(chain_threads(C)), lds, s, a, ws);
   return hipGetLastError();
 }
 template <class M, int NP, bool VL>
