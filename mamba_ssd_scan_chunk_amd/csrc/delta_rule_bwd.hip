@@ -21,6 +21,8 @@
 // delta_grad_kernel, a block a (window, head), all windows at once; and
 // delta_finish_kernel, which adds the heads of a key group and takes the
 // gradients through the unit length.
+#include <type_traits>
+
 #include "delta_rule.hpp"
 
 namespace ssd {
@@ -550,10 +552,12 @@ template <> struct GradTile<DeltaF> {
     return DeltaF::global8(p + 2 * kPlane + t * kPitch + col);
   }
 };
+// The token-by-token matrices as left operands: M1 lower, M2 upper triangular, M3 whole.
+constexpr int kGradFrags = 2 * kTriFrags + 8;
 template <class M, int WV>
 constexpr size_t grad_lds() {
   const size_t tile = GradTile<M>::bytes(), tri = (size_t)3 * kC * kTP * 4;
-  return (tile > tri ? tile : tri) + kC * 8 + (size_t)(7 + 3 * WV + 2 + 1) * kC * 4 + 16 * 4;
+  return (tile > tri ? tile : tri) + kGradFrags * 2048 + kC * 8 + (size_t)(7 + 3 * WV + 2 + 1) * kC * 4 + 16 * 4;
 }
 
 // Sum over the 16 lanes of a group, in every lane.
@@ -580,7 +584,8 @@ __global__ __launch_bounds__(64 * WV, 2) void delta_grad_kernel(DeltaArgs a, Del
   float(*M1)[kTP] = reinterpret_cast<float(*)[kTP]>(lds);
   float(*M2)[kTP] = M1 + kC;
   float(*M3)[kTP] = M2 + kC;
-  double* sG = reinterpret_cast<double*>(lds + kBig);
+  char* frags = lds + kBig;
+  double* sG = reinterpret_cast<double*>(frags + kGradFrags * 2048);
   float* gt = reinterpret_cast<float*>(sG + kC);
   const float *sBeta = gt, *sKout = gt + 3 * kC, *sIn = gt + 4 * kC, *sRk = gt + 5 * kC, *sRq = gt + 6 * kC;
   float(*rowS)[kC] = reinterpret_cast<float(*)[kC]>(gt + 7 * kC);  // by wave
@@ -622,9 +627,9 @@ __global__ __launch_bounds__(64 * WV, 2) void delta_grad_kernel(DeltaArgs a, Del
   float sumA = 0.f, sumB = 0.f;  // of dA and ddt_bias, in wave 0
   const f32x4_t zero4 = {0.f, 0.f, 0.f, 0.f};
 
-  int begin = 0;
-  while (begin < n) {
-    const int end = VL ? piece_end(cuts.piece, begin, n) : n;
+  // PARTS: a piece of a window of several
+  auto piece = [&](auto parts, const int begin, const int end) {
+    constexpr bool PARTS = decltype(parts)::value;
     // only a row's first piece begins with a state, only its last one hands one on
     const bool first = begin == 0, last = end == n;
     const __amdgpu_buffer_rsrc_t Sr = rows_of(wsS, first ? N * P * 4 : 0), Dr = rows_of(wsD, last ? N * P * 4 : 0);
@@ -665,7 +670,7 @@ __global__ __launch_bounds__(64 * WV, 2) void delta_grad_kernel(DeltaArgs a, Del
       __syncthreads();
       {
         const int t = tid / WV, col = tid % WV * kCols;
-        const bool on = !VL || (t >= begin && t < end);
+        const bool on = !PARTS || (t >= begin && t < end);
         const float beta = sBeta[t];
 #pragma unroll
         for (int e = 0; e < kCols / 8; ++e) {
@@ -680,7 +685,7 @@ __global__ __launch_bounds__(64 * WV, 2) void delta_grad_kernel(DeltaArgs a, Del
               const uint32_t two = __float_as_uint(dy[e][k / 2]);
               yv[k] = __uint_as_float(k % 2 ? two & 0xffff0000u : two << 16);
             }
-            if constexpr (VL) {
+            if constexpr (PARTS) {
               wv[k] = on ? wv[k] : 0.f;
               uv[k] = on ? uv[k] : 0.f;
               yv[k] = on ? yv[k] : 0.f;
@@ -688,7 +693,7 @@ __global__ __launch_bounds__(64 * WV, 2) void delta_grad_kernel(DeltaArgs a, Del
             db = fmaf(wv[k], uv[k], db);
             wv[k] *= beta;
             uv[k] *= beta;
-            if constexpr (VL) {  // another piece's b may be NaN
+            if constexpr (PARTS) {  // another piece's b may be NaN
               wv[k] = on ? wv[k] : 0.f;
               uv[k] = on ? uv[k] : 0.f;
             }
@@ -845,6 +850,24 @@ __global__ __launch_bounds__(64 * WV, 2) void delta_grad_kernel(DeltaArgs a, Del
       }
     }
     __syncthreads();
+    // the matrices as operands, each rounded by one wave
+    for (int f = wave; f < kGradFrags; f += WV) {
+      const bool up = f >= kTriFrags && f < 2 * kTriFrags;
+      float v[8];
+      if (up) {  // columns 16 i .. of M2, rows 32 s ..
+        const int u = f - kTriFrags, i = u < 4 ? u / 2 : u - 2, s = u < 4 ? u % 2 : 1;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = M2[32 * s + 16 * (e / 4) + 4 * g + e % 4][16 * i + c];
+      } else {  // rows 16 i .. of M1 or M3, columns 32 s ..
+        const int l = f - 2 * kTriFrags;
+        const bool m3 = l >= 0;
+        const int i = m3 ? l / 2 : f < 2 ? f : 2 + (f - 2) / 2, s = m3 ? l % 2 : f < 2 ? 0 : (f - 2) % 2;
+        const float* q = m3 ? &M3[16 * i + c][32 * s + 4 * g] : &M1[16 * i + c][32 * s + 4 * g];
+        load_vec<IoF32, 4>(q, v);
+        load_vec<IoF32, 4>(q + 16, v + 4);
+      }
+      M::store(frags + f * 2048, lane, M::two(v));
+    }
     // dq and dk of the wave's columns
     One kb[NTW][2], qb[NTW][2];
 #pragma unroll
@@ -858,11 +881,11 @@ __global__ __launch_bounds__(64 * WV, 2) void delta_grad_kernel(DeltaArgs a, Del
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         rs[r] = cd[r] = 0.f;
-        const bool on = !VL || (t + r >= begin && t + r < end);
+        const bool on = !PARTS || (t + r >= begin && t + r < end);
         const float rest = ko[r] / rk[r];
 #pragma unroll
         for (int m = 0; m < NTW; ++m) {
-          if (VL && !on) kv[m][4 * i + r] = qv[m][4 * i + r] = 0;
+          if (PARTS && !on) kv[m][4 * i + r] = qv[m][4 * i + r] = 0;
           const float k = input(kv[m][4 * i + r]), q = input(qv[m][4 * i + r]);
           const float x = in[r] * qS[m][i][r], y = in[r] * wS[m][i][r], z = uD[m][i][r];
           rs[r] += (rq[r] * q) * x - (rk[r] * k) * y;
@@ -893,29 +916,22 @@ __global__ __launch_bounds__(64 * WV, 2) void delta_grad_kernel(DeltaArgs a, Del
         kb[m][s] = M::one(x);
         qb[m][s] = M::one(y);
       }
+    __syncthreads();
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float v[8];
-        auto row8 = [&](float(*q)[kTP]) {
-          load_vec<IoF32, 4>(&q[16 * i + c][32 * s + 4 * g], v);
-          load_vec<IoF32, 4>(&q[16 * i + c][32 * s + 16 + 4 * g], v + 4);
-          return M::two(v);
-        };
-        if (2 * s <= i) {  // rows 16 i .. of M1, columns 32 s ..
-          const Two f = row8(M1);
+        if (2 * s <= i) {
+          const Two f = M::load(frags + low_frag(i, s) * 2048, lane);
 #pragma unroll
           for (int m = 0; m < NTW; ++m) qS[m][i] = M::mma(f, kb[m][s], qS[m][i]);
         }
-        if (i < 2 * s + 2) {  // columns 16 i .. of M2, rows 32 s ..
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = M2[32 * s + 16 * (e / 4) + 4 * g + e % 4][16 * i + c];
-          const Two f = M::two(v);
+        if (i < 2 * s + 2) {
+          const Two f = M::load(frags + (kTriFrags + up_frag(i, s)) * 2048, lane);
 #pragma unroll
           for (int m = 0; m < NTW; ++m) wS[m][i] = M::mma(f, qb[m][s], wS[m][i]);
         }
-        const Two f = row8(M3);
+        const Two f = M::load(frags + (2 * kTriFrags + 2 * i + s) * 2048, lane);
 #pragma unroll
         for (int m = 0; m < NTW; ++m) wS[m][i] = M::mma(f, kb[m][s], wS[m][i]);
       }
@@ -927,7 +943,7 @@ __global__ __launch_bounds__(64 * WV, 2) void delta_grad_kernel(DeltaArgs a, Del
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const int t = (int)Column::row(e) + 4 * g;
-        const bool on = (int)nn < N && (!VL || (t >= begin && t < end));
+        const bool on = (int)nn < N && (!PARTS || (t >= begin && t < end));
         const uint32_t off = on ? (4 * g * N + nn) * 4 : kNowhere;
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(qS[m][e / 4][e % 4]), dqr, off, Column::row(e) * N * 4, 0);
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(wS[m][e / 4][e % 4]), dkr, off, Column::row(e) * N * 4, 0);
@@ -983,7 +999,14 @@ __global__ __launch_bounds__(64 * WV, 2) void delta_grad_kernel(DeltaArgs a, Del
       sumA += pa;
       sumB += pb;
     }
-    begin = end;
+  };
+  if (!VL || cuts.piece == 0) {
+    piece(std::false_type(), 0, n);
+  } else {
+    for (int begin = 0, end; begin < n; begin = end) {
+      end = piece_end(cuts.piece, begin, n);
+      piece(std::true_type(), begin, end);
+    }
   }
   if (tid == 0) {
     float* part = reinterpret_cast<float*>(a.ws + ws.part) + 2 * ((b * ws.nw + win) * a.H + h);
