@@ -15,7 +15,7 @@ from .ops import _DT, _F32, _IO, _on_stream, _opt, _ptr, _req, _req_rows, _seq_s
 def _here(t: torch.Tensor) -> None:
     """A call runs on the current device's stream: its tensors are there."""
     i = getattr(t.device, "index", None)
-    if i is not None and i != torch.cuda.current_device():
+    if isinstance(i, int) and i != torch.cuda.current_device():
         raise ValueError(f"tensors are on {t.device}, the current device is {torch.cuda.current_device()}")
 
 
