@@ -19,9 +19,11 @@ ssd_status check_delta(const ssd_delta_shape* s, bool step) {
   if (s->nheads % s->ngroups != 0) return SSD_ERR_SHAPE;
   if (s->dstate % 16 != 0 || s->headdim % 16 != 0 || s->dstate > ssd::kDeltaMaxDim || s->headdim > ssd::kDeltaMaxDim)
     return SSD_ERR_UNSUPPORTED;
-  // blocks of up to 512 threads, one a (row, window, head), in one dimension of a launch; of 64 a (row, head, 16 columns)
+  // a launch holds fewer than 2^32 threads in a dimension (one that asks for more runs the rest and reports
+  // success): up to 512 a (row, window, head), 64 a (row, head, 16 columns), 512 a (row, head, 32 columns)
   SSD_TRY(product({s->batch, s->nheads, (s->seqlen - 1) / ssd::kDeltaC + 1}, (int64_t(1) << 23) - 1));
   SSD_TRY(product({s->batch, s->nheads}, (int64_t(1) << 22) - 1));
+  SSD_TRY(product({s->batch, s->nheads, s->headdim}, (int64_t(1) << 28) - 1));
   if (s->nheads * s->headdim >= int64_t(1) << 23) return SSD_ERR_UNSUPPORTED;
   return product({s->batch, s->seqlen, s->nheads, s->headdim}, kMaxElems);
 }

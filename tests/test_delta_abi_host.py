@@ -53,6 +53,8 @@ def step(lib, s=None, rows=None, st=F, so=F, y=F, **kw):
     (dict(headdim=8), UNSUP), (dict(dstate=272), UNSUP), (dict(headdim=512), UNSUP),
     (dict(batch=1 << 20, nheads=4), UNSUP), (dict(batch=1 << 10, seqlen=1 << 20), UNSUP),
     (dict(nheads=1 << 17, ngroups=1), UNSUP),
+    # 2^20 heads of rows of 256 values: 2^32 threads of 512 a 32 values
+    (dict(batch=1 << 18, nheads=4, headdim=256), UNSUP),
     (dict(batch=(1 << 63) - 1, seqlen=(1 << 63) - 1, nheads=(1 << 63) - 1, ngroups=1), UNSUP),
 ])
 def test_delta_shapes(lib, kw, code):
