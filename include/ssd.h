@@ -540,7 +540,10 @@ size_t ssd_layer_norm_backward_workspace_bytes(int64_t rows, int64_t dim);
  * [B,H,N,P], seq_states [nseq,H,N,P] fp32, optional.  N (dstate) and P
  * (headdim) multiples of 16 up to 256, B H < 2^22, B H P < 2^28, B H ceil(L/64) < 2^23,
  * H P and row strides < 2^23 (else SSD_ERR_UNSUPPORTED).  q and k of prompts are 16-byte aligned with row
- * strides in whole 16 bytes.  final_states may be initial_states.
+ * strides in whole 16 bytes.  final_states may be initial_states.  A token with a
+ * NaN or infinity makes NaN of its sequence from its window of 64 tokens on, the
+ * window's earlier tokens included; other sequences stay as they are (a padded
+ * tail that may hold any bits: a sequence of its own).
  *
  * Precision: fp32 inputs use fp32 matrix instructions.  bf16 inputs enter the
  * products as they are; computed operands (states, u, the triangular matrices

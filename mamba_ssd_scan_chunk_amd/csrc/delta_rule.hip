@@ -849,7 +849,9 @@ __global__ __launch_bounds__(MODE == kOut ? chain_threads(C) : 128 * C, C) void 
   }
 }
 
-// The states that enter the stretches of a row: S' = M S + R, one wave 16 columns.
+// The states that enter the stretches of a row: S' = M S + R, one wave 16
+// columns.  Where a sequence begins in the stretch it is R alone, and M is not
+// multiplied: its zeros would make NaN of what the sequence before left.
 template <int NP>
 __global__ __launch_bounds__(64) void delta_enter_kernel(DeltaArgs a, DeltaWs ws) {
   typedef DeltaB M;
@@ -869,6 +871,13 @@ __global__ __launch_bounds__(64) void delta_enter_kernel(DeltaArgs a, DeltaWs ws
   for (int64_t seg = 0;; ++seg) {
     put_state<NT>(reinterpret_cast<float*>(a.ws + ws.enter) + (bh * ws.segs + seg) * N * P, N, P, 4 * g * P + p, S);
     if (seg == ws.segs - 1) break;
+    bool begins = false;
+    if (a.seq_idx) {
+      const Cuts* list = reinterpret_cast<const Cuts*>(a.ws + ws.cuts) + bh / a.H * ws.nw;
+      const int64_t to = min((seg + 1) * ws.seg_wins, ws.nw);
+      for (int64_t w = seg * ws.seg_wins + lane; w < to; w += 64) begins |= list[w].fresh != 0;
+      begins = __ballot(begins) != 0;
+    }
     const float* m = reinterpret_cast<const float*>(a.ws + ws.trans) + (bh * (ws.segs - 1) + seg) * N * cols;
     const __amdgpu_buffer_rsrc_t r = rows_of(m, (uint32_t)N * cols * 4);
     M::Two sb[KS];
@@ -883,6 +892,7 @@ __global__ __launch_bounds__(64) void delta_enter_kernel(DeltaArgs a, DeltaWs ws
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         S[j][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (4 * g * cols + N + p) * 4, (16 * j + e) * cols * 4, 0));
+    if (begins) continue;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       f32x4_t x[KS][2];

@@ -314,3 +314,24 @@ def test_long_rows_of_few_heads(shape, starts):
     check(got[1], wf, BF, "final")
     for s, i in enumerate(last):
         check(got[2][s], asked[i], BF, f"state after {i}")
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_nan_stays_in_its_sequence_across_stretches(bad):
+    """What a stretch hands on ends with its sequence, whatever it is."""
+    a = ref.inputs(1, 1500, 2, 1, 64, 32, dtype=BF, seed=3)
+    idx = torch.zeros((1, 1500), dtype=torch.int32)
+    idx[:, 300:] = 1
+    idx[:, 1280:] = 2
+    clean = call(a, seq_idx=idx.cuda())
+    for at, safe in ((100, slice(300, 1500)), (400, slice(1280, 1500))):
+        d = dict(a, v=a["v"].clone())
+        d["v"][:, at] = bad
+        y, fin = call(d, seq_idx=idx.cuda())
+        assert torch.equal(y[:, safe], clean[0][:, safe]) and torch.equal(fin, clean[1])
+        # of its own sequence, the windows of 64 tokens in front
+        assert torch.equal(y[:, :at // 64 * 64], clean[0][:, :at // 64 * 64])
+    d = dict(a, h0=a["h0"].clone())
+    d["h0"][:] = bad
+    y, fin = call(d, seq_idx=idx.cuda())
+    assert torch.equal(y[:, 300:], clean[0][:, 300:]) and torch.equal(fin, clean[1])
