@@ -330,7 +330,7 @@ template <class M, int NP, bool VL, bool SAVE>
 __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs ws) {
   typedef typename M::IO::type T;
   typedef typename M::Two Two;
-  constexpr int NT = NP / 16, KS = NP / 32, LP = chain_pitch<M, NP>(), V = M::IO::kVec;
+  constexpr int NT = NP / 16, KS = NP / 32, LP = chain_pitch<M, NP>();
   extern __shared__ __align__(16) char lds[];
   T* kt = reinterpret_cast<T*>(lds);
   T* qt = kt + (SAVE ? 0 : kC * LP);
@@ -338,11 +338,12 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs w
   const float *sBeta = gt, *sKin = gt + kC, *sQin = gt + 2 * kC, *sKout = gt + 3 * kC, *sIn = gt + 4 * kC;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int nthr = blockDim.x, c = lane & 15, g = lane >> 4;
+  const int w = chain_columns(a.P), c = lane & 15, g = lane >> 4;
+  const bool column = wave < w;
   const uint32_t bid = near_block(blockIdx.x, gridDim.x);
-  const uint32_t slices = (uint32_t)(a.P / 16) / (nthr / 64);
+  const uint32_t slices = (uint32_t)(a.P / 16) / w;
   const int64_t bh = bid / slices, h = bh % a.H, b = bh / a.H, grp = h / (a.H / a.G);
-  const int64_t p = ((bid % slices) * (nthr / 64) + wave) * 16 + c;
+  const int64_t p = ((bid % slices) * w + wave) * 16 + c;
   const int N = (int)a.N;
   const int64_t row = b * a.L;
   const uint8_t* marks = !SAVE && a.nseq > 0 ? reinterpret_cast<const uint8_t*>(a.ws + ws.marks) : nullptr;
@@ -353,7 +354,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs w
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int nn = 16 * j + 4 * g + r;
-      S[j][r] = a.h0 && nn < N ? a.h0[(bh * N + nn) * a.P + p] : 0.f;
+      S[j][r] = a.h0 && column && nn < N ? a.h0[(bh * N + nn) * a.P + p] : 0.f;
     }
 
   for (int64_t win = 0; win < ws.nw; ++win) {
@@ -374,7 +375,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs w
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int nn = 16 * j + 4 * g + r;
-          if (nn < N) out[nn * a.P] = S[j][r];
+          if (column && nn < N) out[nn * a.P] = S[j][r];
         }
     }
     const char* fr = a.ws + ws.low_r + bhw * kTriBytes;
@@ -386,21 +387,29 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs w
 #pragma unroll
         for (int j = 0; j < NT; ++j) S[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       }
-      // rows of other pieces are zero
-      __syncthreads();
-      for (int i = tid; i < kC * (NP / V); i += nthr) {
-        const int t = i / (NP / V), col = i % (NP / V) * V;
-        uint4 kv = make_uint4(0, 0, 0, 0), qv = kv;
-        if (t >= begin && t < end && col < N) {
-          kv = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.k) + (row + t0 + t) * a.rows.k + grp * N + col);
-          if (!SAVE)
-            qv = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (row + t0 + t) * a.rows.q + grp * N + col);
-        }
-        *reinterpret_cast<uint4*>(kt + t * LP + col) = kv;
-        if (!SAVE) *reinterpret_cast<uint4*>(qt + t * LP + col) = qv;
+      const T* kb = static_cast<const T*>(a.k) + (row + t0) * a.rows.k + grp * N;
+      const T* qb = static_cast<const T*>(a.q) + (row + t0) * a.rows.q + grp * N;
+      if (!column) {
+        const float* gates = reinterpret_cast<const float*>(reinterpret_cast<const DeltaGates*>(a.ws + ws.gates) + bhw);
+        const int st = tid - 64 * w, sn = 256 - 64 * w;
+        Stager<M, NP, !SAVE> sg;
+        sg.load(kb, (uint32_t)a.rows.k, qb, (uint32_t)a.rows.q, gates, N, n, begin, end, st, sn);
+        __syncthreads();
+        sg.store(kt, qt, gt, LP, kb, (uint32_t)a.rows.k, qb, (uint32_t)a.rows.q, N, n, begin, end, st, sn);
+        __syncthreads();
+        begin = end;
+        continue;
       }
-      const float* gsrc = reinterpret_cast<const float*>(reinterpret_cast<const DeltaGates*>(a.ws + ws.gates) + bhw);
-      for (int i = tid; i < 5 * kC; i += nthr) gt[i] = i % kC >= begin && i % kC < end ? gsrc[i] : 0.f;
+      // asked for before the rows are there, where there are registers for it (above 128 it spills)
+      constexpr bool kEarly = NP < 256;
+      Two rf[kTriFrags];
+      uint32_t vq[16];
+#pragma unroll
+      for (int f = 0; f < kTriFrags; ++f)
+        if constexpr (kEarly) rf[f] = M::load(fr + f * 2048, lane);
+      load_column<typename M::IO>(static_cast<const T*>(a.v) + (row + t0) * a.rows.v + h * a.P, (uint32_t)a.rows.v, p, n,
+                                  begin, end, g, vq);
+      __syncthreads();
       __syncthreads();
 
       f32x4_t X[4], Q[4];
@@ -422,7 +431,6 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs w
         }
       }
       // X = v - e^G k S
-      const T* vp = static_cast<const T*>(a.v) + (row + t0) * a.rows.v + h * a.P + p;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float4 kin = *reinterpret_cast<const float4*>(sKin + 16 * i + 4 * g);
@@ -430,8 +438,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs w
         const float ki[4] = {kin.x, kin.y, kin.z, kin.w}, qi[4] = {qin.x, qin.y, qin.z, qin.w};
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int t = 16 * i + 4 * g + r;
-          const float v = t >= begin && t < end ? M::IO::get(vp[t * a.rows.v]) : 0.f;
+          const float v = column_value<typename M::IO>(vq[4 * i + r]);
           X[i][r] = v - ki[r] * X[i][r];
           Q[i][r] *= qi[r];
         }
@@ -454,7 +461,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs w
         slots(u[2 * s], u[2 * s + 1], v);
         const Two xb = M::two(v);
 #pragma unroll
-        for (int i = 2 * s; i < 4; ++i) X[i] = M::mma(M::load(fr + low_frag(i, s) * 2048, lane), xb, X[i]);
+        for (int i = 2 * s; i < 4; ++i) X[i] = M::mma(kEarly ? rf[low_frag(i, s)] : M::load(fr + low_frag(i, s) * 2048, lane), xb, X[i]);
       }
       if constexpr (SAVE) {
         float* out = reinterpret_cast<float*>(a.ws + ws.w) + bhw * kC * a.P + p;
@@ -515,7 +522,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs w
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
                 const int nn = 16 * j + 4 * g + r;
-                if (nn < N) out[nn * a.P] = S[j][r];
+                if (column && nn < N) out[nn * a.P] = S[j][r];
               }
           }
         }
@@ -529,7 +536,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs w
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int nn = 16 * j + 4 * g + r;
-        if (nn < N) a.hfin[(bh * N + nn) * a.P + p] = S[j][r];
+        if (column && nn < N) a.hfin[(bh * N + nn) * a.P + p] = S[j][r];
       }
   }
 }
@@ -1051,22 +1058,13 @@ hipError_t launch_delta_prepare(const DeltaArgs& a, const DeltaWs& ws, bool back
   return back ? prepare_at<DeltaF, true>(a, ws, s) : prepare_at<DeltaF, false>(a, ws, s);
 }
 
-// Enough blocks for every compute unit come before waves that share k and q.
-int delta_chain_waves(int64_t B, int64_t H, int64_t P) {
-  const int64_t waves = P / 16;
-  for (int w = 4; w > 1; w /= 2)
-    if (waves % w == 0 && B * H * (waves / w) >= device_cu_count()) return w;
-  return waves % 2 == 0 ? 2 : 1;
-}
-
 template <class M, int NP, bool VL, bool SAVE>
 static hipError_t chain(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) {
   auto kern = delta_chain_kernel<M, NP, VL, SAVE>;
   const size_t lds = chain_lds<M, NP, SAVE>();
   hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  const int w = delta_chain_waves(a.B, a.H, a.P);
-  hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * a.H * (a.P / 16 / w))), dim3(64 * w), lds, s, a, ws);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * a.H * (a.P / 16 / chain_columns(a.P)))), dim3(256), lds, s, a, ws);
   return hipGetLastError();
 }
 template <int NP, int C, bool VL, ChainMode MODE>

@@ -318,6 +318,91 @@ struct RowTile {
     }
   }
 };
+// The rows and gates of one piece for the general chains, brought by the waves
+// of a block that hold no columns: asked for while the others work on the piece
+// before, put when they are done.  Rows outside [begin, end) are zero.
+template <class M, int NP, bool Q>
+struct Stager {
+  typedef typename M::IO::type T;
+  static constexpr int V = M::IO::kVec, kPer = NP / V, es = 16 / V;
+  static constexpr int kEach = kC * kPer / 128;    // of one tile, for the least number of threads
+  static constexpr bool kAhead = NP < 256;          // else eight at a time when they are put, which spills less
+  u32x4v k[kAhead ? kEach : 1], q[kAhead && Q ? kEach : 1];
+  float gate[3];
+
+  static __device__ __forceinline__ u32x4v ask(__amdgpu_buffer_rsrc_t r, int i, uint32_t stride, int N, int begin, int end) {
+    const int t = i / kPer, col = i % kPer * V;
+    const bool on = t >= begin && t < end && col < N;
+    return __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(r, on ? (t * stride + col) * es : kNowhere, 0, 0));
+  }
+  static __device__ __forceinline__ void put(T* tile, int pitch, int i, u32x4v v) {
+    if (i < kC * kPer) *reinterpret_cast<u32x4v*>(tile + i / kPer * pitch + i % kPer * V) = v;
+  }
+  static __device__ __forceinline__ void all(T* tile, int pitch, const T* base, uint32_t stride, int N, int n, int begin,
+                                             int end, int tid, int nthr) {
+    const __amdgpu_buffer_rsrc_t r = rows_of(base, (uint32_t)n * stride * es);
+    for (int i0 = tid; i0 < kC * kPer; i0 += 8 * nthr) {
+      u32x4v v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = ask(r, i0 + e * nthr, stride, N, begin, end);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) put(tile, pitch, i0 + e * nthr, v[e]);
+    }
+  }
+  __device__ __forceinline__ void load(const T* kb, uint32_t ks, const T* qb, uint32_t qs, const float* gates, int N, int n,
+                                       int begin, int end, int tid, int nthr) {
+#pragma unroll
+    for (int e = 0; e < 3; ++e) {
+      const int i = tid + e * nthr;
+      gate[e] = i < 5 * kC && i % kC >= begin && i % kC < end ? gates[i] : 0.f;
+    }
+    if constexpr (kAhead) {
+      const __amdgpu_buffer_rsrc_t rk = rows_of(kb, (uint32_t)n * ks * es);
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) k[e] = ask(rk, tid + e * nthr, ks, N, begin, end);
+      if constexpr (Q) {
+        const __amdgpu_buffer_rsrc_t rq = rows_of(qb, (uint32_t)n * qs * es);
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) q[e] = ask(rq, tid + e * nthr, qs, N, begin, end);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* kt, T* qt, float* gt, int pitch, const T* kb, uint32_t ks, const T* qb, uint32_t qs,
+                                        int N, int n, int begin, int end, int tid, int nthr) {
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+      if (tid + e * nthr < 5 * kC) gt[tid + e * nthr] = gate[e];
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) put(kt, pitch, tid + e * nthr, k[e]);
+      if constexpr (Q) {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) put(qt, pitch, tid + e * nthr, q[e]);
+      }
+    } else {
+      all(kt, pitch, kb, ks, N, n, begin, end, tid, nthr);
+      if constexpr (Q) all(qt, pitch, qb, qs, N, n, begin, end, tid, nthr);
+    }
+  }
+};
+// A lane's 16 tokens of one column of any type, zero outside [begin, end).
+template <class IO>
+__device__ __forceinline__ void load_column(const typename IO::type* base, uint32_t stride, uint32_t col, int n, int begin,
+                                            int end, int g, uint32_t* q) {
+  constexpr int es = sizeof(typename IO::type);
+  const __amdgpu_buffer_rsrc_t r = rows_of(base, (uint32_t)n * stride * es);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int t = 16 * (e / 4) + 4 * g + e % 4;
+    const uint32_t off = t >= begin && t < end ? (t * stride + col) * es : kNowhere;
+    if constexpr (es == 2) q[e] = __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+    else q[e] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+  }
+}
+template <class IO>
+__device__ __forceinline__ float column_value(uint32_t v) {
+  return sizeof(typename IO::type) == 2 ? bf16_bits_to_f32(v) : __uint_as_float(v);
+}
 // Five gates of 64 tokens, zero outside [begin, end) (behind the row's end they are zero as prepared).
 template <int NTHR>
 struct GateTile {
@@ -445,6 +530,7 @@ inline DeltaWs delta_ws(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P, b
 hipError_t launch_delta_prepare(const DeltaArgs& a, const DeltaWs& ws, bool back, bool bf16, hipStream_t s);
 hipError_t launch_delta_chain(const DeltaArgs& a, const DeltaWs& ws, bool save, bool bf16, hipStream_t s);
 // Waves of 16 value columns a block of the chains.
-int delta_chain_waves(int64_t B, int64_t H, int64_t P);
+// Column waves of a block of the general chains, of four waves; the others stage.
+__host__ __device__ inline int chain_columns(int64_t P) { return P / 16 % 2 == 0 ? 2 : 1; }
 
 }  // namespace ssd

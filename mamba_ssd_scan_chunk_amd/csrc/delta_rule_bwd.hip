@@ -41,7 +41,7 @@ template <class M, int NP, bool VL>
 __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, DeltaWs ws) {
   typedef typename M::IO::type T;
   typedef typename M::Two Two;
-  constexpr int NT = NP / 16, KS = NP / 32, LP = rev_pitch<M, NP>(), V = M::IO::kVec;
+  constexpr int NT = NP / 16, KS = NP / 32, LP = rev_pitch<M, NP>();
   extern __shared__ __align__(16) char lds[];
   T* kt = reinterpret_cast<T*>(lds);
   T* qt = kt + kC * LP;
@@ -49,11 +49,12 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, DeltaWs
   const float *sBeta = gt, *sKin = gt + kC, *sQin = gt + 2 * kC, *sKout = gt + 3 * kC, *sIn = gt + 4 * kC;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int nthr = blockDim.x, c = lane & 15, g = lane >> 4;
+  const int w = chain_columns(a.P), c = lane & 15, g = lane >> 4;
+  const bool column = wave < w;
   const uint32_t bid = near_block(blockIdx.x, gridDim.x);
-  const uint32_t slices = (uint32_t)(a.P / 16) / (nthr / 64);
+  const uint32_t slices = (uint32_t)(a.P / 16) / w;
   const int64_t bh = bid / slices, h = bh % a.H, b = bh / a.H, grp = h / (a.H / a.G);
-  const int64_t p = ((bid % slices) * (nthr / 64) + wave) * 16 + c;
+  const int64_t p = ((bid % slices) * w + wave) * 16 + c;
   const int N = (int)a.N;
   const int64_t row = b * a.L;
 
@@ -63,7 +64,7 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, DeltaWs
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int nn = 16 * j + 4 * g + r;
-      D[j][r] = a.dfinal && nn < N ? a.dfinal[(bh * N + nn) * a.P + p] : 0.f;
+      D[j][r] = a.dfinal && column && nn < N ? a.dfinal[(bh * N + nn) * a.P + p] : 0.f;
     }
 
   for (int64_t win = ws.nw - 1; win >= 0; --win) {
@@ -78,7 +79,7 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, DeltaWs
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int nn = 16 * j + 4 * g + r;
-          if (nn < N) out[nn * a.P] = D[j][r];
+          if (column && nn < N) out[nn * a.P] = D[j][r];
         }
     }
     const char* fr = a.ws + ws.up_r + bhw * kTriBytes;
@@ -86,29 +87,40 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, DeltaWs
     int end = n;
     while (end > 0) {
       const int begin = VL ? piece_begin(cuts.piece, end) : 0;
-      __syncthreads();
-      for (int i = tid; i < kC * (NP / V); i += nthr) {
-        const int t = i / (NP / V), col = i % (NP / V) * V;
-        uint4 kv = make_uint4(0, 0, 0, 0), qv = kv;
-        if (t >= begin && t < end && col < N) {
-          kv = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.k) + (row + t0 + t) * a.rows.k + grp * N + col);
-          qv = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (row + t0 + t) * a.rows.q + grp * N + col);
-        }
-        *reinterpret_cast<uint4*>(kt + t * LP + col) = kv;
-        *reinterpret_cast<uint4*>(qt + t * LP + col) = qv;
+      const T* kb = static_cast<const T*>(a.k) + (row + t0) * a.rows.k + grp * N;
+      const T* qb = static_cast<const T*>(a.q) + (row + t0) * a.rows.q + grp * N;
+      if (!column) {
+        const float* gates = reinterpret_cast<const float*>(reinterpret_cast<const DeltaGates*>(a.ws + ws.gates) + bhw);
+        const int st = tid - 64 * w, sn = 256 - 64 * w;
+        Stager<M, NP, true> sg;
+        sg.load(kb, (uint32_t)a.rows.k, qb, (uint32_t)a.rows.q, gates, N, n, begin, end, st, sn);
+        __syncthreads();
+        sg.store(kt, qt, gt, LP, kb, (uint32_t)a.rows.k, qb, (uint32_t)a.rows.q, N, n, begin, end, st, sn);
+        __syncthreads();
+        end = begin;
+        continue;
       }
-      const float* gsrc = reinterpret_cast<const float*>(reinterpret_cast<const DeltaGates*>(a.ws + ws.gates) + bhw);
-      for (int i = tid; i < 5 * kC; i += nthr) gt[i] = i % kC >= begin && i % kC < end ? gsrc[i] : 0.f;
+      // asked for before the rows are there, where there are registers for it (above 128 it spills)
+      constexpr bool kEarly = NP < 256;
+      Two rf[kTriFrags], pf[kTriFrags];
+      uint32_t yq[16];
+#pragma unroll
+      for (int f = 0; f < kTriFrags; ++f)
+        if constexpr (kEarly) {
+          rf[f] = M::load(fr + f * 2048, lane);
+          pf[f] = M::load(fp + f * 2048, lane);
+        }
+      load_column<typename M::IO>(static_cast<const T*>(a.dy) + ((row + t0) * a.H + h) * a.P, (uint32_t)(a.H * a.P), p, n,
+                                  begin, end, g, yq);
+      __syncthreads();
       __syncthreads();
 
       f32x4_t dy[4], du[4];
-      const T* yp = static_cast<const T*>(a.dy) + ((row + t0) * a.H + h) * a.P + p;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int t = 16 * i + 4 * g + r;
-          dy[i][r] = t >= begin && t < end ? M::IO::get(yp[t * a.H * a.P]) : 0.f;
+          dy[i][r] = column_value<typename M::IO>(yq[4 * i + r]);
           du[i][r] = 0.f;
         }
 #pragma unroll
@@ -137,7 +149,7 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, DeltaWs
         slots(dy[2 * s], dy[2 * s + 1], v);
         const typename M::One yb = M::one(v);
 #pragma unroll
-        for (int i = 0; i < 2 * s + 2; ++i) du[i] = M::mma(M::load(fp + up_frag(i, s) * 2048, lane), yb, du[i]);
+        for (int i = 0; i < 2 * s + 2; ++i) du[i] = M::mma(kEarly ? pf[up_frag(i, s)] : M::load(fp + up_frag(i, s) * 2048, lane), yb, du[i]);
       }
       // du += R^T (b du); the products read what was before them
       Two xb[2];
@@ -154,7 +166,7 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, DeltaWs
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int i = 0; i < 2 * s + 2; ++i) du[i] = M::mma(M::load(fr + up_frag(i, s) * 2048, lane), xb[s], du[i]);
+        for (int i = 0; i < 2 * s + 2; ++i) du[i] = M::mma(kEarly ? rf[up_frag(i, s)] : M::load(fr + up_frag(i, s) * 2048, lane), xb[s], du[i]);
       float* out = reinterpret_cast<float*>(a.ws + ws.du) + bhw * kC * a.P + p;
       T* dvp = static_cast<T*>(a.dv) + (row + t0) * a.grows.v + h * a.P + p;
       f32x4_t dw[4];
@@ -202,7 +214,7 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, DeltaWs
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int nn = 16 * j + 4 * g + r;
-        if (nn < N) a.dinit[(bh * N + nn) * a.P + p] = D[j][r];
+        if (column && nn < N) a.dinit[(bh * N + nn) * a.P + p] = D[j][r];
       }
   }
 }
@@ -1107,8 +1119,7 @@ static hipError_t reverse(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) 
   const size_t lds = rev_lds<M, NP>();
   hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  const int w = delta_chain_waves(a.B, a.H, a.P);
-  hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * a.H * (a.P / 16 / w))), dim3(64 * w), lds, s, a, ws);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(a.B * a.H * (a.P / 16 / chain_columns(a.P)))), dim3(256), lds, s, a, ws);
   return hipGetLastError();
 }
 template <int NP, int C, bool VL>
