@@ -856,67 +856,89 @@ __global__ __launch_bounds__(MODE == kOut ? chain_threads(C) : 128 * C, C) void 
   }
 }
 
-// The states that enter the stretches of a row: S' = M S + R, one wave 16
-// columns.  Where a sequence begins in the stretch it is R alone, and M is not
-// multiplied: its zeros would make NaN of what the sequence before left.
+// The states that enter the stretches of a row: S' = M S + R, a block 16 columns
+// and a wave 32 rows of them, so that the next stretch's map is asked for while
+// one is multiplied; the waves meet once a stretch, for S as operands.  Where a
+// sequence begins in the stretch it is R alone, and M is not multiplied: its
+// zeros would make NaN of what the sequence before left.
 template <int NP>
-__global__ __launch_bounds__(64) void delta_enter_kernel(DeltaArgs a, DeltaWs ws) {
+__global__ __launch_bounds__(2 * NP) void delta_enter_kernel(DeltaArgs a, DeltaWs ws) {
   typedef DeltaB M;
-  constexpr int NT = NP / 16, KS = NP / 32;
-  const int lane = threadIdx.x, c = lane & 15, g = lane >> 4, N = (int)a.N;
+  constexpr int KS = NP / 32;
+  __shared__ M::Two sS[2][KS][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4, N = (int)a.N;
   const uint32_t P = (uint32_t)a.P, cols = N + P, tiles = P / 16;
   const int64_t bh = blockIdx.x / tiles;
   const uint32_t p = blockIdx.x % tiles * 16 + c;
-  f32x4_t S[NT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int nn = 16 * j + 4 * g + r;
-      S[j][r] = a.h0 && nn < N ? a.h0[(bh * N + nn) * a.P + p] : 0.f;
-    }
-  for (int64_t seg = 0;; ++seg) {
-    put_state<NT>(reinterpret_cast<float*>(a.ws + ws.enter) + (bh * ws.segs + seg) * N * P, N, P, 4 * g * P + p, S);
-    if (seg == ws.segs - 1) break;
-    bool begins = false;
-    if (a.seq_idx) {
-      const Cuts* list = reinterpret_cast<const Cuts*>(a.ws + ws.cuts) + bh / a.H * ws.nw;
+  const Cuts* list = a.seq_idx ? reinterpret_cast<const Cuts*>(a.ws + ws.cuts) + bh / a.H * ws.nw : nullptr;
+  f32x4_t S[2], R[2], x[2][KS][2];
+  bool begins = false;
+  auto ask = [&](int64_t seg) {
+    if (list) {
+      bool any = false;
       const int64_t to = min((seg + 1) * ws.seg_wins, ws.nw);
-      for (int64_t w = seg * ws.seg_wins + lane; w < to; w += 64) begins |= list[w].fresh != 0;
-      begins = __ballot(begins) != 0;
+      for (int64_t w = seg * ws.seg_wins + lane; w < to; w += 64) any |= list[w].fresh != 0;
+      begins = __ballot(any) != 0;
     }
     const float* m = reinterpret_cast<const float*>(a.ws + ws.trans) + (bh * (ws.segs - 1) + seg) * N * cols;
     const __amdgpu_buffer_rsrc_t r = rows_of(m, (uint32_t)N * cols * 4);
-    M::Two sb[KS];
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      float v[8];
-      slots(S[2 * s], S[2 * s + 1], v);
-      sb[s] = M::two(v);
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t base = (32 * wave + 16 * i) * cols * 4;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        S[j][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (4 * g * cols + N + p) * 4, (16 * j + e) * cols * 4, 0));
-    if (begins) continue;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      f32x4_t x[KS][2];
+        R[i][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (4 * g * cols + N + p) * 4, base + e * cols * 4, 0));
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int col = 32 * s + 16 * t + 4 * g;
-          x[s][t] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                                    r, col < N ? (c * cols + col) * 4 : kNowhere, 16 * j * cols * 4, 0));
+          x[i][s][t] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                       r, col < N ? (c * cols + col) * 4 : kNowhere, base, 0));
         }
+    }
+  };
+  ask(0);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int nn = 32 * wave + 16 * i + 4 * g + r;
+      S[i][r] = a.h0 && nn < N ? a.h0[(bh * N + nn) * a.P + p] : 0.f;
+    }
+  for (int64_t seg = 0;; ++seg) {
+    float* out = reinterpret_cast<float*>(a.ws + ws.enter) + (bh * ws.segs + seg) * N * P;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int nn = 32 * wave + 16 * i + 4 * g + r;
+        if (nn < N) out[nn * P + p] = S[i][r];
+      }
+    if (seg == ws.segs - 1) break;
+    float v[8];
+    slots(S[0], S[1], v);
+    sS[seg & 1][wave][lane] = M::two(v);
+    M::Two map[2][KS];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      S[i] = R[i];
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        float v[8];
-        slots(x[s][0], x[s][1], v);
-        S[j] = M::mma(M::two(v), sb[s], S[j]);
+        slots(x[i][s][0], x[i][s][1], v);
+        map[i][s] = M::two(v);
       }
+    }
+    const bool only = begins;
+    if (seg + 1 < ws.segs - 1) ask(seg + 1);
+    __syncthreads();  // a wave writes the other half next, and meets the others before this one again
+    if (only) continue;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const M::Two sb = sS[seg & 1][s][lane];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) S[i] = M::mma(map[i][s], sb, S[i]);
     }
   }
 }
@@ -1089,7 +1111,7 @@ static hipError_t chain_bf16_of(const DeltaArgs& a, const DeltaWs& ws, bool save
   if (ws.segs > 1) {
     hipError_t e = chain_bf16_as<NP, VL, kStretch>(a, ws, s);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(delta_enter_kernel<NP>, dim3((unsigned)(a.B * a.H * (a.P / 16))), dim3(64), 0, s, a, ws);
+    hipLaunchKernelGGL(delta_enter_kernel<NP>, dim3((unsigned)(a.B * a.H * (a.P / 16))), dim3(2 * NP), 0, s, a, ws);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -1101,13 +1123,13 @@ static hipError_t chain_bf16_at(const DeltaArgs& a, const DeltaWs& ws, bool save
   return vl ? chain_bf16_of<NP, true>(a, ws, save, s) : chain_bf16_of<NP, false>(a, ws, save, s);
 }
 // Stretches of a row: as many as leave each compute unit a block (of 32 columns)
-// and each stretch four windows; from four on the second pass pays.  Only the
+// and each stretch eight windows; from four on the second pass pays.  Only the
 // bf16 chain of up to 128 key columns has them.
 int64_t delta_segments(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P, bool bf16) {
   if (!bf16 || N > 128) return 1;
   const int64_t nw = (L + kDeltaC - 1) / kDeltaC, blocks = B * H * (P % 32 == 0 ? P / 32 : P / 16);
   int64_t segs = device_cu_count() / blocks;
-  if (segs > nw / 4) segs = nw / 4;
+  if (segs > nw / 8) segs = nw / 8;
   if (segs < 4) return 1;
   return (nw + (nw + segs - 1) / segs - 1) / ((nw + segs - 1) / segs);  // none of them empty
 }

@@ -299,7 +299,8 @@ def test_gradients_into_column_slices(dtype):
     assert (wide[..., -3:] == 5).all() and (ab[..., -1:] == 5).all()
 
 
-@pytest.mark.parametrize("shape", [(1, 1500, 2, 1, 64, 32), (1, 2111, 1, 1, 48, 16), (2, 1030, 2, 2, 128, 128)])
+@pytest.mark.parametrize("shape", [(1, 1500, 2, 1, 64, 32), (1, 2111, 1, 1, 48, 16), (2, 1030, 2, 2, 128, 128),
+                                   (1, 4500, 2, 1, 64, 32), (2, 2100, 2, 2, 128, 128), (1, 3001, 3, 3, 32, 16)])
 @pytest.mark.parametrize("starts", [0, 6])
 def test_long_rows_of_few_heads(shape, starts):
     """Rows cut into stretches that are walked side by side."""
@@ -316,15 +317,16 @@ def test_long_rows_of_few_heads(shape, starts):
         check(got[2][s], asked[i], BF, f"state after {i}")
 
 
+@pytest.mark.parametrize("L", [1500, 3000])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-def test_nan_stays_in_its_sequence_across_stretches(bad):
+def test_nan_stays_in_its_sequence_across_stretches(bad, L):
     """What a stretch hands on ends with its sequence, whatever it is."""
-    a = ref.inputs(1, 1500, 2, 1, 64, 32, dtype=BF, seed=3)
-    idx = torch.zeros((1, 1500), dtype=torch.int32)
+    a = ref.inputs(1, L, 2, 1, 64, 32, dtype=BF, seed=3)
+    idx = torch.zeros((1, L), dtype=torch.int32)
     idx[:, 300:] = 1
     idx[:, 1280:] = 2
     clean = call(a, seq_idx=idx.cuda())
-    for at, safe in ((100, slice(300, 1500)), (400, slice(1280, 1500))):
+    for at, safe in ((100, slice(300, L)), (400, slice(1280, L))):
         d = dict(a, v=a["v"].clone())
         d["v"][:, at] = bad
         y, fin = call(d, seq_idx=idx.cuda())
