@@ -1,10 +1,11 @@
 // delta_rule.hip -- the gated delta rule: prompts and single tokens.  The
 // formulas and the operands' types are in delta_rule.hpp.
 //
-// A prompt takes two launches.  delta_prepare_kernel, one block a (window,
-// head), leaves what needs no state: the triangular operands R and P, laid out
-// as the chain's fragments, and the scalars of the rows.  delta_chain_kernel
-// walks the windows in order.  A wave owns 16 value columns of a head, whose
+// A prompt takes two launches (long rows of few heads four, see
+// delta_segments).  delta_prepare_kernel, one block a (window, head), leaves
+// what needs no state: the triangular operands R and P, laid out as the chain's
+// fragments, and the scalars of the rows.  The chain walks the windows in
+// order.  A column wave owns 16 value columns of a head, whose
 // state it holds in accumulators, and nothing passes between waves: every
 // product of the chain contracts over what are rows of the one before (state
 // rows, tokens), and an accumulator's rows are the contraction slots of the
@@ -40,7 +41,9 @@ __device__ __forceinline__ float times(float e, float b) { return e != 0.f ? e *
 // matrix instructions; R takes E's place in LDS.  Entries between pieces are
 // set, not multiplied, to zero, so that no value of one sequence meets
 // another's.  Bound by the latency of its few dependent parts: all of a
-// wave's loads (of 128 key columns) are asked for together.
+// wave's loads (of 128 key columns) are asked for together, and one matrix in
+// LDS leaves five blocks a compute unit.  2 x 8192 tokens of 32 heads, bf16, N =
+// 128: 117 us; for the gradients of 2 x 2048: 59; a lone block takes some 16.
 template <class M, int NP, bool BACK, bool VL>
 __global__ __launch_bounds__(256, 2) void delta_prepare_kernel(DeltaArgs a, DeltaWs ws) {
   typedef typename M::IO::type T;
@@ -325,7 +328,12 @@ constexpr size_t chain_lds() {
   return (size_t)(SAVE ? 1 : 2) * kC * chain_pitch<M, NP>() * sizeof(typename M::IO::type) + 5 * kC * 4;
 }
 
-// SAVE: for the gradients, the state in front of every window and w instead of y.
+// fp32 inputs, and bf16 ones of more than 128 key columns, whose state fills a
+// wave's registers.  Of four waves one or two hold columns, the others bring the
+// next piece's k, q and gates.  SAVE: for the gradients, the state in front of
+// every window and w instead of y.  Bound by the length of the chain, about 6 us a
+// window of fp32 (2 x 777 tokens, N = 48, P = 80: 76 us; 157 where every wave had
+// columns and staged for itself).
 template <class M, int NP, bool VL, bool SAVE>
 __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs ws) {
   typedef typename M::IO::type T;
@@ -547,6 +555,12 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs w
 // which is the chain's length; the stagers put the next piece's operands, asked
 // for a step before, into the other half of LDS; the output waves work out the
 // piece before, from the operands (state, u) that the column waves left in LDS.
+// Two column waves a block: with one, k and q are staged twice as often; four
+// leave half of the chip idle at 64 heads of 128 columns.  Bound by the column
+// waves' latency, 2.4 us a window of which their own products, roundings and LDS
+// reads take 1.75; the matrix units are busy 8 to 18%.  2 x 8192 tokens of 32
+// heads, N = P = 128: 300 us (one kernel of waves that stage for themselves 2370),
+// the whole call 1.0 TB/s of its bytes.
 template <int NP, int C>
 struct ChainLds {
   static constexpr int kPitch = NP + 24;  // rows as the products read them begin in different banks
@@ -860,7 +874,8 @@ __global__ __launch_bounds__(MODE == kOut ? chain_threads(C) : 128 * C, C) void 
 // and a wave 32 rows of them, so that the next stretch's map is asked for while
 // one is multiplied; the waves meet once a stretch, for S as operands.  Where a
 // sequence begins in the stretch it is R alone, and M is not multiplied: its
-// zeros would make NaN of what the sequence before left.
+// zeros would make NaN of what the sequence before left.  About 1 us a stretch;
+// one wave for all rows, which read each map only when its turn came, took 6.
 template <int NP>
 __global__ __launch_bounds__(2 * NP) void delta_enter_kernel(DeltaArgs a, DeltaWs ws) {
   typedef DeltaB M;
@@ -947,7 +962,8 @@ __global__ __launch_bounds__(2 * NP) void delta_enter_kernel(DeltaArgs a, DeltaW
 // A block takes 64 value columns of a (row, head): 16 threads of four columns
 // by 16 state rows, whose up to 16 rows a thread are all asked for first.
 // Bound by the state, read and written once: k^T h and q^T h are summed
-// together, for y = a q^T h + (q.k) u.
+// together, for y = a q^T h + (q.k) u.  64 streams of 32 heads, N = P = 128: 52 us
+// for 268 MB, 5.1 TB/s, the rate of a copy.
 constexpr int kStepCols = 64, kStepRows = (int)kDeltaMaxDim / 16;
 template <class IO>
 __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a, const float* state, float* state_out) {
@@ -1123,14 +1139,17 @@ static hipError_t chain_bf16_at(const DeltaArgs& a, const DeltaWs& ws, bool save
   return vl ? chain_bf16_of<NP, true>(a, ws, save, s) : chain_bf16_of<NP, false>(a, ws, save, s);
 }
 // Stretches of a row: as many as leave each compute unit a block (of 32 columns)
-// and each stretch eight windows; from four on the second pass pays.  Only the
-// bf16 chain of up to 128 key columns has them.
+// and each stretch eight windows; from three on the second pass pays.  Only the
+// bf16 chain of up to 128 key columns has them.  Calls of one row, N = P = 128,
+// without stretches and with them, us: 2048 tokens of 8 heads 75 and 59, 8192 of
+// 2 heads 254 and 87, of 20 heads (three stretches) 280 and 247; two stretches
+// take what one does.  Stretches of four windows: 1024 tokens of 8 heads 44 and 54.
 int64_t delta_segments(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P, bool bf16) {
   if (!bf16 || N > 128) return 1;
   const int64_t nw = (L + kDeltaC - 1) / kDeltaC, blocks = B * H * (P % 32 == 0 ? P / 32 : P / 16);
   int64_t segs = device_cu_count() / blocks;
   if (segs > nw / 8) segs = nw / 8;
-  if (segs < 4) return 1;
+  if (segs < 3) return 1;
   return (nw + (nw + segs - 1) / segs - 1) / ((nw + segs - 1) / segs);  // none of them empty
 }
 template <class M, int NP>

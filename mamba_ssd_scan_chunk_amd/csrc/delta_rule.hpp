@@ -82,7 +82,7 @@ struct DeltaB {
     *reinterpret_cast<uint4*>(p + 1024 + 16 * lane) = t.lo.v;
   }
   // eight consecutive inputs
-  __device__ __forceinline__ static One global8(const uint16_t* p) {
+  __device__ __forceinline__ static One row8(const uint16_t* p) {
     One f;
     f.v = *reinterpret_cast<const uint4*>(p);
     return f;
@@ -93,7 +93,6 @@ struct DeltaB {
     f.v = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, lane, row, 0));
     return f;
   }
-  __device__ __forceinline__ static One zero() { return OpBF16::zero(); }
   // rows of a tile in LDS as the transposed operand: lane (i, g) gets, as slots
   // 4t + r, tile[16t + 4g + r][i]
   __device__ __forceinline__ static One transposed(const uint16_t* tile, int pitch, int lane) {
@@ -117,14 +116,13 @@ struct DeltaF {
     *reinterpret_cast<float4*>(p + 16 * lane) = t.lo;
     *reinterpret_cast<float4*>(p + 1024 + 16 * lane) = t.hi;
   }
-  __device__ __forceinline__ static One global8(const float* p) { return Lds<OpF32>::load8(p); }
+  __device__ __forceinline__ static One row8(const float* p) { return Lds<OpF32>::load8(p); }
   __device__ __forceinline__ static One rows8(__amdgpu_buffer_rsrc_t r, uint32_t lane, uint32_t row) {
     One f;
     f.lo = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(r, lane, row, 0));
     f.hi = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(r, lane, row + 16, 0));
     return f;
   }
-  __device__ __forceinline__ static One zero() { return OpF32::zero(); }
   __device__ __forceinline__ static One transposed(const float* tile, int pitch, int lane) {
     const float* p = tile + 4 * (lane >> 4) * pitch + (lane & 15);
     One f;
@@ -529,7 +527,6 @@ inline DeltaWs delta_ws(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P, b
 // Launches shared by the forward and the gradients (delta_rule.hip).
 hipError_t launch_delta_prepare(const DeltaArgs& a, const DeltaWs& ws, bool back, bool bf16, hipStream_t s);
 hipError_t launch_delta_chain(const DeltaArgs& a, const DeltaWs& ws, bool save, bool bf16, hipStream_t s);
-// Waves of 16 value columns a block of the chains.
 // Column waves of a block of the general chains, of four waves; the others stage.
 __host__ __device__ inline int chain_columns(int64_t P) { return P / 16 % 2 == 0 ? 2 : 1; }
 

@@ -30,6 +30,9 @@ namespace ssd {
 constexpr int kTP = kC + 4;
 
 // ---------------------------------------------------------------- the chain, back to front
+// fp32 inputs, and bf16 ones of more than 128 key columns; the waves as in the
+// forward's general chain.  2 x 777 tokens, N = 48, P = 80, fp32: 96 us, the
+// length of the chain (224 where every wave staged for itself).
 template <class M, int NP>
 constexpr int rev_pitch() { return NP + 16 / (int)sizeof(typename M::IO::type); }
 template <class M, int NP>
@@ -222,7 +225,10 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, DeltaWs
 // ---------------------------------------------------------------- the same of bf16 inputs
 // C column waves and C stagers, as in the forward chain, and C waves that work
 // out a step ahead what the next piece adds whatever D is, P^T dy to its values
-// and q^T diag(e^G) dy to D, and leave it in LDS as accumulators.
+// and q^T diag(e^G) dy to D, and leave it in LDS as accumulators.  Bound by the
+// column waves' latency: 2 x 2048 tokens of 32 heads, N = P = 128, 136 us, 4.2 a
+// window (858 with waves that do everything; waves wait for 57% of their cycles
+// and the matrix units are busy 8%).
 template <int NP, int C>
 struct ReverseLds {
   static constexpr int kPitch = NP + 24;  // rows as the products read them begin in different banks
@@ -521,6 +527,12 @@ __global__ __launch_bounds__(chain_threads(C), C) void delta_reverse_bf16_kernel
 }
 
 // ---------------------------------------------------------------- all windows at once
+// The products over value columns go a slice of 64 columns at a time, every
+// operand of the slice asked for before the one in front is worked out; the 64 x
+// 64 matrices are rounded once a block and shared by its eight waves.  Bound by
+// issue and LDS: 2 x 2048 tokens of 32 heads, N = P = 128, 250 us, 145 of them in
+// the slices; its traffic (S, D and w, du in fp32) alone is about 110.
+
 // Left operands of 64 tokens by 64 value columns in LDS.
 template <class M> struct GradTile;
 template <> struct GradTile<DeltaB> {
@@ -537,11 +549,11 @@ template <> struct GradTile<DeltaB> {
     *reinterpret_cast<uint4*>(q + 3 * kPlane) = y.hi.v;
     *reinterpret_cast<uint4*>(q + 4 * kPlane) = y.lo.v;
   }
-  __device__ __forceinline__ DeltaB::One dy(int t, int col) const { return DeltaB::global8(p + t * kPitch + col); }
+  __device__ __forceinline__ DeltaB::One dy(int t, int col) const { return DeltaB::row8(p + t * kPitch + col); }
   __device__ __forceinline__ DeltaB::Two two(int plane, int t, int col) const {
     DeltaB::Two x;
-    x.hi = DeltaB::global8(p + plane * kPlane + t * kPitch + col);
-    x.lo = DeltaB::global8(p + (plane + 1) * kPlane + t * kPitch + col);
+    x.hi = DeltaB::row8(p + plane * kPlane + t * kPitch + col);
+    x.lo = DeltaB::row8(p + (plane + 1) * kPlane + t * kPitch + col);
     return x;
   }
   __device__ __forceinline__ DeltaB::Two u(int t, int col) const { return two(1, t, col); }
@@ -558,10 +570,10 @@ template <> struct GradTile<DeltaF> {
     Lds<OpF32>::store8(q + kPlane, u);
     Lds<OpF32>::store8(q + 2 * kPlane, dw);
   }
-  __device__ __forceinline__ DeltaF::One dy(int t, int col) const { return DeltaF::global8(p + t * kPitch + col); }
-  __device__ __forceinline__ DeltaF::Two u(int t, int col) const { return DeltaF::global8(p + kPlane + t * kPitch + col); }
+  __device__ __forceinline__ DeltaF::One dy(int t, int col) const { return DeltaF::row8(p + t * kPitch + col); }
+  __device__ __forceinline__ DeltaF::Two u(int t, int col) const { return DeltaF::row8(p + kPlane + t * kPitch + col); }
   __device__ __forceinline__ DeltaF::Two dw(int t, int col) const {
-    return DeltaF::global8(p + 2 * kPlane + t * kPitch + col);
+    return DeltaF::row8(p + 2 * kPlane + t * kPitch + col);
   }
 };
 // The token-by-token matrices as left operands: M1 lower, M2 upper triangular, M3 whole.
@@ -1029,7 +1041,8 @@ __global__ __launch_bounds__(64 * WV, 2) void delta_grad_kernel(DeltaArgs a, Del
 
 // ---------------------------------------------------------------- heads of a group together, unit length
 // W lanes of four columns a (token, key group); blockIdx.y: q or k.  Bound by
-// memory: the heads' fp32 shares, read once.
+// memory: the heads' fp32 shares, read once (2 x 2048 tokens of 32 heads over 16,
+// N = 128: 36 us, 4.6 TB/s).
 template <class IO, int W>
 __global__ __launch_bounds__(256) void delta_finish_kernel(DeltaArgs a, DeltaWs ws) {
   typedef typename IO::type T;
