@@ -874,8 +874,8 @@ __global__ __launch_bounds__(MODE == kOut ? chain_threads(C) : 128 * C, C) void 
 // and a wave 32 rows of them, so that the next stretch's map is asked for while
 // one is multiplied; the waves meet once a stretch, for S as operands.  Where a
 // sequence begins in the stretch it is R alone, and M is not multiplied: its
-// zeros would make NaN of what the sequence before left.  About 1 us a stretch;
-// one wave for all rows, which read each map only when its turn came, took 6.
+// zeros would make NaN of what the sequence before left.  3 us a stretch; one
+// wave for all rows, which read each map only when its turn came, took 6.
 template <int NP>
 __global__ __launch_bounds__(2 * NP) void delta_enter_kernel(DeltaArgs a, DeltaWs ws) {
   typedef DeltaB M;
