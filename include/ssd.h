@@ -539,7 +539,7 @@ size_t ssd_layer_norm_backward_workspace_bytes(int64_t rows, int64_t dim);
  * fp32, dt_bias optional.  y [B,L,H,P] in `in`; initial_states, final_states
  * [B,H,N,P], seq_states [nseq,H,N,P] fp32, optional.  N (dstate) and P
  * (headdim) multiples of 16 up to 256, B H < 2^22, B H P < 2^28, B H ceil(L/64) < 2^23,
- * H P and row strides < 2^23 (else SSD_ERR_UNSUPPORTED).  q and k of prompts are 16-byte aligned with row
+ * H P, G N and row strides < 2^23 (else SSD_ERR_UNSUPPORTED).  q and k of prompts are 16-byte aligned with row
  * strides in whole 16 bytes.  final_states may be initial_states.  A token with a
  * NaN or infinity makes NaN of its sequence from its window of 64 tokens on, the
  * window's earlier tokens included; other sequences stay as they are (a padded

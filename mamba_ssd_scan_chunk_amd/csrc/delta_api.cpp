@@ -11,6 +11,9 @@ using namespace ssd::api;
 
 namespace {
 
+// 64 rows of up to 4 bytes an element are addressed by 32-bit byte offsets
+constexpr int64_t kMaxRow = int64_t(1) << 23;
+
 ssd_status check_delta(const ssd_delta_shape* s, bool step) {
   if (!s) return SSD_ERR_NULL;
   if (s->batch <= 0 || s->seqlen <= 0 || s->nheads <= 0 || s->headdim <= 0 || s->dstate <= 0 || s->ngroups <= 0)
@@ -24,7 +27,9 @@ ssd_status check_delta(const ssd_delta_shape* s, bool step) {
   SSD_TRY(product({s->batch, s->nheads, (s->seqlen - 1) / ssd::kDeltaC + 1}, (int64_t(1) << 23) - 1));
   SSD_TRY(product({s->batch, s->nheads}, (int64_t(1) << 22) - 1));
   SSD_TRY(product({s->batch, s->nheads, s->headdim}, (int64_t(1) << 28) - 1));
-  if (s->nheads * s->headdim >= int64_t(1) << 23) return SSD_ERR_UNSUPPORTED;
+  // dense rows, of v (those of dt and beta are shorter) and of q and k
+  SSD_TRY(product({s->nheads, s->headdim}, kMaxRow - 1));
+  SSD_TRY(product({s->ngroups, s->dstate}, kMaxRow - 1));
   return product({s->batch, s->seqlen, s->nheads, s->headdim}, kMaxElems);
 }
 
@@ -32,9 +37,8 @@ ssd_status delta_rows(const ssd_delta_shape* s, const ssd_delta_rows* r, ssd::De
   const ssd_delta_rows none = {0, 0, 0, 0, 0};
   if (!r) r = &none;
   const int64_t qk = s->ngroups * s->dstate;
-  // 64 rows of up to 4 bytes an element are addressed by 32-bit byte offsets
   for (int64_t given : {r->q, r->k, r->v, r->dt, r->beta})
-    if (given >= int64_t(1) << 23) return SSD_ERR_UNSUPPORTED;
+    if (given >= kMaxRow) return SSD_ERR_UNSUPPORTED;
   SSD_TRY(row_stride(r->q, qk, s->batch, s->seqlen, &o->q));
   SSD_TRY(row_stride(r->k, qk, s->batch, s->seqlen, &o->k));
   SSD_TRY(row_stride(r->v, s->nheads * s->headdim, s->batch, s->seqlen, &o->v));

@@ -109,6 +109,27 @@ def test_delta_rows(lib, i, dense):
         assert fwd(lib, rows=rows(dense + 4)) == ALIGN  # q and k are read 16 bytes at a time
 
 
+@pytest.mark.parametrize("ty", [0, 1])
+@pytest.mark.parametrize("kw,given", [
+    (dict(nheads=1 << 15, ngroups=1 << 15, dstate=256, headdim=16), 0),   # rows of q and k of 2^23 elements
+    (dict(nheads=1 << 16, ngroups=1 << 16, dstate=256, headdim=16), 0),   # 2^24: 64 fp32 rows are 2^32 bytes
+    (dict(nheads=1 << 16, ngroups=1 << 16, dstate=128, headdim=16), 0),
+    (dict(nheads=1 << 15, ngroups=1 << 15, dstate=256, headdim=16), 1 << 23),
+])
+def test_delta_dense_rows(lib, kw, given, ty):
+    """Dense rows are held to the bound of given ones, in the calls and the queries."""
+    s = shape(batch=1, seqlen=64, **kw)
+    r = SSDDeltaRows(given, given, 0, 0, 0)
+    assert fwd(lib, s, rows=r, ty=ty, ws=None) == UNSUP and bwd(lib, s, rows=r, ty=ty, ws=None) == UNSUP
+    assert bwd(lib, s, grows=r, ty=ty, ws=None) == UNSUP
+    assert lib.ssd_delta_rule_workspace_bytes(s) == 0 and lib.ssd_delta_rule_backward_workspace_bytes(s) == 0
+    s.seqlen = 1
+    assert step(lib, s, rows=r, ty=ty, y=None) == UNSUP
+    # the widest rows that are taken get as far as the workspace
+    wide = shape(batch=1, seqlen=64, nheads=(1 << 15) - 1, ngroups=(1 << 15) - 1, dstate=256, headdim=16)
+    assert fwd(lib, wide, ty=ty, ws=None) == WS and bwd(lib, wide, ty=ty, ws=None) == WS
+
+
 # ---------------------------------------------------------------- group norm, 8 bits
 
 def gn(lib, rows=6, dim=128, groups=2, x=F, ty=1, z=F, zrow=0, w=F, b=F, flags=1, y=F, mean=None, rstd=F):
