@@ -153,9 +153,9 @@ def ssd_delta_rule_backward(q, k, v, dt, beta, A, dy, dt_bias=None, softplus=Tru
 def _flat_rows(t, name: str, shape, dtypes) -> int:
     """Checks ``t`` [..., D] whose rows may be column slices of wider rows that
     follow each other evenly; returns the row stride in elements (0: dense)."""
-    if t is not None and t.dim() > 2 and tuple(t.shape) == tuple(shape) and not t.is_contiguous():
+    if t is not None and t.dim() != 2 and tuple(t.shape) == tuple(shape) and not t.is_contiguous():
         try:
-            t = t.view(-1, shape[-1])
+            t = t[None] if t.dim() == 1 else t.view(-1, shape[-1])
         except RuntimeError:
             raise ValueError(f"{name}'s rows must follow each other evenly") from None
         shape = t.shape

@@ -273,3 +273,42 @@ def test_the_calls_are_found_under_ops():
     assert all(getattr(ops, n) is getattr(delta_ops, n) for n in CALLS) and set(CALLS) <= set(dir(ops))
     with pytest.raises(AttributeError):
         ops.ssd_no_such_call
+
+
+class _Strided(base._Tensor):
+    """The same of a CPU tensor's strides."""
+
+    def __init__(self, log, t):
+        super().__init__(log, t.shape, t.dtype)
+        self.t = t
+
+    def is_contiguous(self):
+        return self.t.is_contiguous()
+
+    def stride(self):
+        return self.t.stride()
+
+    def __getitem__(self, i):
+        return _Strided(self.log, self.t[i])
+
+    def view(self, *shape):
+        return _Strided(self.log, self.t.view(*shape))
+
+
+@pytest.mark.parametrize("make", [lambda m: m[:, 3], lambda m: m.flatten()[:16:2], lambda m: m[:, ::2],
+                                  lambda m: m.view(2, 4, 16)[..., ::2]])
+def test_columns_that_are_not_side_by_side_are_refused(stand_in, make):
+    """A row's columns are read side by side, one row without a leading
+    dimension too."""
+    log = stand_in
+    x = make(torch.zeros(8, 16))
+    t = lambda *s, dtype=torch.float32: base._Tensor(log, s, dtype)
+    D, lead = x.shape[-1], x.shape[:-1]
+    s = _Strided(log, x)
+    q8 = (t(*x.shape, dtype=torch.int8), t(*lead, 1, dtype=torch.bfloat16))
+    for call in (lambda: ops.ssd_pack8(s), lambda: ops.ssd_unpack8(*q8, x=s),
+                 lambda: ops.ssd_group_norm(t(*x.shape), t(D), z=s),
+                 lambda: ops.ssd_group_norm_backward(t(*x.shape), t(*x.shape), t(D), None, t(*lead, 1), z=s)):
+        with pytest.raises(ValueError, match="contiguous within"):
+            call()
+    assert not log.launched
