@@ -137,7 +137,7 @@ def ssd_delta_rule_backward(q, k, v, dt, beta, A, dy, dt_bias=None, softplus=Tru
         if absent.get(n):
             r[n] = None
             continue
-        r[n] = given[n] if given.get(n) is not None else torch.empty(shp, device=v.device)
+        r[n] = given[n] if given.get(n) is not None else torch.empty(shp, device=v.device, dtype=torch.float32)
         _req(r[n], n, shp, _F32)
     lib = load_library()
     workspace, wsb = _workspace(workspace, lib.ssd_delta_rule_backward_workspace_bytes, (sh,), v.device)

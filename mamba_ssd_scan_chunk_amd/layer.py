@@ -63,12 +63,12 @@ class MambaWeights:
         log-uniform in [1e-3, 1e-1] by the bias."""
         R = (-(-dm // 16) + 1) // 2 * 2 if R is None else R
         g = torch.Generator(device=device).manual_seed(seed)
+        f = dict(device=device, dtype=torch.float32)
 
         def u(shape, bound):
-            return (torch.rand(shape, generator=g, device=device) * 2 - 1) * bound
+            return (torch.rand(shape, generator=g, **f) * 2 - 1) * bound
 
-        dt = torch.exp(torch.rand((D,), generator=g, device=device) * math.log(100.0) + math.log(1e-3))
-        f = dict(device=device, dtype=torch.float32)
+        dt = torch.exp(torch.rand((D,), generator=g, **f) * math.log(100.0) + math.log(1e-3))
         return cls(norm_w=torch.ones(dm, **f), norm_b=torch.zeros(dm, **f),
                    in_proj=u((2 * D, dm), dm ** -0.5).to(dtype), conv_w=u((D, W), W ** -0.5), conv_b=u((D,), W ** -0.5),
                    x_proj=u((R + 2 * N, D), D ** -0.5).to(dtype), dt_proj=u((D, R), R ** -0.5).to(dtype),
@@ -88,7 +88,7 @@ class MambaLayer:
         """Zero states of `batch` streams: (conv [B,W-1,D], scan [B,N,D])."""
         w = self.w
         conv = torch.zeros((batch, w.conv_w.shape[1] - 1, self.D), device=w.A.device, dtype=dtype or w.in_proj.dtype)
-        return conv, torch.zeros((batch, self.N, self.D), device=w.A.device)
+        return conv, torch.zeros((batch, self.N, self.D), device=w.A.device, dtype=torch.float32)
 
     def _split(self, t):
         """q | B | C of the x projection's columns, B and C with their one group."""
@@ -199,16 +199,16 @@ class DeltaWeights:
         """Weights as such layers start out: decay rates -1 .. -16, time steps
         log-uniform in [1e-3, 1e-1] by the bias."""
         g = torch.Generator(device=device).manual_seed(seed)
+        f = dict(device=device, dtype=torch.float32)
 
         def u(shape, bound):
-            return (torch.rand(shape, generator=g, device=device) * 2 - 1) * bound
+            return (torch.rand(shape, generator=g, **f) * 2 - 1) * bound
 
         D = 2 * G * N + H * P
-        dt = torch.exp(torch.rand((H,), generator=g, device=device) * math.log(100.0) + math.log(1e-3))
-        f = dict(device=device, dtype=torch.float32)
+        dt = torch.exp(torch.rand((H,), generator=g, **f) * math.log(100.0) + math.log(1e-3))
         return cls(norm_w=torch.ones(dm, **f), norm_b=torch.zeros(dm, **f),
                    in_proj=u((D + H * P + 2 * H, dm), dm ** -0.5).to(dtype), conv_w=u((D, W), W ** -0.5),
-                   conv_b=u((D,), W ** -0.5), A=-1 - 15 * torch.rand((H,), generator=g, device=device),
+                   conv_b=u((D,), W ** -0.5), A=-1 - 15 * torch.rand((H,), generator=g, **f),
                    dt_bias=dt + torch.log(-torch.expm1(-dt)), gnorm_w=torch.ones(P, **f),
                    out_proj=u((dm, H * P), (H * P) ** -0.5).to(dtype))
 
@@ -229,7 +229,7 @@ class DeltaLayer:
         """Zero states of `batch` streams: (conv [B,W-1,D], delta [B,H,N,P])."""
         w = self.w
         conv = torch.zeros((batch, w.conv_w.shape[1] - 1, self.D), device=w.A.device, dtype=dtype or w.in_proj.dtype)
-        return conv, torch.zeros((batch, self.H, self.N, self.P), device=w.A.device)
+        return conv, torch.zeros((batch, self.H, self.N, self.P), device=w.A.device, dtype=torch.float32)
 
     def _qkv(self, u):
         n = self.G * self.N

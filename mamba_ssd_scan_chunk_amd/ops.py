@@ -442,7 +442,7 @@ def ssd_backward(shape, x, dt, A, Bm, Cm, D, dy, initial_states=None, dfinal=Non
         if k == "dinitial" and not want_dinitial:
             out[k] = None
             continue
-        out[k] = given[k] if given.get(k) is not None else torch.empty(shp, device=dev)
+        out[k] = given[k] if given.get(k) is not None else torch.empty(shp, device=dev, dtype=torch.float32)
         _req(out[k], k, shp, f32)
     lib = load_library()
     need = int(lib.ssd_backward_workspace_bytes(sh))
@@ -746,7 +746,7 @@ def ssd_selective_scan_backward(u, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=No
         if absent.get(k):
             r[k] = None
             continue
-        r[k] = given[k] if given.get(k) is not None else torch.empty(shp, device=u.device)
+        r[k] = given[k] if given.get(k) is not None else torch.empty(shp, device=u.device, dtype=torch.float32)
         _req(r[k], k, shp, _F32)
     lib = load_library()
     workspace, wsb = _workspace(workspace, lib.ssd_selective_scan_backward_workspace_bytes, (sh,), u.device)
