@@ -58,9 +58,10 @@ inline ssd_status check_states(const void* initial, const void* final) {
   return final && final == initial ? SSD_ERR_UNSUPPORTED : SSD_OK;
 }
 
+constexpr int64_t kMaxSeqStates = 65535;
 inline ssd_status check_seq_list(int64_t nseq, const int64_t* last, const void* states) {
   if (nseq < 0) return SSD_ERR_SHAPE;
-  if (nseq > 65535) return SSD_ERR_UNSUPPORTED;
+  if (nseq > kMaxSeqStates) return SSD_ERR_UNSUPPORTED;
   if (nseq > 0 && (!last || !states)) return SSD_ERR_NULL;
   if (nseq > 0 && (!a16(last) || !a16(states))) return SSD_ERR_ALIGN;
   return SSD_OK;

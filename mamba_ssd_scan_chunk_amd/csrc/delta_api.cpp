@@ -99,6 +99,7 @@ ssd_status ssd_delta_rule(const ssd_delta_shape* shape, const ssd_delta_rows* ro
   SSD_TRY(delta_inputs(shape, rows, q, k, v, dt, beta, A, dt_bias, flags, scale, in, false, &a));
   if (!y) return SSD_ERR_NULL;
   SSD_TRY(check_seq_list(nseq, seq_last, seq_states));
+  static_assert(ssd::kDeltaMaxStates >= kMaxSeqStates, "the workspace holds a link for every state");
   if (!workspace || workspace_bytes < ssd_delta_rule_workspace_bytes(shape)) return SSD_ERR_WORKSPACE;
   if (!a16(initial_states) || !a16(seq_idx) || !a16(y) || !a16(final_states) || !a16(workspace)) return SSD_ERR_ALIGN;
   a.h0 = initial_states;

@@ -11,6 +11,7 @@ namespace ssd {
 
 constexpr int64_t kDeltaC = 64;        // tokens a window
 constexpr int64_t kDeltaMaxDim = 256;  // of a key or value head
+constexpr int64_t kDeltaMaxStates = 65535;  // states after tokens
 
 struct DeltaRows {
   int64_t q, k, v, dt, beta;  // elements from a token to the next

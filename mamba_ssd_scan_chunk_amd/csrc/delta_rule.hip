@@ -30,6 +30,11 @@ __device__ __forceinline__ float lane_value(float v, int lane) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
 }
 
+__device__ __forceinline__ Wanted wanted_states(const DeltaArgs& a, const DeltaWs& ws) {
+  if (a.nseq <= 0) return {nullptr, nullptr};
+  return {reinterpret_cast<const int*>(a.ws + ws.wanted), reinterpret_cast<const int*>(a.ws + ws.wanted_next)};
+}
+
 // e b where e is not zero: an entry between pieces stays zero whatever b is.
 __device__ __forceinline__ float times(float e, float b) { return e != 0.f ? e * b : 0.f; }
 
@@ -120,8 +125,7 @@ __global__ __launch_bounds__(256, 2) void delta_prepare_kernel(DeltaArgs a, Delt
   }
   Cuts both = {0, 0};
   if constexpr (VL) {
-    const uint8_t* marks = !BACK && a.nseq > 0 ? reinterpret_cast<const uint8_t*>(a.ws + ws.marks) : nullptr;
-    both = window_cuts(a.seq_idx, marks, row, t0, a.L, lane);
+    both = window_cuts(a.seq_idx, BACK ? Wanted{} : wanted_states(a, ws), row, t0, a.L, lane);
     if (h == 0 && threadIdx.x == 0) reinterpret_cast<Cuts*>(a.ws + ws.cuts)[b * ws.nw + win] = both;
   }
   const uint64_t cuts = both.piece;
@@ -310,14 +314,15 @@ __global__ __launch_bounds__(256, 2) void delta_prepare_kernel(DeltaArgs a, Delt
   }
 }
 
-// ---------------------------------------------------------------- marks of the tokens whose state is asked for
-__global__ __launch_bounds__(256) void delta_marks_clear_kernel(uint8_t* marks, int64_t n) {
+// ---------------------------------------------------------------- tokens whose state is asked for
+__global__ __launch_bounds__(256) void delta_wanted_clear_kernel(int* of, int64_t n) {
   const int64_t i = (int64_t)flat_block() * 256 + threadIdx.x;
-  if (i < n) marks[i] = 0;
+  if (i < n) of[i] = -1;
 }
-__global__ __launch_bounds__(256) void delta_marks_kernel(uint8_t* marks, int64_t n, const int64_t* last, int64_t nseq) {
+// The order of a token's list is whatever the exchanges make it: all of it gets the same state.
+__global__ __launch_bounds__(256) void delta_wanted_kernel(int* of, int* next, int64_t n, const int64_t* last, int64_t nseq) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i < nseq && last[i] >= 0 && last[i] < n) marks[last[i]] = 1;
+  if (i < nseq && last[i] >= 0 && last[i] < n) next[i] = atomicExch(of + last[i], (int)i);
 }
 
 // ---------------------------------------------------------------- the chain
@@ -354,7 +359,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs w
   const int64_t p = ((bid % slices) * w + wave) * 16 + c;
   const int N = (int)a.N;
   const int64_t row = b * a.L;
-  const uint8_t* marks = !SAVE && a.nseq > 0 ? reinterpret_cast<const uint8_t*>(a.ws + ws.marks) : nullptr;
+  const Wanted wanted = VL && !SAVE ? wanted_states(a, ws) : Wanted{};
 
   f32x4_t S[NT];
 #pragma unroll
@@ -370,7 +375,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs w
     const int n = (int)(a.L - t0 < kC ? a.L - t0 : kC);
     Cuts cuts = {0, 0};
     if constexpr (VL) {
-      cuts = window_cuts(a.seq_idx, marks, row, t0, a.L, lane);
+      cuts = window_cuts(a.seq_idx, wanted, row, t0, a.L, lane);
       if (cuts.fresh & 1) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) S[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -521,18 +526,15 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs w
         for (int j = 0; j < NT; ++j) S[j] = M::mma(M::transposed(kt + 32 * s * LP + 16 * j, LP, lane), ub, S[j]);
       }
       if constexpr (VL) {
-        if (marks && marks[row + t0 + end - 1]) {
-          for (int64_t s = 0; s < a.nseq; ++s) {
-            if (a.seq_last[s] != row + t0 + end - 1) continue;
-            float* out = a.seq_states + (s * a.H + h) * N * a.P + p;
+        for (int s = wanted.first(row + t0 + end - 1); s >= 0; s = wanted.after(s)) {
+          float* out = a.seq_states + (s * a.H + h) * N * a.P + p;
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+          for (int j = 0; j < NT; ++j)
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const int nn = 16 * j + 4 * g + r;
-                if (column && nn < N) out[nn * a.P] = S[j][r];
-              }
-          }
+            for (int r = 0; r < 4; ++r) {
+              const int nn = 16 * j + 4 * g + r;
+              if (column && nn < N) out[nn * a.P] = S[j][r];
+            }
         }
       }
       begin = end;
@@ -598,7 +600,7 @@ __global__ __launch_bounds__(MODE == kOut ? chain_threads(C) : 128 * C, C) void 
   if (MODE == kStretch && !unit) p -= N;
   const uint32_t P = (uint32_t)a.P;
   const int64_t row = b * a.L;
-  const uint8_t* marks = VL && OUT && a.nseq > 0 ? reinterpret_cast<const uint8_t*>(a.ws + ws.marks) : nullptr;
+  const Wanted wanted = VL && OUT ? wanted_states(a, ws) : Wanted{};
   Pieces pc;
   const int64_t w0 = MODE == kSave ? 0 : seg * ws.seg_wins;
   pc.first(VL ? reinterpret_cast<const Cuts*>(a.ws + ws.cuts) + b * ws.nw : nullptr, w0,
@@ -853,12 +855,8 @@ __global__ __launch_bounds__(MODE == kOut ? chain_threads(C) : 128 * C, C) void 
       for (int j = 0; j < NT; ++j) S[j] = M::mma(kT[s][j], ub.hi, S[j]);
     }
     if constexpr (VL) {
-      const int64_t last = row + win * kC + end - 1;
-      if (marks && marks[last]) {
-        for (int64_t s = 0; s < a.nseq; ++s)
-          if (a.seq_last[s] == last)
-            put_state<NT>(a.seq_states + (s * a.H + h) * N * a.P, N, P, 4 * g * P + p, S);
-      }
+      for (int s = wanted.first(row + win * kC + end - 1); s >= 0; s = wanted.after(s))
+        put_state<NT>(a.seq_states + (s * a.H + h) * N * a.P, N, P, 4 * g * P + p, S);
     }
     __syncthreads();
   }
@@ -1176,10 +1174,10 @@ hipError_t launch_delta_chain(const DeltaArgs& a, const DeltaWs& ws, bool save, 
 hipError_t launch_delta_forward(const DeltaArgs& a, bool bf16, hipStream_t s) {
   const DeltaWs ws = delta_ws(a.B, a.L, a.H, a.N, a.P, false, delta_segments(a.B, a.L, a.H, a.N, a.P, bf16));
   if (a.nseq > 0) {
-    uint8_t* marks = reinterpret_cast<uint8_t*>(a.ws + ws.marks);
-    hipLaunchKernelGGL(delta_marks_clear_kernel, flat_grid((a.B * a.L + 255) / 256), dim3(256), 0, s, marks, a.B * a.L);
-    hipLaunchKernelGGL(delta_marks_kernel, dim3((unsigned)((a.nseq + 255) / 256)), dim3(256), 0, s, marks, a.B * a.L,
-                       a.seq_last, a.nseq);
+    int* of = reinterpret_cast<int*>(a.ws + ws.wanted);
+    hipLaunchKernelGGL(delta_wanted_clear_kernel, flat_grid((a.B * a.L + 255) / 256), dim3(256), 0, s, of, a.B * a.L);
+    hipLaunchKernelGGL(delta_wanted_kernel, dim3((unsigned)((a.nseq + 255) / 256)), dim3(256), 0, s, of,
+                       reinterpret_cast<int*>(a.ws + ws.wanted_next), a.B * a.L, a.seq_last, a.nseq);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

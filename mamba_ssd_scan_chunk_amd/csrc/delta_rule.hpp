@@ -158,6 +158,18 @@ __host__ __device__ constexpr int low_frag(int i, int s) { return i < 2 ? i : 2 
 // its transpose, upper triangular: (0,0) (0,1) (1,0) (1,1) (2,1) (3,1)
 __host__ __device__ constexpr int up_frag(int i, int s) { return i < 2 ? 2 * i + s : 2 + i; }
 
+// ---- tokens whose state is asked for ----
+// The first asked-for state of every token of the batch (-1: none), and of a
+// state the next one after the same token: a token goes straight to its states,
+// however many there are.  Null `of`: none are asked for.
+struct Wanted {
+  const int *of, *next;
+  __device__ __forceinline__ int first(int64_t token) const {
+    return of ? __builtin_amdgcn_readfirstlane(of[token]) : -1;
+  }
+  __device__ __forceinline__ int after(int s) const { return __builtin_amdgcn_readfirstlane(next[s]); }
+};
+
 // ---- pieces of a window ----
 // Bits of the tokens t > 0 of a window at which a piece begins: another
 // sequence, or behind a token whose state is asked for; `fresh`: where a
@@ -170,13 +182,13 @@ __device__ __forceinline__ uint64_t uniform64(uint64_t v) {
          ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) << 32);
 }
 // Every lane of a wave calls this; row: the batch's first token, t0 the window's.
-__device__ __forceinline__ Cuts window_cuts(const int* seq_idx, const uint8_t* marks, int64_t row, int64_t t0,
-                                            int64_t L, int lane) {
+__device__ __forceinline__ Cuts window_cuts(const int* seq_idx, const Wanted& wanted, int64_t row, int64_t t0, int64_t L,
+                                            int lane) {
   const int64_t t = t0 + lane;
   bool fresh = false, mark = false;
   if (t < L && t > 0) {
     if (seq_idx) fresh = seq_idx[row + t] != seq_idx[row + t - 1];
-    if (marks) mark = marks[row + t - 1] != 0;
+    if (wanted.of) mark = wanted.of[row + t - 1] >= 0;
   }
   Cuts c;
   c.fresh = uniform64(__ballot(fresh));
@@ -483,7 +495,7 @@ __device__ __forceinline__ uint32_t near_block(uint32_t bid, uint32_t n) {
 // ---- the workspace ----
 struct DeltaWs {
   int64_t nw;        // windows a row
-  size_t gates, cuts, low_r, low_p, up_r, up_p, marks, trans, enter, S, D, w, du, dq, dk, part, total;
+  size_t gates, cuts, low_r, low_p, up_r, up_p, wanted, wanted_next, trans, enter, S, D, w, du, dq, dk, part, total;
   int64_t segs, seg_wins;  // stretches of a row that are walked side by side, and their windows
 };
 // segs: see delta_segments().
@@ -502,7 +514,8 @@ inline DeltaWs delta_ws(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P, b
   o.low_r = take(bhw * kTriBytes);
   if (!back) {
     o.low_p = take(bhw * kTriBytes);
-    o.marks = take((size_t)(B * L));
+    o.wanted = take((size_t)(B * L) * 4);
+    o.wanted_next = take((size_t)kDeltaMaxStates * 4);
     o.segs = segs;
     o.seg_wins = (o.nw + segs - 1) / segs;
     if (segs > 1) {

@@ -74,7 +74,7 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, DeltaWs
     const int64_t t0 = win * kC, bhw = bh * ws.nw + win;
     const int n = (int)(a.L - t0 < kC ? a.L - t0 : kC);
     Cuts cuts = {0, 0};
-    if constexpr (VL) cuts = window_cuts(a.seq_idx, nullptr, row, t0, a.L, lane);
+    if constexpr (VL) cuts = window_cuts(a.seq_idx, Wanted{}, row, t0, a.L, lane);
     {
       float* out = reinterpret_cast<float*>(a.ws + ws.D) + bhw * N * a.P + p;
 #pragma unroll

@@ -337,3 +337,37 @@ def test_nan_stays_in_its_sequence_across_stretches(bad, L):
     d["h0"][:] = bad
     y, fin = call(d, seq_idx=idx.cuda())
     assert torch.equal(y[:, 300:], clean[0][:, 300:]) and torch.equal(fin, clean[1])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_many_states_after_tokens(dtype):
+    """A state after every token of a row of single tokens, in any order.  Each
+    costs its own writing: the call takes no more than four times what the same
+    pieces take without states, where a search of the whole list for every token
+    takes some seventy times that."""
+    L, N, P = 8192, 16, 16
+    a = ref.inputs(1, L, 1, 1, N, P, dtype=dtype, seed=2, h0=False)
+    idx = torch.arange(L, dtype=torch.int32)[None].cuda()
+    last = torch.randperm(L, generator=torch.Generator().manual_seed(1)).cuda()
+    states = torch.empty((L, 1, N, P), device="cuda")
+
+    def time(**how):
+        best = float("inf")
+        for _ in range(3):
+            start, stop = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            start.record()
+            got = call(a, seq_idx=idx, **how)
+            stop.record()
+            torch.cuda.synchronize()
+            best = min(best, start.elapsed_time(stop))
+        return best, got
+
+    plain, (y, fin) = time()
+    each, (y2, fin2, st) = time(seq_last=last, seq_states=states)
+    assert torch.equal(y, y2) and torch.equal(fin, fin2)
+    # a single token from a state of zeros leaves k (w v)^T
+    d = {n: t.double() for n, t in a.items() if t is not None}
+    k = d["k"] / torch.sqrt((d["k"] ** 2).sum(-1, keepdim=True) + ref.QK_EPS)
+    want = k[0, :, 0, :, None] * (d["beta"].sigmoid()[0, :, 0, None] * d["v"][0, :, 0])[:, None, :]
+    check(st[:, 0], want[last.cpu()], dtype, "states")
+    assert each < 4 * plain, (each, plain)
