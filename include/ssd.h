@@ -550,6 +550,10 @@ size_t ssd_layer_norm_backward_workspace_bytes(int64_t rows, int64_t dim);
  * of a window of 64 tokens) enter as the sum of two bf16 values, 16 bits;
  * sums and states are fp32.  fp32 outputs of bf16 inputs are so within 1e-5 of
  * their values (2-norm), bf16 ones one rounding.
+ *
+ * Workspace: device memory of ssd_delta_rule_workspace_bytes(shape) bytes, asked
+ * for on the device of the call (it depends on the compute units).  It serves
+ * every smaller prompt of the same N and P too: the size never falls with B, L or H.
  * ------------------------------------------------------------------------ */
 typedef struct {
   int64_t batch, seqlen, nheads, headdim, dstate, ngroups;
@@ -582,7 +586,10 @@ ssd_status ssd_delta_step(const ssd_delta_shape* shape, const ssd_delta_rows* ro
  * `in`, laid out like their inputs with the row strides of `grad_rows` (NULL =
  * dense); dA, ddt_bias (optional) [H] and dinitial [B,H,N,P] (optional) fp32.
  * B L G <= 2^25 (else SSD_ERR_UNSUPPORTED).  Workspace: device memory of
- * ssd_delta_rule_backward_workspace_bytes(shape) bytes.
+ * ssd_delta_rule_backward_workspace_bytes(shape) bytes, which serves smaller
+ * prompts too.  It holds the windows' states and their gradients, and q's and k's
+ * gradients by head, in fp32: about 8 H (N P / 64 + N + P) + 620 H bytes a token,
+ * 2.5 GB for 2 x 8192 tokens of 32 heads, N = P = 128.
  */
 ssd_status ssd_delta_rule_backward(const ssd_delta_shape* shape, const ssd_delta_rows* rows, const void* q,
                                    const void* k, const void* v, const void* dt, const void* beta, const float* A,

@@ -1072,8 +1072,12 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a, const floa
 
 // ---------------------------------------------------------------- launches
 int64_t delta_segments(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P, bool bf16);
+int64_t delta_stretch_room(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P);
+static DeltaWs forward_ws(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P, bool bf16) {
+  return delta_ws(B, L, H, N, P, false, delta_segments(B, L, H, N, P, bf16), delta_stretch_room(B, L, H, N, P));
+}
 size_t delta_forward_ws_bytes(int64_t B, int64_t L, int64_t H, int64_t G, int64_t N, int64_t P) {
-  return delta_ws(B, L, H, N, P, false, delta_segments(B, L, H, N, P, true)).total;
+  return forward_ws(B, L, H, N, P, true).total;
 }
 
 template <class M, int NP, bool BACK>
@@ -1142,13 +1146,23 @@ static hipError_t chain_bf16_at(const DeltaArgs& a, const DeltaWs& ws, bool save
 // without stretches and with them, us: 2048 tokens of 8 heads 75 and 59, 8192 of
 // 2 heads 254 and 87, of 20 heads (three stretches) 280 and 247; two stretches
 // take what one does.  Stretches of four windows: 1024 tokens of 8 heads 44 and 54.
+constexpr int64_t kSegWins = 8, kSegMost = 128;  // windows a stretch at least, key columns at most
+static int64_t head_blocks(int64_t P) { return P % 32 == 0 ? P / 32 : P / 16; }
 int64_t delta_segments(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P, bool bf16) {
-  if (!bf16 || N > 128) return 1;
-  const int64_t nw = (L + kDeltaC - 1) / kDeltaC, blocks = B * H * (P % 32 == 0 ? P / 32 : P / 16);
-  int64_t segs = device_cu_count() / blocks;
-  if (segs > nw / 8) segs = nw / 8;
+  if (!bf16 || N > kSegMost) return 1;
+  const int64_t nw = (L + kDeltaC - 1) / kDeltaC;
+  int64_t segs = device_cu_count() / (B * H * head_blocks(P));
+  if (segs > nw / kSegWins) segs = nw / kSegWins;
   if (segs < 3) return 1;
   return (nw + (nw + segs - 1) / segs - 1) / ((nw + segs - 1) / segs);  // none of them empty
+}
+// Stretches that the workspace has room for: no call has more, and no call of
+// more rows, tokens or heads has room for fewer, so that a workspace serves every
+// smaller prompt too.  At most one a compute unit: 25 MB.
+int64_t delta_stretch_room(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P) {
+  if (N > kSegMost) return 0;
+  const int64_t all = B * H * ((L + kDeltaC - 1) / kDeltaC / kSegWins), most = device_cu_count() / head_blocks(P);
+  return all < most ? all : most;
 }
 template <class M, int NP>
 static hipError_t chain_of(const DeltaArgs& a, const DeltaWs& ws, bool save, hipStream_t s) {
@@ -1172,7 +1186,7 @@ hipError_t launch_delta_chain(const DeltaArgs& a, const DeltaWs& ws, bool save, 
 }
 
 hipError_t launch_delta_forward(const DeltaArgs& a, bool bf16, hipStream_t s) {
-  const DeltaWs ws = delta_ws(a.B, a.L, a.H, a.N, a.P, false, delta_segments(a.B, a.L, a.H, a.N, a.P, bf16));
+  const DeltaWs ws = forward_ws(a.B, a.L, a.H, a.N, a.P, bf16);
   if (a.nseq > 0) {
     int* of = reinterpret_cast<int*>(a.ws + ws.wanted);
     hipLaunchKernelGGL(delta_wanted_clear_kernel, flat_grid((a.B * a.L + 255) / 256), dim3(256), 0, s, of, a.B * a.L);

@@ -498,8 +498,8 @@ struct DeltaWs {
   size_t gates, cuts, low_r, low_p, up_r, up_p, wanted, wanted_next, trans, enter, S, D, w, du, dq, dk, part, total;
   int64_t segs, seg_wins;  // stretches of a row that are walked side by side, and their windows
 };
-// segs: see delta_segments().
-inline DeltaWs delta_ws(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P, bool back, int64_t segs = 1) {
+// segs, room: see delta_segments() and delta_stretch_room().
+inline DeltaWs delta_ws(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P, bool back, int64_t segs = 1, int64_t room = 0) {
   DeltaWs o = {};
   o.nw = (L + kDeltaC - 1) / kDeltaC;
   const size_t bhw = (size_t)(B * H * o.nw);
@@ -518,10 +518,8 @@ inline DeltaWs delta_ws(int64_t B, int64_t L, int64_t H, int64_t N, int64_t P, b
     o.wanted_next = take((size_t)kDeltaMaxStates * 4);
     o.segs = segs;
     o.seg_wins = (o.nw + segs - 1) / segs;
-    if (segs > 1) {
-      o.trans = take((size_t)(B * H * (segs - 1) * N * (N + P)) * 4);
-      o.enter = take((size_t)(B * H * segs * N * P) * 4);
-    }
+    o.trans = take((size_t)(room * N * (N + P)) * 4);
+    o.enter = take((size_t)(room * N * P) * 4);
   } else {
     o.up_r = take(bhw * kTriBytes);
     o.up_p = take(bhw * kTriBytes);

@@ -130,6 +130,18 @@ def test_delta_dense_rows(lib, kw, given, ty):
     assert fwd(lib, wide, ty=ty, ws=None) == WS and bwd(lib, wide, ty=ty, ws=None) == WS
 
 
+@pytest.mark.parametrize("N,P", [(128, 64), (128, 128), (64, 32), (16, 16), (128, 256), (96, 48), (256, 64)])
+def test_a_workspace_serves_smaller_prompts(lib, N, P):
+    """The sizes never fall with the rows, the tokens or the heads."""
+    for f in (lib.ssd_delta_rule_workspace_bytes, lib.ssd_delta_rule_backward_workspace_bytes):
+        q = lambda B, L, H: f(SSDDeltaShape(B, L, H, P, N, 1))
+        runs = [[q(1, L, H) for L in range(1, 70000, 63)] for H in (1, 2, 7)]
+        runs += [[q(B, L, 1) for B in range(1, 300)] for L in (64, 1600, 8192)]
+        runs += [[q(2, L, H) for H in range(1, 300)] for L in (64, 1600, 8192)]
+        for r in runs:
+            assert r[0] > 0 and all(a <= b for a, b in zip(r, r[1:]))
+
+
 # ---------------------------------------------------------------- group norm, 8 bits
 
 def gn(lib, rows=6, dim=128, groups=2, x=F, ty=1, z=F, zrow=0, w=F, b=F, flags=1, y=F, mean=None, rstd=F):
