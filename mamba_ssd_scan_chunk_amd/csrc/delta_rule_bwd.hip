@@ -1001,6 +1001,7 @@ __global__ __launch_bounds__(64 * WV, 2) void delta_grad_kernel(DeltaArgs a, Del
       if (on) {
         const int64_t t = row + t0 + lane;
         float raw = M::IO::get(static_cast<const T*>(a.dt)[t * a.rows.dt + h]);
+        const float be = M::IO::get(static_cast<const T*>(a.beta)[t * a.rows.beta + h]);
         if (a.dt_bias) raw += a.dt_bias[h];
         const float step = a.softplus ? softplus2(raw * kLog2e) * kLn2 : raw;
         float d = dg * a.A[h];
@@ -1009,10 +1010,7 @@ __global__ __launch_bounds__(64 * WV, 2) void delta_grad_kernel(DeltaArgs a, Del
         pb = d;
         static_cast<T*>(a.ddt)[t * a.grows.dt + h] = M::IO::put(d);
         float e = sDb[lane];
-        if (a.sigmoid) {
-          const float be = sBeta[lane];
-          e *= be * (1.f - be);
-        }
+        if (a.sigmoid) e *= sBeta[lane] * sigmoid(-be);  // near b = 1 the difference 1 - b has few bits
         static_cast<T*>(a.dbeta)[t * a.grows.beta + h] = M::IO::put(e);
       }
 #pragma unroll
