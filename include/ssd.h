@@ -540,10 +540,14 @@ size_t ssd_layer_norm_backward_workspace_bytes(int64_t rows, int64_t dim);
  * [B,H,N,P], seq_states [nseq,H,N,P] fp32, optional.  N (dstate) and P
  * (headdim) multiples of 16 up to 256, B H < 2^22, B H P < 2^28, B H ceil(L/64) < 2^23,
  * H P, G N and row strides < 2^23 (else SSD_ERR_UNSUPPORTED).  q and k of prompts are 16-byte aligned with row
- * strides in whole 16 bytes.  final_states may be initial_states.  A token with a
- * NaN or infinity makes NaN of its sequence from its window of 64 tokens on, the
- * window's earlier tokens included; other sequences stay as they are (a padded
- * tail that may hold any bits: a sequence of its own).
+ * strides in whole 16 bytes.  final_states may be initial_states.
+ *
+ * A token with a NaN or infinity (in k, dt or beta; in v, of its column) makes no
+ * numbers of its sequence's outputs from itself on and of its states, one in q of
+ * its own output; earlier tokens and other sequences stay as they are, so a padded
+ * tail may hold any bits (the state in front of it: seq_last).  A call that meets
+ * such tokens takes up to six times as long.  Gradients promise less: a sequence
+ * with such a token may have none at any of its tokens, others keep theirs.
  *
  * Precision: fp32 inputs use fp32 matrix instructions.  bf16 inputs enter the
  * products as they are; computed operands (states, u, the triangular matrices

@@ -276,8 +276,14 @@ __global__ __launch_bounds__(256, 2) void delta_prepare_kernel(DeltaArgs a, Delt
       const float4 m = make_float4(-times(e.x, be.x), -times(e.y, be.y), -times(e.z, be.z), -times(e.w, be.w));
       acc = mma4(m, col[k], acc);
     }
+    // a row that holds no number stays so, and does not reach the rows in front of it
+    f32x4_t num;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) num[r] = fabsf(acc[r]) < __builtin_huge_valf() ? acc[r] : 0.f;
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-    col[i] = mma4(*reinterpret_cast<const float4*>(&Md[i][c][4 * g]), acc, zero);
+    col[i] = mma4(*reinterpret_cast<const float4*>(&Md[i][c][4 * g]), num, zero);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) col[i][r] += acc[r] - num[r];
   }
   // what lies between pieces may hold another sequence's NaN by now
   if constexpr (VL) {
@@ -468,6 +474,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs w
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) u[i][r] = be[i][r] * X[i][r];
+      if constexpr (!SAVE) keep_causal<M>(u, X, g);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         float v[8];
@@ -493,7 +500,9 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs w
           const int t = 16 * i + 4 * g + r;
           u[i][r] = !VL || (t >= begin && t < end) ? be[i][r] * X[i][r] : 0.f;
         }
+      float whole = sIn[end - 1];
       if constexpr (!SAVE) {
+        if (keep_causal<M>(u, Q, g)) whole = __builtin_nanf("");
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           float v[8];
@@ -512,7 +521,6 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs w
           }
       }
       // S = e^G_end S + k^T (e^{G_end - G} u)
-      const float whole = sIn[end - 1];
 #pragma unroll
       for (int j = 0; j < NT; ++j) S[j] *= whole;
 #pragma unroll
@@ -572,6 +580,143 @@ struct ChainLds {
   static constexpr int q = 2 * half, x = q + 2 * kRows, total = x + 2 * C * kX;
 };
 
+// Where a wave's columns came to hold no number, it walks their pieces once more,
+// by itself, and writes the outputs of the piece in which a column did so: the NaN
+// or infinity has reached those in front of it (keep_causal).  Later ones hold no
+// number by their state, and every state and other output is right already.
+// Operands come straight from memory, some ten times slower.  `lost`: the lane's
+// column ends so; without packed sequences all is done once each such has been met.
+template <int NP, bool VL>
+__device__ __forceinline__ void mend_outputs(const DeltaArgs& a, const DeltaWs& ws, Pieces pc, f32x4_t* S, bool lost,
+                                             int64_t bh, uint32_t p, int lane) {
+  typedef DeltaB M;
+  typedef DeltaB::One One;
+  typedef DeltaB::Two Two;
+  constexpr int NT = NP / 16, KS = NP / 32;
+  const int c = lane & 15, g = lane >> 4, N = (int)a.N;
+  const int64_t h = bh % a.H, row = bh / a.H * a.L, grp = h / (a.H / a.G);
+  const uint32_t krow = (uint32_t)a.rows.k, qrow = (uint32_t)a.rows.q, yrow = (uint32_t)(a.H * a.P);
+  for (; pc.valid() && (VL || __ballot(lost) != 0); pc.step()) {
+    const int begin = pc.begin, end = pc.end, n = pc.n;
+    const int64_t t0 = row + pc.win * kC, bhw = bh * ws.nw + pc.win;
+    const DeltaGates* gates = reinterpret_cast<const DeltaGates*>(a.ws + ws.gates) + bhw;
+    const uint16_t* kb = static_cast<const uint16_t*>(a.k) + t0 * a.rows.k + grp * N;
+    const uint16_t* qb = static_cast<const uint16_t*>(a.q) + t0 * a.rows.q + grp * N;
+    if (VL && pc.fresh()) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) S[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    auto in_piece = [&](int t) { return t >= begin && t < end; };
+    // rows of the window times the state
+    auto times_state = [&](const uint16_t* base, uint32_t stride, f32x4_t* out) {
+      const __amdgpu_buffer_rsrc_t r = rows_of(base, (uint32_t)n * stride * 2);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) out[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        float v[8];
+        slots(S[2 * s], S[2 * s + 1], v);
+        const Two sb = M::two(v);
+        const int col = 32 * s + 4 * g;
+        const uint32_t off = (c * stride + col) * 2;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const auto lo = __builtin_amdgcn_raw_buffer_load_b64(r, col < N ? off : kNowhere, 16 * i * stride * 2, 0);
+          const auto hi = __builtin_amdgcn_raw_buffer_load_b64(r, col + 16 < N ? off + 32 : kNowhere, 16 * i * stride * 2, 0);
+          One f;
+          f.v = make_uint4(lo[0], lo[1], hi[0], hi[1]);
+          out[i] = M::mma(f, sb, out[i]);
+        }
+        __builtin_amdgcn_sched_barrier(0);  // a few loads at a time: for registers, not time
+      }
+    };
+    f32x4_t X[4], u[4];
+    auto triangle = [&](size_t at, f32x4_t* y) {
+      const char* f = a.ws + at + bhw * kTriBytes;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        float v[8];
+        slots(u[2 * s], u[2 * s + 1], v);
+        const Two ub = M::two(v);
+#pragma unroll
+        for (int i = 2 * s; i < 4; ++i) y[i] = M::mma(M::load(f + low_frag(i, s) * 2048, lane), ub, y[i]);
+      }
+    };
+    auto strengthen = [&] {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = 16 * i + 4 * g + r;
+          u[i][r] = in_piece(t) ? gates->beta[t] * X[i][r] : 0.f;
+        }
+    };
+    times_state(kb, krow, X);
+    uint32_t q[16];
+    load_column<IoBF16>(static_cast<const uint16_t*>(a.v) + t0 * a.rows.v + h * a.P, (uint32_t)a.rows.v, p, n, begin, end, g, q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 16 * i + 4 * g + r;
+        X[i][r] = in_piece(t) ? fmaf(-gates->kin[t], X[i][r], bf16_bits_to_f32(q[4 * i + r])) : 0.f;
+      }
+    strengthen();
+    keep_causal<M>(u, X, g);
+    triangle(ws.low_r, X);
+    strengthen();
+    if (!all_numbers<M>(u)) {
+      times_state(qb, qrow, X);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) X[i][r] *= gates->qin[16 * i + 4 * g + r];
+      const bool met = keep_causal<M>(u, X, g);
+      triangle(ws.low_p, X);
+      const __amdgpu_buffer_rsrc_t yr =
+          rows_of(static_cast<uint16_t*>(a.y) + (t0 * a.H + h) * a.P, (uint32_t)n * yrow * 2);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const uint32_t t = Column::row(e) + 4 * g;
+        __builtin_amdgcn_raw_buffer_store_b16(IoBF16::put(X[e / 4][e % 4]), yr,
+                                              met && in_piece((int)t) ? (t * yrow + p) * 2 : kNowhere, 0, 0);
+      }
+      if (met) {
+        lost = false;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) S[j][r] = __builtin_nanf("");
+      }
+    }
+    const float whole = gates->in[end - 1];
+    Two ub[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int t = 32 * s + 16 * (e / 4) + 4 * g + e % 4;
+        v[e] = in_piece(t) ? u[2 * s + e / 4][e % 4] * gates->kout[t] : 0.f;
+      }
+      ub[s] = M::two(v);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      S[j] *= whole;
+      load_column<IoBF16>(kb, krow, min(16 * j, N - 16) + c, n, begin, end, g, q);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint32_t* w = q + 8 * s;
+        One f;
+        f.v = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+        S[j] = M::mma(f, ub[s], S[j]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
 // Rows too long and too few to fill the chip are cut into stretches, walked side
 // by side in two passes.  A stretch maps the state in front of it to M S + R:
 // kStretch walks it from the unit matrix (N more columns, without values) and
@@ -603,8 +748,11 @@ __global__ __launch_bounds__(MODE == kOut ? chain_threads(C) : 128 * C, C) void 
   const Wanted wanted = VL && OUT ? wanted_states(a, ws) : Wanted{};
   Pieces pc;
   const int64_t w0 = MODE == kSave ? 0 : seg * ws.seg_wins;
-  pc.first(VL ? reinterpret_cast<const Cuts*>(a.ws + ws.cuts) + b * ws.nw : nullptr, w0,
-           MODE == kSave || w0 + ws.seg_wins > ws.nw ? ws.nw : w0 + ws.seg_wins, a.L);
+  auto first_piece = [&] {
+    pc.first(VL ? reinterpret_cast<const Cuts*>(a.ws + ws.cuts) + b * ws.nw : nullptr, w0,
+             MODE == kSave || w0 + ws.seg_wins > ws.nw ? ws.nw : w0 + ws.seg_wins, a.L);
+  };
+  first_piece();
 
   constexpr int SG = OUT ? first_stager(C) : C;
   if (wave >= SG) {
@@ -646,6 +794,7 @@ __global__ __launch_bounds__(MODE == kOut ? chain_threads(C) : 128 * C, C) void 
       }
       __syncthreads();
     }
+    if (OUT) __syncthreads();  // the outputs'
     return;
   }
   if (wave >= 2 * C) return;
@@ -718,6 +867,8 @@ __global__ __launch_bounds__(MODE == kOut ? chain_threads(C) : 128 * C, C) void 
       pc.step();
       __syncthreads();
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // a column wave may write them again
+    __syncthreads();
     return;
   }
 
@@ -726,16 +877,29 @@ __global__ __launch_bounds__(MODE == kOut ? chain_threads(C) : 128 * C, C) void 
   f32x4_t S[NT];
   const float* from = a.h0 ? a.h0 + bh * N * a.P : nullptr;
   if (MODE == kOut && segs > 1) from = reinterpret_cast<const float*>(a.ws + ws.enter) + (bh * segs + seg) * N * a.P;
+  auto enter = [&](f32x4_t* s) {
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int nn = 16 * j + 4 * g + r;
-      if (MODE == kStretch) S[j][r] = unit && nn == (int)p ? 1.f : 0.f;
-      else S[j][r] = from && nn < N ? from[nn * a.P + p] : 0.f;
-    }
+      for (int r = 0; r < 4; ++r) {
+        const int nn = 16 * j + 4 * g + r;
+        if (MODE == kStretch) s[j][r] = unit && nn == (int)p ? 1.f : 0.f;
+        else s[j][r] = from && nn < N ? from[nn * a.P + p] : 0.f;
+      }
+  };
+  enter(S);
   const uint32_t vrow = (uint32_t)a.rows.v, voff = 4 * g * vrow + p;
   const uint16_t* vb = static_cast<const uint16_t*>(a.v) + row * a.rows.v + h * a.P;
+  // of the lane's column: a token that is no number leaves none in its state, to the end of its sequence
+  auto numbers = [&] {
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) sum += (fabsf(S[j][0]) + fabsf(S[j][1])) + (fabsf(S[j][2]) + fabsf(S[j][3]));
+    sum += __shfl_xor(sum, 16, 64);
+    sum += __shfl_xor(sum, 32, 64);
+    return sum < M::kMost;
+  };
+  bool again = false;
   Column vn;
   vn.load(vb + pc.win * kC * a.rows.v, vrow, voff, unit ? 0 : pc.n);
   __syncthreads();
@@ -748,6 +912,7 @@ __global__ __launch_bounds__(MODE == kOut ? chain_threads(C) : 128 * C, C) void 
     const float *sBeta = gt, *sKin = gt + kC, *sKout = gt + 3 * kC, *sIn = gt + 4 * kC;
     char* x = lds + Lay::x + ((step & 1) * C + wave) * Lay::kX;
     if (VL && pc.fresh()) {
+      if (OUT) again |= __ballot(!numbers()) != 0;
 #pragma unroll
       for (int j = 0; j < NT; ++j) S[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
@@ -803,7 +968,7 @@ __global__ __launch_bounds__(MODE == kOut ? chain_threads(C) : 128 * C, C) void 
       for (int j = 0; j < NT; ++j) kT[s][j] = M::transposed(kt + 32 * s * LP + 16 * j, LP, lane);
     __builtin_amdgcn_sched_barrier(0);
     // X = v - e^G k S; in packed rows the others' values are left out (what is behind the row reads as zero)
-    float bx[4][4];
+    f32x4_t bx[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -860,7 +1025,18 @@ __global__ __launch_bounds__(MODE == kOut ? chain_threads(C) : 128 * C, C) void 
     }
     __syncthreads();
   }
-  if (OUT && a.hfin && seg == segs - 1) put_state<NT>(a.hfin + bh * N * a.P, N, P, 4 * g * P + p, S);
+  if constexpr (OUT) {
+    __syncthreads();  // the outputs are written
+    const bool lost = !numbers();
+    again |= __ballot(lost) != 0;
+    f32x4_t S0[NT];
+    if (__builtin_expect(again, 0)) enter(S0);  // before the last state may take its place
+    if (a.hfin && seg == segs - 1) put_state<NT>(a.hfin + bh * N * a.P, N, P, 4 * g * P + p, S);
+    if (__builtin_expect(again, 0)) {
+      first_piece();
+      mend_outputs<NP, VL>(a, ws, pc, S0, lost, bh, p, lane);
+    }
+  }
   if constexpr (MODE == kStretch) {
     const uint32_t cols = (uint32_t)N + P;
     put_state<NT>(reinterpret_cast<float*>(a.ws + ws.trans) + (bh * segs + seg) * N * cols, N, cols,

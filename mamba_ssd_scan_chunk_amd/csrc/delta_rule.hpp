@@ -42,6 +42,7 @@ typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));  // copied as a val
 
 // One: an operand of inputs.  Two: of computed values.
 struct DeltaB {
+  static constexpr float kMost = 3.3961775e38f;  // computed values from here on are infinite as bf16
   typedef IoBF16 IO;
   typedef OpBF16::Frag One;
   struct Two { One hi, lo; };
@@ -100,6 +101,7 @@ struct DeltaB {
   }
 };
 struct DeltaF {
+  static constexpr float kMost = __builtin_huge_valf();
   typedef IoF32 IO;
   typedef OpF32::Frag One;
   typedef OpF32::Frag Two;
@@ -280,6 +282,57 @@ __device__ __forceinline__ void slots(const f32x4_t& lo, const f32x4_t& hi, floa
     o[r] = lo[r];
     o[4 + r] = hi[r];
   }
+}
+
+// ---- causality of values that are not numbers ----
+// A product over tokens multiplies every token's value, those behind a row with
+// zeros, and zero times a NaN or infinity is NaN.  So that a token reaches no
+// earlier one, its values and all behind it in the column are taken out of such
+// an operand and put in where a row only adds.  v: of tokens 16 i + 4 g + r.
+template <class M>
+__device__ __forceinline__ bool all_numbers(const f32x4_t* v) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s += (fabsf(v[i][0]) + fabsf(v[i][1])) + (fabsf(v[i][2]) + fabsf(v[i][3]));
+  return __builtin_expect(__ballot(!(s < M::kMost)) == 0, 1);
+}
+// Of the lane's column, the first token whose value cannot be an operand (kC:
+// none).  Whole-register masks here and below: compares would hold two scalars
+// each and push a chain's own out.
+template <class M>
+__device__ __forceinline__ int first_bad(const f32x4_t* v, int g) {
+  int first = kC;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      int good = ((int)(__float_as_uint(v[i][r]) & 0x7fffffffu) - (int)__builtin_bit_cast(uint32_t, M::kMost)) >> 31;
+      asm("" : "+v"(good));
+      first = min(first, 16 * i + 4 * g + r + (good & kC));
+    }
+  first = min(first, __shfl_xor(first, 16, 64));
+  return min(first, __shfl_xor(first, 32, 64));
+}
+// Values from token `first` on become `to`.
+__device__ __forceinline__ void set_from(f32x4_t* v, int first, int g, float to) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      int on = (16 * i + 4 * g + r - first) >> 31;
+      asm("" : "+v"(on));
+      v[i][r] = __int_as_float((__float_as_int(v[i][r]) & on) | (__float_as_int(to) & ~on));
+    }
+}
+// Makes v an operand and x, which the product is added to, NaN where v is none.
+// Returns whether the lane's column has such a token.
+template <class M>
+__device__ __forceinline__ bool keep_causal(f32x4_t* v, f32x4_t* x, int g) {
+  if (all_numbers<M>(v)) return false;
+  const int first = first_bad<M>(v, g);
+  set_from(x, first, g, __builtin_nanf(""));
+  set_from(v, first, g, 0.f);
+  return first < kC;
 }
 
 // ---- staging by a chain's helper waves ----

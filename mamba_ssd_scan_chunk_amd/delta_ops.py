@@ -58,7 +58,8 @@ def ssd_delta_rule(q, k, v, dt, beta, A, dt_bias=None, softplus=True, sigmoid=Tr
     with q and k of unit length (``qk_norm``) and q times ``scale`` (default
     N^-1/2).  Returns (y, final_states or None), and with seq_last (see
     ssd_forward_varlen) also seq_states [nseq,H,N,P].  final_states may be the
-    initial_states tensor."""
+    initial_states tensor.  A token that is no number makes none of its
+    sequence's outputs from itself on; earlier ones stay as they are."""
     if stream is not None:
         return _on_stream(ssd_delta_rule, locals())
     sh, rows, flags, scale = _delta_inputs(q, k, v, dt, beta, A, dt_bias, softplus, sigmoid, qk_norm, scale, 2)
