@@ -635,7 +635,8 @@ ssd_status ssd_group_norm(int64_t rows, int64_t dim, int64_t groups, const void*
  * forward's: dx [rows,dim] and dz rows (dz_row; given exactly when z is) in
  * `in`; dw and dbias (optional) fp32, like w.  Where x_scale is given, x (and z,
  * with z_scale; both or neither) are in 8 bits as ssd_pack8 leaves them: x, z
- * int8 [rows,dim] dense, the scales bf16 [rows, ceil(dim/64)].  Workspace:
+ * int8 [rows,dim] dense, the scales bf16 [rows, ceil(dim/64)]; derivatives are at
+ * the values these stand for, mean and rstd as they are given.  Workspace:
  * ssd_group_norm_backward_workspace_bytes(rows, dim, groups) bytes.
  */
 ssd_status ssd_group_norm_backward(int64_t rows, int64_t dim, int64_t groups, const void* dy, ssd_dtype in,
