@@ -553,7 +553,8 @@ size_t ssd_layer_norm_backward_workspace_bytes(int64_t rows, int64_t dim);
  * products as they are; computed operands (states, u, the triangular matrices
  * of a window of 64 tokens) enter as the sum of two bf16 values, 16 bits;
  * sums and states are fp32.  fp32 outputs of bf16 inputs are so within 1e-5 of
- * their values (2-norm), bf16 ones one rounding.
+ * their values (2-norm; the gradients of A and dt_bias, sums of both signs, of the
+ * values and the terms), bf16 ones one rounding.  Widen the inputs to fp32 for more.
  *
  * Workspace: device memory of ssd_delta_rule_workspace_bytes(shape) bytes, asked
  * for on the device of the call (it depends on the compute units).  It serves

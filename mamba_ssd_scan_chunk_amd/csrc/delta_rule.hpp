@@ -16,8 +16,10 @@
 //
 // Matrix operands.  bf16 inputs enter as they are; what is computed (states,
 // corrected values, R, P) enters as the sum of two bf16 values, 16 bits, and
-// every sum and the states themselves are fp32, so that states and sums over
-// tokens are 4e-6 from the 64-bit values, not 4e-3 as with one bf16 operand.
+// every sum and the states themselves are fp32, so that states are 2 to 3e-6 and
+// sums over tokens up to 6e-6 from the 64-bit values, where one bf16 operand would
+// be 2^-9 off.  fp32 products (1 to 2e-7) have an eighth of the rate: a caller who
+// wants them passes fp32 inputs.
 // Unit length goes into the fp32 scalars of a row, never into rounded rows.
 // fp32 inputs use the fp32 matrix instructions throughout.
 #pragma once
