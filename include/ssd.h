@@ -619,8 +619,8 @@ size_t ssd_delta_rule_backward_workspace_bytes(const ssd_delta_shape* shape);
  *                      or y = act(xh w + bias)   (SSD_GROUP_SILU, without a gate behind)
  * x [rows,dim] dense, z rows (z_row), y [rows,dim] in `in`; w, bias (optional)
  * fp32 [dim], or [S] for all groups (SSD_GROUP_SHARED); mean (NULL exactly for
- * RMS) and rstd fp32 [rows,groups].  S <= 16384, rows groups < 2^31 (else
- * SSD_ERR_UNSUPPORTED).
+ * RMS) and rstd fp32 [rows,groups].  S <= 16384, dim <= 2^24, rows groups < 2^31,
+ * strides of several rows < 2^25 (else SSD_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------ */
 #define SSD_GROUP_RMS 1
 #define SSD_GROUP_GATE_FIRST 2
@@ -654,7 +654,8 @@ size_t ssd_group_norm_backward_workspace_bytes(int64_t rows, int64_t dim, int64_
  * 127 (0 where s = 0); they come back as q s.  A block with an infinity or NaN has
  * s = NaN and comes back as NaN.  q int8 [rows,dim], scale bf16
  * [rows, ceil(dim/64)], dense, of any alignment to their elements.
- * rows < 2^31, dim <= 2^24, rows ceil(dim/64) < 2^36 (else SSD_ERR_UNSUPPORTED).
+ * rows < 2^31, dim <= 2^24, rows ceil(dim/64) < 2^36, strides of several rows
+ * < 2^25 (else SSD_ERR_UNSUPPORTED).
  */
 ssd_status ssd_pack8(int64_t rows, int64_t dim, const void* x, int64_t x_row, ssd_dtype in, int8_t* q, void* scale,
                      void* stream);

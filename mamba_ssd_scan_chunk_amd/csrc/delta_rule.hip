@@ -48,7 +48,7 @@ __device__ __forceinline__ float times(float e, float b) { return e != 0.f ? e *
 // another's.  Bound by the latency of its few dependent parts: all of a
 // wave's loads (of 128 key columns) are asked for together, and one matrix in
 // LDS leaves five blocks a compute unit.  2 x 8192 tokens of 32 heads, bf16, N =
-// 128: 117 us; for the gradients of 2 x 2048: 59; a lone block takes some 16.
+// 128: 117 us; for the gradients of 2 x 2048: 49; a lone block takes some 17.
 template <class M, int NP, bool BACK, bool VL>
 __global__ __launch_bounds__(256, 2) void delta_prepare_kernel(DeltaArgs a, DeltaWs ws) {
   typedef typename M::IO::type T;
@@ -567,10 +567,12 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaArgs a, DeltaWs w
 // piece before, from the operands (state, u) that the column waves left in LDS.
 // Two column waves a block: with one, k and q are staged twice as often; four
 // leave half of the chip idle at 64 heads of 128 columns.  Bound by the column
-// waves' latency, 2.4 us a window of which their own products, roundings and LDS
+// waves' latency, 2.2 us a window of which their own products, roundings and LDS
 // reads take 1.75; the matrix units are busy 8 to 18%.  2 x 8192 tokens of 32
-// heads, N = P = 128: 300 us (one kernel of waves that stage for themselves 2370),
-// the whole call 1.0 TB/s of its bytes.
+// heads, N = P = 128: 280 us (one kernel of waves that stage for themselves 2370),
+// the whole call 1.0 TB/s of its bytes.  Looking at the last state for what is no
+// number (mend_outputs) costs 1 to 2 us a call; looking at every piece's values in
+// its column and output waves cost 6 of these, and 13 of 180 in packed rows.
 template <int NP, int C>
 struct ChainLds {
   static constexpr int kPitch = NP + 24;  // rows as the products read them begin in different banks

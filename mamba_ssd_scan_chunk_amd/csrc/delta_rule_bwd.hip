@@ -15,12 +15,13 @@
 // and k.dk the pairs on one side of t would cancel only up to the products'
 // rounding; from one Z they cancel exactly.
 //
-// Five launches: the preparation and the forward chain (delta_rule.hip), which
+// Six launches: the preparation and the forward chain (delta_rule.hip), which
 // leave the states in front of the windows and w; delta_reverse_kernel, a wave
 // 16 value columns as there, which leaves D of every window and du;
-// delta_grad_kernel, a block a (window, head), all windows at once; and
+// delta_grad_kernel, a block a (window, head), all windows at once;
 // delta_finish_kernel, which adds the heads of a key group and takes the
-// gradients through the unit length.
+// gradients through the unit length; and delta_param_kernel, which adds dA and the
+// bias' gradient over the windows.
 #include <type_traits>
 
 #include "delta_rule.hpp"
