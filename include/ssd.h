@@ -554,7 +554,9 @@ size_t ssd_layer_norm_backward_workspace_bytes(int64_t rows, int64_t dim);
  * of a window of 64 tokens) enter as the sum of two bf16 values, 16 bits;
  * sums and states are fp32.  fp32 outputs of bf16 inputs are so within 1e-5 of
  * their values (2-norm; the gradients of A and dt_bias, sums of both signs, of the
- * values and the terms), bf16 ones one rounding.  Widen the inputs to fp32 for more.
+ * values and the terms), bf16 ones one rounding.  SSD_DELTA_MMA_F32 gives bf16
+ * inputs fp32 products as fp32 ones have them (1e-6), for 2.5 to 5 times the time,
+ * long rows of few heads up to 20; a single token has no others.
  *
  * Workspace: device memory of ssd_delta_rule_workspace_bytes(shape) bytes, asked
  * for on the device of the call (it depends on the compute units).  It serves
@@ -569,6 +571,7 @@ typedef struct {
 #define SSD_DELTA_SOFTPLUS 1
 #define SSD_DELTA_SIGMOID 2
 #define SSD_DELTA_QK_NORM 4
+#define SSD_DELTA_MMA_F32 32 /* bf16 inputs: fp32 matrix instructions for every product */
 
 ssd_status ssd_delta_rule(const ssd_delta_shape* shape, const ssd_delta_rows* rows, const void* q, const void* k,
                           const void* v, const void* dt, const void* beta, const float* A, const float* dt_bias,

@@ -61,7 +61,7 @@ class SSDDeltaRows(ctypes.Structure):
                 ("beta", ctypes.c_int64)]
 
 
-SSD_DELTA_SOFTPLUS, SSD_DELTA_SIGMOID, SSD_DELTA_QK_NORM = 1, 2, 4
+SSD_DELTA_SOFTPLUS, SSD_DELTA_SIGMOID, SSD_DELTA_QK_NORM, SSD_DELTA_MMA_F32 = 1, 2, 4, 32
 SSD_GROUP_RMS, SSD_GROUP_GATE_FIRST, SSD_GROUP_SILU, SSD_GROUP_SHARED = 1, 2, 4, 8
 
 _P = ctypes.c_void_p

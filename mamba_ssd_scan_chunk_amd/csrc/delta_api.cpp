@@ -50,7 +50,7 @@ ssd_status delta_inputs(const ssd_delta_shape* s, const ssd_delta_rows* rows, co
                         const void* v, const void* dt, const void* beta, const float* A, const float* dt_bias,
                         int flags, float scale, ssd_dtype in, bool step, ssd::DeltaArgs* a) {
   SSD_TRY(check_dtype(in));
-  if (flags & ~(SSD_DELTA_SOFTPLUS | SSD_DELTA_SIGMOID | SSD_DELTA_QK_NORM)) return SSD_ERR_UNSUPPORTED;
+  if (flags & ~(SSD_DELTA_SOFTPLUS | SSD_DELTA_SIGMOID | SSD_DELTA_QK_NORM | SSD_DELTA_MMA_F32)) return SSD_ERR_UNSUPPORTED;
   if (!q || !k || !v || !dt || !beta || !A) return SSD_ERR_NULL;
   SSD_TRY(delta_rows(s, rows, &a->rows));
   const uintptr_t e = elem(in);
@@ -69,6 +69,7 @@ ssd_status delta_inputs(const ssd_delta_shape* s, const ssd_delta_rows* rows, co
   a->softplus = flags & SSD_DELTA_SOFTPLUS;
   a->sigmoid = flags & SSD_DELTA_SIGMOID;
   a->qk_norm = flags & SSD_DELTA_QK_NORM;
+  a->f32_products = flags & SSD_DELTA_MMA_F32;
   a->scale = scale;
   a->q = q;
   a->k = k;

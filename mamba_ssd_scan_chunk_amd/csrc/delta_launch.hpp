@@ -20,6 +20,7 @@ struct DeltaArgs {
   int64_t B, L, H, G, N, P;
   DeltaRows rows, grows;
   bool softplus, sigmoid, qk_norm;
+  bool f32_products;  // of bf16 inputs; fp32 ones have no others
   float scale;
   const void *q, *k, *v, *dt, *beta;
   const float *A, *dt_bias;  // dt_bias may be null

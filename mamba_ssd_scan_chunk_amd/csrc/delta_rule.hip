@@ -339,7 +339,7 @@ constexpr size_t chain_lds() {
   return (size_t)(SAVE ? 1 : 2) * kC * chain_pitch<M, NP>() * sizeof(typename M::IO::type) + 5 * kC * 4;
 }
 
-// fp32 inputs, and bf16 ones of more than 128 key columns, whose state fills a
+// fp32 products, and bf16 inputs of more than 128 key columns, whose state fills a
 // wave's registers.  Of four waves one or two hold columns, the others bring the
 // next piece's k, q and gates.  SAVE: for the gradients, the state in front of
 // every window and w instead of y.  Bound by the length of the chain, about 6 us a
@@ -1271,9 +1271,14 @@ static hipError_t prepare_at(const DeltaArgs& a, const DeltaWs& ws, hipStream_t 
          : a.N <= 128 ? prepare<M, 128, BACK>(a, ws, s)
                       : prepare<M, 256, BACK>(a, ws, s);
 }
+template <class M>
+static hipError_t prepare_of(const DeltaArgs& a, const DeltaWs& ws, bool back, hipStream_t s) {
+  return back ? prepare_at<M, true>(a, ws, s) : prepare_at<M, false>(a, ws, s);
+}
 hipError_t launch_delta_prepare(const DeltaArgs& a, const DeltaWs& ws, bool back, bool bf16, hipStream_t s) {
-  if (bf16) return back ? prepare_at<DeltaB, true>(a, ws, s) : prepare_at<DeltaB, false>(a, ws, s);
-  return back ? prepare_at<DeltaF, true>(a, ws, s) : prepare_at<DeltaF, false>(a, ws, s);
+  return !bf16            ? prepare_of<DeltaF>(a, ws, back, s)
+         : a.f32_products ? prepare_of<DeltaW>(a, ws, back, s)
+                          : prepare_of<DeltaB>(a, ws, back, s);
 }
 
 template <class M, int NP, bool VL, bool SAVE>
@@ -1357,6 +1362,7 @@ static hipError_t chain_at(const DeltaArgs& a, const DeltaWs& ws, bool save, hip
 }
 hipError_t launch_delta_chain(const DeltaArgs& a, const DeltaWs& ws, bool save, bool bf16, hipStream_t s) {
   if (!bf16) return chain_at<DeltaF>(a, ws, save, s);
+  if (a.f32_products) return chain_at<DeltaW>(a, ws, save, s);
   if (a.N <= 32) return chain_bf16_at<32>(a, ws, save, s);
   if (a.N <= 64) return chain_bf16_at<64>(a, ws, save, s);
   if (a.N <= 128) return chain_bf16_at<128>(a, ws, save, s);
@@ -1364,7 +1370,7 @@ hipError_t launch_delta_chain(const DeltaArgs& a, const DeltaWs& ws, bool save, 
 }
 
 hipError_t launch_delta_forward(const DeltaArgs& a, bool bf16, hipStream_t s) {
-  const DeltaWs ws = forward_ws(a.B, a.L, a.H, a.N, a.P, bf16);
+  const DeltaWs ws = forward_ws(a.B, a.L, a.H, a.N, a.P, bf16 && !a.f32_products);
   if (a.nseq > 0) {
     int* of = reinterpret_cast<int*>(a.ws + ws.wanted);
     hipLaunchKernelGGL(delta_wanted_clear_kernel, flat_grid((a.B * a.L + 255) / 256), dim3(256), 0, s, of, a.B * a.L);

@@ -18,11 +18,13 @@
 // corrected values, R, P) enters as the sum of two bf16 values, 16 bits, and
 // every sum and the states themselves are fp32, so that states are 2 to 3e-6 and
 // sums over tokens up to 6e-6 from the 64-bit values, where one bf16 operand would
-// be 2^-9 off.  fp32 products (1 to 2e-7) have an eighth of the rate: a caller who
-// wants them passes fp32 inputs.
+// be 2^-9 off.  fp32 products (1 to 2e-7) have an eighth of the rate; a caller who
+// wants them asks for them (DeltaW) or passes fp32 inputs.
 // Unit length goes into the fp32 scalars of a row, never into rounded rows.
 // fp32 inputs use the fp32 matrix instructions throughout.
 #pragma once
+
+#include <type_traits>
 
 #include "delta_launch.hpp"
 #include "layer_device.hpp"
@@ -102,9 +104,9 @@ struct DeltaB {
     return lds_frag_tr(tile, pitch, lane);
   }
 };
-struct DeltaF {
+// fp32 products: of fp32 inputs, and of bf16 ones where the caller asks for them.
+struct Fp32Products {
   static constexpr float kMost = __builtin_huge_valf();
-  typedef IoF32 IO;
   typedef OpF32::Frag One;
   typedef OpF32::Frag Two;
   __device__ __forceinline__ static Two two(const float* s) { return OpF32::from_f32(s); }
@@ -121,6 +123,9 @@ struct DeltaF {
     *reinterpret_cast<float4*>(p + 1024 + 16 * lane) = t.hi;
   }
   __device__ __forceinline__ static One row8(const float* p) { return Lds<OpF32>::load8(p); }
+};
+struct DeltaF : Fp32Products {
+  typedef IoF32 IO;
   __device__ __forceinline__ static One rows8(__amdgpu_buffer_rsrc_t r, uint32_t lane, uint32_t row) {
     One f;
     f.lo = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(r, lane, row, 0));
@@ -136,10 +141,28 @@ struct DeltaF {
     return f;
   }
 };
+struct DeltaW : Fp32Products {
+  typedef IoBF16 IO;
+  __device__ __forceinline__ static One wide(const uint4& v) {
+    One f;
+    f.lo = make_float4(bf16_bits_to_f32(v.x & 0xffffu), __uint_as_float(v.x & 0xffff0000u),
+                       bf16_bits_to_f32(v.y & 0xffffu), __uint_as_float(v.y & 0xffff0000u));
+    f.hi = make_float4(bf16_bits_to_f32(v.z & 0xffffu), __uint_as_float(v.z & 0xffff0000u),
+                       bf16_bits_to_f32(v.w & 0xffffu), __uint_as_float(v.w & 0xffff0000u));
+    return f;
+  }
+  __device__ __forceinline__ static One rows8(__amdgpu_buffer_rsrc_t r, uint32_t lane, uint32_t row) {
+    return wide(DeltaB::rows8(r, lane, row).v);
+  }
+  __device__ __forceinline__ static One transposed(const uint16_t* tile, int pitch, int lane) {
+    return wide(DeltaB::transposed(tile, pitch, lane).v);
+  }
+};
 // Slots 0..3 of p0, 4..7 of p1.
 template <class M>
 __device__ __forceinline__ typename M::One lds_4x2(const typename M::IO::type* p0, const typename M::IO::type* p1) {
-  if constexpr (sizeof(typename M::IO::type) == 2) return Lds<OpBF16>::load4x2(p0, p1);
+  if constexpr (std::is_same<M, DeltaW>::value) return M::wide(Lds<OpBF16>::load4x2(p0, p1).v);
+  else if constexpr (sizeof(typename M::IO::type) == 2) return Lds<OpBF16>::load4x2(p0, p1);
   else return Lds<OpF32>::load4x2(p0, p1);
 }
 

@@ -22,8 +22,6 @@
 // delta_finish_kernel, which adds the heads of a key group and takes the
 // gradients through the unit length; and delta_param_kernel, which adds dA and the
 // bias' gradient over the windows.
-#include <type_traits>
-
 #include "delta_rule.hpp"
 
 namespace ssd {
@@ -31,7 +29,7 @@ namespace ssd {
 constexpr int kTP = kC + 4;
 
 // ---------------------------------------------------------------- the chain, back to front
-// fp32 inputs, and bf16 ones of more than 128 key columns; the waves as in the
+// fp32 products, and bf16 inputs of more than 128 key columns; the waves as in the
 // forward's general chain.  2 x 777 tokens, N = 48, P = 80, fp32: 96 us, the
 // length of the chain (224 where every wave staged for itself).
 template <class M, int NP>
@@ -560,10 +558,10 @@ template <> struct GradTile<DeltaB> {
   __device__ __forceinline__ DeltaB::Two u(int t, int col) const { return two(1, t, col); }
   __device__ __forceinline__ DeltaB::Two dw(int t, int col) const { return two(3, t, col); }
 };
-template <> struct GradTile<DeltaF> {
+struct GradTileF {
   static constexpr int kPitch = 68, kPlane = kC * kPitch;
   float* p;  // dy, u, dw
-  __device__ __forceinline__ explicit GradTile(char* lds) : p(reinterpret_cast<float*>(lds)) {}
+  __device__ __forceinline__ explicit GradTileF(char* lds) : p(reinterpret_cast<float*>(lds)) {}
   static constexpr size_t bytes() { return (size_t)3 * kPlane * 4; }
   __device__ __forceinline__ void put8(int t, int col, const float* dy, const float* u, const float* dw) {
     float* q = p + t * kPitch + col;
@@ -577,6 +575,8 @@ template <> struct GradTile<DeltaF> {
     return DeltaF::row8(p + 2 * kPlane + t * kPitch + col);
   }
 };
+template <> struct GradTile<DeltaF> : GradTileF { using GradTileF::GradTileF; };
+template <> struct GradTile<DeltaW> : GradTileF { using GradTileF::GradTileF; };
 // The token-by-token matrices as left operands: M1 lower, M2 upper triangular, M3 whole.
 constexpr int kGradFrags = 2 * kTriFrags + 8;
 template <class M, int WV>
@@ -1145,7 +1145,7 @@ static hipError_t reverse_bf16(const DeltaArgs& a, const DeltaWs& ws, hipStream_
 }
 template <class M, int NP, bool VL>
 static hipError_t reverse_at(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) {
-  if constexpr (sizeof(typename M::IO::type) == 2 && NP <= 128)
+  if constexpr (std::is_same<M, DeltaB>::value && NP <= 128)
     return a.P % 32 == 0 ? reverse_bf16<NP, 2, VL>(a, ws, s) : reverse_bf16<NP, 1, VL>(a, ws, s);
   else
     return reverse<M, NP, VL>(a, ws, s);
@@ -1183,13 +1183,16 @@ static hipError_t back_of(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) 
   return hipGetLastError();
 }
 
+template <class M>
+static hipError_t back_as(const DeltaArgs& a, const DeltaWs& ws, hipStream_t s) {
+  return a.seq_idx ? back_of<M, true>(a, ws, s) : back_of<M, false>(a, ws, s);
+}
 hipError_t launch_delta_backward(const DeltaArgs& a, bool bf16, hipStream_t s) {
   const DeltaWs ws = delta_ws(a.B, a.L, a.H, a.N, a.P, true);
   hipError_t e = launch_delta_prepare(a, ws, true, bf16, s);
   if (e == hipSuccess) e = launch_delta_chain(a, ws, true, bf16, s);
   if (e != hipSuccess) return e;
-  if (bf16) return a.seq_idx ? back_of<DeltaB, true>(a, ws, s) : back_of<DeltaB, false>(a, ws, s);
-  return a.seq_idx ? back_of<DeltaF, true>(a, ws, s) : back_of<DeltaF, false>(a, ws, s);
+  return !bf16 ? back_as<DeltaF>(a, ws, s) : a.f32_products ? back_as<DeltaW>(a, ws, s) : back_as<DeltaB>(a, ws, s);
 }
 
 }  // namespace ssd

@@ -7,9 +7,10 @@ from typing import Dict, Optional
 
 import torch
 
-from ._lib import (SSD_DELTA_QK_NORM, SSD_DELTA_SIGMOID, SSD_DELTA_SOFTPLUS, SSD_GROUP_GATE_FIRST, SSD_GROUP_RMS,
-                   SSD_GROUP_SHARED, SSD_GROUP_SILU, SSDDeltaRows, SSDDeltaShape, check, load_library)
-from .ops import _DT, _F32, _IO, _on_stream, _opt, _ptr, _req, _req_rows, _seq_states, _stream, _workspace
+from ._lib import (MMA, SSD_DELTA_MMA_F32, SSD_DELTA_QK_NORM, SSD_DELTA_SIGMOID, SSD_DELTA_SOFTPLUS,
+                   SSD_GROUP_GATE_FIRST, SSD_GROUP_RMS, SSD_GROUP_SHARED, SSD_GROUP_SILU, SSDDeltaRows, SSDDeltaShape,
+                   check, load_library)
+from .ops import _DT, _F32, _IO, _mma, _on_stream, _opt, _ptr, _req, _req_rows, _seq_states, _stream, _workspace
 
 
 def _here(t: torch.Tensor) -> None:
@@ -19,7 +20,7 @@ def _here(t: torch.Tensor) -> None:
         raise ValueError(f"tensors are on {t.device}, the current device is {torch.cuda.current_device()}")
 
 
-def _delta_inputs(q, k, v, dt, beta, A, dt_bias, softplus, sigmoid, qk_norm, scale, lead):
+def _delta_inputs(q, k, v, dt, beta, A, dt_bias, softplus, sigmoid, qk_norm, scale, lead, mma="bf16"):
     """Checks the inputs shared by the delta rule's calls; returns the shape
     struct, the row strides, the flags and the scale."""
     tok = tuple(v.shape[:lead])
@@ -34,7 +35,8 @@ def _delta_inputs(q, k, v, dt, beta, A, dt_bias, softplus, sigmoid, qk_norm, sca
     _req(A, "A", (H,), _F32)
     _opt(dt_bias, "dt_bias", (H,), _F32)
     _here(v)
-    flags = SSD_DELTA_SOFTPLUS * bool(softplus) | SSD_DELTA_SIGMOID * bool(sigmoid) | SSD_DELTA_QK_NORM * bool(qk_norm)
+    flags = (SSD_DELTA_SOFTPLUS * bool(softplus) | SSD_DELTA_SIGMOID * bool(sigmoid) | SSD_DELTA_QK_NORM * bool(qk_norm) |
+             SSD_DELTA_MMA_F32 * (_mma(mma) == MMA["f32"]))
     sh = SSDDeltaShape(tok[0], tok[1] if lead == 2 else 1, H, P, N, G)
     return sh, rows, flags, float(N ** -0.5 if scale is None else scale)
 
@@ -47,7 +49,7 @@ def ssd_delta_rule_workspace_bytes(batch, seqlen, nheads, ngroups, dstate, headd
 
 def ssd_delta_rule(q, k, v, dt, beta, A, dt_bias=None, softplus=True, sigmoid=True, qk_norm=True, scale=None,
                    initial_states=None, seq_idx=None, y=None, final_states=None, want_final=True, seq_last=None,
-                   seq_states=None, workspace=None, stream=None):
+                   seq_states=None, workspace=None, mma="bf16", stream=None):
     """Gated delta rule over q, k [B,L,G,N], v [B,L,H,P] and the raw decays and
     writing strengths dt, beta [B,L,H] (each may be a column slice of wider
     rows), A, dt_bias [H] fp32, states [B,H,N,P] fp32:
@@ -59,10 +61,12 @@ def ssd_delta_rule(q, k, v, dt, beta, A, dt_bias=None, softplus=True, sigmoid=Tr
     N^-1/2).  Returns (y, final_states or None), and with seq_last (see
     ssd_forward_varlen) also seq_states [nseq,H,N,P].  final_states may be the
     initial_states tensor.  A token that is no number makes none of its
-    sequence's outputs from itself on; earlier ones stay as they are."""
+    sequence's outputs from itself on; earlier ones stay as they are.
+    ``mma="f32"``: fp32 products for bf16 inputs too, whose states are otherwise
+    some 2e-6 off (fp32 inputs have no others)."""
     if stream is not None:
         return _on_stream(ssd_delta_rule, locals())
-    sh, rows, flags, scale = _delta_inputs(q, k, v, dt, beta, A, dt_bias, softplus, sigmoid, qk_norm, scale, 2)
+    sh, rows, flags, scale = _delta_inputs(q, k, v, dt, beta, A, dt_bias, softplus, sigmoid, qk_norm, scale, 2, mma)
     B, L, H, P, N = sh.batch, sh.seqlen, sh.nheads, sh.headdim, sh.dstate
     _opt(initial_states, "initial_states", (B, H, N, P), _F32)
     _opt(seq_idx, "seq_idx", (B, L), (torch.int32,))
@@ -112,14 +116,15 @@ def ssd_delta_rule_backward_workspace_bytes(batch, seqlen, nheads, ngroups, dsta
 
 def ssd_delta_rule_backward(q, k, v, dt, beta, A, dy, dt_bias=None, softplus=True, sigmoid=True, qk_norm=True,
                             scale=None, initial_states=None, dfinal=None, seq_idx=None, want_dinitial=False,
-                            workspace=None, out=None, stream=None) -> Dict[str, Optional[torch.Tensor]]:
+                            workspace=None, out=None, mma="bf16", stream=None) -> Dict[str, Optional[torch.Tensor]]:
     """Gradients of ssd_delta_rule for dL/dy = dy [B,L,H,P] and dL/dfinal =
     dfinal (None: zero): dq, dk, dv, ddt, dbeta (of the raw dt and beta) in v's
     dtype (given ``out`` tensors may be column slices), dA, ddt_bias, dinitial
-    fp32; None where the input is absent, dinitial unless ``want_dinitial``."""
+    fp32; None where the input is absent, dinitial unless ``want_dinitial``;
+    ``mma`` as there."""
     if stream is not None:
         return _on_stream(ssd_delta_rule_backward, locals())
-    sh, rows, flags, scale = _delta_inputs(q, k, v, dt, beta, A, dt_bias, softplus, sigmoid, qk_norm, scale, 2)
+    sh, rows, flags, scale = _delta_inputs(q, k, v, dt, beta, A, dt_bias, softplus, sigmoid, qk_norm, scale, 2, mma)
     B, L, H, P, N, G = sh.batch, sh.seqlen, sh.nheads, sh.headdim, sh.dstate, sh.ngroups
     io = (v.dtype,)
     _req(dy, "dy", (B, L, H, P), io)

@@ -142,6 +142,21 @@ def test_a_workspace_serves_smaller_prompts(lib, N, P):
             assert r[0] > 0 and all(a <= b for a, b in zip(r, r[1:]))
 
 
+def test_delta_fp32_products(lib, stand_in):
+    """The flag gets as far as the workspace; the binding knows two kinds."""
+    for ty in (0, 1):
+        assert fwd(lib, flags=39, ty=ty, ws=None) == WS and bwd(lib, flags=32, ty=ty, ws=None) == WS
+        assert step(lib, flags=35, ty=ty, y=None) == NULL
+    assert fwd(lib, flags=64) == UNSUP and bwd(lib, flags=40) == UNSUP and step(lib, flags=48) == UNSUP
+    t = lambda *s, dtype=torch.float32: base._Tensor(stand_in, s, dtype)
+    for name in ("ssd_delta_rule", "ssd_delta_rule_backward"):
+        for mma in ("f32", "bf16"):
+            getattr(ops, name)(**_args(name, t), mma=mma)
+        with pytest.raises(ValueError, match="mma must be"):
+            getattr(ops, name)(**_args(name, t), mma="f16")
+    assert len(stand_in.launched) == 4
+
+
 # ---------------------------------------------------------------- group norm, 8 bits
 
 def gn(lib, rows=6, dim=128, groups=2, x=F, ty=1, z=F, zrow=0, w=F, b=F, flags=1, y=F, mean=None, rstd=F):
