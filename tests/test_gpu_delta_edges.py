@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import delta_reference as ref
+from mamba_ssd_scan_chunk_amd import ops
 from test_gpu_delta import BF, F32, back, call, check, check_grads, cotangents
 
 pytestmark = pytest.mark.gpu
@@ -99,3 +100,26 @@ def test_a_token_that_is_no_number_reaches_no_earlier_one(shape, tokens, starts,
                 st = got[2][s].cpu()
                 assert torch.equal(st[~lost], clean[2][s].cpu()[~lost]), (what, t)
                 assert not torch.isfinite(st[lost]).any(), (what, t)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_the_widest_dense_rows(dtype):
+    """One key head of 256 below rows of 2^23 elements, whose 64 fp32 rows are all
+    but 2^31 bytes: each head is what it is by itself."""
+    L, H, N, P = 64, (1 << 15) - 1, 256, 16
+    g = torch.Generator(device="cuda").manual_seed(6)
+    rn = lambda *s: torch.randn(s, generator=g, device="cuda", dtype=torch.float32).to(dtype)
+    q, k, v, dt, beta = rn(1, L, H, N), rn(1, L, H, N), rn(1, L, H, P), rn(1, L, H), rn(1, L, H)
+    A, h0 = -torch.rand(H, generator=g, device="cuda") - 0.5, torch.randn((1, H, N, P), generator=g, device="cuda")
+    dy = rn(1, L, H, P)
+    y, fin = ops.ssd_delta_rule(q, k, v, dt, beta, A, initial_states=h0)
+    r = ops.ssd_delta_rule_backward(q, k, v, dt, beta, A, dy, initial_states=h0, want_dinitial=True)
+    some = torch.tensor([0, 1, H // 2, H - 1], device="cuda")
+    one = [t[:, :, some].contiguous() for t in (q, k, v, dt, beta)]
+    y1, fin1 = ops.ssd_delta_rule(*one, A[some].contiguous(), initial_states=h0[:, some].contiguous())
+    r1 = ops.ssd_delta_rule_backward(*one, A[some].contiguous(), dy[:, :, some].contiguous(),
+                                     initial_states=h0[:, some].contiguous(), want_dinitial=True)
+    assert torch.equal(y[:, :, some], y1) and torch.equal(fin[:, some], fin1)
+    for n in ("dq", "dk", "dv", "ddt", "dbeta"):
+        assert torch.equal(r[n][:, :, some], r1[n]), n
+    assert torch.equal(r["dA"][some], r1["dA"]) and torch.equal(r["dinitial"][:, some], r1["dinitial"])
